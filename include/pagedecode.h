@@ -77,6 +77,8 @@ typedef enum {
 #define PD_FLAG_BAD_LAST_PAGE_LEN 0x2 /* last_page_len outside [0, page_size]: clamped to that range */
 #define PD_FLAG_BAD_INDPTR 0x4        /* indptr decreasing, negative or past num_indices: all outputs invalid */
 #define PD_FLAG_WAIT_TIMEOUT 0x8      /* a copy pipeline wait passed its time limit; outputs invalid */
+#define PD_FLAG_BAD_NEW_ROWS 0x10     /* new_indptr decreasing, outside [0, total_new], or more new rows than kv_len */
+#define PD_FLAG_BAD_PATH 0x20         /* a path that does not increase, leaves the new rows or passes max_path */
 
 /* Bytes at the start of every workspace that hold the status word and the
  * decode's work-distribution counters (zero between calls). */
@@ -425,6 +427,181 @@ pd_status pd_paged_decode_noalloc(const void* q, const void* k_data, const void*
  * stream. Allocates nothing. The word is cleared by the next noalloc call.
  */
 pd_status pd_paged_decode_noalloc_flags(int32_t* flags, void* stream);
+
+/*
+ * Speculative decoding. The four groups of calls below are an extension of
+ * this library, not calls of the pages above. A step with drafted tokens
+ * rotates q and k and appends k and v (pd_paged_rope_append), attends for all
+ * drafted tokens at once (pd_paged_tree_decode), and keeps the accepted ones
+ * (pd_paged_tree_commit). A prompt, or a piece of one, goes through the first
+ * two as a chain.
+ *
+ * New rows. Request b's new tokens are rows new_indptr[b] .. new_indptr[b+1]
+ * of the ragged tensors (new_indptr: device int32 [batch + 1], increasing from
+ * 0 to total_new), n_b of them, and are the LAST n_b tokens of its cache: the
+ * page table already describes them (the caller's update for n_b tokens).
+ * n_b may be 0. A malformed new_indptr, or n_b > kv_len, is flagged with
+ * PD_FLAG_BAD_NEW_ROWS and that request's rows are not written to the pool.
+ */
+
+/*
+ * Rotary positions. Pair i of a head at position p turns by the angle p f_i:
+ *
+ *   (a, b)  ->  rope_scale * (a cos - b sin, b cos + a sin)
+ *
+ * for the pairs of the leading rot_dim elements: (i, i + rot_dim / 2) with
+ * PD_ROPE_HALF, (2i, 2i + 1) with PD_ROPE_PAIRS. Elements from rot_dim on are
+ * copied. Arithmetic is f32, rounded once to T. Positions are int32 and may be
+ * negative: rotating by -p undoes rotating by p, and is also the gradient of
+ * pd_rope (of the same rope_scale).
+ *
+ * freqs: device uint64 [rot_dim / 2], 8-byte aligned: f_i in turns (2 pi
+ * radians) per position, as a binary fraction, floor(f_i / (2 pi) * 2^64) for
+ * f_i in radians. The angle modulo one turn is then exact at any position.
+ */
+#define PD_ROPE_HALF 0
+#define PD_ROPE_PAIRS 1
+
+/*
+ * Fill freqs (HOST memory, rot_dim / 2 entries; the caller copies it to the
+ * device) and *rope_scale (host). With f_i = theta^(-2i / rot_dim):
+ *  PD_ROPE_PLAIN   f_i
+ *  PD_ROPE_LINEAR  f_i / factor
+ *  PD_ROPE_BASE    theta replaced by theta * factor^(rot_dim / (rot_dim - 2))
+ *  PD_ROPE_BANDED  k f_i + (1 - k) f_i / factor, k = clamp((turns - low) /
+ *                  (high - low), 0, 1), turns = original_positions f_i / 2 pi
+ *  PD_ROPE_YARN    the same with k falling linearly over the pair index, from
+ *                  1 at the (floored) index that makes `high` turns over
+ *                  original_positions to 0 at the (ceiled) one that makes
+ *                  `low`; rope_scale = 0.1 ln(factor) + 1 (1 for the others)
+ * factor >= 1 (ignored by PLAIN); 0 < low < high and original_positions > 0
+ * for BANDED and YARN (ignored by the others). Needs no device.
+ */
+#define PD_ROPE_PLAIN 0
+#define PD_ROPE_LINEAR 1
+#define PD_ROPE_BASE 2
+#define PD_ROPE_BANDED 3
+#define PD_ROPE_YARN 4
+pd_status pd_rope_frequencies(uint64_t* freqs, float* rope_scale, int rot_dim, double theta, int scaling,
+                              double factor, double low, double high, int original_positions);
+
+/*
+ * Rotate num_tokens tokens. x, out: device T; head h of token t is the
+ * head_dim elements at t * stride + h * head_dim (strides in elements, at
+ * least num_heads * head_dim: a token's heads are contiguous, tokens may be
+ * slices of a wider row). out may be x (the same stride), and must not
+ * otherwise overlap it. Elements between the tokens of out are left alone.
+ * positions: device int32 [num_tokens]. rot_dim even, 0 .. head_dim; head_dim
+ * up to 4096. 16-byte accesses where x, out and their strides allow it and
+ * rot_dim is a multiple of 16 (f32: 8); single elements otherwise.
+ */
+pd_status pd_rope(const void* x, const int32_t* positions, const uint64_t* freqs, void* out, int num_tokens,
+                  int num_heads, int head_dim, int rot_dim, int64_t x_stride, int64_t out_stride, int layout,
+                  float rope_scale, pd_dtype dtype, void* stream);
+
+/*
+ * Append n_b new tokens to every request, with the rotation on the way: row
+ * kv_len - n_b + j of request b's cache becomes the rotated k_new row (K pool)
+ * and, bit for bit, the v_new row (V pool) of its new token j; q_out receives
+ * the rotated q rows.
+ *
+ * q: device [total_new] tokens of num_qo_heads heads, q_stride elements apart;
+ *   q_out: device [total_new, num_qo_heads, head_dim], may be q if q is laid
+ *   out so. num_qo_heads = 0 leaves q out (q, q_out may be NULL).
+ * k_new, v_new: device [total_new] tokens of num_kv_heads heads, k_stride and
+ *   v_stride elements apart. q, k_new and v_new may be views of one tensor.
+ * positions: device int32 [total_new], or NULL for each token's index in its
+ *   cache. A tree's nodes sit at positions given by their depth, not by their
+ *   row: give them.
+ * rot_dim = 0 (freqs may be NULL) appends without rotation.
+ * k_data, v_data: device, 16-byte aligned, modified in place. No two requests
+ *   may own the page that a new row falls in.
+ * workspace: at least PD_WORKSPACE_HEADER_BYTES (the status word).
+ * A new row whose request or page is bad is flagged and not written; its q
+ * row is still rotated when positions are given, and undefined otherwise.
+ *
+ * The _fp8 form writes E4M3 codes of the rotated k / k_scale[h] and of v /
+ * v_scale[h] (the f32 values, divided in f32, rounded once to the nearest
+ * code, ties to even, saturating at +-448). dtype PD_F16 or PD_BF16.
+ */
+pd_status pd_paged_rope_append(const void* q, const void* k_new, const void* v_new, const int32_t* positions,
+                               const uint64_t* freqs, void* q_out, void* k_data, void* v_data, const int32_t* indices,
+                               const int32_t* indptr, const int32_t* last_page_len, const int32_t* new_indptr,
+                               int batch, int total_new, int num_qo_heads, int num_kv_heads, int head_dim, int rot_dim,
+                               int page_size, int num_total_pages, int num_indices, int64_t q_stride, int64_t k_stride,
+                               int64_t v_stride, int layout, float rope_scale, pd_dtype dtype, void* workspace,
+                               size_t workspace_bytes, void* stream);
+pd_status pd_paged_rope_append_fp8(const void* q, const void* k_new, const void* v_new, const int32_t* positions,
+                                   const uint64_t* freqs, void* q_out, const float* k_scale, const float* v_scale,
+                                   void* k_data, void* v_data, const int32_t* indices, const int32_t* indptr,
+                                   const int32_t* last_page_len, const int32_t* new_indptr, int batch, int total_new,
+                                   int num_qo_heads, int num_kv_heads, int head_dim, int rot_dim, int page_size,
+                                   int num_total_pages, int num_indices, int64_t q_stride, int64_t k_stride,
+                                   int64_t v_stride, int layout, float rope_scale, pd_dtype dtype, void* workspace,
+                                   size_t workspace_bytes, void* stream);
+
+/*
+ * Attention of every request's new tokens (its nodes) over its cache, their
+ * own rows among it. Node j of request b attends every one of the first
+ * kv_len - n_b tokens, and node i of the request iff bit i % 32 of
+ * tree_mask[new_indptr[b] + j][i / 32] is set (a node sees itself only if its
+ * own bit is set; bits from 32 * mask_words on count as clear). tree_mask =
+ * NULL is a chain: node j attends nodes 0 .. j. With s_t = sm_scale * q . k_t
+ * over the attended tokens,
+ *
+ *   o = sum_t exp(s_t - lse) v_t        lse = ln sum_t exp(s_t)
+ *
+ * and a node that attends nothing gets o = 0, lse = -infinity. Tokens that a
+ * node does not attend have no part in its result, whatever they hold (NaN and
+ * infinities included).
+ *
+ * q, o: device [total_new, num_qo_heads, head_dim] T, 16-byte aligned.
+ * tree_mask: device uint32 [total_new, mask_words], or NULL.
+ * lse: device float32 [total_new, num_qo_heads].
+ * The rest is as for pd_paged_decode. workspace: at least
+ * pd_paged_tree_decode_workspace_bytes(...) bytes, header zeroed once; it may
+ * be shared with the other calls on the same stream. Results do not depend on
+ * timing: the work is cut at fixed places and merged in a fixed order.
+ * A node of a bad request (bad indptr, or n_b > kv_len) attends nothing.
+ *
+ * 16-bit q runs on the tensor cores (tcgen05) for groups of up to 128 q heads;
+ * f32, and larger groups, on CUDA cores. Weights are rounded to T before they
+ * meet V, sums are f32.
+ * The _fp8 form reads E4M3 pools as pd_paged_decode_fp8 does (dtype PD_F16 or
+ * PD_BF16 is the type of q and o).
+ */
+size_t pd_paged_tree_decode_workspace_bytes(int num_qo_heads, int num_kv_heads, int head_dim, pd_dtype dtype);
+pd_status pd_paged_tree_decode(const void* q, const void* k_data, const void* v_data, const int32_t* indices,
+                               const int32_t* indptr, const int32_t* last_page_len, const int32_t* new_indptr,
+                               const uint32_t* tree_mask, void* o, float* lse, int batch, int total_new,
+                               int mask_words, int num_qo_heads, int num_kv_heads, int head_dim, int page_size,
+                               int num_total_pages, int num_indices, float sm_scale, pd_dtype dtype, void* workspace,
+                               size_t workspace_bytes, void* stream);
+pd_status pd_paged_tree_decode_fp8(const void* q, const void* k_data, const void* v_data, const float* k_scale,
+                                   const float* v_scale, const int32_t* indices, const int32_t* indptr,
+                                   const int32_t* last_page_len, const int32_t* new_indptr, const uint32_t* tree_mask,
+                                   void* o, float* lse, int batch, int total_new, int mask_words, int num_qo_heads,
+                                   int num_kv_heads, int head_dim, int page_size, int num_total_pages, int num_indices,
+                                   float sm_scale, pd_dtype dtype, void* workspace, size_t workspace_bytes,
+                                   void* stream);
+
+/*
+ * Keep the accepted nodes: for i < path_len[b], the K and V rows of node
+ * path[b][i] move, bit for bit, to the place of node i. A path increases
+ * strictly (a parent comes before its child); node i = path[b][i] stays where
+ * it is. The caller then shortens the request to kv_len - n_b + path_len[b]
+ * tokens. Rows of the new tokens past path_len[b] are left as they fall.
+ *
+ * path: device int32 [batch, max_path]; path_len: device int32 [batch], 0 ..
+ * max_path. elem_bytes: 1 (E4M3 pools), 2 or 4. workspace as for
+ * pd_paged_rope_append. The table is the one of the tree decode. A request
+ * with a bad path or table is flagged and left as it is.
+ */
+pd_status pd_paged_tree_commit(void* k_data, void* v_data, const int32_t* indices, const int32_t* indptr,
+                               const int32_t* last_page_len, const int32_t* new_indptr, const int32_t* path,
+                               const int32_t* path_len, int batch, int total_new, int max_path, int num_kv_heads,
+                               int head_dim, int page_size, int num_total_pages, int num_indices, int elem_bytes,
+                               void* workspace, size_t workspace_bytes, void* stream);
 
 /* Message for the last error status returned on this host thread ("" if none). */
 const char* pd_last_error_string(void);

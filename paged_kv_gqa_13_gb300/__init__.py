@@ -29,7 +29,10 @@ _lib = ctypes.CDLL(LIBRARY_PATH)
 PD_F32, PD_F16, PD_BF16 = 0, 1, 2
 PD_OK, PD_ERR_INVALID, PD_ERR_UNSUPPORTED, PD_ERR_WORKSPACE, PD_ERR_CUDA = 0, 1, 2, 3, 4
 PD_FLAG_BAD_PAGE_ID, PD_FLAG_BAD_LAST_PAGE_LEN, PD_FLAG_BAD_INDPTR, PD_FLAG_WAIT_TIMEOUT = 1, 2, 4, 8
+PD_FLAG_BAD_NEW_ROWS, PD_FLAG_BAD_PATH = 16, 32
 PD_WORKSPACE_HEADER_BYTES = 256
+PD_ROPE_HALF, PD_ROPE_PAIRS = 0, 1
+PD_ROPE_PLAIN, PD_ROPE_LINEAR, PD_ROPE_BASE, PD_ROPE_BANDED, PD_ROPE_YARN = 0, 1, 2, 3, 4
 PD_KERNEL_NONE, PD_KERNEL_CUDA_CORES, PD_KERNEL_TENSOR_CORES, PD_KERNEL_FP8_TENSOR_CORES = 0, 1, 2, 3
 PD_KERNEL_FP8_TCGEN05 = 4
 
@@ -37,6 +40,7 @@ STATUS_NAMES = {0: "PD_OK", 1: "PD_ERR_INVALID", 2: "PD_ERR_UNSUPPORTED", 3: "PD
                 4: "PD_ERR_CUDA"}
 
 _P, _I, _F, _S = ctypes.c_void_p, ctypes.c_int, ctypes.c_float, ctypes.c_size_t
+_L, _D = ctypes.c_int64, ctypes.c_double
 
 _SIGS = {
     "pd_paged_decode_workspace_bytes": (_S, [_I, _I, _I, _I, _I]),
@@ -69,6 +73,14 @@ _SIGS = {
     "pd_paged_decode_noalloc": (_I, [_P, _P, _P, _P, _P, _P, _P, _P, _I, _I, _I, _I, _I, _I, _I, _F, _I, _P]),
     "pd_paged_decode_noalloc_flags": (_I, [ctypes.POINTER(ctypes.c_int32), _P]),
     "pd_decode_kernel_kind": (_I, [_I, _I, _I, _I, _I]),
+    "pd_rope_frequencies": (_I, [_P, ctypes.POINTER(ctypes.c_float), _I, _D, _I, _D, _D, _D, _I]),
+    "pd_rope": (_I, [_P, _P, _P, _P, _I, _I, _I, _I, _L, _L, _I, _F, _I, _P]),
+    "pd_paged_rope_append": (_I, [_P] * 12 + [_I] * 9 + [_L] * 3 + [_I, _F, _I, _P, _S, _P]),
+    "pd_paged_rope_append_fp8": (_I, [_P] * 14 + [_I] * 9 + [_L] * 3 + [_I, _F, _I, _P, _S, _P]),
+    "pd_paged_tree_decode_workspace_bytes": (_S, [_I, _I, _I, _I]),
+    "pd_paged_tree_decode": (_I, [_P] * 10 + [_I] * 9 + [_F, _I, _P, _S, _P]),
+    "pd_paged_tree_decode_fp8": (_I, [_P] * 12 + [_I] * 9 + [_F, _I, _P, _S, _P]),
+    "pd_paged_tree_commit": (_I, [_P] * 8 + [_I] * 9 + [_P, _S, _P]),
     "pd_last_error_string": (ctypes.c_char_p, []),
     "pd_version": (_I, []),
 }
@@ -352,3 +364,198 @@ def pd_select_fp8_kernel(kind: int) -> None:
 def pd_test_inject_wait_timeout(extra_bytes: int) -> None:
     """Test-only: make each decode's first warp wait for bytes that never arrive (0 turns it off)."""
     _check(_lib.pd_test_inject_wait_timeout(int(extra_bytes)))
+
+
+# --- speculative decoding: request b's new tokens are rows new_indptr[b] .. new_indptr[b + 1] of the ragged
+# tensors and the last rows of its cache -----------------------------------------------------------------------
+
+def _tokens(t, heads, head_dim):
+    """(pointer, elements between tokens) of [tokens, heads, head_dim] rows whose heads are contiguous."""
+    stride = t.stride()
+    if t.dim() != 3 or t.shape[1] != heads or t.shape[2] != head_dim or (
+            t.numel() and (stride[2] != 1 or (stride[1] != head_dim and heads != 1))):
+        raise PagedecodeError(PD_ERR_INVALID, "expected [tokens, heads, head_dim] with contiguous heads")
+    return t.data_ptr(), stride[0] if t.shape[0] > 1 else max(stride[0], heads * head_dim)
+
+
+def _same_dtype(*tensors) -> int:
+    code = _dtype_code(tensors[0])
+    if any(t.dtype != tensors[0].dtype for t in tensors):
+        raise PagedecodeError(PD_ERR_INVALID, "tensors must have the same dtype")
+    return code
+
+
+def _int32(t):
+    """Pointer of a contiguous 32-bit integer tensor (None stays None)."""
+    if t is None:
+        return None
+    if t.element_size() != 4 or t.is_floating_point():
+        raise PagedecodeError(PD_ERR_INVALID, "table, position, mask and path tensors hold 32-bit integers")
+    return _ptr(t)
+
+
+def _table(indices, indptr, last_page_len, new_indptr):
+    batch = last_page_len.numel()
+    if indptr.numel() != batch + 1 or new_indptr.numel() != batch + 1:
+        raise PagedecodeError(PD_ERR_INVALID, "indptr and new_indptr hold one entry more than last_page_len")
+    return (_int32(indices) if indices.numel() else None, _int32(indptr), _int32(last_page_len),
+            _int32(new_indptr)), batch
+
+
+def _pools(k_data, v_data):
+    if k_data.dim() != 4 or k_data.shape != v_data.shape or k_data.dtype != v_data.dtype:
+        raise PagedecodeError(PD_ERR_INVALID, "k_data and v_data are [pages, Hk, page_size, D] of the same type")
+    return k_data.shape
+
+
+def pd_rope_frequencies(rot_dim: int, theta: float = 10000.0, scaling: int = PD_ROPE_PLAIN, factor: float = 1.0,
+                        low: float = 1.0, high: float = 4.0, original_positions: int = 8192, device="cuda"):
+    """(freqs, rope_scale): int64 [rot_dim / 2] turns per position in units of 2^-64 turn, and the rotated part's factor."""
+    import torch
+
+    host = (ctypes.c_uint64 * max(1, int(rot_dim) // 2))()
+    scale = ctypes.c_float(1.0)
+    _check(_lib.pd_rope_frequencies(host, ctypes.byref(scale), int(rot_dim), float(theta), int(scaling), float(factor),
+                                    float(low), float(high), int(original_positions)))
+    freqs = torch.frombuffer(host, dtype=torch.int64, count=int(rot_dim) // 2).to(device, copy=True)
+    return freqs, scale.value
+
+
+def _freqs(freqs):
+    if freqs is None:
+        return None, 0
+    if freqs.element_size() != 8 or freqs.is_floating_point():
+        raise PagedecodeError(PD_ERR_INVALID, "freqs hold 64-bit integers")
+    return _ptr(freqs), 2 * freqs.numel()
+
+
+def pd_rope(x, positions, freqs, out, layout: int = PD_ROPE_HALF, rope_scale: float = 1.0, stream=None) -> None:
+    """x, out [tokens, heads, D] (tokens may be strided); positions int32 [tokens]; out may be x."""
+    tokens, heads, head_dim = x.shape
+    if out.shape != x.shape or positions.numel() != tokens:
+        raise PagedecodeError(PD_ERR_INVALID, "out is shaped as x, and there is one position for each token")
+    (xp, xs), (op, os_) = _tokens(x, heads, head_dim), _tokens(out, heads, head_dim)
+    fp, rot = _freqs(freqs)
+    _check(_lib.pd_rope(xp, _int32(positions), fp, op, tokens, heads, head_dim, rot, xs, os_, layout, rope_scale,
+                        _same_dtype(x, out), _stream(stream)))
+
+
+def _rope_append(fn, scales, q, k_new, v_new, positions, freqs, q_out, k_data, v_data, indices, indptr, last_page_len,
+                 new_indptr, workspace, layout, rope_scale, stream):
+    total_new, num_kv_heads, head_dim = k_new.shape
+    num_total_pages, hk, page_size, d = _pools(k_data, v_data)
+    if (hk, d) != (num_kv_heads, head_dim) or v_new.shape != k_new.shape:
+        raise PagedecodeError(PD_ERR_INVALID, "k_new, v_new and the pools differ in heads or head_dim")
+    (kp, ks), (vp, vs) = _tokens(k_new, num_kv_heads, head_dim), _tokens(v_new, num_kv_heads, head_dim)
+    qp, qs, op, num_qo_heads = None, 0, None, 0
+    code = _same_dtype(k_new, v_new)
+    if q is not None:
+        num_qo_heads = q.shape[1]
+        if q.shape[0] != total_new or q_out.shape != q.shape:
+            raise PagedecodeError(PD_ERR_INVALID, "q holds one row for each new token, and q_out is shaped as q")
+        qp, qs = _tokens(q, num_qo_heads, head_dim)
+        op = _ptr(q_out)
+        _same_dtype(k_new, q, q_out)
+    if positions is not None and positions.numel() != total_new:
+        raise PagedecodeError(PD_ERR_INVALID, "there is one position for each new token")
+    fp, rot = _freqs(freqs)
+    table, batch = _table(indices, indptr, last_page_len, new_indptr)
+    _check(fn(qp, kp, vp, _int32(positions), fp, op, *scales, _ptr(k_data), _ptr(v_data), *table, batch, total_new,
+              num_qo_heads, num_kv_heads, head_dim, rot, page_size, num_total_pages, indices.numel(), qs, ks, vs, layout,
+              rope_scale, code, _ptr(workspace), workspace.numel(), _stream(stream)))
+
+
+def pd_paged_rope_append(q, k_new, v_new, positions, freqs, q_out, k_data, v_data, indices, indptr, last_page_len,
+                         new_indptr, workspace, layout: int = PD_ROPE_HALF, rope_scale: float = 1.0,
+                         stream=None) -> None:
+    """Rotate q into q_out and k_new into its pages, copy v_new into its pages.
+
+    q, k_new, v_new [total_new, heads, D], tokens may be strided (views of one projection); q, q_out may be None;
+    positions int32 [total_new] or None (the index in the cache); freqs None appends without rotation.
+    """
+    if _same_dtype(k_data) != _dtype_code(k_new):
+        raise PagedecodeError(PD_ERR_INVALID, "the pools have the type of k_new")
+    _rope_append(_lib.pd_paged_rope_append, (), q, k_new, v_new, positions, freqs, q_out, k_data, v_data, indices, indptr,
+                 last_page_len, new_indptr, workspace, layout, rope_scale, stream)
+
+
+def pd_paged_rope_append_fp8(q, k_new, v_new, positions, freqs, q_out, k_scale, v_scale, k_data, v_data, indices,
+                             indptr, last_page_len, new_indptr, workspace, layout: int = PD_ROPE_HALF,
+                             rope_scale: float = 1.0, stream=None) -> None:
+    """pd_paged_rope_append into E4M3 pools (k_data, v_data uint8; scales f32 [Hk])."""
+    scales = _scales(k_scale, v_scale, k_data)
+    _rope_append(_lib.pd_paged_rope_append_fp8, scales, q, k_new, v_new, positions, freqs, q_out, k_data, v_data, indices,
+                 indptr, last_page_len, new_indptr, workspace, layout, rope_scale, stream)
+
+
+def _scales(k_scale, v_scale, k_data):
+    import torch
+
+    if any(s.dtype != torch.float32 or s.numel() != k_data.shape[1] for s in (k_scale, v_scale)):
+        raise PagedecodeError(PD_ERR_INVALID, "k_scale and v_scale are float32, one for each kv head")
+    if k_data.element_size() != 1:
+        raise PagedecodeError(PD_ERR_INVALID, "E4M3 pools hold one byte for each element")
+    return _ptr(k_scale), _ptr(v_scale)
+
+
+def pd_paged_tree_decode_workspace_bytes(num_qo_heads: int, num_kv_heads: int, head_dim: int, dtype: int) -> int:
+    n = _lib.pd_paged_tree_decode_workspace_bytes(num_qo_heads, num_kv_heads, head_dim, dtype)
+    if n == 0:
+        raise PagedecodeError(PD_ERR_INVALID, pd_last_error_string())
+    return n
+
+
+def _tree_decode(fn, scales, q, k_data, v_data, indices, indptr, last_page_len, new_indptr, tree_mask, o, lse, sm_scale,
+                 workspace, stream):
+    import torch
+
+    total_new, num_qo_heads, head_dim = q.shape
+    num_total_pages, num_kv_heads, page_size, d = _pools(k_data, v_data)
+    if d != head_dim or o.shape != q.shape or lse.shape != q.shape[:2] or lse.dtype != torch.float32:
+        raise PagedecodeError(PD_ERR_INVALID, "q and o [total_new, Hq, D], lse float32 [total_new, Hq], the pools' D")
+    words = 0
+    if tree_mask is not None:
+        if tree_mask.dim() != 2 or tree_mask.shape[0] != total_new:
+            raise PagedecodeError(PD_ERR_INVALID, "tree_mask is [total_new, words] of 32 bits each")
+        words = tree_mask.shape[1]
+    table, batch = _table(indices, indptr, last_page_len, new_indptr)
+    _check(fn(_ptr(q), _ptr(k_data), _ptr(v_data), *scales, *table, _int32(tree_mask), _ptr(o), _ptr(lse), batch, total_new,
+              words, num_qo_heads, num_kv_heads, head_dim, page_size, num_total_pages, indices.numel(), sm_scale,
+              _same_dtype(q, o), _ptr(workspace), workspace.numel(), _stream(stream)))
+
+
+def pd_paged_tree_decode(q, k_data, v_data, indices, indptr, last_page_len, new_indptr, tree_mask, o, lse,
+                         sm_scale: float, workspace, stream=None) -> None:
+    """Attention of each request's last rows (its nodes) over its cache and over each other.
+
+    q, o [total_new, Hq, D]; lse [total_new, Hq] f32; tree_mask int32 (or uint32) [total_new, words]: bit i of a node's
+    words says that it attends node i of its request; None: a chain (nodes up to itself).
+    """
+    if _same_dtype(k_data) != _dtype_code(q):
+        raise PagedecodeError(PD_ERR_INVALID, "the pools have the type of q")
+    _tree_decode(_lib.pd_paged_tree_decode, (), q, k_data, v_data, indices, indptr, last_page_len, new_indptr, tree_mask, o,
+                 lse, sm_scale, workspace, stream)
+
+
+def pd_paged_tree_decode_fp8(q, k_data, v_data, k_scale, v_scale, indices, indptr, last_page_len, new_indptr, tree_mask,
+                             o, lse, sm_scale: float, workspace, stream=None) -> None:
+    """pd_paged_tree_decode over E4M3 pools (k_data, v_data uint8; scales f32 [Hk]); q, o f16 or bf16."""
+    _tree_decode(_lib.pd_paged_tree_decode_fp8, _scales(k_scale, v_scale, k_data), q, k_data, v_data, indices, indptr,
+                 last_page_len, new_indptr, tree_mask, o, lse, sm_scale, workspace, stream)
+
+
+def pd_paged_tree_commit(k_data, v_data, indices, indptr, last_page_len, new_indptr, path, path_len, workspace,
+                         stream=None, total_new: int | None = None) -> None:
+    """Move the K/V rows of each request's accepted nodes path[b, :path_len[b]] to the places of its first nodes.
+
+    path int32 [batch, max_path], strictly increasing; path_len int32 [batch]. total_new bounds new_indptr (default:
+    no bound).
+    """
+    num_total_pages, num_kv_heads, page_size, head_dim = _pools(k_data, v_data)
+    table, batch = _table(indices, indptr, last_page_len, new_indptr)
+    if path.dim() != 2 or path.shape[0] != batch or path_len.numel() != batch:
+        raise PagedecodeError(PD_ERR_INVALID, "path is [batch, max_path], path_len [batch]")
+    _check(_lib.pd_paged_tree_commit(
+        _ptr(k_data), _ptr(v_data), *table, _int32(path), _int32(path_len), batch,
+        0x7fffffff if total_new is None else total_new, path.shape[1], num_kv_heads, head_dim, page_size, num_total_pages,
+        indices.numel(), k_data.element_size(), _ptr(workspace), workspace.numel(), _stream(stream)))

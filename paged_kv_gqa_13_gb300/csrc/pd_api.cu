@@ -12,6 +12,7 @@
 #include <cudaTypedefs.h>
 
 #include "pagedecode.h"
+#include "pd_host.h"
 #include "pd_kernels.cuh"
 
 namespace pd {
@@ -606,6 +607,31 @@ pd_status check_workspace(void* ws, size_t have, size_t need) {
 }
 
 }  // namespace
+
+namespace pd {
+namespace host {
+
+pd_status fail(pd_status st, const char* fmt, ...) {
+    va_list ap;
+    va_start(ap, fmt);
+    vsnprintf(g_err, sizeof(g_err), fmt, ap);
+    va_end(ap);
+    return st;
+}
+pd_status ok() { return ::ok(); }
+pd_status cuda_fail(cudaError_t e, const char* what) { return ::cuda_fail(e, what); }
+pd_status check_workspace(void* ws, size_t have, size_t need) { return ::check_workspace(ws, have, need); }
+pd_status sm_count(int* sms) {
+    DeviceInfo di;
+    const pd_status st = device_info(&di);
+    if (st == PD_OK) *sms = di.sms;
+    return st;
+}
+pd_status allow_smem(const void* fn, int bytes) { return ::allow_smem(fn, bytes); }
+PFN_cuTensorMapEncodeTiled_v12000 tensor_map_encoder() { return ::tensor_map_encoder(); }
+
+}  // namespace host
+}  // namespace pd
 
 extern "C" {
 

@@ -1,0 +1,221 @@
+// Tree decode: argument checks, the choice of kernel, launches.
+#include <cmath>
+#include <type_traits>
+
+#include "pd_host.h"
+#include "pd_tree.cuh"
+
+namespace pd {
+namespace {
+
+struct TreeKernels {
+    const void* main;
+    const void* merge;
+    int threads, smem, per_sm;       // of main
+    int tile_rows, tiles;            // rows of a row tile, row tiles per segment
+    int block_tokens;                // tokens of a key block
+    bool tensor;
+};
+
+template <typename T, typename KV, int D>
+TreeKernels cc_kernels() {
+    using C = CfgTreeCc<D>;
+    TreeKernels k{};
+    k.main = reinterpret_cast<const void*>(tree_cc_kernel<T, KV, D>);
+    k.merge = reinterpret_cast<const void*>(tree_merge_kernel<T, D>);
+    k.threads = C::kThreads;
+    k.smem = C::kBytes;
+    k.per_sm = C::kBlocksPerSm;
+    k.tile_rows = C::kRows;
+    k.tiles = 1;
+    k.block_tokens = C::kBlockTokens;
+    return k;
+}
+
+template <typename T, typename KV>
+bool cc_by_dim(int D, TreeKernels* k) {
+    switch (D) {
+        case 64: *k = cc_kernels<T, KV, 64>(); return true;
+        case 128: *k = cc_kernels<T, KV, 128>(); return true;
+        case 256: *k = cc_kernels<T, KV, 256>(); return true;
+    }
+    return false;
+}
+
+bool pick(pd_dtype dt, bool fp8, int D, int group, TreeKernels* k) {
+    (void)group;
+    switch (dt) {
+        case PD_F32: return !fp8 && cc_by_dim<float, float>(D, k);
+        case PD_F16: return fp8 ? cc_by_dim<__half, uint8_t>(D, k) : cc_by_dim<__half, __half>(D, k);
+        case PD_BF16: return fp8 ? cc_by_dim<__nv_bfloat16, uint8_t>(D, k) : cc_by_dim<__nv_bfloat16, __nv_bfloat16>(D, k);
+    }
+    return false;
+}
+
+size_t round256(size_t x) { return (x + 255) / 256 * 256; }
+
+// Workspace: header | split descriptors | partial lse | partial o, for a grid of `ctas`.
+struct TreeSpace {
+    size_t splits, lse, o, bytes;
+};
+TreeSpace space(const TreeKernels& k, int ctas, int D) {
+    TreeSpace s;
+    const size_t rows = size_t(2) * ctas * k.tile_rows * k.tiles;
+    s.splits = PD_WORKSPACE_HEADER_BYTES;
+    s.lse = s.splits + round256(size_t(ctas) * sizeof(TreeSplit));
+    s.o = s.lse + round256(rows * 4);
+    s.bytes = s.o + rows * D * 4;
+    return s;
+}
+
+pd_status check_heads(int Hq, int Hk, int D, pd_dtype dt) {
+    if (!host::known_dtype(dt)) return host::fail(PD_ERR_UNSUPPORTED, "dtype must be PD_F32, PD_F16 or PD_BF16");
+    if (Hq <= 0 || Hk <= 0) return host::fail(PD_ERR_INVALID, "num_qo_heads and num_kv_heads must be positive");
+    if (Hq % Hk != 0) return host::fail(PD_ERR_INVALID, "num_qo_heads (%d) must be a multiple of num_kv_heads (%d)", Hq, Hk);
+    if (D != 64 && D != 128 && D != 256) return host::fail(PD_ERR_UNSUPPORTED, "head_dim must be 64, 128 or 256 (got %d)", D);
+    return PD_OK;
+}
+
+pd_status tree_impl(const void* q, const void* k_data, const void* v_data, const float* k_scale, const float* v_scale,
+                    const int32_t* indices, const int32_t* indptr, const int32_t* last_page_len,
+                    const int32_t* new_indptr, const uint32_t* tree_mask, void* o, float* lse, int batch, int total_new,
+                    int mask_words, int Hq, int Hk, int D, int page_size, int num_total_pages, int num_indices,
+                    float sm_scale, pd_dtype dt, void* workspace, size_t workspace_bytes, void* stream, bool fp8) {
+    pd_status st = check_heads(Hq, Hk, D, dt);
+    if (st != PD_OK) return st;
+    if (fp8 && dt == PD_F32) return host::fail(PD_ERR_UNSUPPORTED, "E4M3 pools take PD_F16 or PD_BF16 q and o");
+    if (batch <= 0 || page_size <= 0 || num_total_pages <= 0)
+        return host::fail(PD_ERR_INVALID, "batch, page_size and num_total_pages must be positive");
+    if (total_new < 0 || num_indices < 0) return host::fail(PD_ERR_INVALID, "total_new and num_indices must not be negative");
+    if (tree_mask ? mask_words <= 0 : mask_words != 0)
+        return host::fail(PD_ERR_INVALID, "mask_words must be positive with a tree_mask and 0 without (got %d)", mask_words);
+    if (!std::isfinite(sm_scale)) return host::fail(PD_ERR_INVALID, "sm_scale must be finite");
+    if (!k_data || !v_data || !indptr || !last_page_len || !new_indptr || (num_indices > 0 && !indices) ||
+        (total_new > 0 && (!q || !o || !lse)) || (fp8 && (!k_scale || !v_scale)))
+        return host::fail(PD_ERR_INVALID, "null pointer argument");
+    if (!host::aligned(q, 16) || !host::aligned(k_data, 16) || !host::aligned(v_data, 16) || !host::aligned(o, 16))
+        return host::fail(PD_ERR_UNSUPPORTED, "q, k_data, v_data and o must be 16-byte aligned");
+    if (!host::aligned(lse, 4) || !host::aligned(indices, 4) || !host::aligned(indptr, 4) ||
+        !host::aligned(last_page_len, 4) || !host::aligned(new_indptr, 4) || !host::aligned(tree_mask, 4) ||
+        !host::aligned(k_scale, 4) || !host::aligned(v_scale, 4))
+        return host::fail(PD_ERR_UNSUPPORTED, "lse, the table, tree_mask and the scales must be 4-byte aligned");
+    const int group = Hq / Hk;
+    TreeKernels kn{};
+    if (!pick(dt, fp8, D, group, &kn)) return host::fail(PD_ERR_UNSUPPORTED, "no kernel for this type and head_dim");
+    int sms = 0;
+    if ((st = host::sm_count(&sms)) != PD_OK) return st;
+    const int most = sms * kn.per_sm;
+    const TreeSpace sp = space(kn, most, D);
+    if ((st = host::check_workspace(workspace, workspace_bytes, sp.bytes)) != PD_OK) return st;
+    if (total_new == 0) return host::ok();
+
+    uint8_t* ws = static_cast<uint8_t*>(workspace);
+    TreeArgs a{};
+    a.q = q;
+    a.k = k_data;
+    a.v = v_data;
+    a.indices = indices;
+    a.indptr = indptr;
+    a.last_page_len = last_page_len;
+    a.new_indptr = new_indptr;
+    a.mask = tree_mask;
+    a.o = o;
+    a.lse = lse;
+    a.k_scale = k_scale;
+    a.v_scale = v_scale;
+    a.splits = reinterpret_cast<TreeSplit*>(ws + sp.splits);
+    a.part_lse = reinterpret_cast<float*>(ws + sp.lse);
+    a.part_o = reinterpret_cast<float*>(ws + sp.o);
+    a.flags = reinterpret_cast<int*>(ws);
+    a.batch = batch;
+    a.total_new = total_new;
+    a.mask_words = mask_words;
+    a.num_qo_heads = Hq;
+    a.num_kv_heads = Hk;
+    a.group = group;
+    a.page_size = page_size;
+    a.num_total_pages = num_total_pages;
+    a.num_indices = num_indices;
+    a.tile_rows = kn.tile_rows;
+    a.seg_rows = kn.tile_rows * kn.tiles;
+    a.hs = (group + kn.tile_rows - 1) / kn.tile_rows;
+    a.hpt = (group + a.hs - 1) / a.hs;
+    a.npt = kn.tile_rows / a.hpt;
+    a.nps = a.npt * kn.tiles;
+    a.slot_rows = 1;
+    a.cpp = page_size;
+    a.spb = kn.block_tokens;
+    a.scale_log2 = sm_scale * kLog2e;
+
+    // No more CTAs than there can be units: segments x key blocks of the longest possible request.
+    const long long segs = ((long long)total_new / a.nps + batch) * a.hs * Hk;
+    const long long blocks = ((long long)num_indices * a.cpp + a.spb - 1) / a.spb;
+    const long long bound = segs * (blocks < 1 ? 1 : blocks);
+    const int grid = int(bound < most ? bound : most);
+    cudaStream_t cs = static_cast<cudaStream_t>(stream);
+    if ((st = host::allow_smem(kn.main, kn.smem)) != PD_OK) return st;
+    void* args[] = {&a};
+    cudaError_t e = cudaLaunchKernel(kn.main, dim3(grid), dim3(kn.threads), args, kn.smem, cs);
+    if (e != cudaSuccess) return host::cuda_fail(e, "tree decode launch");
+    if (grid > 1 && blocks > 1) {  // otherwise no segment can be split
+        cudaLaunchConfig_t cfg{};
+        cfg.gridDim = dim3(grid - 1, (a.seg_rows + 7) / 8);
+        cfg.blockDim = dim3(256);
+        cfg.stream = cs;
+        cudaLaunchAttribute attr[1];
+        attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+        attr[0].val.programmaticStreamSerializationAllowed = 1;
+        cfg.attrs = attr;
+        cfg.numAttrs = 1;
+        e = cudaLaunchKernelExC(&cfg, kn.merge, args);
+        if (e != cudaSuccess) return host::cuda_fail(e, "tree merge launch");
+    }
+    return host::ok();
+}
+
+}  // namespace
+}  // namespace pd
+
+using namespace pd;
+
+extern "C" {
+
+size_t pd_paged_tree_decode_workspace_bytes(int num_qo_heads, int num_kv_heads, int head_dim, pd_dtype dtype) {
+    if (check_heads(num_qo_heads, num_kv_heads, head_dim, dtype) != PD_OK) return 0;
+    int sms = 0;
+    if (host::sm_count(&sms) != PD_OK) return 0;
+    size_t most = 0;  // of the kernels that take this type, with either pool
+    for (int fp8 = 0; fp8 < 2; ++fp8) {
+        TreeKernels k{};
+        if (!pick(dtype, fp8 != 0, head_dim, num_qo_heads / num_kv_heads, &k)) continue;
+        const size_t n = space(k, sms * k.per_sm, head_dim).bytes;
+        if (n > most) most = n;
+    }
+    host::ok();
+    return most;
+}
+
+pd_status pd_paged_tree_decode(const void* q, const void* k_data, const void* v_data, const int32_t* indices,
+                               const int32_t* indptr, const int32_t* last_page_len, const int32_t* new_indptr,
+                               const uint32_t* tree_mask, void* o, float* lse, int batch, int total_new,
+                               int mask_words, int num_qo_heads, int num_kv_heads, int head_dim, int page_size,
+                               int num_total_pages, int num_indices, float sm_scale, pd_dtype dtype, void* workspace,
+                               size_t workspace_bytes, void* stream) {
+    return tree_impl(q, k_data, v_data, nullptr, nullptr, indices, indptr, last_page_len, new_indptr, tree_mask, o, lse,
+                     batch, total_new, mask_words, num_qo_heads, num_kv_heads, head_dim, page_size, num_total_pages,
+                     num_indices, sm_scale, dtype, workspace, workspace_bytes, stream, false);
+}
+
+pd_status pd_paged_tree_decode_fp8(const void* q, const void* k_data, const void* v_data, const float* k_scale,
+                                   const float* v_scale, const int32_t* indices, const int32_t* indptr,
+                                   const int32_t* last_page_len, const int32_t* new_indptr, const uint32_t* tree_mask,
+                                   void* o, float* lse, int batch, int total_new, int mask_words, int num_qo_heads,
+                                   int num_kv_heads, int head_dim, int page_size, int num_total_pages, int num_indices,
+                                   float sm_scale, pd_dtype dtype, void* workspace, size_t workspace_bytes,
+                                   void* stream) {
+    return tree_impl(q, k_data, v_data, k_scale, v_scale, indices, indptr, last_page_len, new_indptr, tree_mask, o, lse,
+                     batch, total_new, mask_words, num_qo_heads, num_kv_heads, head_dim, page_size, num_total_pages,
+                     num_indices, sm_scale, dtype, workspace, workspace_bytes, stream, true);
+}
+
+}  // extern "C"

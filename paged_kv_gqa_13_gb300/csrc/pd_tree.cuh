@@ -1,0 +1,498 @@
+// Attention of several query tokens per request (a chain or a tree of drafted
+// tokens, or a piece of a prompt) over a paged KV cache: the work partition
+// and its walk, the merge of split segments, and the CUDA-core kernel.
+//
+// Segments. The rows of one request and one tile of q heads of a kv head (at
+// most `hpt` heads) are cut into segments of up to `nps` nodes; a segment's
+// rows share every K/V row that they read. Its keys are cut into blocks of
+// `spb` slots of `slot_rows` tokens (a page is `cpp` slots; a page that is not
+// a whole number of slots leaves rows of its last one unused). In a chain a
+// segment's blocks end with its last node's own token.
+//
+// Partition. The blocks of all segments, in the order (request, head tile,
+// segment, block), are one line of U units, cut into equal ranges of W = ceil(U
+// / grid), one per CTA. A segment inside one range is written out by its CTA;
+// one that crosses ranges leaves a partial (o, lse) per CTA, and the merge
+// kernel combines them in CTA order. Only the device knows the lengths: every
+// CTA sums the requests' units itself (each thread a run of requests, one
+// block-wide scan) and finds its place; the first CTA past a boundary inside a
+// segment that starts in the range before writes the merge's descriptor.
+#pragma once
+
+#include "pd_merge.cuh"
+
+namespace pd {
+
+constexpr int kFlagBadNewRows = 0x10;
+
+struct TreeSplit {
+    int parts;       // 0: nothing to merge
+    int row0;        // the request's first q row + the segment's first node
+    int nodes;       // nodes of the segment
+    int hh;          // head tile
+    int c0;          // CTA of the first part
+    int slot0;       // its partial slot; part p > 0 is in slot 2 (c0 + p)
+    int pad[2];
+};
+
+struct TreeArgs {
+    const void* q;
+    const void* k;
+    const void* v;
+    const int32_t* indices;
+    const int32_t* indptr;
+    const int32_t* last_page_len;
+    const int32_t* new_indptr;
+    const uint32_t* mask;  // null: a chain
+    void* o;
+    float* lse;
+    const float* k_scale;  // E4M3 pools
+    const float* v_scale;
+    float* part_o;    // [2 * grid][seg_rows][D], normalised
+    float* part_lse;  // [2 * grid][seg_rows], log2 units
+    TreeSplit* splits;  // [grid]
+    int* flags;
+    int batch, total_new, mask_words, num_qo_heads, num_kv_heads, group;
+    int page_size, num_total_pages, num_indices;
+    int hs, hpt;         // head tiles per group, q heads per tile (the last may hold fewer)
+    int npt, nps;        // nodes per row tile, nodes per segment (one or two row tiles)
+    int tile_rows, seg_rows;  // rows of a row tile and of a segment, as the partials are laid out
+    int slot_rows, cpp, spb;
+    float scale_log2;    // sm_scale * log2(e)
+    int test_extra_tx;
+};
+
+// One request as the table gives it. A bad one keeps its nodes and loses its
+// tokens (len 0), so that every one of its rows is written as empty.
+struct TreeReq {
+    int n = 0, start = 0;  // nodes, first q row
+    int len = 0, lo = 0;   // tokens, first entry of indices
+    int bad = 0;
+    __device__ __forceinline__ int ctx() const { return len - n; }
+};
+
+__device__ __forceinline__ TreeReq tree_request(const TreeArgs& a, int b) {
+    TreeReq r;
+    const int s = __ldg(a.new_indptr + b), e = __ldg(a.new_indptr + b + 1);
+    const int lo = __ldg(a.indptr + b), hi = __ldg(a.indptr + b + 1);
+    int last = __ldg(a.last_page_len + b);
+    if (s < 0 || e < s || e > a.total_new) {
+        r.bad = kFlagBadNewRows;
+        return r;
+    }
+    r.start = s;
+    r.n = e - s;
+    if (lo < 0 || hi < lo || hi > a.num_indices) {
+        r.bad = kFlagBadIndptr;
+        return r;
+    }
+    long long len = 0;
+    if (hi > lo) {
+        if (last < 0 || last > a.page_size) {
+            r.bad = kFlagBadLastPageLen;
+            last = last < 0 ? 0 : a.page_size;
+        }
+        len = (long long)(hi - lo - 1) * a.page_size + last;
+    }
+    if (len < r.n || len > 0x3fffffff) {
+        r.bad |= kFlagBadNewRows;
+        return r;
+    }
+    r.len = int(len);
+    r.lo = lo;
+    return r;
+}
+
+__device__ __forceinline__ int tree_slots(const TreeArgs& a, int tokens) {
+    return tokens / a.page_size * a.cpp + (tokens % a.page_size + a.slot_rows - 1) / a.slot_rows;
+}
+
+// Key blocks of segment tau; at least one, so that a segment with no keys is still written.
+__device__ __forceinline__ int tree_blocks(const TreeArgs& a, const TreeReq& r, int tau) {
+    int limit = r.len;
+    if (a.mask == nullptr) limit = min(limit, max(0, r.ctx()) + min(r.n, (tau + 1) * a.nps));
+    return max(1, (tree_slots(a, limit) + a.spb - 1) / a.spb);
+}
+
+__device__ __forceinline__ long long tree_cost(const TreeArgs& a, const TreeReq& r) {
+    const int segs = (r.n + a.nps - 1) / a.nps;
+    long long sum = 0;
+    if (a.mask != nullptr || segs <= 1) {
+        sum = segs > 0 ? (long long)segs * tree_blocks(a, r, segs - 1) : 0;
+    } else {
+        for (int t = 0; t < segs; ++t) sum += tree_blocks(a, r, t);
+    }
+    return sum * a.hs * a.num_kv_heads;
+}
+
+// A CTA's place on the line of units, and the walk over its segments.
+struct TreeWalk {
+    int b, hh, tau, blk;
+    long long unit, end;  // current unit and the end of this CTA's range
+    long long W;
+    TreeReq r;
+
+    // One portion of a segment: blocks [blk0, blk1) of nblk.
+    struct Seg {
+        int hh, kvh, head0, heads;   // head tile, its kv head, its first q head and how many
+        int row0, node0, nodes;      // first q row, first node within the request, nodes
+        int blk0, blk1;
+        int slot;                    // partial slot; -1: the whole segment, written out
+        TreeReq r;
+    };
+
+    __device__ __forceinline__ bool next(const TreeArgs& a, Seg* s) {
+        if (unit >= end) return false;
+        while (tau * a.nps >= r.n) {  // past the request's last segment
+            tau = 0;
+            if (++hh >= a.hs * a.num_kv_heads || r.n == 0) {
+                hh = 0;
+                if (++b >= a.batch) return false;
+                r = tree_request(a, b);
+            }
+        }
+        const int nblk = tree_blocks(a, r, tau);
+        s->r = r;
+        s->hh = hh;
+        s->kvh = hh / a.hs;
+        const int h0 = (hh % a.hs) * a.hpt;
+        s->head0 = s->kvh * a.group + h0;
+        s->heads = min(a.hpt, a.group - h0);
+        s->node0 = tau * a.nps;
+        s->nodes = min(a.nps, r.n - s->node0);
+        s->row0 = r.start + s->node0;
+        s->blk0 = blk;
+        s->blk1 = int(min((long long)nblk, blk + (end - unit)));
+        const long long begin = unit - blk;
+        s->slot = (blk == 0 && s->blk1 == nblk) ? -1 : 2 * int(blockIdx.x) + (begin > end_of_previous() ? 1 : 0);
+        unit += s->blk1 - s->blk0;
+        blk = 0;
+        ++tau;
+        return true;
+    }
+    __device__ __forceinline__ long long end_of_previous() const { return (long long)blockIdx.x * W; }
+};
+
+struct TreePlanScratch {
+    long long sums[32];
+    int b, hh, tau, blk;
+    long long total;
+};
+
+// Find this CTA's range. All threads of the block call it; ends with a block barrier.
+__device__ __forceinline__ TreeWalk tree_plan(const TreeArgs& a, TreePlanScratch* sc) {
+    const int tid = threadIdx.x, lane = tid & 31, wid = tid >> 5, nt = blockDim.x, nw = nt >> 5;
+    const int per = (a.batch + nt - 1) / nt;
+    const int b0 = min(tid * per, a.batch), b1 = min(b0 + per, a.batch);
+    long long mine = 0;
+    for (int b = b0; b < b1; ++b) {
+        const TreeReq r = tree_request(a, b);
+        if (r.bad != 0 && blockIdx.x == 0) atomicOr(a.flags, r.bad);
+        mine += tree_cost(a, r);
+    }
+    long long inc = mine;
+#pragma unroll
+    for (int off = 1; off < 32; off <<= 1) {
+        const long long x = __shfl_up_sync(kFull, inc, off);
+        if (lane >= off) inc += x;
+    }
+    if (lane == 31) sc->sums[wid] = inc;
+    if (tid == 0) sc->b = -1;
+    __syncthreads();
+    long long before = inc - mine, total = 0;
+    for (int w = 0; w < nw; ++w) {
+        const long long x = sc->sums[w];
+        if (w < wid) before += x;
+        total += x;
+    }
+    TreeWalk wk;
+    wk.W = (total + gridDim.x - 1) / gridDim.x;
+    wk.unit = (long long)blockIdx.x * wk.W;
+    wk.end = min(wk.unit + wk.W, total);
+    if (wk.unit < wk.end && before <= wk.unit && wk.unit < before + mine) {
+        long long left = wk.unit - before;
+        for (int b = b0; b < b1; ++b) {
+            const TreeReq r = tree_request(a, b);
+            const long long c = tree_cost(a, r);
+            if (left >= c) {
+                left -= c;
+                continue;
+            }
+            const long long each = c / (a.hs * a.num_kv_heads);
+            sc->hh = int(left / each);
+            left %= each;
+            int tau = 0;
+            for (;; ++tau) {
+                const int nb = tree_blocks(a, r, tau);
+                if (left < nb) break;
+                left -= nb;
+            }
+            sc->tau = tau;
+            sc->blk = int(left);
+            sc->b = b;
+            break;
+        }
+    }
+    __syncthreads();
+    wk.b = sc->b;
+    wk.hh = sc->hh;
+    wk.tau = sc->tau;
+    wk.blk = sc->blk;
+    if (wk.b < 0) {
+        wk.end = wk.unit;
+    } else {
+        wk.r = tree_request(a, wk.b);
+    }
+    // the merge's descriptor of a segment that starts in the previous range and reaches into this one
+    if (tid == 0) {
+        TreeSplit s{};
+        const long long begin = wk.unit - wk.blk, prev = wk.unit - wk.W;
+        if (wk.b >= 0 && wk.blk > 0 && begin >= prev) {
+            const long long stop = begin + tree_blocks(a, wk.r, wk.tau);
+            s.c0 = int(blockIdx.x) - 1;
+            s.parts = int((stop - 1) / wk.W) - s.c0 + 1;
+            s.slot0 = 2 * s.c0 + (begin > prev ? 1 : 0);
+            s.hh = wk.hh;
+            s.row0 = wk.r.start + wk.tau * a.nps;
+            s.nodes = min(a.nps, wk.r.n - wk.tau * a.nps);
+        }
+        a.splits[blockIdx.x] = s;
+    }
+    return wk;
+}
+
+// Which of 32 consecutive tokens t0 .. t0 + 31 (only the first `count` stand
+// for tokens) node `node` of the request attends, as bits.
+__device__ __forceinline__ uint32_t tree_allow(const TreeArgs& a, const TreeReq& r, int node, int t0, int count) {
+    uint32_t bits = count >= 32 ? ~0u : count <= 0 ? 0u : (1u << count) - 1u;
+    if (t0 + 32 > r.len) bits &= r.len <= t0 ? 0u : r.len - t0 >= 32 ? ~0u : (1u << (r.len - t0)) - 1u;
+    const int i0 = t0 - r.ctx();  // node index of t0
+    if (i0 + 32 <= 0 || bits == 0u) return bits;
+    if (a.mask == nullptr) {
+        const int seen = node + 1 - i0;  // tokens t0 .. of the chain up to the node itself
+        return bits & (seen >= 32 ? ~0u : seen <= 0 ? 0u : (1u << seen) - 1u);
+    }
+    const uint32_t* row = a.mask + size_t(r.start + node) * a.mask_words;
+    auto word = [&](int w) { return w < 0 ? ~0u : w < a.mask_words ? __ldg(row + w) : 0u; };
+    const int w = i0 >= 0 ? i0 / 32 : -1, sh = i0 - 32 * w;  // sh in 0 .. 31
+    return bits & __funnelshift_r(word(w), word(w + 1), sh);
+}
+
+// q row (and o row) index of row `row` of a segment, or -1.
+__device__ __forceinline__ long long tree_row(const TreeArgs& a, int row0, int nodes, int hh, int row) {
+    const int tile = row / a.tile_rows, x = row % a.tile_rows;
+    const int node = tile * a.npt + x / a.hpt, h = (hh % a.hs) * a.hpt + x % a.hpt;
+    if (x >= a.npt * a.hpt || node >= nodes || h >= a.group) return -1;
+    return (long long)(row0 + node) * a.num_qo_heads + hh / a.hs * a.group + h;
+}
+
+// One warp per row of a split segment: parts in CTA order.
+template <typename T, int D>
+__global__ void __launch_bounds__(256) tree_merge_kernel(const TreeArgs a) {
+    constexpr int kPer = D / 32;
+    const float kNegInf = -__int_as_float(0x7f800000);
+    grid_dependency_wait();
+    const TreeSplit s = a.splits[blockIdx.x + 1];
+    if (s.parts == 0) return;
+    const int row = int(blockIdx.y) * 8 + (threadIdx.x >> 5);
+    const long long at = row < a.seg_rows ? tree_row(a, s.row0, s.nodes, s.hh, row) : -1;
+    if (at < 0) return;
+    auto slot = [&](int p) { return size_t(p == 0 ? s.slot0 : 2 * (s.c0 + p)) * a.seg_rows + row; };
+    float acc[kPer] = {};
+    const float L = merge_rows<kPer, 8>(
+        s.parts, [&](int p) { return a.part_lse[slot(p)]; }, [&](int p) { return a.part_o + slot(p) * D; }, acc);
+    store_row<T, kPer>(static_cast<T*>(a.o) + at * D, acc);
+    if ((threadIdx.x & 31) == 0) a.lse[at] = L == kNegInf ? kNegInf : L * kLn2;
+}
+
+// ---------------------------------------------------------------- CUDA cores
+
+// Eight or four elements of a pool row to f32.
+template <typename KV>
+__device__ __forceinline__ void pool_load4(const KV* p, float s, float* f) {
+    if constexpr (sizeof(KV) == 4) {
+        const float4 x = __ldg(reinterpret_cast<const float4*>(p));
+        f[0] = x.x, f[1] = x.y, f[2] = x.z, f[3] = x.w;
+    } else if constexpr (sizeof(KV) == 2) {
+        const uint2 w = __ldg(reinterpret_cast<const uint2*>(p));
+        float t[8];
+        Elt<KV>::to_f32(make_uint4(w.x, w.y, 0u, 0u), t);
+        f[0] = t[0], f[1] = t[1], f[2] = t[2], f[3] = t[3];
+    } else {
+        float t[8];
+        e4m3x8_to_f32(make_uint2(__ldg(reinterpret_cast<const uint32_t*>(p)), 0u), t);
+        f[0] = t[0] * s, f[1] = t[1] * s, f[2] = t[2] * s, f[3] = t[3] * s;
+    }
+}
+
+template <int D>
+struct CfgTreeCc {
+    static constexpr int kRows = 32, kKeys = 32, kThreads = 128, kBlockTokens = 128;
+    static constexpr int kLd = D + 4;  // row step of q and K in shared memory: 16-byte reads of 8 rows hit all banks
+    static constexpr int kFloats = 2 * kRows * kLd + kKeys * D + kRows * (kKeys + 1);
+    static constexpr int kBytes = kFloats * 4;
+    static constexpr int kBlocksPerSm = D == 64 ? 6 : D == 128 ? 4 : 2;
+};
+
+// f32 arithmetic on CUDA cores: f32 q (no tensor-core type holds it) and
+// groups of more than 128 heads. 32 rows x 32 keys per step: thread (tr, tc)
+// of 16 x 8 holds rows 2 tr, 2 tr + 1: scores of keys tc + 8 i, outputs of
+// columns 4 tc + 32 i. The 8 lanes of a row sit in one warp, so the softmax
+// needs no block barrier. Bound by FFMA issue: 4 D flops per row and key
+// against shared-memory reads of 6 (scores) and 1 (outputs) vectors per 32 and
+// 8 multiply-adds.
+template <typename T, typename KV, int D>
+__global__ void __launch_bounds__(128, CfgTreeCc<D>::kBlocksPerSm) tree_cc_kernel(const TreeArgs a) {
+    using C = CfgTreeCc<D>;
+    const float kNegInf = -__int_as_float(0x7f800000);
+    extern __shared__ __align__(16) float tree_smem[];
+    __shared__ TreePlanScratch plan;
+    __shared__ long long row_off[C::kKeys];  // element offset of each key's row in the pools; -1: none
+    float* sq = tree_smem;
+    float* sk = sq + C::kRows * C::kLd;
+    float* sv = sk + C::kKeys * C::kLd;
+    float* sp = sv + C::kKeys * D;
+    const int tid = threadIdx.x, tr = tid >> 3, tc = tid & 7;
+    TreeWalk walk = tree_plan(a, &plan);
+    launch_dependents();
+    TreeWalk::Seg s;
+    while (walk.next(a, &s)) {
+        __syncthreads();
+        const float ks = a.k_scale != nullptr ? __ldg(a.k_scale + s.kvh) : 1.f;
+        const float vs = a.v_scale != nullptr ? __ldg(a.v_scale + s.kvh) : 1.f;
+        for (int i = tid; i < C::kRows * (D / 4); i += C::kThreads) {
+            const int row = i / (D / 4), e = i % (D / 4) * 4;
+            const long long at = tree_row(a, s.row0, s.nodes, s.hh, row);
+            float f[4] = {};
+            if (at >= 0) pool_load4(static_cast<const T*>(a.q) + at * D + e, 1.f, f);
+            *reinterpret_cast<float4*>(sq + row * C::kLd + e) = make_float4(f[0], f[1], f[2], f[3]);
+        }
+        float m[2] = {kNegInf, kNegInf}, l[2] = {}, o[2][D / 8] = {};
+        const int node[2] = {s.node0 + 2 * tr / a.hpt, s.node0 + (2 * tr + 1) / a.hpt};
+        for (int t0 = s.blk0 * C::kBlockTokens; t0 < min(s.blk1 * C::kBlockTokens, s.r.len); t0 += C::kKeys) {
+            __syncthreads();
+            if (tid < C::kKeys) {
+                const int t = t0 + tid;
+                long long off = -1;
+                if (t < s.r.len) {
+                    const int page = __ldg(a.indices + s.r.lo + t / a.page_size);
+                    if (page >= 0 && page < a.num_total_pages)
+                        off = (((long long)page * a.num_kv_heads + s.kvh) * a.page_size + t % a.page_size) * D;
+                    else
+                        atomicOr(a.flags, kFlagBadPage);
+                }
+                row_off[tid] = off;
+            }
+            __syncthreads();
+            for (int i = tid; i < C::kKeys * (D / 4); i += C::kThreads) {
+                const int key = i / (D / 4), e = i % (D / 4) * 4;
+                const long long off = row_off[key];
+                float fk[4] = {}, fv[4] = {};
+                if (off >= 0) {
+                    pool_load4(static_cast<const KV*>(a.k) + off + e, ks, fk);
+                    pool_load4(static_cast<const KV*>(a.v) + off + e, vs, fv);
+                }
+                *reinterpret_cast<float4*>(sk + key * C::kLd + e) = make_float4(fk[0], fk[1], fk[2], fk[3]);
+                *reinterpret_cast<float4*>(sv + key * D + e) = make_float4(fv[0], fv[1], fv[2], fv[3]);
+            }
+            __syncthreads();
+            float x[2][4] = {};
+#pragma unroll 4
+            for (int e = 0; e < D; e += 4) {
+                const float4 q0 = *reinterpret_cast<const float4*>(sq + (2 * tr) * C::kLd + e);
+                const float4 q1 = *reinterpret_cast<const float4*>(sq + (2 * tr + 1) * C::kLd + e);
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    const float4 k = *reinterpret_cast<const float4*>(sk + (tc + 8 * i) * C::kLd + e);
+                    x[0][i] = fmaf(q0.w, k.w, fmaf(q0.z, k.z, fmaf(q0.y, k.y, fmaf(q0.x, k.x, x[0][i]))));
+                    x[1][i] = fmaf(q1.w, k.w, fmaf(q1.z, k.z, fmaf(q1.y, k.y, fmaf(q1.x, k.x, x[1][i]))));
+                }
+            }
+            const bool tail = t0 + C::kKeys > s.r.ctx();  // holds tokens that some row does not attend
+#pragma unroll
+            for (int j = 0; j < 2; ++j) {
+                const uint32_t allow = tree_allow(a, s.r, min(node[j], s.r.n - 1), t0, C::kKeys);
+                float top = kNegInf;
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    const bool in = ((allow >> (tc + 8 * i)) & 1u) != 0 && row_off[tc + 8 * i] >= 0;
+                    x[j][i] = in ? x[j][i] * a.scale_log2 : kNegInf;
+                    top = fmaxf(top, x[j][i]);
+                }
+#pragma unroll
+                for (int off = 1; off < 8; off <<= 1) top = fmaxf(top, __shfl_xor_sync(kFull, top, off));
+                const float mn = fmaxf(m[j], top), mu = mn == kNegInf ? 0.f : mn;
+                const float al = ex2(m[j] - mu);
+                m[j] = mn;
+                float sum = 0.f;
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    const float p = ex2(x[j][i] - mu);
+                    sum += p;
+                    sp[(2 * tr + j) * (C::kKeys + 1) + tc + 8 * i] = p;
+                }
+                l[j] = l[j] * al + sum;
+#pragma unroll
+                for (int i = 0; i < D / 8; ++i) o[j][i] *= al;
+            }
+            __syncwarp();
+            auto accumulate = [&](auto guard) {
+#pragma unroll 2
+                for (int key = 0; key < C::kKeys; ++key) {
+                    const float p0 = sp[(2 * tr) * (C::kKeys + 1) + key], p1 = sp[(2 * tr + 1) * (C::kKeys + 1) + key];
+#pragma unroll
+                    for (int i = 0; i < D / 32; ++i) {
+                        const float4 v = *reinterpret_cast<const float4*>(sv + key * D + 4 * tc + 32 * i);
+                        const float f[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+                        for (int c = 0; c < 4; ++c) {
+                            // a row that does not attend the key takes no part of it, not 0 * NaN either
+                            if (!decltype(guard)::value || p0 != 0.f) o[0][4 * i + c] = fmaf(p0, f[c], o[0][4 * i + c]);
+                            if (!decltype(guard)::value || p1 != 0.f) o[1][4 * i + c] = fmaf(p1, f[c], o[1][4 * i + c]);
+                        }
+                    }
+                }
+            };
+            if (tail)
+                accumulate(std::true_type{});
+            else
+                accumulate(std::false_type{});
+            __syncwarp();
+        }
+#pragma unroll
+        for (int j = 0; j < 2; ++j) {
+            const int row = 2 * tr + j;
+            float L = l[j];
+#pragma unroll
+            for (int off = 1; off < 8; off <<= 1) L += __shfl_xor_sync(kFull, L, off);
+            const long long at = tree_row(a, s.row0, s.nodes, s.hh, row);
+            if (at < 0) continue;
+            const float inv = m[j] == kNegInf ? 0.f : 1.f / L;
+            const float lse2 = m[j] == kNegInf ? kNegInf : m[j] + log2f(L);
+#pragma unroll
+            for (int i = 0; i < D / 32; ++i) {
+                float f[8] = {};
+#pragma unroll
+                for (int c = 0; c < 4; ++c) f[c] = o[j][4 * i + c] * inv;
+                const int e = 4 * tc + 32 * i;
+                if (s.slot >= 0) {
+                    *reinterpret_cast<float4*>(a.part_o + (size_t(s.slot) * a.seg_rows + row) * D + e) =
+                        make_float4(f[0], f[1], f[2], f[3]);
+                } else if constexpr (sizeof(T) == 4) {
+                    *reinterpret_cast<float4*>(static_cast<T*>(a.o) + at * D + e) = make_float4(f[0], f[1], f[2], f[3]);
+                } else {
+                    *reinterpret_cast<uint2*>(static_cast<T*>(a.o) + at * D + e) =
+                        make_uint2(Elt<T>::pack(f[0], f[1]), Elt<T>::pack(f[2], f[3]));
+                }
+            }
+            if (tc == 0) {
+                if (s.slot >= 0)
+                    a.part_lse[size_t(s.slot) * a.seg_rows + row] = lse2;
+                else
+                    a.lse[at] = lse2 == kNegInf ? kNegInf : lse2 * kLn2;
+            }
+        }
+    }
+}
+
+}  // namespace pd

@@ -1,0 +1,287 @@
+"""Rotary positions, the rotated paged append and the commit of accepted nodes, against plain 64-bit forms."""
+import math
+
+import numpy as np
+import pytest
+import torch
+
+from tests.spec_helpers import TYPES, Paged, rope_reference, rope_tolerance
+
+pytestmark = pytest.mark.gpu
+
+
+def _inv(rot, theta=10000.0):
+    return theta ** (-2.0 * np.arange(rot // 2) / rot)
+
+
+def _ws():
+    import paged_kv_gqa_13_gb300 as pd
+
+    return pd.alloc_workspace(256)
+
+
+@pytest.mark.parametrize("dtype", ["f32", "f16", "bf16"])
+@pytest.mark.parametrize("layout", [0, 1])
+@pytest.mark.parametrize("tokens,heads,d,rot", [(1, 1, 128, 128), (3, 40, 128, 64), (37, 5, 256, 256), (700, 3, 64, 64),
+                                                (9, 7, 80, 40), (5, 2, 128, 6), (4, 3, 128, 0), (6, 33, 96, 96), (1, 2, 2, 2),
+                                                (2, 1, 4096, 4096)])
+def test_rope_matches_the_formula(dtype, layout, tokens, heads, d, rot):
+    import paged_kv_gqa_13_gb300 as pd
+
+    g = torch.Generator().manual_seed(tokens + d)
+    x = torch.randn(tokens, heads, d, generator=g).to(TYPES[dtype])
+    pos = torch.randint(0, 1 << 20, (tokens,), generator=g, dtype=torch.int32)
+    freqs = pd.pd_rope_frequencies(rot)[0] if rot else torch.zeros(0, dtype=torch.int64, device="cuda")
+    out = torch.full_like(x, math.nan, device="cuda")
+    pd.pd_rope(x.cuda(), pos.cuda(), freqs, out, layout=layout, rope_scale=1.2)
+    ref = rope_reference(x, pos, _inv(rot) if rot else np.zeros(0), layout, 1.2)
+    assert bool(((out.double().cpu() - ref).abs() <= rope_tolerance(x, ref, dtype, 1.2)).all())
+    assert torch.equal(out[..., rot:].cpu(), x[..., rot:])
+
+
+@pytest.mark.parametrize("tokens,heads,d,rot,dtype", [(50, 6, 128, 128, "bf16"), (7, 3, 64, 20, "f16"), (3, 5, 128, 64, "f32")])
+def test_rope_strided_views_in_place_and_unaligned(tokens, heads, d, rot, dtype):
+    import paged_kv_gqa_13_gb300 as pd
+
+    freqs, _ = pd.pd_rope_frequencies(rot)
+    x = torch.randn(tokens, heads + 3, d, dtype=TYPES[dtype], device="cuda")
+    keep = x.clone()
+    pos = torch.arange(tokens, dtype=torch.int32, device="cuda") * 977
+    view = x[:, 1:1 + heads]
+    pd.pd_rope(view, pos, freqs, view)
+    ref = rope_reference(keep[:, 1:1 + heads].cpu(), pos.cpu(), _inv(rot), 0)
+    assert bool(((view.double().cpu() - ref).abs() <= rope_tolerance(keep[:, 1:1 + heads].cpu(), ref, dtype)).all())
+    assert torch.equal(x[:, 0], keep[:, 0]) and torch.equal(x[:, 1 + heads:], keep[:, 1 + heads:])
+    # rows that start one element off a 16-byte boundary
+    flat = torch.randn(tokens * heads * d + 1, dtype=TYPES[dtype], device="cuda")[1:].view(tokens, heads, d)
+    out = torch.empty(tokens * heads * d + 3, dtype=TYPES[dtype], device="cuda")[3:].view(tokens, heads, d)
+    pd.pd_rope(flat, pos, freqs, out, layout=1)
+    ref = rope_reference(flat.cpu(), pos.cpu(), _inv(rot), 1)
+    assert bool(((out.double().cpu() - ref).abs() <= rope_tolerance(flat.cpu(), ref, dtype)).all())
+
+
+def test_rope_far_and_negative_positions_and_inverse():
+    import paged_kv_gqa_13_gb300 as pd
+
+    freqs, _ = pd.pd_rope_frequencies(128, 500000.0)
+    pos = torch.tensor([0, 1, -1, 131071, -131071, 2 ** 31 - 1, -2 ** 31, 10 ** 9], dtype=torch.int32)
+    x = torch.randn(8, 4, 128, generator=torch.Generator().manual_seed(1))
+    out = torch.empty_like(x, device="cuda")
+    pd.pd_rope(x.cuda(), pos.cuda(), freqs, out)
+    # the reference angle in exact integers: position times the table's fraction of a turn, modulo one turn
+    f = [int(v) & (2 ** 64 - 1) for v in freqs.cpu()]
+    turns = np.array([[((int(p) * v) % 2 ** 64) / 2 ** 64 for v in f] for p in pos])
+    c, s = (torch.from_numpy(fn(2 * math.pi * turns))[:, None] for fn in (np.cos, np.sin))
+    a, b = x.double()[..., :64], x.double()[..., 64:]
+    ref = torch.cat([a * c - b * s, b * c + a * s], -1)
+    assert bool(((out.double().cpu() - ref).abs() <= rope_tolerance(x, ref, "f32")).all())
+    back = torch.empty_like(out)
+    pd.pd_rope(out[:6].contiguous(), -pos[:6].cuda(), freqs, back[:6])
+    assert float((back[:6].cpu() - x[:6]).abs().max()) < 1e-5
+
+
+def test_rope_gradient_is_the_rotation_by_the_negated_position():
+    import paged_kv_gqa_13_gb300 as pd
+
+    freqs, _ = pd.pd_rope_frequencies(64)
+    pos = torch.tensor([5, 1000, 77], dtype=torch.int32, device="cuda")
+    x = torch.randn(3, 2, 64, device="cuda")
+    w = torch.randn(3, 2, 64, device="cuda")
+
+    def f(y):
+        out = torch.empty_like(y)
+        pd.pd_rope(y, pos, freqs, out, rope_scale=1.3)
+        return out
+
+    grad = torch.empty_like(w)
+    pd.pd_rope(w, -pos, freqs, grad, rope_scale=1.3)
+    leaf = x.double().cpu().requires_grad_()
+    a = pos.cpu().double()[:, None] * torch.from_numpy(_inv(64))
+    c, s = a.cos()[:, None] * 1.3, a.sin()[:, None] * 1.3
+    u, v = leaf[..., :32], leaf[..., 32:]
+    (torch.cat([u * c - v * s, v * c + u * s], -1) * w.double().cpu()).sum().backward()
+    assert float((grad.double().cpu() - leaf.grad).abs().max()) < 1e-5
+    # the rotation is linear: a difference over any step is the derivative up to f32 rounding
+    dx = torch.randn_like(x)
+    lhs = float(((f(x + dx) - f(x - dx)).double() * w.double()).sum()) / 2
+    assert abs(lhs - float((grad.double() * dx.double()).sum())) < 1e-3
+
+
+def _append_case(dtype, pool, kv, new, hq, hk, d, rot, page, layout, positions, seed=0):
+    import paged_kv_gqa_13_gb300 as pd
+
+    c = Paged(kv, new, hk, d, page, dtype, seed, fp8=pool == "e4m3")
+    g = torch.Generator().manual_seed(seed + 1)
+    t = sum(new)
+    qkv = torch.randn(t, hq + 2 * hk, d, generator=g).to(TYPES[dtype])
+    at = torch.from_numpy(np.concatenate([np.arange(l - n, l) for l, n in zip(kv, new)]).astype(np.int32))
+    pos = at if positions is None else at * 3 + 7
+    dev = qkv.cuda()
+    q_out = torch.empty(t, hq, d, dtype=TYPES[dtype], device="cuda")
+    k, v, ws = c.k.cuda(), c.v.cuda(), _ws()
+    freqs = pd.pd_rope_frequencies(rot)[0] if rot else None
+    scales = (c.k_scale.cuda(), c.v_scale.cuda()) if c.fp8 else ()
+    fn = pd.pd_paged_rope_append_fp8 if c.fp8 else pd.pd_paged_rope_append
+    fn(dev[:, :hq] if hq else None, dev[:, hq:hq + hk], dev[:, hq + hk:], None if positions is None else pos.cuda(), freqs,
+       q_out if hq else None, *scales, k, v, *c.table(), ws, layout=layout)
+    assert pd.pd_read_device_flags(ws) == 0
+    return c, qkv, pos, q_out, k, v
+
+
+@pytest.mark.parametrize("dtype,pool", [("f32", "f32"), ("f16", "f16"), ("bf16", "bf16"), ("f16", "e4m3"), ("bf16", "e4m3")])
+@pytest.mark.parametrize("hq,hk,d,rot,page,layout,positions", [(8, 2, 128, 128, 16, 0, None), (4, 4, 64, 32, 5, 1, "given"),
+                                                               (0, 3, 256, 256, 1, 0, "given"), (7, 1, 128, 10, 32, 1, None),
+                                                               (2, 2, 64, 0, 24, 0, None)])
+def test_append_writes_the_rotated_rows_and_nothing_else(dtype, pool, hq, hk, d, rot, page, layout, positions):
+    kv, new = [1, 40, 16, 0, 33, 7, 100], [1, 3, 16, 0, 17, 0, 70]
+    c, qkv, pos, q_out, k, v = _append_case(dtype, pool, kv, new, hq, hk, d, rot, page, layout, positions)
+    inv = _inv(rot) if rot else np.zeros(0)
+    if hq:
+        ref = rope_reference(qkv[:, :hq], pos, inv, layout)
+        assert bool(((q_out.double().cpu() - ref).abs() <= rope_tolerance(qkv[:, :hq], ref, dtype)).all())
+    ref = rope_reference(qkv[:, hq:hq + hk], pos, inv, layout)
+    tol = rope_tolerance(qkv[:, hq:hq + hk], ref, "f32" if c.fp8 else dtype)
+    kg, vg = k.cpu(), v.cpu()
+    seen = torch.zeros(c.total, page, dtype=torch.bool)
+    for b in range(len(kv)):
+        p, r = c.rows(b, np.arange(kv[b] - new[b], kv[b]))
+        seen[p, r] = True
+        rows = slice(int(c.new_indptr[b]), int(c.new_indptr[b + 1]))
+        if not c.fp8:
+            assert bool(((kg[p, :, r].double() - ref[rows]).abs() <= tol[rows]).all())
+            assert torch.equal(vg[p, :, r], qkv[rows, hq + hk:])
+            continue
+        # the code of a value within the tolerance of the reference
+        got = kg[p, :, r].view(torch.float8_e4m3fn).double()
+        s = c.k_scale[:, None]
+        lo, hi = (((ref[rows] + e * tol[rows]).float() / s).clamp(-448, 448).to(torch.float8_e4m3fn).double() for e in (-1, 1))
+        assert bool(((got >= torch.minimum(lo, hi)) & (got <= torch.maximum(lo, hi))).all())
+        want = (qkv[rows, hq + hk:].float() / c.v_scale[:, None]).clamp(-448, 448).to(torch.float8_e4m3fn).view(torch.uint8)
+        assert torch.equal(vg[p, :, r], want)
+    same = lambda x, y: torch.equal(x.permute(0, 2, 1, 3)[~seen].contiguous().view(torch.uint8),  # noqa: E731
+                                    y.permute(0, 2, 1, 3)[~seen].contiguous().view(torch.uint8))
+    assert same(kg, c.k) and same(vg, c.v)
+
+
+def test_append_many_requests_finds_each_tokens_request():
+    rng = np.random.default_rng(3)
+    new = [int(x) for x in rng.integers(0, 4, 1500)]
+    kv = [n + int(x) for n, x in zip(new, rng.integers(0, 20, 1500))]
+    c, qkv, pos, _, k, v = _append_case("f16", "f16", kv, new, 0, 1, 64, 64, 8, 0, None)
+    vg = v.cpu()
+    for b in range(len(kv)):
+        p, r = c.rows(b, np.arange(kv[b] - new[b], kv[b]))
+        assert torch.equal(vg[p, :, r], qkv[int(c.new_indptr[b]):int(c.new_indptr[b + 1]), 1:])
+
+
+def test_append_flags_bad_tables_and_writes_the_others():
+    import paged_kv_gqa_13_gb300 as pd
+
+    kv, new = [20, 30, 10, 12], [2, 3, 2, 4]
+    c = Paged(kv, new, 2, 64, 16, "f16")
+    rows = torch.randn(sum(new), 2, 64).half().cuda()
+    freqs, _ = pd.pd_rope_frequencies(64)
+
+    def run(change):
+        t = [x.clone() for x in c.table()]
+        change(t)
+        k, v, ws = c.k.cuda(), c.v.cuda(), _ws()
+        pd.pd_paged_rope_append(None, rows, rows, None, freqs, None, k, v, *t, ws)
+        got = v.cpu()
+        ok = []
+        for b in range(4):
+            p, r = c.rows(b, np.arange(kv[b] - new[b], kv[b]))
+            ok.append(torch.equal(got[p, :, r], rows[int(c.new_indptr[b]):int(c.new_indptr[b + 1])].cpu()))
+        return pd.pd_read_device_flags(ws), ok
+
+    def page(t):
+        t[0][int(c.indptr[2]) - 1] = c.total
+
+    assert run(page) == (pd.PD_FLAG_BAD_PAGE_ID, [True, False, True, True])
+
+    def last(t):
+        t[2][1] = 17
+
+    assert run(last) == (pd.PD_FLAG_BAD_LAST_PAGE_LEN, [True, False, True, True])
+
+    def many(t):
+        t[2][2] = 1  # one token, two new rows
+
+    assert run(many) == (pd.PD_FLAG_BAD_NEW_ROWS, [True, True, False, True])
+
+    def short(t):
+        t[3][4] -= 1  # the last token belongs to no request
+
+    flags, ok = run(short)
+    assert flags == pd.PD_FLAG_BAD_NEW_ROWS and ok[:3] == [True, True, True]
+
+
+def test_append_on_another_stream_and_in_a_graph():
+    import paged_kv_gqa_13_gb300 as pd
+
+    c = Paged([33, 5], [4, 1], 2, 128, 16, "bf16")
+    rows = torch.randn(5, 2, 128).bfloat16().cuda()
+    freqs, _ = pd.pd_rope_frequencies(128)
+    k, v, ws, t = c.k.cuda(), c.v.cuda(), _ws(), c.table()
+    k1, v1 = k.clone(), v.clone()
+    pd.pd_paged_rope_append(None, rows, rows, None, freqs, None, k1, v1, *t, ws)
+    torch.cuda.synchronize()
+    side = torch.cuda.Stream()
+    k2, v2 = k.clone(), v.clone()
+    torch.cuda.synchronize()
+    pd.pd_paged_rope_append(None, rows, rows, None, freqs, None, k2, v2, *t, ws, stream=side)
+    side.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    k3, v3 = k.clone(), v.clone()
+    torch.cuda.synchronize()
+    with torch.cuda.graph(graph):
+        pd.pd_paged_rope_append(None, rows, rows, None, freqs, None, k3, v3, *t, ws)
+    graph.replay()
+    torch.cuda.synchronize()
+    for a, b in ((k1, k2), (v1, v2), (k1, k3), (v1, v3)):
+        assert torch.equal(a.view(torch.int16), b.view(torch.int16))
+
+
+@pytest.mark.parametrize("fp8", [False, True])
+@pytest.mark.parametrize("d,page", [(64, 16), (128, 5), (256, 1), (128, 32)])
+def test_commit_moves_the_accepted_rows(fp8, d, page):
+    import paged_kv_gqa_13_gb300 as pd
+
+    kv, new = [50, 12, 9, 200, 40, 30], [10, 12, 0, 64, 33, 6]
+    paths = [[1, 2, 3, 7], [0, 1, 2], [], sorted(np.random.default_rng(0).choice(64, 41, replace=False)), list(range(33)), []]
+    c = Paged(kv, new, 3, d, page, "f16", fp8=fp8)
+    most = max(len(p) for p in paths)
+    path = torch.full((6, most), -9, dtype=torch.int32)
+    for b, p in enumerate(paths):
+        path[b, :len(p)] = torch.tensor([int(x) for x in p], dtype=torch.int32)
+    plen = torch.tensor([len(p) for p in paths], dtype=torch.int32)
+    k, v, ws = c.k.cuda(), c.v.cuda(), _ws()
+    pd.pd_paged_tree_commit(k, v, *c.table(), path.cuda(), plen.cuda(), ws, total_new=sum(new))
+    assert pd.pd_read_device_flags(ws) == 0
+    for got, old in ((k.cpu(), c.k), (v.cpu(), c.v)):
+        want = old.clone()
+        for b, p in enumerate(paths):
+            first = kv[b] - new[b]
+            src, dst = c.rows(b, first + np.array(p, np.int64)), c.rows(b, first + np.arange(len(p)))
+            want[dst[0], :, dst[1]] = old[src[0], :, src[1]]
+        assert torch.equal(got.view(torch.uint8), want.view(torch.uint8))
+
+
+def test_commit_flags_bad_paths_and_leaves_those_requests():
+    import paged_kv_gqa_13_gb300 as pd
+
+    kv, new = [20, 20, 20, 20, 20], [6, 6, 6, 6, 6]
+    c = Paged(kv, new, 2, 64, 16, "f16")
+    path = torch.tensor([[2, 1], [1, 6], [-1, 3], [2, 4], [1, 2]], dtype=torch.int32)
+    k, v, ws, t = c.k.cuda(), c.v.cuda(), _ws(), c.table()
+    pd.pd_paged_tree_commit(k, v, *t, path.cuda(), torch.tensor([2, 2, 2, 2, 3], dtype=torch.int32).cuda(), ws)
+    assert pd.pd_read_device_flags(ws) == pd.PD_FLAG_BAD_PATH
+    want = c.k.clone()
+    src, dst = c.rows(3, np.array([16, 18])), c.rows(3, np.array([14, 15]))
+    want[dst[0], :, dst[1]] = c.k[src[0], :, src[1]]
+    assert torch.equal(k.cpu().view(torch.uint8), want.view(torch.uint8))
+    t[0][int(c.indptr[3])] = -1  # a bad page under the nodes of request 3
+    ws = _ws()
+    k = c.k.cuda()
+    pd.pd_paged_tree_commit(k, v, *t, path.cuda(), torch.tensor([0, 0, 0, 2, 0], dtype=torch.int32).cuda(), ws)
+    assert pd.pd_read_device_flags(ws) == pd.PD_FLAG_BAD_PAGE_ID

@@ -4,18 +4,10 @@
 
 #include "pd_host.h"
 #include "pd_tree.cuh"
+#include "pd_tree_kernels.h"
 
 namespace pd {
 namespace {
-
-struct TreeKernels {
-    const void* main;
-    const void* merge;
-    int threads, smem, per_sm;       // of main
-    int tile_rows, tiles;            // rows of a row tile, row tiles per segment
-    int block_tokens;                // tokens of a key block
-    bool tensor;
-};
 
 template <typename T, typename KV, int D>
 TreeKernels cc_kernels() {
@@ -42,14 +34,44 @@ bool cc_by_dim(int D, TreeKernels* k) {
     return false;
 }
 
+// 16-bit q of a group that fits a row tile runs on the tensor cores; f32 q,
+// which no tensor-core type holds, and larger groups on CUDA cores.
 bool pick(pd_dtype dt, bool fp8, int D, int group, TreeKernels* k) {
-    (void)group;
+    if (dt != PD_F32 && group <= 128 && !fp8)
+        return dt == PD_F16 ? tree_tc_f16(D, k) : tree_tc_bf16(D, k);
     switch (dt) {
         case PD_F32: return !fp8 && cc_by_dim<float, float>(D, k);
         case PD_F16: return fp8 ? cc_by_dim<__half, uint8_t>(D, k) : cc_by_dim<__half, __half>(D, k);
-        case PD_BF16: return fp8 ? cc_by_dim<__nv_bfloat16, uint8_t>(D, k) : cc_by_dim<__nv_bfloat16, __nv_bfloat16>(D, k);
+        case PD_BF16:
+            return fp8 ? cc_by_dim<__nv_bfloat16, uint8_t>(D, k) : cc_by_dim<__nv_bfloat16, __nv_bfloat16>(D, k);
     }
     return false;
+}
+
+pd_status encode(CUtensorMap* map, pd_dtype dt, int rank, const void* base, const cuuint64_t* dims,
+                 const cuuint64_t* strides, const cuuint32_t* box) {
+    PFN_cuTensorMapEncodeTiled_v12000 enc = host::tensor_map_encoder();
+    if (enc == nullptr) return host::fail(PD_ERR_CUDA, "cuTensorMapEncodeTiled is not available from the driver");
+    const cuuint32_t ones[4] = {1, 1, 1, 1};
+    const CUresult r = enc(map, dt == PD_BF16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16,
+                           cuuint32_t(rank), const_cast<void*>(base), dims, strides, box, ones,
+                           CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                           CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+    return r == CUDA_SUCCESS ? PD_OK : host::fail(PD_ERR_CUDA, "cuTensorMapEncodeTiled failed (%d)", int(r));
+}
+
+// Boxes of 64 columns: of q {64, heads of a tile, nodes of a row tile}, of K and V {64, rows of a slot}.
+pd_status make_maps(const TreeArgs& a, pd_dtype dt, int D, CUtensorMap* q, CUtensorMap* k, CUtensorMap* v) {
+    const cuuint64_t e = 2, d = cuuint64_t(D), ps = cuuint64_t(a.page_size), hk = cuuint64_t(a.num_kv_heads),
+                     hq = cuuint64_t(a.num_qo_heads);
+    const cuuint64_t qd[3] = {d, hq, cuuint64_t(a.total_new)}, qs[2] = {d * e, hq * d * e};
+    const cuuint32_t qb[3] = {64, cuuint32_t(a.hpt), cuuint32_t(a.npt)};
+    pd_status st = encode(q, dt, 3, a.q, qd, qs, qb);
+    if (st != PD_OK) return st;
+    const cuuint64_t kd[4] = {d, ps, hk, cuuint64_t(a.num_total_pages)}, ks[3] = {d * e, ps * d * e, hk * ps * d * e};
+    const cuuint32_t kb[4] = {64, cuuint32_t(a.slot_rows), 1, 1};
+    if ((st = encode(k, dt, 4, a.k, kd, ks, kb)) != PD_OK) return st;
+    return encode(v, dt, 4, a.v, kd, ks, kb);
 }
 
 size_t round256(size_t x) { return (x + 255) / 256 * 256; }
@@ -143,8 +165,13 @@ pd_status tree_impl(const void* q, const void* k_data, const void* v_data, const
     a.npt = kn.tile_rows / a.hpt;
     a.nps = a.npt * kn.tiles;
     a.slot_rows = 1;
-    a.cpp = page_size;
-    a.spb = kn.block_tokens;
+    if (kn.tensor) {
+        // a slot is one copy: the largest power of two that divides the page, from 8 rows (the swizzle's period) to a block
+        a.slot_rows = 8;
+        while (a.slot_rows < kn.block_tokens && page_size % (2 * a.slot_rows) == 0) a.slot_rows *= 2;
+    }
+    a.cpp = (page_size + a.slot_rows - 1) / a.slot_rows;
+    a.spb = kn.block_tokens / a.slot_rows;
     a.scale_log2 = sm_scale * kLog2e;
 
     // No more CTAs than there can be units: segments x key blocks of the longest possible request.
@@ -154,7 +181,9 @@ pd_status tree_impl(const void* q, const void* k_data, const void* v_data, const
     const int grid = int(bound < most ? bound : most);
     cudaStream_t cs = static_cast<cudaStream_t>(stream);
     if ((st = host::allow_smem(kn.main, kn.smem)) != PD_OK) return st;
-    void* args[] = {&a};
+    CUtensorMap maps[3];
+    if (kn.tensor && (st = make_maps(a, dt, D, &maps[0], &maps[1], &maps[2])) != PD_OK) return st;
+    void* args[] = {&a, &maps[0], &maps[1], &maps[2]};
     cudaError_t e = cudaLaunchKernel(kn.main, dim3(grid), dim3(kn.threads), args, kn.smem, cs);
     if (e != cudaSuccess) return host::cuda_fail(e, "tree decode launch");
     if (grid > 1 && blocks > 1) {  // otherwise no segment can be split

@@ -1,0 +1,666 @@
+// Tree decode on the 5th-generation tensor cores (tcgen05.mma kind::f16, f32
+// accumulators in tensor memory) for 16-bit q over 16-bit paged pools.
+//
+// A row tile is up to 128 rows (nodes x q heads of one kv head): the M of both
+// products. Per block of KB keys and row tile: S = Q K^T (A = Q and B = K from
+// shared memory, K-major as they lie), then the softmax warps turn S into
+// weights P in place (tensor memory), then O += P V (A = P from tensor memory,
+// B = V from shared memory, MN-major as it lies).
+//
+// Two row-tile pipelines t = 0, 1, each with its own S/P and O columns and its
+// own 4 softmax warps, run out of phase: while one's softmax runs, the tensor
+// cores work for the other. A segment of more than one row tile (up to two)
+// gives each pipeline its own rows, both over every block ("wide"); one of a
+// single row tile gives both the same rows over alternate blocks, and joins
+// the two (m, l, O) at the end. At head_dim 256 tensor memory holds one O:
+// blocks of 64 keys, S double-buffered, one set of softmax warps.
+//
+// Roles (16 warps): 0-3 and 4-7 softmax of pipeline 0 and 1; 8 producer (TMA
+// of q, K and V into a ring of slots of one K or V block); 9 issues the mma;
+// 12-15 make V safe where weights can be zero: a zero weight does not undo a
+// NaN or an infinity, so in blocks that hold tokens some row does not attend,
+// rows past the end are zeroed and non-finite elements of node rows are
+// replaced by zero, to be added to the rows that attend them at the end.
+// Registers move from the last two warpgroups to the softmax warps, whose
+// threads hold a row of S.
+//
+// Producer, mma and inspectors follow the same sequence of steps, which each
+// of them generates for itself (TcSteps): a pipeline's next S is issued as
+// soon as its last P V has been, so the ring is filled in the order in which
+// the mma warp waits.
+//
+// The running maximum of a row moves only when it rises by more than 2^8 (the
+// weights then stay below 2^8, and O, in tensor memory, is rescaled rarely).
+#pragma once
+
+#include "pd_decode_tc.cuh"
+#include "pd_tree.cuh"
+
+namespace pd {
+
+// ---------------------------------------------------------------- PTX wrappers
+
+__device__ __forceinline__ void tma_load_3d(uint32_t dst, const void* tmap, int c0, int c1, int c2, uint32_t bar) {
+    asm volatile(
+        "cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
+        " [%0], [%1, {%2, %3, %4}], [%5];" ::"r"(dst),
+        "l"(tmap), "r"(c0), "r"(c1), "r"(c2), "r"(bar)
+        : "memory");
+}
+
+__device__ __forceinline__ uint64_t l2_evict_normal_policy() {
+    uint64_t p;
+    asm volatile("createpolicy.fractional.L2::evict_normal.b64 %0, 1.0;" : "=l"(p));
+    return p;
+}
+
+// Instruction descriptor of kind::f16: 16-bit A and B of one type, f32 accumulator.
+// neg_a: A is negated; b_mn: B is MN-major.
+__host__ __device__ constexpr uint32_t tc_idesc_f16(bool bf16, int M, int N, bool b_mn) {
+    return (1u << 4) | (bf16 ? (1u << 7) | (1u << 10) : 0u) | (b_mn ? 1u << 16 : 0u) | (uint32_t(N >> 3) << 17) |
+           (uint32_t(M >> 4) << 24);
+}
+constexpr uint32_t kIdescNegA = 1u << 13;
+
+// D = A * B (+ D when acc), A and B from shared memory.
+__device__ __forceinline__ void tc_mma_f16(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, bool acc) {
+    asm volatile(
+        "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
+        "tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
+        "l"(a), "l"(b), "r"(idesc), "r"(uint32_t(acc))
+        : "memory");
+}
+
+// The same with A in tensor memory (two 16-bit elements per column).
+__device__ __forceinline__ void tc_mma_f16_ta(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, bool acc) {
+    asm volatile(
+        "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
+        "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d),
+        "r"(a), "l"(b), "r"(idesc), "r"(uint32_t(acc))
+        : "memory");
+}
+
+// 32 consecutive columns of this thread's tensor-memory lane.
+__device__ __forceinline__ void tmem_ld32(uint32_t taddr, uint32_t* r) {
+    asm volatile(
+        "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, "
+        "%15, %16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31}, [%32];"
+        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]),
+          "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15]),
+          "=r"(r[16]), "=r"(r[17]), "=r"(r[18]), "=r"(r[19]), "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]),
+          "=r"(r[24]), "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
+        : "r"(taddr)
+        : "memory");
+}
+
+__device__ __forceinline__ void tmem_st32(uint32_t taddr, const uint32_t* r) {
+    asm volatile(
+        "tcgen05.st.sync.aligned.32x32b.x32.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, "
+        "%15, %16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31, %32};" ::"r"(taddr),
+        "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]),
+        "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15]), "r"(r[16]), "r"(r[17]), "r"(r[18]),
+        "r"(r[19]), "r"(r[20]), "r"(r[21]), "r"(r[22]), "r"(r[23]), "r"(r[24]), "r"(r[25]), "r"(r[26]), "r"(r[27]),
+        "r"(r[28]), "r"(r[29]), "r"(r[30]), "r"(r[31])
+        : "memory");
+}
+
+__device__ __forceinline__ void tmem_wait_st() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
+
+template <int R>
+__device__ __forceinline__ void regs_inc() {
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(R));
+}
+template <int R>
+__device__ __forceinline__ void regs_dec() {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(R));
+}
+
+// ---------------------------------------------------------------- configuration
+
+template <int D>
+struct CfgTree {
+    static constexpr int kRows = 128;
+    static constexpr int kTiles = D == 256 ? 1 : 2;    // O accumulators
+    static constexpr int kKeys = D == 256 ? 64 : 128;  // keys per block
+    static constexpr int kHalves = D / 64;             // 128-byte column blocks of a row
+    static constexpr int kSlotBytes = kKeys * D * 2;   // one K or V block
+    static constexpr int kQBytes = kRows * D * 2;      // one row tile of q
+    static constexpr int kQSlots = kTiles;
+    static constexpr int kSlots = D == 64 ? 10 : 5;
+    static constexpr int kRingOff = kQSlots * kQBytes;
+    static constexpr int kBarOff = kRingOff + kSlots * kSlotBytes;
+    // barriers: full[], empty[], vok[] per slot, then these
+    static constexpr int kBars = 3 * kSlots + 2 * 2 + 2 + 2 + 2 + 3;
+    static constexpr int kStatOff = kBarOff + (kBars * 8 + 15) / 16 * 16;  // pipeline 1's (m, l) per row
+    static constexpr int kMiscOff = kStatOff + kRows * 8;  // tensor-memory address, abort flag, bad-V tags[4]
+    static constexpr int kBytes = kMiscOff + 32 + 1024;    // 1024: alignment of the base
+    static constexpr int kOCols = D;
+    static constexpr int kSCol = kTiles * D;
+    static constexpr int kThreads = 512;
+    static_assert(kSCol + 2 * kKeys <= 512, "tensor memory");
+    static_assert(kBytes <= 232448, "shared memory");
+};
+
+// A segment's mode and its jobs: job j of a segment is block j / 2 for pipeline
+// j % 2 (wide), or block j for pipeline (S buffer, at head_dim 256) j % 2.
+template <int D>
+struct TcJobs {
+    bool wide;
+    int jobs;
+    __device__ __forceinline__ TcJobs(const TreeArgs& a, const TreeWalk::Seg& s) {
+        wide = CfgTree<D>::kTiles == 2 && s.nodes > a.npt;
+        jobs = (s.blk1 - s.blk0) * (wide ? 2 : 1);
+    }
+    __device__ __forceinline__ int block(const TreeWalk::Seg& s, int j) const { return s.blk0 + (wide ? j >> 1 : j); }
+    __device__ __forceinline__ int row_tile(int j) const { return wide ? j & 1 : 0; }
+    __device__ __forceinline__ bool first_use(int j) const { return !wide || (j & 1) == 0; }  // of its K (or V) block
+    __device__ __forceinline__ bool last_use(int j) const { return !wide || (j & 1) == 1; }
+};
+
+// The order of the mma warp's steps. on_qk(seg, index of seg, jobs, j) and
+// on_pv(...) return false to stop.
+template <int D, class OnQk, class OnPv>
+__device__ __forceinline__ void tc_steps(const TreeArgs& a, const TreeWalk& start, OnQk on_qk, OnPv on_pv) {
+    TreeWalk wq = start, wp = start;
+    TreeWalk::Seg sq, sp;
+    bool more_q = wq.next(a, &sq), more_p = wp.next(a, &sp);
+    int jq = 0, jp = 0, iq = 0, ip = 0;
+    int ahead[2] = {0, 0};  // S issued and not yet used by its P V, per pipeline
+    while (more_p) {
+        while (more_q) {
+            if (ahead[jq & 1] != 0) break;
+            const TcJobs<D> w(a, sq);
+            if (!on_qk(sq, iq, w, jq)) return;
+            ahead[jq & 1] = 1;
+            if (++jq == w.jobs) {
+                more_q = wq.next(a, &sq);
+                jq = 0;
+                ++iq;
+            }
+        }
+        const TcJobs<D> w(a, sp);
+        if (!on_pv(sp, ip, w, jp)) return;
+        ahead[jp & 1] = 0;
+        if (++jp == w.jobs) {
+            more_p = wp.next(a, &sp);
+            jp = 0;
+            ++ip;
+        }
+    }
+}
+
+// Whether block blk holds a slot with a token from ctx on (or past the end).
+__device__ __forceinline__ bool tree_tail_block(const TreeArgs& a, const TreeReq& r, int blk) {
+    return (blk + 1) * a.spb > r.ctx() / a.page_size * a.cpp + (r.ctx() % a.page_size) / a.slot_rows;
+}
+
+// Token of column col of block blk (col % slot_rows rows into its slot); -1 for a row past its page.
+__device__ __forceinline__ int tree_token(const TreeArgs& a, int blk, int col) {
+    const int s = blk * a.spb + col / a.slot_rows;
+    const int row = s % a.cpp * a.slot_rows + col % a.slot_rows;
+    return row < a.page_size ? s / a.cpp * a.page_size + row : -1;
+}
+
+// ---------------------------------------------------------------- the kernel
+
+template <typename T, int D>
+__global__ void __launch_bounds__(512, 1)
+    tree_tc_kernel(const TreeArgs a, const __grid_constant__ CUtensorMap tmq, const __grid_constant__ CUtensorMap tmk,
+                   const __grid_constant__ CUtensorMap tmv) {
+    using C = CfgTree<D>;
+    constexpr bool kBf16 = std::is_same<T, __nv_bfloat16>::value;
+    const float kNegInf = -__int_as_float(0x7f800000);
+    extern __shared__ __align__(16) uint8_t tree_tc_smem[];
+    __shared__ TreePlanScratch plan;
+    uint8_t* smem = tree_tc_smem + ((1024u - (smem_u32(tree_tc_smem) & 1023u)) & 1023u);
+    const uint32_t sbase = smem_u32(smem);
+    const int tid = threadIdx.x, lane = tid & 31, wid = tid >> 5;
+    auto bar = [&](int i) { return sbase + C::kBarOff + 8u * uint32_t(i); };
+    constexpr int kFullB = 0, kEmptyB = C::kSlots, kVokB = 2 * C::kSlots, kQFull = 3 * C::kSlots, kQEmpty = kQFull + 2,
+                  kSFull = kQEmpty + 2, kPFull = kSFull + 2, kPvDone = kPFull + 2, kOneDone = kPvDone + 2,
+                  kOneFree = kOneDone + 1, kAllDone = kOneFree + 1;
+    static_assert(kAllDone + 1 == C::kBars, "barrier count");
+    float2* stat = reinterpret_cast<float2*>(smem + C::kStatOff);
+    uint32_t* tslot = reinterpret_cast<uint32_t*>(smem + C::kMiscOff);
+    volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + C::kMiscOff + 4);
+    volatile int* bad_v = reinterpret_cast<volatile int*>(smem + C::kMiscOff + 16);
+
+    if (tid == 0) {
+        for (int i = 0; i < C::kSlots; ++i) {
+            mbar_init(bar(kFullB + i), 1);
+            mbar_init(bar(kEmptyB + i), 1 + 4);  // the last mma that reads the slot, and the inspectors
+            mbar_init(bar(kVokB + i), 4);
+        }
+        for (int i = 0; i < 2; ++i) {
+            mbar_init(bar(kQFull + i), 1);
+            mbar_init(bar(kQEmpty + i), 1);
+            mbar_init(bar(kSFull + i), 1);
+            mbar_init(bar(kPFull + i), 4);
+            mbar_init(bar(kPvDone + i), 1);
+        }
+        mbar_init(bar(kOneDone), 4);
+        mbar_init(bar(kOneFree), 4);
+        mbar_init(bar(kAllDone), 1);
+        fence_mbar_init();
+        *abort_flag = 0;
+        for (int i = 0; i < 4; ++i) bad_v[i] = 0;
+    }
+    if (wid == 9) tmem_alloc(smem_u32(tslot), 512);
+    if (wid == 8 && lane == 0) {
+        prefetch_tensormap(&tmq);
+        prefetch_tensormap(&tmk);
+        prefetch_tensormap(&tmv);
+    }
+    const TreeWalk start = tree_plan(a, &plan);
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    launch_dependents();
+    const uint32_t tmem = *tslot;
+
+    if (wid >= 8) {
+        regs_dec<64>();
+        if (wid == 8) {
+            // ============================================================ producer
+            const uint64_t once = l2_evict_first_policy(), again = l2_evict_normal_policy();
+            int loads = 0, qloads = 0;
+            auto load_block = [&](const TreeWalk::Seg& s, int blk, const CUtensorMap* tm) -> bool {
+                const int slot = loads % C::kSlots, use = loads / C::kSlots;
+                // one box per lane: slot_rows rows x 64 columns
+                const int sl = lane / C::kHalves, hf = lane % C::kHalves;
+                const int p = blk * a.spb + sl, row = p % a.cpp * a.slot_rows;
+                int page = a.num_total_pages;  // out of range: the copy fills zeros
+                if (sl < a.spb && p < tree_slots(a, s.r.len)) {
+                    page = __ldg(a.indices + s.r.lo + p / a.cpp);
+                    if (page < 0 || page >= a.num_total_pages) page = a.num_total_pages;
+                }
+                if (use > 0 && !tc_wait_warp(bar(kEmptyB + slot), uint32_t(use - 1) & 1u, abort_flag, a.flags)) return false;
+                if (lane == 0) mbar_arrive_expect_tx(bar(kFullB + slot), C::kSlotBytes);
+                __syncwarp();
+                if (sl < a.spb)
+                    tma_load_4d(sbase + C::kRingOff + slot * C::kSlotBytes + hf * (C::kKeys * 128) + sl * a.slot_rows * 128, tm,
+                                hf * 64, row, s.kvh, page, bar(kFullB + slot), s.r.n > a.nps ? again : once);
+                ++loads;
+                return true;
+            };
+            tc_steps<D>(
+                a, start,
+                [&](const TreeWalk::Seg& s, int, const TcJobs<D>& w, int j) {
+                    if (j == 0 || (w.wide && j == 1)) {
+                        const int qs = qloads % C::kQSlots, use = qloads / C::kQSlots;
+                        if (use > 0 && !tc_wait_warp(bar(kQEmpty + qs), uint32_t(use - 1) & 1u, abort_flag, a.flags)) return false;
+                        if (lane == 0) {
+                            mbar_arrive_expect_tx(bar(kQFull + qs), uint32_t(a.npt * a.hpt) * D * 2);
+                            for (int hf = 0; hf < C::kHalves; ++hf)
+                                tma_load_3d(sbase + qs * C::kQBytes + hf * (C::kRows * 128), &tmq, hf * 64, s.head0,
+                                            s.row0 + w.row_tile(j) * a.npt, bar(kQFull + qs));
+                        }
+                        __syncwarp();
+                        ++qloads;
+                    }
+                    return !w.first_use(j) || load_block(s, w.block(s, j), &tmk);
+                },
+                [&](const TreeWalk::Seg& s, int, const TcJobs<D>& w, int j) {
+                    return !w.first_use(j) || load_block(s, w.block(s, j), &tmv);
+                });
+            // copies issued last may still be landing when another role has stopped early
+            for (int i = max(0, loads - C::kSlots); i < loads; ++i)
+                mbar_wait_bounded(bar(kFullB + i % C::kSlots), uint32_t(i / C::kSlots) & 1u);
+            for (int i = max(0, qloads - C::kQSlots); i < qloads; ++i)
+                mbar_wait_bounded(bar(kQFull + i % C::kQSlots), uint32_t(i / C::kQSlots) & 1u);
+        } else if (wid == 9) {
+            // ============================================================ mma
+            if (lane == 0) {
+                const uint32_t idesc_s = tc_idesc_f16(kBf16, C::kRows, C::kKeys, false) | (a.scale_log2 < 0.f ? kIdescNegA : 0u);
+                constexpr uint32_t idesc_o = tc_idesc_f16(kBf16, C::kRows, D, true);
+                int loads = 0, kslot = 0, vslot = 0, q0 = 0;  // q0: q slots used before this segment
+                uint32_t vok = 0;                             // phase of each slot's vok barrier
+                int n_p[2] = {0, 0};
+                auto take = [&](int* slot) {
+                    *slot = loads % C::kSlots;
+                    const bool ok = tc_wait(bar(kFullB + *slot), uint32_t(loads / C::kSlots) & 1u, abort_flag, a.flags);
+                    ++loads;
+                    return ok;
+                };
+                tc_steps<D>(
+                    a, start,
+                    [&](const TreeWalk::Seg&, int, const TcJobs<D>& w, int j) {
+                        const int qn = q0 + w.row_tile(j), qs = qn % C::kQSlots;
+                        if ((j == 0 || (w.wide && j == 1)) &&
+                            !tc_wait(bar(kQFull + qs), uint32_t(qn / C::kQSlots) & 1u, abort_flag, a.flags))
+                            return false;
+                        if (w.first_use(j) && !take(&kslot)) return false;
+                        tc_fence_after();
+                        const uint32_t kb = sbase + C::kRingOff + kslot * C::kSlotBytes, qb = sbase + qs * C::kQBytes;
+                        const uint32_t d = tmem + C::kSCol + (j & 1) * C::kKeys;
+#pragma unroll
+                        for (int k = 0; k < D / 16; ++k)
+                            tc_mma_f16(d, smem_desc_sw128(qb + (k / 4) * (C::kRows * 128) + (k % 4) * 32, 16, 1024),
+                                       smem_desc_sw128(kb + (k / 4) * (C::kKeys * 128) + (k % 4) * 32, 16, 1024), idesc_s, k > 0);
+                        tc_commit(bar(kSFull + (j & 1)));
+                        if (w.last_use(j)) tc_commit(bar(kEmptyB + kslot));
+                        if (j + 1 == w.jobs || (w.wide && j + 2 == w.jobs)) {
+                            tc_commit(bar(kQEmpty + qs));
+                            if (j + 1 == w.jobs) q0 += w.wide ? 2 : 1;
+                        }
+                        return true;
+                    },
+                    [&](const TreeWalk::Seg& s, int, const TcJobs<D>& w, int j) {
+                        const int t = j & 1;
+                        if (w.first_use(j)) {
+                            if (!take(&vslot)) return false;
+                            if (tree_tail_block(a, s.r, w.block(s, j))) {
+                                if (!tc_wait(bar(kVokB + vslot), (vok >> vslot) & 1u, abort_flag, a.flags)) return false;
+                                vok ^= 1u << vslot;
+                            }
+                        }
+                        if (!tc_wait(bar(kPFull + t), uint32_t(n_p[t]++) & 1u, abort_flag, a.flags)) return false;
+                        tc_fence_after();
+                        const uint32_t vb = sbase + C::kRingOff + vslot * C::kSlotBytes;
+                        const uint32_t d = tmem + (C::kTiles == 2 ? t * C::kOCols : 0);
+                        const bool fresh = C::kTiles == 2 ? j < 2 : j == 0;
+#pragma unroll
+                        for (int k = 0; k < C::kKeys / 16; ++k)
+                            tc_mma_f16_ta(d, tmem + C::kSCol + t * C::kKeys + 8 * k,
+                                          smem_desc_sw128(vb + k * 2048, C::kKeys * 128, 1024), idesc_o, !fresh || k > 0);
+                        tc_commit(bar(kPvDone + t));
+                        if (w.last_use(j)) tc_commit(bar(kEmptyB + vslot));
+                        return true;
+                    });
+                // every mma has completed before the tensor memory is released
+                tc_commit(bar(kAllDone));
+                mbar_wait_bounded(bar(kAllDone), 0u);
+            }
+        } else if (wid >= 12) {
+            // ============================================================ V inspectors
+            // They see every load land and give every slot back, so that no
+            // barrier gets two phases ahead of them.
+            int loads = 0;
+            const int t = tid - 384;
+            auto landed = [&](int* slot) {
+                *slot = loads % C::kSlots;
+                const bool ok = tc_wait_warp(bar(kFullB + *slot), uint32_t(loads / C::kSlots) & 1u, abort_flag, a.flags);
+                ++loads;
+                return ok;
+            };
+            tc_steps<D>(
+                a, start,
+                [&](const TreeWalk::Seg&, int, const TcJobs<D>& w, int j) {
+                    if (!w.first_use(j)) return true;
+                    int slot;
+                    if (!landed(&slot)) return false;
+                    if (lane == 0) mbar_arrive(bar(kEmptyB + slot));
+                    return true;
+                },
+                [&](const TreeWalk::Seg& s, int seg, const TcJobs<D>& w, int j) {
+                    if (!w.first_use(j)) return true;
+                    const int blk = w.block(s, j);
+                    int slot;
+                    if (!landed(&slot)) return false;
+                    if (!tree_tail_block(a, s.r, blk)) {
+                        if (lane == 0) mbar_arrive(bar(kEmptyB + slot));
+                        return true;
+                    }
+                    uint8_t* vb = smem + C::kRingOff + slot * C::kSlotBytes;
+                    // one row per thread (two threads per row of a 64-key block)
+                    constexpr int kPer = 128 / C::kKeys;
+                    const int row = t / kPer;
+                    const int tok = tree_token(a, blk, row);
+                    const bool dead = tok < 0 || tok >= s.r.len, node = tok >= s.r.ctx();
+                    constexpr uint32_t kExp = kBf16 ? 0x7f807f80u : 0x7c007c00u;
+                    bool found = false;
+                    if (dead || node) {
+                        for (int hf = t % kPer; hf < C::kHalves; hf += kPer) {
+#pragma unroll
+                            for (int c = 0; c < 8; ++c) {
+                                uint4* at = reinterpret_cast<uint4*>(vb + hf * (C::kKeys * 128) + row * 128 + ((c ^ (row & 7)) << 4));
+                                uint4 x = dead ? make_uint4(0u, 0u, 0u, 0u) : *at;
+                                const uint32_t bx = __vcmpeq2(x.x & kExp, kExp), by = __vcmpeq2(x.y & kExp, kExp),
+                                               bz = __vcmpeq2(x.z & kExp, kExp), bw = __vcmpeq2(x.w & kExp, kExp);
+                                if ((bx | by | bz | bw) != 0u) {
+                                    found = true;
+                                    x = make_uint4(x.x & ~bx, x.y & ~by, x.z & ~bz, x.w & ~bw);
+                                    *at = x;
+                                } else if (dead) {
+                                    *at = x;
+                                }
+                            }
+                        }
+                    }
+                    if (found) bad_v[seg & 3] = seg + 1;
+                    fence_proxy_async_smem();
+                    __syncwarp();
+                    if (lane == 0) {
+                        mbar_arrive(bar(kVokB + slot));
+                        mbar_arrive(bar(kEmptyB + slot));
+                    }
+                    return true;
+                });
+        }
+    } else {
+        regs_inc<192>();
+        // ================================================================ softmax
+        const int t = wid >> 2, row = tid & 127;
+        if (C::kTiles == 2 || t == 0) {
+            const uint32_t lanes = uint32_t(32 * (wid & 3)) << 16;
+            const uint32_t to = tmem + lanes + (C::kTiles == 2 ? t * C::kOCols : 0);
+            const float scale = a.scale_log2 == 0.f ? 1e-38f : fabsf(a.scale_log2);
+            const int per_slot = a.slot_rows < 32 ? a.slot_rows : 32;
+            const bool packed = a.page_size % a.slot_rows == 0;
+            int n_s[2] = {0, 0}, n_one = 0, n_seg = 0;  // n_s[b]: jobs so far in S buffer b
+            int last = 0;                               // S buffer of the last job
+            bool dead = false;
+            TreeWalk walk = start;
+            TreeWalk::Seg s;
+            while (!dead && walk.next(a, &s)) {
+                const TcJobs<D> w(a, s);
+                const int seg = n_seg++;
+                const bool joint = C::kTiles == 2 && !w.wide;  // both pipelines hold parts of the same rows
+                const int node = s.node0 + (w.wide ? t * a.npt : 0) + row / a.hpt;
+                const long long at = tree_row(a, s.row0, s.nodes, s.hh, row + (w.wide ? t * C::kRows : 0));
+                const bool live = __any_sync(kFull, at >= 0);  // a warp without rows only keeps step
+                float m = kNegInf, l = 0.f;
+                // pipeline 1 leaves the last joint segment's O to pipeline 0 until it has been read
+                if (t == 1 && n_one > 0 && !tc_wait_warp(bar(kOneFree), uint32_t(n_one - 1) & 1u, abort_flag, a.flags)) break;
+                const int step = C::kTiles == 2 ? 2 : 1;
+                const int first = C::kTiles == 2 ? t : 0;
+                for (int j = first; j < w.jobs; j += step) {
+                    const int blk = w.block(s, j), sb = j & 1;
+                    // the block's pages, requested before the scores are waited for: lane x < spb has slot x
+                    bool page_ok = true;
+                    if (live && lane < a.spb) {
+                        const int p = blk * a.spb + lane;
+                        if (p < tree_slots(a, s.r.len)) {
+                            const int page = __ldg(a.indices + s.r.lo + p / a.cpp);
+                            page_ok = page >= 0 && page < a.num_total_pages;
+                        }
+                    }
+                    if (!tc_wait_warp(bar(kSFull + sb), uint32_t(n_s[sb]++) & 1u, abort_flag, a.flags)) {
+                        dead = true;
+                        break;
+                    }
+                    if (live) {
+                        tc_fence_after();
+                        const uint32_t ts = tmem + lanes + C::kSCol + sb * C::kKeys;
+                        uint32_t x[C::kKeys];
+#pragma unroll
+                        for (int c = 0; c < C::kKeys; c += 32) tmem_ld32(ts + c, x + c);
+                        const unsigned bad_pages = __ballot_sync(kFull, !page_ok);
+                        if (bad_pages != 0u && lane == 0) atomicOr(a.flags, kFlagBadPage);
+                        tmem_wait_ld();
+                        if (!packed || bad_pages != 0u || tree_tail_block(a, s.r, blk)) {
+                            const int nd = min(node, s.r.n - 1);
+#pragma unroll
+                            for (int c = 0; c < C::kKeys; c += 32) {
+                                uint32_t allow = 0;
+                                if (packed && bad_pages == 0u) {
+                                    allow = tree_allow(a, s.r, nd, (blk * a.spb) * a.slot_rows + c, 32);
+                                } else {
+                                    for (int e = 0; e < 32; e += per_slot) {
+                                        const int col = c + e, p = blk * a.spb + col / a.slot_rows;
+                                        const int r0 = p % a.cpp * a.slot_rows + col % a.slot_rows;
+                                        const int count = min(per_slot, a.page_size - r0);
+                                        if ((bad_pages >> (col / a.slot_rows)) & 1u) continue;
+                                        allow |= tree_allow(a, s.r, nd, p / a.cpp * a.page_size + r0, count) << e;
+                                    }
+                                }
+#pragma unroll
+                                for (int e = 0; e < 32; ++e)
+                                    if (((allow >> e) & 1u) == 0u) x[c + e] = __float_as_uint(kNegInf);
+                            }
+                        }
+                        float top = __uint_as_float(x[0]);
+#pragma unroll
+                        for (int c = 1; c < C::kKeys; ++c) top = fmaxf(top, __uint_as_float(x[c]));
+                        top *= scale;
+                        const bool fresh = C::kTiles == 2 ? j < 2 : j == 0;
+                        if (fresh) {
+                            m = top;
+                        } else {
+                            const bool rise = top > m + 8.f;
+                            if (__any_sync(kFull, rise)) {
+                                const float f = rise ? ex2(m - top) : 1.f;
+                                if (rise) m = top;
+                                l *= f;
+                                // O holds every block before this one once the last P V is done. A
+                                // barrier per S buffer: S of this job was issued after the P V before
+                                // in its buffer, so no barrier is more than one phase behind.
+                                if (!tc_wait_warp(bar(kPvDone + last), uint32_t(n_s[last] - (last == sb ? 2 : 1)) & 1u, abort_flag,
+                                                  a.flags)) {
+                                    dead = true;
+                                    break;
+                                }
+                                tc_fence_after();
+#pragma unroll
+                                for (int c = 0; c < D; c += 32) {
+                                    uint32_t o[32];
+                                    tmem_ld32(to + c, o);
+                                    tmem_wait_ld();
+#pragma unroll
+                                    for (int e = 0; e < 32; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * f);
+                                    tmem_st32(to + c, o);
+                                }
+                            }
+                        }
+                        const float mu = m == kNegInf ? 0.f : m;
+                        float2 sum = make_float2(0.f, 0.f);
+                        const float2 sc2 = make_float2(scale, scale), mu2 = make_float2(-mu, -mu);
+#pragma unroll
+                        for (int c = 0; c < C::kKeys; c += 64) {
+                            uint32_t p[32];
+#pragma unroll
+                            for (int e = 0; e < 32; ++e) {
+                                float2 y = make_float2(__uint_as_float(x[c + 2 * e]), __uint_as_float(x[c + 2 * e + 1]));
+                                y = __ffma2_rn(y, sc2, mu2);
+                                y = make_float2(ex2(y.x), ex2(y.y));
+                                sum = __fadd2_rn(sum, y);
+                                p[e] = Elt<T>::pack(y.x, y.y);
+                            }
+                            tmem_st32(ts + c / 2, p);
+                        }
+                        l += sum.x + sum.y;
+                        tmem_wait_st();
+                        tc_fence_before();
+                    }
+                    last = sb;
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(bar(kPFull + sb));
+                }
+                if (dead) break;
+                // ---- the segment's end
+                const int mine = C::kTiles == 2 ? (w.jobs + 1 - t) / 2 : w.jobs;  // jobs of this pipeline
+                if (mine > 0 && !tc_wait_warp(bar(kPvDone + last), uint32_t(n_s[last] - 1) & 1u, abort_flag, a.flags)) break;
+                tc_fence_after();
+                float2 other = make_float2(kNegInf, 0.f);
+                if (joint) {
+                    if (t == 1) {
+                        stat[row] = make_float2(m, l);
+                        tc_fence_before();
+                        __syncwarp();
+                        if (lane == 0) mbar_arrive(bar(kOneDone));
+                        ++n_one;
+                        continue;
+                    }
+                    if (!tc_wait_warp(bar(kOneDone), uint32_t(n_one++) & 1u, abort_flag, a.flags)) break;
+                    tc_fence_after();
+                    if (w.jobs > 1) other = stat[row];
+                }
+                const bool two = joint && w.jobs > 1;
+                const float mm = fmaxf(m, other.x), mu = mm == kNegInf ? 0.f : mm;
+                const float f0 = ex2(m - mu), f1 = ex2(other.x - mu);
+                const float L = l * f0 + other.y * f1;
+                const float inv = mm == kNegInf ? 0.f : 1.f / L;
+                const float lse2 = mm == kNegInf ? kNegInf : mm + log2f(L);
+                const float i0 = f0 * inv, i1 = f1 * inv;
+                const bool fix = bad_v[seg & 3] == seg + 1;
+                if (live) {
+#pragma unroll 1
+                    for (int c = 0; c < D; c += 32) {
+                        uint32_t o[32];
+                        tmem_ld32(to + c, o);
+                        float f[32];
+                        if (two) {
+                            uint32_t o1[32];
+                            tmem_ld32(to + C::kOCols + c, o1);
+                            tmem_wait_ld();
+#pragma unroll
+                            for (int e = 0; e < 32; ++e)
+                                f[e] = __uint_as_float(o[e]) * i0 + __uint_as_float(o1[e]) * i1;
+                        } else {
+                            tmem_wait_ld();
+#pragma unroll
+                            for (int e = 0; e < 32; ++e) f[e] = __uint_as_float(o[e]) * i0;
+                        }
+                        if (fix && at >= 0) {
+                            // non-finite elements of the node rows in these blocks, for the rows that attend them
+                            for (int i = 0; i < s.r.n; ++i) {
+                                const int tok = s.r.ctx() + i;
+                                const int blk = tree_slots(a, tok + 1) - 1;
+                                if (blk / a.spb < s.blk0 || blk / a.spb >= s.blk1) continue;
+                                if ((tree_allow(a, s.r, node, tok, 1) & 1u) == 0u) continue;
+                                const int page = __ldg(a.indices + s.r.lo + tok / a.page_size);
+                                if (page < 0 || page >= a.num_total_pages) continue;
+                                const T* v = static_cast<const T*>(a.v) +
+                                             ((size_t(page) * a.num_kv_heads + s.kvh) * a.page_size + tok % a.page_size) * D + c;
+#pragma unroll
+                                for (int e = 0; e < 32; ++e) {
+                                    const float y = float(v[e]);
+                                    if (!isfinite(y)) f[e] += y;
+                                }
+                            }
+                        }
+                        if (at >= 0) {
+                            if (s.slot >= 0) {
+                                float4* po = reinterpret_cast<float4*>(
+                                    a.part_o + (size_t(s.slot) * a.seg_rows + row + (w.wide ? t * C::kRows : 0)) * D + c);
+#pragma unroll
+                                for (int e = 0; e < 8; ++e) po[e] = make_float4(f[4 * e], f[4 * e + 1], f[4 * e + 2], f[4 * e + 3]);
+                            } else {
+                                uint4* po = reinterpret_cast<uint4*>(static_cast<T*>(a.o) + at * D + c);
+#pragma unroll
+                                for (int e = 0; e < 4; ++e) po[e] = Elt<T>::from_f32(f + 8 * e);
+                            }
+                        }
+                    }
+                    if (at >= 0) {
+                        if (s.slot >= 0)
+                            a.part_lse[size_t(s.slot) * a.seg_rows + row + (w.wide ? t * C::kRows : 0)] = lse2;
+                        else
+                            a.lse[at] = lse2 == kNegInf ? kNegInf : lse2 * kLn2;
+                    }
+                }
+                if (joint) {
+                    tc_fence_before();
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(bar(kOneFree));
+                }
+            }
+        }
+    }
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    if (wid == 9) tmem_dealloc(tmem, 512);
+}
+
+}  // namespace pd

@@ -1,0 +1,32 @@
+// Tensor-core tree decode with bf16 q.
+#include "pd_tree_kernels.h"
+#include "pd_tree_tc.cuh"
+
+namespace pd {
+
+template <int D>
+static TreeKernels tc_kernels() {
+    using C = CfgTree<D>;
+    TreeKernels k{};
+    k.main = reinterpret_cast<const void*>(tree_tc_kernel<__nv_bfloat16, D>);
+    k.merge = reinterpret_cast<const void*>(tree_merge_kernel<__nv_bfloat16, D>);
+    k.threads = C::kThreads;
+    k.smem = C::kBytes;
+    k.per_sm = 1;
+    k.tile_rows = C::kRows;
+    k.tiles = C::kTiles;
+    k.block_tokens = C::kKeys;
+    k.tensor = true;
+    return k;
+}
+
+bool tree_tc_bf16(int D, TreeKernels* k) {
+    switch (D) {
+        case 64: *k = tc_kernels<64>(); return true;
+        case 128: *k = tc_kernels<128>(); return true;
+        case 256: *k = tc_kernels<256>(); return true;
+    }
+    return false;
+}
+
+}  // namespace pd

@@ -137,6 +137,8 @@ struct TreeWalk {
         int hh, kvh, head0, heads;   // head tile, its kv head, its first q head and how many
         int row0, node0, nodes;      // first q row, first node within the request, nodes
         int blk0, blk1;
+        int tail0;                   // first block that holds a token from the context's end on
+        int slots;                   // slots of the request
         int slot;                    // partial slot; -1: the whole segment, written out
         TreeReq r;
     };
@@ -163,6 +165,9 @@ struct TreeWalk {
         s->row0 = r.start + s->node0;
         s->blk0 = blk;
         s->blk1 = int(min((long long)nblk, blk + (end - unit)));
+        const int ctx = max(0, r.ctx());
+        s->tail0 = (ctx / a.page_size * a.cpp + ctx % a.page_size / a.slot_rows) / a.spb;
+        s->slots = tree_slots(a, r.len);
         const long long begin = unit - blk;
         s->slot = (blk == 0 && s->blk1 == nblk) ? -1 : 2 * int(blockIdx.x) + (begin > end_of_previous() ? 1 : 0);
         unit += s->blk1 - s->blk0;

@@ -93,6 +93,15 @@ __device__ __forceinline__ void tmem_ld32(uint32_t taddr, uint32_t* r) {
         : "memory");
 }
 
+__device__ __forceinline__ void tmem_st16(uint32_t taddr, const uint32_t (&r)[16]) {
+    asm volatile(
+        "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, "
+        "%15, %16};" ::"r"(taddr),
+        "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]),
+        "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15])
+        : "memory");
+}
+
 __device__ __forceinline__ void tmem_st32(uint32_t taddr, const uint32_t* r) {
     asm volatile(
         "tcgen05.st.sync.aligned.32x32b.x32.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, "
@@ -115,6 +124,29 @@ __device__ __forceinline__ void regs_dec() {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(R));
 }
 
+// Wait for phase `parity` of `bar`; false when the CTA is aborting or the wait
+// runs out, which sets the abort flag and the status bit. The limit is counted
+// on the SM clock (4e9 cycles, about 2 s): a read of the global timer takes
+// longer than most of these waits.
+constexpr long long kWaitCycles = 4000000000ll;
+__device__ __forceinline__ bool tree_wait(uint32_t bar, uint32_t parity, volatile int* abort_flag, int* flags) {
+    if (mbar_try_wait(bar, parity)) return true;
+    const long long t0 = clock64();
+    for (;;) {
+        if (mbar_try_wait(bar, parity)) return true;
+        if (*abort_flag) return false;
+        if (clock64() - t0 > kWaitCycles) {
+            *abort_flag = 1;
+            atomicOr(flags, kFlagTimeout);
+            return false;
+        }
+    }
+}
+// The same for a whole warp: true only if every lane's wait succeeded.
+__device__ __forceinline__ bool tree_wait_warp(uint32_t bar, uint32_t parity, volatile int* abort_flag, int* flags) {
+    return __all_sync(kFull, tree_wait(bar, parity, abort_flag, flags));
+}
+
 // ---------------------------------------------------------------- configuration
 
 template <int D>
@@ -130,10 +162,13 @@ struct CfgTree {
     static constexpr int kRingOff = kQSlots * kQBytes;
     static constexpr int kBarOff = kRingOff + kSlots * kSlotBytes;
     // barriers: full[], empty[], vok[] per slot, then these
-    static constexpr int kBars = 3 * kSlots + 2 * 2 + 2 + 2 + 2 + 3;
+    static constexpr int kBars = 3 * kSlots + 2 * 2 + 2 + 2 + 2 + 3 + 2 * 8;
     static constexpr int kStatOff = kBarOff + (kBars * 8 + 15) / 16 * 16;  // pipeline 1's (m, l) per row
     static constexpr int kMiscOff = kStatOff + kRows * 8;  // tensor-memory address, abort flag, bad-V tags[4]
-    static constexpr int kBytes = kMiscOff + 32 + 1024;    // 1024: alignment of the base
+    static constexpr int kBadRing = 16;  // more than the K blocks that the producer is ahead of the softmax warps
+    static constexpr int kSegOff = kMiscOff + 32 + 4 * kBadRing;
+    static constexpr int kBytes = kSegOff + 8 * 64 + 1024;  // 1024: alignment of the base
+    static constexpr int kWalkers = 1 + 1 + 4 + (kTiles == 2 ? 8 : 4);  // warps that read the segments
     static constexpr int kOCols = D;
     static constexpr int kSCol = kTiles * D;
     static constexpr int kThreads = 512;
@@ -141,58 +176,89 @@ struct CfgTree {
     static_assert(kBytes <= 232448, "shared memory");
 };
 
-// A segment's mode and its jobs: job j of a segment is block j / 2 for pipeline
-// j % 2 (wide), or block j for pipeline (S buffer, at head_dim 256) j % 2.
-template <int D>
-struct TcJobs {
-    bool wide;
-    int jobs;
-    __device__ __forceinline__ TcJobs(const TreeArgs& a, const TreeWalk::Seg& s) {
-        wide = CfgTree<D>::kTiles == 2 && s.nodes > a.npt;
-        jobs = (s.blk1 - s.blk0) * (wide ? 2 : 1);
+// Segments come to the roles through a ring in shared memory, filled by one
+// warp that walks them. blk1 = blk0 ends the line.
+struct alignas(16) TcSeg {
+    int blk0, blk1, tail0, slots;     // blocks; first block with node tokens; slots of the request
+    int slot, row0, node0, nodes;     // partial slot or -1; q rows and nodes of the segment
+    int hh, head0, kvh, lo;           // head tile, its first q head and kv head; first entry of indices
+    int len, n, start, wide;          // the request: tokens, nodes, first q row; two row tiles
+    __device__ __forceinline__ TreeReq req() const {
+        TreeReq r;
+        r.n = n;
+        r.start = start;
+        r.len = len;
+        r.lo = lo;
+        return r;
     }
-    __device__ __forceinline__ int block(const TreeWalk::Seg& s, int j) const { return s.blk0 + (wide ? j >> 1 : j); }
-    __device__ __forceinline__ int row_tile(int j) const { return wide ? j & 1 : 0; }
-    __device__ __forceinline__ bool first_use(int j) const { return !wide || (j & 1) == 0; }  // of its K (or V) block
-    __device__ __forceinline__ bool last_use(int j) const { return !wide || (j & 1) == 1; }
+};
+constexpr int kSegRing = 8;
+
+// One step of the sequence. Job j of a segment is block j / 2 for pipeline
+// j % 2 (wide), or block j for pipeline (S buffer, at head_dim 256) j % 2.
+struct TcStep {
+    int j = 0, jobs = 0, seg = -1;  // job, jobs of the segment, segments before it
+    int blk0 = 0, tail0 = 0;
+    bool wide = false;
+    __device__ __forceinline__ bool enter(const TcSeg& s) {
+        wide = s.wide != 0;
+        blk0 = s.blk0;
+        tail0 = s.tail0;
+        jobs = (s.blk1 - blk0) * (wide ? 2 : 1);
+        j = 0;
+        ++seg;
+        return jobs > 0;
+    }
+    __device__ __forceinline__ int block() const { return blk0 + (wide ? j >> 1 : j); }
+    __device__ __forceinline__ bool tail() const { return block() >= tail0; }
+    __device__ __forceinline__ int row_tile() const { return wide ? j & 1 : 0; }
+    __device__ __forceinline__ bool opens_tile() const { return j == 0 || (wide && j == 1); }
+    __device__ __forceinline__ bool closes_tile() const { return j + 1 == jobs || (wide && j + 2 == jobs); }
+    __device__ __forceinline__ bool first_use() const { return !wide || (j & 1) == 0; }  // of its K (or V) block
+    __device__ __forceinline__ bool last_use() const { return !wide || (j & 1) == 1; }
 };
 
-// The order of the mma warp's steps. on_qk(seg, index of seg, jobs, j) and
-// on_pv(...) return false to stop.
-template <int D, class OnQk, class OnPv>
-__device__ __forceinline__ void tc_steps(const TreeArgs& a, const TreeWalk& start, OnQk on_qk, OnPv on_pv) {
-    TreeWalk wq = start, wp = start;
-    TreeWalk::Seg sq, sp;
-    bool more_q = wq.next(a, &sq), more_p = wp.next(a, &sp);
-    int jq = 0, jp = 0, iq = 0, ip = 0;
-    int ahead[2] = {0, 0};  // S issued and not yet used by its P V, per pipeline
-    while (more_p) {
-        while (more_q) {
-            if (ahead[jq & 1] != 0) break;
-            const TcJobs<D> w(a, sq);
-            if (!on_qk(sq, iq, w, jq)) return;
-            ahead[jq & 1] = 1;
-            if (++jq == w.jobs) {
-                more_q = wq.next(a, &sq);
-                jq = 0;
-                ++iq;
+// The order of the mma warp's steps. seg_wait(i) waits for segment i and
+// returns it (null to stop), seg_free(i) gives it back; on_qk(step, seg) and
+// on_pv(step, seg) return false to stop.
+template <class SegWait, class SegFree, class OnQk, class OnPv>
+__device__ __forceinline__ void tc_steps(SegWait seg_wait, SegFree seg_free, OnQk on_qk, OnPv on_pv) {
+    TcStep q, p;
+    const TcSeg *sq = seg_wait(0), *sp = sq;
+    if (sq == nullptr || !q.enter(*sq)) return;
+    p = q;
+    bool more = true;
+    int ahead = 0;  // bit t: pipeline t has an S whose P V is still to come
+    for (;;) {
+        while (more && ((ahead >> (q.j & 1)) & 1) == 0) {
+            if (!on_qk(q, *sq)) return;
+            ahead |= 1 << (q.j & 1);
+            if (++q.j == q.jobs) {
+                if ((sq = seg_wait(q.seg + 1)) == nullptr) return;
+                more = q.enter(*sq);
             }
         }
-        const TcJobs<D> w(a, sp);
-        if (!on_pv(sp, ip, w, jp)) return;
-        ahead[jp & 1] = 0;
-        if (++jp == w.jobs) {
-            more_p = wp.next(a, &sp);
-            jp = 0;
-            ++ip;
+        if (!on_pv(p, *sp)) return;
+        ahead &= ~(1 << (p.j & 1));
+        if (++p.j == p.jobs) {
+            seg_free(p.seg);
+            if ((sp = seg_wait(p.seg + 1)) == nullptr || !p.enter(*sp)) return;
         }
     }
 }
 
-// Whether block blk holds a slot with a token from ctx on (or past the end).
-__device__ __forceinline__ bool tree_tail_block(const TreeArgs& a, const TreeReq& r, int blk) {
-    return (blk + 1) * a.spb > r.ctx() / a.page_size * a.cpp + (r.ctx() % a.page_size) / a.slot_rows;
-}
+// A place in a ring of N slots and the phase of its barriers.
+template <int N>
+struct Ring {
+    int slot = 0;
+    uint32_t phase = 0;
+    __device__ __forceinline__ void next() {
+        if (++slot == N) {
+            slot = 0;
+            phase ^= 1u;
+        }
+    }
+};
 
 // Token of column col of block blk (col % slot_rows rows into its slot); -1 for a row past its page.
 __device__ __forceinline__ int tree_token(const TreeArgs& a, int blk, int col) {
@@ -211,19 +277,20 @@ __global__ void __launch_bounds__(512, 1)
     constexpr bool kBf16 = std::is_same<T, __nv_bfloat16>::value;
     const float kNegInf = -__int_as_float(0x7f800000);
     extern __shared__ __align__(16) uint8_t tree_tc_smem[];
-    __shared__ TreePlanScratch plan;
     uint8_t* smem = tree_tc_smem + ((1024u - (smem_u32(tree_tc_smem) & 1023u)) & 1023u);
     const uint32_t sbase = smem_u32(smem);
     const int tid = threadIdx.x, lane = tid & 31, wid = tid >> 5;
     auto bar = [&](int i) { return sbase + C::kBarOff + 8u * uint32_t(i); };
     constexpr int kFullB = 0, kEmptyB = C::kSlots, kVokB = 2 * C::kSlots, kQFull = 3 * C::kSlots, kQEmpty = kQFull + 2,
                   kSFull = kQEmpty + 2, kPFull = kSFull + 2, kPvDone = kPFull + 2, kOneDone = kPvDone + 2,
-                  kOneFree = kOneDone + 1, kAllDone = kOneFree + 1;
-    static_assert(kAllDone + 1 == C::kBars, "barrier count");
+                  kOneFree = kOneDone + 1, kAllDone = kOneFree + 1, kSegFull = kAllDone + 1, kSegFree = kSegFull + kSegRing;
+    static_assert(kSegFree + kSegRing == C::kBars, "barrier count");
     float2* stat = reinterpret_cast<float2*>(smem + C::kStatOff);
     uint32_t* tslot = reinterpret_cast<uint32_t*>(smem + C::kMiscOff);
     volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + C::kMiscOff + 4);
     volatile int* bad_v = reinterpret_cast<volatile int*>(smem + C::kMiscOff + 16);
+    // slots of each K block whose page id is bad, by the K block's number in this CTA
+    volatile uint32_t* bad_slots = reinterpret_cast<volatile uint32_t*>(smem + C::kMiscOff + 32);
 
     if (tid == 0) {
         for (int i = 0; i < C::kSlots; ++i) {
@@ -238,6 +305,10 @@ __global__ void __launch_bounds__(512, 1)
             mbar_init(bar(kPFull + i), 4);
             mbar_init(bar(kPvDone + i), 1);
         }
+        for (int i = 0; i < kSegRing; ++i) {
+            mbar_init(bar(kSegFull + i), 1);
+            mbar_init(bar(kSegFree + i), C::kWalkers);
+        }
         mbar_init(bar(kOneDone), 4);
         mbar_init(bar(kOneFree), 4);
         mbar_init(bar(kAllDone), 1);
@@ -251,57 +322,109 @@ __global__ void __launch_bounds__(512, 1)
         prefetch_tensormap(&tmk);
         prefetch_tensormap(&tmv);
     }
-    const TreeWalk start = tree_plan(a, &plan);
+    TreeWalk walk = tree_plan(a, reinterpret_cast<TreePlanScratch*>(smem + C::kRingOff));
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
     launch_dependents();
     const uint32_t tmem = *tslot;
+    TcSeg* segs = reinterpret_cast<TcSeg*>(smem + C::kSegOff);
+    // one lane / a whole warp
+    auto seg_wait1 = [&](int i) -> const TcSeg* {
+        return tree_wait(bar(kSegFull + i % kSegRing), uint32_t(i / kSegRing) & 1u, abort_flag, a.flags) ? segs + i % kSegRing : nullptr;
+    };
+    auto seg_wait = [&](int i) -> const TcSeg* {
+        return tree_wait_warp(bar(kSegFull + i % kSegRing), uint32_t(i / kSegRing) & 1u, abort_flag, a.flags) ? segs + i % kSegRing
+                                                                                                            : nullptr;
+    };
+    auto seg_free1 = [&](int i) { mbar_arrive(bar(kSegFree + i % kSegRing)); };
+    auto seg_free = [&](int i) {
+        __syncwarp();
+        if (lane == 0) mbar_arrive(bar(kSegFree + i % kSegRing));
+    };
 
     if (wid >= 8) {
         regs_dec<64>();
-        if (wid == 8) {
+        if (wid == 10) {
+            // ============================================================ segments
+            TreeWalk::Seg s;
+            for (int i = 0;; ++i) {
+                const bool more = walk.next(a, &s);
+                if (i >= kSegRing &&
+                    !tree_wait_warp(bar(kSegFree + i % kSegRing), uint32_t(i / kSegRing - 1) & 1u, abort_flag, a.flags))
+                    break;
+                if (lane == 0) {
+                    TcSeg x{};
+                    if (more)
+                        x = TcSeg{s.blk0, s.blk1,  s.tail0, s.slots, s.slot,  s.row0, s.node0,   s.nodes,
+                                  s.hh,   s.head0, s.kvh,   s.r.lo,  s.r.len, s.r.n,  s.r.start, C::kTiles == 2 && s.nodes > a.npt};
+                    segs[i % kSegRing] = x;
+                    mbar_arrive(bar(kSegFull + i % kSegRing));
+                }
+                __syncwarp();
+                if (!more) break;
+            }
+        } else if (wid == 8) {
             // ============================================================ producer
             const uint64_t once = l2_evict_first_policy(), again = l2_evict_normal_policy();
-            int loads = 0, qloads = 0;
-            auto load_block = [&](const TreeWalk::Seg& s, int blk, const CUtensorMap* tm) -> bool {
-                const int slot = loads % C::kSlots, use = loads / C::kSlots;
-                // one box per lane: slot_rows rows x 64 columns
-                const int sl = lane / C::kHalves, hf = lane % C::kHalves;
-                const int p = blk * a.spb + sl, row = p % a.cpp * a.slot_rows;
-                int page = a.num_total_pages;  // out of range: the copy fills zeros
-                if (sl < a.spb && p < tree_slots(a, s.r.len)) {
-                    page = __ldg(a.indices + s.r.lo + p / a.cpp);
-                    if (page < 0 || page >= a.num_total_pages) page = a.num_total_pages;
+            Ring<C::kSlots> ring;
+            Ring<C::kQSlots> qring;
+            int loads = 0, qloads = 0, kblocks = 0;
+            // one box per lane: slot_rows rows x 64 columns
+            const int sl = lane / C::kHalves, hf = lane % C::kHalves;
+            auto load_block = [&](const TcSeg& s, int blk, const CUtensorMap* tm, bool is_k) -> bool {
+                const int p = blk * a.spb + sl;
+                int page = a.num_total_pages, row = 0, at = p;  // page out of range: the copy fills zeros
+                if (a.cpp > 1) {
+                    at = p / a.cpp;
+                    row = (p - at * a.cpp) * a.slot_rows;
                 }
-                if (use > 0 && !tc_wait_warp(bar(kEmptyB + slot), uint32_t(use - 1) & 1u, abort_flag, a.flags)) return false;
-                if (lane == 0) mbar_arrive_expect_tx(bar(kFullB + slot), C::kSlotBytes);
+                bool bad = false;
+                if (sl < a.spb && p < s.slots) {
+                    page = __ldg(a.indices + s.lo + at);
+                    bad = page < 0 || page >= a.num_total_pages;
+                    if (bad) page = a.num_total_pages;
+                }
+                if (is_k) {
+                    const unsigned found = __ballot_sync(kFull, bad);
+                    if (lane == 0) {
+                        unsigned bits = 0;
+                        for (unsigned f = found; f != 0u; f &= f - 1u) bits |= 1u << ((__ffs(f) - 1) / C::kHalves);
+                        bad_slots[kblocks % C::kBadRing] = bits;
+                        if (bits != 0u) atomicOr(a.flags, kFlagBadPage);
+                    }
+                    ++kblocks;
+                }
+                if (loads >= C::kSlots && !tree_wait_warp(bar(kEmptyB + ring.slot), ring.phase ^ 1u, abort_flag, a.flags)) return false;
+                if (lane == 0) mbar_arrive_expect_tx(bar(kFullB + ring.slot), C::kSlotBytes);
                 __syncwarp();
                 if (sl < a.spb)
-                    tma_load_4d(sbase + C::kRingOff + slot * C::kSlotBytes + hf * (C::kKeys * 128) + sl * a.slot_rows * 128, tm,
-                                hf * 64, row, s.kvh, page, bar(kFullB + slot), s.r.n > a.nps ? again : once);
+                    tma_load_4d(sbase + C::kRingOff + ring.slot * C::kSlotBytes + hf * (C::kKeys * 128) + sl * a.slot_rows * 128,
+                                tm, hf * 64, row, s.kvh, page, bar(kFullB + ring.slot), s.n > a.nps ? again : once);
                 ++loads;
+                ring.next();
                 return true;
             };
-            tc_steps<D>(
-                a, start,
-                [&](const TreeWalk::Seg& s, int, const TcJobs<D>& w, int j) {
-                    if (j == 0 || (w.wide && j == 1)) {
-                        const int qs = qloads % C::kQSlots, use = qloads / C::kQSlots;
-                        if (use > 0 && !tc_wait_warp(bar(kQEmpty + qs), uint32_t(use - 1) & 1u, abort_flag, a.flags)) return false;
+            tc_steps(
+                seg_wait, seg_free,
+                [&](const TcStep& w, const TcSeg& s) {
+                    if (w.opens_tile()) {
+                        if (qloads >= C::kQSlots && !tree_wait_warp(bar(kQEmpty + qring.slot), qring.phase ^ 1u, abort_flag, a.flags))
+                            return false;
                         if (lane == 0) {
-                            mbar_arrive_expect_tx(bar(kQFull + qs), uint32_t(a.npt * a.hpt) * D * 2);
-                            for (int hf = 0; hf < C::kHalves; ++hf)
-                                tma_load_3d(sbase + qs * C::kQBytes + hf * (C::kRows * 128), &tmq, hf * 64, s.head0,
-                                            s.row0 + w.row_tile(j) * a.npt, bar(kQFull + qs));
+                            mbar_arrive_expect_tx(bar(kQFull + qring.slot), uint32_t(a.npt * a.hpt) * D * 2);
+                            for (int h = 0; h < C::kHalves; ++h)
+                                tma_load_3d(sbase + qring.slot * C::kQBytes + h * (C::kRows * 128), &tmq, h * 64, s.head0,
+                                            s.row0 + w.row_tile() * a.npt, bar(kQFull + qring.slot));
                         }
                         __syncwarp();
                         ++qloads;
+                        qring.next();
                     }
-                    return !w.first_use(j) || load_block(s, w.block(s, j), &tmk);
+                    return !w.first_use() || load_block(s, w.block(), &tmk, true);
                 },
-                [&](const TreeWalk::Seg& s, int, const TcJobs<D>& w, int j) {
-                    return !w.first_use(j) || load_block(s, w.block(s, j), &tmv);
+                [&](const TcStep& w, const TcSeg& s) {
+                    return !w.first_use() || load_block(s, w.block(), &tmv, false);
                 });
             // copies issued last may still be landing when another role has stopped early
             for (int i = max(0, loads - C::kSlots); i < loads; ++i)
@@ -313,58 +436,64 @@ __global__ void __launch_bounds__(512, 1)
             if (lane == 0) {
                 const uint32_t idesc_s = tc_idesc_f16(kBf16, C::kRows, C::kKeys, false) | (a.scale_log2 < 0.f ? kIdescNegA : 0u);
                 constexpr uint32_t idesc_o = tc_idesc_f16(kBf16, C::kRows, D, true);
-                int loads = 0, kslot = 0, vslot = 0, q0 = 0;  // q0: q slots used before this segment
-                uint32_t vok = 0;                             // phase of each slot's vok barrier
-                int n_p[2] = {0, 0};
+                // operand descriptors of slot 0 (K K-major, V MN-major) and of q slot 0; addresses count 16 bytes
+                const uint64_t kdesc = smem_desc_sw128(sbase + C::kRingOff, 16, 1024);
+                const uint64_t vdesc = smem_desc_sw128(sbase + C::kRingOff, C::kKeys * 128, 1024);
+                const uint64_t qdesc = smem_desc_sw128(sbase, 16, 1024);
+                Ring<C::kSlots> ring;
+                Ring<C::kQSlots> qring;
+                int kslot = 0, vslot = 0, qtile[2] = {0, 0};
+                uint32_t vok = 0;          // phase of each slot's vok barrier
+                uint32_t p_phase = 0;      // bit t: phase of pfull t
                 auto take = [&](int* slot) {
-                    *slot = loads % C::kSlots;
-                    const bool ok = tc_wait(bar(kFullB + *slot), uint32_t(loads / C::kSlots) & 1u, abort_flag, a.flags);
-                    ++loads;
+                    *slot = ring.slot;
+                    const bool ok = tree_wait(bar(kFullB + ring.slot), ring.phase, abort_flag, a.flags);
+                    ring.next();
                     return ok;
                 };
-                tc_steps<D>(
-                    a, start,
-                    [&](const TreeWalk::Seg&, int, const TcJobs<D>& w, int j) {
-                        const int qn = q0 + w.row_tile(j), qs = qn % C::kQSlots;
-                        if ((j == 0 || (w.wide && j == 1)) &&
-                            !tc_wait(bar(kQFull + qs), uint32_t(qn / C::kQSlots) & 1u, abort_flag, a.flags))
-                            return false;
-                        if (w.first_use(j) && !take(&kslot)) return false;
+                tc_steps(
+                    seg_wait1, seg_free1,
+                    [&](const TcStep& w, const TcSeg&) {
+                        const int t = w.j & 1, rt = w.row_tile();
+                        if (w.opens_tile()) {
+                            if (!tree_wait(bar(kQFull + qring.slot), qring.phase, abort_flag, a.flags)) return false;
+                            qtile[rt] = qring.slot;
+                            qring.next();
+                        }
+                        if (w.first_use() && !take(&kslot)) return false;
+                        const int qs = rt == 0 ? qtile[0] : qtile[1];
                         tc_fence_after();
-                        const uint32_t kb = sbase + C::kRingOff + kslot * C::kSlotBytes, qb = sbase + qs * C::kQBytes;
-                        const uint32_t d = tmem + C::kSCol + (j & 1) * C::kKeys;
+                        const uint64_t kb = kdesc + uint32_t(kslot * (C::kSlotBytes / 16)), qb = qdesc + uint32_t(qs * (C::kQBytes / 16));
+                        const uint32_t d = tmem + C::kSCol + t * C::kKeys;
 #pragma unroll
                         for (int k = 0; k < D / 16; ++k)
-                            tc_mma_f16(d, smem_desc_sw128(qb + (k / 4) * (C::kRows * 128) + (k % 4) * 32, 16, 1024),
-                                       smem_desc_sw128(kb + (k / 4) * (C::kKeys * 128) + (k % 4) * 32, 16, 1024), idesc_s, k > 0);
-                        tc_commit(bar(kSFull + (j & 1)));
-                        if (w.last_use(j)) tc_commit(bar(kEmptyB + kslot));
-                        if (j + 1 == w.jobs || (w.wide && j + 2 == w.jobs)) {
-                            tc_commit(bar(kQEmpty + qs));
-                            if (j + 1 == w.jobs) q0 += w.wide ? 2 : 1;
-                        }
+                            tc_mma_f16(d, qb + ((k / 4) * (C::kRows * 128) + (k % 4) * 32) / 16,
+                                       kb + ((k / 4) * (C::kKeys * 128) + (k % 4) * 32) / 16, idesc_s, k > 0);
+                        tc_commit(bar(kSFull + t));
+                        if (w.last_use()) tc_commit(bar(kEmptyB + kslot));
+                        if (w.closes_tile()) tc_commit(bar(kQEmpty + qs));
                         return true;
                     },
-                    [&](const TreeWalk::Seg& s, int, const TcJobs<D>& w, int j) {
-                        const int t = j & 1;
-                        if (w.first_use(j)) {
+                    [&](const TcStep& w, const TcSeg&) {
+                        const int t = w.j & 1;
+                        if (w.first_use()) {
                             if (!take(&vslot)) return false;
-                            if (tree_tail_block(a, s.r, w.block(s, j))) {
-                                if (!tc_wait(bar(kVokB + vslot), (vok >> vslot) & 1u, abort_flag, a.flags)) return false;
+                            if (w.tail()) {
+                                if (!tree_wait(bar(kVokB + vslot), (vok >> vslot) & 1u, abort_flag, a.flags)) return false;
                                 vok ^= 1u << vslot;
                             }
                         }
-                        if (!tc_wait(bar(kPFull + t), uint32_t(n_p[t]++) & 1u, abort_flag, a.flags)) return false;
+                        if (!tree_wait(bar(kPFull + t), (p_phase >> t) & 1u, abort_flag, a.flags)) return false;
+                        p_phase ^= 1u << t;
                         tc_fence_after();
-                        const uint32_t vb = sbase + C::kRingOff + vslot * C::kSlotBytes;
+                        const uint64_t vb = vdesc + uint32_t(vslot * (C::kSlotBytes / 16));
                         const uint32_t d = tmem + (C::kTiles == 2 ? t * C::kOCols : 0);
-                        const bool fresh = C::kTiles == 2 ? j < 2 : j == 0;
+                        const bool fresh = C::kTiles == 2 ? w.j < 2 : w.j == 0;
 #pragma unroll
                         for (int k = 0; k < C::kKeys / 16; ++k)
-                            tc_mma_f16_ta(d, tmem + C::kSCol + t * C::kKeys + 8 * k,
-                                          smem_desc_sw128(vb + k * 2048, C::kKeys * 128, 1024), idesc_o, !fresh || k > 0);
+                            tc_mma_f16_ta(d, tmem + C::kSCol + t * C::kKeys + 8 * k, vb + k * 128, idesc_o, !fresh || k > 0);
                         tc_commit(bar(kPvDone + t));
-                        if (w.last_use(j)) tc_commit(bar(kEmptyB + vslot));
+                        if (w.last_use()) tc_commit(bar(kEmptyB + vslot));
                         return true;
                     });
                 // every mma has completed before the tensor memory is released
@@ -375,29 +504,29 @@ __global__ void __launch_bounds__(512, 1)
             // ============================================================ V inspectors
             // They see every load land and give every slot back, so that no
             // barrier gets two phases ahead of them.
-            int loads = 0;
+            Ring<C::kSlots> ring;
             const int t = tid - 384;
             auto landed = [&](int* slot) {
-                *slot = loads % C::kSlots;
-                const bool ok = tc_wait_warp(bar(kFullB + *slot), uint32_t(loads / C::kSlots) & 1u, abort_flag, a.flags);
-                ++loads;
+                *slot = ring.slot;
+                const bool ok = tree_wait_warp(bar(kFullB + ring.slot), ring.phase, abort_flag, a.flags);
+                ring.next();
                 return ok;
             };
-            tc_steps<D>(
-                a, start,
-                [&](const TreeWalk::Seg&, int, const TcJobs<D>& w, int j) {
-                    if (!w.first_use(j)) return true;
+            tc_steps(
+                seg_wait, seg_free,
+                [&](const TcStep& w, const TcSeg&) {
+                    if (!w.first_use()) return true;
                     int slot;
                     if (!landed(&slot)) return false;
                     if (lane == 0) mbar_arrive(bar(kEmptyB + slot));
                     return true;
                 },
-                [&](const TreeWalk::Seg& s, int seg, const TcJobs<D>& w, int j) {
-                    if (!w.first_use(j)) return true;
-                    const int blk = w.block(s, j);
+                [&](const TcStep& w, const TcSeg& s) {
+                    if (!w.first_use()) return true;
+                    const int blk = w.block();
                     int slot;
                     if (!landed(&slot)) return false;
-                    if (!tree_tail_block(a, s.r, blk)) {
+                    if (!w.tail()) {
                         if (lane == 0) mbar_arrive(bar(kEmptyB + slot));
                         return true;
                     }
@@ -406,7 +535,7 @@ __global__ void __launch_bounds__(512, 1)
                     constexpr int kPer = 128 / C::kKeys;
                     const int row = t / kPer;
                     const int tok = tree_token(a, blk, row);
-                    const bool dead = tok < 0 || tok >= s.r.len, node = tok >= s.r.ctx();
+                    const bool dead = tok < 0 || tok >= s.len, node = tok >= s.len - s.n;
                     constexpr uint32_t kExp = kBf16 ? 0x7f807f80u : 0x7c007c00u;
                     bool found = false;
                     if (dead || node) {
@@ -427,7 +556,7 @@ __global__ void __launch_bounds__(512, 1)
                             }
                         }
                     }
-                    if (found) bad_v[seg & 3] = seg + 1;
+                    if (found) bad_v[w.seg & 3] = w.seg + 1;
                     fence_proxy_async_smem();
                     __syncwarp();
                     if (lane == 0) {
@@ -450,10 +579,13 @@ __global__ void __launch_bounds__(512, 1)
             int n_s[2] = {0, 0}, n_one = 0, n_seg = 0;  // n_s[b]: jobs so far in S buffer b
             int last = 0;                               // S buffer of the last job
             bool dead = false;
-            TreeWalk walk = start;
-            TreeWalk::Seg s;
-            while (!dead && walk.next(a, &s)) {
-                const TcJobs<D> w(a, s);
+            int kblocks = 0;  // K blocks before this segment
+            while (!dead) {
+                const TcSeg* sp = seg_wait(n_seg);
+                TcStep w;
+                if (sp == nullptr || !w.enter(*sp)) break;
+                const TcSeg& s = *sp;
+                const TreeReq r = s.req();
                 const int seg = n_seg++;
                 const bool joint = C::kTiles == 2 && !w.wide;  // both pipelines hold parts of the same rows
                 const int node = s.node0 + (w.wide ? t * a.npt : 0) + row / a.hpt;
@@ -461,21 +593,13 @@ __global__ void __launch_bounds__(512, 1)
                 const bool live = __any_sync(kFull, at >= 0);  // a warp without rows only keeps step
                 float m = kNegInf, l = 0.f;
                 // pipeline 1 leaves the last joint segment's O to pipeline 0 until it has been read
-                if (t == 1 && n_one > 0 && !tc_wait_warp(bar(kOneFree), uint32_t(n_one - 1) & 1u, abort_flag, a.flags)) break;
+                if (t == 1 && n_one > 0 && !tree_wait_warp(bar(kOneFree), uint32_t(n_one - 1) & 1u, abort_flag, a.flags)) break;
                 const int step = C::kTiles == 2 ? 2 : 1;
                 const int first = C::kTiles == 2 ? t : 0;
                 for (int j = first; j < w.jobs; j += step) {
-                    const int blk = w.block(s, j), sb = j & 1;
-                    // the block's pages, requested before the scores are waited for: lane x < spb has slot x
-                    bool page_ok = true;
-                    if (live && lane < a.spb) {
-                        const int p = blk * a.spb + lane;
-                        if (p < tree_slots(a, s.r.len)) {
-                            const int page = __ldg(a.indices + s.r.lo + p / a.cpp);
-                            page_ok = page >= 0 && page < a.num_total_pages;
-                        }
-                    }
-                    if (!tc_wait_warp(bar(kSFull + sb), uint32_t(n_s[sb]++) & 1u, abort_flag, a.flags)) {
+                    w.j = j;
+                    const int blk = w.block(), sb = j & 1;
+                    if (!tree_wait_warp(bar(kSFull + sb), uint32_t(n_s[sb]++) & 1u, abort_flag, a.flags)) {
                         dead = true;
                         break;
                     }
@@ -485,23 +609,22 @@ __global__ void __launch_bounds__(512, 1)
                         uint32_t x[C::kKeys];
 #pragma unroll
                         for (int c = 0; c < C::kKeys; c += 32) tmem_ld32(ts + c, x + c);
-                        const unsigned bad_pages = __ballot_sync(kFull, !page_ok);
-                        if (bad_pages != 0u && lane == 0) atomicOr(a.flags, kFlagBadPage);
+                        const unsigned bad_pages = bad_slots[(kblocks + blk - s.blk0) % C::kBadRing];
                         tmem_wait_ld();
-                        if (!packed || bad_pages != 0u || tree_tail_block(a, s.r, blk)) {
-                            const int nd = min(node, s.r.n - 1);
+                        if (!packed || bad_pages != 0u || w.tail()) {
+                            const int nd = min(node, r.n - 1);
 #pragma unroll
                             for (int c = 0; c < C::kKeys; c += 32) {
                                 uint32_t allow = 0;
                                 if (packed && bad_pages == 0u) {
-                                    allow = tree_allow(a, s.r, nd, (blk * a.spb) * a.slot_rows + c, 32);
+                                    allow = tree_allow(a, r, nd, (blk * a.spb) * a.slot_rows + c, 32);
                                 } else {
                                     for (int e = 0; e < 32; e += per_slot) {
                                         const int col = c + e, p = blk * a.spb + col / a.slot_rows;
                                         const int r0 = p % a.cpp * a.slot_rows + col % a.slot_rows;
                                         const int count = min(per_slot, a.page_size - r0);
                                         if ((bad_pages >> (col / a.slot_rows)) & 1u) continue;
-                                        allow |= tree_allow(a, s.r, nd, p / a.cpp * a.page_size + r0, count) << e;
+                                        allow |= tree_allow(a, r, nd, p / a.cpp * a.page_size + r0, count) << e;
                                     }
                                 }
 #pragma unroll
@@ -525,20 +648,20 @@ __global__ void __launch_bounds__(512, 1)
                                 // O holds every block before this one once the last P V is done. A
                                 // barrier per S buffer: S of this job was issued after the P V before
                                 // in its buffer, so no barrier is more than one phase behind.
-                                if (!tc_wait_warp(bar(kPvDone + last), uint32_t(n_s[last] - (last == sb ? 2 : 1)) & 1u, abort_flag,
+                                if (!tree_wait_warp(bar(kPvDone + last), uint32_t(n_s[last] - (last == sb ? 2 : 1)) & 1u, abort_flag,
                                                   a.flags)) {
                                     dead = true;
                                     break;
                                 }
                                 tc_fence_after();
-#pragma unroll
-                                for (int c = 0; c < D; c += 32) {
-                                    uint32_t o[32];
-                                    tmem_ld32(to + c, o);
+#pragma unroll 1
+                                for (int c = 0; c < D; c += 16) {
+                                    uint32_t o[16];
+                                    tmem_ld16(to + c, o);
                                     tmem_wait_ld();
 #pragma unroll
-                                    for (int e = 0; e < 32; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * f);
-                                    tmem_st32(to + c, o);
+                                    for (int e = 0; e < 16; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * f);
+                                    tmem_st16(to + c, o);
                                 }
                             }
                         }
@@ -567,9 +690,10 @@ __global__ void __launch_bounds__(512, 1)
                     if (lane == 0) mbar_arrive(bar(kPFull + sb));
                 }
                 if (dead) break;
+                kblocks += s.blk1 - s.blk0;
                 // ---- the segment's end
                 const int mine = C::kTiles == 2 ? (w.jobs + 1 - t) / 2 : w.jobs;  // jobs of this pipeline
-                if (mine > 0 && !tc_wait_warp(bar(kPvDone + last), uint32_t(n_s[last] - 1) & 1u, abort_flag, a.flags)) break;
+                if (mine > 0 && !tree_wait_warp(bar(kPvDone + last), uint32_t(n_s[last] - 1) & 1u, abort_flag, a.flags)) break;
                 tc_fence_after();
                 float2 other = make_float2(kNegInf, 0.f);
                 if (joint) {
@@ -579,9 +703,10 @@ __global__ void __launch_bounds__(512, 1)
                         __syncwarp();
                         if (lane == 0) mbar_arrive(bar(kOneDone));
                         ++n_one;
+                        seg_free(seg);
                         continue;
                     }
-                    if (!tc_wait_warp(bar(kOneDone), uint32_t(n_one++) & 1u, abort_flag, a.flags)) break;
+                    if (!tree_wait_warp(bar(kOneDone), uint32_t(n_one++) & 1u, abort_flag, a.flags)) break;
                     tc_fence_after();
                     if (w.jobs > 1) other = stat[row];
                 }
@@ -613,12 +738,12 @@ __global__ void __launch_bounds__(512, 1)
                         }
                         if (fix && at >= 0) {
                             // non-finite elements of the node rows in these blocks, for the rows that attend them
-                            for (int i = 0; i < s.r.n; ++i) {
-                                const int tok = s.r.ctx() + i;
+                            for (int i = 0; i < r.n; ++i) {
+                                const int tok = r.ctx() + i;
                                 const int blk = tree_slots(a, tok + 1) - 1;
                                 if (blk / a.spb < s.blk0 || blk / a.spb >= s.blk1) continue;
-                                if ((tree_allow(a, s.r, node, tok, 1) & 1u) == 0u) continue;
-                                const int page = __ldg(a.indices + s.r.lo + tok / a.page_size);
+                                if ((tree_allow(a, r, node, tok, 1) & 1u) == 0u) continue;
+                                const int page = __ldg(a.indices + r.lo + tok / a.page_size);
                                 if (page < 0 || page >= a.num_total_pages) continue;
                                 const T* v = static_cast<const T*>(a.v) +
                                              ((size_t(page) * a.num_kv_heads + s.kvh) * a.page_size + tok % a.page_size) * D + c;
@@ -654,6 +779,7 @@ __global__ void __launch_bounds__(512, 1)
                     __syncwarp();
                     if (lane == 0) mbar_arrive(bar(kOneFree));
                 }
+                seg_free(seg);
             }
         }
     }

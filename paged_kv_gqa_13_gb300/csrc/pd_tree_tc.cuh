@@ -15,9 +15,10 @@
 // the two (m, l, O) at the end. At head_dim 256 tensor memory holds one O:
 // blocks of 64 keys, S double-buffered, one set of softmax warps.
 //
-// Roles (16 warps): 0-3 and 4-7 softmax of pipeline 0 and 1; 8 producer (TMA
-// of q, K and V into a ring of slots of one K or V block); 9 issues the mma;
-// 12-15 make V safe where weights can be zero: a zero weight does not undo a
+// Roles (16 warps): 0-3 and 4-7 softmax of pipeline 0 and 1; 8, 12 and 13
+// producers (TMA of q, K and V into a ring of slots of one K or V block), 9 and
+// 11 issue the mma of pipeline 0 and 1, 10 walks the segments;
+// 14 and 15 make V safe where weights can be zero: a zero weight does not undo a
 // NaN or an infinity, so in blocks that hold tokens some row does not attend,
 // rows past the end are zeroed and non-finite elements of node rows are
 // replaced by zero, to be added to the rows that attend them at the end.
@@ -162,13 +163,14 @@ struct CfgTree {
     static constexpr int kRingOff = kQSlots * kQBytes;
     static constexpr int kBarOff = kRingOff + kSlots * kSlotBytes;
     // barriers: full[], empty[], vok[] per slot, then these
-    static constexpr int kBars = 3 * kSlots + 2 * 2 + 2 + 2 + 2 + 3 + 2 * 8;
+    static constexpr int kBars = 3 * kSlots + 2 * 2 + 2 + 2 + 2 + 4 + 2 * 8;
     static constexpr int kStatOff = kBarOff + (kBars * 8 + 15) / 16 * 16;  // pipeline 1's (m, l) per row
     static constexpr int kMiscOff = kStatOff + kRows * 8;  // tensor-memory address, abort flag, bad-V tags[4]
     static constexpr int kBadRing = 16;  // more than the K blocks that the producer is ahead of the softmax warps
     static constexpr int kSegOff = kMiscOff + 32 + 4 * kBadRing;
     static constexpr int kBytes = kSegOff + 8 * 64 + 1024;  // 1024: alignment of the base
-    static constexpr int kWalkers = 1 + 1 + 4 + (kTiles == 2 ? 8 : 4);  // warps that read the segments
+    static constexpr int kProducers = 3, kInspectors = 2;
+    static constexpr int kWalkers = kProducers + kTiles + kInspectors + 4 * kTiles;  // warps that read the segments
     static constexpr int kOCols = D;
     static constexpr int kSCol = kTiles * D;
     static constexpr int kThreads = 512;
@@ -215,7 +217,6 @@ struct TcStep {
     __device__ __forceinline__ bool opens_tile() const { return j == 0 || (wide && j == 1); }
     __device__ __forceinline__ bool closes_tile() const { return j + 1 == jobs || (wide && j + 2 == jobs); }
     __device__ __forceinline__ bool first_use() const { return !wide || (j & 1) == 0; }  // of its K (or V) block
-    __device__ __forceinline__ bool last_use() const { return !wide || (j & 1) == 1; }
 };
 
 // The order of the mma warp's steps. seg_wait(i) waits for segment i and
@@ -283,7 +284,7 @@ __global__ void __launch_bounds__(512, 1)
     auto bar = [&](int i) { return sbase + C::kBarOff + 8u * uint32_t(i); };
     constexpr int kFullB = 0, kEmptyB = C::kSlots, kVokB = 2 * C::kSlots, kQFull = 3 * C::kSlots, kQEmpty = kQFull + 2,
                   kSFull = kQEmpty + 2, kPFull = kSFull + 2, kPvDone = kPFull + 2, kOneDone = kPvDone + 2,
-                  kOneFree = kOneDone + 1, kAllDone = kOneFree + 1, kSegFull = kAllDone + 1, kSegFree = kSegFull + kSegRing;
+                  kOneFree = kOneDone + 1, kAllDone = kOneFree + 1, kSegFull = kAllDone + 2, kSegFree = kSegFull + kSegRing;
     static_assert(kSegFree + kSegRing == C::kBars, "barrier count");
     float2* stat = reinterpret_cast<float2*>(smem + C::kStatOff);
     uint32_t* tslot = reinterpret_cast<uint32_t*>(smem + C::kMiscOff);
@@ -295,12 +296,12 @@ __global__ void __launch_bounds__(512, 1)
     if (tid == 0) {
         for (int i = 0; i < C::kSlots; ++i) {
             mbar_init(bar(kFullB + i), 1);
-            mbar_init(bar(kEmptyB + i), 1 + 4);  // the last mma that reads the slot, and the inspectors
-            mbar_init(bar(kVokB + i), 4);
+            mbar_init(bar(kEmptyB + i), C::kTiles + C::kInspectors);  // the mma warps and the inspectors
+            mbar_init(bar(kVokB + i), C::kInspectors);
         }
         for (int i = 0; i < 2; ++i) {
             mbar_init(bar(kQFull + i), 1);
-            mbar_init(bar(kQEmpty + i), 1);
+            mbar_init(bar(kQEmpty + i), C::kTiles);
             mbar_init(bar(kSFull + i), 1);
             mbar_init(bar(kPFull + i), 4);
             mbar_init(bar(kPvDone + i), 1);
@@ -312,6 +313,7 @@ __global__ void __launch_bounds__(512, 1)
         mbar_init(bar(kOneDone), 4);
         mbar_init(bar(kOneFree), 4);
         mbar_init(bar(kAllDone), 1);
+        mbar_init(bar(kAllDone + 1), 1);
         fence_mbar_init();
         *abort_flag = 0;
         for (int i = 0; i < 4; ++i) bad_v[i] = 0;
@@ -364,51 +366,56 @@ __global__ void __launch_bounds__(512, 1)
                 __syncwarp();
                 if (!more) break;
             }
-        } else if (wid == 8) {
-            // ============================================================ producer
+        } else if (wid == 8 || wid == 12 || wid == 13) {
+            // ============================================================ producers (load i by producer i % kProducers)
             const uint64_t once = l2_evict_first_policy(), again = l2_evict_normal_policy();
             Ring<C::kSlots> ring;
             Ring<C::kQSlots> qring;
             int loads = 0, qloads = 0, kblocks = 0;
+            const int me = wid == 8 ? 0 : wid - 11;  // warps 8, 12, 13
+            int turn = 0;                            // the producer whose load is next
             // one box per lane: slot_rows rows x 64 columns
             const int sl = lane / C::kHalves, hf = lane % C::kHalves;
             auto load_block = [&](const TcSeg& s, int blk, const CUtensorMap* tm, bool is_k) -> bool {
+                const bool mine = turn == me;
                 const int p = blk * a.spb + sl;
-                int page = a.num_total_pages, row = 0, at = p;  // page out of range: the copy fills zeros
-                if (a.cpp > 1) {
-                    at = p / a.cpp;
-                    row = (p - at * a.cpp) * a.slot_rows;
-                }
+                int page = a.num_total_pages, row = 0;  // page out of range: the copy fills zeros
                 bool bad = false;
-                if (sl < a.spb && p < s.slots) {
+                if (mine && sl < a.spb && p < s.slots) {
+                    const int at = a.cpp > 1 ? p / a.cpp : p;
+                    row = (p - at * a.cpp) * a.slot_rows;
                     page = __ldg(a.indices + s.lo + at);
                     bad = page < 0 || page >= a.num_total_pages;
                     if (bad) page = a.num_total_pages;
                 }
-                if (is_k) {
-                    const unsigned found = __ballot_sync(kFull, bad);
-                    if (lane == 0) {
-                        unsigned bits = 0;
-                        for (unsigned f = found; f != 0u; f &= f - 1u) bits |= 1u << ((__ffs(f) - 1) / C::kHalves);
-                        bad_slots[kblocks % C::kBadRing] = bits;
-                        if (bits != 0u) atomicOr(a.flags, kFlagBadPage);
-                    }
-                    ++kblocks;
-                }
+                // every producer sees every slot come free, so that no barrier gets two phases ahead of it
                 if (loads >= C::kSlots && !tree_wait_warp(bar(kEmptyB + ring.slot), ring.phase ^ 1u, abort_flag, a.flags)) return false;
-                if (lane == 0) mbar_arrive_expect_tx(bar(kFullB + ring.slot), C::kSlotBytes);
-                __syncwarp();
-                if (sl < a.spb)
-                    tma_load_4d(sbase + C::kRingOff + ring.slot * C::kSlotBytes + hf * (C::kKeys * 128) + sl * a.slot_rows * 128,
-                                tm, hf * 64, row, s.kvh, page, bar(kFullB + ring.slot), s.n > a.nps ? again : once);
+                if (mine) {
+                    if (is_k) {
+                        const unsigned found = __ballot_sync(kFull, bad);
+                        if (lane == 0) {
+                            unsigned bits = 0;
+                            for (unsigned f = found; f != 0u; f &= f - 1u) bits |= 1u << ((__ffs(f) - 1) / C::kHalves);
+                            bad_slots[kblocks % C::kBadRing] = bits;
+                            if (bits != 0u) atomicOr(a.flags, kFlagBadPage);
+                        }
+                    }
+                    if (lane == 0) mbar_arrive_expect_tx(bar(kFullB + ring.slot), C::kSlotBytes);
+                    __syncwarp();
+                    if (sl < a.spb)
+                        tma_load_4d(sbase + C::kRingOff + ring.slot * C::kSlotBytes + hf * (C::kKeys * 128) + sl * a.slot_rows * 128,
+                                    tm, hf * 64, row, s.kvh, page, bar(kFullB + ring.slot), s.n > a.nps ? again : once);
+                }
+                kblocks += is_k;
                 ++loads;
                 ring.next();
+                if (++turn == C::kProducers) turn = 0;
                 return true;
             };
             tc_steps(
                 seg_wait, seg_free,
                 [&](const TcStep& w, const TcSeg& s) {
-                    if (w.opens_tile()) {
+                    if (me == 0 && w.opens_tile()) {
                         if (qloads >= C::kQSlots && !tree_wait_warp(bar(kQEmpty + qring.slot), qring.phase ^ 1u, abort_flag, a.flags))
                             return false;
                         if (lane == 0) {
@@ -431,8 +438,14 @@ __global__ void __launch_bounds__(512, 1)
                 mbar_wait_bounded(bar(kFullB + i % C::kSlots), uint32_t(i / C::kSlots) & 1u);
             for (int i = max(0, qloads - C::kQSlots); i < qloads; ++i)
                 mbar_wait_bounded(bar(kQFull + i % C::kQSlots), uint32_t(i / C::kQSlots) & 1u);
-        } else if (wid == 9) {
+        } else if (wid == 9 || (C::kTiles == 2 && wid == 11)) {
             // ============================================================ mma
+            // Warp 9 issues for pipeline 0, warp 11 for pipeline 1 (head_dim 256: warp
+            // 9 for both S buffers, whose P V add to one O in order). A warp steps
+            // over the other's jobs, so that it sees every load land, but does not
+            // wait for the other's weights: while one prepares and waits, the tensor
+            // cores run what the other has issued.
+            const int own = wid == 9 ? 0 : 1;
             if (lane == 0) {
                 const uint32_t idesc_s = tc_idesc_f16(kBf16, C::kRows, C::kKeys, false) | (a.scale_log2 < 0.f ? kIdescNegA : 0u);
                 constexpr uint32_t idesc_o = tc_idesc_f16(kBf16, C::kRows, D, true);
@@ -455,6 +468,7 @@ __global__ void __launch_bounds__(512, 1)
                     seg_wait1, seg_free1,
                     [&](const TcStep& w, const TcSeg&) {
                         const int t = w.j & 1, rt = w.row_tile();
+                        const bool mine = C::kTiles == 1 || t == own;
                         if (w.opens_tile()) {
                             if (!tree_wait(bar(kQFull + qring.slot), qring.phase, abort_flag, a.flags)) return false;
                             qtile[rt] = qring.slot;
@@ -462,6 +476,11 @@ __global__ void __launch_bounds__(512, 1)
                         }
                         if (w.first_use() && !take(&kslot)) return false;
                         const int qs = rt == 0 ? qtile[0] : qtile[1];
+                        if (!mine) {
+                            if (!w.wide) mbar_arrive(bar(kEmptyB + kslot));
+                            if (w.closes_tile()) tc_commit(bar(kQEmpty + qs));
+                            return true;
+                        }
                         tc_fence_after();
                         const uint64_t kb = kdesc + uint32_t(kslot * (C::kSlotBytes / 16)), qb = qdesc + uint32_t(qs * (C::kQBytes / 16));
                         const uint32_t d = tmem + C::kSCol + t * C::kKeys;
@@ -470,7 +489,7 @@ __global__ void __launch_bounds__(512, 1)
                             tc_mma_f16(d, qb + ((k / 4) * (C::kRows * 128) + (k % 4) * 32) / 16,
                                        kb + ((k / 4) * (C::kKeys * 128) + (k % 4) * 32) / 16, idesc_s, k > 0);
                         tc_commit(bar(kSFull + t));
-                        if (w.last_use()) tc_commit(bar(kEmptyB + kslot));
+                        tc_commit(bar(kEmptyB + kslot));
                         if (w.closes_tile()) tc_commit(bar(kQEmpty + qs));
                         return true;
                     },
@@ -483,6 +502,10 @@ __global__ void __launch_bounds__(512, 1)
                                 vok ^= 1u << vslot;
                             }
                         }
+                        if (C::kTiles == 2 && t != own) {
+                            if (!w.wide) mbar_arrive(bar(kEmptyB + vslot));
+                            return true;
+                        }
                         if (!tree_wait(bar(kPFull + t), (p_phase >> t) & 1u, abort_flag, a.flags)) return false;
                         p_phase ^= 1u << t;
                         tc_fence_after();
@@ -493,19 +516,19 @@ __global__ void __launch_bounds__(512, 1)
                         for (int k = 0; k < C::kKeys / 16; ++k)
                             tc_mma_f16_ta(d, tmem + C::kSCol + t * C::kKeys + 8 * k, vb + k * 128, idesc_o, !fresh || k > 0);
                         tc_commit(bar(kPvDone + t));
-                        if (w.last_use()) tc_commit(bar(kEmptyB + vslot));
+                        tc_commit(bar(kEmptyB + vslot));
                         return true;
                     });
                 // every mma has completed before the tensor memory is released
-                tc_commit(bar(kAllDone));
-                mbar_wait_bounded(bar(kAllDone), 0u);
+                tc_commit(bar(kAllDone + own));
+                mbar_wait_bounded(bar(kAllDone + own), 0u);
             }
-        } else if (wid >= 12) {
+        } else if (wid >= 14) {
             // ============================================================ V inspectors
             // They see every load land and give every slot back, so that no
             // barrier gets two phases ahead of them.
             Ring<C::kSlots> ring;
-            const int t = tid - 384;
+            const int t = tid - 448;
             auto landed = [&](int* slot) {
                 *slot = ring.slot;
                 const bool ok = tree_wait_warp(bar(kFullB + ring.slot), ring.phase, abort_flag, a.flags);
@@ -531,15 +554,13 @@ __global__ void __launch_bounds__(512, 1)
                         return true;
                     }
                     uint8_t* vb = smem + C::kRingOff + slot * C::kSlotBytes;
-                    // one row per thread (two threads per row of a 64-key block)
-                    constexpr int kPer = 128 / C::kKeys;
-                    const int row = t / kPer;
-                    const int tok = tree_token(a, blk, row);
-                    const bool dead = tok < 0 || tok >= s.len, node = tok >= s.len - s.n;
                     constexpr uint32_t kExp = kBf16 ? 0x7f807f80u : 0x7c007c00u;
                     bool found = false;
+                    for (int row = t; row < C::kKeys; row += 32 * C::kInspectors) {
+                    const int tok = tree_token(a, blk, row);
+                    const bool dead = tok < 0 || tok >= s.len, node = tok >= s.len - s.n;
                     if (dead || node) {
-                        for (int hf = t % kPer; hf < C::kHalves; hf += kPer) {
+                        for (int hf = 0; hf < C::kHalves; ++hf) {
 #pragma unroll
                             for (int c = 0; c < 8; ++c) {
                                 uint4* at = reinterpret_cast<uint4*>(vb + hf * (C::kKeys * 128) + row * 128 + ((c ^ (row & 7)) << 4));
@@ -555,6 +576,7 @@ __global__ void __launch_bounds__(512, 1)
                                 }
                             }
                         }
+                    }
                     }
                     if (found) bad_v[w.seg & 3] = w.seg + 1;
                     fence_proxy_async_smem();

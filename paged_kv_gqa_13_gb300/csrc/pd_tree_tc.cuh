@@ -2,33 +2,32 @@
 // accumulators in tensor memory) for 16-bit q over 16-bit paged pools.
 //
 // A row tile is up to 128 rows (nodes x q heads of one kv head): the M of both
-// products. Per block of KB keys and row tile: S = Q K^T (A = Q and B = K from
+// products. Per job of 64 keys and row tile: S = Q K^T (A = Q and B = K from
 // shared memory, K-major as they lie), then the softmax warps turn S into
 // weights P in place (tensor memory), then O += P V (A = P from tensor memory,
 // B = V from shared memory, MN-major as it lies).
 //
-// Two row-tile pipelines t = 0, 1, each with its own S/P and O columns and its
-// own 4 softmax warps, run out of phase: while one's softmax runs, the tensor
-// cores work for the other. A segment of more than one row tile (up to two)
-// gives each pipeline its own rows, both over every block ("wide"); one of a
-// single row tile gives both the same rows over alternate blocks, and joins
-// the two (m, l, O) at the end. At head_dim 256 tensor memory holds one O:
-// blocks of 64 keys, S double-buffered, one set of softmax warps.
+// Two pipelines t = 0, 1, each with its own O, two S buffers, an mma warp and 4
+// softmax warps. A pipeline's next S is computed while its softmax works on
+// the one before, and the other pipeline's products fill the rest. A segment
+// of more than one row tile (up to two) gives each pipeline its own rows, both
+// over every block ("wide"); one of a single row tile gives both the same rows
+// over alternate blocks, and joins the two (m, l, O) at the end. At head_dim
+// 256 tensor memory holds one O: one pipeline.
+//
+// K and V come in blocks of kKeys keys through one ring of slots, K and V of
+// block n as loads 2 n and 2 n + 1 of the CTA. Every role that waits for
+// loads steps over all of them in order, so that no barrier gets two phases
+// ahead of a role (a wait tells phases apart by parity only).
 //
 // Roles (16 warps): 0-3 and 4-7 softmax of pipeline 0 and 1; 8, 12 and 13
-// producers (TMA of q, K and V into a ring of slots of one K or V block), 9 and
-// 11 issue the mma of pipeline 0 and 1, 10 walks the segments;
-// 14 and 15 make V safe where weights can be zero: a zero weight does not undo a
-// NaN or an infinity, so in blocks that hold tokens some row does not attend,
-// rows past the end are zeroed and non-finite elements of node rows are
-// replaced by zero, to be added to the rows that attend them at the end.
-// Registers move from the last two warpgroups to the softmax warps, whose
-// threads hold a row of S.
-//
-// Producer, mma and inspectors follow the same sequence of steps, which each
-// of them generates for itself (TcSteps): a pipeline's next S is issued as
-// soon as its last P V has been, so the ring is filled in the order in which
-// the mma warp waits.
+// producers (TMA; load i by producer i % 3: a box of 16 rows x 128 bytes costs
+// its issuing warp about 75 cycles, and one warp alone kept the ring from
+// filling); 9 and 11 mma of pipeline 0 and 1; 10 walks the segments; 14 and 15
+// make V safe where weights can be zero: a zero weight does not undo a NaN or
+// an infinity, so in blocks that hold tokens some row does not attend, rows
+// past the end are zeroed and non-finite elements of node rows are replaced by
+// zero, to be added to the rows that attend them at the end.
 //
 // The running maximum of a row moves only when it rises by more than 2^8 (the
 // weights then stay below 2^8, and O, in tensor memory, is rescaled rarely).
@@ -116,15 +115,6 @@ __device__ __forceinline__ void tmem_st32(uint32_t taddr, const uint32_t* r) {
 
 __device__ __forceinline__ void tmem_wait_st() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
 
-template <int R>
-__device__ __forceinline__ void regs_inc() {
-    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(R));
-}
-template <int R>
-__device__ __forceinline__ void regs_dec() {
-    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(R));
-}
-
 // Wait for phase `parity` of `bar`; false when the CTA is aborting or the wait
 // runs out, which sets the abort flag and the status bit. The limit is counted
 // on the SM clock (4e9 cycles, about 2 s): a read of the global timer takes
@@ -153,28 +143,33 @@ __device__ __forceinline__ bool tree_wait_warp(uint32_t bar, uint32_t parity, vo
 template <int D>
 struct CfgTree {
     static constexpr int kRows = 128;
-    static constexpr int kTiles = D == 256 ? 1 : 2;    // O accumulators
-    static constexpr int kKeys = D == 256 ? 64 : 128;  // keys per block
+    static constexpr int kTiles = D == 256 ? 1 : 2;    // pipelines, O accumulators
+    static constexpr int kKeys = D == 256 ? 64 : 128;  // keys per K or V block
+    static constexpr int kJobKeys = 64;
+    static constexpr int kJobs = kKeys / kJobKeys;     // jobs per block
     static constexpr int kHalves = D / 64;             // 128-byte column blocks of a row
     static constexpr int kSlotBytes = kKeys * D * 2;   // one K or V block
     static constexpr int kQBytes = kRows * D * 2;      // one row tile of q
     static constexpr int kQSlots = kTiles;
     static constexpr int kSlots = D == 64 ? 10 : 5;
-    static constexpr int kRingOff = kQSlots * kQBytes;
-    static constexpr int kBarOff = kRingOff + kSlots * kSlotBytes;
-    // barriers: full[], empty[], vok[] per slot, then these
-    static constexpr int kBars = 3 * kSlots + 2 * 2 + 2 + 2 + 2 + 4 + 2 * 8;
-    static constexpr int kStatOff = kBarOff + (kBars * 8 + 15) / 16 * 16;  // pipeline 1's (m, l) per row
-    static constexpr int kMiscOff = kStatOff + kRows * 8;  // tensor-memory address, abort flag, bad-V tags[4]
-    static constexpr int kBadRing = 16;  // more than the K blocks that the producer is ahead of the softmax warps
-    static constexpr int kSegOff = kMiscOff + 32 + 4 * kBadRing;
-    static constexpr int kBytes = kSegOff + 8 * 64 + 1024;  // 1024: alignment of the base
     static constexpr int kProducers = 3, kInspectors = 2;
     static constexpr int kWalkers = kProducers + kTiles + kInspectors + 4 * kTiles;  // warps that read the segments
-    static constexpr int kOCols = D;
-    static constexpr int kSCol = kTiles * D;
+    static constexpr int kSegRing = 8;
+    static constexpr int kBadRing = 16;  // more than the K blocks that the producers are ahead of the softmax warps
+    // barriers (8 bytes each)
+    static constexpr int kFull = 0, kEmpty = kFull + kSlots, kVok = kEmpty + kSlots, kQFull = kVok + kSlots,
+                         kQEmpty = kQFull + 2, kSFull = kQEmpty + 2, kPFull = kSFull + 4, kPvDone = kPFull + 4,
+                         kOneDone = kPvDone + 4, kOneFree = kOneDone + 1, kAllDone = kOneFree + 1, kSegFull = kAllDone + 2,
+                         kSegFree = kSegFull + kSegRing, kBars = kSegFree + kSegRing;
+    static constexpr int kRingOff = kQSlots * kQBytes;
+    static constexpr int kBarOff = kRingOff + kSlots * kSlotBytes;
+    static constexpr int kStatOff = kBarOff + round_up(kBars * 8, 16);  // pipeline 1's (m, l) per row
+    static constexpr int kMiscOff = kStatOff + kRows * 8;  // tensor-memory address, abort flag, bad-V tags[4], bad slots
+    static constexpr int kSegOff = kMiscOff + 32 + 4 * kBadRing;
+    static constexpr int kBytes = kSegOff + kSegRing * 64 + 1024;  // 1024: alignment of the base
+    static constexpr int kSCol = kTiles * D;               // S buffer b of pipeline t at kSCol + (2 t + b) * kJobKeys
     static constexpr int kThreads = 512;
-    static_assert(kSCol + 2 * kKeys <= 512, "tensor memory");
+    static_assert(kSCol + 2 * kTiles * kJobKeys <= 512, "tensor memory");
     static_assert(kBytes <= 232448, "shared memory");
 };
 
@@ -194,59 +189,6 @@ struct alignas(16) TcSeg {
         return r;
     }
 };
-constexpr int kSegRing = 8;
-
-// One step of the sequence. Job j of a segment is block j / 2 for pipeline
-// j % 2 (wide), or block j for pipeline (S buffer, at head_dim 256) j % 2.
-struct TcStep {
-    int j = 0, jobs = 0, seg = -1;  // job, jobs of the segment, segments before it
-    int blk0 = 0, tail0 = 0;
-    bool wide = false;
-    __device__ __forceinline__ bool enter(const TcSeg& s) {
-        wide = s.wide != 0;
-        blk0 = s.blk0;
-        tail0 = s.tail0;
-        jobs = (s.blk1 - blk0) * (wide ? 2 : 1);
-        j = 0;
-        ++seg;
-        return jobs > 0;
-    }
-    __device__ __forceinline__ int block() const { return blk0 + (wide ? j >> 1 : j); }
-    __device__ __forceinline__ bool tail() const { return block() >= tail0; }
-    __device__ __forceinline__ int row_tile() const { return wide ? j & 1 : 0; }
-    __device__ __forceinline__ bool opens_tile() const { return j == 0 || (wide && j == 1); }
-    __device__ __forceinline__ bool closes_tile() const { return j + 1 == jobs || (wide && j + 2 == jobs); }
-    __device__ __forceinline__ bool first_use() const { return !wide || (j & 1) == 0; }  // of its K (or V) block
-};
-
-// The order of the mma warp's steps. seg_wait(i) waits for segment i and
-// returns it (null to stop), seg_free(i) gives it back; on_qk(step, seg) and
-// on_pv(step, seg) return false to stop.
-template <class SegWait, class SegFree, class OnQk, class OnPv>
-__device__ __forceinline__ void tc_steps(SegWait seg_wait, SegFree seg_free, OnQk on_qk, OnPv on_pv) {
-    TcStep q, p;
-    const TcSeg *sq = seg_wait(0), *sp = sq;
-    if (sq == nullptr || !q.enter(*sq)) return;
-    p = q;
-    bool more = true;
-    int ahead = 0;  // bit t: pipeline t has an S whose P V is still to come
-    for (;;) {
-        while (more && ((ahead >> (q.j & 1)) & 1) == 0) {
-            if (!on_qk(q, *sq)) return;
-            ahead |= 1 << (q.j & 1);
-            if (++q.j == q.jobs) {
-                if ((sq = seg_wait(q.seg + 1)) == nullptr) return;
-                more = q.enter(*sq);
-            }
-        }
-        if (!on_pv(p, *sp)) return;
-        ahead &= ~(1 << (p.j & 1));
-        if (++p.j == p.jobs) {
-            seg_free(p.seg);
-            if ((sp = seg_wait(p.seg + 1)) == nullptr || !p.enter(*sp)) return;
-        }
-    }
-}
 
 // A place in a ring of N slots and the phase of its barriers.
 template <int N>
@@ -282,38 +224,36 @@ __global__ void __launch_bounds__(512, 1)
     const uint32_t sbase = smem_u32(smem);
     const int tid = threadIdx.x, lane = tid & 31, wid = tid >> 5;
     auto bar = [&](int i) { return sbase + C::kBarOff + 8u * uint32_t(i); };
-    constexpr int kFullB = 0, kEmptyB = C::kSlots, kVokB = 2 * C::kSlots, kQFull = 3 * C::kSlots, kQEmpty = kQFull + 2,
-                  kSFull = kQEmpty + 2, kPFull = kSFull + 2, kPvDone = kPFull + 2, kOneDone = kPvDone + 2,
-                  kOneFree = kOneDone + 1, kAllDone = kOneFree + 1, kSegFull = kAllDone + 2, kSegFree = kSegFull + kSegRing;
-    static_assert(kSegFree + kSegRing == C::kBars, "barrier count");
     float2* stat = reinterpret_cast<float2*>(smem + C::kStatOff);
     uint32_t* tslot = reinterpret_cast<uint32_t*>(smem + C::kMiscOff);
     volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + C::kMiscOff + 4);
     volatile int* bad_v = reinterpret_cast<volatile int*>(smem + C::kMiscOff + 16);
     // slots of each K block whose page id is bad, by the K block's number in this CTA
     volatile uint32_t* bad_slots = reinterpret_cast<volatile uint32_t*>(smem + C::kMiscOff + 32);
+    TcSeg* segs = reinterpret_cast<TcSeg*>(smem + C::kSegOff);
 
     if (tid == 0) {
         for (int i = 0; i < C::kSlots; ++i) {
-            mbar_init(bar(kFullB + i), 1);
-            mbar_init(bar(kEmptyB + i), C::kTiles + C::kInspectors);  // the mma warps and the inspectors
-            mbar_init(bar(kVokB + i), C::kInspectors);
+            mbar_init(bar(C::kFull + i), 1);
+            mbar_init(bar(C::kEmpty + i), C::kTiles + C::kInspectors);  // the mma warps and the inspectors
+            mbar_init(bar(C::kVok + i), C::kInspectors);
         }
         for (int i = 0; i < 2; ++i) {
-            mbar_init(bar(kQFull + i), 1);
-            mbar_init(bar(kQEmpty + i), C::kTiles);
-            mbar_init(bar(kSFull + i), 1);
-            mbar_init(bar(kPFull + i), 4);
-            mbar_init(bar(kPvDone + i), 1);
+            mbar_init(bar(C::kQFull + i), 1);
+            mbar_init(bar(C::kQEmpty + i), C::kTiles);
+            mbar_init(bar(C::kAllDone + i), 1);
         }
-        for (int i = 0; i < kSegRing; ++i) {
-            mbar_init(bar(kSegFull + i), 1);
-            mbar_init(bar(kSegFree + i), C::kWalkers);
+        for (int i = 0; i < 4; ++i) {
+            mbar_init(bar(C::kSFull + i), 1);
+            mbar_init(bar(C::kPFull + i), 4);
+            mbar_init(bar(C::kPvDone + i), 1);
         }
-        mbar_init(bar(kOneDone), 4);
-        mbar_init(bar(kOneFree), 4);
-        mbar_init(bar(kAllDone), 1);
-        mbar_init(bar(kAllDone + 1), 1);
+        for (int i = 0; i < C::kSegRing; ++i) {
+            mbar_init(bar(C::kSegFull + i), 1);
+            mbar_init(bar(C::kSegFree + i), C::kWalkers);
+        }
+        mbar_init(bar(C::kOneDone), 4);
+        mbar_init(bar(C::kOneFree), 4);
         fence_mbar_init();
         *abort_flag = 0;
         for (int i = 0; i < 4; ++i) bad_v[i] = 0;
@@ -330,236 +270,256 @@ __global__ void __launch_bounds__(512, 1)
     tc_fence_after();
     launch_dependents();
     const uint32_t tmem = *tslot;
-    TcSeg* segs = reinterpret_cast<TcSeg*>(smem + C::kSegOff);
-    // one lane / a whole warp
-    auto seg_wait1 = [&](int i) -> const TcSeg* {
-        return tree_wait(bar(kSegFull + i % kSegRing), uint32_t(i / kSegRing) & 1u, abort_flag, a.flags) ? segs + i % kSegRing : nullptr;
-    };
-    auto seg_wait = [&](int i) -> const TcSeg* {
-        return tree_wait_warp(bar(kSegFull + i % kSegRing), uint32_t(i / kSegRing) & 1u, abort_flag, a.flags) ? segs + i % kSegRing
-                                                                                                            : nullptr;
-    };
-    auto seg_free1 = [&](int i) { mbar_arrive(bar(kSegFree + i % kSegRing)); };
+
+    auto wait1 = [&](int b, uint32_t phase) { return tree_wait(bar(b), phase, abort_flag, a.flags); };
+    auto wait = [&](int b, uint32_t phase) { return tree_wait_warp(bar(b), phase, abort_flag, a.flags); };
+    // Segment i (a segment without blocks ends the line), waiting for it, and giving it back.
+    auto seg_at = [&](int i) -> const TcSeg& { return segs[i % C::kSegRing]; };
+    auto seg_wait = [&](int i) { return wait(C::kSegFull + i % C::kSegRing, uint32_t(i / C::kSegRing) & 1u); };
     auto seg_free = [&](int i) {
         __syncwarp();
-        if (lane == 0) mbar_arrive(bar(kSegFree + i % kSegRing));
+        if (lane == 0) mbar_arrive(bar(C::kSegFree + i % C::kSegRing));
     };
 
-    if (wid >= 8) {
-        regs_dec<64>();
-        if (wid == 10) {
-            // ============================================================ segments
-            TreeWalk::Seg s;
-            for (int i = 0;; ++i) {
-                const bool more = walk.next(a, &s);
-                if (i >= kSegRing &&
-                    !tree_wait_warp(bar(kSegFree + i % kSegRing), uint32_t(i / kSegRing - 1) & 1u, abort_flag, a.flags))
-                    break;
+    if (wid == 10) {
+        // ================================================================ segments
+        TreeWalk::Seg s;
+        for (int i = 0;; ++i) {
+            const bool more = walk.next(a, &s);
+            if (i >= C::kSegRing && !wait(C::kSegFree + i % C::kSegRing, uint32_t(i / C::kSegRing - 1) & 1u)) break;
+            if (lane == 0) {
+                TcSeg x{};
+                if (more)
+                    x = TcSeg{s.blk0, s.blk1,  s.tail0, s.slots, s.slot,  s.row0, s.node0,   s.nodes,
+                              s.hh,   s.head0, s.kvh,   s.r.lo,  s.r.len, s.r.n,  s.r.start, C::kTiles == 2 && s.nodes > a.npt};
+                segs[i % C::kSegRing] = x;
+                mbar_arrive(bar(C::kSegFull + i % C::kSegRing));
+            }
+            __syncwarp();
+            if (!more) break;
+        }
+    } else if (wid == 8 || wid == 12 || wid == 13) {
+        // ================================================================ producers
+        const uint64_t once = l2_evict_first_policy(), again = l2_evict_normal_policy();
+        const int me = wid == 8 ? 0 : wid - 11;
+        Ring<C::kSlots> ring;
+        Ring<C::kQSlots> qring;
+        int loads = 0, qloads = 0, kblocks = 0, turn = 0;  // turn: the producer whose load is next
+        bool ok = true;
+        // one box per lane: slot_rows rows x 64 columns
+        const int sl = lane / C::kHalves, hf = lane % C::kHalves;
+        auto load_block = [&](const TcSeg& s, int blk, const CUtensorMap* tm, bool is_k) -> bool {
+            const bool mine = turn == me;
+            const int p = blk * a.spb + sl;
+            int page = a.num_total_pages, row = 0;  // page out of range: the copy fills zeros
+            bool bad = false;
+            if (mine && sl < a.spb && p < s.slots) {
+                const int at = a.cpp > 1 ? p / a.cpp : p;
+                row = (p - at * a.cpp) * a.slot_rows;
+                page = __ldg(a.indices + s.lo + at);
+                bad = page < 0 || page >= a.num_total_pages;
+                if (bad) page = a.num_total_pages;
+            }
+            if (loads >= C::kSlots && !wait(C::kEmpty + ring.slot, ring.phase ^ 1u)) return false;
+            if (mine) {
+                if (is_k) {
+                    const unsigned found = __ballot_sync(kFull, bad);
+                    if (lane == 0) {
+                        unsigned bits = 0;
+                        for (unsigned f = found; f != 0u; f &= f - 1u) bits |= 1u << ((__ffs(f) - 1) / C::kHalves);
+                        bad_slots[kblocks % C::kBadRing] = bits;
+                        if (bits != 0u) atomicOr(a.flags, kFlagBadPage);
+                    }
+                }
+                if (lane == 0) mbar_arrive_expect_tx(bar(C::kFull + ring.slot), C::kSlotBytes);
+                __syncwarp();
+                if (sl < a.spb)
+                    tma_load_4d(sbase + C::kRingOff + ring.slot * C::kSlotBytes + hf * (C::kKeys * 128) + sl * a.slot_rows * 128,
+                                tm, hf * 64, row, s.kvh, page, bar(C::kFull + ring.slot), s.n > a.nps ? again : once);
+            }
+            ++loads;
+            ring.next();
+            if (++turn == C::kProducers) turn = 0;
+            return true;
+        };
+        for (int i = 0; ok; ++i) {
+            if (!seg_wait(i)) break;
+            const TcSeg& s = seg_at(i);
+            const int blk0 = s.blk0, blk1 = s.blk1;
+            if (blk0 == blk1) break;
+            for (int rt = 0; me == 0 && rt <= s.wide && ok; ++rt) {
+                ok = qloads < C::kQSlots || wait(C::kQEmpty + qring.slot, qring.phase ^ 1u);
+                if (!ok) break;
                 if (lane == 0) {
-                    TcSeg x{};
-                    if (more)
-                        x = TcSeg{s.blk0, s.blk1,  s.tail0, s.slots, s.slot,  s.row0, s.node0,   s.nodes,
-                                  s.hh,   s.head0, s.kvh,   s.r.lo,  s.r.len, s.r.n,  s.r.start, C::kTiles == 2 && s.nodes > a.npt};
-                    segs[i % kSegRing] = x;
-                    mbar_arrive(bar(kSegFull + i % kSegRing));
+                    mbar_arrive_expect_tx(bar(C::kQFull + qring.slot), uint32_t(a.npt * a.hpt) * D * 2);
+                    for (int h = 0; h < C::kHalves; ++h)
+                        tma_load_3d(sbase + qring.slot * C::kQBytes + h * (C::kRows * 128), &tmq, h * 64, s.head0,
+                                    s.row0 + rt * a.npt, bar(C::kQFull + qring.slot));
                 }
                 __syncwarp();
-                if (!more) break;
+                ++qloads;
+                qring.next();
             }
-        } else if (wid == 8 || wid == 12 || wid == 13) {
-            // ============================================================ producers (load i by producer i % kProducers)
-            const uint64_t once = l2_evict_first_policy(), again = l2_evict_normal_policy();
+            for (int blk = blk0; blk < blk1 && ok; ++blk, ++kblocks)
+                ok = load_block(s, blk, &tmk, true) && load_block(s, blk, &tmv, false);
+            seg_free(i);
+        }
+        // copies issued last may still be landing when another role has stopped early
+        for (int i = max(0, loads - C::kSlots); i < loads; ++i)
+            mbar_wait_bounded(bar(C::kFull + i % C::kSlots), uint32_t(i / C::kSlots) & 1u);
+        for (int i = max(0, qloads - C::kQSlots); i < qloads; ++i)
+            mbar_wait_bounded(bar(C::kQFull + i % C::kQSlots), uint32_t(i / C::kQSlots) & 1u);
+    } else if (wid == 9 || (C::kTiles == 2 && wid == 11)) {
+        // ================================================================ mma of pipeline `own`
+        const int own = wid == 9 ? 0 : 1;
+        if (lane == 0) {
+            const uint32_t idesc_s = tc_idesc_f16(kBf16, C::kRows, C::kJobKeys, false) | (a.scale_log2 < 0.f ? kIdescNegA : 0u);
+            constexpr uint32_t idesc_o = tc_idesc_f16(kBf16, C::kRows, D, true);
+            // operand descriptors of slot 0 (K K-major, V MN-major) and of q slot 0; addresses count 16 bytes
+            const uint64_t kdesc = smem_desc_sw128(sbase + C::kRingOff, 16, 1024);
+            const uint64_t vdesc = smem_desc_sw128(sbase + C::kRingOff, C::kKeys * 128, 1024);
+            const uint64_t qdesc = smem_desc_sw128(sbase, 16, 1024);
+            const uint32_t s_cols = tmem + C::kSCol + own * 2 * C::kJobKeys, o_cols = tmem + own * D;
             Ring<C::kSlots> ring;
             Ring<C::kQSlots> qring;
-            int loads = 0, qloads = 0, kblocks = 0;
-            const int me = wid == 8 ? 0 : wid - 11;  // warps 8, 12, 13
-            int turn = 0;                            // the producer whose load is next
-            // one box per lane: slot_rows rows x 64 columns
-            const int sl = lane / C::kHalves, hf = lane % C::kHalves;
-            auto load_block = [&](const TcSeg& s, int blk, const CUtensorMap* tm, bool is_k) -> bool {
-                const bool mine = turn == me;
-                const int p = blk * a.spb + sl;
-                int page = a.num_total_pages, row = 0;  // page out of range: the copy fills zeros
-                bool bad = false;
-                if (mine && sl < a.spb && p < s.slots) {
-                    const int at = a.cpp > 1 ? p / a.cpp : p;
-                    row = (p - at * a.cpp) * a.slot_rows;
-                    page = __ldg(a.indices + s.lo + at);
-                    bad = page < 0 || page >= a.num_total_pages;
-                    if (bad) page = a.num_total_pages;
-                }
-                // every producer sees every slot come free, so that no barrier gets two phases ahead of it
-                if (loads >= C::kSlots && !tree_wait_warp(bar(kEmptyB + ring.slot), ring.phase ^ 1u, abort_flag, a.flags)) return false;
-                if (mine) {
-                    if (is_k) {
-                        const unsigned found = __ballot_sync(kFull, bad);
-                        if (lane == 0) {
-                            unsigned bits = 0;
-                            for (unsigned f = found; f != 0u; f &= f - 1u) bits |= 1u << ((__ffs(f) - 1) / C::kHalves);
-                            bad_slots[kblocks % C::kBadRing] = bits;
-                            if (bits != 0u) atomicOr(a.flags, kFlagBadPage);
-                        }
-                    }
-                    if (lane == 0) mbar_arrive_expect_tx(bar(kFullB + ring.slot), C::kSlotBytes);
-                    __syncwarp();
-                    if (sl < a.spb)
-                        tma_load_4d(sbase + C::kRingOff + ring.slot * C::kSlotBytes + hf * (C::kKeys * 128) + sl * a.slot_rows * 128,
-                                    tm, hf * 64, row, s.kvh, page, bar(kFullB + ring.slot), s.n > a.nps ? again : once);
-                }
-                kblocks += is_k;
-                ++loads;
-                ring.next();
-                if (++turn == C::kProducers) turn = 0;
-                return true;
-            };
-            tc_steps(
-                seg_wait, seg_free,
-                [&](const TcStep& w, const TcSeg& s) {
-                    if (me == 0 && w.opens_tile()) {
-                        if (qloads >= C::kQSlots && !tree_wait_warp(bar(kQEmpty + qring.slot), qring.phase ^ 1u, abort_flag, a.flags))
-                            return false;
-                        if (lane == 0) {
-                            mbar_arrive_expect_tx(bar(kQFull + qring.slot), uint32_t(a.npt * a.hpt) * D * 2);
-                            for (int h = 0; h < C::kHalves; ++h)
-                                tma_load_3d(sbase + qring.slot * C::kQBytes + h * (C::kRows * 128), &tmq, h * 64, s.head0,
-                                            s.row0 + w.row_tile() * a.npt, bar(kQFull + qring.slot));
-                        }
-                        __syncwarp();
-                        ++qloads;
-                        qring.next();
-                    }
-                    return !w.first_use() || load_block(s, w.block(), &tmk, true);
-                },
-                [&](const TcStep& w, const TcSeg& s) {
-                    return !w.first_use() || load_block(s, w.block(), &tmv, false);
-                });
-            // copies issued last may still be landing when another role has stopped early
-            for (int i = max(0, loads - C::kSlots); i < loads; ++i)
-                mbar_wait_bounded(bar(kFullB + i % C::kSlots), uint32_t(i / C::kSlots) & 1u);
-            for (int i = max(0, qloads - C::kQSlots); i < qloads; ++i)
-                mbar_wait_bounded(bar(kQFull + i % C::kQSlots), uint32_t(i / C::kQSlots) & 1u);
-        } else if (wid == 9 || (C::kTiles == 2 && wid == 11)) {
-            // ============================================================ mma
-            // Warp 9 issues for pipeline 0, warp 11 for pipeline 1 (head_dim 256: warp
-            // 9 for both S buffers, whose P V add to one O in order). A warp steps
-            // over the other's jobs, so that it sees every load land, but does not
-            // wait for the other's weights: while one prepares and waits, the tensor
-            // cores run what the other has issued.
-            const int own = wid == 9 ? 0 : 1;
-            if (lane == 0) {
-                const uint32_t idesc_s = tc_idesc_f16(kBf16, C::kRows, C::kKeys, false) | (a.scale_log2 < 0.f ? kIdescNegA : 0u);
-                constexpr uint32_t idesc_o = tc_idesc_f16(kBf16, C::kRows, D, true);
-                // operand descriptors of slot 0 (K K-major, V MN-major) and of q slot 0; addresses count 16 bytes
-                const uint64_t kdesc = smem_desc_sw128(sbase + C::kRingOff, 16, 1024);
-                const uint64_t vdesc = smem_desc_sw128(sbase + C::kRingOff, C::kKeys * 128, 1024);
-                const uint64_t qdesc = smem_desc_sw128(sbase, 16, 1024);
-                Ring<C::kSlots> ring;
-                Ring<C::kQSlots> qring;
-                int kslot = 0, vslot = 0, qtile[2] = {0, 0};
-                uint32_t vok = 0;          // phase of each slot's vok barrier
-                uint32_t p_phase = 0;      // bit t: phase of pfull t
-                auto take = [&](int* slot) {
-                    *slot = ring.slot;
-                    const bool ok = tree_wait(bar(kFullB + ring.slot), ring.phase, abort_flag, a.flags);
-                    ring.next();
-                    return ok;
-                };
-                tc_steps(
-                    seg_wait1, seg_free1,
-                    [&](const TcStep& w, const TcSeg&) {
-                        const int t = w.j & 1, rt = w.row_tile();
-                        const bool mine = C::kTiles == 1 || t == own;
-                        if (w.opens_tile()) {
-                            if (!tree_wait(bar(kQFull + qring.slot), qring.phase, abort_flag, a.flags)) return false;
-                            qtile[rt] = qring.slot;
-                            qring.next();
-                        }
-                        if (w.first_use() && !take(&kslot)) return false;
-                        const int qs = rt == 0 ? qtile[0] : qtile[1];
-                        if (!mine) {
-                            if (!w.wide) mbar_arrive(bar(kEmptyB + kslot));
-                            if (w.closes_tile()) tc_commit(bar(kQEmpty + qs));
-                            return true;
-                        }
-                        tc_fence_after();
-                        const uint64_t kb = kdesc + uint32_t(kslot * (C::kSlotBytes / 16)), qb = qdesc + uint32_t(qs * (C::kQBytes / 16));
-                        const uint32_t d = tmem + C::kSCol + t * C::kKeys;
-#pragma unroll
-                        for (int k = 0; k < D / 16; ++k)
-                            tc_mma_f16(d, qb + ((k / 4) * (C::kRows * 128) + (k % 4) * 32) / 16,
-                                       kb + ((k / 4) * (C::kKeys * 128) + (k % 4) * 32) / 16, idesc_s, k > 0);
-                        tc_commit(bar(kSFull + t));
-                        tc_commit(bar(kEmptyB + kslot));
-                        if (w.closes_tile()) tc_commit(bar(kQEmpty + qs));
-                        return true;
-                    },
-                    [&](const TcStep& w, const TcSeg&) {
-                        const int t = w.j & 1;
-                        if (w.first_use()) {
-                            if (!take(&vslot)) return false;
-                            if (w.tail()) {
-                                if (!tree_wait(bar(kVokB + vslot), (vok >> vslot) & 1u, abort_flag, a.flags)) return false;
-                                vok ^= 1u << vslot;
-                            }
-                        }
-                        if (C::kTiles == 2 && t != own) {
-                            if (!w.wide) mbar_arrive(bar(kEmptyB + vslot));
-                            return true;
-                        }
-                        if (!tree_wait(bar(kPFull + t), (p_phase >> t) & 1u, abort_flag, a.flags)) return false;
-                        p_phase ^= 1u << t;
-                        tc_fence_after();
-                        const uint64_t vb = vdesc + uint32_t(vslot * (C::kSlotBytes / 16));
-                        const uint32_t d = tmem + (C::kTiles == 2 ? t * C::kOCols : 0);
-                        const bool fresh = C::kTiles == 2 ? w.j < 2 : w.j == 0;
-#pragma unroll
-                        for (int k = 0; k < C::kKeys / 16; ++k)
-                            tc_mma_f16_ta(d, tmem + C::kSCol + t * C::kKeys + 8 * k, vb + k * 128, idesc_o, !fresh || k > 0);
-                        tc_commit(bar(kPvDone + t));
-                        tc_commit(bar(kEmptyB + vslot));
-                        return true;
-                    });
-                // every mma has completed before the tensor memory is released
-                tc_commit(bar(kAllDone + own));
-                mbar_wait_bounded(bar(kAllDone + own), 0u);
-            }
-        } else if (wid >= 14) {
-            // ============================================================ V inspectors
-            // They see every load land and give every slot back, so that no
-            // barrier gets two phases ahead of them.
-            Ring<C::kSlots> ring;
-            const int t = tid - 448;
-            auto landed = [&](int* slot) {
+            uint32_t vok = 0;             // phase of each slot's vok barrier
+            int n_qk = 0, n_pv = 0;       // jobs issued; job x is in S buffer x & 1
+            // The place of the S products: segment, block, and what of them is needed.
+            int seg = -1, blk = 0, blk0 = 0, blk1 = 0, tail0 = 0, kslot = 0, vslot = 0, qslot = 0, nq = 0;
+            bool wide = false, first = false;
+            auto land = [&](int* slot) {
                 *slot = ring.slot;
-                const bool ok = tree_wait_warp(bar(kFullB + ring.slot), ring.phase, abort_flag, a.flags);
+                const bool ok = wait1(C::kFull + ring.slot, ring.phase);
                 ring.next();
                 return ok;
             };
-            tc_steps(
-                seg_wait, seg_free,
-                [&](const TcStep& w, const TcSeg&) {
-                    if (!w.first_use()) return true;
-                    int slot;
-                    if (!landed(&slot)) return false;
-                    if (lane == 0) mbar_arrive(bar(kEmptyB + slot));
-                    return true;
-                },
-                [&](const TcStep& w, const TcSeg& s) {
-                    if (!w.first_use()) return true;
-                    const int blk = w.block();
-                    int slot;
-                    if (!landed(&slot)) return false;
-                    if (!w.tail()) {
-                        if (lane == 0) mbar_arrive(bar(kEmptyB + slot));
-                        return true;
+            auto land_v = [&]() {
+                if (!land(&vslot)) return false;
+                if (blk >= tail0) {
+                    const bool ok = wait1(C::kVok + vslot, (vok >> vslot) & 1u);
+                    vok ^= 1u << vslot;
+                    return ok;
+                }
+                return true;
+            };
+            // To the pipeline's next block, over the other's; its K has landed then
+            // (1). 0: none left, -1: stop, 2: not among the next `limit` blocks (call
+            // again). While a P V of this pipeline holds its V slot, the ring lets
+            // only the next two blocks land, so that the limit is 2 then.
+            auto advance = [&](int limit) -> int {
+                for (; limit > 0; --limit) {
+                    if (++blk >= blk1) {
+                        if (seg >= 0) {  // every S of this segment has been issued
+                            for (int i = 0; i < nq; ++i) tc_commit(bar(C::kQEmpty + (C::kQSlots == 1 ? 0 : (qslot + i) % 2)));
+                            mbar_arrive(bar(C::kSegFree + seg % C::kSegRing));
+                        }
+                        ++seg;
+                        if (!wait1(C::kSegFull + seg % C::kSegRing, uint32_t(seg / C::kSegRing) & 1u)) return -1;
+                        const TcSeg& s = seg_at(seg);
+                        if (s.blk0 == s.blk1) return 0;
+                        blk = blk0 = s.blk0;
+                        blk1 = s.blk1;
+                        tail0 = s.tail0;
+                        wide = s.wide != 0;
+                        nq = wide ? 2 : 1;
+                        qslot = qring.slot;
+                        for (int i = 0; i < nq; ++i) {
+                            if (!wait1(C::kQFull + qring.slot, qring.phase)) return -1;
+                            qring.next();
+                        }
+                        first = true;
                     }
-                    uint8_t* vb = smem + C::kRingOff + slot * C::kSlotBytes;
-                    constexpr uint32_t kExp = kBf16 ? 0x7f807f80u : 0x7c007c00u;
+                    if (!land(&kslot)) return -1;
+                    if (C::kTiles == 1 || wide || ((blk - blk0) & 1) == own) return 1;
+                    // the other pipeline's block: seen to land, and given back
+                    int vs;
+                    if (!land(&vs)) return -1;
+                    if (blk >= tail0) vok ^= 1u << vs;
+                    mbar_arrive(bar(C::kEmpty + kslot));
+                    mbar_arrive(bar(C::kEmpty + vs));
+                }
+                return 2;
+            };
+            constexpr int kAny = 0x7fffffff;
+            auto issue_s = [&](int half) {
+                tc_fence_after();
+                const int qs = C::kQSlots == 1 ? 0 : wide ? (qslot + own) % 2 : qslot;
+                const uint64_t kb = kdesc + uint32_t(kslot * (C::kSlotBytes / 16) + half * (C::kJobKeys * 8));
+                const uint64_t qb = qdesc + uint32_t(qs * (C::kQBytes / 16));
+                const uint32_t d = s_cols + (n_qk & 1) * C::kJobKeys;
+#pragma unroll
+                for (int k = 0; k < D / 16; ++k)
+                    tc_mma_f16(d, qb + ((k / 4) * (C::kRows * 128) + (k % 4) * 32) / 16,
+                               kb + ((k / 4) * (C::kKeys * 128) + (k % 4) * 32) / 16, idesc_s, k > 0);
+                tc_commit(bar(C::kSFull + 2 * own + (n_qk & 1)));
+                if (half == C::kJobs - 1) tc_commit(bar(C::kEmpty + kslot));
+                ++n_qk;
+            };
+            int more = advance(kAny);
+            if (more == 1) issue_s(0);
+            while (more == 1) {
+                if (!land_v()) break;
+                const int vs = vslot;
+                const bool fresh = first;
+                first = false;
+                bool ok = true;
+#pragma unroll
+                for (int half = 0; half < C::kJobs; ++half) {
+                    // the next job's S, then this job's P V
+                    if (half + 1 < C::kJobs) {
+                        issue_s(half + 1);
+                    } else {
+                        more = advance(2);
+                        if (more < 0) {
+                            ok = false;
+                            break;
+                        }
+                        if (more == 1) issue_s(0);
+                    }
+                    const int buf = n_pv & 1;
+                    if (!wait1(C::kPFull + 2 * own + buf, uint32_t(n_pv >> 1) & 1u)) {
+                        ok = false;
+                        break;
+                    }
+                    tc_fence_after();
+                    const uint64_t vb = vdesc + uint32_t(vs * (C::kSlotBytes / 16) + half * (C::kJobKeys * 8));
+#pragma unroll
+                    for (int k = 0; k < C::kJobKeys / 16; ++k)
+                        tc_mma_f16_ta(o_cols, s_cols + buf * C::kJobKeys + 8 * k, vb + k * 128, idesc_o,
+                                      !fresh || half > 0 || k > 0);
+                    tc_commit(bar(C::kPvDone + 2 * own + buf));
+                    if (half == C::kJobs - 1) tc_commit(bar(C::kEmpty + vs));
+                    ++n_pv;
+                }
+                if (!ok) break;
+                if (more == 2 && (more = advance(kAny)) == 1) issue_s(0);
+            }
+            // every mma has completed before the tensor memory is released
+            tc_commit(bar(C::kAllDone + own));
+            mbar_wait_bounded(bar(C::kAllDone + own), 0u);
+        }
+    } else if (wid >= 14) {
+        // ================================================================ V inspectors
+        Ring<C::kSlots> ring;
+        constexpr uint32_t kExp = kBf16 ? 0x7f807f80u : 0x7c007c00u;
+        bool ok = true;
+        for (int i = 0; ok; ++i) {
+            if (!seg_wait(i)) break;
+            const TcSeg& s = seg_at(i);
+            const int blk1 = s.blk1;
+            if (s.blk0 == blk1) break;
+            for (int blk = s.blk0; blk < blk1; ++blk) {
+                if (!(ok = wait(C::kFull + ring.slot, ring.phase))) break;
+                if (lane == 0) mbar_arrive(bar(C::kEmpty + ring.slot));  // K
+                ring.next();
+                if (!(ok = wait(C::kFull + ring.slot, ring.phase))) break;
+                if (blk >= s.tail0) {
+                    uint8_t* vb = smem + C::kRingOff + ring.slot * C::kSlotBytes;
                     bool found = false;
-                    for (int row = t; row < C::kKeys; row += 32 * C::kInspectors) {
-                    const int tok = tree_token(a, blk, row);
-                    const bool dead = tok < 0 || tok >= s.len, node = tok >= s.len - s.n;
-                    if (dead || node) {
+                    for (int row = tid - 448; row < C::kKeys; row += 32 * C::kInspectors) {
+                        const int tok = tree_token(a, blk, row);
+                        const bool dead = tok < 0 || tok >= s.len, node = tok >= s.len - s.n;
+                        if (!dead && !node) continue;
                         for (int hf = 0; hf < C::kHalves; ++hf) {
 #pragma unroll
                             for (int c = 0; c < 8; ++c) {
@@ -577,72 +537,65 @@ __global__ void __launch_bounds__(512, 1)
                             }
                         }
                     }
-                    }
-                    if (found) bad_v[w.seg & 3] = w.seg + 1;
+                    if (found) bad_v[i & 3] = i + 1;
                     fence_proxy_async_smem();
                     __syncwarp();
-                    if (lane == 0) {
-                        mbar_arrive(bar(kVokB + slot));
-                        mbar_arrive(bar(kEmptyB + slot));
-                    }
-                    return true;
-                });
+                    if (lane == 0) mbar_arrive(bar(C::kVok + ring.slot));
+                }
+                if (lane == 0) mbar_arrive(bar(C::kEmpty + ring.slot));
+                ring.next();
+            }
+            seg_free(i);
         }
-    } else {
-        regs_inc<192>();
-        // ================================================================ softmax
+    } else if (wid < 4 * C::kTiles) {
+        // ================================================================ softmax of pipeline t
         const int t = wid >> 2, row = tid & 127;
-        if (C::kTiles == 2 || t == 0) {
-            const uint32_t lanes = uint32_t(32 * (wid & 3)) << 16;
-            const uint32_t to = tmem + lanes + (C::kTiles == 2 ? t * C::kOCols : 0);
-            const float scale = a.scale_log2 == 0.f ? 1e-38f : fabsf(a.scale_log2);
-            const int per_slot = a.slot_rows < 32 ? a.slot_rows : 32;
-            const bool packed = a.page_size % a.slot_rows == 0;
-            int n_s[2] = {0, 0}, n_one = 0, n_seg = 0;  // n_s[b]: jobs so far in S buffer b
-            int last = 0;                               // S buffer of the last job
-            bool dead = false;
-            int kblocks = 0;  // K blocks before this segment
-            while (!dead) {
-                const TcSeg* sp = seg_wait(n_seg);
-                TcStep w;
-                if (sp == nullptr || !w.enter(*sp)) break;
-                const TcSeg& s = *sp;
-                const TreeReq r = s.req();
-                const int seg = n_seg++;
-                const bool joint = C::kTiles == 2 && !w.wide;  // both pipelines hold parts of the same rows
-                const int node = s.node0 + (w.wide ? t * a.npt : 0) + row / a.hpt;
-                const long long at = tree_row(a, s.row0, s.nodes, s.hh, row + (w.wide ? t * C::kRows : 0));
-                const bool live = __any_sync(kFull, at >= 0);  // a warp without rows only keeps step
-                float m = kNegInf, l = 0.f;
-                // pipeline 1 leaves the last joint segment's O to pipeline 0 until it has been read
-                if (t == 1 && n_one > 0 && !tree_wait_warp(bar(kOneFree), uint32_t(n_one - 1) & 1u, abort_flag, a.flags)) break;
-                const int step = C::kTiles == 2 ? 2 : 1;
-                const int first = C::kTiles == 2 ? t : 0;
-                for (int j = first; j < w.jobs; j += step) {
-                    w.j = j;
-                    const int blk = w.block(), sb = j & 1;
-                    if (!tree_wait_warp(bar(kSFull + sb), uint32_t(n_s[sb]++) & 1u, abort_flag, a.flags)) {
-                        dead = true;
-                        break;
-                    }
+        const uint32_t lanes = uint32_t(32 * (wid & 3)) << 16;
+        const uint32_t to = tmem + lanes + t * D, ts0 = tmem + lanes + C::kSCol + t * 2 * C::kJobKeys;
+        const float scale = a.scale_log2 == 0.f ? 1e-38f : fabsf(a.scale_log2);
+        const int per_slot = a.slot_rows < 32 ? a.slot_rows : 32;
+        const bool packed = a.page_size % a.slot_rows == 0;
+        int jobs = 0, n_one = 0, kblocks = 0;  // kblocks: K blocks before this segment
+        bool ok = true;
+        for (int seg = 0; ok; ++seg) {
+            if (!seg_wait(seg)) break;
+            const TcSeg& s = seg_at(seg);
+            const int blk0 = s.blk0, blk1 = s.blk1, tail0 = s.tail0;
+            if (blk0 == blk1) break;
+            const TreeReq r = s.req();
+            const bool wide = s.wide != 0, joint = C::kTiles == 2 && !wide;  // joint: both pipelines hold parts of the same rows
+            const int node = s.node0 + (wide ? t * a.npt : 0) + row / a.hpt;
+            const long long at = tree_row(a, s.row0, s.nodes, s.hh, row + (wide ? t * C::kRows : 0));
+            const bool live = __any_sync(kFull, at >= 0);  // a warp without rows only keeps step
+            float m = kNegInf, l = 0.f;
+            // pipeline 1 leaves the last joint segment's O to pipeline 0 until it has been read
+            if (t == 1 && n_one > 0 && !wait(C::kOneFree, uint32_t(n_one - 1) & 1u)) break;
+            bool fresh = true;
+            for (int blk = blk0 + (joint ? t : 0); blk < blk1 && ok; blk += joint ? 2 : 1) {
+#pragma unroll 1
+                for (int half = 0; half < C::kJobs; ++half) {
+                    const int buf = jobs & 1;
+                    const uint32_t phase = uint32_t(jobs >> 1) & 1u;
+                    if (!(ok = wait(C::kSFull + 2 * t + buf, phase))) break;
                     if (live) {
                         tc_fence_after();
-                        const uint32_t ts = tmem + lanes + C::kSCol + sb * C::kKeys;
-                        uint32_t x[C::kKeys];
-#pragma unroll
-                        for (int c = 0; c < C::kKeys; c += 32) tmem_ld32(ts + c, x + c);
-                        const unsigned bad_pages = bad_slots[(kblocks + blk - s.blk0) % C::kBadRing];
+                        const uint32_t ts = ts0 + buf * C::kJobKeys;
+                        uint32_t x[C::kJobKeys];
+                        tmem_ld32(ts, x);
+                        tmem_ld32(ts + 32, x + 32);
+                        const unsigned bad_pages = bad_slots[(kblocks + blk - blk0) % C::kBadRing];
                         tmem_wait_ld();
-                        if (!packed || bad_pages != 0u || w.tail()) {
+                        if (!packed || bad_pages != 0u || blk >= tail0) {
                             const int nd = min(node, r.n - 1);
 #pragma unroll
-                            for (int c = 0; c < C::kKeys; c += 32) {
+                            for (int c = 0; c < C::kJobKeys; c += 32) {
+                                const int c0 = half * C::kJobKeys + c;
                                 uint32_t allow = 0;
                                 if (packed && bad_pages == 0u) {
-                                    allow = tree_allow(a, r, nd, (blk * a.spb) * a.slot_rows + c, 32);
+                                    allow = tree_allow(a, r, nd, (blk * a.spb) * a.slot_rows + c0, 32);
                                 } else {
                                     for (int e = 0; e < 32; e += per_slot) {
-                                        const int col = c + e, p = blk * a.spb + col / a.slot_rows;
+                                        const int col = c0 + e, p = blk * a.spb + col / a.slot_rows;
                                         const int r0 = p % a.cpp * a.slot_rows + col % a.slot_rows;
                                         const int count = min(per_slot, a.page_size - r0);
                                         if ((bad_pages >> (col / a.slot_rows)) & 1u) continue;
@@ -656,9 +609,8 @@ __global__ void __launch_bounds__(512, 1)
                         }
                         float top = __uint_as_float(x[0]);
 #pragma unroll
-                        for (int c = 1; c < C::kKeys; ++c) top = fmaxf(top, __uint_as_float(x[c]));
+                        for (int c = 1; c < C::kJobKeys; ++c) top = fmaxf(top, __uint_as_float(x[c]));
                         top *= scale;
-                        const bool fresh = C::kTiles == 2 ? j < 2 : j == 0;
                         if (fresh) {
                             m = top;
                         } else {
@@ -667,14 +619,10 @@ __global__ void __launch_bounds__(512, 1)
                                 const float f = rise ? ex2(m - top) : 1.f;
                                 if (rise) m = top;
                                 l *= f;
-                                // O holds every block before this one once the last P V is done. A
-                                // barrier per S buffer: S of this job was issued after the P V before
-                                // in its buffer, so no barrier is more than one phase behind.
-                                if (!tree_wait_warp(bar(kPvDone + last), uint32_t(n_s[last] - (last == sb ? 2 : 1)) & 1u, abort_flag,
-                                                  a.flags)) {
-                                    dead = true;
-                                    break;
-                                }
+                                // O holds every job before this one once the last P V is done. S of this
+                                // job was issued after the P V before in its buffer, so that no barrier is
+                                // more than one phase behind.
+                                if (!(ok = wait(C::kPvDone + 2 * t + (buf ^ 1), uint32_t((jobs - 1) >> 1) & 1u))) break;
                                 tc_fence_after();
 #pragma unroll 1
                                 for (int c = 0; c < D; c += 16) {
@@ -690,119 +638,115 @@ __global__ void __launch_bounds__(512, 1)
                         const float mu = m == kNegInf ? 0.f : m;
                         float2 sum = make_float2(0.f, 0.f);
                         const float2 sc2 = make_float2(scale, scale), mu2 = make_float2(-mu, -mu);
+                        uint32_t p[C::kJobKeys / 2];
 #pragma unroll
-                        for (int c = 0; c < C::kKeys; c += 64) {
-                            uint32_t p[32];
-#pragma unroll
-                            for (int e = 0; e < 32; ++e) {
-                                float2 y = make_float2(__uint_as_float(x[c + 2 * e]), __uint_as_float(x[c + 2 * e + 1]));
-                                y = __ffma2_rn(y, sc2, mu2);
-                                y = make_float2(ex2(y.x), ex2(y.y));
-                                sum = __fadd2_rn(sum, y);
-                                p[e] = Elt<T>::pack(y.x, y.y);
-                            }
-                            tmem_st32(ts + c / 2, p);
+                        for (int e = 0; e < C::kJobKeys / 2; ++e) {
+                            float2 y = make_float2(__uint_as_float(x[2 * e]), __uint_as_float(x[2 * e + 1]));
+                            y = __ffma2_rn(y, sc2, mu2);
+                            y = make_float2(ex2(y.x), ex2(y.y));
+                            sum = __fadd2_rn(sum, y);
+                            p[e] = Elt<T>::pack(y.x, y.y);
                         }
+                        tmem_st32(ts, p);
                         l += sum.x + sum.y;
                         tmem_wait_st();
                         tc_fence_before();
                     }
-                    last = sb;
+                    fresh = false;
+                    ++jobs;
                     __syncwarp();
-                    if (lane == 0) mbar_arrive(bar(kPFull + sb));
+                    if (lane == 0) mbar_arrive(bar(C::kPFull + 2 * t + buf));
                 }
-                if (dead) break;
-                kblocks += s.blk1 - s.blk0;
-                // ---- the segment's end
-                const int mine = C::kTiles == 2 ? (w.jobs + 1 - t) / 2 : w.jobs;  // jobs of this pipeline
-                if (mine > 0 && !tree_wait_warp(bar(kPvDone + last), uint32_t(n_s[last] - 1) & 1u, abort_flag, a.flags)) break;
+            }
+            if (!ok) break;
+            kblocks += blk1 - blk0;
+            // ---- the segment's end
+            if (!fresh && !wait(C::kPvDone + 2 * t + ((jobs - 1) & 1), uint32_t((jobs - 1) >> 1) & 1u)) break;
+            tc_fence_after();
+            float2 other = make_float2(kNegInf, 0.f);
+            const bool two = joint && blk1 - blk0 > 1;  // pipeline 1 had a block
+            if (joint) {
+                if (t == 1) {
+                    stat[row] = make_float2(m, l);
+                    tc_fence_before();
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(bar(C::kOneDone));
+                    ++n_one;
+                    seg_free(seg);
+                    continue;
+                }
+                if (!wait(C::kOneDone, uint32_t(n_one++) & 1u)) break;
                 tc_fence_after();
-                float2 other = make_float2(kNegInf, 0.f);
-                if (joint) {
-                    if (t == 1) {
-                        stat[row] = make_float2(m, l);
-                        tc_fence_before();
-                        __syncwarp();
-                        if (lane == 0) mbar_arrive(bar(kOneDone));
-                        ++n_one;
-                        seg_free(seg);
-                        continue;
-                    }
-                    if (!tree_wait_warp(bar(kOneDone), uint32_t(n_one++) & 1u, abort_flag, a.flags)) break;
-                    tc_fence_after();
-                    if (w.jobs > 1) other = stat[row];
-                }
-                const bool two = joint && w.jobs > 1;
-                const float mm = fmaxf(m, other.x), mu = mm == kNegInf ? 0.f : mm;
-                const float f0 = ex2(m - mu), f1 = ex2(other.x - mu);
-                const float L = l * f0 + other.y * f1;
-                const float inv = mm == kNegInf ? 0.f : 1.f / L;
-                const float lse2 = mm == kNegInf ? kNegInf : mm + log2f(L);
-                const float i0 = f0 * inv, i1 = f1 * inv;
-                const bool fix = bad_v[seg & 3] == seg + 1;
-                if (live) {
+                if (two) other = stat[row];
+            }
+            const float mm = fmaxf(m, other.x), mu = mm == kNegInf ? 0.f : mm;
+            const float f0 = ex2(m - mu), f1 = ex2(other.x - mu);
+            const float L = l * f0 + other.y * f1;
+            const float inv = mm == kNegInf ? 0.f : 1.f / L;
+            const float lse2 = mm == kNegInf ? kNegInf : mm + log2f(L);
+            const float i0 = f0 * inv, i1 = f1 * inv;
+            const bool fix = bad_v[seg & 3] == seg + 1;
+            if (live) {
 #pragma unroll 1
-                    for (int c = 0; c < D; c += 32) {
-                        uint32_t o[32];
-                        tmem_ld32(to + c, o);
-                        float f[32];
-                        if (two) {
-                            uint32_t o1[32];
-                            tmem_ld32(to + C::kOCols + c, o1);
-                            tmem_wait_ld();
+                for (int c = 0; c < D; c += 32) {
+                    uint32_t o[32];
+                    tmem_ld32(to + c, o);
+                    float f[32];
+                    if (two) {
+                        uint32_t o1[32];
+                        tmem_ld32(to + D + c, o1);
+                        tmem_wait_ld();
 #pragma unroll
-                            for (int e = 0; e < 32; ++e)
-                                f[e] = __uint_as_float(o[e]) * i0 + __uint_as_float(o1[e]) * i1;
-                        } else {
-                            tmem_wait_ld();
+                        for (int e = 0; e < 32; ++e) f[e] = __uint_as_float(o[e]) * i0 + __uint_as_float(o1[e]) * i1;
+                    } else {
+                        tmem_wait_ld();
 #pragma unroll
-                            for (int e = 0; e < 32; ++e) f[e] = __uint_as_float(o[e]) * i0;
-                        }
-                        if (fix && at >= 0) {
-                            // non-finite elements of the node rows in these blocks, for the rows that attend them
-                            for (int i = 0; i < r.n; ++i) {
-                                const int tok = r.ctx() + i;
-                                const int blk = tree_slots(a, tok + 1) - 1;
-                                if (blk / a.spb < s.blk0 || blk / a.spb >= s.blk1) continue;
-                                if ((tree_allow(a, r, node, tok, 1) & 1u) == 0u) continue;
-                                const int page = __ldg(a.indices + r.lo + tok / a.page_size);
-                                if (page < 0 || page >= a.num_total_pages) continue;
-                                const T* v = static_cast<const T*>(a.v) +
-                                             ((size_t(page) * a.num_kv_heads + s.kvh) * a.page_size + tok % a.page_size) * D + c;
+                        for (int e = 0; e < 32; ++e) f[e] = __uint_as_float(o[e]) * i0;
+                    }
+                    if (fix && at >= 0) {
+                        // non-finite elements of the node rows in these blocks, for the rows that attend them
+                        for (int i = 0; i < r.n; ++i) {
+                            const int tok = r.ctx() + i;
+                            const int blk = (tree_slots(a, tok + 1) - 1) / a.spb;
+                            if (blk < blk0 || blk >= blk1) continue;
+                            if ((tree_allow(a, r, node, tok, 1) & 1u) == 0u) continue;
+                            const int page = __ldg(a.indices + r.lo + tok / a.page_size);
+                            if (page < 0 || page >= a.num_total_pages) continue;
+                            const T* v = static_cast<const T*>(a.v) +
+                                         ((size_t(page) * a.num_kv_heads + s.kvh) * a.page_size + tok % a.page_size) * D + c;
 #pragma unroll
-                                for (int e = 0; e < 32; ++e) {
-                                    const float y = float(v[e]);
-                                    if (!isfinite(y)) f[e] += y;
-                                }
-                            }
-                        }
-                        if (at >= 0) {
-                            if (s.slot >= 0) {
-                                float4* po = reinterpret_cast<float4*>(
-                                    a.part_o + (size_t(s.slot) * a.seg_rows + row + (w.wide ? t * C::kRows : 0)) * D + c);
-#pragma unroll
-                                for (int e = 0; e < 8; ++e) po[e] = make_float4(f[4 * e], f[4 * e + 1], f[4 * e + 2], f[4 * e + 3]);
-                            } else {
-                                uint4* po = reinterpret_cast<uint4*>(static_cast<T*>(a.o) + at * D + c);
-#pragma unroll
-                                for (int e = 0; e < 4; ++e) po[e] = Elt<T>::from_f32(f + 8 * e);
+                            for (int e = 0; e < 32; ++e) {
+                                const float y = float(v[e]);
+                                if (!isfinite(y)) f[e] += y;
                             }
                         }
                     }
                     if (at >= 0) {
-                        if (s.slot >= 0)
-                            a.part_lse[size_t(s.slot) * a.seg_rows + row + (w.wide ? t * C::kRows : 0)] = lse2;
-                        else
-                            a.lse[at] = lse2 == kNegInf ? kNegInf : lse2 * kLn2;
+                        if (s.slot >= 0) {
+                            float4* po = reinterpret_cast<float4*>(
+                                a.part_o + (size_t(s.slot) * a.seg_rows + row + (wide ? t * C::kRows : 0)) * D + c);
+#pragma unroll
+                            for (int e = 0; e < 8; ++e) po[e] = make_float4(f[4 * e], f[4 * e + 1], f[4 * e + 2], f[4 * e + 3]);
+                        } else {
+                            uint4* po = reinterpret_cast<uint4*>(static_cast<T*>(a.o) + at * D + c);
+#pragma unroll
+                            for (int e = 0; e < 4; ++e) po[e] = Elt<T>::from_f32(f + 8 * e);
+                        }
                     }
                 }
-                if (joint) {
-                    tc_fence_before();
-                    __syncwarp();
-                    if (lane == 0) mbar_arrive(bar(kOneFree));
+                if (at >= 0) {
+                    if (s.slot >= 0)
+                        a.part_lse[size_t(s.slot) * a.seg_rows + row + (wide ? t * C::kRows : 0)] = lse2;
+                    else
+                        a.lse[at] = lse2 == kNegInf ? kNegInf : lse2 * kLn2;
                 }
-                seg_free(seg);
             }
+            if (joint) {
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(bar(C::kOneFree));
+            }
+            seg_free(seg);
         }
     }
     tc_fence_before();

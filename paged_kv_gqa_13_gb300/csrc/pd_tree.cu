@@ -20,6 +20,7 @@ TreeKernels cc_kernels() {
     k.per_sm = C::kBlocksPerSm;
     k.tile_rows = C::kRows;
     k.tiles = 1;
+    k.workers = 1;
     k.block_tokens = C::kBlockTokens;
     return k;
 }
@@ -36,9 +37,10 @@ bool cc_by_dim(int D, TreeKernels* k) {
 
 // 16-bit q of a group that fits a row tile runs on the tensor cores; f32 q,
 // which no tensor-core type holds, and larger groups on CUDA cores.
-bool pick(pd_dtype dt, bool fp8, int D, int group, TreeKernels* k) {
+// `wide`: two row tiles per segment (where a kernel for it exists).
+bool pick(pd_dtype dt, bool fp8, int D, int group, bool wide, TreeKernels* k) {
     if (dt != PD_F32 && group <= 128 && !fp8)
-        return dt == PD_F16 ? tree_tc_f16(D, k) : tree_tc_bf16(D, k);
+        return dt == PD_F16 ? tree_tc_f16(D, wide, k) : tree_tc_bf16(D, wide, k);
     switch (dt) {
         case PD_F32: return !fp8 && cc_by_dim<float, float>(D, k);
         case PD_F16: return fp8 ? cc_by_dim<__half, uint8_t>(D, k) : cc_by_dim<__half, __half>(D, k);
@@ -82,9 +84,9 @@ struct TreeSpace {
 };
 TreeSpace space(const TreeKernels& k, int ctas, int D) {
     TreeSpace s;
-    const size_t rows = size_t(2) * ctas * k.tile_rows * k.tiles;
+    const size_t rows = size_t(2) * ctas * k.workers * k.tile_rows * k.tiles;
     s.splits = PD_WORKSPACE_HEADER_BYTES;
-    s.lse = s.splits + round256(size_t(ctas) * sizeof(TreeSplit));
+    s.lse = s.splits + round256(size_t(ctas) * k.workers * sizeof(TreeSplit));
     s.o = s.lse + round256(rows * 4);
     s.bytes = s.o + rows * D * 4;
     return s;
@@ -123,7 +125,10 @@ pd_status tree_impl(const void* q, const void* k_data, const void* v_data, const
         return host::fail(PD_ERR_UNSUPPORTED, "lse, the table, tree_mask and the scales must be 4-byte aligned");
     const int group = Hq / Hk;
     TreeKernels kn{};
-    if (!pick(dt, fp8, D, group, &kn)) return host::fail(PD_ERR_UNSUPPORTED, "no kernel for this type and head_dim");
+    // More rows per request than a row tile holds: segments of two row tiles, which
+    // read K and V once for both. Fewer: two independent halves of each CTA.
+    const bool wide = (long long)total_new * group > 128ll * batch;
+    if (!pick(dt, fp8, D, group, wide, &kn)) return host::fail(PD_ERR_UNSUPPORTED, "no kernel for this type and head_dim");
     int sms = 0;
     if ((st = host::sm_count(&sms)) != PD_OK) return st;
     const int most = sms * kn.per_sm;
@@ -178,7 +183,8 @@ pd_status tree_impl(const void* q, const void* k_data, const void* v_data, const
     const long long segs = ((long long)total_new / a.nps + batch) * a.hs * Hk;
     const long long blocks = ((long long)num_indices * a.cpp + a.spb - 1) / a.spb;
     const long long bound = segs * (blocks < 1 ? 1 : blocks);
-    const int grid = int(bound < most ? bound : most);
+    const long long ctas = (bound + kn.workers - 1) / kn.workers;
+    const int grid = int(ctas < most ? ctas : most);
     cudaStream_t cs = static_cast<cudaStream_t>(stream);
     if ((st = host::allow_smem(kn.main, kn.smem)) != PD_OK) return st;
     CUtensorMap maps[3];
@@ -186,9 +192,10 @@ pd_status tree_impl(const void* q, const void* k_data, const void* v_data, const
     void* args[] = {&a, &maps[0], &maps[1], &maps[2]};
     cudaError_t e = cudaLaunchKernel(kn.main, dim3(grid), dim3(kn.threads), args, kn.smem, cs);
     if (e != cudaSuccess) return host::cuda_fail(e, "tree decode launch");
-    if (grid > 1 && blocks > 1) {  // otherwise no segment can be split
+    const int workers = grid * kn.workers;
+    if (workers > 1 && blocks > 1) {  // otherwise no segment can be split
         cudaLaunchConfig_t cfg{};
-        cfg.gridDim = dim3(grid - 1, (a.seg_rows + 7) / 8);
+        cfg.gridDim = dim3((workers - 1) * kMergeBlocks);
         cfg.blockDim = dim3(256);
         cfg.stream = cs;
         cudaLaunchAttribute attr[1];
@@ -214,9 +221,9 @@ size_t pd_paged_tree_decode_workspace_bytes(int num_qo_heads, int num_kv_heads, 
     int sms = 0;
     if (host::sm_count(&sms) != PD_OK) return 0;
     size_t most = 0;  // of the kernels that take this type, with either pool
-    for (int fp8 = 0; fp8 < 2; ++fp8) {
+    for (int form = 0; form < 4; ++form) {
         TreeKernels k{};
-        if (!pick(dtype, fp8 != 0, head_dim, num_qo_heads / num_kv_heads, &k)) continue;
+        if (!pick(dtype, (form & 1) != 0, head_dim, num_qo_heads / num_kv_heads, (form & 2) != 0, &k)) continue;
         const size_t n = space(k, sms * k.per_sm, head_dim).bytes;
         if (n > most) most = n;
     }

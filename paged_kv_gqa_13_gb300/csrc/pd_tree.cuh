@@ -11,12 +11,13 @@
 //
 // Partition. The blocks of all segments, in the order (request, head tile,
 // segment, block), are one line of U units, cut into equal ranges of W = ceil(U
-// / grid), one per CTA. A segment inside one range is written out by its CTA;
-// one that crosses ranges leaves a partial (o, lse) per CTA, and the merge
-// kernel combines them in CTA order. Only the device knows the lengths: every
-// CTA sums the requests' units itself (each thread a run of requests, one
-// block-wide scan) and finds its place; the first CTA past a boundary inside a
-// segment that starts in the range before writes the merge's descriptor.
+// / ranges), one per worker (a CTA, or one of the two halves of one). A segment
+// inside one range is written out by its worker; one that crosses ranges leaves
+// a partial (o, lse) per worker, and the merge kernel combines them in order.
+// Only the device knows the lengths: every CTA sums the requests' units itself
+// (each thread a run of requests, one block-wide scan) and finds its place; the
+// first worker past a boundary inside a segment that starts in the range before
+// writes the merge's descriptor.
 #pragma once
 
 #include "pd_merge.cuh"
@@ -30,7 +31,7 @@ struct TreeSplit {
     int row0;        // the request's first q row + the segment's first node
     int nodes;       // nodes of the segment
     int hh;          // head tile
-    int c0;          // CTA of the first part
+    int c0;          // worker of the first part
     int slot0;       // its partial slot; part p > 0 is in slot 2 (c0 + p)
     int pad[2];
 };
@@ -48,9 +49,9 @@ struct TreeArgs {
     float* lse;
     const float* k_scale;  // E4M3 pools
     const float* v_scale;
-    float* part_o;    // [2 * grid][seg_rows][D], normalised
-    float* part_lse;  // [2 * grid][seg_rows], log2 units
-    TreeSplit* splits;  // [grid]
+    float* part_o;    // [2 * workers][seg_rows][D], normalised
+    float* part_lse;  // [2 * workers][seg_rows], log2 units
+    TreeSplit* splits;  // [workers]
     int* flags;
     int batch, total_new, mask_words, num_qo_heads, num_kv_heads, group;
     int page_size, num_total_pages, num_indices;
@@ -125,10 +126,11 @@ __device__ __forceinline__ long long tree_cost(const TreeArgs& a, const TreeReq&
     return sum * a.hs * a.num_kv_heads;
 }
 
-// A CTA's place on the line of units, and the walk over its segments.
+// A worker's place on the line of units, and the walk over its segments.
 struct TreeWalk {
+    int worker;
     int b, hh, tau, blk;
-    long long unit, end;  // current unit and the end of this CTA's range
+    long long unit, end;  // current unit and the end of this worker's range
     long long W;
     TreeReq r;
 
@@ -169,23 +171,31 @@ struct TreeWalk {
         s->tail0 = (ctx / a.page_size * a.cpp + ctx % a.page_size / a.slot_rows) / a.spb;
         s->slots = tree_slots(a, r.len);
         const long long begin = unit - blk;
-        s->slot = (blk == 0 && s->blk1 == nblk) ? -1 : 2 * int(blockIdx.x) + (begin > end_of_previous() ? 1 : 0);
+        s->slot = (blk == 0 && s->blk1 == nblk) ? -1 : 2 * worker + (begin > worker * W ? 1 : 0);
         unit += s->blk1 - s->blk0;
         blk = 0;
         ++tau;
         return true;
     }
-    __device__ __forceinline__ long long end_of_previous() const { return (long long)blockIdx.x * W; }
 };
 
 struct TreePlanScratch {
     long long sums[32];
-    int b, hh, tau, blk;
-    long long total;
+    long long total, W;
+    struct {
+        int b, hh, tau, blk;
+    } at[2];  // where each worker of the CTA starts
 };
 
-// Find this CTA's range. All threads of the block call it; ends with a block barrier.
-__device__ __forceinline__ TreeWalk tree_plan(const TreeArgs& a, TreePlanScratch* sc) {
+// ceil(x / y); most lines are short enough for a 32-bit division.
+__device__ __forceinline__ long long tree_ceil_div(long long x, int y) {
+    return x < 0x7fffffffll - y ? (unsigned(x) + unsigned(y) - 1u) / unsigned(y) : (x + y - 1) / y;
+}
+
+// Find the ranges of this CTA's kWorkers workers. All threads of the block
+// call it; ends with a block barrier, after which tree_start gives the walks.
+template <int kWorkers>
+__device__ __forceinline__ void tree_plan(const TreeArgs& a, TreePlanScratch* sc) {
     const int tid = threadIdx.x, lane = tid & 31, wid = tid >> 5, nt = blockDim.x, nw = nt >> 5;
     const int per = (a.batch + nt - 1) / nt;
     const int b0 = min(tid * per, a.batch), b1 = min(b0 + per, a.batch);
@@ -202,7 +212,7 @@ __device__ __forceinline__ TreeWalk tree_plan(const TreeArgs& a, TreePlanScratch
         if (lane >= off) inc += x;
     }
     if (lane == 31) sc->sums[wid] = inc;
-    if (tid == 0) sc->b = -1;
+    if (tid < kWorkers) sc->at[tid].b = -1;
     __syncthreads();
     long long before = inc - mine, total = 0;
     for (int w = 0; w < nw; ++w) {
@@ -210,12 +220,16 @@ __device__ __forceinline__ TreeWalk tree_plan(const TreeArgs& a, TreePlanScratch
         if (w < wid) before += x;
         total += x;
     }
-    TreeWalk wk;
-    wk.W = (total + gridDim.x - 1) / gridDim.x;
-    wk.unit = (long long)blockIdx.x * wk.W;
-    wk.end = min(wk.unit + wk.W, total);
-    if (wk.unit < wk.end && before <= wk.unit && wk.unit < before + mine) {
-        long long left = wk.unit - before;
+    const long long W = tree_ceil_div(total, int(gridDim.x) * kWorkers);
+    if (tid == 0) {
+        sc->total = total;
+        sc->W = W;
+    }
+#pragma unroll
+    for (int k = 0; k < kWorkers; ++k) {
+        const long long unit = ((long long)blockIdx.x * kWorkers + k) * W;
+        if (unit >= total || unit < before || unit >= before + mine) continue;
+        long long left = unit - before;
         for (int b = b0; b < b1; ++b) {
             const TreeReq r = tree_request(a, b);
             const long long c = tree_cost(a, r);
@@ -224,7 +238,7 @@ __device__ __forceinline__ TreeWalk tree_plan(const TreeArgs& a, TreePlanScratch
                 continue;
             }
             const long long each = c / (a.hs * a.num_kv_heads);
-            sc->hh = int(left / each);
+            sc->at[k].hh = int(left / each);
             left %= each;
             int tau = 0;
             for (;; ++tau) {
@@ -232,38 +246,47 @@ __device__ __forceinline__ TreeWalk tree_plan(const TreeArgs& a, TreePlanScratch
                 if (left < nb) break;
                 left -= nb;
             }
-            sc->tau = tau;
-            sc->blk = int(left);
-            sc->b = b;
+            sc->at[k].tau = tau;
+            sc->at[k].blk = int(left);
+            sc->at[k].b = b;
             break;
         }
     }
     __syncthreads();
-    wk.b = sc->b;
-    wk.hh = sc->hh;
-    wk.tau = sc->tau;
-    wk.blk = sc->blk;
-    if (wk.b < 0) {
-        wk.end = wk.unit;
-    } else {
-        wk.r = tree_request(a, wk.b);
-    }
-    // the merge's descriptor of a segment that starts in the previous range and reaches into this one
-    if (tid == 0) {
+}
+
+// The walk of worker k of this CTA; `write`: this thread leaves the merge's
+// descriptor of a segment that starts in the range before and reaches into this one.
+template <int kWorkers>
+__device__ __forceinline__ TreeWalk tree_start(const TreeArgs& a, const TreePlanScratch* sc, int k, bool write) {
+    TreeWalk w;
+    w.worker = int(blockIdx.x) * kWorkers + k;
+    w.W = sc->W;
+    w.unit = w.worker * w.W;
+    w.end = min(w.unit + w.W, sc->total);
+    w.b = sc->at[k].b;
+    w.hh = sc->at[k].hh;
+    w.tau = sc->at[k].tau;
+    w.blk = sc->at[k].blk;
+    if (w.b < 0)
+        w.end = w.unit;
+    else
+        w.r = tree_request(a, w.b);
+    if (write) {
         TreeSplit s{};
-        const long long begin = wk.unit - wk.blk, prev = wk.unit - wk.W;
-        if (wk.b >= 0 && wk.blk > 0 && begin >= prev) {
-            const long long stop = begin + tree_blocks(a, wk.r, wk.tau);
-            s.c0 = int(blockIdx.x) - 1;
-            s.parts = int((stop - 1) / wk.W) - s.c0 + 1;
+        const long long begin = w.unit - w.blk, prev = w.unit - w.W;
+        if (w.b >= 0 && w.blk > 0 && begin >= prev) {
+            const long long stop = begin + tree_blocks(a, w.r, w.tau);
+            s.c0 = w.worker - 1;
+            s.parts = int((stop - 1) / w.W) - s.c0 + 1;
             s.slot0 = 2 * s.c0 + (begin > prev ? 1 : 0);
-            s.hh = wk.hh;
-            s.row0 = wk.r.start + wk.tau * a.nps;
-            s.nodes = min(a.nps, wk.r.n - wk.tau * a.nps);
+            s.hh = w.hh;
+            s.row0 = w.r.start + w.tau * a.nps;
+            s.nodes = min(a.nps, w.r.n - w.tau * a.nps);
         }
-        a.splits[blockIdx.x] = s;
+        a.splits[w.worker] = s;
     }
-    return wk;
+    return w;
 }
 
 // Which of 32 consecutive tokens t0 .. t0 + 31 (only the first `count` stand
@@ -291,23 +314,27 @@ __device__ __forceinline__ long long tree_row(const TreeArgs& a, int row0, int n
     return (long long)(row0 + node) * a.num_qo_heads + hh / a.hs * a.group + h;
 }
 
-// One warp per row of a split segment: parts in CTA order.
+constexpr int kMergeBlocks = 4;  // blocks per possible split
+
+// One warp per row of a split segment at a time: parts in worker order.
 template <typename T, int D>
 __global__ void __launch_bounds__(256) tree_merge_kernel(const TreeArgs a) {
     constexpr int kPer = D / 32;
     const float kNegInf = -__int_as_float(0x7f800000);
     grid_dependency_wait();
-    const TreeSplit s = a.splits[blockIdx.x + 1];
+    const TreeSplit s = a.splits[blockIdx.x / kMergeBlocks + 1];
     if (s.parts == 0) return;
-    const int row = int(blockIdx.y) * 8 + (threadIdx.x >> 5);
-    const long long at = row < a.seg_rows ? tree_row(a, s.row0, s.nodes, s.hh, row) : -1;
-    if (at < 0) return;
-    auto slot = [&](int p) { return size_t(p == 0 ? s.slot0 : 2 * (s.c0 + p)) * a.seg_rows + row; };
-    float acc[kPer] = {};
-    const float L = merge_rows<kPer, 8>(
-        s.parts, [&](int p) { return a.part_lse[slot(p)]; }, [&](int p) { return a.part_o + slot(p) * D; }, acc);
-    store_row<T, kPer>(static_cast<T*>(a.o) + at * D, acc);
-    if ((threadIdx.x & 31) == 0) a.lse[at] = L == kNegInf ? kNegInf : L * kLn2;
+    for (int i = int(blockIdx.x % kMergeBlocks) * 8 + (threadIdx.x >> 5); i < s.nodes * a.hpt; i += 8 * kMergeBlocks) {
+        const int per_tile = a.npt * a.hpt, row = i / per_tile * a.tile_rows + i % per_tile;
+        const long long at = tree_row(a, s.row0, s.nodes, s.hh, row);
+        if (at < 0) continue;  // past the group's last head
+        auto slot = [&](int p) { return size_t(p == 0 ? s.slot0 : 2 * (s.c0 + p)) * a.seg_rows + row; };
+        float acc[kPer] = {};
+        const float L = merge_rows<kPer, 8>(
+            s.parts, [&](int p) { return a.part_lse[slot(p)]; }, [&](int p) { return a.part_o + slot(p) * D; }, acc);
+        store_row<T, kPer>(static_cast<T*>(a.o) + at * D, acc);
+        if ((threadIdx.x & 31) == 0) a.lse[at] = L == kNegInf ? kNegInf : L * kLn2;
+    }
 }
 
 // ---------------------------------------------------------------- CUDA cores
@@ -358,7 +385,8 @@ __global__ void __launch_bounds__(128, CfgTreeCc<D>::kBlocksPerSm) tree_cc_kerne
     float* sv = sk + C::kKeys * C::kLd;
     float* sp = sv + C::kKeys * D;
     const int tid = threadIdx.x, tr = tid >> 3, tc = tid & 7;
-    TreeWalk walk = tree_plan(a, &plan);
+    tree_plan<1>(a, &plan);
+    TreeWalk walk = tree_start<1>(a, &plan, 0, tid == 0);
     launch_dependents();
     TreeWalk::Seg s;
     while (walk.next(a, &s)) {

@@ -8,11 +8,12 @@ struct TreeKernels {
     const void* merge;
     int threads, smem, per_sm;  // of main
     int tile_rows, tiles;       // rows of a row tile, row tiles per segment
+    int workers;                // independent ranges of work per CTA
     int block_tokens;           // tokens of a key block
     bool tensor;                // main takes tensor maps of q, K and V
 };
 
-bool tree_tc_f16(int head_dim, TreeKernels* k);
-bool tree_tc_bf16(int head_dim, TreeKernels* k);
+bool tree_tc_f16(int head_dim, bool wide, TreeKernels* k);
+bool tree_tc_bf16(int head_dim, bool wide, TreeKernels* k);
 
 }  // namespace pd

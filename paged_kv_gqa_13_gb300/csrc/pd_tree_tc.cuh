@@ -7,27 +7,27 @@
 // weights P in place (tensor memory), then O += P V (A = P from tensor memory,
 // B = V from shared memory, MN-major as it lies).
 //
-// Two pipelines t = 0, 1, each with its own O, two S buffers, an mma warp and 4
-// softmax warps. A pipeline's next S is computed while its softmax works on
-// the one before, and the other pipeline's products fill the rest. A segment
-// of more than one row tile (up to two) gives each pipeline its own rows, both
-// over every block ("wide"); one of a single row tile gives both the same rows
-// over alternate blocks, and joins the two (m, l, O) at the end. At head_dim
-// 256 tensor memory holds one O: one pipeline.
+// A pipeline has a row tile's O, two S buffers, an mma warp and 4 softmax
+// warps: its next S is computed while its softmax works on the one before.
+// Two pipelines share the tensor cores. Where requests have more rows than a
+// row tile (kWide) they hold the two row tiles of a segment over the same K and
+// V; elsewhere they are lines of their own, each with a range of the work, a
+// ring and producers of its own (head_dim 256: one line, for tensor memory
+// holds one O).
 //
-// K and V come in blocks of kKeys keys through one ring of slots, K and V of
-// block n as loads 2 n and 2 n + 1 of the CTA. Every role that waits for
+// K and V come in blocks of kKeys keys through a ring of slots, K and V of
+// block n as loads 2 n and 2 n + 1 of the line. Every role that waits for
 // loads steps over all of them in order, so that no barrier gets two phases
 // ahead of a role (a wait tells phases apart by parity only).
 //
-// Roles (16 warps): 0-3 and 4-7 softmax of pipeline 0 and 1; 8, 12 and 13
-// producers (TMA; load i by producer i % 3: a box of 16 rows x 128 bytes costs
+// Roles beside the softmax warps, per line: an mma warp per pipeline; producers
+// (TMA; load i by producer i % kProducers: a box of 16 rows x 128 bytes costs
 // its issuing warp about 75 cycles, and one warp alone kept the ring from
-// filling); 9 and 11 mma of pipeline 0 and 1; 10 walks the segments; 14 and 15
-// make V safe where weights can be zero: a zero weight does not undo a NaN or
-// an infinity, so in blocks that hold tokens some row does not attend, rows
-// past the end are zeroed and non-finite elements of node rows are replaced by
-// zero, to be added to the rows that attend them at the end.
+// filling); inspectors, which make V safe where weights can be zero: a zero
+// weight does not undo a NaN or an infinity, so in blocks that hold tokens some
+// row does not attend, rows past the end are zeroed and non-finite elements of
+// node rows are replaced by zero, to be added to the rows that attend them at
+// the end. The first inspector also walks the segments.
 //
 // The running maximum of a row moves only when it rises by more than 2^8 (the
 // weights then stay below 2^8, and O, in tensor memory, is rescaled rarely).
@@ -140,46 +140,58 @@ __device__ __forceinline__ bool tree_wait_warp(uint32_t bar, uint32_t parity, vo
 
 // ---------------------------------------------------------------- configuration
 
-template <int D>
+// Lines are independent: each walks a range of work of its own through a ring
+// of its own. kWide: one line, two pipelines over the same blocks. Otherwise
+// two lines of one pipeline (head_dim 256: one, for tensor memory holds one O).
+template <int D, bool kWide>
 struct CfgTree {
     static constexpr int kRows = 128;
-    static constexpr int kTiles = D == 256 ? 1 : 2;    // pipelines, O accumulators
-    static constexpr int kKeys = D == 256 ? 64 : 128;  // keys per K or V block
+    static constexpr int kLines = kWide || D == 256 ? 1 : 2;
+    static constexpr int kPipes = kWide ? 2 : 1;       // pipelines (row tiles) per line
+    static constexpr int kKeys = kWide ? 128 : 64;     // keys per K or V block
     static constexpr int kJobKeys = 64;
     static constexpr int kJobs = kKeys / kJobKeys;     // jobs per block
     static constexpr int kHalves = D / 64;             // 128-byte column blocks of a row
     static constexpr int kSlotBytes = kKeys * D * 2;   // one K or V block
     static constexpr int kQBytes = kRows * D * 2;      // one row tile of q
-    static constexpr int kQSlots = kTiles;
     static constexpr int kSlots = D == 64 ? 10 : 5;
-    static constexpr int kProducers = 3, kInspectors = 2;
-    static constexpr int kWalkers = kProducers + kTiles + kInspectors + 4 * kTiles;  // warps that read the segments
+    // warps of a line after the softmax warps of all lines: mma, producers, inspectors
+    static constexpr int kProducers = kLines == 2 ? 2 : 4;
+    static constexpr int kInspectors = kLines == 2 ? 1 : 2;
+    static constexpr int kOthers = kPipes + kProducers + kInspectors;
+    static constexpr int kSoftWarps = 4 * kLines * kPipes;
+    static constexpr int kThreads = round_up(32 * (kSoftWarps + kLines * kOthers), 128);
+    static constexpr int kWalkers = kOthers + 4 * kPipes;  // warps that read a line's segments
     static constexpr int kSegRing = 8;
     static constexpr int kBadRing = 16;  // more than the K blocks that the producers are ahead of the softmax warps
-    // barriers (8 bytes each)
+    // a line's barriers (8 bytes each); those of S buffer b of pipeline p at 2 p + b
     static constexpr int kFull = 0, kEmpty = kFull + kSlots, kVok = kEmpty + kSlots, kQFull = kVok + kSlots,
-                         kQEmpty = kQFull + 2, kSFull = kQEmpty + 2, kPFull = kSFull + 4, kPvDone = kPFull + 4,
-                         kOneDone = kPvDone + 4, kOneFree = kOneDone + 1, kAllDone = kOneFree + 1, kSegFull = kAllDone + 2,
+                         kQEmpty = kQFull + kPipes, kSFull = kQEmpty + kPipes, kPFull = kSFull + 2 * kPipes,
+                         kPvDone = kPFull + 2 * kPipes, kAllDone = kPvDone + 2 * kPipes, kSegFull = kAllDone + kPipes,
                          kSegFree = kSegFull + kSegRing, kBars = kSegFree + kSegRing;
-    static constexpr int kRingOff = kQSlots * kQBytes;
-    static constexpr int kBarOff = kRingOff + kSlots * kSlotBytes;
-    static constexpr int kStatOff = kBarOff + round_up(kBars * 8, 16);  // pipeline 1's (m, l) per row
-    static constexpr int kMiscOff = kStatOff + kRows * 8;  // tensor-memory address, abort flag, bad-V tags[4], bad slots
-    static constexpr int kSegOff = kMiscOff + 32 + 4 * kBadRing;
-    static constexpr int kBytes = kSegOff + kSegRing * 64 + 1024;  // 1024: alignment of the base
-    static constexpr int kSCol = kTiles * D;               // S buffer b of pipeline t at kSCol + (2 t + b) * kJobKeys
-    static constexpr int kThreads = 512;
-    static_assert(kSCol + 2 * kTiles * kJobKeys <= 512, "tensor memory");
+    // a line's shared memory: q, ring | barriers, bad-V tags[4], bad slots, segments (of all lines, after the data)
+    static constexpr int kRingOff = kPipes * kQBytes;
+    static constexpr int kLineBytes = kRingOff + kSlots * kSlotBytes;
+    static constexpr int kTagOff = round_up(kBars * 8, 16);
+    static constexpr int kSegOff = kTagOff + 16 + 4 * kBadRing;
+    static constexpr int kCtlBytes = kSegOff + kSegRing * 64;
+    static constexpr int kCtlOff = kLines * kLineBytes;
+    static constexpr int kMiscOff = kCtlOff + kLines * kCtlBytes;  // tensor-memory address, abort flag
+    static constexpr int kBytes = kMiscOff + 16 + 1024;            // 1024: alignment of the base
+    // tensor memory: O of every pipeline, then its two S buffers
+    static constexpr int kSCol = kLines * kPipes * D;
+    static_assert(kSCol + kLines * kPipes * 2 * kJobKeys <= 512, "tensor memory");
     static_assert(kBytes <= 232448, "shared memory");
+    static_assert(kLineBytes % 1024 == 0 && kSlotBytes % 1024 == 0, "operand tiles stay 1024-byte aligned");
 };
 
-// Segments come to the roles through a ring in shared memory, filled by one
-// warp that walks them. blk1 = blk0 ends the line.
+// Segments come to a line's roles through a ring in shared memory, filled by
+// the warp that walks them. blk1 = blk0 ends the line.
 struct alignas(16) TcSeg {
     int blk0, blk1, tail0, slots;     // blocks; first block with node tokens; slots of the request
     int slot, row0, node0, nodes;     // partial slot or -1; q rows and nodes of the segment
     int hh, head0, kvh, lo;           // head tile, its first q head and kv head; first entry of indices
-    int len, n, start, wide;          // the request: tokens, nodes, first q row; two row tiles
+    int len, n, start, pad;           // the request: tokens, nodes, first q row
     __device__ __forceinline__ TreeReq req() const {
         TreeReq r;
         r.n = n;
@@ -212,99 +224,213 @@ __device__ __forceinline__ int tree_token(const TreeArgs& a, int blk, int col) {
 
 // ---------------------------------------------------------------- the kernel
 
-template <typename T, int D>
-__global__ void __launch_bounds__(512, 1)
+template <typename T, int D, bool kWide>
+__global__ void __launch_bounds__(CfgTree<D, kWide>::kThreads, 1)
     tree_tc_kernel(const TreeArgs a, const __grid_constant__ CUtensorMap tmq, const __grid_constant__ CUtensorMap tmk,
                    const __grid_constant__ CUtensorMap tmv) {
-    using C = CfgTree<D>;
+    using C = CfgTree<D, kWide>;
     constexpr bool kBf16 = std::is_same<T, __nv_bfloat16>::value;
     const float kNegInf = -__int_as_float(0x7f800000);
     extern __shared__ __align__(16) uint8_t tree_tc_smem[];
-    uint8_t* smem = tree_tc_smem + ((1024u - (smem_u32(tree_tc_smem) & 1023u)) & 1023u);
-    const uint32_t sbase = smem_u32(smem);
+    uint8_t* base = tree_tc_smem + ((1024u - (smem_u32(tree_tc_smem) & 1023u)) & 1023u);
     const int tid = threadIdx.x, lane = tid & 31, wid = tid >> 5;
-    auto bar = [&](int i) { return sbase + C::kBarOff + 8u * uint32_t(i); };
-    float2* stat = reinterpret_cast<float2*>(smem + C::kStatOff);
-    uint32_t* tslot = reinterpret_cast<uint32_t*>(smem + C::kMiscOff);
-    volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + C::kMiscOff + 4);
-    volatile int* bad_v = reinterpret_cast<volatile int*>(smem + C::kMiscOff + 16);
-    // slots of each K block whose page id is bad, by the K block's number in this CTA
-    volatile uint32_t* bad_slots = reinterpret_cast<volatile uint32_t*>(smem + C::kMiscOff + 32);
-    TcSeg* segs = reinterpret_cast<TcSeg*>(smem + C::kSegOff);
+    // role: softmax warps first; then each line's mma, producers and inspectors
+    const bool soft = wid < C::kSoftWarps;
+    const int rest = wid - C::kSoftWarps;
+    const int line = soft ? wid / (4 * C::kPipes) : rest / C::kOthers, part = soft ? 0 : rest % C::kOthers;
+    const bool idle = line >= C::kLines;
+    uint8_t* smem = base + (idle ? 0 : line) * C::kLineBytes;
+    uint8_t* ctl = base + C::kCtlOff + (idle ? 0 : line) * C::kCtlBytes;
+    const uint32_t sbase = smem_u32(smem), bars = smem_u32(ctl);
+    auto bar = [&](int i) { return bars + 8u * uint32_t(i); };
+    volatile int* bad_v = reinterpret_cast<volatile int*>(ctl + C::kTagOff);
+    // slots of each K block whose page id is bad, by the K block's number in this line
+    volatile uint32_t* bad_slots = reinterpret_cast<volatile uint32_t*>(ctl + C::kTagOff + 16);
+    TcSeg* segs = reinterpret_cast<TcSeg*>(ctl + C::kSegOff);
+    uint32_t* tslot = reinterpret_cast<uint32_t*>(base + C::kMiscOff);
+    volatile int* abort_flag = reinterpret_cast<volatile int*>(base + C::kMiscOff + 4);
+    TreePlanScratch* plan = reinterpret_cast<TreePlanScratch*>(base);  // before the first copy lands there
 
-    if (tid == 0) {
-        for (int i = 0; i < C::kSlots; ++i) {
-            mbar_init(bar(C::kFull + i), 1);
-            mbar_init(bar(C::kEmpty + i), C::kTiles + C::kInspectors);  // the mma warps and the inspectors
-            mbar_init(bar(C::kVok + i), C::kInspectors);
+    if (!soft && !idle && part == 0) {
+        if (lane == 0) {
+            for (int i = 0; i < C::kSlots; ++i) {
+                mbar_init(bar(C::kFull + i), 1);
+                mbar_init(bar(C::kEmpty + i), C::kPipes + C::kInspectors);  // the mma warps and the inspectors
+                mbar_init(bar(C::kVok + i), C::kInspectors);
+            }
+            for (int i = 0; i < C::kPipes; ++i) {
+                mbar_init(bar(C::kQFull + i), 1);
+                mbar_init(bar(C::kQEmpty + i), 1);
+                mbar_init(bar(C::kAllDone + i), 1);
+            }
+            for (int i = 0; i < 2 * C::kPipes; ++i) {
+                mbar_init(bar(C::kSFull + i), 1);
+                mbar_init(bar(C::kPFull + i), 4);
+                mbar_init(bar(C::kPvDone + i), 1);
+            }
+            for (int i = 0; i < C::kSegRing; ++i) {
+                mbar_init(bar(C::kSegFull + i), 1);
+                mbar_init(bar(C::kSegFree + i), C::kWalkers);
+            }
+            fence_mbar_init();
+            *abort_flag = 0;
+            for (int i = 0; i < 4; ++i) bad_v[i] = 0;
         }
-        for (int i = 0; i < 2; ++i) {
-            mbar_init(bar(C::kQFull + i), 1);
-            mbar_init(bar(C::kQEmpty + i), C::kTiles);
-            mbar_init(bar(C::kAllDone + i), 1);
-        }
-        for (int i = 0; i < 4; ++i) {
-            mbar_init(bar(C::kSFull + i), 1);
-            mbar_init(bar(C::kPFull + i), 4);
-            mbar_init(bar(C::kPvDone + i), 1);
-        }
-        for (int i = 0; i < C::kSegRing; ++i) {
-            mbar_init(bar(C::kSegFull + i), 1);
-            mbar_init(bar(C::kSegFree + i), C::kWalkers);
-        }
-        mbar_init(bar(C::kOneDone), 4);
-        mbar_init(bar(C::kOneFree), 4);
-        fence_mbar_init();
-        *abort_flag = 0;
-        for (int i = 0; i < 4; ++i) bad_v[i] = 0;
+        __syncwarp();
+        if (line == 0) tmem_alloc(smem_u32(tslot), 512);
     }
-    if (wid == 9) tmem_alloc(smem_u32(tslot), 512);
-    if (wid == 8 && lane == 0) {
+    if (wid == C::kSoftWarps + C::kPipes && lane == 0) {
         prefetch_tensormap(&tmq);
         prefetch_tensormap(&tmk);
         prefetch_tensormap(&tmv);
     }
-    TreeWalk walk = tree_plan(a, reinterpret_cast<TreePlanScratch*>(smem + C::kRingOff));
+    tree_plan<C::kLines>(a, plan);
+    TreeWalk walk;
+    const bool walker = !soft && !idle && part == C::kPipes + C::kProducers;
+    if (walker) walk = tree_start<C::kLines>(a, plan, line, lane == 0);
     tc_fence_before();
-    __syncthreads();
+    __syncthreads();  // the walks have been read: copies may land
     tc_fence_after();
     launch_dependents();
     const uint32_t tmem = *tslot;
 
     auto wait1 = [&](int b, uint32_t phase) { return tree_wait(bar(b), phase, abort_flag, a.flags); };
     auto wait = [&](int b, uint32_t phase) { return tree_wait_warp(bar(b), phase, abort_flag, a.flags); };
-    // Segment i (a segment without blocks ends the line), waiting for it, and giving it back.
+    // Segment i, waiting for it, and giving it back.
     auto seg_at = [&](int i) -> const TcSeg& { return segs[i % C::kSegRing]; };
-    auto seg_wait = [&](int i) { return wait(C::kSegFull + i % C::kSegRing, uint32_t(i / C::kSegRing) & 1u); };
+    auto seg_phase = [&](int i) { return uint32_t(i / C::kSegRing) & 1u; };
+    auto seg_wait = [&](int i) { return wait(C::kSegFull + i % C::kSegRing, seg_phase(i)); };
     auto seg_free = [&](int i) {
         __syncwarp();
         if (lane == 0) mbar_arrive(bar(C::kSegFree + i % C::kSegRing));
     };
 
-    if (wid == 10) {
-        // ================================================================ segments
-        TreeWalk::Seg s;
-        for (int i = 0;; ++i) {
-            const bool more = walk.next(a, &s);
-            if (i >= C::kSegRing && !wait(C::kSegFree + i % C::kSegRing, uint32_t(i / C::kSegRing - 1) & 1u)) break;
-            if (lane == 0) {
-                TcSeg x{};
-                if (more)
-                    x = TcSeg{s.blk0, s.blk1,  s.tail0, s.slots, s.slot,  s.row0, s.node0,   s.nodes,
-                              s.hh,   s.head0, s.kvh,   s.r.lo,  s.r.len, s.r.n,  s.r.start, C::kTiles == 2 && s.nodes > a.npt};
-                segs[i % C::kSegRing] = x;
-                mbar_arrive(bar(C::kSegFull + i % C::kSegRing));
+    if (idle) {
+    } else if (!soft && part < C::kPipes) {
+        // ================================================================ mma of pipeline `part`
+        if (lane == 0) {
+            const uint32_t idesc_s = tc_idesc_f16(kBf16, C::kRows, C::kJobKeys, false) | (a.scale_log2 < 0.f ? kIdescNegA : 0u);
+            constexpr uint32_t idesc_o = tc_idesc_f16(kBf16, C::kRows, D, true);
+            // operand descriptors of slot 0 (K K-major, V MN-major) and of the row tile's q; addresses count 16 bytes
+            const uint64_t kdesc = smem_desc_sw128(sbase + C::kRingOff, 16, 1024);
+            const uint64_t vdesc = smem_desc_sw128(sbase + C::kRingOff, C::kKeys * 128, 1024);
+            const uint64_t qb = smem_desc_sw128(sbase + part * C::kQBytes, 16, 1024);
+            const int pipe = line * C::kPipes + part;
+            const uint32_t s_cols = tmem + C::kSCol + pipe * 2 * C::kJobKeys, o_cols = tmem + pipe * D;
+            Ring<C::kSlots> ring;
+            uint32_t vok = 0;        // phase of each slot's vok barrier
+            int n_qk = 0, n_pv = 0;  // jobs issued; job x is in S buffer x & 1
+            // The place of the S products: segment and block.
+            int seg = -1, blk = 0, blk1 = 0, tail0 = 0, kslot = 0;
+            bool first = false;
+            auto land = [&](int* slot) {
+                *slot = ring.slot;
+                const bool ok = wait1(C::kFull + ring.slot, ring.phase);
+                ring.next();
+                return ok;
+            };
+            // To the next block, waiting until its K has landed (1). 0: none left, -1: stop.
+            auto advance = [&]() -> int {
+                if (++blk >= blk1) {
+                    ++seg;
+                    if (!wait1(C::kSegFull + seg % C::kSegRing, seg_phase(seg))) return -1;
+                    const TcSeg& s = seg_at(seg);
+                    if (s.blk0 == s.blk1) return 0;
+                    blk = s.blk0;
+                    blk1 = s.blk1;
+                    tail0 = s.tail0;
+                    if (!wait1(C::kQFull + part, uint32_t(seg) & 1u)) return -1;
+                    first = true;
+                }
+                return land(&kslot) ? 1 : -1;
+            };
+            // Whether advance() would not wait.
+            auto ready = [&]() {
+                if (blk + 1 >= blk1) {
+                    const int i = seg + 1;
+                    if (!mbar_test_wait(bar(C::kSegFull + i % C::kSegRing), seg_phase(i))) return false;
+                    if (seg_at(i).blk0 == seg_at(i).blk1) return true;
+                    if (!mbar_test_wait(bar(C::kQFull + part), uint32_t(i) & 1u)) return false;
+                }
+                return mbar_test_wait(bar(C::kFull + ring.slot), ring.phase);
+            };
+            auto issue_s = [&](int half) {
+                tc_fence_after();
+                const uint64_t kb = kdesc + uint32_t(kslot * (C::kSlotBytes / 16) + half * (C::kJobKeys * 8));
+                const uint32_t d = s_cols + (n_qk & 1) * C::kJobKeys;
+#pragma unroll
+                for (int k = 0; k < D / 16; ++k)
+                    tc_mma_f16(d, qb + ((k / 4) * (C::kRows * 128) + (k % 4) * 32) / 16,
+                               kb + ((k / 4) * (C::kKeys * 128) + (k % 4) * 32) / 16, idesc_s, k > 0);
+                tc_commit(bar(C::kSFull + 2 * part + (n_qk & 1)));
+                if (half == C::kJobs - 1) {
+                    tc_commit(bar(C::kEmpty + kslot));
+                    if (blk + 1 == blk1) {  // the segment's last S
+                        tc_commit(bar(C::kQEmpty + part));
+                        mbar_arrive(bar(C::kSegFree + seg % C::kSegRing));
+                    }
+                }
+                ++n_qk;
+            };
+            int more = advance();
+            if (more == 1) issue_s(0);
+            while (more == 1) {
+                int vs;
+                const bool tail = blk >= tail0, fresh = first;
+                first = false;
+                if (!land(&vs)) break;
+                if (tail) {
+                    if (!wait1(C::kVok + vs, (vok >> vs) & 1u)) break;
+                    vok ^= 1u << vs;
+                }
+                bool ok = true;
+#pragma unroll
+                for (int half = 0; half < C::kJobs; ++half) {
+                    const int buf = n_pv & 1;
+                    const int pfull = C::kPFull + 2 * part + buf;
+                    const uint32_t phase = uint32_t(n_pv >> 1) & 1u;
+                    bool moved = true;
+                    // The next job's S before this job's P V, unless its K comes later than this job's weights.
+                    if (half + 1 < C::kJobs) {
+                        issue_s(half + 1);
+                    } else {
+                        const long long t0 = clock64();
+                        while (!(moved = ready()) && !mbar_test_wait(bar(pfull), phase) && !*abort_flag &&
+                               clock64() - t0 < kWaitCycles) {
+                        }
+                        if (moved && (more = advance()) == 1) issue_s(0);
+                        if (more < 0) {
+                            ok = false;
+                            break;
+                        }
+                    }
+                    if (!wait1(pfull, phase)) {
+                        ok = false;
+                        break;
+                    }
+                    tc_fence_after();
+                    const uint64_t vb = vdesc + uint32_t(vs * (C::kSlotBytes / 16) + half * (C::kJobKeys * 8));
+#pragma unroll
+                    for (int k = 0; k < C::kJobKeys / 16; ++k)
+                        tc_mma_f16_ta(o_cols, s_cols + buf * C::kJobKeys + 8 * k, vb + k * 128, idesc_o,
+                                      !fresh || half > 0 || k > 0);
+                    tc_commit(bar(C::kPvDone + 2 * part + buf));
+                    if (half == C::kJobs - 1) tc_commit(bar(C::kEmpty + vs));
+                    ++n_pv;
+                    if (!moved && (more = advance()) == 1) issue_s(0);
+                }
+                if (!ok) break;
             }
-            __syncwarp();
-            if (!more) break;
+            // every mma has completed before the tensor memory is released
+            tc_commit(bar(C::kAllDone + part));
+            mbar_wait_bounded(bar(C::kAllDone + part), 0u);
         }
-    } else if (wid == 8 || wid == 12 || wid == 13) {
+    } else if (!soft && part < C::kPipes + C::kProducers) {
         // ================================================================ producers
         const uint64_t once = l2_evict_first_policy(), again = l2_evict_normal_policy();
-        const int me = wid == 8 ? 0 : wid - 11;
+        const int me = part - C::kPipes;
         Ring<C::kSlots> ring;
-        Ring<C::kQSlots> qring;
-        int loads = 0, qloads = 0, kblocks = 0, turn = 0;  // turn: the producer whose load is next
+        int loads = 0, segments = 0, kblocks = 0, turn = 0;  // turn: the producer whose load is next
         bool ok = true;
         // one box per lane: slot_rows rows x 64 columns
         const int sl = lane / C::kHalves, hf = lane % C::kHalves;
@@ -342,169 +468,65 @@ __global__ void __launch_bounds__(512, 1)
             if (++turn == C::kProducers) turn = 0;
             return true;
         };
-        for (int i = 0; ok; ++i) {
-            if (!seg_wait(i)) break;
-            const TcSeg& s = seg_at(i);
+        for (; ok; ++segments) {
+            if (!seg_wait(segments)) break;
+            const TcSeg& s = seg_at(segments);
             const int blk0 = s.blk0, blk1 = s.blk1;
             if (blk0 == blk1) break;
-            for (int rt = 0; me == 0 && rt <= s.wide && ok; ++rt) {
-                ok = qloads < C::kQSlots || wait(C::kQEmpty + qring.slot, qring.phase ^ 1u);
+            for (int p = 0; me == 0 && p < C::kPipes && ok; ++p) {
+                // a row tile past the segment's nodes is loaded like another (rows of other requests, or zeros) and not used
+                ok = segments == 0 || wait(C::kQEmpty + p, uint32_t(segments - 1) & 1u);
                 if (!ok) break;
                 if (lane == 0) {
-                    mbar_arrive_expect_tx(bar(C::kQFull + qring.slot), uint32_t(a.npt * a.hpt) * D * 2);
+                    mbar_arrive_expect_tx(bar(C::kQFull + p), uint32_t(a.npt * a.hpt) * D * 2);
                     for (int h = 0; h < C::kHalves; ++h)
-                        tma_load_3d(sbase + qring.slot * C::kQBytes + h * (C::kRows * 128), &tmq, h * 64, s.head0,
-                                    s.row0 + rt * a.npt, bar(C::kQFull + qring.slot));
+                        tma_load_3d(sbase + p * C::kQBytes + h * (C::kRows * 128), &tmq, h * 64, s.head0, s.row0 + p * a.npt,
+                                    bar(C::kQFull + p));
                 }
                 __syncwarp();
-                ++qloads;
-                qring.next();
             }
             for (int blk = blk0; blk < blk1 && ok; ++blk, ++kblocks)
                 ok = load_block(s, blk, &tmk, true) && load_block(s, blk, &tmv, false);
-            seg_free(i);
+            seg_free(segments);
         }
         // copies issued last may still be landing when another role has stopped early
         for (int i = max(0, loads - C::kSlots); i < loads; ++i)
             mbar_wait_bounded(bar(C::kFull + i % C::kSlots), uint32_t(i / C::kSlots) & 1u);
-        for (int i = max(0, qloads - C::kQSlots); i < qloads; ++i)
-            mbar_wait_bounded(bar(C::kQFull + i % C::kQSlots), uint32_t(i / C::kQSlots) & 1u);
-    } else if (wid == 9 || (C::kTiles == 2 && wid == 11)) {
-        // ================================================================ mma of pipeline `own`
-        const int own = wid == 9 ? 0 : 1;
-        if (lane == 0) {
-            const uint32_t idesc_s = tc_idesc_f16(kBf16, C::kRows, C::kJobKeys, false) | (a.scale_log2 < 0.f ? kIdescNegA : 0u);
-            constexpr uint32_t idesc_o = tc_idesc_f16(kBf16, C::kRows, D, true);
-            // operand descriptors of slot 0 (K K-major, V MN-major) and of q slot 0; addresses count 16 bytes
-            const uint64_t kdesc = smem_desc_sw128(sbase + C::kRingOff, 16, 1024);
-            const uint64_t vdesc = smem_desc_sw128(sbase + C::kRingOff, C::kKeys * 128, 1024);
-            const uint64_t qdesc = smem_desc_sw128(sbase, 16, 1024);
-            const uint32_t s_cols = tmem + C::kSCol + own * 2 * C::kJobKeys, o_cols = tmem + own * D;
-            Ring<C::kSlots> ring;
-            Ring<C::kQSlots> qring;
-            uint32_t vok = 0;             // phase of each slot's vok barrier
-            int n_qk = 0, n_pv = 0;       // jobs issued; job x is in S buffer x & 1
-            // The place of the S products: segment, block, and what of them is needed.
-            int seg = -1, blk = 0, blk0 = 0, blk1 = 0, tail0 = 0, kslot = 0, vslot = 0, qslot = 0, nq = 0;
-            bool wide = false, first = false;
-            auto land = [&](int* slot) {
-                *slot = ring.slot;
-                const bool ok = wait1(C::kFull + ring.slot, ring.phase);
-                ring.next();
-                return ok;
-            };
-            auto land_v = [&]() {
-                if (!land(&vslot)) return false;
-                if (blk >= tail0) {
-                    const bool ok = wait1(C::kVok + vslot, (vok >> vslot) & 1u);
-                    vok ^= 1u << vslot;
-                    return ok;
-                }
-                return true;
-            };
-            // To the pipeline's next block, over the other's; its K has landed then
-            // (1). 0: none left, -1: stop, 2: not among the next `limit` blocks (call
-            // again). While a P V of this pipeline holds its V slot, the ring lets
-            // only the next two blocks land, so that the limit is 2 then.
-            auto advance = [&](int limit) -> int {
-                for (; limit > 0; --limit) {
-                    if (++blk >= blk1) {
-                        if (seg >= 0) {  // every S of this segment has been issued
-                            for (int i = 0; i < nq; ++i) tc_commit(bar(C::kQEmpty + (C::kQSlots == 1 ? 0 : (qslot + i) % 2)));
-                            mbar_arrive(bar(C::kSegFree + seg % C::kSegRing));
-                        }
-                        ++seg;
-                        if (!wait1(C::kSegFull + seg % C::kSegRing, uint32_t(seg / C::kSegRing) & 1u)) return -1;
-                        const TcSeg& s = seg_at(seg);
-                        if (s.blk0 == s.blk1) return 0;
-                        blk = blk0 = s.blk0;
-                        blk1 = s.blk1;
-                        tail0 = s.tail0;
-                        wide = s.wide != 0;
-                        nq = wide ? 2 : 1;
-                        qslot = qring.slot;
-                        for (int i = 0; i < nq; ++i) {
-                            if (!wait1(C::kQFull + qring.slot, qring.phase)) return -1;
-                            qring.next();
-                        }
-                        first = true;
-                    }
-                    if (!land(&kslot)) return -1;
-                    if (C::kTiles == 1 || wide || ((blk - blk0) & 1) == own) return 1;
-                    // the other pipeline's block: seen to land, and given back
-                    int vs;
-                    if (!land(&vs)) return -1;
-                    if (blk >= tail0) vok ^= 1u << vs;
-                    mbar_arrive(bar(C::kEmpty + kslot));
-                    mbar_arrive(bar(C::kEmpty + vs));
-                }
-                return 2;
-            };
-            constexpr int kAny = 0x7fffffff;
-            auto issue_s = [&](int half) {
-                tc_fence_after();
-                const int qs = C::kQSlots == 1 ? 0 : wide ? (qslot + own) % 2 : qslot;
-                const uint64_t kb = kdesc + uint32_t(kslot * (C::kSlotBytes / 16) + half * (C::kJobKeys * 8));
-                const uint64_t qb = qdesc + uint32_t(qs * (C::kQBytes / 16));
-                const uint32_t d = s_cols + (n_qk & 1) * C::kJobKeys;
-#pragma unroll
-                for (int k = 0; k < D / 16; ++k)
-                    tc_mma_f16(d, qb + ((k / 4) * (C::kRows * 128) + (k % 4) * 32) / 16,
-                               kb + ((k / 4) * (C::kKeys * 128) + (k % 4) * 32) / 16, idesc_s, k > 0);
-                tc_commit(bar(C::kSFull + 2 * own + (n_qk & 1)));
-                if (half == C::kJobs - 1) tc_commit(bar(C::kEmpty + kslot));
-                ++n_qk;
-            };
-            int more = advance(kAny);
-            if (more == 1) issue_s(0);
-            while (more == 1) {
-                if (!land_v()) break;
-                const int vs = vslot;
-                const bool fresh = first;
-                first = false;
-                bool ok = true;
-#pragma unroll
-                for (int half = 0; half < C::kJobs; ++half) {
-                    // the next job's S, then this job's P V
-                    if (half + 1 < C::kJobs) {
-                        issue_s(half + 1);
-                    } else {
-                        more = advance(2);
-                        if (more < 0) {
-                            ok = false;
-                            break;
-                        }
-                        if (more == 1) issue_s(0);
-                    }
-                    const int buf = n_pv & 1;
-                    if (!wait1(C::kPFull + 2 * own + buf, uint32_t(n_pv >> 1) & 1u)) {
-                        ok = false;
+        if (me == 0 && segments > 0)
+            for (int p = 0; p < C::kPipes; ++p) mbar_wait_bounded(bar(C::kQFull + p), uint32_t(segments - 1) & 1u);
+    } else if (!soft) {
+        // ================================================================ V inspectors; the first also walks the segments
+        constexpr uint32_t kExp = kBf16 ? 0x7f807f80u : 0x7c007c00u;
+        const int me = part - C::kPipes - C::kProducers;
+        Ring<C::kSlots> ring;
+        bool ok = true, more = walker;
+        int walked = 0;
+        for (int i = 0; ok; ++i) {
+            // Keep the ring of segments full; wait for a place only when fewer than four are ahead.
+            while (more && walked < i + C::kSegRing) {
+                if (walked >= C::kSegRing) {
+                    const int place = C::kSegFree + walked % C::kSegRing;
+                    const uint32_t phase = seg_phase(walked) ^ 1u;
+                    if (walked > i + 3) {
+                        if (!__all_sync(kFull, mbar_test_wait(bar(place), phase))) break;
+                    } else if (!(ok = wait(place, phase))) {
                         break;
                     }
-                    tc_fence_after();
-                    const uint64_t vb = vdesc + uint32_t(vs * (C::kSlotBytes / 16) + half * (C::kJobKeys * 8));
-#pragma unroll
-                    for (int k = 0; k < C::kJobKeys / 16; ++k)
-                        tc_mma_f16_ta(o_cols, s_cols + buf * C::kJobKeys + 8 * k, vb + k * 128, idesc_o,
-                                      !fresh || half > 0 || k > 0);
-                    tc_commit(bar(C::kPvDone + 2 * own + buf));
-                    if (half == C::kJobs - 1) tc_commit(bar(C::kEmpty + vs));
-                    ++n_pv;
                 }
-                if (!ok) break;
-                if (more == 2 && (more = advance(kAny)) == 1) issue_s(0);
+                TreeWalk::Seg s;
+                more = walk.next(a, &s);
+                if (lane == 0) {
+                    TcSeg x{};
+                    if (more)
+                        x = TcSeg{s.blk0, s.blk1,  s.tail0, s.slots, s.slot,  s.row0, s.node0,   s.nodes,
+                                  s.hh,   s.head0, s.kvh,   s.r.lo,  s.r.len, s.r.n,  s.r.start, 0};
+                    segs[walked % C::kSegRing] = x;
+                    mbar_arrive(bar(C::kSegFull + walked % C::kSegRing));
+                }
+                __syncwarp();
+                ++walked;
             }
-            // every mma has completed before the tensor memory is released
-            tc_commit(bar(C::kAllDone + own));
-            mbar_wait_bounded(bar(C::kAllDone + own), 0u);
-        }
-    } else if (wid >= 14) {
-        // ================================================================ V inspectors
-        Ring<C::kSlots> ring;
-        constexpr uint32_t kExp = kBf16 ? 0x7f807f80u : 0x7c007c00u;
-        bool ok = true;
-        for (int i = 0; ok; ++i) {
-            if (!seg_wait(i)) break;
+            if (!ok || !seg_wait(i)) break;
             const TcSeg& s = seg_at(i);
             const int blk1 = s.blk1;
             if (s.blk0 == blk1) break;
@@ -516,7 +538,7 @@ __global__ void __launch_bounds__(512, 1)
                 if (blk >= s.tail0) {
                     uint8_t* vb = smem + C::kRingOff + ring.slot * C::kSlotBytes;
                     bool found = false;
-                    for (int row = tid - 448; row < C::kKeys; row += 32 * C::kInspectors) {
+                    for (int row = 32 * me + lane; row < C::kKeys; row += 32 * C::kInspectors) {
                         const int tok = tree_token(a, blk, row);
                         const bool dead = tok < 0 || tok >= s.len, node = tok >= s.len - s.n;
                         if (!dead && !node) continue;
@@ -547,15 +569,15 @@ __global__ void __launch_bounds__(512, 1)
             }
             seg_free(i);
         }
-    } else if (wid < 4 * C::kTiles) {
-        // ================================================================ softmax of pipeline t
-        const int t = wid >> 2, row = tid & 127;
+    } else {
+        // ================================================================ softmax of pipeline p
+        const int pipe = wid >> 2, p = pipe % C::kPipes, row = tid & 127;
         const uint32_t lanes = uint32_t(32 * (wid & 3)) << 16;
-        const uint32_t to = tmem + lanes + t * D, ts0 = tmem + lanes + C::kSCol + t * 2 * C::kJobKeys;
+        const uint32_t to = tmem + lanes + pipe * D, ts0 = tmem + lanes + C::kSCol + pipe * 2 * C::kJobKeys;
         const float scale = a.scale_log2 == 0.f ? 1e-38f : fabsf(a.scale_log2);
         const int per_slot = a.slot_rows < 32 ? a.slot_rows : 32;
         const bool packed = a.page_size % a.slot_rows == 0;
-        int jobs = 0, n_one = 0, kblocks = 0;  // kblocks: K blocks before this segment
+        int jobs = 0, kblocks = 0;  // kblocks: K blocks before this segment
         bool ok = true;
         for (int seg = 0; ok; ++seg) {
             if (!seg_wait(seg)) break;
@@ -563,20 +585,15 @@ __global__ void __launch_bounds__(512, 1)
             const int blk0 = s.blk0, blk1 = s.blk1, tail0 = s.tail0;
             if (blk0 == blk1) break;
             const TreeReq r = s.req();
-            const bool wide = s.wide != 0, joint = C::kTiles == 2 && !wide;  // joint: both pipelines hold parts of the same rows
-            const int node = s.node0 + (wide ? t * a.npt : 0) + row / a.hpt;
-            const long long at = tree_row(a, s.row0, s.nodes, s.hh, row + (wide ? t * C::kRows : 0));
+            const int node = s.node0 + p * a.npt + row / a.hpt;
+            const long long at = tree_row(a, s.row0, s.nodes, s.hh, row + p * C::kRows);
             const bool live = __any_sync(kFull, at >= 0);  // a warp without rows only keeps step
             float m = kNegInf, l = 0.f;
-            // pipeline 1 leaves the last joint segment's O to pipeline 0 until it has been read
-            if (t == 1 && n_one > 0 && !wait(C::kOneFree, uint32_t(n_one - 1) & 1u)) break;
-            bool fresh = true;
-            for (int blk = blk0 + (joint ? t : 0); blk < blk1 && ok; blk += joint ? 2 : 1) {
+            for (int blk = blk0; blk < blk1 && ok; ++blk) {
 #pragma unroll 1
                 for (int half = 0; half < C::kJobs; ++half) {
                     const int buf = jobs & 1;
-                    const uint32_t phase = uint32_t(jobs >> 1) & 1u;
-                    if (!(ok = wait(C::kSFull + 2 * t + buf, phase))) break;
+                    if (!(ok = wait(C::kSFull + 2 * p + buf, uint32_t(jobs >> 1) & 1u))) break;
                     if (live) {
                         tc_fence_after();
                         const uint32_t ts = ts0 + buf * C::kJobKeys;
@@ -595,11 +612,11 @@ __global__ void __launch_bounds__(512, 1)
                                     allow = tree_allow(a, r, nd, (blk * a.spb) * a.slot_rows + c0, 32);
                                 } else {
                                     for (int e = 0; e < 32; e += per_slot) {
-                                        const int col = c0 + e, p = blk * a.spb + col / a.slot_rows;
-                                        const int r0 = p % a.cpp * a.slot_rows + col % a.slot_rows;
+                                        const int col = c0 + e, q = blk * a.spb + col / a.slot_rows;
+                                        const int r0 = q % a.cpp * a.slot_rows + col % a.slot_rows;
                                         const int count = min(per_slot, a.page_size - r0);
                                         if ((bad_pages >> (col / a.slot_rows)) & 1u) continue;
-                                        allow |= tree_allow(a, r, nd, p / a.cpp * a.page_size + r0, count) << e;
+                                        allow |= tree_allow(a, r, nd, q / a.cpp * a.page_size + r0, count) << e;
                                     }
                                 }
 #pragma unroll
@@ -611,7 +628,7 @@ __global__ void __launch_bounds__(512, 1)
 #pragma unroll
                         for (int c = 1; c < C::kJobKeys; ++c) top = fmaxf(top, __uint_as_float(x[c]));
                         top *= scale;
-                        if (fresh) {
+                        if (blk == blk0 && half == 0) {
                             m = top;
                         } else {
                             const bool rise = top > m + 8.f;
@@ -622,7 +639,7 @@ __global__ void __launch_bounds__(512, 1)
                                 // O holds every job before this one once the last P V is done. S of this
                                 // job was issued after the P V before in its buffer, so that no barrier is
                                 // more than one phase behind.
-                                if (!(ok = wait(C::kPvDone + 2 * t + (buf ^ 1), uint32_t((jobs - 1) >> 1) & 1u))) break;
+                                if (!(ok = wait(C::kPvDone + 2 * p + (buf ^ 1), uint32_t((jobs - 1) >> 1) & 1u))) break;
                                 tc_fence_after();
 #pragma unroll 1
                                 for (int c = 0; c < D; c += 16) {
@@ -638,72 +655,45 @@ __global__ void __launch_bounds__(512, 1)
                         const float mu = m == kNegInf ? 0.f : m;
                         float2 sum = make_float2(0.f, 0.f);
                         const float2 sc2 = make_float2(scale, scale), mu2 = make_float2(-mu, -mu);
-                        uint32_t p[C::kJobKeys / 2];
+                        uint32_t w[C::kJobKeys / 2];
 #pragma unroll
                         for (int e = 0; e < C::kJobKeys / 2; ++e) {
                             float2 y = make_float2(__uint_as_float(x[2 * e]), __uint_as_float(x[2 * e + 1]));
                             y = __ffma2_rn(y, sc2, mu2);
                             y = make_float2(ex2(y.x), ex2(y.y));
                             sum = __fadd2_rn(sum, y);
-                            p[e] = Elt<T>::pack(y.x, y.y);
+                            w[e] = Elt<T>::pack(y.x, y.y);
                         }
-                        tmem_st32(ts, p);
+                        tmem_st32(ts, w);
                         l += sum.x + sum.y;
                         tmem_wait_st();
                         tc_fence_before();
                     }
-                    fresh = false;
                     ++jobs;
                     __syncwarp();
-                    if (lane == 0) mbar_arrive(bar(C::kPFull + 2 * t + buf));
+                    if (lane == 0) mbar_arrive(bar(C::kPFull + 2 * p + buf));
                 }
             }
             if (!ok) break;
             kblocks += blk1 - blk0;
             // ---- the segment's end
-            if (!fresh && !wait(C::kPvDone + 2 * t + ((jobs - 1) & 1), uint32_t((jobs - 1) >> 1) & 1u)) break;
+            if (!wait(C::kPvDone + 2 * p + ((jobs - 1) & 1), uint32_t((jobs - 1) >> 1) & 1u)) break;
             tc_fence_after();
-            float2 other = make_float2(kNegInf, 0.f);
-            const bool two = joint && blk1 - blk0 > 1;  // pipeline 1 had a block
-            if (joint) {
-                if (t == 1) {
-                    stat[row] = make_float2(m, l);
-                    tc_fence_before();
-                    __syncwarp();
-                    if (lane == 0) mbar_arrive(bar(C::kOneDone));
-                    ++n_one;
-                    seg_free(seg);
-                    continue;
-                }
-                if (!wait(C::kOneDone, uint32_t(n_one++) & 1u)) break;
-                tc_fence_after();
-                if (two) other = stat[row];
-            }
-            const float mm = fmaxf(m, other.x), mu = mm == kNegInf ? 0.f : mm;
-            const float f0 = ex2(m - mu), f1 = ex2(other.x - mu);
-            const float L = l * f0 + other.y * f1;
-            const float inv = mm == kNegInf ? 0.f : 1.f / L;
-            const float lse2 = mm == kNegInf ? kNegInf : mm + log2f(L);
-            const float i0 = f0 * inv, i1 = f1 * inv;
-            const bool fix = bad_v[seg & 3] == seg + 1;
             if (live) {
+                const float inv = m == kNegInf ? 0.f : 1.f / l;
+                const float lse2 = m == kNegInf ? kNegInf : m + log2f(l);
+                const bool fix = bad_v[seg & 3] == seg + 1;
+                const size_t prow = size_t(s.slot) * a.seg_rows + row + p * C::kRows;
 #pragma unroll 1
                 for (int c = 0; c < D; c += 32) {
                     uint32_t o[32];
-                    tmem_ld32(to + c, o);
                     float f[32];
-                    if (two) {
-                        uint32_t o1[32];
-                        tmem_ld32(to + D + c, o1);
-                        tmem_wait_ld();
+                    tmem_ld32(to + c, o);
+                    tmem_wait_ld();
 #pragma unroll
-                        for (int e = 0; e < 32; ++e) f[e] = __uint_as_float(o[e]) * i0 + __uint_as_float(o1[e]) * i1;
-                    } else {
-                        tmem_wait_ld();
-#pragma unroll
-                        for (int e = 0; e < 32; ++e) f[e] = __uint_as_float(o[e]) * i0;
-                    }
-                    if (fix && at >= 0) {
+                    for (int e = 0; e < 32; ++e) f[e] = __uint_as_float(o[e]) * inv;
+                    if (at < 0) continue;
+                    if (fix) {
                         // non-finite elements of the node rows in these blocks, for the rows that attend them
                         for (int i = 0; i < r.n; ++i) {
                             const int tok = r.ctx() + i;
@@ -721,30 +711,23 @@ __global__ void __launch_bounds__(512, 1)
                             }
                         }
                     }
-                    if (at >= 0) {
-                        if (s.slot >= 0) {
-                            float4* po = reinterpret_cast<float4*>(
-                                a.part_o + (size_t(s.slot) * a.seg_rows + row + (wide ? t * C::kRows : 0)) * D + c);
+                    if (s.slot >= 0) {
+                        float4* po = reinterpret_cast<float4*>(a.part_o + prow * D + c);
 #pragma unroll
-                            for (int e = 0; e < 8; ++e) po[e] = make_float4(f[4 * e], f[4 * e + 1], f[4 * e + 2], f[4 * e + 3]);
-                        } else {
-                            uint4* po = reinterpret_cast<uint4*>(static_cast<T*>(a.o) + at * D + c);
+                        for (int e = 0; e < 8; ++e) po[e] = make_float4(f[4 * e], f[4 * e + 1], f[4 * e + 2], f[4 * e + 3]);
+                    } else {
+                        uint4* po = reinterpret_cast<uint4*>(static_cast<T*>(a.o) + at * D + c);
 #pragma unroll
-                            for (int e = 0; e < 4; ++e) po[e] = Elt<T>::from_f32(f + 8 * e);
-                        }
+                        for (int e = 0; e < 4; ++e) po[e] = Elt<T>::from_f32(f + 8 * e);
                     }
                 }
                 if (at >= 0) {
                     if (s.slot >= 0)
-                        a.part_lse[size_t(s.slot) * a.seg_rows + row + (wide ? t * C::kRows : 0)] = lse2;
+                        a.part_lse[prow] = lse2;
                     else
                         a.lse[at] = lse2 == kNegInf ? kNegInf : lse2 * kLn2;
                 }
-            }
-            if (joint) {
                 tc_fence_before();
-                __syncwarp();
-                if (lane == 0) mbar_arrive(bar(C::kOneFree));
             }
             seg_free(seg);
         }
@@ -752,7 +735,7 @@ __global__ void __launch_bounds__(512, 1)
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
-    if (wid == 9) tmem_dealloc(tmem, 512);
+    if (wid == C::kSoftWarps) tmem_dealloc(tmem, 512);
 }
 
 }  // namespace pd

@@ -39,8 +39,10 @@ bool cc_by_dim(int D, TreeKernels* k) {
 // which no tensor-core type holds, and larger groups on CUDA cores.
 // `wide`: two row tiles per segment (where a kernel for it exists).
 bool pick(pd_dtype dt, bool fp8, int D, int group, bool wide, TreeKernels* k) {
-    if (dt != PD_F32 && group <= 128 && !fp8)
+    if (dt != PD_F32 && group <= 128) {
+        if (fp8) return dt == PD_F16 ? tree_tc_f16_fp8(D, wide, k) : tree_tc_bf16_fp8(D, wide, k);
         return dt == PD_F16 ? tree_tc_f16(D, wide, k) : tree_tc_bf16(D, wide, k);
+    }
     switch (dt) {
         case PD_F32: return !fp8 && cc_by_dim<float, float>(D, k);
         case PD_F16: return fp8 ? cc_by_dim<__half, uint8_t>(D, k) : cc_by_dim<__half, __half>(D, k);
@@ -50,30 +52,34 @@ bool pick(pd_dtype dt, bool fp8, int D, int group, bool wide, TreeKernels* k) {
     return false;
 }
 
-pd_status encode(CUtensorMap* map, pd_dtype dt, int rank, const void* base, const cuuint64_t* dims,
+pd_status encode(CUtensorMap* map, CUtensorMapDataType ty, int rank, const void* base, const cuuint64_t* dims,
                  const cuuint64_t* strides, const cuuint32_t* box) {
     PFN_cuTensorMapEncodeTiled_v12000 enc = host::tensor_map_encoder();
     if (enc == nullptr) return host::fail(PD_ERR_CUDA, "cuTensorMapEncodeTiled is not available from the driver");
     const cuuint32_t ones[4] = {1, 1, 1, 1};
-    const CUresult r = enc(map, dt == PD_BF16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16,
-                           cuuint32_t(rank), const_cast<void*>(base), dims, strides, box, ones,
-                           CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+    const CUtensorMapSwizzle swizzle = ty == CU_TENSOR_MAP_DATA_TYPE_UINT8 ? CU_TENSOR_MAP_SWIZZLE_NONE : CU_TENSOR_MAP_SWIZZLE_128B;
+    const CUresult r = enc(map, ty, cuuint32_t(rank), const_cast<void*>(base), dims, strides, box, ones,
+                           CU_TENSOR_MAP_INTERLEAVE_NONE, swizzle, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
                            CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
     return r == CUDA_SUCCESS ? PD_OK : host::fail(PD_ERR_CUDA, "cuTensorMapEncodeTiled failed (%d)", int(r));
 }
 
-// Boxes of 64 columns: of q {64, heads of a tile, nodes of a row tile}, of K and V {64, rows of a slot}.
-pd_status make_maps(const TreeArgs& a, pd_dtype dt, int D, CUtensorMap* q, CUtensorMap* k, CUtensorMap* v) {
-    const cuuint64_t e = 2, d = cuuint64_t(D), ps = cuuint64_t(a.page_size), hk = cuuint64_t(a.num_kv_heads),
-                     hq = cuuint64_t(a.num_qo_heads);
-    const cuuint64_t qd[3] = {d, hq, cuuint64_t(a.total_new)}, qs[2] = {d * e, hq * d * e};
-    const cuuint32_t qb[3] = {64, cuuint32_t(a.hpt), cuuint32_t(a.npt)};
-    pd_status st = encode(q, dt, 3, a.q, qd, qs, qb);
-    if (st != PD_OK) return st;
+// Boxes: of q {64 columns, heads of a tile, nodes of a row tile}; of K and V {64
+// columns, rows of a slot}, of codes {head_dim columns, rows of a slot}. E4M3
+// pools: the kernel reads q itself.
+pd_status make_maps(const TreeArgs& a, pd_dtype dt, bool fp8, int D, CUtensorMap* q, CUtensorMap* k, CUtensorMap* v) {
+    const CUtensorMapDataType qt = dt == PD_BF16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16;
+    const CUtensorMapDataType kt = fp8 ? CU_TENSOR_MAP_DATA_TYPE_UINT8 : qt;
+    const cuuint64_t d = cuuint64_t(D), ps = cuuint64_t(a.page_size), hk = cuuint64_t(a.num_kv_heads),
+                     hq = cuuint64_t(a.num_qo_heads), e = fp8 ? 1 : 2;
     const cuuint64_t kd[4] = {d, ps, hk, cuuint64_t(a.num_total_pages)}, ks[3] = {d * e, ps * d * e, hk * ps * d * e};
-    const cuuint32_t kb[4] = {64, cuuint32_t(a.slot_rows), 1, 1};
-    if ((st = encode(k, dt, 4, a.k, kd, ks, kb)) != PD_OK) return st;
-    return encode(v, dt, 4, a.v, kd, ks, kb);
+    const cuuint32_t kb[4] = {fp8 ? cuuint32_t(D) : 64u, cuuint32_t(a.slot_rows), 1, 1};
+    pd_status st = encode(k, kt, 4, a.k, kd, ks, kb);
+    if (st == PD_OK) st = encode(v, kt, 4, a.v, kd, ks, kb);
+    if (st != PD_OK || fp8) return st;
+    const cuuint64_t qd[3] = {d, hq, cuuint64_t(a.total_new)}, qs[2] = {d * 2, hq * d * 2};
+    const cuuint32_t qb[3] = {64, cuuint32_t(a.hpt), cuuint32_t(a.npt)};
+    return encode(q, qt, 3, a.q, qd, qs, qb);
 }
 
 size_t round256(size_t x) { return (x + 255) / 256 * 256; }
@@ -187,8 +193,8 @@ pd_status tree_impl(const void* q, const void* k_data, const void* v_data, const
     const int grid = int(ctas < most ? ctas : most);
     cudaStream_t cs = static_cast<cudaStream_t>(stream);
     if ((st = host::allow_smem(kn.main, kn.smem)) != PD_OK) return st;
-    CUtensorMap maps[3];
-    if (kn.tensor && (st = make_maps(a, dt, D, &maps[0], &maps[1], &maps[2])) != PD_OK) return st;
+    CUtensorMap maps[3]{};
+    if (kn.tensor && (st = make_maps(a, dt, fp8, D, &maps[0], &maps[1], &maps[2])) != PD_OK) return st;
     void* args[] = {&a, &maps[0], &maps[1], &maps[2]};
     cudaError_t e = cudaLaunchKernel(kn.main, dim3(grid), dim3(kn.threads), args, kn.smem, cs);
     if (e != cudaSuccess) return host::cuda_fail(e, "tree decode launch");

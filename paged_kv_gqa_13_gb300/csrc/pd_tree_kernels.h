@@ -15,5 +15,7 @@ struct TreeKernels {
 
 bool tree_tc_f16(int head_dim, bool wide, TreeKernels* k);
 bool tree_tc_bf16(int head_dim, bool wide, TreeKernels* k);
+bool tree_tc_f16_fp8(int head_dim, bool wide, TreeKernels* k);
+bool tree_tc_bf16_fp8(int head_dim, bool wide, TreeKernels* k);
 
 }  // namespace pd

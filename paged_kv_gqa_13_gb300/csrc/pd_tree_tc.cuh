@@ -29,12 +29,19 @@
 // node rows are replaced by zero, to be added to the rows that attend them at
 // the end. The first inspector also walks the segments.
 //
+// E4M3 pools (kFp8): copies bring codes into stages, and converters, in the
+// inspectors' place, widen them into the operand slots. Every code is an f16
+// value, one conversion per pair of codes (a bf16 value takes four
+// instructions), so both products run in f16 for bf16 q too: the softmax warps
+// write q rows as f16 times a power of two each.
+//
 // The running maximum of a row moves only when it rises by more than 2^8 (the
 // weights then stay below 2^8, and O, in tensor memory, is rescaled rarely).
 #pragma once
 
 #include "pd_decode_tc.cuh"
 #include "pd_tree.cuh"
+#include "pd_tree_kernels.h"
 
 namespace pd {
 
@@ -143,7 +150,7 @@ __device__ __forceinline__ bool tree_wait_warp(uint32_t bar, uint32_t parity, vo
 // Lines are independent: each walks a range of work of its own through a ring
 // of its own. kWide: one line, two pipelines over the same blocks. Otherwise
 // two lines of one pipeline (head_dim 256: one, for tensor memory holds one O).
-template <int D, bool kWide>
+template <int D, bool kWide, bool kFp8>
 struct CfgTree {
     static constexpr int kRows = 128;
     static constexpr int kLines = kWide || D == 256 ? 1 : 2;
@@ -154,10 +161,12 @@ struct CfgTree {
     static constexpr int kHalves = D / 64;             // 128-byte column blocks of a row
     static constexpr int kSlotBytes = kKeys * D * 2;   // one K or V block
     static constexpr int kQBytes = kRows * D * 2;      // one row tile of q
-    static constexpr int kSlots = D == 64 ? 10 : 5;
-    // warps of a line after the softmax warps of all lines: mma, producers, inspectors
-    static constexpr int kProducers = kLines == 2 ? 2 : 4;
-    static constexpr int kInspectors = kLines == 2 ? 1 : 2;
+    static constexpr int kSlots = kFp8 ? (D == 64 ? 4 : 3) : D == 64 ? 10 : 5;
+    static constexpr int kStages = kFp8 ? 4 : 0;       // E4M3 pools: blocks of codes on their way
+    static constexpr int kStageBytes = kKeys * D;
+    // warps of a line after the softmax warps of all lines: mma, producers, inspectors (E4M3 pools: converters)
+    static constexpr int kProducers = kFp8 ? (kLines == 2 ? 1 : 2) : kLines == 2 ? 2 : 4;
+    static constexpr int kInspectors = kFp8 ? (kLines == 2 ? 2 : 4) : kLines == 2 ? 1 : 2;
     static constexpr int kOthers = kPipes + kProducers + kInspectors;
     static constexpr int kSoftWarps = 4 * kLines * kPipes;
     static constexpr int kThreads = round_up(32 * (kSoftWarps + kLines * kOthers), 128);
@@ -168,10 +177,12 @@ struct CfgTree {
     static constexpr int kFull = 0, kEmpty = kFull + kSlots, kVok = kEmpty + kSlots, kQFull = kVok + kSlots,
                          kQEmpty = kQFull + kPipes, kSFull = kQEmpty + kPipes, kPFull = kSFull + 2 * kPipes,
                          kPvDone = kPFull + 2 * kPipes, kAllDone = kPvDone + 2 * kPipes, kSegFull = kAllDone + kPipes,
-                         kSegFree = kSegFull + kSegRing, kBars = kSegFree + kSegRing;
+                         kSegFree = kSegFull + kSegRing, kStFull = kSegFree + kSegRing, kStEmpty = kStFull + kStages,
+                         kBars = kStEmpty + kStages;
     // a line's shared memory: q, ring | barriers, bad-V tags[4], bad slots, segments (of all lines, after the data)
     static constexpr int kRingOff = kPipes * kQBytes;
-    static constexpr int kLineBytes = kRingOff + kSlots * kSlotBytes;
+    static constexpr int kStageOff = kRingOff + kSlots * kSlotBytes;
+    static constexpr int kLineBytes = kStageOff + kStages * kStageBytes;
     static constexpr int kTagOff = round_up(kBars * 8, 16);
     static constexpr int kSegOff = kTagOff + 16 + 4 * kBadRing;
     static constexpr int kCtlBytes = kSegOff + kSegRing * 64;
@@ -224,12 +235,13 @@ __device__ __forceinline__ int tree_token(const TreeArgs& a, int blk, int col) {
 
 // ---------------------------------------------------------------- the kernel
 
-template <typename T, int D, bool kWide>
-__global__ void __launch_bounds__(CfgTree<D, kWide>::kThreads, 1)
+template <typename T, int D, bool kWide, bool kFp8>
+__global__ void __launch_bounds__(CfgTree<D, kWide, kFp8>::kThreads, 1)
     tree_tc_kernel(const TreeArgs a, const __grid_constant__ CUtensorMap tmq, const __grid_constant__ CUtensorMap tmk,
                    const __grid_constant__ CUtensorMap tmv) {
-    using C = CfgTree<D, kWide>;
-    constexpr bool kBf16 = std::is_same<T, __nv_bfloat16>::value;
+    using C = CfgTree<D, kWide, kFp8>;
+    using M = typename std::conditional<kFp8, __half, T>::type;  // operand type
+    constexpr bool kBf16 = std::is_same<M, __nv_bfloat16>::value;
     const float kNegInf = -__int_as_float(0x7f800000);
     extern __shared__ __align__(16) uint8_t tree_tc_smem[];
     uint8_t* base = tree_tc_smem + ((1024u - (smem_u32(tree_tc_smem) & 1023u)) & 1023u);
@@ -254,12 +266,16 @@ __global__ void __launch_bounds__(CfgTree<D, kWide>::kThreads, 1)
     if (!soft && !idle && part == 0) {
         if (lane == 0) {
             for (int i = 0; i < C::kSlots; ++i) {
-                mbar_init(bar(C::kFull + i), 1);
-                mbar_init(bar(C::kEmpty + i), C::kPipes + C::kInspectors);  // the mma warps and the inspectors
+                mbar_init(bar(C::kFull + i), kFp8 ? C::kInspectors : 1);
+                mbar_init(bar(C::kEmpty + i), kFp8 ? C::kPipes : C::kPipes + C::kInspectors);  // mma warps and inspectors
                 mbar_init(bar(C::kVok + i), C::kInspectors);
             }
+            for (int i = 0; i < C::kStages; ++i) {
+                mbar_init(bar(C::kStFull + i), 1);
+                mbar_init(bar(C::kStEmpty + i), C::kInspectors);
+            }
             for (int i = 0; i < C::kPipes; ++i) {
-                mbar_init(bar(C::kQFull + i), 1);
+                mbar_init(bar(C::kQFull + i), kFp8 ? 4 : 1);
                 mbar_init(bar(C::kQEmpty + i), 1);
                 mbar_init(bar(C::kAllDone + i), 1);
             }
@@ -280,7 +296,7 @@ __global__ void __launch_bounds__(CfgTree<D, kWide>::kThreads, 1)
         if (line == 0) tmem_alloc(smem_u32(tslot), 512);
     }
     if (wid == C::kSoftWarps + C::kPipes && lane == 0) {
-        prefetch_tensormap(&tmq);
+        if (!kFp8) prefetch_tensormap(&tmq);
         prefetch_tensormap(&tmk);
         prefetch_tensormap(&tmv);
     }
@@ -309,7 +325,7 @@ __global__ void __launch_bounds__(CfgTree<D, kWide>::kThreads, 1)
     } else if (!soft && part < C::kPipes) {
         // ================================================================ mma of pipeline `part`
         if (lane == 0) {
-            const uint32_t idesc_s = tc_idesc_f16(kBf16, C::kRows, C::kJobKeys, false) | (a.scale_log2 < 0.f ? kIdescNegA : 0u);
+            const uint32_t idesc_s = tc_idesc_f16(kBf16, C::kRows, C::kJobKeys, false) | (!kFp8 && a.scale_log2 < 0.f ? kIdescNegA : 0u);
             constexpr uint32_t idesc_o = tc_idesc_f16(kBf16, C::kRows, D, true);
             // operand descriptors of slot 0 (K K-major, V MN-major) and of the row tile's q; addresses count 16 bytes
             const uint64_t kdesc = smem_desc_sw128(sbase + C::kRingOff, 16, 1024);
@@ -366,7 +382,7 @@ __global__ void __launch_bounds__(CfgTree<D, kWide>::kThreads, 1)
                 if (half == C::kJobs - 1) {
                     tc_commit(bar(C::kEmpty + kslot));
                     if (blk + 1 == blk1) {  // the segment's last S
-                        tc_commit(bar(C::kQEmpty + part));
+                        if (!kFp8) tc_commit(bar(C::kQEmpty + part));
                         mbar_arrive(bar(C::kSegFree + seg % C::kSegRing));
                     }
                 }
@@ -379,7 +395,7 @@ __global__ void __launch_bounds__(CfgTree<D, kWide>::kThreads, 1)
                 const bool tail = blk >= tail0, fresh = first;
                 first = false;
                 if (!land(&vs)) break;
-                if (tail) {
+                if (!kFp8 && tail) {
                     if (!wait1(C::kVok + vs, (vok >> vs) & 1u)) break;
                     vok ^= 1u << vs;
                 }
@@ -429,11 +445,16 @@ __global__ void __launch_bounds__(CfgTree<D, kWide>::kThreads, 1)
         // ================================================================ producers
         const uint64_t once = l2_evict_first_policy(), again = l2_evict_normal_policy();
         const int me = part - C::kPipes;
-        Ring<C::kSlots> ring;
+        // the ring that the copies land in: operand slots, or stages of codes
+        constexpr int kPlaces = kFp8 ? C::kStages : C::kSlots, kPlaceFull = kFp8 ? C::kStFull : C::kFull,
+                      kPlaceEmpty = kFp8 ? C::kStEmpty : C::kEmpty, kPlaceOff = kFp8 ? C::kStageOff : C::kRingOff,
+                      kPlaceBytes = kFp8 ? C::kStageBytes : C::kSlotBytes;
+        Ring<kPlaces> ring;
         int loads = 0, segments = 0, kblocks = 0, turn = 0;  // turn: the producer whose load is next
         bool ok = true;
-        // one box per lane: slot_rows rows x 64 columns
-        const int sl = lane / C::kHalves, hf = lane % C::kHalves;
+        // one box per lane: slot_rows rows x 64 columns (codes: x head_dim columns)
+        constexpr int kBoxes = kFp8 ? 1 : C::kHalves, kRowBytes = kFp8 ? D : 128;
+        const int sl = lane / kBoxes, hf = lane % kBoxes;
         auto load_block = [&](const TcSeg& s, int blk, const CUtensorMap* tm, bool is_k) -> bool {
             const bool mine = turn == me;
             const int p = blk * a.spb + sl;
@@ -446,22 +467,22 @@ __global__ void __launch_bounds__(CfgTree<D, kWide>::kThreads, 1)
                 bad = page < 0 || page >= a.num_total_pages;
                 if (bad) page = a.num_total_pages;
             }
-            if (loads >= C::kSlots && !wait(C::kEmpty + ring.slot, ring.phase ^ 1u)) return false;
+            if (loads >= kPlaces && !wait(kPlaceEmpty + ring.slot, ring.phase ^ 1u)) return false;
             if (mine) {
                 if (is_k) {
                     const unsigned found = __ballot_sync(kFull, bad);
                     if (lane == 0) {
                         unsigned bits = 0;
-                        for (unsigned f = found; f != 0u; f &= f - 1u) bits |= 1u << ((__ffs(f) - 1) / C::kHalves);
+                        for (unsigned f = found; f != 0u; f &= f - 1u) bits |= 1u << ((__ffs(f) - 1) / kBoxes);
                         bad_slots[kblocks % C::kBadRing] = bits;
                         if (bits != 0u) atomicOr(a.flags, kFlagBadPage);
                     }
                 }
-                if (lane == 0) mbar_arrive_expect_tx(bar(C::kFull + ring.slot), C::kSlotBytes);
+                if (lane == 0) mbar_arrive_expect_tx(bar(kPlaceFull + ring.slot), kPlaceBytes);
                 __syncwarp();
                 if (sl < a.spb)
-                    tma_load_4d(sbase + C::kRingOff + ring.slot * C::kSlotBytes + hf * (C::kKeys * 128) + sl * a.slot_rows * 128,
-                                tm, hf * 64, row, s.kvh, page, bar(C::kFull + ring.slot), s.n > a.nps ? again : once);
+                    tma_load_4d(sbase + kPlaceOff + ring.slot * kPlaceBytes + hf * (C::kKeys * 128) + sl * a.slot_rows * kRowBytes,
+                                tm, hf * 64, row, s.kvh, page, bar(kPlaceFull + ring.slot), s.n > a.nps ? again : once);
             }
             ++loads;
             ring.next();
@@ -473,7 +494,7 @@ __global__ void __launch_bounds__(CfgTree<D, kWide>::kThreads, 1)
             const TcSeg& s = seg_at(segments);
             const int blk0 = s.blk0, blk1 = s.blk1;
             if (blk0 == blk1) break;
-            for (int p = 0; me == 0 && p < C::kPipes && ok; ++p) {
+            for (int p = 0; !kFp8 && me == 0 && p < C::kPipes && ok; ++p) {
                 // a row tile past the segment's nodes is loaded like another (rows of other requests, or zeros) and not used
                 ok = segments == 0 || wait(C::kQEmpty + p, uint32_t(segments - 1) & 1u);
                 if (!ok) break;
@@ -490,15 +511,17 @@ __global__ void __launch_bounds__(CfgTree<D, kWide>::kThreads, 1)
             seg_free(segments);
         }
         // copies issued last may still be landing when another role has stopped early
-        for (int i = max(0, loads - C::kSlots); i < loads; ++i)
-            mbar_wait_bounded(bar(C::kFull + i % C::kSlots), uint32_t(i / C::kSlots) & 1u);
-        if (me == 0 && segments > 0)
+        for (int i = max(0, loads - kPlaces); i < loads; ++i)
+            mbar_wait_bounded(bar(kPlaceFull + i % kPlaces), uint32_t(i / kPlaces) & 1u);
+        if (!kFp8 && me == 0 && segments > 0)
             for (int p = 0; p < C::kPipes; ++p) mbar_wait_bounded(bar(C::kQFull + p), uint32_t(segments - 1) & 1u);
     } else if (!soft) {
-        // ================================================================ V inspectors; the first also walks the segments
+        // ================================================================ inspectors / converters; the first also walks the segments
         constexpr uint32_t kExp = kBf16 ? 0x7f807f80u : 0x7c007c00u;
         const int me = part - C::kPipes - C::kProducers;
         Ring<C::kSlots> ring;
+        Ring<kFp8 ? C::kStages : 1> stage;
+        int loads = 0;
         bool ok = true, more = walker;
         int walked = 0;
         for (int i = 0; ok; ++i) {
@@ -531,41 +554,81 @@ __global__ void __launch_bounds__(CfgTree<D, kWide>::kThreads, 1)
             const int blk1 = s.blk1;
             if (s.blk0 == blk1) break;
             for (int blk = s.blk0; blk < blk1; ++blk) {
-                if (!(ok = wait(C::kFull + ring.slot, ring.phase))) break;
-                if (lane == 0) mbar_arrive(bar(C::kEmpty + ring.slot));  // K
-                ring.next();
-                if (!(ok = wait(C::kFull + ring.slot, ring.phase))) break;
-                if (blk >= s.tail0) {
-                    uint8_t* vb = smem + C::kRingOff + ring.slot * C::kSlotBytes;
-                    bool found = false;
-                    for (int row = 32 * me + lane; row < C::kKeys; row += 32 * C::kInspectors) {
-                        const int tok = tree_token(a, blk, row);
-                        const bool dead = tok < 0 || tok >= s.len, node = tok >= s.len - s.n;
-                        if (!dead && !node) continue;
-                        for (int hf = 0; hf < C::kHalves; ++hf) {
+                if constexpr (kFp8) {
+                    // codes to f16 (exact), 8 at a time, into the operand layout: K, then V
+                    for (int kv = 0; kv < 2; ++kv, ++loads, ring.next(), stage.next()) {
+                        if (!(ok = wait(C::kStFull + stage.slot, stage.phase))) break;
+                        if (loads >= C::kSlots && !(ok = wait(C::kEmpty + ring.slot, ring.phase ^ 1u))) break;
+                        const uint8_t* from = smem + C::kStageOff + stage.slot * C::kStageBytes;
+                        uint8_t* to = smem + C::kRingOff + ring.slot * C::kSlotBytes;
+                        constexpr int kPerRow = D / 8, kStep = 32 * C::kInspectors / kPerRow;  // lanes per row, rows per round
+                        const int at = 32 * me + lane, piece = at % kPerRow;
+                        const bool guard = kv == 1 && blk >= s.tail0;
+                        bool found = false;
+#pragma unroll 4
+                        for (int row = at / kPerRow; row < C::kKeys; row += kStep) {
+                            uint2 w = *reinterpret_cast<const uint2*>(from + row * D + piece * 8);
+                            if (guard) {
+                                const int tok = tree_token(a, blk, row);
+                                if (tok < 0 || tok >= s.len) {
+                                    w = make_uint2(0u, 0u);
+                                } else if (tok >= s.len - s.n) {
+                                    const uint32_t nx = __vcmpeq4(w.x & 0x7f7f7f7fu, 0x7f7f7f7fu),
+                                                   ny = __vcmpeq4(w.y & 0x7f7f7f7fu, 0x7f7f7f7fu);
+                                    found |= (nx | ny) != 0u;
+                                    w = make_uint2(w.x & ~nx, w.y & ~ny);
+                                }
+                            }
+                            *reinterpret_cast<uint4*>(to + piece / 8 * (C::kKeys * 128) + row * 128 + (((piece & 7) ^ (row & 7)) << 4)) =
+                                make_uint4(e4m3x2_to_f16x2(w.x), e4m3x2_to_f16x2(w.x >> 16), e4m3x2_to_f16x2(w.y),
+                                           e4m3x2_to_f16x2(w.y >> 16));
+                        }
+                        if (found) bad_v[i & 3] = i + 1;
+                        fence_proxy_async_smem();
+                        __syncwarp();
+                        if (lane == 0) {
+                            mbar_arrive(bar(C::kFull + ring.slot));
+                            mbar_arrive(bar(C::kStEmpty + stage.slot));
+                        }
+                    }
+                    if (!ok) break;
+                } else {
+                    if (!(ok = wait(C::kFull + ring.slot, ring.phase))) break;
+                    if (lane == 0) mbar_arrive(bar(C::kEmpty + ring.slot));  // K
+                    ring.next();
+                    if (!(ok = wait(C::kFull + ring.slot, ring.phase))) break;
+                    if (blk >= s.tail0) {
+                        uint8_t* vb = smem + C::kRingOff + ring.slot * C::kSlotBytes;
+                        bool found = false;
+                        for (int row = 32 * me + lane; row < C::kKeys; row += 32 * C::kInspectors) {
+                            const int tok = tree_token(a, blk, row);
+                            const bool dead = tok < 0 || tok >= s.len, node = tok >= s.len - s.n;
+                            if (!dead && !node) continue;
+                            for (int hf = 0; hf < C::kHalves; ++hf) {
 #pragma unroll
-                            for (int c = 0; c < 8; ++c) {
-                                uint4* at = reinterpret_cast<uint4*>(vb + hf * (C::kKeys * 128) + row * 128 + ((c ^ (row & 7)) << 4));
-                                uint4 x = dead ? make_uint4(0u, 0u, 0u, 0u) : *at;
-                                const uint32_t bx = __vcmpeq2(x.x & kExp, kExp), by = __vcmpeq2(x.y & kExp, kExp),
-                                               bz = __vcmpeq2(x.z & kExp, kExp), bw = __vcmpeq2(x.w & kExp, kExp);
-                                if ((bx | by | bz | bw) != 0u) {
-                                    found = true;
-                                    x = make_uint4(x.x & ~bx, x.y & ~by, x.z & ~bz, x.w & ~bw);
-                                    *at = x;
-                                } else if (dead) {
-                                    *at = x;
+                                for (int c = 0; c < 8; ++c) {
+                                    uint4* at = reinterpret_cast<uint4*>(vb + hf * (C::kKeys * 128) + row * 128 + ((c ^ (row & 7)) << 4));
+                                    uint4 x = dead ? make_uint4(0u, 0u, 0u, 0u) : *at;
+                                    const uint32_t bx = __vcmpeq2(x.x & kExp, kExp), by = __vcmpeq2(x.y & kExp, kExp),
+                                                   bz = __vcmpeq2(x.z & kExp, kExp), bw = __vcmpeq2(x.w & kExp, kExp);
+                                    if ((bx | by | bz | bw) != 0u) {
+                                        found = true;
+                                        x = make_uint4(x.x & ~bx, x.y & ~by, x.z & ~bz, x.w & ~bw);
+                                        *at = x;
+                                    } else if (dead) {
+                                        *at = x;
+                                    }
                                 }
                             }
                         }
+                        if (found) bad_v[i & 3] = i + 1;
+                        fence_proxy_async_smem();
+                        __syncwarp();
+                        if (lane == 0) mbar_arrive(bar(C::kVok + ring.slot));
                     }
-                    if (found) bad_v[i & 3] = i + 1;
-                    fence_proxy_async_smem();
-                    __syncwarp();
-                    if (lane == 0) mbar_arrive(bar(C::kVok + ring.slot));
+                    if (lane == 0) mbar_arrive(bar(C::kEmpty + ring.slot));
+                    ring.next();
                 }
-                if (lane == 0) mbar_arrive(bar(C::kEmpty + ring.slot));
-                ring.next();
             }
             seg_free(i);
         }
@@ -574,7 +637,7 @@ __global__ void __launch_bounds__(CfgTree<D, kWide>::kThreads, 1)
         const int pipe = wid >> 2, p = pipe % C::kPipes, row = tid & 127;
         const uint32_t lanes = uint32_t(32 * (wid & 3)) << 16;
         const uint32_t to = tmem + lanes + pipe * D, ts0 = tmem + lanes + C::kSCol + pipe * 2 * C::kJobKeys;
-        const float scale = a.scale_log2 == 0.f ? 1e-38f : fabsf(a.scale_log2);
+        float scale = a.scale_log2 == 0.f ? 1e-38f : fabsf(a.scale_log2);
         const int per_slot = a.slot_rows < 32 ? a.slot_rows : 32;
         const bool packed = a.page_size % a.slot_rows == 0;
         int jobs = 0, kblocks = 0;  // kblocks: K blocks before this segment
@@ -589,6 +652,38 @@ __global__ void __launch_bounds__(CfgTree<D, kWide>::kThreads, 1)
             const long long at = tree_row(a, s.row0, s.nodes, s.hh, row + p * C::kRows);
             const bool live = __any_sync(kFull, at >= 0);  // a warp without rows only keeps step
             float m = kNegInf, l = 0.f;
+            if constexpr (kFp8) {
+                // This thread's q row as f16, times a power of two that brings its largest element near 2^14
+                // (exact but for elements more than 2^28 below it) and the sign of the score scale, into the
+                // operand tile: the last S of the segment before has been read, so the tile is free.
+                const float ks = a.scale_log2 * __ldg(a.k_scale + s.kvh);
+                const uint4* qr = reinterpret_cast<const uint4*>(static_cast<const T*>(a.q) + (at < 0 ? 0 : at) * D);
+                float big = 0.f;
+#pragma unroll 4
+                for (int c = 0; c < D / 8; ++c) {
+                    float f[8];
+                    Elt<T>::to_f32(__ldg(qr + c), f);
+#pragma unroll
+                    for (int e = 0; e < 8; ++e) big = fmaxf(big, fabsf(f[e]));
+                }
+                int up = 0;
+                if (!std::is_same<T, __half>::value && big > 0.f) up = max(-126, min(126, 141 - int(__float_as_uint(big) >> 23)));
+                const float by = __uint_as_float(uint32_t(127 + up) << 23) * (ks < 0.f ? -1.f : 1.f);
+                uint8_t* tile = smem + p * C::kQBytes;
+#pragma unroll 4
+                for (int c = 0; c < D / 8; ++c) {
+                    float f[8];
+                    Elt<T>::to_f32(__ldg(qr + c), f);
+#pragma unroll
+                    for (int e = 0; e < 8; ++e) f[e] = at < 0 ? 0.f : f[e] * by;
+                    *reinterpret_cast<uint4*>(tile + c / 8 * (C::kRows * 128) + row * 128 + (((c & 7) ^ (row & 7)) << 4)) =
+                        Elt<__half>::from_f32(f);
+                }
+                scale = ks == 0.f ? 1e-38f : fabsf(ks) * __uint_as_float(uint32_t(127 - up) << 23);
+                fence_proxy_async_smem();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(bar(C::kQFull + p));
+            }
             for (int blk = blk0; blk < blk1 && ok; ++blk) {
 #pragma unroll 1
                 for (int half = 0; half < C::kJobs; ++half) {
@@ -662,7 +757,7 @@ __global__ void __launch_bounds__(CfgTree<D, kWide>::kThreads, 1)
                             y = __ffma2_rn(y, sc2, mu2);
                             y = make_float2(ex2(y.x), ex2(y.y));
                             sum = __fadd2_rn(sum, y);
-                            w[e] = Elt<T>::pack(y.x, y.y);
+                            w[e] = Elt<M>::pack(y.x, y.y);
                         }
                         tmem_st32(ts, w);
                         l += sum.x + sum.y;
@@ -680,7 +775,7 @@ __global__ void __launch_bounds__(CfgTree<D, kWide>::kThreads, 1)
             if (!wait(C::kPvDone + 2 * p + ((jobs - 1) & 1), uint32_t((jobs - 1) >> 1) & 1u)) break;
             tc_fence_after();
             if (live) {
-                const float inv = m == kNegInf ? 0.f : 1.f / l;
+                const float inv = (m == kNegInf ? 0.f : 1.f / l) * (kFp8 ? __ldg(a.v_scale + s.kvh) : 1.f);
                 const float lse2 = m == kNegInf ? kNegInf : m + log2f(l);
                 const bool fix = bad_v[seg & 3] == seg + 1;
                 const size_t prow = size_t(s.slot) * a.seg_rows + row + p * C::kRows;
@@ -702,11 +797,14 @@ __global__ void __launch_bounds__(CfgTree<D, kWide>::kThreads, 1)
                             if ((tree_allow(a, r, node, tok, 1) & 1u) == 0u) continue;
                             const int page = __ldg(a.indices + r.lo + tok / a.page_size);
                             if (page < 0 || page >= a.num_total_pages) continue;
-                            const T* v = static_cast<const T*>(a.v) +
-                                         ((size_t(page) * a.num_kv_heads + s.kvh) * a.page_size + tok % a.page_size) * D + c;
+                            const size_t vrow = ((size_t(page) * a.num_kv_heads + s.kvh) * a.page_size + tok % a.page_size) * D + c;
 #pragma unroll
                             for (int e = 0; e < 32; ++e) {
-                                const float y = float(v[e]);
+                                float y;
+                                if constexpr (kFp8)  // the only non-finite codes are NaN
+                                    y = (static_cast<const uint8_t*>(a.v)[vrow + e] & 0x7f) == 0x7f ? __int_as_float(0x7fc00000) : 0.f;
+                                else
+                                    y = float(static_cast<const T*>(a.v)[vrow + e]);
                                 if (!isfinite(y)) f[e] += y;
                             }
                         }
@@ -736,6 +834,35 @@ __global__ void __launch_bounds__(CfgTree<D, kWide>::kThreads, 1)
     __syncthreads();
     tc_fence_after();
     if (wid == C::kSoftWarps) tmem_dealloc(tmem, 512);
+}
+
+// ---------------------------------------------------------------- lookup
+
+template <typename T, int D, bool kWide, bool kFp8>
+TreeKernels tree_tc_kernels() {
+    using C = CfgTree<D, kWide, kFp8>;
+    TreeKernels k{};
+    k.main = reinterpret_cast<const void*>(tree_tc_kernel<T, D, kWide, kFp8>);
+    k.merge = reinterpret_cast<const void*>(tree_merge_kernel<T, D>);
+    k.threads = C::kThreads;
+    k.smem = C::kBytes;
+    k.per_sm = 1;
+    k.tile_rows = C::kRows;
+    k.tiles = C::kPipes;
+    k.workers = C::kLines;
+    k.block_tokens = C::kKeys;
+    k.tensor = true;
+    return k;
+}
+
+template <typename T, bool kFp8>
+bool tree_tc_lookup(int D, bool wide, TreeKernels* k) {
+    switch (D) {
+        case 64: *k = wide ? tree_tc_kernels<T, 64, true, kFp8>() : tree_tc_kernels<T, 64, false, kFp8>(); return true;
+        case 128: *k = wide ? tree_tc_kernels<T, 128, true, kFp8>() : tree_tc_kernels<T, 128, false, kFp8>(); return true;
+        case 256: *k = tree_tc_kernels<T, 256, false, kFp8>(); return true;
+    }
+    return false;
 }
 
 }  // namespace pd

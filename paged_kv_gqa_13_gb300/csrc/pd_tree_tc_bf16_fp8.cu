@@ -1,0 +1,6 @@
+// Tensor-core tree decode with bf16 q over E4M3 pools.
+#include "pd_tree_tc.cuh"
+
+namespace pd {
+bool tree_tc_bf16_fp8(int D, bool wide, TreeKernels* k) { return tree_tc_lookup<__nv_bfloat16, true>(D, wide, k); }
+}  // namespace pd

@@ -73,7 +73,7 @@ pd_status make_maps(const TreeArgs& a, pd_dtype dt, bool fp8, int D, CUtensorMap
     const cuuint64_t d = cuuint64_t(D), ps = cuuint64_t(a.page_size), hk = cuuint64_t(a.num_kv_heads),
                      hq = cuuint64_t(a.num_qo_heads), e = fp8 ? 1 : 2;
     const cuuint64_t kd[4] = {d, ps, hk, cuuint64_t(a.num_total_pages)}, ks[3] = {d * e, ps * d * e, hk * ps * d * e};
-    const cuuint32_t kb[4] = {fp8 ? cuuint32_t(D) : 64u, cuuint32_t(a.slot_rows), 1, 1};
+    const cuuint32_t kb[4] = {fp8 ? cuuint32_t(D) : 64u, 1u << a.slot_shift, 1, 1};
     pd_status st = encode(k, kt, 4, a.k, kd, ks, kb);
     if (st == PD_OK) st = encode(v, kt, 4, a.v, kd, ks, kb);
     if (st != PD_OK || fp8) return st;
@@ -117,6 +117,7 @@ pd_status tree_impl(const void* q, const void* k_data, const void* v_data, const
     if (batch <= 0 || page_size <= 0 || num_total_pages <= 0)
         return host::fail(PD_ERR_INVALID, "batch, page_size and num_total_pages must be positive");
     if (total_new < 0 || num_indices < 0) return host::fail(PD_ERR_INVALID, "total_new and num_indices must not be negative");
+    if (total_new > (1 << 30) || Hq > (1 << 20)) return host::fail(PD_ERR_INVALID, "at most 2^30 new rows and 2^20 heads");
     if (tree_mask ? mask_words <= 0 : mask_words != 0)
         return host::fail(PD_ERR_INVALID, "mask_words must be positive with a tree_mask and 0 without (got %d)", mask_words);
     if (!std::isfinite(sm_scale)) return host::fail(PD_ERR_INVALID, "sm_scale must be finite");
@@ -169,25 +170,33 @@ pd_status tree_impl(const void* q, const void* k_data, const void* v_data, const
     a.page_size = page_size;
     a.num_total_pages = num_total_pages;
     a.num_indices = num_indices;
-    a.tile_rows = kn.tile_rows;
+    while ((1 << a.tile_shift) < kn.tile_rows) ++a.tile_shift;
     a.seg_rows = kn.tile_rows * kn.tiles;
     a.hs = (group + kn.tile_rows - 1) / kn.tile_rows;
     a.hpt = (group + a.hs - 1) / a.hs;
     a.npt = kn.tile_rows / a.hpt;
     a.nps = a.npt * kn.tiles;
-    a.slot_rows = 1;
+    int slot_rows = 1;
     if (kn.tensor) {
         // a slot is one copy: the largest power of two that divides the page, from 8 rows (the swizzle's period) to a block
-        a.slot_rows = 8;
-        while (a.slot_rows < kn.block_tokens && page_size % (2 * a.slot_rows) == 0) a.slot_rows *= 2;
+        slot_rows = 8;
+        while (slot_rows < kn.block_tokens && page_size % (2 * slot_rows) == 0) slot_rows *= 2;
     }
-    a.cpp = (page_size + a.slot_rows - 1) / a.slot_rows;
-    a.spb = kn.block_tokens / a.slot_rows;
+    while ((1 << a.slot_shift) < slot_rows) ++a.slot_shift;
+    while ((slot_rows << a.spb_shift) < kn.block_tokens) ++a.spb_shift;
+    a.cpp = int(((long long)page_size + slot_rows - 1) / slot_rows);
+    a.packed = page_size % slot_rows == 0;
+    a.by_page = FastDiv::of(page_size);
+    a.by_cpp = FastDiv::of(a.cpp);
+    a.by_nps = FastDiv::of(a.nps);
+    a.by_hpt = FastDiv::of(a.hpt);
+    a.by_hs = FastDiv::of(a.hs);
+    a.by_heads = FastDiv::of(a.hs * Hk);
     a.scale_log2 = sm_scale * kLog2e;
 
     // No more CTAs than there can be units: segments x key blocks of the longest possible request.
     const long long segs = ((long long)total_new / a.nps + batch) * a.hs * Hk;
-    const long long blocks = ((long long)num_indices * a.cpp + a.spb - 1) / a.spb;
+    const long long blocks = (((long long)num_indices * a.cpp - 1) >> a.spb_shift) + 1;
     const long long bound = segs * (blocks < 1 ? 1 : blocks);
     const long long ctas = (bound + kn.workers - 1) / kn.workers;
     const int grid = int(ctas < most ? ctas : most);

@@ -36,6 +36,25 @@ struct TreeSplit {
     int pad[2];
 };
 
+// Division of 0 <= x < 2^31 by a divisor that the host knows: with s =
+// ceil(log2 d) and m = floor(2^(31 + s) / d) + 1, m d exceeds 2^(31 + s) by at
+// most d <= 2^s, so that x m / 2^(31 + s) is x / d plus less than 1 / d.
+struct FastDiv {
+    uint32_t d = 1, m = 0x80000001u;
+    int s = 31;
+    __host__ static FastDiv of(int divisor) {
+        FastDiv f;
+        f.d = uint32_t(divisor);
+        int s = 0;
+        while ((1ull << s) < f.d) ++s;
+        f.m = uint32_t((1ull << (31 + s)) / f.d + 1);
+        f.s = 31 + s;
+        return f;
+    }
+    __device__ __forceinline__ int div(int x) const { return int((uint64_t(uint32_t(x)) * m) >> s); }
+    __device__ __forceinline__ int mod(int x) const { return x - div(x) * int(d); }
+};
+
 struct TreeArgs {
     const void* q;
     const void* k;
@@ -57,8 +76,10 @@ struct TreeArgs {
     int page_size, num_total_pages, num_indices;
     int hs, hpt;         // head tiles per group, q heads per tile (the last may hold fewer)
     int npt, nps;        // nodes per row tile, nodes per segment (one or two row tiles)
-    int tile_rows, seg_rows;  // rows of a row tile and of a segment, as the partials are laid out
-    int slot_rows, cpp, spb;
+    int tile_shift, seg_rows;  // rows of a row tile (log2) and of a segment, as the partials are laid out
+    int slot_shift, cpp, spb_shift;  // rows of a slot (log2), slots of a page, slots of a block (log2)
+    FastDiv by_page, by_cpp, by_nps, by_hpt, by_hs, by_heads;  // by page_size, cpp, nps, hpt, hs, hs * num_kv_heads
+    int packed;          // pages are whole slots: the tokens of a block are consecutive
     float scale_log2;    // sm_scale * log2(e)
     int test_extra_tx;
 };
@@ -66,14 +87,14 @@ struct TreeArgs {
 // One request as the table gives it. A bad one keeps its nodes and loses its
 // tokens (len 0), so that every one of its rows is written as empty.
 struct TreeReq {
-    int n = 0, start = 0;  // nodes, first q row
-    int len = 0, lo = 0;   // tokens, first entry of indices
-    int bad = 0;
+    int n, start;  // nodes, first q row
+    int len, lo;   // tokens, first entry of indices
+    int bad;       // status bits
     __device__ __forceinline__ int ctx() const { return len - n; }
 };
 
 __device__ __forceinline__ TreeReq tree_request(const TreeArgs& a, int b) {
-    TreeReq r;
+    TreeReq r = {0, 0, 0, 0, 0};
     const int s = __ldg(a.new_indptr + b), e = __ldg(a.new_indptr + b + 1);
     const int lo = __ldg(a.indptr + b), hi = __ldg(a.indptr + b + 1);
     int last = __ldg(a.last_page_len + b);
@@ -105,18 +126,25 @@ __device__ __forceinline__ TreeReq tree_request(const TreeArgs& a, int b) {
 }
 
 __device__ __forceinline__ int tree_slots(const TreeArgs& a, int tokens) {
-    return tokens / a.page_size * a.cpp + (tokens % a.page_size + a.slot_rows - 1) / a.slot_rows;
+    const int page = a.by_page.div(tokens), row = tokens - page * a.page_size;
+    return page * a.cpp + ((row + (1 << a.slot_shift) - 1) >> a.slot_shift);
+}
+
+// The slot that holds a token.
+__device__ __forceinline__ int tree_slot_of(const TreeArgs& a, int token) {
+    const int page = a.by_page.div(token), row = token - page * a.page_size;
+    return page * a.cpp + (row >> a.slot_shift);
 }
 
 // Key blocks of segment tau; at least one, so that a segment with no keys is still written.
 __device__ __forceinline__ int tree_blocks(const TreeArgs& a, const TreeReq& r, int tau) {
     int limit = r.len;
     if (a.mask == nullptr) limit = min(limit, max(0, r.ctx()) + min(r.n, (tau + 1) * a.nps));
-    return max(1, (tree_slots(a, limit) + a.spb - 1) / a.spb);
+    return max(1, (tree_slots(a, limit) + (1 << a.spb_shift) - 1) >> a.spb_shift);
 }
 
 __device__ __forceinline__ long long tree_cost(const TreeArgs& a, const TreeReq& r) {
-    const int segs = (r.n + a.nps - 1) / a.nps;
+    const int segs = a.by_nps.div(r.n + a.nps - 1);
     long long sum = 0;
     if (a.mask != nullptr || segs <= 1) {
         sum = segs > 0 ? (long long)segs * tree_blocks(a, r, segs - 1) : 0;
@@ -158,8 +186,8 @@ struct TreeWalk {
         const int nblk = tree_blocks(a, r, tau);
         s->r = r;
         s->hh = hh;
-        s->kvh = hh / a.hs;
-        const int h0 = (hh % a.hs) * a.hpt;
+        s->kvh = a.by_hs.div(hh);
+        const int h0 = (hh - s->kvh * a.hs) * a.hpt;
         s->head0 = s->kvh * a.group + h0;
         s->heads = min(a.hpt, a.group - h0);
         s->node0 = tau * a.nps;
@@ -167,8 +195,7 @@ struct TreeWalk {
         s->row0 = r.start + s->node0;
         s->blk0 = blk;
         s->blk1 = int(min((long long)nblk, blk + (end - unit)));
-        const int ctx = max(0, r.ctx());
-        s->tail0 = (ctx / a.page_size * a.cpp + ctx % a.page_size / a.slot_rows) / a.spb;
+        s->tail0 = tree_slot_of(a, max(0, r.ctx())) >> a.spb_shift;
         s->slots = tree_slots(a, r.len);
         const long long begin = unit - blk;
         s->slot = (blk == 0 && s->blk1 == nblk) ? -1 : 2 * worker + (begin > worker * W ? 1 : 0);
@@ -184,6 +211,7 @@ struct TreePlanScratch {
     long long total, W;
     struct {
         int b, hh, tau, blk;
+        TreeReq r;
     } at[2];  // where each worker of the CTA starts
 };
 
@@ -237,9 +265,15 @@ __device__ __forceinline__ void tree_plan(const TreeArgs& a, TreePlanScratch* sc
                 left -= c;
                 continue;
             }
-            const long long each = c / (a.hs * a.num_kv_heads);
-            sc->at[k].hh = int(left / each);
-            left %= each;
+            if (c < 0x7fffffffll) {
+                const int each = a.by_heads.div(int(c)), hh = int(unsigned(left) / unsigned(each));
+                sc->at[k].hh = hh;
+                left -= (long long)hh * each;
+            } else {
+                const long long each = c / (a.hs * a.num_kv_heads);
+                sc->at[k].hh = int(left / each);
+                left %= each;
+            }
             int tau = 0;
             for (;; ++tau) {
                 const int nb = tree_blocks(a, r, tau);
@@ -248,6 +282,7 @@ __device__ __forceinline__ void tree_plan(const TreeArgs& a, TreePlanScratch* sc
             }
             sc->at[k].tau = tau;
             sc->at[k].blk = int(left);
+            sc->at[k].r = r;
             sc->at[k].b = b;
             break;
         }
@@ -271,7 +306,7 @@ __device__ __forceinline__ TreeWalk tree_start(const TreeArgs& a, const TreePlan
     if (w.b < 0)
         w.end = w.unit;
     else
-        w.r = tree_request(a, w.b);
+        w.r = sc->at[k].r;
     if (write) {
         TreeSplit s{};
         const long long begin = w.unit - w.blk, prev = w.unit - w.W;
@@ -308,10 +343,11 @@ __device__ __forceinline__ uint32_t tree_allow(const TreeArgs& a, const TreeReq&
 
 // q row (and o row) index of row `row` of a segment, or -1.
 __device__ __forceinline__ long long tree_row(const TreeArgs& a, int row0, int nodes, int hh, int row) {
-    const int tile = row / a.tile_rows, x = row % a.tile_rows;
-    const int node = tile * a.npt + x / a.hpt, h = (hh % a.hs) * a.hpt + x % a.hpt;
+    const int tile = row >> a.tile_shift, x = row - (tile << a.tile_shift);
+    const int y = a.by_hpt.div(x), kvh = a.by_hs.div(hh);
+    const int node = tile * a.npt + y, h = (hh - kvh * a.hs) * a.hpt + x - y * a.hpt;
     if (x >= a.npt * a.hpt || node >= nodes || h >= a.group) return -1;
-    return (long long)(row0 + node) * a.num_qo_heads + hh / a.hs * a.group + h;
+    return (long long)(row0 + node) * a.num_qo_heads + kvh * a.group + h;
 }
 
 constexpr int kMergeBlocks = 4;  // blocks per possible split
@@ -325,7 +361,7 @@ __global__ void __launch_bounds__(256) tree_merge_kernel(const TreeArgs a) {
     const TreeSplit s = a.splits[blockIdx.x / kMergeBlocks + 1];
     if (s.parts == 0) return;
     for (int i = int(blockIdx.x % kMergeBlocks) * 8 + (threadIdx.x >> 5); i < s.nodes * a.hpt; i += 8 * kMergeBlocks) {
-        const int per_tile = a.npt * a.hpt, row = i / per_tile * a.tile_rows + i % per_tile;
+        const int per_tile = a.npt * a.hpt, tile = i / per_tile, row = (tile << a.tile_shift) + i - tile * per_tile;
         const long long at = tree_row(a, s.row0, s.nodes, s.hh, row);
         if (at < 0) continue;  // past the group's last head
         auto slot = [&](int p) { return size_t(p == 0 ? s.slot0 : 2 * (s.c0 + p)) * a.seg_rows + row; };
@@ -401,16 +437,16 @@ __global__ void __launch_bounds__(128, CfgTreeCc<D>::kBlocksPerSm) tree_cc_kerne
             *reinterpret_cast<float4*>(sq + row * C::kLd + e) = make_float4(f[0], f[1], f[2], f[3]);
         }
         float m[2] = {kNegInf, kNegInf}, l[2] = {}, o[2][D / 8] = {};
-        const int node[2] = {s.node0 + 2 * tr / a.hpt, s.node0 + (2 * tr + 1) / a.hpt};
+        const int node[2] = {s.node0 + a.by_hpt.div(2 * tr), s.node0 + a.by_hpt.div(2 * tr + 1)};
         for (int t0 = s.blk0 * C::kBlockTokens; t0 < min(s.blk1 * C::kBlockTokens, s.r.len); t0 += C::kKeys) {
             __syncthreads();
             if (tid < C::kKeys) {
                 const int t = t0 + tid;
                 long long off = -1;
                 if (t < s.r.len) {
-                    const int page = __ldg(a.indices + s.r.lo + t / a.page_size);
+                    const int nth = a.by_page.div(t), page = __ldg(a.indices + s.r.lo + nth);
                     if (page >= 0 && page < a.num_total_pages)
-                        off = (((long long)page * a.num_kv_heads + s.kvh) * a.page_size + t % a.page_size) * D;
+                        off = (((long long)page * a.num_kv_heads + s.kvh) * a.page_size + t - nth * a.page_size) * D;
                     else
                         atomicOr(a.flags, kFlagBadPage);
                 }

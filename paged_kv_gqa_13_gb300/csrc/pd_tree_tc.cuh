@@ -204,12 +204,7 @@ struct alignas(16) TcSeg {
     int hh, head0, kvh, lo;           // head tile, its first q head and kv head; first entry of indices
     int len, n, start, pad;           // the request: tokens, nodes, first q row
     __device__ __forceinline__ TreeReq req() const {
-        TreeReq r;
-        r.n = n;
-        r.start = start;
-        r.len = len;
-        r.lo = lo;
-        return r;
+        return TreeReq{n, start, len, lo, 0};
     }
 };
 
@@ -226,11 +221,12 @@ struct Ring {
     }
 };
 
-// Token of column col of block blk (col % slot_rows rows into its slot); -1 for a row past its page.
+// Token of column col of block blk; -1 for a row past its page.
 __device__ __forceinline__ int tree_token(const TreeArgs& a, int blk, int col) {
-    const int s = blk * a.spb + col / a.slot_rows;
-    const int row = s % a.cpp * a.slot_rows + col % a.slot_rows;
-    return row < a.page_size ? s / a.cpp * a.page_size + row : -1;
+    if (a.packed) return (((blk << a.spb_shift)) << a.slot_shift) + col;
+    const int s = (blk << a.spb_shift) + (col >> a.slot_shift), page = a.by_cpp.div(s);
+    const int row = ((s - page * a.cpp) << a.slot_shift) + col - (col >> a.slot_shift << a.slot_shift);
+    return row < a.page_size ? page * a.page_size + row : -1;
 }
 
 // ---------------------------------------------------------------- the kernel
@@ -454,15 +450,15 @@ __global__ void __launch_bounds__(CfgTree<D, kWide, kFp8>::kThreads, 1)
         bool ok = true;
         // one box per lane: slot_rows rows x 64 columns (codes: x head_dim columns)
         constexpr int kBoxes = kFp8 ? 1 : C::kHalves, kRowBytes = kFp8 ? D : 128;
-        const int sl = lane / kBoxes, hf = lane % kBoxes;
+        const int sl = lane / kBoxes, hf = lane % kBoxes, spb = 1 << a.spb_shift;
         auto load_block = [&](const TcSeg& s, int blk, const CUtensorMap* tm, bool is_k) -> bool {
             const bool mine = turn == me;
-            const int p = blk * a.spb + sl;
+            const int p = (blk << a.spb_shift) + sl;
             int page = a.num_total_pages, row = 0;  // page out of range: the copy fills zeros
             bool bad = false;
-            if (mine && sl < a.spb && p < s.slots) {
-                const int at = a.cpp > 1 ? p / a.cpp : p;
-                row = (p - at * a.cpp) * a.slot_rows;
+            if (mine && sl < spb && p < s.slots) {
+                const int at = a.by_cpp.div(p);
+                row = (p - at * a.cpp) << a.slot_shift;
                 page = __ldg(a.indices + s.lo + at);
                 bad = page < 0 || page >= a.num_total_pages;
                 if (bad) page = a.num_total_pages;
@@ -480,8 +476,8 @@ __global__ void __launch_bounds__(CfgTree<D, kWide, kFp8>::kThreads, 1)
                 }
                 if (lane == 0) mbar_arrive_expect_tx(bar(kPlaceFull + ring.slot), kPlaceBytes);
                 __syncwarp();
-                if (sl < a.spb)
-                    tma_load_4d(sbase + kPlaceOff + ring.slot * kPlaceBytes + hf * (C::kKeys * 128) + sl * a.slot_rows * kRowBytes,
+                if (sl < spb)
+                    tma_load_4d(sbase + kPlaceOff + ring.slot * kPlaceBytes + hf * (C::kKeys * 128) + (sl << a.slot_shift) * kRowBytes,
                                 tm, hf * 64, row, s.kvh, page, bar(kPlaceFull + ring.slot), s.n > a.nps ? again : once);
             }
             ++loads;
@@ -565,23 +561,41 @@ __global__ void __launch_bounds__(CfgTree<D, kWide, kFp8>::kThreads, 1)
                         const int at = 32 * me + lane, piece = at % kPerRow;
                         const bool guard = kv == 1 && blk >= s.tail0;
                         bool found = false;
-#pragma unroll 4
-                        for (int row = at / kPerRow; row < C::kKeys; row += kStep) {
-                            uint2 w = *reinterpret_cast<const uint2*>(from + row * D + piece * 8);
+                        const int row0 = at / kPerRow;
+                        // rounds of eight rows per lane: all loads, then the conversions and stores
+                        constexpr int kRound = C::kKeys / kStep < 8 ? C::kKeys / kStep : 8;
+                        const uint8_t* src = from + row0 * D + piece * 8;
+                        uint8_t* dst = to + piece / 8 * (C::kKeys * 128);
+#pragma unroll 1
+                        for (int r0 = row0; r0 < C::kKeys; r0 += kRound * kStep, src += kRound * kStep * D) {
+                            uint2 w[kRound];
+#pragma unroll
+                            for (int x = 0; x < kRound; ++x) w[x] = *reinterpret_cast<const uint2*>(src + x * kStep * D);
                             if (guard) {
-                                const int tok = tree_token(a, blk, row);
-                                if (tok < 0 || tok >= s.len) {
-                                    w = make_uint2(0u, 0u);
-                                } else if (tok >= s.len - s.n) {
-                                    const uint32_t nx = __vcmpeq4(w.x & 0x7f7f7f7fu, 0x7f7f7f7fu),
-                                                   ny = __vcmpeq4(w.y & 0x7f7f7f7fu, 0x7f7f7f7fu);
-                                    found |= (nx | ny) != 0u;
-                                    w = make_uint2(w.x & ~nx, w.y & ~ny);
+#pragma unroll 1
+                                for (int x = 0; x < kRound; ++x) {
+                                    const int tok = tree_token(a, blk, r0 + x * kStep);
+                                    uint32_t keep_x = ~0u, keep_y = ~0u;
+                                    if (tok < 0 || tok >= s.len) {
+                                        keep_x = keep_y = 0u;
+                                    } else if (tok >= s.len - s.n) {
+                                        const uint2 y = *reinterpret_cast<const uint2*>(src + x * kStep * D);
+                                        keep_x = ~__vcmpeq4(y.x & 0x7f7f7f7fu, 0x7f7f7f7fu);
+                                        keep_y = ~__vcmpeq4(y.y & 0x7f7f7f7fu, 0x7f7f7f7fu);
+                                        found |= (keep_x & keep_y) != ~0u;
+                                    }
+#pragma unroll
+                                    for (int z = 0; z < kRound; ++z)
+                                        if (z == x) w[z] = make_uint2(w[z].x & keep_x, w[z].y & keep_y);
                                 }
                             }
-                            *reinterpret_cast<uint4*>(to + piece / 8 * (C::kKeys * 128) + row * 128 + (((piece & 7) ^ (row & 7)) << 4)) =
-                                make_uint4(e4m3x2_to_f16x2(w.x), e4m3x2_to_f16x2(w.x >> 16), e4m3x2_to_f16x2(w.y),
-                                           e4m3x2_to_f16x2(w.y >> 16));
+#pragma unroll
+                            for (int x = 0; x < kRound; ++x) {
+                                const int row = r0 + x * kStep;
+                                *reinterpret_cast<uint4*>(dst + row * 128 + (((piece & 7) ^ (row & 7)) << 4)) =
+                                    make_uint4(e4m3x2_to_f16x2(w[x].x), e4m3x2_to_f16x2(w[x].x >> 16), e4m3x2_to_f16x2(w[x].y),
+                                               e4m3x2_to_f16x2(w[x].y >> 16));
+                            }
                         }
                         if (found) bad_v[i & 3] = i + 1;
                         fence_proxy_async_smem();
@@ -638,8 +652,8 @@ __global__ void __launch_bounds__(CfgTree<D, kWide, kFp8>::kThreads, 1)
         const uint32_t lanes = uint32_t(32 * (wid & 3)) << 16;
         const uint32_t to = tmem + lanes + pipe * D, ts0 = tmem + lanes + C::kSCol + pipe * 2 * C::kJobKeys;
         float scale = a.scale_log2 == 0.f ? 1e-38f : fabsf(a.scale_log2);
-        const int per_slot = a.slot_rows < 32 ? a.slot_rows : 32;
-        const bool packed = a.page_size % a.slot_rows == 0;
+        const int per_slot = min(1 << a.slot_shift, 32);
+        const bool packed = a.packed != 0;
         int jobs = 0, kblocks = 0;  // kblocks: K blocks before this segment
         bool ok = true;
         for (int seg = 0; ok; ++seg) {
@@ -648,7 +662,7 @@ __global__ void __launch_bounds__(CfgTree<D, kWide, kFp8>::kThreads, 1)
             const int blk0 = s.blk0, blk1 = s.blk1, tail0 = s.tail0;
             if (blk0 == blk1) break;
             const TreeReq r = s.req();
-            const int node = s.node0 + p * a.npt + row / a.hpt;
+            const int node = s.node0 + p * a.npt + a.by_hpt.div(row);
             const long long at = tree_row(a, s.row0, s.nodes, s.hh, row + p * C::kRows);
             const bool live = __any_sync(kFull, at >= 0);  // a warp without rows only keeps step
             float m = kNegInf, l = 0.f;
@@ -704,14 +718,15 @@ __global__ void __launch_bounds__(CfgTree<D, kWide, kFp8>::kThreads, 1)
                                 const int c0 = half * C::kJobKeys + c;
                                 uint32_t allow = 0;
                                 if (packed && bad_pages == 0u) {
-                                    allow = tree_allow(a, r, nd, (blk * a.spb) * a.slot_rows + c0, 32);
+                                    allow = tree_allow(a, r, nd, tree_token(a, blk, c0), 32);
                                 } else {
                                     for (int e = 0; e < 32; e += per_slot) {
-                                        const int col = c0 + e, q = blk * a.spb + col / a.slot_rows;
-                                        const int r0 = q % a.cpp * a.slot_rows + col % a.slot_rows;
+                                        const int col = c0 + e, x0 = col >> a.slot_shift, q = (blk << a.spb_shift) + x0;
+                                        const int page = a.by_cpp.div(q);
+                                        const int r0 = ((q - page * a.cpp) << a.slot_shift) + col - (x0 << a.slot_shift);
                                         const int count = min(per_slot, a.page_size - r0);
-                                        if ((bad_pages >> (col / a.slot_rows)) & 1u) continue;
-                                        allow |= tree_allow(a, r, nd, q / a.cpp * a.page_size + r0, count) << e;
+                                        if ((bad_pages >> x0) & 1u) continue;
+                                        allow |= tree_allow(a, r, nd, page * a.page_size + r0, count) << e;
                                     }
                                 }
 #pragma unroll
@@ -792,7 +807,7 @@ __global__ void __launch_bounds__(CfgTree<D, kWide, kFp8>::kThreads, 1)
                         // non-finite elements of the node rows in these blocks, for the rows that attend them
                         for (int i = 0; i < r.n; ++i) {
                             const int tok = r.ctx() + i;
-                            const int blk = (tree_slots(a, tok + 1) - 1) / a.spb;
+                            const int blk = tree_slot_of(a, tok) >> a.spb_shift;
                             if (blk < blk0 || blk >= blk1) continue;
                             if ((tree_allow(a, r, node, tok, 1) & 1u) == 0u) continue;
                             const int page = __ldg(a.indices + r.lo + tok / a.page_size);

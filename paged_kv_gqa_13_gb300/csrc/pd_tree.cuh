@@ -313,7 +313,8 @@ __device__ __forceinline__ TreeWalk tree_start(const TreeArgs& a, const TreePlan
         if (w.b >= 0 && w.blk > 0 && begin >= prev) {
             const long long stop = begin + tree_blocks(a, w.r, w.tau);
             s.c0 = w.worker - 1;
-            s.parts = int((stop - 1) / w.W) - s.c0 + 1;
+            const long long last = stop <= 0x7fffffffll ? unsigned(stop - 1) / unsigned(w.W) : (stop - 1) / w.W;
+            s.parts = int(last) - s.c0 + 1;
             s.slot0 = 2 * s.c0 + (begin > prev ? 1 : 0);
             s.hh = w.hh;
             s.row0 = w.r.start + w.tau * a.nps;

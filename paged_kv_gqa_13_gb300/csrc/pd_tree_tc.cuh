@@ -547,7 +547,7 @@ __global__ void __launch_bounds__(CfgTree<D, kWide, kFp8>::kThreads, 1)
             }
             if (!ok || !seg_wait(i)) break;
             const TcSeg& s = seg_at(i);
-            const int blk1 = s.blk1;
+            const int blk1 = s.blk1, tail0 = s.tail0, len = s.len, ctx = s.len - s.n;
             if (s.blk0 == blk1) break;
             for (int blk = s.blk0; blk < blk1; ++blk) {
                 if constexpr (kFp8) {
@@ -559,7 +559,7 @@ __global__ void __launch_bounds__(CfgTree<D, kWide, kFp8>::kThreads, 1)
                         uint8_t* to = smem + C::kRingOff + ring.slot * C::kSlotBytes;
                         constexpr int kPerRow = D / 8, kStep = 32 * C::kInspectors / kPerRow;  // lanes per row, rows per round
                         const int at = 32 * me + lane, piece = at % kPerRow;
-                        const bool guard = kv == 1 && blk >= s.tail0;
+                        const bool guard = kv == 1 && blk >= tail0;
                         bool found = false;
                         const int row0 = at / kPerRow;
                         // rounds of eight rows per lane: all loads, then the conversions and stores
@@ -572,21 +572,15 @@ __global__ void __launch_bounds__(CfgTree<D, kWide, kFp8>::kThreads, 1)
 #pragma unroll
                             for (int x = 0; x < kRound; ++x) w[x] = *reinterpret_cast<const uint2*>(src + x * kStep * D);
                             if (guard) {
-#pragma unroll 1
+#pragma unroll
                                 for (int x = 0; x < kRound; ++x) {
                                     const int tok = tree_token(a, blk, r0 + x * kStep);
-                                    uint32_t keep_x = ~0u, keep_y = ~0u;
-                                    if (tok < 0 || tok >= s.len) {
-                                        keep_x = keep_y = 0u;
-                                    } else if (tok >= s.len - s.n) {
-                                        const uint2 y = *reinterpret_cast<const uint2*>(src + x * kStep * D);
-                                        keep_x = ~__vcmpeq4(y.x & 0x7f7f7f7fu, 0x7f7f7f7fu);
-                                        keep_y = ~__vcmpeq4(y.y & 0x7f7f7f7fu, 0x7f7f7f7fu);
-                                        found |= (keep_x & keep_y) != ~0u;
-                                    }
-#pragma unroll
-                                    for (int z = 0; z < kRound; ++z)
-                                        if (z == x) w[z] = make_uint2(w[z].x & keep_x, w[z].y & keep_y);
+                                    const uint32_t nx = __vcmpeq4(w[x].x & 0x7f7f7f7fu, 0x7f7f7f7fu),
+                                                   ny = __vcmpeq4(w[x].y & 0x7f7f7f7fu, 0x7f7f7f7fu);
+                                    const bool dead = tok < 0 || tok >= len, node = !dead && tok >= ctx;
+                                    found |= node && (nx | ny) != 0u;
+                                    if (dead) w[x] = make_uint2(0u, 0u);
+                                    if (node) w[x] = make_uint2(w[x].x & ~nx, w[x].y & ~ny);
                                 }
                             }
 #pragma unroll
@@ -611,12 +605,12 @@ __global__ void __launch_bounds__(CfgTree<D, kWide, kFp8>::kThreads, 1)
                     if (lane == 0) mbar_arrive(bar(C::kEmpty + ring.slot));  // K
                     ring.next();
                     if (!(ok = wait(C::kFull + ring.slot, ring.phase))) break;
-                    if (blk >= s.tail0) {
+                    if (blk >= tail0) {
                         uint8_t* vb = smem + C::kRingOff + ring.slot * C::kSlotBytes;
                         bool found = false;
                         for (int row = 32 * me + lane; row < C::kKeys; row += 32 * C::kInspectors) {
                             const int tok = tree_token(a, blk, row);
-                            const bool dead = tok < 0 || tok >= s.len, node = tok >= s.len - s.n;
+                            const bool dead = tok < 0 || tok >= len, node = tok >= ctx;
                             if (!dead && !node) continue;
                             for (int hf = 0; hf < C::kHalves; ++hf) {
 #pragma unroll
@@ -672,26 +666,40 @@ __global__ void __launch_bounds__(CfgTree<D, kWide, kFp8>::kThreads, 1)
                 // operand tile: the last S of the segment before has been read, so the tile is free.
                 const float ks = a.scale_log2 * __ldg(a.k_scale + s.kvh);
                 const uint4* qr = reinterpret_cast<const uint4*>(static_cast<const T*>(a.q) + (at < 0 ? 0 : at) * D);
+                // chunks of 64 elements; the first stays in registers between its maximum and its store
+                constexpr int kHold = 8;
+                uint4 w[kHold];
                 float big = 0.f;
-#pragma unroll 4
-                for (int c = 0; c < D / 8; ++c) {
-                    float f[8];
-                    Elt<T>::to_f32(__ldg(qr + c), f);
+#pragma unroll 1
+                for (int c0 = D / 8 - kHold; c0 >= 0; c0 -= kHold) {
 #pragma unroll
-                    for (int e = 0; e < 8; ++e) big = fmaxf(big, fabsf(f[e]));
+                    for (int c = 0; c < kHold; ++c) w[c] = __ldg(qr + c0 + c);
+#pragma unroll
+                    for (int c = 0; c < kHold; ++c) {
+                        float f[8];
+                        Elt<T>::to_f32(w[c], f);
+#pragma unroll
+                        for (int e = 0; e < 8; ++e) big = fmaxf(big, fabsf(f[e]));
+                    }
                 }
                 int up = 0;
                 if (!std::is_same<T, __half>::value && big > 0.f) up = max(-126, min(126, 141 - int(__float_as_uint(big) >> 23)));
-                const float by = __uint_as_float(uint32_t(127 + up) << 23) * (ks < 0.f ? -1.f : 1.f);
+                const float by = at < 0 ? 0.f : __uint_as_float(uint32_t(127 + up) << 23) * (ks < 0.f ? -1.f : 1.f);
                 uint8_t* tile = smem + p * C::kQBytes;
-#pragma unroll 4
-                for (int c = 0; c < D / 8; ++c) {
-                    float f[8];
-                    Elt<T>::to_f32(__ldg(qr + c), f);
+#pragma unroll 1
+                for (int c0 = 0; c0 < D / 8; c0 += kHold) {
+                    if (c0 > 0)
 #pragma unroll
-                    for (int e = 0; e < 8; ++e) f[e] = at < 0 ? 0.f : f[e] * by;
-                    *reinterpret_cast<uint4*>(tile + c / 8 * (C::kRows * 128) + row * 128 + (((c & 7) ^ (row & 7)) << 4)) =
-                        Elt<__half>::from_f32(f);
+                        for (int c = 0; c < kHold; ++c) w[c] = __ldg(qr + c0 + c);
+#pragma unroll
+                    for (int c = 0; c < kHold; ++c) {
+                        float f[8];
+                        Elt<T>::to_f32(w[c], f);
+#pragma unroll
+                        for (int e = 0; e < 8; ++e) f[e] *= by;
+                        *reinterpret_cast<uint4*>(tile + (c0 + c) / 8 * (C::kRows * 128) + row * 128 + ((((c0 + c) & 7) ^ (row & 7)) << 4)) =
+                            Elt<__half>::from_f32(f);
+                    }
                 }
                 scale = ks == 0.f ? 1e-38f : fabsf(ks) * __uint_as_float(uint32_t(127 - up) << 23);
                 fence_proxy_async_smem();
@@ -734,10 +742,12 @@ __global__ void __launch_bounds__(CfgTree<D, kWide, kFp8>::kThreads, 1)
                                     if (((allow >> e) & 1u) == 0u) x[c + e] = __float_as_uint(kNegInf);
                             }
                         }
-                        float top = __uint_as_float(x[0]);
+                        float tops[4];
 #pragma unroll
-                        for (int c = 1; c < C::kJobKeys; ++c) top = fmaxf(top, __uint_as_float(x[c]));
-                        top *= scale;
+                        for (int c = 0; c < 4; ++c) tops[c] = __uint_as_float(x[c]);
+#pragma unroll
+                        for (int c = 4; c < C::kJobKeys; ++c) tops[c % 4] = fmaxf(tops[c % 4], __uint_as_float(x[c]));
+                        const float top = fmaxf(fmaxf(tops[0], tops[1]), fmaxf(tops[2], tops[3])) * scale;
                         if (blk == blk0 && half == 0) {
                             m = top;
                         } else {
@@ -763,7 +773,7 @@ __global__ void __launch_bounds__(CfgTree<D, kWide, kFp8>::kThreads, 1)
                             }
                         }
                         const float mu = m == kNegInf ? 0.f : m;
-                        float2 sum = make_float2(0.f, 0.f);
+                        float2 sums[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
                         const float2 sc2 = make_float2(scale, scale), mu2 = make_float2(-mu, -mu);
                         uint32_t w[C::kJobKeys / 2];
 #pragma unroll
@@ -771,11 +781,12 @@ __global__ void __launch_bounds__(CfgTree<D, kWide, kFp8>::kThreads, 1)
                             float2 y = make_float2(__uint_as_float(x[2 * e]), __uint_as_float(x[2 * e + 1]));
                             y = __ffma2_rn(y, sc2, mu2);
                             y = make_float2(ex2(y.x), ex2(y.y));
-                            sum = __fadd2_rn(sum, y);
+                            sums[e % 2] = __fadd2_rn(sums[e % 2], y);
                             w[e] = Elt<M>::pack(y.x, y.y);
                         }
                         tmem_st32(ts, w);
-                        l += sum.x + sum.y;
+                        sums[0] = __fadd2_rn(sums[0], sums[1]);
+                        l += sums[0].x + sums[0].y;
                         tmem_wait_st();
                         tc_fence_before();
                     }

@@ -69,21 +69,31 @@ __host__ __device__ constexpr uint32_t tc_idesc_f16(bool bf16, int M, int N, boo
 }
 constexpr uint32_t kIdescNegA = 1u << 13;
 
+// The tcgen05 instructions of an mma warp: the whole warp runs its code, so
+// that descriptors stay in uniform registers, and lane 0 (`lead`) issues.
 // D = A * B (+ D when acc), A and B from shared memory.
-__device__ __forceinline__ void tc_mma_f16(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, bool acc) {
+__device__ __forceinline__ void tc_mma_f16(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, bool acc, bool lead) {
     asm volatile(
-        "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
-        "tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
-        "l"(a), "l"(b), "r"(idesc), "r"(uint32_t(acc))
+        "{\n\t.reg .pred p, q;\n\tsetp.ne.b32 p, %4, 0;\n\tsetp.ne.b32 q, %5, 0;\n\t"
+        "@q tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
+        "l"(a), "l"(b), "r"(idesc), "r"(uint32_t(acc)), "r"(uint32_t(lead))
         : "memory");
 }
 
 // The same with A in tensor memory (two 16-bit elements per column).
-__device__ __forceinline__ void tc_mma_f16_ta(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, bool acc) {
+__device__ __forceinline__ void tc_mma_f16_ta(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, bool acc, bool lead) {
     asm volatile(
-        "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
-        "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d),
-        "r"(a), "l"(b), "r"(idesc), "r"(uint32_t(acc))
+        "{\n\t.reg .pred p, q;\n\tsetp.ne.b32 p, %4, 0;\n\tsetp.ne.b32 q, %5, 0;\n\t"
+        "@q tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d),
+        "r"(a), "l"(b), "r"(idesc), "r"(uint32_t(acc)), "r"(uint32_t(lead))
+        : "memory");
+}
+
+__device__ __forceinline__ void tc_commit_if(uint32_t bar, bool lead) {
+    asm volatile(
+        "{\n\t.reg .pred q;\n\tsetp.ne.b32 q, %1, 0;\n\t"
+        "@q tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n\t}" ::"r"(bar),
+        "r"(uint32_t(lead))
         : "memory");
 }
 
@@ -241,7 +251,7 @@ __global__ void __launch_bounds__(CfgTree<D, kWide, kFp8>::kThreads, 1)
     const float kNegInf = -__int_as_float(0x7f800000);
     extern __shared__ __align__(16) uint8_t tree_tc_smem[];
     uint8_t* base = tree_tc_smem + ((1024u - (smem_u32(tree_tc_smem) & 1023u)) & 1023u);
-    const int tid = threadIdx.x, lane = tid & 31, wid = tid >> 5;
+    const int tid = threadIdx.x, lane = tid & 31, wid = __shfl_sync(kFull, tid >> 5, 0);
     // role: softmax warps first; then each line's mma, producers and inspectors
     const bool soft = wid < C::kSoftWarps;
     const int rest = wid - C::kSoftWarps;
@@ -306,7 +316,7 @@ __global__ void __launch_bounds__(CfgTree<D, kWide, kFp8>::kThreads, 1)
     launch_dependents();
     const uint32_t tmem = *tslot;
 
-    auto wait1 = [&](int b, uint32_t phase) { return tree_wait(bar(b), phase, abort_flag, a.flags); };
+    auto test = [&](int b, uint32_t phase) { return __all_sync(kFull, mbar_test_wait(bar(b), phase)) != 0; };
     auto wait = [&](int b, uint32_t phase) { return tree_wait_warp(bar(b), phase, abort_flag, a.flags); };
     // Segment i, waiting for it, and giving it back.
     auto seg_at = [&](int i) -> const TcSeg& { return segs[i % C::kSegRing]; };
@@ -320,7 +330,8 @@ __global__ void __launch_bounds__(CfgTree<D, kWide, kFp8>::kThreads, 1)
     if (idle) {
     } else if (!soft && part < C::kPipes) {
         // ================================================================ mma of pipeline `part`
-        if (lane == 0) {
+        {
+            const bool lead = lane == 0;
             const uint32_t idesc_s = tc_idesc_f16(kBf16, C::kRows, C::kJobKeys, false) | (!kFp8 && a.scale_log2 < 0.f ? kIdescNegA : 0u);
             constexpr uint32_t idesc_o = tc_idesc_f16(kBf16, C::kRows, D, true);
             // operand descriptors of slot 0 (K K-major, V MN-major) and of the row tile's q; addresses count 16 bytes
@@ -337,7 +348,7 @@ __global__ void __launch_bounds__(CfgTree<D, kWide, kFp8>::kThreads, 1)
             bool first = false;
             auto land = [&](int* slot) {
                 *slot = ring.slot;
-                const bool ok = wait1(C::kFull + ring.slot, ring.phase);
+                const bool ok = wait(C::kFull + ring.slot, ring.phase);
                 ring.next();
                 return ok;
             };
@@ -345,13 +356,13 @@ __global__ void __launch_bounds__(CfgTree<D, kWide, kFp8>::kThreads, 1)
             auto advance = [&]() -> int {
                 if (++blk >= blk1) {
                     ++seg;
-                    if (!wait1(C::kSegFull + seg % C::kSegRing, seg_phase(seg))) return -1;
+                    if (!wait(C::kSegFull + seg % C::kSegRing, seg_phase(seg))) return -1;
                     const TcSeg& s = seg_at(seg);
                     if (s.blk0 == s.blk1) return 0;
                     blk = s.blk0;
                     blk1 = s.blk1;
                     tail0 = s.tail0;
-                    if (!wait1(C::kQFull + part, uint32_t(seg) & 1u)) return -1;
+                    if (!wait(C::kQFull + part, uint32_t(seg) & 1u)) return -1;
                     first = true;
                 }
                 return land(&kslot) ? 1 : -1;
@@ -360,11 +371,11 @@ __global__ void __launch_bounds__(CfgTree<D, kWide, kFp8>::kThreads, 1)
             auto ready = [&]() {
                 if (blk + 1 >= blk1) {
                     const int i = seg + 1;
-                    if (!mbar_test_wait(bar(C::kSegFull + i % C::kSegRing), seg_phase(i))) return false;
+                    if (!test(C::kSegFull + i % C::kSegRing, seg_phase(i))) return false;
                     if (seg_at(i).blk0 == seg_at(i).blk1) return true;
-                    if (!mbar_test_wait(bar(C::kQFull + part), uint32_t(i) & 1u)) return false;
+                    if (!test(C::kQFull + part, uint32_t(i) & 1u)) return false;
                 }
-                return mbar_test_wait(bar(C::kFull + ring.slot), ring.phase);
+                return test(C::kFull + ring.slot, ring.phase);
             };
             auto issue_s = [&](int half) {
                 tc_fence_after();
@@ -373,13 +384,13 @@ __global__ void __launch_bounds__(CfgTree<D, kWide, kFp8>::kThreads, 1)
 #pragma unroll
                 for (int k = 0; k < D / 16; ++k)
                     tc_mma_f16(d, qb + ((k / 4) * (C::kRows * 128) + (k % 4) * 32) / 16,
-                               kb + ((k / 4) * (C::kKeys * 128) + (k % 4) * 32) / 16, idesc_s, k > 0);
-                tc_commit(bar(C::kSFull + 2 * part + (n_qk & 1)));
+                               kb + ((k / 4) * (C::kKeys * 128) + (k % 4) * 32) / 16, idesc_s, k > 0, lead);
+                tc_commit_if(bar(C::kSFull + 2 * part + (n_qk & 1)), lead);
                 if (half == C::kJobs - 1) {
-                    tc_commit(bar(C::kEmpty + kslot));
+                    tc_commit_if(bar(C::kEmpty + kslot), lead);
                     if (blk + 1 == blk1) {  // the segment's last S
-                        if (!kFp8) tc_commit(bar(C::kQEmpty + part));
-                        mbar_arrive(bar(C::kSegFree + seg % C::kSegRing));
+                        if (!kFp8) tc_commit_if(bar(C::kQEmpty + part), lead);
+                        if (lead) mbar_arrive(bar(C::kSegFree + seg % C::kSegRing));
                     }
                 }
                 ++n_qk;
@@ -390,12 +401,13 @@ __global__ void __launch_bounds__(CfgTree<D, kWide, kFp8>::kThreads, 1)
                 int vs;
                 const bool tail = blk >= tail0, fresh = first;
                 first = false;
+                bool ok = true;
+                if (C::kJobs > 1) issue_s(1);
                 if (!land(&vs)) break;
                 if (!kFp8 && tail) {
-                    if (!wait1(C::kVok + vs, (vok >> vs) & 1u)) break;
+                    if (!wait(C::kVok + vs, (vok >> vs) & 1u)) break;
                     vok ^= 1u << vs;
                 }
-                bool ok = true;
 #pragma unroll
                 for (int half = 0; half < C::kJobs; ++half) {
                     const int buf = n_pv & 1;
@@ -403,12 +415,9 @@ __global__ void __launch_bounds__(CfgTree<D, kWide, kFp8>::kThreads, 1)
                     const uint32_t phase = uint32_t(n_pv >> 1) & 1u;
                     bool moved = true;
                     // The next job's S before this job's P V, unless its K comes later than this job's weights.
-                    if (half + 1 < C::kJobs) {
-                        issue_s(half + 1);
-                    } else {
+                    if (half + 1 == C::kJobs) {
                         const long long t0 = clock64();
-                        while (!(moved = ready()) && !mbar_test_wait(bar(pfull), phase) && !*abort_flag &&
-                               clock64() - t0 < kWaitCycles) {
+                        while (!(moved = ready()) && !test(pfull, phase) && !__any_sync(kFull, *abort_flag != 0 || clock64() - t0 > kWaitCycles)) {
                         }
                         if (moved && (more = advance()) == 1) issue_s(0);
                         if (more < 0) {
@@ -416,7 +425,7 @@ __global__ void __launch_bounds__(CfgTree<D, kWide, kFp8>::kThreads, 1)
                             break;
                         }
                     }
-                    if (!wait1(pfull, phase)) {
+                    if (!wait(pfull, phase)) {
                         ok = false;
                         break;
                     }
@@ -425,16 +434,16 @@ __global__ void __launch_bounds__(CfgTree<D, kWide, kFp8>::kThreads, 1)
 #pragma unroll
                     for (int k = 0; k < C::kJobKeys / 16; ++k)
                         tc_mma_f16_ta(o_cols, s_cols + buf * C::kJobKeys + 8 * k, vb + k * 128, idesc_o,
-                                      !fresh || half > 0 || k > 0);
-                    tc_commit(bar(C::kPvDone + 2 * part + buf));
-                    if (half == C::kJobs - 1) tc_commit(bar(C::kEmpty + vs));
+                                      !fresh || half > 0 || k > 0, lead);
+                    tc_commit_if(bar(C::kPvDone + 2 * part + buf), lead);
+                    if (half == C::kJobs - 1) tc_commit_if(bar(C::kEmpty + vs), lead);
                     ++n_pv;
                     if (!moved && (more = advance()) == 1) issue_s(0);
                 }
                 if (!ok) break;
             }
             // every mma has completed before the tensor memory is released
-            tc_commit(bar(C::kAllDone + part));
+            tc_commit_if(bar(C::kAllDone + part), lead);
             mbar_wait_bounded(bar(C::kAllDone + part), 0u);
         }
     } else if (!soft && part < C::kPipes + C::kProducers) {

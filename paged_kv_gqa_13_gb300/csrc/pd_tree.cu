@@ -65,8 +65,7 @@ pd_status encode(CUtensorMap* map, CUtensorMapDataType ty, int rank, const void*
 }
 
 // Boxes: of q {64 columns, heads of a tile, nodes of a row tile}; of K and V {64
-// columns, rows of a slot}, of codes {head_dim columns, rows of a slot}. E4M3
-// pools: the kernel reads q itself.
+// columns, rows of a slot}, of codes {head_dim columns, rows of a slot}.
 pd_status make_maps(const TreeArgs& a, pd_dtype dt, bool fp8, int D, CUtensorMap* q, CUtensorMap* k, CUtensorMap* v) {
     const CUtensorMapDataType qt = dt == PD_BF16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16;
     const CUtensorMapDataType kt = fp8 ? CU_TENSOR_MAP_DATA_TYPE_UINT8 : qt;
@@ -76,7 +75,7 @@ pd_status make_maps(const TreeArgs& a, pd_dtype dt, bool fp8, int D, CUtensorMap
     const cuuint32_t kb[4] = {fp8 ? cuuint32_t(D) : 64u, 1u << a.slot_shift, 1, 1};
     pd_status st = encode(k, kt, 4, a.k, kd, ks, kb);
     if (st == PD_OK) st = encode(v, kt, 4, a.v, kd, ks, kb);
-    if (st != PD_OK || fp8) return st;
+    if (st != PD_OK) return st;
     const cuuint64_t qd[3] = {d, hq, cuuint64_t(a.total_new)}, qs[2] = {d * 2, hq * d * 2};
     const cuuint32_t qb[3] = {64, cuuint32_t(a.hpt), cuuint32_t(a.npt)};
     return encode(q, qt, 3, a.q, qd, qs, qb);

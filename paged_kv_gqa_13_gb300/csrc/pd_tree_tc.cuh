@@ -155,6 +155,13 @@ __device__ __forceinline__ bool tree_wait_warp(uint32_t bar, uint32_t parity, vo
     return __all_sync(kFull, tree_wait(bar, parity, abort_flag, flags));
 }
 
+// 32 bytes at once: a thread that owns a row writes whole sectors.
+__device__ __forceinline__ void store32(void* p, const uint32_t (&r)[8]) {
+    asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(p), "r"(r[0]), "r"(r[1]), "r"(r[2]),
+                 "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7])
+                 : "memory");
+}
+
 // ---------------------------------------------------------------- configuration
 
 // Lines are independent: each walks a range of work of its own through a ring
@@ -185,7 +192,7 @@ struct CfgTree {
     static constexpr int kBadRing = 16;  // more than the K blocks that the producers are ahead of the softmax warps
     // a line's barriers (8 bytes each); those of S buffer b of pipeline p at 2 p + b
     static constexpr int kFull = 0, kEmpty = kFull + kSlots, kVok = kEmpty + kSlots, kQFull = kVok + kSlots,
-                         kQEmpty = kQFull + kPipes, kSFull = kQEmpty + kPipes, kPFull = kSFull + 2 * kPipes,
+                         kQEmpty = kQFull + kPipes, kQRaw = kQEmpty + kPipes, kSFull = kQRaw + kPipes, kPFull = kSFull + 2 * kPipes,
                          kPvDone = kPFull + 2 * kPipes, kAllDone = kPvDone + 2 * kPipes, kSegFull = kAllDone + kPipes,
                          kSegFree = kSegFull + kSegRing, kStFull = kSegFree + kSegRing, kStEmpty = kStFull + kStages,
                          kBars = kStEmpty + kStages;
@@ -255,7 +262,9 @@ __global__ void __launch_bounds__(CfgTree<D, kWide, kFp8>::kThreads, 1)
     // role: softmax warps first; then each line's mma, producers and inspectors
     const bool soft = wid < C::kSoftWarps;
     const int rest = wid - C::kSoftWarps;
-    const int line = soft ? wid / (4 * C::kPipes) : rest / C::kOthers, part = soft ? 0 : rest % C::kOthers;
+    const int line = soft ? wid / (4 * C::kPipes) : rest / C::kOthers;
+    // (E4M3 pools: the first line's converters come first, so that both lines' spread over all four schedulers)
+    const int part = soft ? 0 : kFp8 && C::kLines == 2 && line == 0 ? (rest + 2) % C::kOthers : rest % C::kOthers;
     const bool idle = line >= C::kLines;
     uint8_t* smem = base + (idle ? 0 : line) * C::kLineBytes;
     uint8_t* ctl = base + C::kCtlOff + (idle ? 0 : line) * C::kCtlBytes;
@@ -283,6 +292,7 @@ __global__ void __launch_bounds__(CfgTree<D, kWide, kFp8>::kThreads, 1)
             for (int i = 0; i < C::kPipes; ++i) {
                 mbar_init(bar(C::kQFull + i), kFp8 ? 4 : 1);
                 mbar_init(bar(C::kQEmpty + i), 1);
+                mbar_init(bar(C::kQRaw + i), 1);
                 mbar_init(bar(C::kAllDone + i), 1);
             }
             for (int i = 0; i < 2 * C::kPipes; ++i) {
@@ -301,8 +311,8 @@ __global__ void __launch_bounds__(CfgTree<D, kWide, kFp8>::kThreads, 1)
         __syncwarp();
         if (line == 0) tmem_alloc(smem_u32(tslot), 512);
     }
-    if (wid == C::kSoftWarps + C::kPipes && lane == 0) {
-        if (!kFp8) prefetch_tensormap(&tmq);
+    if (!soft && line == 0 && part == C::kPipes && lane == 0) {
+        prefetch_tensormap(&tmq);
         prefetch_tensormap(&tmk);
         prefetch_tensormap(&tmv);
     }
@@ -389,7 +399,7 @@ __global__ void __launch_bounds__(CfgTree<D, kWide, kFp8>::kThreads, 1)
                 if (half == C::kJobs - 1) {
                     tc_commit_if(bar(C::kEmpty + kslot), lead);
                     if (blk + 1 == blk1) {  // the segment's last S
-                        if (!kFp8) tc_commit_if(bar(C::kQEmpty + part), lead);
+                        tc_commit_if(bar(C::kQEmpty + part), lead);
                         if (lead) mbar_arrive(bar(C::kSegFree + seg % C::kSegRing));
                     }
                 }
@@ -453,7 +463,7 @@ __global__ void __launch_bounds__(CfgTree<D, kWide, kFp8>::kThreads, 1)
         // the ring that the copies land in: operand slots, or stages of codes
         constexpr int kPlaces = kFp8 ? C::kStages : C::kSlots, kPlaceFull = kFp8 ? C::kStFull : C::kFull,
                       kPlaceEmpty = kFp8 ? C::kStEmpty : C::kEmpty, kPlaceOff = kFp8 ? C::kStageOff : C::kRingOff,
-                      kPlaceBytes = kFp8 ? C::kStageBytes : C::kSlotBytes;
+                      kPlaceBytes = kFp8 ? C::kStageBytes : C::kSlotBytes, kQLanded = kFp8 ? C::kQRaw : C::kQFull;
         Ring<kPlaces> ring;
         int loads = 0, segments = 0, kblocks = 0, turn = 0;  // turn: the producer whose load is next
         bool ok = true;
@@ -499,15 +509,15 @@ __global__ void __launch_bounds__(CfgTree<D, kWide, kFp8>::kThreads, 1)
             const TcSeg& s = seg_at(segments);
             const int blk0 = s.blk0, blk1 = s.blk1;
             if (blk0 == blk1) break;
-            for (int p = 0; !kFp8 && me == 0 && p < C::kPipes && ok; ++p) {
+            for (int p = 0; me == 0 && p < C::kPipes && ok; ++p) {
                 // a row tile past the segment's nodes is loaded like another (rows of other requests, or zeros) and not used
                 ok = segments == 0 || wait(C::kQEmpty + p, uint32_t(segments - 1) & 1u);
                 if (!ok) break;
                 if (lane == 0) {
-                    mbar_arrive_expect_tx(bar(C::kQFull + p), uint32_t(a.npt * a.hpt) * D * 2);
+                    mbar_arrive_expect_tx(bar(kQLanded + p), uint32_t(a.npt * a.hpt) * D * 2);
                     for (int h = 0; h < C::kHalves; ++h)
                         tma_load_3d(sbase + p * C::kQBytes + h * (C::kRows * 128), &tmq, h * 64, s.head0, s.row0 + p * a.npt,
-                                    bar(C::kQFull + p));
+                                    bar(kQLanded + p));
                 }
                 __syncwarp();
             }
@@ -518,8 +528,8 @@ __global__ void __launch_bounds__(CfgTree<D, kWide, kFp8>::kThreads, 1)
         // copies issued last may still be landing when another role has stopped early
         for (int i = max(0, loads - kPlaces); i < loads; ++i)
             mbar_wait_bounded(bar(kPlaceFull + i % kPlaces), uint32_t(i / kPlaces) & 1u);
-        if (!kFp8 && me == 0 && segments > 0)
-            for (int p = 0; p < C::kPipes; ++p) mbar_wait_bounded(bar(C::kQFull + p), uint32_t(segments - 1) & 1u);
+        if (me == 0 && segments > 0)
+            for (int p = 0; p < C::kPipes; ++p) mbar_wait_bounded(bar(kQLanded + p), uint32_t(segments - 1) & 1u);
     } else if (!soft) {
         // ================================================================ inspectors / converters; the first also walks the segments
         constexpr uint32_t kExp = kBf16 ? 0x7f807f80u : 0x7c007c00u;
@@ -574,9 +584,12 @@ __global__ void __launch_bounds__(CfgTree<D, kWide, kFp8>::kThreads, 1)
                         // rounds of eight rows per lane: all loads, then the conversions and stores
                         constexpr int kRound = C::kKeys / kStep < 8 ? C::kKeys / kStep : 8;
                         const uint8_t* src = from + row0 * D + piece * 8;
-                        uint8_t* dst = to + piece / 8 * (C::kKeys * 128);
+                        // row & 7 of the rows of a round: all the same, or (steps of four rows) in turn row0 and row0 + 4
+                        static_assert(kStep == 4 || kStep % 8 == 0, "rows of a round");
+                        uint8_t* dst = to + piece / 8 * (C::kKeys * 128) + row0 * 128;
+                        const uint32_t in_row = uint32_t(((piece & 7) ^ (row0 & 7)) << 4);
 #pragma unroll 1
-                        for (int r0 = row0; r0 < C::kKeys; r0 += kRound * kStep, src += kRound * kStep * D) {
+                        for (int r0 = row0; r0 < C::kKeys; r0 += kRound * kStep, src += kRound * kStep * D, dst += kRound * kStep * 128) {
                             uint2 w[kRound];
 #pragma unroll
                             for (int x = 0; x < kRound; ++x) w[x] = *reinterpret_cast<const uint2*>(src + x * kStep * D);
@@ -594,8 +607,7 @@ __global__ void __launch_bounds__(CfgTree<D, kWide, kFp8>::kThreads, 1)
                             }
 #pragma unroll
                             for (int x = 0; x < kRound; ++x) {
-                                const int row = r0 + x * kStep;
-                                *reinterpret_cast<uint4*>(dst + row * 128 + (((piece & 7) ^ (row & 7)) << 4)) =
+                                *reinterpret_cast<uint4*>(dst + x * kStep * 128 + (in_row ^ (kStep == 4 && x % 2 == 1 ? 64u : 0u))) =
                                     make_uint4(e4m3x2_to_f16x2(w[x].x), e4m3x2_to_f16x2(w[x].x >> 16), e4m3x2_to_f16x2(w[x].y),
                                                e4m3x2_to_f16x2(w[x].y >> 16));
                             }
@@ -656,7 +668,7 @@ __global__ void __launch_bounds__(CfgTree<D, kWide, kFp8>::kThreads, 1)
         const uint32_t to = tmem + lanes + pipe * D, ts0 = tmem + lanes + C::kSCol + pipe * 2 * C::kJobKeys;
         float scale = a.scale_log2 == 0.f ? 1e-38f : fabsf(a.scale_log2);
         const int per_slot = min(1 << a.slot_shift, 32);
-        const bool packed = a.packed != 0;
+        const bool packed = a.packed != 0, o_wide = (reinterpret_cast<uintptr_t>(a.o) & 31u) == 0;
         int jobs = 0, kblocks = 0;  // kblocks: K blocks before this segment
         bool ok = true;
         for (int seg = 0; ok; ++seg) {
@@ -670,45 +682,33 @@ __global__ void __launch_bounds__(CfgTree<D, kWide, kFp8>::kThreads, 1)
             const bool live = __any_sync(kFull, at >= 0);  // a warp without rows only keeps step
             float m = kNegInf, l = 0.f;
             if constexpr (kFp8) {
-                // This thread's q row as f16, times a power of two that brings its largest element near 2^14
-                // (exact but for elements more than 2^28 below it) and the sign of the score scale, into the
-                // operand tile: the last S of the segment before has been read, so the tile is free.
+                // This thread's q row, where the copy put it, as f16 times a power of two that brings its
+                // largest element near 2^14 (exact but for elements more than 2^28 below it) and the sign of
+                // the score scale.
                 const float ks = a.scale_log2 * __ldg(a.k_scale + s.kvh);
-                const uint4* qr = reinterpret_cast<const uint4*>(static_cast<const T*>(a.q) + (at < 0 ? 0 : at) * D);
-                // chunks of 64 elements; the first stays in registers between its maximum and its store
-                constexpr int kHold = 8;
-                uint4 w[kHold];
+                uint8_t* tile = smem + p * C::kQBytes + row * 128;
+                auto piece = [&](int c) { return reinterpret_cast<uint4*>(tile + c / 8 * (C::kRows * 128) + (((c & 7) ^ (row & 7)) << 4)); };
+                if (!(ok = wait(C::kQRaw + p, uint32_t(seg) & 1u))) break;
                 float big = 0.f;
-#pragma unroll 1
-                for (int c0 = D / 8 - kHold; c0 >= 0; c0 -= kHold) {
-#pragma unroll
-                    for (int c = 0; c < kHold; ++c) w[c] = __ldg(qr + c0 + c);
-#pragma unroll
-                    for (int c = 0; c < kHold; ++c) {
+                if (!std::is_same<T, __half>::value) {
+#pragma unroll 8
+                    for (int c = 0; c < D / 8; ++c) {
                         float f[8];
-                        Elt<T>::to_f32(w[c], f);
+                        Elt<T>::to_f32(*piece(c), f);
 #pragma unroll
                         for (int e = 0; e < 8; ++e) big = fmaxf(big, fabsf(f[e]));
                     }
                 }
                 int up = 0;
-                if (!std::is_same<T, __half>::value && big > 0.f) up = max(-126, min(126, 141 - int(__float_as_uint(big) >> 23)));
-                const float by = at < 0 ? 0.f : __uint_as_float(uint32_t(127 + up) << 23) * (ks < 0.f ? -1.f : 1.f);
-                uint8_t* tile = smem + p * C::kQBytes;
-#pragma unroll 1
-                for (int c0 = 0; c0 < D / 8; c0 += kHold) {
-                    if (c0 > 0)
+                if (big > 0.f) up = max(-126, min(126, 141 - int(__float_as_uint(big) >> 23)));
+                const float by = __uint_as_float(uint32_t(127 + up) << 23) * (ks < 0.f ? -1.f : 1.f);
+#pragma unroll 8
+                for (int c = 0; c < D / 8; ++c) {
+                    float f[8];
+                    Elt<T>::to_f32(*piece(c), f);
 #pragma unroll
-                        for (int c = 0; c < kHold; ++c) w[c] = __ldg(qr + c0 + c);
-#pragma unroll
-                    for (int c = 0; c < kHold; ++c) {
-                        float f[8];
-                        Elt<T>::to_f32(w[c], f);
-#pragma unroll
-                        for (int e = 0; e < 8; ++e) f[e] *= by;
-                        *reinterpret_cast<uint4*>(tile + (c0 + c) / 8 * (C::kRows * 128) + row * 128 + ((((c0 + c) & 7) ^ (row & 7)) << 4)) =
-                            Elt<__half>::from_f32(f);
-                    }
+                    for (int e = 0; e < 8; ++e) f[e] *= by;
+                    *piece(c) = Elt<__half>::from_f32(f);
                 }
                 scale = ks == 0.f ? 1e-38f : fabsf(ks) * __uint_as_float(uint32_t(127 - up) << 23);
                 fence_proxy_async_smem();
@@ -845,13 +845,27 @@ __global__ void __launch_bounds__(CfgTree<D, kWide, kFp8>::kThreads, 1)
                         }
                     }
                     if (s.slot >= 0) {
-                        float4* po = reinterpret_cast<float4*>(a.part_o + prow * D + c);
 #pragma unroll
-                        for (int e = 0; e < 8; ++e) po[e] = make_float4(f[4 * e], f[4 * e + 1], f[4 * e + 2], f[4 * e + 3]);
+                        for (int e = 0; e < 32; e += 8) {
+                            uint32_t v[8];
+#pragma unroll
+                            for (int x = 0; x < 8; ++x) v[x] = __float_as_uint(f[e + x]);
+                            store32(a.part_o + prow * D + c + e, v);
+                        }
                     } else {
-                        uint4* po = reinterpret_cast<uint4*>(static_cast<T*>(a.o) + at * D + c);
 #pragma unroll
-                        for (int e = 0; e < 4; ++e) po[e] = Elt<T>::from_f32(f + 8 * e);
+                        for (int e = 0; e < 32; e += 16) {
+                            uint32_t v[8];
+#pragma unroll
+                            for (int x = 0; x < 8; ++x) v[x] = Elt<T>::pack(f[e + 2 * x], f[e + 2 * x + 1]);
+                            T* po = static_cast<T*>(a.o) + at * D + c + e;
+                            if (o_wide) {
+                                store32(po, v);
+                            } else {
+                                reinterpret_cast<uint4*>(po)[0] = make_uint4(v[0], v[1], v[2], v[3]);
+                                reinterpret_cast<uint4*>(po)[1] = make_uint4(v[4], v[5], v[6], v[7]);
+                            }
+                        }
                     }
                 }
                 if (at >= 0) {
@@ -868,7 +882,7 @@ __global__ void __launch_bounds__(CfgTree<D, kWide, kFp8>::kThreads, 1)
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
-    if (wid == C::kSoftWarps) tmem_dealloc(tmem, 512);
+    if (!soft && line == 0 && part == 0) tmem_dealloc(tmem, 512);
 }
 
 // ---------------------------------------------------------------- lookup

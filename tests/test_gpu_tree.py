@@ -271,3 +271,39 @@ def test_pools_past_two_to_the_31_elements(dtype):
     pd.pd_paged_tree_commit(k, v, far.cuda(), p, l, n, path, torch.tensor([3], dtype=torch.int32, device="cuda"), ws)
     assert torch.equal(v[page[:3].cuda(), :, rr[:3].cuda()], rows[[1, 3, 6]])
     assert pd.pd_read_device_flags(ws) == 0
+
+
+@pytest.mark.parametrize("dtype,fp8", [("f32", False), ("f16", False), ("bf16", True)])
+def test_tensors_that_start_16_bytes_off(dtype, fp8):
+    """q and o need 16-byte alignment and no more."""
+    import paged_kv_gqa_13_gb300 as pd
+
+    c = Paged([300, 9], [3, 9], 2, 128, 16, dtype, fp8=fp8)
+    q = torch.randn(12, 4, 128).to(TYPES[dtype])
+    masks = [tree_bits(np.random.default_rng(0), n) for n in c.new]
+    off = 16 // q.element_size()
+    qd, o = (torch.empty(q.numel() + off, dtype=q.dtype, device="cuda")[off:].view(q.shape) for _ in range(2))
+    qd.copy_(q)
+    lse = torch.empty(12, 4, device="cuda")
+    code = {"f32": pd.PD_F32, "f16": pd.PD_F16, "bf16": pd.PD_BF16}[dtype]
+    ws = pd.alloc_workspace(pd.pd_paged_tree_decode_workspace_bytes(4, 2, 128, code))
+    scales = (c.k_scale.cuda(), c.v_scale.cuda()) if fp8 else ()
+    fn = pd.pd_paged_tree_decode_fp8 if fp8 else pd.pd_paged_tree_decode
+    fn(qd, c.k.cuda(), c.v.cuda(), *scales, *c.table(), pack(masks, 1).cuda(), o, lse, 0.1, ws)
+    check_tree(o, lse, tree_reference(c, q, masks, 0.1), dtype)
+
+
+@pytest.mark.parametrize("dtype", ["f16", "bf16"])
+@pytest.mark.parametrize("size", [1e-30, 3e4])
+def test_q_of_extreme_size_over_e4m3_pools(dtype, size):
+    """bf16 rows far outside the range of f16, and rows of zeros, keep their scores."""
+    if dtype == "f16" and size < 1e-7:
+        pytest.skip("not an f16 value")
+    c = Paged([300], [5], 2, 128, 16, dtype, fp8=True)
+    q = torch.randn(5, 4, 128).to(TYPES[dtype]) * size
+    q = q.clamp(-6e4, 6e4).to(TYPES[dtype])
+    q[2] = 0
+    masks = [tree_bits(np.random.default_rng(0), 5)]
+    scale = 0.1 / size
+    o, lse, _ = _run(c, q, masks, 1, scale, dtype)
+    check_tree(o, lse, tree_reference(c, q, masks, float(np.float32(scale))), dtype)

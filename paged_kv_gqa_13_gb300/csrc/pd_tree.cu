@@ -133,7 +133,7 @@ pd_status tree_impl(const void* q, const void* k_data, const void* v_data, const
     TreeKernels kn{};
     // More rows per request than a row tile holds: segments of two row tiles, which
     // read K and V once for both. Fewer: two independent halves of each CTA.
-    const bool wide = (long long)total_new * group > 128ll * batch;
+    const bool wide = (long long)total_new * group > 64ll * batch;
     if (!pick(dt, fp8, D, group, wide, &kn)) return host::fail(PD_ERR_UNSUPPORTED, "no kernel for this type and head_dim");
     int sms = 0;
     if ((st = host::sm_count(&sms)) != PD_OK) return st;

@@ -290,10 +290,9 @@ __device__ __forceinline__ void tree_plan(const TreeArgs& a, TreePlanScratch* sc
     __syncthreads();
 }
 
-// The walk of worker k of this CTA; `write`: this thread leaves the merge's
-// descriptor of a segment that starts in the range before and reaches into this one.
+// The walk of worker k of this CTA.
 template <int kWorkers>
-__device__ __forceinline__ TreeWalk tree_start(const TreeArgs& a, const TreePlanScratch* sc, int k, bool write) {
+__device__ __forceinline__ TreeWalk tree_start(const TreePlanScratch* sc, int k) {
     TreeWalk w;
     w.worker = int(blockIdx.x) * kWorkers + k;
     w.W = sc->W;
@@ -303,26 +302,27 @@ __device__ __forceinline__ TreeWalk tree_start(const TreeArgs& a, const TreePlan
     w.hh = sc->at[k].hh;
     w.tau = sc->at[k].tau;
     w.blk = sc->at[k].blk;
-    if (w.b < 0)
-        w.end = w.unit;
-    else
-        w.r = sc->at[k].r;
-    if (write) {
-        TreeSplit s{};
-        const long long begin = w.unit - w.blk, prev = w.unit - w.W;
-        if (w.b >= 0 && w.blk > 0 && begin >= prev) {
-            const long long stop = begin + tree_blocks(a, w.r, w.tau);
-            s.c0 = w.worker - 1;
-            const long long last = stop <= 0x7fffffffll ? unsigned(stop - 1) / unsigned(w.W) : (stop - 1) / w.W;
-            s.parts = int(last) - s.c0 + 1;
-            s.slot0 = 2 * s.c0 + (begin > prev ? 1 : 0);
-            s.hh = w.hh;
-            s.row0 = w.r.start + w.tau * a.nps;
-            s.nodes = min(a.nps, w.r.n - w.tau * a.nps);
-        }
-        a.splits[w.worker] = s;
-    }
+    w.r = sc->at[k].r;
+    if (w.b < 0) w.end = w.unit;
     return w;
+}
+
+// The merge's descriptor of a segment that starts in the range before the
+// worker's and reaches into its own (w: the walk as it starts). One thread.
+__device__ __forceinline__ void tree_split(const TreeArgs& a, const TreeWalk& w) {
+    TreeSplit s{};
+    const long long begin = w.unit - w.blk, prev = w.unit - w.W;
+    if (w.b >= 0 && w.blk > 0 && begin >= prev) {
+        const long long stop = begin + tree_blocks(a, w.r, w.tau);
+        const long long last = stop <= 0x7fffffffll ? unsigned(stop - 1) / unsigned(w.W) : (stop - 1) / w.W;
+        s.c0 = w.worker - 1;
+        s.parts = int(last) - s.c0 + 1;
+        s.slot0 = 2 * s.c0 + (begin > prev ? 1 : 0);
+        s.hh = w.hh;
+        s.row0 = w.r.start + w.tau * a.nps;
+        s.nodes = min(a.nps, w.r.n - w.tau * a.nps);
+    }
+    a.splits[w.worker] = s;
 }
 
 // Which of 32 consecutive tokens t0 .. t0 + 31 (only the first `count` stand
@@ -423,7 +423,8 @@ __global__ void __launch_bounds__(128, CfgTreeCc<D>::kBlocksPerSm) tree_cc_kerne
     float* sp = sv + C::kKeys * D;
     const int tid = threadIdx.x, tr = tid >> 3, tc = tid & 7;
     tree_plan<1>(a, &plan);
-    TreeWalk walk = tree_start<1>(a, &plan, 0, tid == 0);
+    TreeWalk walk = tree_start<1>(&plan, 0);
+    if (tid == 0) tree_split(a, walk);
     launch_dependents();
     TreeWalk::Seg s;
     while (walk.next(a, &s)) {

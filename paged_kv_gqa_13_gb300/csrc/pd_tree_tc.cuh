@@ -202,7 +202,7 @@ struct CfgTree {
     static constexpr int kLineBytes = kStageOff + kStages * kStageBytes;
     static constexpr int kTagOff = round_up(kBars * 8, 16);
     static constexpr int kSegOff = kTagOff + 16 + 4 * kBadRing;
-    static constexpr int kCtlBytes = kSegOff + kSegRing * 64;
+    static constexpr int kCtlBytes = kSegOff + kSegRing * 72;
     static constexpr int kCtlOff = kLines * kLineBytes;
     static constexpr int kMiscOff = kCtlOff + kLines * kCtlBytes;  // tensor-memory address, abort flag
     static constexpr int kBytes = kMiscOff + 16 + 1024;            // 1024: alignment of the base
@@ -215,11 +215,12 @@ struct CfgTree {
 
 // Segments come to a line's roles through a ring in shared memory, filled by
 // the warp that walks them. blk1 = blk0 ends the line.
-struct alignas(16) TcSeg {
+struct TcSeg {
     int blk0, blk1, tail0, slots;     // blocks; first block with node tokens; slots of the request
     int slot, row0, node0, nodes;     // partial slot or -1; q rows and nodes of the segment
     int hh, head0, kvh, lo;           // head tile, its first q head and kv head; first entry of indices
-    int len, n, start, pad;           // the request: tokens, nodes, first q row
+    int len, n, start;                // the request: tokens, nodes, first q row
+    float k_scale, v_scale;           // of the kv head (E4M3 pools)
     __device__ __forceinline__ TreeReq req() const {
         return TreeReq{n, start, len, lo, 0};
     }
@@ -319,7 +320,7 @@ __global__ void __launch_bounds__(CfgTree<D, kWide, kFp8>::kThreads, 1)
     tree_plan<C::kLines>(a, plan);
     TreeWalk walk;
     const bool walker = !soft && !idle && part == C::kPipes + C::kProducers;
-    if (walker) walk = tree_start<C::kLines>(a, plan, line, lane == 0);
+    if (walker) walk = tree_start<C::kLines>(plan, line);
     tc_fence_before();
     __syncthreads();  // the walks have been read: copies may land
     tc_fence_after();
@@ -465,7 +466,7 @@ __global__ void __launch_bounds__(CfgTree<D, kWide, kFp8>::kThreads, 1)
                       kPlaceEmpty = kFp8 ? C::kStEmpty : C::kEmpty, kPlaceOff = kFp8 ? C::kStageOff : C::kRingOff,
                       kPlaceBytes = kFp8 ? C::kStageBytes : C::kSlotBytes, kQLanded = kFp8 ? C::kQRaw : C::kQFull;
         Ring<kPlaces> ring;
-        int loads = 0, segments = 0, kblocks = 0, turn = 0;  // turn: the producer whose load is next
+        int loads = 0, qloads = 0, segments = 0, kblocks = 0, turn = 0;  // turn: the producer whose load is next
         bool ok = true;
         // one box per lane: slot_rows rows x 64 columns (codes: x head_dim columns)
         constexpr int kBoxes = kFp8 ? 1 : C::kHalves, kRowBytes = kFp8 ? D : 128;
@@ -510,7 +511,7 @@ __global__ void __launch_bounds__(CfgTree<D, kWide, kFp8>::kThreads, 1)
             const int blk0 = s.blk0, blk1 = s.blk1;
             if (blk0 == blk1) break;
             for (int p = 0; me == 0 && p < C::kPipes && ok; ++p) {
-                // a row tile past the segment's nodes is loaded like another (rows of other requests, or zeros) and not used
+                // a row tile past the segment's nodes is copied like another (rows of other requests, or zeros) and not used
                 ok = segments == 0 || wait(C::kQEmpty + p, uint32_t(segments - 1) & 1u);
                 if (!ok) break;
                 if (lane == 0) {
@@ -520,16 +521,18 @@ __global__ void __launch_bounds__(CfgTree<D, kWide, kFp8>::kThreads, 1)
                                     bar(kQLanded + p));
                 }
                 __syncwarp();
+                ++qloads;
             }
             for (int blk = blk0; blk < blk1 && ok; ++blk, ++kblocks)
                 ok = load_block(s, blk, &tmk, true) && load_block(s, blk, &tmv, false);
+            if (!ok) break;
             seg_free(segments);
         }
         // copies issued last may still be landing when another role has stopped early
         for (int i = max(0, loads - kPlaces); i < loads; ++i)
             mbar_wait_bounded(bar(kPlaceFull + i % kPlaces), uint32_t(i / kPlaces) & 1u);
-        if (me == 0 && segments > 0)
-            for (int p = 0; p < C::kPipes; ++p) mbar_wait_bounded(bar(kQLanded + p), uint32_t(segments - 1) & 1u);
+        for (int i = max(0, qloads - C::kPipes); i < qloads; ++i)
+            mbar_wait_bounded(bar(kQLanded + i % C::kPipes), uint32_t(i / C::kPipes) & 1u);
     } else if (!soft) {
         // ================================================================ inspectors / converters; the first also walks the segments
         constexpr uint32_t kExp = kBf16 ? 0x7f807f80u : 0x7c007c00u;
@@ -539,6 +542,7 @@ __global__ void __launch_bounds__(CfgTree<D, kWide, kFp8>::kThreads, 1)
         int loads = 0;
         bool ok = true, more = walker;
         int walked = 0;
+        const TreeWalk first = walk;
         for (int i = 0; ok; ++i) {
             // Keep the ring of segments full; wait for a place only when fewer than four are ahead.
             while (more && walked < i + C::kSegRing) {
@@ -555,11 +559,17 @@ __global__ void __launch_bounds__(CfgTree<D, kWide, kFp8>::kThreads, 1)
                 more = walk.next(a, &s);
                 if (lane == 0) {
                     TcSeg x{};
-                    if (more)
+                    if (more) {
                         x = TcSeg{s.blk0, s.blk1,  s.tail0, s.slots, s.slot,  s.row0, s.node0,   s.nodes,
-                                  s.hh,   s.head0, s.kvh,   s.r.lo,  s.r.len, s.r.n,  s.r.start, 0};
+                                  s.hh,   s.head0, s.kvh,   s.r.lo,  s.r.len, s.r.n,  s.r.start, 1.f, 1.f};
+                        if (kFp8) {
+                            x.k_scale = __ldg(a.k_scale + s.kvh);
+                            x.v_scale = __ldg(a.v_scale + s.kvh);
+                        }
+                    }
                     segs[walked % C::kSegRing] = x;
                     mbar_arrive(bar(C::kSegFull + walked % C::kSegRing));
+                    if (walked == 0) tree_split(a, first);
                 }
                 __syncwarp();
                 ++walked;
@@ -597,12 +607,15 @@ __global__ void __launch_bounds__(CfgTree<D, kWide, kFp8>::kThreads, 1)
 #pragma unroll
                                 for (int x = 0; x < kRound; ++x) {
                                     const int tok = tree_token(a, blk, r0 + x * kStep);
-                                    const uint32_t nx = __vcmpeq4(w[x].x & 0x7f7f7f7fu, 0x7f7f7f7fu),
-                                                   ny = __vcmpeq4(w[x].y & 0x7f7f7f7fu, 0x7f7f7f7fu);
-                                    const bool dead = tok < 0 || tok >= len, node = !dead && tok >= ctx;
-                                    found |= node && (nx | ny) != 0u;
-                                    if (dead) w[x] = make_uint2(0u, 0u);
-                                    if (node) w[x] = make_uint2(w[x].x & ~nx, w[x].y & ~ny);
+                                    if (tok >= 0 && tok < ctx) continue;
+                                    if (tok < 0 || tok >= len) {
+                                        w[x] = make_uint2(0u, 0u);
+                                    } else {
+                                        const uint32_t nx = __vcmpeq4(w[x].x & 0x7f7f7f7fu, 0x7f7f7f7fu),
+                                                       ny = __vcmpeq4(w[x].y & 0x7f7f7f7fu, 0x7f7f7f7fu);
+                                        found |= (nx | ny) != 0u;
+                                        w[x] = make_uint2(w[x].x & ~nx, w[x].y & ~ny);
+                                    }
                                 }
                             }
 #pragma unroll
@@ -671,6 +684,41 @@ __global__ void __launch_bounds__(CfgTree<D, kWide, kFp8>::kThreads, 1)
         const bool packed = a.packed != 0, o_wide = (reinterpret_cast<uintptr_t>(a.o) & 31u) == 0;
         int jobs = 0, kblocks = 0;  // kblocks: K blocks before this segment
         bool ok = true;
+        auto turn_q = [&](const TcSeg& s, int seg) -> bool {
+            // This thread's q row, where the copy put it, as f16 times a power of two that brings its
+            // largest element near 2^14 (exact but for elements more than 2^28 below it) and the sign of
+            // the score scale.
+            const float ks = a.scale_log2 * s.k_scale;
+            uint8_t* tile = smem + p * C::kQBytes + row * 128;
+            auto piece = [&](int c) { return reinterpret_cast<uint4*>(tile + c / 8 * (C::kRows * 128) + (((c & 7) ^ (row & 7)) << 4)); };
+            if (!wait(C::kQRaw + p, uint32_t(seg) & 1u)) return false;
+            float big = 0.f;
+            if (!std::is_same<T, __half>::value) {
+#pragma unroll 8
+                for (int c = 0; c < D / 8; ++c) {
+                    float f[8];
+                    Elt<T>::to_f32(*piece(c), f);
+#pragma unroll
+                    for (int e = 0; e < 8; ++e) big = fmaxf(big, fabsf(f[e]));
+                }
+            }
+            int up = 0;
+            if (big > 0.f) up = max(-126, min(126, 141 - int(__float_as_uint(big) >> 23)));
+            const float by = __uint_as_float(uint32_t(127 + up) << 23) * (ks < 0.f ? -1.f : 1.f);
+#pragma unroll 8
+            for (int c = 0; c < D / 8; ++c) {
+                float f[8];
+                Elt<T>::to_f32(*piece(c), f);
+#pragma unroll
+                for (int e = 0; e < 8; ++e) f[e] *= by;
+                *piece(c) = Elt<__half>::from_f32(f);
+            }
+            scale = ks == 0.f ? 1e-38f : fabsf(ks) * __uint_as_float(uint32_t(127 - up) << 23);
+            fence_proxy_async_smem();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(bar(C::kQFull + p));
+            return true;
+        };
         for (int seg = 0; ok; ++seg) {
             if (!seg_wait(seg)) break;
             const TcSeg& s = seg_at(seg);
@@ -681,39 +729,8 @@ __global__ void __launch_bounds__(CfgTree<D, kWide, kFp8>::kThreads, 1)
             const long long at = tree_row(a, s.row0, s.nodes, s.hh, row + p * C::kRows);
             const bool live = __any_sync(kFull, at >= 0);  // a warp without rows only keeps step
             float m = kNegInf, l = 0.f;
-            if constexpr (kFp8) {
-                // This thread's q row, where the copy put it, as f16 times a power of two that brings its
-                // largest element near 2^14 (exact but for elements more than 2^28 below it) and the sign of
-                // the score scale.
-                const float ks = a.scale_log2 * __ldg(a.k_scale + s.kvh);
-                uint8_t* tile = smem + p * C::kQBytes + row * 128;
-                auto piece = [&](int c) { return reinterpret_cast<uint4*>(tile + c / 8 * (C::kRows * 128) + (((c & 7) ^ (row & 7)) << 4)); };
-                if (!(ok = wait(C::kQRaw + p, uint32_t(seg) & 1u))) break;
-                float big = 0.f;
-                if (!std::is_same<T, __half>::value) {
-#pragma unroll 8
-                    for (int c = 0; c < D / 8; ++c) {
-                        float f[8];
-                        Elt<T>::to_f32(*piece(c), f);
-#pragma unroll
-                        for (int e = 0; e < 8; ++e) big = fmaxf(big, fabsf(f[e]));
-                    }
-                }
-                int up = 0;
-                if (big > 0.f) up = max(-126, min(126, 141 - int(__float_as_uint(big) >> 23)));
-                const float by = __uint_as_float(uint32_t(127 + up) << 23) * (ks < 0.f ? -1.f : 1.f);
-#pragma unroll 8
-                for (int c = 0; c < D / 8; ++c) {
-                    float f[8];
-                    Elt<T>::to_f32(*piece(c), f);
-#pragma unroll
-                    for (int e = 0; e < 8; ++e) f[e] *= by;
-                    *piece(c) = Elt<__half>::from_f32(f);
-                }
-                scale = ks == 0.f ? 1e-38f : fabsf(ks) * __uint_as_float(uint32_t(127 - up) << 23);
-                fence_proxy_async_smem();
-                __syncwarp();
-                if (lane == 0) mbar_arrive(bar(C::kQFull + p));
+            if (kFp8) {
+                if (!(ok = turn_q(s, seg))) break;
             }
             for (int blk = blk0; blk < blk1 && ok; ++blk) {
 #pragma unroll 1
@@ -810,7 +827,7 @@ __global__ void __launch_bounds__(CfgTree<D, kWide, kFp8>::kThreads, 1)
             if (!wait(C::kPvDone + 2 * p + ((jobs - 1) & 1), uint32_t((jobs - 1) >> 1) & 1u)) break;
             tc_fence_after();
             if (live) {
-                const float inv = (m == kNegInf ? 0.f : 1.f / l) * (kFp8 ? __ldg(a.v_scale + s.kvh) : 1.f);
+                const float inv = (m == kNegInf ? 0.f : 1.f / l) * s.v_scale;
                 const float lse2 = m == kNegInf ? kNegInf : m + log2f(l);
                 const bool fix = bad_v[seg & 3] == seg + 1;
                 const size_t prow = size_t(s.slot) * a.seg_rows + row + p * C::kRows;

@@ -367,45 +367,81 @@ def pd_test_inject_wait_timeout(extra_bytes: int) -> None:
 
 
 # --- speculative decoding: request b's new tokens are rows new_indptr[b] .. new_indptr[b + 1] of the ragged
-# tensors and the last rows of its cache -----------------------------------------------------------------------
+# tensors and the last rows of its cache. These calls are short (a few microseconds on the device), so their checks
+# are a few attribute reads and the current stream is asked for by its raw handle. --------------------------------
 
-def _tokens(t, heads, head_dim):
-    """(pointer, elements between tokens) of [tokens, heads, head_dim] rows whose heads are contiguous."""
-    stride = t.stride()
-    if t.dim() != 3 or t.shape[1] != heads or t.shape[2] != head_dim or (
-            t.numel() and (stride[2] != 1 or (stride[1] != head_dim and heads != 1))):
-        raise PagedecodeError(PD_ERR_INVALID, "expected [tokens, heads, head_dim] with contiguous heads")
-    return t.data_ptr(), stride[0] if t.shape[0] > 1 else max(stride[0], heads * head_dim)
+_TYPES: dict = {}  # torch dtype -> PD_* code, filled on first use
+_raw_stream = None
 
 
-def _same_dtype(*tensors) -> int:
-    code = _dtype_code(tensors[0])
-    if any(t.dtype != tensors[0].dtype for t in tensors):
-        raise PagedecodeError(PD_ERR_INVALID, "tensors must have the same dtype")
+def _torch_facts():
+    import torch
+
+    global _raw_stream
+    _TYPES.update({torch.float32: PD_F32, torch.float16: PD_F16, torch.bfloat16: PD_BF16})
+    _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
+        lambda device: torch.cuda.current_stream(device).cuda_stream)
+
+
+def _code_of(dtype) -> int:
+    if not _TYPES:
+        _torch_facts()
+    code = _TYPES.get(dtype)
+    if code is None:
+        raise PagedecodeError(PD_ERR_UNSUPPORTED, f"unsupported dtype {dtype}")
     return code
+
+
+def _stream_for(t, stream):
+    if stream is None:
+        if _raw_stream is None:
+            _torch_facts()
+        return _raw_stream(t.get_device())
+    return getattr(stream, "cuda_stream", stream)
+
+
+def _bad(message):
+    raise PagedecodeError(PD_ERR_INVALID, message)
+
+
+def _token_stride(t, heads, head_dim):
+    """Elements between the tokens of [tokens, heads, head_dim] rows whose heads are contiguous."""
+    s0, s1, s2 = t.stride()
+    if (s2 != 1 or (s1 != head_dim and heads != 1)) and t.numel():
+        _bad("expected [tokens, heads, head_dim] with contiguous heads")
+    return s0 if t.shape[0] > 1 else max(s0, heads * head_dim)
 
 
 def _int32(t):
     """Pointer of a contiguous 32-bit integer tensor (None stays None)."""
     if t is None:
         return None
-    if t.element_size() != 4 or t.is_floating_point():
-        raise PagedecodeError(PD_ERR_INVALID, "table, position, mask and path tensors hold 32-bit integers")
-    return _ptr(t)
+    if t.element_size() != 4 or t.is_floating_point() or not t.is_contiguous():
+        _bad("table, position, mask and path tensors hold contiguous 32-bit integers")
+    return t.data_ptr()
 
 
 def _table(indices, indptr, last_page_len, new_indptr):
-    batch = last_page_len.numel()
-    if indptr.numel() != batch + 1 or new_indptr.numel() != batch + 1:
-        raise PagedecodeError(PD_ERR_INVALID, "indptr and new_indptr hold one entry more than last_page_len")
-    return (_int32(indices) if indices.numel() else None, _int32(indptr), _int32(last_page_len),
-            _int32(new_indptr)), batch
+    """(pointers, batch, entries of indices)"""
+    batch, entries = last_page_len.shape[0], indices.shape[0]
+    if indptr.shape[0] != batch + 1 or new_indptr.shape[0] != batch + 1:
+        _bad("indptr and new_indptr hold one entry more than last_page_len")
+    return (_int32(indices) if entries else None, _int32(indptr), _int32(last_page_len), _int32(new_indptr)), batch, entries
 
 
 def _pools(k_data, v_data):
-    if k_data.dim() != 4 or k_data.shape != v_data.shape or k_data.dtype != v_data.dtype:
-        raise PagedecodeError(PD_ERR_INVALID, "k_data and v_data are [pages, Hk, page_size, D] of the same type")
-    return k_data.shape
+    shape = k_data.shape
+    if len(shape) != 4 or shape != v_data.shape or k_data.dtype != v_data.dtype:
+        _bad("k_data and v_data are [pages, Hk, page_size, D] of the same type")
+    return shape
+
+
+def _scales(k_scale, v_scale, k_data):
+    if any(s.element_size() != 4 or not s.is_floating_point() or s.numel() != k_data.shape[1] for s in (k_scale, v_scale)):
+        _bad("k_scale and v_scale are float32, one for each kv head")
+    if k_data.element_size() != 1:
+        _bad("E4M3 pools hold one byte for each element")
+    return _ptr(k_scale), _ptr(v_scale)
 
 
 def pd_rope_frequencies(rot_dim: int, theta: float = 10000.0, scaling: int = PD_ROPE_PLAIN, factor: float = 1.0,
@@ -422,47 +458,46 @@ def pd_rope_frequencies(rot_dim: int, theta: float = 10000.0, scaling: int = PD_
 
 
 def _freqs(freqs):
+    """(pointer, rot_dim)"""
     if freqs is None:
         return None, 0
-    if freqs.element_size() != 8 or freqs.is_floating_point():
-        raise PagedecodeError(PD_ERR_INVALID, "freqs hold 64-bit integers")
-    return _ptr(freqs), 2 * freqs.numel()
+    if freqs.element_size() != 8 or freqs.is_floating_point() or not freqs.is_contiguous():
+        _bad("freqs hold contiguous 64-bit integers")
+    return freqs.data_ptr(), 2 * freqs.shape[0]
 
 
 def pd_rope(x, positions, freqs, out, layout: int = PD_ROPE_HALF, rope_scale: float = 1.0, stream=None) -> None:
     """x, out [tokens, heads, D] (tokens may be strided); positions int32 [tokens]; out may be x."""
     tokens, heads, head_dim = x.shape
-    if out.shape != x.shape or positions.numel() != tokens:
-        raise PagedecodeError(PD_ERR_INVALID, "out is shaped as x, and there is one position for each token")
-    (xp, xs), (op, os_) = _tokens(x, heads, head_dim), _tokens(out, heads, head_dim)
+    if out.shape != x.shape or out.dtype != x.dtype or positions.shape[0] != tokens:
+        _bad("out is shaped and typed as x, and there is one position for each token")
     fp, rot = _freqs(freqs)
-    _check(_lib.pd_rope(xp, _int32(positions), fp, op, tokens, heads, head_dim, rot, xs, os_, layout, rope_scale,
-                        _same_dtype(x, out), _stream(stream)))
+    _check(_lib.pd_rope(x.data_ptr(), _int32(positions), fp, out.data_ptr(), tokens, heads, head_dim, rot,
+                        _token_stride(x, heads, head_dim), _token_stride(out, heads, head_dim), layout, rope_scale,
+                        _code_of(x.dtype), _stream_for(x, stream)))
 
 
 def _rope_append(fn, scales, q, k_new, v_new, positions, freqs, q_out, k_data, v_data, indices, indptr, last_page_len,
                  new_indptr, workspace, layout, rope_scale, stream):
     total_new, num_kv_heads, head_dim = k_new.shape
     num_total_pages, hk, page_size, d = _pools(k_data, v_data)
-    if (hk, d) != (num_kv_heads, head_dim) or v_new.shape != k_new.shape:
-        raise PagedecodeError(PD_ERR_INVALID, "k_new, v_new and the pools differ in heads or head_dim")
-    (kp, ks), (vp, vs) = _tokens(k_new, num_kv_heads, head_dim), _tokens(v_new, num_kv_heads, head_dim)
+    dtype = k_new.dtype
+    if hk != num_kv_heads or d != head_dim or v_new.shape != k_new.shape or v_new.dtype != dtype:
+        _bad("k_new, v_new and the pools differ in heads, head_dim or type")
     qp, qs, op, num_qo_heads = None, 0, None, 0
-    code = _same_dtype(k_new, v_new)
     if q is not None:
         num_qo_heads = q.shape[1]
-        if q.shape[0] != total_new or q_out.shape != q.shape:
-            raise PagedecodeError(PD_ERR_INVALID, "q holds one row for each new token, and q_out is shaped as q")
-        qp, qs = _tokens(q, num_qo_heads, head_dim)
-        op = _ptr(q_out)
-        _same_dtype(k_new, q, q_out)
-    if positions is not None and positions.numel() != total_new:
-        raise PagedecodeError(PD_ERR_INVALID, "there is one position for each new token")
+        if q.shape[0] != total_new or q.shape[2] != head_dim or q_out.shape != q.shape or q.dtype != dtype or q_out.dtype != dtype:
+            _bad("q holds one row for each new token, typed as k_new, and q_out is shaped and typed as q")
+        qp, qs, op = q.data_ptr(), _token_stride(q, num_qo_heads, head_dim), _ptr(q_out)
+    if positions is not None and positions.shape[0] != total_new:
+        _bad("there is one position for each new token")
     fp, rot = _freqs(freqs)
-    table, batch = _table(indices, indptr, last_page_len, new_indptr)
-    _check(fn(qp, kp, vp, _int32(positions), fp, op, *scales, _ptr(k_data), _ptr(v_data), *table, batch, total_new,
-              num_qo_heads, num_kv_heads, head_dim, rot, page_size, num_total_pages, indices.numel(), qs, ks, vs, layout,
-              rope_scale, code, _ptr(workspace), workspace.numel(), _stream(stream)))
+    table, batch, entries = _table(indices, indptr, last_page_len, new_indptr)
+    _check(fn(qp, k_new.data_ptr(), v_new.data_ptr(), _int32(positions), fp, op, *scales, _ptr(k_data), _ptr(v_data), *table,
+              batch, total_new, num_qo_heads, num_kv_heads, head_dim, rot, page_size, num_total_pages, entries, qs,
+              _token_stride(k_new, num_kv_heads, head_dim), _token_stride(v_new, num_kv_heads, head_dim), layout, rope_scale,
+              _code_of(dtype), _ptr(workspace), workspace.numel(), _stream_for(k_new, stream)))
 
 
 def pd_paged_rope_append(q, k_new, v_new, positions, freqs, q_out, k_data, v_data, indices, indptr, last_page_len,
@@ -473,8 +508,8 @@ def pd_paged_rope_append(q, k_new, v_new, positions, freqs, q_out, k_data, v_dat
     q, k_new, v_new [total_new, heads, D], tokens may be strided (views of one projection); q, q_out may be None;
     positions int32 [total_new] or None (the index in the cache); freqs None appends without rotation.
     """
-    if _same_dtype(k_data) != _dtype_code(k_new):
-        raise PagedecodeError(PD_ERR_INVALID, "the pools have the type of k_new")
+    if k_data.dtype != k_new.dtype:
+        _bad("the pools have the type of k_new")
     _rope_append(_lib.pd_paged_rope_append, (), q, k_new, v_new, positions, freqs, q_out, k_data, v_data, indices, indptr,
                  last_page_len, new_indptr, workspace, layout, rope_scale, stream)
 
@@ -483,19 +518,8 @@ def pd_paged_rope_append_fp8(q, k_new, v_new, positions, freqs, q_out, k_scale, 
                              indptr, last_page_len, new_indptr, workspace, layout: int = PD_ROPE_HALF,
                              rope_scale: float = 1.0, stream=None) -> None:
     """pd_paged_rope_append into E4M3 pools (k_data, v_data uint8; scales f32 [Hk])."""
-    scales = _scales(k_scale, v_scale, k_data)
-    _rope_append(_lib.pd_paged_rope_append_fp8, scales, q, k_new, v_new, positions, freqs, q_out, k_data, v_data, indices,
-                 indptr, last_page_len, new_indptr, workspace, layout, rope_scale, stream)
-
-
-def _scales(k_scale, v_scale, k_data):
-    import torch
-
-    if any(s.dtype != torch.float32 or s.numel() != k_data.shape[1] for s in (k_scale, v_scale)):
-        raise PagedecodeError(PD_ERR_INVALID, "k_scale and v_scale are float32, one for each kv head")
-    if k_data.element_size() != 1:
-        raise PagedecodeError(PD_ERR_INVALID, "E4M3 pools hold one byte for each element")
-    return _ptr(k_scale), _ptr(v_scale)
+    _rope_append(_lib.pd_paged_rope_append_fp8, _scales(k_scale, v_scale, k_data), q, k_new, v_new, positions, freqs, q_out,
+                 k_data, v_data, indices, indptr, last_page_len, new_indptr, workspace, layout, rope_scale, stream)
 
 
 def pd_paged_tree_decode_workspace_bytes(num_qo_heads: int, num_kv_heads: int, head_dim: int, dtype: int) -> int:
@@ -507,21 +531,20 @@ def pd_paged_tree_decode_workspace_bytes(num_qo_heads: int, num_kv_heads: int, h
 
 def _tree_decode(fn, scales, q, k_data, v_data, indices, indptr, last_page_len, new_indptr, tree_mask, o, lse, sm_scale,
                  workspace, stream):
-    import torch
-
     total_new, num_qo_heads, head_dim = q.shape
     num_total_pages, num_kv_heads, page_size, d = _pools(k_data, v_data)
-    if d != head_dim or o.shape != q.shape or lse.shape != q.shape[:2] or lse.dtype != torch.float32:
-        raise PagedecodeError(PD_ERR_INVALID, "q and o [total_new, Hq, D], lse float32 [total_new, Hq], the pools' D")
+    if d != head_dim or o.shape != q.shape or o.dtype != q.dtype or lse.shape != q.shape[:2] or lse.element_size() != 4 \
+            or not lse.is_floating_point():
+        _bad("q and o [total_new, Hq, D] of one type, lse float32 [total_new, Hq], the pools' D")
     words = 0
     if tree_mask is not None:
         if tree_mask.dim() != 2 or tree_mask.shape[0] != total_new:
-            raise PagedecodeError(PD_ERR_INVALID, "tree_mask is [total_new, words] of 32 bits each")
+            _bad("tree_mask is [total_new, words] of 32 bits each")
         words = tree_mask.shape[1]
-    table, batch = _table(indices, indptr, last_page_len, new_indptr)
+    table, batch, entries = _table(indices, indptr, last_page_len, new_indptr)
     _check(fn(_ptr(q), _ptr(k_data), _ptr(v_data), *scales, *table, _int32(tree_mask), _ptr(o), _ptr(lse), batch, total_new,
-              words, num_qo_heads, num_kv_heads, head_dim, page_size, num_total_pages, indices.numel(), sm_scale,
-              _same_dtype(q, o), _ptr(workspace), workspace.numel(), _stream(stream)))
+              words, num_qo_heads, num_kv_heads, head_dim, page_size, num_total_pages, entries, sm_scale, _code_of(q.dtype),
+              _ptr(workspace), workspace.numel(), _stream_for(q, stream)))
 
 
 def pd_paged_tree_decode(q, k_data, v_data, indices, indptr, last_page_len, new_indptr, tree_mask, o, lse,
@@ -531,8 +554,8 @@ def pd_paged_tree_decode(q, k_data, v_data, indices, indptr, last_page_len, new_
     q, o [total_new, Hq, D]; lse [total_new, Hq] f32; tree_mask int32 (or uint32) [total_new, words]: bit i of a node's
     words says that it attends node i of its request; None: a chain (nodes up to itself).
     """
-    if _same_dtype(k_data) != _dtype_code(q):
-        raise PagedecodeError(PD_ERR_INVALID, "the pools have the type of q")
+    if k_data.dtype != q.dtype:
+        _bad("the pools have the type of q")
     _tree_decode(_lib.pd_paged_tree_decode, (), q, k_data, v_data, indices, indptr, last_page_len, new_indptr, tree_mask, o,
                  lse, sm_scale, workspace, stream)
 
@@ -552,10 +575,10 @@ def pd_paged_tree_commit(k_data, v_data, indices, indptr, last_page_len, new_ind
     no bound).
     """
     num_total_pages, num_kv_heads, page_size, head_dim = _pools(k_data, v_data)
-    table, batch = _table(indices, indptr, last_page_len, new_indptr)
-    if path.dim() != 2 or path.shape[0] != batch or path_len.numel() != batch:
-        raise PagedecodeError(PD_ERR_INVALID, "path is [batch, max_path], path_len [batch]")
+    table, batch, entries = _table(indices, indptr, last_page_len, new_indptr)
+    if path.dim() != 2 or path.shape[0] != batch or path_len.shape[0] != batch:
+        _bad("path is [batch, max_path], path_len [batch]")
     _check(_lib.pd_paged_tree_commit(
         _ptr(k_data), _ptr(v_data), *table, _int32(path), _int32(path_len), batch,
         0x7fffffff if total_new is None else total_new, path.shape[1], num_kv_heads, head_dim, page_size, num_total_pages,
-        indices.numel(), k_data.element_size(), _ptr(workspace), workspace.numel(), _stream(stream)))
+        entries, k_data.element_size(), _ptr(workspace), workspace.numel(), _stream_for(k_data, stream)))

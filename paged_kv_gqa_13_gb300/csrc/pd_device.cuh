@@ -453,6 +453,25 @@ struct ReduceScatter2 {
     }
 };
 
+// Division of 0 <= x < 2^31 by a divisor that the host knows: with s =
+// ceil(log2 d) and m = floor(2^(31 + s) / d) + 1, m d exceeds 2^(31 + s) by at
+// most d <= 2^s, so that x m / 2^(31 + s) is x / d plus less than 1 / d.
+struct FastDiv {
+    uint32_t d = 1, m = 0x80000001u;
+    int s = 31;
+    __host__ static FastDiv of(int divisor) {
+        FastDiv f;
+        f.d = uint32_t(divisor);
+        int s = 0;
+        while ((1ull << s) < f.d) ++s;
+        f.m = uint32_t((1ull << (31 + s)) / f.d + 1);
+        f.s = 31 + s;
+        return f;
+    }
+    __device__ __forceinline__ int div(int x) const { return int((uint64_t(uint32_t(x)) * m) >> s); }
+    __device__ __forceinline__ int mod(int x) const { return x - div(x) * int(d); }
+};
+
 // ---------------------------------------------------------------- arguments
 
 struct DecodeArgs {

@@ -13,6 +13,7 @@
 // slice of its heads when there are few tokens), so a lane computes the sines
 // of its pairs once and uses them for every head.
 #include <cmath>
+#include <type_traits>
 
 #include "pd_device.cuh"
 #include "pd_host.h"
@@ -50,15 +51,19 @@ struct RopeArgs {
     float scale;
     int head_dim, rot_dim;
     int tokens, slices;
+    FastDiv by_rest, by_chunks;  // by the accesses of a head's elements past rot_dim, and of a whole head
 };
 
 // V elements of a row: one 16-byte access, or one element (V = 1).
 template <typename T, int V>
-__device__ __forceinline__ void load_elems(const T* p, float (&f)[V]) {
+using Raw = typename std::conditional<V == 1, T, uint4>::type;
+
+template <typename T, int V>
+__device__ __forceinline__ void widen(const Raw<T, V>& w, float (&f)[V]) {
     if constexpr (V == 1)
-        f[0] = float(*p);
+        f[0] = float(w);
     else
-        Elt<T>::to_f32(*reinterpret_cast<const uint4*>(p), f);
+        Elt<T>::to_f32(w, f);
 }
 
 template <typename T, int V>
@@ -108,9 +113,10 @@ __device__ __forceinline__ int request_of(const int32_t* new_indptr, int batch, 
 // Unit u of a rotated head is V pairs: elements u V .. and rot/2 + u V ..
 // (half layout) or 2 u V .. 2 u V + 2 V - 1 (pairs layout). A lane keeps one
 // unit at a time and takes heads in rounds of kRound, whose loads are all
-// issued before the first store (out may be x).
+// issued before the first store (out may be x) and kept as they come, so that
+// 24 warps per SM have up to 4 KB each in flight.
 template <typename T, bool kFp8, int V, bool kPairs>
-__global__ void __launch_bounds__(128) rope_kernel(const RopeArgs a) {
+__global__ void __launch_bounds__(128, 6) rope_kernel(const RopeArgs a) {
     constexpr int kRound = 4;
     const int lane = threadIdx.x & 31;
     const long long w = (long long)blockIdx.x * 4 + (threadIdx.x >> 5);
@@ -194,24 +200,27 @@ __global__ void __launch_bounds__(128) rope_kernel(const RopeArgs a) {
             }
             const int e0 = kPairs ? 2 * u * V : u * V, e1 = kPairs ? e0 + V : rot / 2 + u * V;
             for (int h = i0 + lane / across; h < h_end; h += heads * kRound) {
-                float x[kRound][V], y[kRound][V];
+                Raw<T, V> xs[kRound], ys[kRound];
 #pragma unroll
                 for (int r = 0; r < kRound; ++r) {
                     if (h + r * heads < h_end) {
                         const T* row = source(h + r * heads);
-                        load_elems<T, V>(row + e0, x[r]);
-                        load_elems<T, V>(row + e1, y[r]);
+                        xs[r] = *reinterpret_cast<const Raw<T, V>*>(row + e0);
+                        ys[r] = *reinterpret_cast<const Raw<T, V>*>(row + e1);
                     }
                 }
 #pragma unroll
                 for (int r = 0; r < kRound; ++r) {
                     if (h + r * heads >= h_end) continue;
+                    float x[V], y[V];
+                    widen<T, V>(xs[r], x);
+                    widen<T, V>(ys[r], y);
                     float lo[V], hi[V];
 #pragma unroll
                     for (int i = 0; i < V; ++i) {
                         // pair i: (x[i], y[i]) in the half layout; (z[2i], z[2i + 1]), z = x then y, in the pairs layout
-                        const float p = kPairs && V > 1 ? (2 * i < V ? x[r][2 * i % V] : y[r][2 * i % V]) : x[r][i];
-                        const float q = kPairs && V > 1 ? (2 * i < V ? x[r][(2 * i + 1) % V] : y[r][(2 * i + 1) % V]) : y[r][i];
+                        const float p = kPairs && V > 1 ? (2 * i < V ? x[2 * i % V] : y[2 * i % V]) : x[i];
+                        const float q = kPairs && V > 1 ? (2 * i < V ? x[(2 * i + 1) % V] : y[(2 * i + 1) % V]) : y[i];
                         const float pr = p * c[i] - q * s[i], qr2 = q * c[i] + p * s[i];
                         if (kPairs && V > 1) {
                             (2 * i < V ? lo : hi)[2 * i % V] = pr;
@@ -230,26 +239,51 @@ __global__ void __launch_bounds__(128) rope_kernel(const RopeArgs a) {
     // ---- elements past rot_dim of the q and k heads (q in place: nothing to do), then the v heads: plain copies
     const int rest = (D - rot) / V;
     const int q_from = (a.q_out == a.q && a.q_stride == a.q_out_stride) ? max(i0, a.hq) : i0;
-    for (int x = lane; x < rest * (h_end - q_from); x += 32) {
-        const int h = q_from + x / rest, e = rot + (x % rest) * V;
-        float f[V];
-        load_elems<T, V>(source(h) + e, f);
-        store(h, e, f);
-    }
+    // n chunks of V elements, `at` giving a chunk's head and element; loads of a round before its stores
+    auto copy = [&](int n, auto at, auto from, auto to) {
+        constexpr int kCopies = 8;
+        for (int x = lane; x < n; x += 32 * kCopies) {
+            Raw<T, V> w[kCopies];
+#pragma unroll
+            for (int r = 0; r < kCopies; ++r)
+                if (x + 32 * r < n) {
+                    const int2 c = at(x + 32 * r);
+                    w[r] = *reinterpret_cast<const Raw<T, V>*>(from(c.x) + c.y);
+                }
+#pragma unroll
+            for (int r = 0; r < kCopies; ++r)
+                if (x + 32 * r < n) {
+                    const int2 c = at(x + 32 * r);
+                    float f[V];
+                    widen<T, V>(w[r], f);
+                    to(c.x, c.y, f);
+                }
+        }
+    };
+    copy(
+        rest * (h_end - q_from),
+        [&](int x) {
+            const int h = a.by_rest.div(x);
+            return make_int2(q_from + h, rot + (x - h * rest) * V);
+        },
+        source, store);
     if (!write_kv) return;
-    const int chunks = D / V, v0 = max(i0 - a.hq - a.hk, 0), v1 = i1 - a.hq - a.hk;
+    const int v0 = max(i0 - a.hq - a.hk, 0), v1 = i1 - a.hq - a.hk;
     const T* vr = static_cast<const T*>(a.v) + (long long)t * a.v_stride;
-#pragma unroll 4
-    for (int x = lane; x < chunks * (v1 - v0); x += 32) {
-        const int kh = v0 + x / chunks, e = (x % chunks) * V;
-        float f[V];
-        load_elems<T, V>(vr + (long long)kh * D + e, f);
-        const size_t at = dst + size_t(kh) * head_step + e;
-        if constexpr (kFp8)
-            store_codes<V>(static_cast<uint8_t*>(a.v_data) + at, f, __ldg(a.v_scale + kh));
-        else
-            store_elems<T, V>(static_cast<T*>(a.v_data) + at, f);
-    }
+    copy(
+        D / V * (v1 - v0),
+        [&](int x) {
+            const int h = a.by_chunks.div(x);
+            return make_int2(v0 + h, (x - h * (D / V)) * V);
+        },
+        [&](int h) { return vr + (long long)h * D; },
+        [&](int h, int e, const float(&f)[V]) {
+            const size_t at = dst + size_t(h) * head_step + e;
+            if constexpr (kFp8)
+                store_codes<V>(static_cast<uint8_t*>(a.v_data) + at, f, __ldg(a.v_scale + h));
+            else
+                store_elems<T, V>(static_cast<T*>(a.v_data) + at, f);
+        });
 }
 
 template <typename T, bool kFp8, int V>
@@ -280,6 +314,9 @@ pd_status launch(RopeArgs& a, pd_dtype dt, bool fp8, int layout, cudaStream_t st
     const int items = a.hq + 2 * a.hk;
     const long long want = ((long long)sms * 8 + a.tokens - 1) / a.tokens;
     a.slices = int(want < 1 ? 1 : want > (items + 3) / 4 ? (items + 3) / 4 : want);
+    const int per = wide ? vec : 1;
+    if (a.head_dim > a.rot_dim) a.by_rest = FastDiv::of((a.head_dim - a.rot_dim) / per);
+    a.by_chunks = FastDiv::of(a.head_dim / per);
     const long long warps = (long long)a.tokens * a.slices;
     const void* fn = dt == PD_F32   ? pick_kernel<float, false>(layout, wide)
                      : dt == PD_F16 ? (fp8 ? pick_kernel<__half, true>(layout, wide) : pick_kernel<__half, false>(layout, wide))

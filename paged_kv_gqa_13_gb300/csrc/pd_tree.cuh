@@ -36,25 +36,6 @@ struct TreeSplit {
     int pad[2];
 };
 
-// Division of 0 <= x < 2^31 by a divisor that the host knows: with s =
-// ceil(log2 d) and m = floor(2^(31 + s) / d) + 1, m d exceeds 2^(31 + s) by at
-// most d <= 2^s, so that x m / 2^(31 + s) is x / d plus less than 1 / d.
-struct FastDiv {
-    uint32_t d = 1, m = 0x80000001u;
-    int s = 31;
-    __host__ static FastDiv of(int divisor) {
-        FastDiv f;
-        f.d = uint32_t(divisor);
-        int s = 0;
-        while ((1ull << s) < f.d) ++s;
-        f.m = uint32_t((1ull << (31 + s)) / f.d + 1);
-        f.s = 31 + s;
-        return f;
-    }
-    __device__ __forceinline__ int div(int x) const { return int((uint64_t(uint32_t(x)) * m) >> s); }
-    __device__ __forceinline__ int mod(int x) const { return x - div(x) * int(d); }
-};
-
 struct TreeArgs {
     const void* q;
     const void* k;
@@ -394,13 +375,23 @@ __device__ __forceinline__ void pool_load4(const KV* p, float s, float* f) {
     }
 }
 
+// 16 bytes from global to shared memory, or 16 zero bytes.
+__device__ __forceinline__ void copy16_async(void* dst, const void* src, bool there) {
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(smem_u32(dst)), "l"(src), "r"(there ? 16 : 0)
+                 : "memory");
+}
+__device__ __forceinline__ void copy_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+__device__ __forceinline__ void copy_wait() { asm volatile("cp.async.wait_all;" ::: "memory"); }
+
 template <int D>
 struct CfgTreeCc {
     static constexpr int kRows = 32, kKeys = 32, kThreads = 128, kBlockTokens = 128;
     static constexpr int kLd = D + 4;  // row step of q and K in shared memory: 16-byte reads of 8 rows hit all banks
-    static constexpr int kFloats = 2 * kRows * kLd + kKeys * D + kRows * (kKeys + 1);
+    static constexpr int kBufs = D == 256 ? 1 : 2;   // of K and V: the next keys on their way
+    static constexpr int kKv = kKeys * kLd + kKeys * D;
+    static constexpr int kFloats = kRows * kLd + kBufs * kKv + kRows * (kKeys + 1);
     static constexpr int kBytes = kFloats * 4;
-    static constexpr int kBlocksPerSm = D == 64 ? 6 : D == 128 ? 4 : 2;
+    static constexpr int kBlocksPerSm = D == 64 ? 4 : 2;
 };
 
 // f32 arithmetic on CUDA cores: f32 q (no tensor-core type holds it) and
@@ -416,11 +407,10 @@ __global__ void __launch_bounds__(128, CfgTreeCc<D>::kBlocksPerSm) tree_cc_kerne
     const float kNegInf = -__int_as_float(0x7f800000);
     extern __shared__ __align__(16) float tree_smem[];
     __shared__ TreePlanScratch plan;
-    __shared__ long long row_off[C::kKeys];  // element offset of each key's row in the pools; -1: none
+    __shared__ long long row_offs[C::kBlockTokens];  // element offset of each key's row in the pools; -1: none
     float* sq = tree_smem;
-    float* sk = sq + C::kRows * C::kLd;
-    float* sv = sk + C::kKeys * C::kLd;
-    float* sp = sv + C::kKeys * D;
+    float* kv = sq + C::kRows * C::kLd;
+    float* sp = kv + C::kBufs * C::kKv;
     const int tid = threadIdx.x, tr = tid >> 3, tc = tid & 7;
     tree_plan<1>(a, &plan);
     TreeWalk walk = tree_start<1>(&plan, 0);
@@ -440,9 +430,35 @@ __global__ void __launch_bounds__(128, CfgTreeCc<D>::kBlocksPerSm) tree_cc_kerne
         }
         float m[2] = {kNegInf, kNegInf}, l[2] = {}, o[2][D / 8] = {};
         const int node[2] = {s.node0 + a.by_hpt.div(2 * tr), s.node0 + a.by_hpt.div(2 * tr + 1)};
-        for (int t0 = s.blk0 * C::kBlockTokens; t0 < min(s.blk1 * C::kBlockTokens, s.r.len); t0 += C::kKeys) {
-            __syncthreads();
-            if (tid < C::kKeys) {
+        // Keys t0 .. of the pools into buffer `buf` (zeros where there is no row): asynchronous copies of f32
+        // pools, loads and conversions of others.
+        auto load = [&](int t0, int buf) {
+            float* sk = kv + buf * C::kKv;
+            float* sv = sk + C::kKeys * C::kLd;
+            for (int i = tid; i < C::kKeys * (D / 4); i += C::kThreads) {
+                const int key = i / (D / 4), e = i % (D / 4) * 4;
+                const long long off = row_offs[t0 % C::kBlockTokens + key];
+                if constexpr (sizeof(KV) == 4) {
+                    const long long at = off < 0 ? 0 : off + e;
+                    copy16_async(sk + key * C::kLd + e, static_cast<const float*>(a.k) + at, off >= 0);
+                    copy16_async(sv + key * D + e, static_cast<const float*>(a.v) + at, off >= 0);
+                } else {
+                    float fk[4] = {}, fv[4] = {};
+                    if (off >= 0) {
+                        pool_load4(static_cast<const KV*>(a.k) + off + e, ks, fk);
+                        pool_load4(static_cast<const KV*>(a.v) + off + e, vs, fv);
+                    }
+                    *reinterpret_cast<float4*>(sk + key * C::kLd + e) = make_float4(fk[0], fk[1], fk[2], fk[3]);
+                    *reinterpret_cast<float4*>(sv + key * D + e) = make_float4(fv[0], fv[1], fv[2], fv[3]);
+                }
+            }
+            copy_commit();
+        };
+        const int t_end = min(s.blk1 * C::kBlockTokens, s.r.len);
+        for (int t0 = s.blk0 * C::kBlockTokens; t0 < t_end; t0 += C::kKeys) {
+            const int buf = t0 / C::kKeys % C::kBufs;
+            if (t0 % C::kBlockTokens == 0) {  // the rows of a whole block at once
+                __syncthreads();
                 const int t = t0 + tid;
                 long long off = -1;
                 if (t < s.r.len) {
@@ -452,21 +468,20 @@ __global__ void __launch_bounds__(128, CfgTreeCc<D>::kBlocksPerSm) tree_cc_kerne
                     else
                         atomicOr(a.flags, kFlagBadPage);
                 }
-                row_off[tid] = off;
+                row_offs[tid] = off;
+                __syncthreads();
+                load(t0, buf);
+            } else if (C::kBufs == 1) {
+                __syncthreads();
+                load(t0, buf);
             }
+            copy_wait();
             __syncthreads();
-            for (int i = tid; i < C::kKeys * (D / 4); i += C::kThreads) {
-                const int key = i / (D / 4), e = i % (D / 4) * 4;
-                const long long off = row_off[key];
-                float fk[4] = {}, fv[4] = {};
-                if (off >= 0) {
-                    pool_load4(static_cast<const KV*>(a.k) + off + e, ks, fk);
-                    pool_load4(static_cast<const KV*>(a.v) + off + e, vs, fv);
-                }
-                *reinterpret_cast<float4*>(sk + key * C::kLd + e) = make_float4(fk[0], fk[1], fk[2], fk[3]);
-                *reinterpret_cast<float4*>(sv + key * D + e) = make_float4(fv[0], fv[1], fv[2], fv[3]);
-            }
-            __syncthreads();
+            const bool ahead = C::kBufs == 2 && t0 + C::kKeys < t_end && (t0 + C::kKeys) % C::kBlockTokens != 0;
+            if (ahead) load(t0 + C::kKeys, buf ^ 1);
+            const float* sk = kv + buf * C::kKv;
+            const float* sv = sk + C::kKeys * C::kLd;
+            const long long* row_off = row_offs + t0 % C::kBlockTokens;
             float x[2][4] = {};
 #pragma unroll 4
             for (int e = 0; e < D; e += 4) {

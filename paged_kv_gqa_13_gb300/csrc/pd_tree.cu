@@ -84,14 +84,16 @@ pd_status make_maps(const TreeArgs& a, pd_dtype dt, bool fp8, int D, CUtensorMap
 size_t round256(size_t x) { return (x + 255) / 256 * 256; }
 
 // Workspace: header | split descriptors | partial lse | partial o, for a grid of `ctas`.
+constexpr size_t kClaimsOff = 128;  // of TreeArgs::claims in the workspace header
+
 struct TreeSpace {
     size_t splits, lse, o, bytes;
 };
 TreeSpace space(const TreeKernels& k, int ctas, int D) {
     TreeSpace s;
-    const size_t rows = size_t(2) * ctas * k.workers * k.tile_rows * k.tiles;
+    const size_t ranges = size_t(2) * ctas * k.workers, rows = 2 * ranges * k.tile_rows * k.tiles;
     s.splits = PD_WORKSPACE_HEADER_BYTES;
-    s.lse = s.splits + round256(size_t(ctas) * k.workers * sizeof(TreeSplit));
+    s.lse = s.splits + round256((ranges + 1) * sizeof(TreeSplit));
     s.o = s.lse + round256(rows * 4);
     s.bytes = s.o + rows * D * 4;
     return s;
@@ -160,6 +162,7 @@ pd_status tree_impl(const void* q, const void* k_data, const void* v_data, const
     a.part_lse = reinterpret_cast<float*>(ws + sp.lse);
     a.part_o = reinterpret_cast<float*>(ws + sp.o);
     a.flags = reinterpret_cast<int*>(ws);
+    a.claims = reinterpret_cast<unsigned*>(ws + kClaimsOff);
     a.batch = batch;
     a.total_new = total_new;
     a.mask_words = mask_words;
@@ -199,6 +202,10 @@ pd_status tree_impl(const void* q, const void* k_data, const void* v_data, const
     const long long bound = segs * (blocks < 1 ? 1 : blocks);
     const long long ctas = (bound + kn.workers - 1) / kn.workers;
     const int grid = int(ctas < most ? ctas : most);
+    const int workers = grid * kn.workers;
+    const bool merge = workers > 1 && blocks > 1;  // otherwise no segment can be split
+    a.seg_cost = kn.seg_cost;
+    a.tails = merge && !(wide && kn.tensor && !fp8);
     cudaStream_t cs = static_cast<cudaStream_t>(stream);
     if ((st = host::allow_smem(kn.main, kn.smem)) != PD_OK) return st;
     CUtensorMap maps[3]{};
@@ -206,10 +213,9 @@ pd_status tree_impl(const void* q, const void* k_data, const void* v_data, const
     void* args[] = {&a, &maps[0], &maps[1], &maps[2]};
     cudaError_t e = cudaLaunchKernel(kn.main, dim3(grid), dim3(kn.threads), args, kn.smem, cs);
     if (e != cudaSuccess) return host::cuda_fail(e, "tree decode launch");
-    const int workers = grid * kn.workers;
-    if (workers > 1 && blocks > 1) {  // otherwise no segment can be split
+    if (merge) {
         cudaLaunchConfig_t cfg{};
-        cfg.gridDim = dim3((workers - 1) * kMergeBlocks);
+        cfg.gridDim = dim3(((a.tails ? 2 : 1) * workers - 1) * kMergeBlocks);
         cfg.blockDim = dim3(256);
         cfg.stream = cs;
         cudaLaunchAttribute attr[1];

@@ -9,14 +9,19 @@
 // a whole number of slots leaves rows of its last one unused). In a chain a
 // segment's blocks end with its last node's own token.
 //
-// Partition. The blocks of all segments, in the order (request, head tile,
-// segment, block), are one line of U units, cut into equal ranges of W = ceil(U
-// / ranges), one per worker (a CTA, or one of the two halves of one). A segment
-// inside one range is written out by its worker; one that crosses ranges leaves
-// a partial (o, lse) per worker, and the merge kernel combines them in order.
-// Only the device knows the lengths: every CTA sums the requests' units itself
-// (each thread a run of requests, one block-wide scan) and finds its place; the
-// first worker past a boundary inside a segment that starts in the range before
+// Partition. A segment costs its blocks and `seg_cost` units more (its q, its
+// output), which lie before its first block. All segments, in the order
+// (request, head tile, segment), are one line of U units, cut into shares of S
+// = ceil(U / workers); a worker is a CTA, or one of the two halves of one. SMs
+// stream at rates that differ by up to a quarter, so the last T units of every
+// share (a quarter of short shares, an eighth of long ones) are a range of
+// their own that goes to whichever worker asks first when it comes to the end
+// of what it has. The cuts are fixed: results do not depend on who runs a
+// range. A segment inside one range is written out there; one that is cut
+// leaves a partial (o, lse) in each of its ranges, and the merge kernel combines
+// them in order. Only the device knows the lengths: every CTA sums the requests'
+// units itself (each thread a run of requests, one block-wide scan) and finds
+// its shares; the range whose start is the first cut through a segment's blocks
 // writes the merge's descriptor.
 #pragma once
 
@@ -31,8 +36,8 @@ struct TreeSplit {
     int row0;        // the request's first q row + the segment's first node
     int nodes;       // nodes of the segment
     int hh;          // head tile
-    int c0;          // worker of the first part
-    int slot0;       // its partial slot; part p > 0 is in slot 2 (c0 + p)
+    int r0;          // range of the first part
+    int slot0;       // its partial slot; part p > 0 is in slot 2 (r0 + p)
     int pad[2];
 };
 
@@ -49,9 +54,10 @@ struct TreeArgs {
     float* lse;
     const float* k_scale;  // E4M3 pools
     const float* v_scale;
-    float* part_o;    // [2 * workers][seg_rows][D], normalised
-    float* part_lse;  // [2 * workers][seg_rows], log2 units
-    TreeSplit* splits;  // [workers]
+    float* part_o;    // [2 * ranges][seg_rows][D], normalised
+    float* part_lse;  // [2 * ranges][seg_rows], log2 units
+    TreeSplit* splits;  // [ranges]; the first holds a TreeLine
+    unsigned* claims;   // ranges asked for so far in this call; the merge sets it back to 0
     int* flags;
     int batch, total_new, mask_words, num_qo_heads, num_kv_heads, group;
     int page_size, num_total_pages, num_indices;
@@ -60,6 +66,8 @@ struct TreeArgs {
     int tile_shift, seg_rows;  // rows of a row tile (log2) and of a segment, as the partials are laid out
     int slot_shift, cpp, spb_shift;  // rows of a slot (log2), slots of a page, slots of a block (log2)
     FastDiv by_page, by_cpp, by_nps, by_hpt, by_hs, by_heads;  // by page_size, cpp, nps, hpt, hs, hs * num_kv_heads
+    int seg_cost;        // units that a segment costs beside its blocks
+    int tails;           // shares may have tails (a merge follows)
     int packed;          // pages are whole slots: the tokens of a block are consecutive
     float scale_log2;    // sm_scale * log2(e)
     int test_extra_tx;
@@ -132,15 +140,42 @@ __device__ __forceinline__ long long tree_cost(const TreeArgs& a, const TreeReq&
     } else {
         for (int t = 0; t < segs; ++t) sum += tree_blocks(a, r, t);
     }
+    sum += (long long)segs * a.seg_cost;
     return sum * a.hs * a.num_kv_heads;
 }
 
-// A worker's place on the line of units, and the walk over its segments.
+// ceil(x / y); most lines are short enough for a 32-bit division.
+__device__ __forceinline__ long long tree_ceil_div(long long x, int y) {
+    return x < 0x7fffffffll - y ? (unsigned(x) + unsigned(y) - 1u) / unsigned(y) : (x + y - 1) / y;
+}
+
+// The line of units and its cuts: range r is share r, or (with tails) r / 2 is
+// the share and r % 2 its tail.
+struct TreeLine {
+    long long total, share, tail;
+    __device__ __forceinline__ static TreeLine of(const TreeArgs& a, long long total, int workers) {
+        TreeLine l;
+        l.total = total;
+        l.share = tree_ceil_div(total, workers);
+        l.tail = !a.tails || l.share < 48 ? 0 : l.share / 8;
+        return l;
+    }
+    __device__ __forceinline__ long long start(int r) const {
+        return tail == 0 ? r * share : (r / 2 + 1) * share - (r % 2 != 0 ? tail : share);
+    }
+    __device__ __forceinline__ long long end(int r) const { return min(start(r + 1), total); }
+    __device__ __forceinline__ int range_of(long long u) const {
+        const int s = u < 0x7fffffffll ? int(unsigned(u) / unsigned(share)) : int(u / share);
+        return tail == 0 ? s : 2 * s + (u - s * share >= share - tail ? 1 : 0);
+    }
+};
+
+// A range and the walk over its segments.
 struct TreeWalk {
-    int worker;
-    int b, hh, tau, blk;
-    long long unit, end;  // current unit and the end of this worker's range
-    long long W;
+    int range;
+    int b, hh, tau;
+    int pos;                     // unit within the segment: its blocks start at seg_cost
+    long long unit, begin, end;  // current unit; the range
     TreeReq r;
 
     // One portion of a segment: blocks [blk0, blk1) of nblk.
@@ -155,53 +190,120 @@ struct TreeWalk {
     };
 
     __device__ __forceinline__ bool next(const TreeArgs& a, Seg* s) {
-        if (unit >= end) return false;
-        while (tau * a.nps >= r.n) {  // past the request's last segment
-            tau = 0;
-            if (++hh >= a.hs * a.num_kv_heads || r.n == 0) {
-                hh = 0;
-                if (++b >= a.batch) return false;
-                r = tree_request(a, b);
+        while (unit < end) {
+            while (tau * a.nps >= r.n) {  // past the request's last segment
+                tau = 0;
+                if (++hh >= a.hs * a.num_kv_heads || r.n == 0) {
+                    hh = 0;
+                    if (++b >= a.batch) return false;
+                    r = tree_request(a, b);
+                }
+            }
+            const int nblk = tree_blocks(a, r, tau), cost = nblk + a.seg_cost;
+            const long long first = unit - pos + a.seg_cost;  // unit of the segment's first block
+            const int take = int(min((long long)(cost - pos), end - unit));
+            s->blk0 = max(0, pos - a.seg_cost);
+            s->blk1 = max(0, pos + take - a.seg_cost);
+            s->node0 = tau * a.nps;
+            unit += take;
+            pos = 0;
+            ++tau;
+            if (s->blk1 <= s->blk0) continue;  // the range ends before the segment's first block
+            s->r = r;
+            s->hh = hh;
+            s->kvh = a.by_hs.div(hh);
+            const int h0 = (hh - s->kvh * a.hs) * a.hpt;
+            s->head0 = s->kvh * a.group + h0;
+            s->heads = min(a.hpt, a.group - h0);
+            s->nodes = min(a.nps, r.n - s->node0);
+            s->row0 = r.start + s->node0;
+            s->tail0 = tree_slot_of(a, max(0, r.ctx())) >> a.spb_shift;
+            s->slots = tree_slots(a, r.len);
+            s->slot = s->blk0 == 0 && s->blk1 == nblk ? -1 : 2 * range + (first > begin ? 1 : 0);
+            return true;
+        }
+        return false;
+    }
+
+    // The place of unit `left` of request b's units.
+    __device__ __forceinline__ void place(const TreeArgs& a, int request, const TreeReq& req, long long cost, long long left) {
+        b = request;
+        r = req;
+        if (cost < 0x7fffffffll) {
+            const int each = a.by_heads.div(int(cost));
+            hh = int(unsigned(left) / unsigned(each));
+            left -= (long long)hh * each;
+        } else {
+            const long long each = cost / (a.hs * a.num_kv_heads);
+            hh = int(left / each);
+            left -= hh * each;
+        }
+        for (tau = 0;; ++tau) {
+            const int c = tree_blocks(a, r, tau) + a.seg_cost;
+            if (left < c) break;
+            left -= c;
+        }
+        pos = int(left);
+    }
+
+    // The merge's descriptor of a segment whose first cut is this range's start. One thread, before next().
+    __device__ __forceinline__ void write_split(const TreeArgs& a, const TreeLine& line) const {
+        TreeSplit s{};
+        if (unit < end && range > 0) {
+            const long long first = unit - pos + a.seg_cost, prev = line.start(range - 1);
+            if (first < unit && first >= prev) {
+                s.r0 = range - 1;
+                s.parts = line.range_of(first + tree_blocks(a, r, tau) - 1) - s.r0 + 1;
+                s.slot0 = 2 * s.r0 + (first > prev ? 1 : 0);
+                s.hh = hh;
+                s.row0 = r.start + tau * a.nps;
+                s.nodes = min(a.nps, r.n - tau * a.nps);
             }
         }
-        const int nblk = tree_blocks(a, r, tau);
-        s->r = r;
-        s->hh = hh;
-        s->kvh = a.by_hs.div(hh);
-        const int h0 = (hh - s->kvh * a.hs) * a.hpt;
-        s->head0 = s->kvh * a.group + h0;
-        s->heads = min(a.hpt, a.group - h0);
-        s->node0 = tau * a.nps;
-        s->nodes = min(a.nps, r.n - s->node0);
-        s->row0 = r.start + s->node0;
-        s->blk0 = blk;
-        s->blk1 = int(min((long long)nblk, blk + (end - unit)));
-        s->tail0 = tree_slot_of(a, max(0, r.ctx())) >> a.spb_shift;
-        s->slots = tree_slots(a, r.len);
-        const long long begin = unit - blk;
-        s->slot = (blk == 0 && s->blk1 == nblk) ? -1 : 2 * worker + (begin > worker * W ? 1 : 0);
-        unit += s->blk1 - s->blk0;
-        blk = 0;
-        ++tau;
-        return true;
+        if (range > 0) a.splits[range] = s;
+    }
+
+    // Find range `rg` by a whole warp: each lane sums a run of requests.
+    __device__ __forceinline__ void locate(const TreeArgs& a, const TreeLine& line, int rg) {
+        const int lane = threadIdx.x & 31;
+        const int per = (a.batch + 31) / 32, b0 = min(lane * per, a.batch), b1 = min(b0 + per, a.batch);
+        range = rg;
+        unit = begin = line.start(rg);
+        end = line.end(rg);
+        long long mine = 0;
+        for (int x = b0; x < b1; ++x) mine += tree_cost(a, tree_request(a, x));
+        long long inc = mine;
+#pragma unroll
+        for (int off = 1; off < 32; off <<= 1) {
+            const long long y = __shfl_up_sync(kFull, inc, off);
+            if (lane >= off) inc += y;
+        }
+        long long left = unit - (inc - mine);
+        const unsigned here = __ballot_sync(kFull, left >= 0 && left < mine);
+        const int src = __ffs(here) - 1;  // some lane: the range is not empty
+        left = __shfl_sync(kFull, left, src);
+        for (int x = src * per;; ++x) {
+            const TreeReq req = tree_request(a, x);
+            const long long c = tree_cost(a, req);
+            if (left < c) {
+                place(a, x, req, c, left);
+                return;
+            }
+            left -= c;
+        }
     }
 };
 
 struct TreePlanScratch {
     long long sums[32];
-    long long total, W;
+    long long total;
     struct {
-        int b, hh, tau, blk;
+        int b, hh, tau, pos;
         TreeReq r;
     } at[2];  // where each worker of the CTA starts
 };
 
-// ceil(x / y); most lines are short enough for a 32-bit division.
-__device__ __forceinline__ long long tree_ceil_div(long long x, int y) {
-    return x < 0x7fffffffll - y ? (unsigned(x) + unsigned(y) - 1u) / unsigned(y) : (x + y - 1) / y;
-}
-
-// Find the ranges of this CTA's kWorkers workers. All threads of the block
+// Find the shares of this CTA's kWorkers workers. All threads of the block
 // call it; ends with a block barrier, after which tree_start gives the walks.
 template <int kWorkers>
 __device__ __forceinline__ void tree_plan(const TreeArgs& a, TreePlanScratch* sc) {
@@ -229,14 +331,14 @@ __device__ __forceinline__ void tree_plan(const TreeArgs& a, TreePlanScratch* sc
         if (w < wid) before += x;
         total += x;
     }
-    const long long W = tree_ceil_div(total, int(gridDim.x) * kWorkers);
+    const TreeLine line = TreeLine::of(a, total, int(gridDim.x) * kWorkers);
     if (tid == 0) {
         sc->total = total;
-        sc->W = W;
+        if (blockIdx.x == 0) *reinterpret_cast<TreeLine*>(a.splits) = line;
     }
 #pragma unroll
     for (int k = 0; k < kWorkers; ++k) {
-        const long long unit = ((long long)blockIdx.x * kWorkers + k) * W;
+        const long long unit = ((long long)blockIdx.x * kWorkers + k) * line.share;
         if (unit >= total || unit < before || unit >= before + mine) continue;
         long long left = unit - before;
         for (int b = b0; b < b1; ++b) {
@@ -246,64 +348,43 @@ __device__ __forceinline__ void tree_plan(const TreeArgs& a, TreePlanScratch* sc
                 left -= c;
                 continue;
             }
-            if (c < 0x7fffffffll) {
-                const int each = a.by_heads.div(int(c)), hh = int(unsigned(left) / unsigned(each));
-                sc->at[k].hh = hh;
-                left -= (long long)hh * each;
-            } else {
-                const long long each = c / (a.hs * a.num_kv_heads);
-                sc->at[k].hh = int(left / each);
-                left %= each;
-            }
-            int tau = 0;
-            for (;; ++tau) {
-                const int nb = tree_blocks(a, r, tau);
-                if (left < nb) break;
-                left -= nb;
-            }
-            sc->at[k].tau = tau;
-            sc->at[k].blk = int(left);
-            sc->at[k].r = r;
-            sc->at[k].b = b;
+            TreeWalk w;
+            w.place(a, b, r, c, left);
+            sc->at[k] = {b, w.hh, w.tau, w.pos, r};
             break;
         }
     }
     __syncthreads();
 }
 
-// The walk of worker k of this CTA.
+// The line, and the walk over the share (without its tail) of worker k of this CTA.
 template <int kWorkers>
-__device__ __forceinline__ TreeWalk tree_start(const TreePlanScratch* sc, int k) {
+__device__ __forceinline__ TreeLine tree_line(const TreeArgs& a, const TreePlanScratch* sc) {
+    return TreeLine::of(a, sc->total, int(gridDim.x) * kWorkers);
+}
+template <int kWorkers>
+__device__ __forceinline__ TreeWalk tree_start(const TreeLine& line, const TreePlanScratch* sc, int k) {
     TreeWalk w;
-    w.worker = int(blockIdx.x) * kWorkers + k;
-    w.W = sc->W;
-    w.unit = w.worker * w.W;
-    w.end = min(w.unit + w.W, sc->total);
+    const int worker = int(blockIdx.x) * kWorkers + k;
+    w.range = line.tail == 0 ? worker : 2 * worker;
+    w.unit = w.begin = line.start(w.range);
     w.b = sc->at[k].b;
     w.hh = sc->at[k].hh;
     w.tau = sc->at[k].tau;
-    w.blk = sc->at[k].blk;
+    w.pos = sc->at[k].pos;
     w.r = sc->at[k].r;
-    if (w.b < 0) w.end = w.unit;
+    w.end = w.b < 0 ? w.unit : line.end(w.range);
     return w;
 }
 
-// The merge's descriptor of a segment that starts in the range before the
-// worker's and reaches into its own (w: the walk as it starts). One thread.
-__device__ __forceinline__ void tree_split(const TreeArgs& a, const TreeWalk& w) {
-    TreeSplit s{};
-    const long long begin = w.unit - w.blk, prev = w.unit - w.W;
-    if (w.b >= 0 && w.blk > 0 && begin >= prev) {
-        const long long stop = begin + tree_blocks(a, w.r, w.tau);
-        const long long last = stop <= 0x7fffffffll ? unsigned(stop - 1) / unsigned(w.W) : (stop - 1) / w.W;
-        s.c0 = w.worker - 1;
-        s.parts = int(last) - s.c0 + 1;
-        s.slot0 = 2 * s.c0 + (begin > prev ? 1 : 0);
-        s.hh = w.hh;
-        s.row0 = w.r.start + w.tau * a.nps;
-        s.nodes = min(a.nps, w.r.n - w.tau * a.nps);
-    }
-    a.splits[w.worker] = s;
+// The next tail that nobody has asked for, by a whole warp. false: none.
+__device__ __forceinline__ bool tree_claim(const TreeArgs& a, const TreeLine& line, int* range) {
+    if (line.tail == 0) return false;
+    int t = 0;
+    if ((threadIdx.x & 31) == 0) t = int(atomicAdd(a.claims, 1u));
+    t = __shfl_sync(kFull, t, 0);
+    *range = 2 * t + 1;
+    return line.start(*range) < line.total;
 }
 
 // Which of 32 consecutive tokens t0 .. t0 + 31 (only the first `count` stand
@@ -334,19 +415,23 @@ __device__ __forceinline__ long long tree_row(const TreeArgs& a, int row0, int n
 
 constexpr int kMergeBlocks = 4;  // blocks per possible split
 
-// One warp per row of a split segment at a time: parts in worker order.
+// One warp per row of a split segment at a time: parts in the order of the line.
 template <typename T, int D>
 __global__ void __launch_bounds__(256) tree_merge_kernel(const TreeArgs a) {
     constexpr int kPer = D / 32;
     const float kNegInf = -__int_as_float(0x7f800000);
     grid_dependency_wait();
-    const TreeSplit s = a.splits[blockIdx.x / kMergeBlocks + 1];
+    if (blockIdx.x == 0 && threadIdx.x == 0) *a.claims = 0;
+    const int range = int(blockIdx.x / kMergeBlocks) + 1;
+    const TreeLine line = *reinterpret_cast<const TreeLine*>(a.splits);
+    if (line.start(range) >= line.total) return;
+    const TreeSplit s = a.splits[range];
     if (s.parts == 0) return;
     for (int i = int(blockIdx.x % kMergeBlocks) * 8 + (threadIdx.x >> 5); i < s.nodes * a.hpt; i += 8 * kMergeBlocks) {
         const int per_tile = a.npt * a.hpt, tile = i / per_tile, row = (tile << a.tile_shift) + i - tile * per_tile;
         const long long at = tree_row(a, s.row0, s.nodes, s.hh, row);
         if (at < 0) continue;  // past the group's last head
-        auto slot = [&](int p) { return size_t(p == 0 ? s.slot0 : 2 * (s.c0 + p)) * a.seg_rows + row; };
+        auto slot = [&](int p) { return size_t(p == 0 ? s.slot0 : 2 * (s.r0 + p)) * a.seg_rows + row; };
         float acc[kPer] = {};
         const float L = merge_rows<kPer, 8>(
             s.parts, [&](int p) { return a.part_lse[slot(p)]; }, [&](int p) { return a.part_o + slot(p) * D; }, acc);
@@ -413,11 +498,26 @@ __global__ void __launch_bounds__(128, CfgTreeCc<D>::kBlocksPerSm) tree_cc_kerne
     float* sp = kv + C::kBufs * C::kKv;
     const int tid = threadIdx.x, tr = tid >> 3, tc = tid & 7;
     tree_plan<1>(a, &plan);
-    TreeWalk walk = tree_start<1>(&plan, 0);
-    if (tid == 0) tree_split(a, walk);
+    const TreeLine line = tree_line<1>(a, &plan);
+    TreeWalk walk = tree_start<1>(line, &plan, 0);
+    if (tid == 0) walk.write_split(a, line);
     launch_dependents();
     TreeWalk::Seg s;
-    while (walk.next(a, &s)) {
+    for (;;) {
+        if (!walk.next(a, &s)) {
+            __shared__ int claimed;
+            __syncthreads();
+            if (tid < 32) {
+                int range;
+                const bool got = tree_claim(a, line, &range);
+                if (tid == 0) claimed = got ? range : -1;
+            }
+            __syncthreads();
+            if (claimed < 0) break;
+            walk.locate(a, line, claimed);
+            if (tid == 0) walk.write_split(a, line);
+            continue;
+        }
         __syncthreads();
         const float ks = a.k_scale != nullptr ? __ldg(a.k_scale + s.kvh) : 1.f;
         const float vs = a.v_scale != nullptr ? __ldg(a.v_scale + s.kvh) : 1.f;

@@ -10,6 +10,7 @@ struct TreeKernels {
     int tile_rows, tiles;       // rows of a row tile, row tiles per segment
     int workers;                // independent ranges of work per CTA
     int block_tokens;           // tokens of a key block
+    int seg_cost;               // TreeArgs::seg_cost
     bool tensor;                // main takes tensor maps of q, K and V
 };
 

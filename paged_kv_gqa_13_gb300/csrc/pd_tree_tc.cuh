@@ -189,6 +189,8 @@ struct CfgTree {
     static constexpr int kThreads = round_up(32 * (kSoftWarps + kLines * kOthers), 128);
     static constexpr int kWalkers = kOthers + 4 * kPipes;  // warps that read a line's segments
     static constexpr int kSegRing = 8;
+    static constexpr int kClaimAhead = kWide ? 3 : 5;
+    static constexpr int kSegCost = kWide ? (kFp8 ? 3 : 0) : 3;       // see TreeArgs::seg_cost: an output takes about 5,000 cycles
     static constexpr int kBadRing = 16;  // more than the K blocks that the producers are ahead of the softmax warps
     // a line's barriers (8 bytes each); those of S buffer b of pipeline p at 2 p + b
     static constexpr int kFull = 0, kEmpty = kFull + kSlots, kVok = kEmpty + kSlots, kQFull = kVok + kSlots,
@@ -320,7 +322,8 @@ __global__ void __launch_bounds__(CfgTree<D, kWide, kFp8>::kThreads, 1)
     tree_plan<C::kLines>(a, plan);
     TreeWalk walk;
     const bool walker = !soft && !idle && part == C::kPipes + C::kProducers;
-    if (walker) walk = tree_start<C::kLines>(plan, line);
+    const TreeLine cuts = tree_line<C::kLines>(a, plan);
+    if (walker) walk = tree_start<C::kLines>(cuts, plan, line);
     tc_fence_before();
     __syncthreads();  // the walks have been read: copies may land
     tc_fence_after();
@@ -542,43 +545,57 @@ __global__ void __launch_bounds__(CfgTree<D, kWide, kFp8>::kThreads, 1)
         int loads = 0;
         bool ok = true, more = walker;
         int walked = 0;
-        const TreeWalk first = walk;
-        for (int i = 0; ok; ++i) {
-            // Keep the ring of segments full; wait for a place only when fewer than four are ahead.
-            while (more && walked < i + C::kSegRing) {
-                if (walked >= C::kSegRing) {
-                    const int place = C::kSegFree + walked % C::kSegRing;
-                    const uint32_t phase = seg_phase(walked) ^ 1u;
-                    if (walked > i + 3) {
-                        if (!__all_sync(kFull, mbar_test_wait(bar(place), phase))) break;
-                    } else if (!(ok = wait(place, phase))) {
-                        break;
-                    }
+        // The next segment into its place of the ring (which is free): of this range, or (claim) of the
+        // next one that nobody has asked for, or the end. false: this range has no more.
+        auto publish = [&](bool claim) -> bool {
+            TreeWalk::Seg s;
+            TcSeg x{};
+            while (!walk.next(a, &s)) {
+                if (!claim) return false;
+                int range;
+                if (!tree_claim(a, cuts, &range)) {
+                    more = false;
+                    break;
                 }
-                TreeWalk::Seg s;
-                more = walk.next(a, &s);
-                if (lane == 0) {
-                    TcSeg x{};
-                    if (more) {
-                        x = TcSeg{s.blk0, s.blk1,  s.tail0, s.slots, s.slot,  s.row0, s.node0,   s.nodes,
-                                  s.hh,   s.head0, s.kvh,   s.r.lo,  s.r.len, s.r.n,  s.r.start, 1.f, 1.f};
-                        if (kFp8) {
-                            x.k_scale = __ldg(a.k_scale + s.kvh);
-                            x.v_scale = __ldg(a.v_scale + s.kvh);
-                        }
-                    }
-                    segs[walked % C::kSegRing] = x;
-                    mbar_arrive(bar(C::kSegFull + walked % C::kSegRing));
-                    if (walked == 0) tree_split(a, first);
-                }
-                __syncwarp();
-                ++walked;
+                walk.locate(a, cuts, range);
+                if (lane == 0) walk.write_split(a, cuts);
             }
+            if (lane == 0) {
+                if (more) {
+                    x = TcSeg{s.blk0, s.blk1,  s.tail0, s.slots, s.slot,  s.row0, s.node0,   s.nodes,
+                              s.hh,   s.head0, s.kvh,   s.r.lo,  s.r.len, s.r.n,  s.r.start, 1.f, 1.f};
+                    if (kFp8) {
+                        x.k_scale = __ldg(a.k_scale + s.kvh);
+                        x.v_scale = __ldg(a.v_scale + s.kvh);
+                    }
+                }
+                segs[walked % C::kSegRing] = x;
+                mbar_arrive(bar(C::kSegFull + walked % C::kSegRing));
+            }
+            __syncwarp();
+            ++walked;
+            return true;
+        };
+        // A place for it in the ring; wait for one only when fewer than four segments are ahead of segment i.
+        auto place = [&](int i) -> bool {
+            if (walked < C::kSegRing) return true;
+            const int b = C::kSegFree + walked % C::kSegRing;
+            const uint32_t phase = seg_phase(walked) ^ 1u;
+            return walked > i + 3 ? test(b, phase) : (ok = wait(b, phase));
+        };
+        const TreeWalk share = walk;
+        for (int i = 0; ok; ++i) {
+            while (more && walked < i + C::kSegRing && place(i) && publish(walked == i)) {
+            }
+            if (walker && i == 0 && lane == 0) share.write_split(a, cuts);
             if (!ok || !seg_wait(i)) break;
             const TcSeg& s = seg_at(i);
             const int blk1 = s.blk1, tail0 = s.tail0, len = s.len, ctx = s.len - s.n;
             if (s.blk0 == blk1) break;
             for (int blk = s.blk0; blk < blk1; ++blk) {
+                // ask for more work a few blocks before the last segment's end, so that its copies follow on
+                if (more && walked == i + 1 && blk + C::kClaimAhead >= blk1 && place(i)) publish(true);
+                if (!ok) break;
                 if constexpr (kFp8) {
                     // codes to f16 (exact), 8 at a time, into the operand layout: K, then V
                     for (int kv = 0; kv < 2; ++kv, ++loads, ring.next(), stage.next()) {
@@ -917,6 +934,7 @@ TreeKernels tree_tc_kernels() {
     k.tiles = C::kPipes;
     k.workers = C::kLines;
     k.block_tokens = C::kKeys;
+    k.seg_cost = C::kSegCost;
     k.tensor = true;
     return k;
 }

@@ -344,11 +344,12 @@ struct CommitArgs {
 
 // One warp per (request, kv head): row first + path[i] moves to row first + i,
 // first the request's first new row, for K (chunks 0 .. n - 1 of 16 bytes) and
-// V (the next n). A lane owns whole columns of chunks and walks the path in
-// order, kRound rows at a time, loads before stores. A path increases, so
-// path[i] >= i: no row is written before it has been read.
+// V (the next n). Lane i finds the places of the path's node i, 32 at a time;
+// then a lane owns whole columns of chunks and walks them in order, kRound rows
+// at a time, loads before stores. A path increases, so path[i] >= i: no row is
+// written before it has been read.
 __global__ void __launch_bounds__(128) commit_kernel(const CommitArgs a) {
-    constexpr int kRound = 4;
+    constexpr int kRound = 8;
     const int lane = threadIdx.x & 31;
     const long long w = (long long)blockIdx.x * 4 + (threadIdx.x >> 5);
     if (w >= (long long)a.batch * a.hk) return;
@@ -357,6 +358,8 @@ __global__ void __launch_bounds__(128) commit_kernel(const CommitArgs a) {
     const int s = __ldg(a.new_indptr + b), e = __ldg(a.new_indptr + b + 1);
     const int lo = __ldg(a.indptr + b), hi = __ldg(a.indptr + b + 1);
     const int last = __ldg(a.last_page_len + b);
+    const int32_t* path = a.path + (long long)b * a.max_path;
+    int mine = lane < a.max_path ? __ldg(path + lane) : 0;  // this lane's node of the first 32
     if (len == 0) return;
     int bad = 0;
     const long long kv = ((long long)hi - lo - 1) * a.page_size + last;
@@ -370,12 +373,15 @@ __global__ void __launch_bounds__(128) commit_kernel(const CommitArgs a) {
         bad = kFlagBadNewRows;
     else if (len < 0 || len > a.max_path)
         bad = kFlagBadPath;
-    const int32_t* path = a.path + (long long)b * a.max_path;
     if (bad == 0) {
         bool wrong = false;
-        for (int i = lane; i < len; i += 32) {
-            const int node = __ldg(path + i);
-            wrong |= node < 0 || node >= e - s || (i > 0 && node <= __ldg(path + i - 1));
+        int before = -1;  // the last node of the 32 before
+        for (int i0 = 0; i0 < len; i0 += 32) {
+            const int node = i0 == 0 ? mine : i0 + lane < len ? __ldg(path + i0 + lane) : 0;
+            int prev = __shfl_up_sync(kFull, node, 1);
+            if (lane == 0) prev = before;
+            before = __shfl_sync(kFull, node, 31);
+            wrong |= i0 + lane < len && (node <= prev || node >= e - s);
         }
         if (__any_sync(kFull, wrong)) bad = kFlagBadPath;
     }
@@ -387,38 +393,48 @@ __global__ void __launch_bounds__(128) commit_kernel(const CommitArgs a) {
     const int chunks = a.row_bytes / 16;
     // byte offset of the request's row `at` of this kv head; false: a bad page
     auto locate = [&](long long at, size_t* off) {
-        const int page = __ldg(a.indices + lo + int(at / a.page_size));
-        *off = ((size_t(page) * a.hk + kh) * a.page_size + size_t(at % a.page_size)) * a.row_bytes;
+        const int nth = int(at / a.page_size), page = __ldg(a.indices + lo + nth);
+        *off = ((size_t(page) * a.hk + kh) * a.page_size + size_t(at - (long long)nth * a.page_size)) * a.row_bytes;
         return page >= 0 && page < a.num_total_pages;
     };
     bool bad_page = false;
-    for (int i0 = 0; i0 < len; i0 += kRound) {
-        size_t from[kRound], to[kRound];
-        bool move[kRound];
+    for (int i0 = 0; i0 < len; i0 += 32) {
+        if (i0 > 0) mine = i0 + lane < len ? __ldg(path + i0 + lane) : 0;
+        size_t from = 0, to = 0;
+        bool go = i0 + lane < len && mine != i0 + lane;
+        if (go) {
+            const bool fine = locate(first + mine, &from) & locate(first + i0 + lane, &to);
+            bad_page |= !fine;
+            go = fine;
+        }
+        const unsigned moves = __ballot_sync(kFull, go);
+        for (unsigned rest = moves; rest != 0u;) {
+            size_t src[kRound], dst[kRound];
+            int n = 0;
 #pragma unroll
-        for (int r = 0; r < kRound; ++r) {
-            move[r] = i0 + r < len;
-            const int node = move[r] ? __ldg(path + i0 + r) : 0;
-            if (move[r] && node == i0 + r) move[r] = false;
-            if (move[r]) {
-                const bool fine = locate(first + node, &from[r]) & locate(first + i0 + r, &to[r]);
-                bad_page |= !fine;
-                move[r] = fine;
+            for (int r = 0; r < kRound; ++r) {
+                if (rest != 0u) {
+                    const int x = __ffs(rest) - 1;
+                    rest &= rest - 1u;
+                    src[r] = __shfl_sync(kFull, from, x);
+                    dst[r] = __shfl_sync(kFull, to, x);
+                    n = r + 1;
+                }
+            }
+            for (int c = lane; c < 2 * chunks; c += 32) {
+                uint8_t* pool = c < chunks ? a.k_data : a.v_data;
+                const size_t at = size_t(c < chunks ? c : c - chunks) * 16;
+                uint4 x[kRound];
+#pragma unroll
+                for (int r = 0; r < kRound; ++r)
+                    if (r < n) x[r] = *reinterpret_cast<const uint4*>(pool + src[r] + at);
+#pragma unroll
+                for (int r = 0; r < kRound; ++r)
+                    if (r < n) *reinterpret_cast<uint4*>(pool + dst[r] + at) = x[r];
             }
         }
-        for (int c = lane; c < 2 * chunks; c += 32) {
-            uint8_t* pool = c < chunks ? a.k_data : a.v_data;
-            const size_t at = size_t(c < chunks ? c : c - chunks) * 16;
-            uint4 x[kRound];
-#pragma unroll
-            for (int r = 0; r < kRound; ++r)
-                if (move[r]) x[r] = *reinterpret_cast<const uint4*>(pool + from[r] + at);
-#pragma unroll
-            for (int r = 0; r < kRound; ++r)
-                if (move[r]) *reinterpret_cast<uint4*>(pool + to[r] + at) = x[r];
-        }
     }
-    if (bad_page && lane == 0 && kh == 0) atomicOr(a.flags, kFlagBadPage);
+    if (__any_sync(kFull, bad_page) && lane == 0 && kh == 0) atomicOr(a.flags, kFlagBadPage);
 }
 
 // Checks shared by pd_rope and the appends.

@@ -375,7 +375,7 @@ pd_status pd_profile_enable(int enable);
  * Test-only failure injection for the bounded waits. While extra_bytes is
  * nonzero (a multiple of 16, at most 1 MiB), every decode call's first warp
  * waits, for its first pipeline stage, for extra_bytes more than its copies
- * deliver. Its wait gives up after its limit (2 s), sets
+ * deliver (the tensor-core tree decode: its first CTA, for its first copy). Its wait gives up after its limit (2 s), sets
  * PD_FLAG_WAIT_TIMEOUT in the status word, lets its other stages' copies
  * land, and returns; the outputs of the requests it held are then undefined,
  * and the GPU context stays usable. 0 (the default) turns it off.

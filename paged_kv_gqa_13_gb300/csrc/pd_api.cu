@@ -628,6 +628,7 @@ pd_status sm_count(int* sms) {
     return st;
 }
 pd_status allow_smem(const void* fn, int bytes) { return ::allow_smem(fn, bytes); }
+int test_extra_tx() { return g_inject_extra_tx.load(std::memory_order_relaxed); }
 PFN_cuTensorMapEncodeTiled_v12000 tensor_map_encoder() { return ::tensor_map_encoder(); }
 
 }  // namespace host

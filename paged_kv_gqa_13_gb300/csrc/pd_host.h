@@ -19,6 +19,8 @@ pd_status cuda_fail(cudaError_t e, const char* what);
 pd_status check_workspace(void* ws, size_t have, size_t need);
 pd_status sm_count(int* sms);
 pd_status allow_smem(const void* fn, int bytes);
+// pd_test_inject_wait_timeout's extra bytes (0: off).
+int test_extra_tx();
 // The driver's tensor-map encoder; null when the driver does not offer it.
 PFN_cuTensorMapEncodeTiled_v12000 tensor_map_encoder();
 

@@ -195,6 +195,7 @@ pd_status tree_impl(const void* q, const void* k_data, const void* v_data, const
     a.by_hs = FastDiv::of(a.hs);
     a.by_heads = FastDiv::of(a.hs * Hk);
     a.scale_log2 = sm_scale * kLog2e;
+    a.test_extra_tx = host::test_extra_tx();
 
     // No more CTAs than there can be units: segments x key blocks of the longest possible request.
     const long long segs = ((long long)total_new / a.nps + batch) * a.hs * Hk;

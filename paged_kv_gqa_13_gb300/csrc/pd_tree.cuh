@@ -70,7 +70,7 @@ struct TreeArgs {
     int tails;           // shares may have tails (a merge follows)
     int packed;          // pages are whole slots: the tokens of a block are consecutive
     float scale_log2;    // sm_scale * log2(e)
-    int test_extra_tx;
+    int test_extra_tx;   // test-only wait-timeout injection (pd_test_inject_wait_timeout); normally 0
 };
 
 // One request as the table gives it. A bad one keeps its nodes and loses its

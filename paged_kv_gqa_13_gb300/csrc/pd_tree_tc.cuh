@@ -497,7 +497,9 @@ __global__ void __launch_bounds__(CfgTree<D, kWide, kFp8>::kThreads, 1)
                         if (bits != 0u) atomicOr(a.flags, kFlagBadPage);
                     }
                 }
-                if (lane == 0) mbar_arrive_expect_tx(bar(kPlaceFull + ring.slot), kPlaceBytes);
+                // (test-only: the first copy of all waits for bytes that never arrive)
+                const int extra = loads == 0 && blockIdx.x == 0 && line == 0 ? a.test_extra_tx : 0;
+                if (lane == 0) mbar_arrive_expect_tx(bar(kPlaceFull + ring.slot), uint32_t(kPlaceBytes + extra));
                 __syncwarp();
                 if (sl < spb)
                     tma_load_4d(sbase + kPlaceOff + ring.slot * kPlaceBytes + hf * (C::kKeys * 128) + (sl << a.slot_shift) * kRowBytes,

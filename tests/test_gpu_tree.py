@@ -307,3 +307,24 @@ def test_q_of_extreme_size_over_e4m3_pools(dtype, size):
     scale = 0.1 / size
     o, lse, _ = _run(c, q, masks, 1, scale, dtype)
     check_tree(o, lse, tree_reference(c, q, masks, float(np.float32(scale))), dtype)
+
+
+@pytest.mark.parametrize("fp8", [False, True])
+@pytest.mark.parametrize("n", [3, 90])
+def test_a_copy_that_never_lands_is_reported_and_later_calls_are_right(fp8, n):
+    import paged_kv_gqa_13_gb300 as pd
+
+    c = Paged([40000, 100], [n, 3], 2, 128, 16, "bf16", fp8=fp8)  # long enough for the first CTA to have a copy
+    q = torch.randn(n + 3, 4, 128).bfloat16()
+    masks = [tree_bits(np.random.default_rng(0), m) for m in c.new]
+    ws = pd.alloc_workspace(pd.pd_paged_tree_decode_workspace_bytes(4, 2, 128, pd.PD_BF16))
+    pd.pd_test_inject_wait_timeout(16)
+    try:
+        _, _, flags = _run(c, q, masks, 3, 0.1, "bf16", ws=ws)
+    finally:
+        pd.pd_test_inject_wait_timeout(0)
+    assert flags & pd.PD_FLAG_WAIT_TIMEOUT
+    pd.pd_workspace_init(ws)
+    o, lse, flags = _run(c, q, masks, 3, 0.1, "bf16", ws=ws)
+    assert flags == 0
+    check_tree(o, lse, tree_reference(c, q, masks, 0.1), "bf16")

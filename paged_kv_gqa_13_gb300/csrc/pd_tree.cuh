@@ -68,6 +68,7 @@ struct TreeArgs {
     FastDiv by_page, by_cpp, by_nps, by_hpt, by_hs, by_heads;  // by page_size, cpp, nps, hpt, hs, hs * num_kv_heads
     int seg_cost;        // units that a segment costs beside its blocks
     int tails;           // shares may have tails (a merge follows)
+    int whole;           // segments are not cut: each is one unit (no merge follows)
     int packed;          // pages are whole slots: the tokens of a block are consecutive
     float scale_log2;    // sm_scale * log2(e)
     int test_extra_tx;   // test-only wait-timeout injection (pd_test_inject_wait_timeout); normally 0
@@ -132,9 +133,16 @@ __device__ __forceinline__ int tree_blocks(const TreeArgs& a, const TreeReq& r, 
     return max(1, (tree_slots(a, limit) + (1 << a.spb_shift) - 1) >> a.spb_shift);
 }
 
+// Units of segment tau.
+__device__ __forceinline__ int tree_units(const TreeArgs& a, const TreeReq& r, int tau) {
+    return a.whole ? 1 : tree_blocks(a, r, tau) + a.seg_cost;
+}
+
 __device__ __forceinline__ long long tree_cost(const TreeArgs& a, const TreeReq& r) {
     const int segs = a.by_nps.div(r.n + a.nps - 1);
     long long sum = 0;
+    if (a.whole)
+        return (long long)segs * a.hs * a.num_kv_heads;
     if (a.mask != nullptr || segs <= 1) {
         sum = segs > 0 ? (long long)segs * tree_blocks(a, r, segs - 1) : 0;
     } else {
@@ -199,11 +207,11 @@ struct TreeWalk {
                     r = tree_request(a, b);
                 }
             }
-            const int nblk = tree_blocks(a, r, tau), cost = nblk + a.seg_cost;
+            const int nblk = tree_blocks(a, r, tau), cost = a.whole ? 1 : nblk + a.seg_cost;
             const long long first = unit - pos + a.seg_cost;  // unit of the segment's first block
             const int take = int(min((long long)(cost - pos), end - unit));
-            s->blk0 = max(0, pos - a.seg_cost);
-            s->blk1 = max(0, pos + take - a.seg_cost);
+            s->blk0 = a.whole ? 0 : max(0, pos - a.seg_cost);
+            s->blk1 = a.whole ? nblk : max(0, pos + take - a.seg_cost);
             s->node0 = tau * a.nps;
             unit += take;
             pos = 0;
@@ -239,7 +247,7 @@ struct TreeWalk {
             left -= hh * each;
         }
         for (tau = 0;; ++tau) {
-            const int c = tree_blocks(a, r, tau) + a.seg_cost;
+            const int c = tree_units(a, r, tau);
             if (left < c) break;
             left -= c;
         }
@@ -249,7 +257,7 @@ struct TreeWalk {
     // The merge's descriptor of a segment whose first cut is this range's start. One thread, before next().
     __device__ __forceinline__ void write_split(const TreeArgs& a, const TreeLine& line) const {
         TreeSplit s{};
-        if (unit < end && range > 0) {
+        if (unit < end && range > 0 && !a.whole) {
             const long long first = unit - pos + a.seg_cost, prev = line.start(range - 1);
             if (first < unit && first >= prev) {
                 s.r0 = range - 1;
@@ -310,11 +318,13 @@ __device__ __forceinline__ void tree_plan(const TreeArgs& a, TreePlanScratch* sc
     const int tid = threadIdx.x, lane = tid & 31, wid = tid >> 5, nt = blockDim.x, nw = nt >> 5;
     const int per = (a.batch + nt - 1) / nt;
     const int b0 = min(tid * per, a.batch), b1 = min(b0 + per, a.batch);
-    long long mine = 0;
+    long long mine = 0, last = 0;
+    TreeReq r{};
     for (int b = b0; b < b1; ++b) {
-        const TreeReq r = tree_request(a, b);
+        r = tree_request(a, b);
         if (r.bad != 0 && blockIdx.x == 0) atomicOr(a.flags, r.bad);
-        mine += tree_cost(a, r);
+        last = tree_cost(a, r);
+        mine += last;
     }
     long long inc = mine;
 #pragma unroll
@@ -326,7 +336,7 @@ __device__ __forceinline__ void tree_plan(const TreeArgs& a, TreePlanScratch* sc
     if (tid < kWorkers) sc->at[tid].b = -1;
     __syncthreads();
     long long before = inc - mine, total = 0;
-    for (int w = 0; w < nw; ++w) {
+    for (int w = 0; w < min(nw, (a.batch + 31) / 32); ++w) {  // the others hold no request
         const long long x = sc->sums[w];
         if (w < wid) before += x;
         total += x;
@@ -342,8 +352,8 @@ __device__ __forceinline__ void tree_plan(const TreeArgs& a, TreePlanScratch* sc
         if (unit >= total || unit < before || unit >= before + mine) continue;
         long long left = unit - before;
         for (int b = b0; b < b1; ++b) {
-            const TreeReq r = tree_request(a, b);
-            const long long c = tree_cost(a, r);
+            if (b1 - b0 > 1) r = tree_request(a, b);  // (one request per thread: r is it)
+            const long long c = b1 - b0 > 1 ? tree_cost(a, r) : last;
             if (left >= c) {
                 left -= c;
                 continue;
@@ -470,11 +480,14 @@ __device__ __forceinline__ void copy_wait() { asm volatile("cp.async.wait_all;" 
 
 template <int D>
 struct CfgTreeCc {
-    static constexpr int kRows = 32, kKeys = 32, kThreads = 128, kBlockTokens = 128;
+    static constexpr int kRows = 32, kKeys = 32, kThreads = 128;
+    static constexpr int kBlockTokens = 32;  // short, so that a small call spreads over SMs
+    static constexpr int kWindow = 128;      // tokens whose rows are looked up at a time
     static constexpr int kLd = D + 4;  // row step of q and K in shared memory: 16-byte reads of 8 rows hit all banks
     static constexpr int kBufs = D == 256 ? 1 : 2;   // of K and V: the next keys on their way
+    static constexpr int kLdP = kKeys + 4;           // row step of the weights: 16-byte reads
     static constexpr int kKv = kKeys * kLd + kKeys * D;
-    static constexpr int kFloats = kRows * kLd + kBufs * kKv + kRows * (kKeys + 1);
+    static constexpr int kFloats = kRows * kLd + kBufs * kKv + kRows * kLdP;
     static constexpr int kBytes = kFloats * 4;
     static constexpr int kBlocksPerSm = D == 64 ? 4 : 2;
 };
@@ -492,7 +505,7 @@ __global__ void __launch_bounds__(128, CfgTreeCc<D>::kBlocksPerSm) tree_cc_kerne
     const float kNegInf = -__int_as_float(0x7f800000);
     extern __shared__ __align__(16) float tree_smem[];
     __shared__ TreePlanScratch plan;
-    __shared__ long long row_offs[C::kBlockTokens];  // element offset of each key's row in the pools; -1: none
+    __shared__ long long row_offs[C::kWindow];  // element offset of each key's row in the pools; -1: none
     float* sq = tree_smem;
     float* kv = sq + C::kRows * C::kLd;
     float* sp = kv + C::kBufs * C::kKv;
@@ -530,6 +543,7 @@ __global__ void __launch_bounds__(128, CfgTreeCc<D>::kBlocksPerSm) tree_cc_kerne
         }
         float m[2] = {kNegInf, kNegInf}, l[2] = {}, o[2][D / 8] = {};
         const int node[2] = {s.node0 + a.by_hpt.div(2 * tr), s.node0 + a.by_hpt.div(2 * tr + 1)};
+        int window;  // first token of row_offs
         // Keys t0 .. of the pools into buffer `buf` (zeros where there is no row): asynchronous copies of f32
         // pools, loads and conversions of others.
         auto load = [&](int t0, int buf) {
@@ -537,7 +551,7 @@ __global__ void __launch_bounds__(128, CfgTreeCc<D>::kBlocksPerSm) tree_cc_kerne
             float* sv = sk + C::kKeys * C::kLd;
             for (int i = tid; i < C::kKeys * (D / 4); i += C::kThreads) {
                 const int key = i / (D / 4), e = i % (D / 4) * 4;
-                const long long off = row_offs[t0 % C::kBlockTokens + key];
+                const long long off = row_offs[t0 - window + key];
                 if constexpr (sizeof(KV) == 4) {
                     const long long at = off < 0 ? 0 : off + e;
                     copy16_async(sk + key * C::kLd + e, static_cast<const float*>(a.k) + at, off >= 0);
@@ -555,10 +569,12 @@ __global__ void __launch_bounds__(128, CfgTreeCc<D>::kBlocksPerSm) tree_cc_kerne
             copy_commit();
         };
         const int t_end = min(s.blk1 * C::kBlockTokens, s.r.len);
+        window = s.blk0 * C::kBlockTokens - C::kWindow;
         for (int t0 = s.blk0 * C::kBlockTokens; t0 < t_end; t0 += C::kKeys) {
             const int buf = t0 / C::kKeys % C::kBufs;
-            if (t0 % C::kBlockTokens == 0) {  // the rows of a whole block at once
+            if (t0 >= window + C::kWindow) {
                 __syncthreads();
+                window = t0;
                 const int t = t0 + tid;
                 long long off = -1;
                 if (t < s.r.len) {
@@ -577,11 +593,11 @@ __global__ void __launch_bounds__(128, CfgTreeCc<D>::kBlocksPerSm) tree_cc_kerne
             }
             copy_wait();
             __syncthreads();
-            const bool ahead = C::kBufs == 2 && t0 + C::kKeys < t_end && (t0 + C::kKeys) % C::kBlockTokens != 0;
+            const bool ahead = C::kBufs == 2 && t0 + C::kKeys < t_end && t0 + C::kKeys < window + C::kWindow;
             if (ahead) load(t0 + C::kKeys, buf ^ 1);
             const float* sk = kv + buf * C::kKv;
             const float* sv = sk + C::kKeys * C::kLd;
-            const long long* row_off = row_offs + t0 % C::kBlockTokens;
+            const long long* row_off = row_offs + (t0 - window);
             float x[2][4] = {};
 #pragma unroll 4
             for (int e = 0; e < D; e += 4) {
@@ -615,7 +631,7 @@ __global__ void __launch_bounds__(128, CfgTreeCc<D>::kBlocksPerSm) tree_cc_kerne
                 for (int i = 0; i < 4; ++i) {
                     const float p = ex2(x[j][i] - mu);
                     sum += p;
-                    sp[(2 * tr + j) * (C::kKeys + 1) + tc + 8 * i] = p;
+                    sp[(2 * tr + j) * C::kLdP + tc + 8 * i] = p;
                 }
                 l[j] = l[j] * al + sum;
 #pragma unroll
@@ -624,17 +640,23 @@ __global__ void __launch_bounds__(128, CfgTreeCc<D>::kBlocksPerSm) tree_cc_kerne
             __syncwarp();
             auto accumulate = [&](auto guard) {
 #pragma unroll 2
-                for (int key = 0; key < C::kKeys; ++key) {
-                    const float p0 = sp[(2 * tr) * (C::kKeys + 1) + key], p1 = sp[(2 * tr + 1) * (C::kKeys + 1) + key];
+                for (int key4 = 0; key4 < C::kKeys; key4 += 4) {
+                    const float4 w0 = *reinterpret_cast<const float4*>(sp + (2 * tr) * C::kLdP + key4);
+                    const float4 w1 = *reinterpret_cast<const float4*>(sp + (2 * tr + 1) * C::kLdP + key4);
+                    const float p0s[4] = {w0.x, w0.y, w0.z, w0.w}, p1s[4] = {w1.x, w1.y, w1.z, w1.w};
 #pragma unroll
-                    for (int i = 0; i < D / 32; ++i) {
-                        const float4 v = *reinterpret_cast<const float4*>(sv + key * D + 4 * tc + 32 * i);
-                        const float f[4] = {v.x, v.y, v.z, v.w};
+                    for (int x = 0; x < 4; ++x) {
+                        const float p0 = p0s[x], p1 = p1s[x];
 #pragma unroll
-                        for (int c = 0; c < 4; ++c) {
-                            // a row that does not attend the key takes no part of it, not 0 * NaN either
-                            if (!decltype(guard)::value || p0 != 0.f) o[0][4 * i + c] = fmaf(p0, f[c], o[0][4 * i + c]);
-                            if (!decltype(guard)::value || p1 != 0.f) o[1][4 * i + c] = fmaf(p1, f[c], o[1][4 * i + c]);
+                        for (int i = 0; i < D / 32; ++i) {
+                            const float4 v = *reinterpret_cast<const float4*>(sv + (key4 + x) * D + 4 * tc + 32 * i);
+                            const float f[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+                            for (int c = 0; c < 4; ++c) {
+                                // a row that does not attend the key takes no part of it, not 0 * NaN either
+                                if (!decltype(guard)::value || p0 != 0.f) o[0][4 * i + c] = fmaf(p0, f[c], o[0][4 * i + c]);
+                                if (!decltype(guard)::value || p1 != 0.f) o[1][4 * i + c] = fmaf(p1, f[c], o[1][4 * i + c]);
+                            }
                         }
                     }
                 }

@@ -695,6 +695,9 @@ __global__ void __launch_bounds__(CfgTree<D, kWide, kFp8>::kThreads, 1)
         }
     } else {
         // ================================================================ softmax of pipeline p
+        // f16 weights are 2^7 times larger than their maximum-relative value: still below 2^15, and normal down
+        // to 2^-21 of the largest (bf16 has the range of f32)
+        constexpr float kShift = kBf16 ? 0.f : 7.f;
         const int pipe = wid >> 2, p = pipe % C::kPipes, row = tid & 127;
         const uint32_t lanes = uint32_t(32 * (wid & 3)) << 16;
         const uint32_t to = tmem + lanes + pipe * D, ts0 = tmem + lanes + C::kSCol + pipe * 2 * C::kJobKeys;
@@ -817,7 +820,7 @@ __global__ void __launch_bounds__(CfgTree<D, kWide, kFp8>::kThreads, 1)
                                 }
                             }
                         }
-                        const float mu = m == kNegInf ? 0.f : m;
+                        const float mu = m == kNegInf ? 0.f : m - kShift;
                         float2 sums[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
                         const float2 sc2 = make_float2(scale, scale), mu2 = make_float2(-mu, -mu);
                         uint32_t w[C::kJobKeys / 2];
@@ -847,7 +850,7 @@ __global__ void __launch_bounds__(CfgTree<D, kWide, kFp8>::kThreads, 1)
             tc_fence_after();
             if (live) {
                 const float inv = (m == kNegInf ? 0.f : 1.f / l) * s.v_scale;
-                const float lse2 = m == kNegInf ? kNegInf : m + log2f(l);
+                const float lse2 = m == kNegInf ? kNegInf : m - kShift + log2f(l);
                 const bool fix = bad_v[seg & 3] == seg + 1;
                 const size_t prow = size_t(s.slot) * a.seg_rows + row + p * C::kRows;
 #pragma unroll 1

@@ -12,6 +12,12 @@
 // element against 2 element sizes of traffic. One warp takes one token (or a
 // slice of its heads when there are few tokens), so a lane computes the sines
 // of its pairs once and uses them for every head.
+//
+// Measured: 8191 tokens of 64 f16 heads in 49.7 us, 80% of the copy rate (the
+// last wave of warps is short of work); 7000 tokens of 80 f16 heads, 16 of them
+// into an E4M3 pool, in 65 us, 62% (lookups, divisions and codes); one token
+// in 2.7 us, which is a launch and two dependent reads. A prefetch of a
+// token's rows into L2 before its lookup made both large calls 4 us longer.
 #include <cmath>
 #include <type_traits>
 
@@ -310,7 +316,10 @@ pd_status launch(RopeArgs& a, pd_dtype dt, bool fp8, int layout, cudaStream_t st
     int sms = 0;
     pd_status st = host::sm_count(&sms);
     if (st != PD_OK) return st;
-    // Few tokens: cut each token's heads into slices so that the card has about 8 warps per SM.
+    // Few tokens: cut each token's heads into slices so that the card has about 8 warps per SM. More slices make
+    // a shorter last wave and more sines and lookups: with 64 warps per SM, 8191 tokens of 64 f16 heads take 47.9
+    // instead of 49.7 us, but 9000 of 8 bf16 heads 22.5 instead of 16.4, and 7000 of 80 heads into an E4M3 pool
+    // 68.2 instead of 64.9.
     const int items = a.hq + 2 * a.hk;
     const long long want = ((long long)sms * 8 + a.tokens - 1) / a.tokens;
     a.slices = int(want < 1 ? 1 : want > (items + 3) / 4 ? (items + 3) / 4 : want);
@@ -347,7 +356,9 @@ struct CommitArgs {
 // V (the next n). Lane i finds the places of the path's node i, 32 at a time;
 // then a lane owns whole columns of chunks and walks them in order, kRound rows
 // at a time, loads before stores. A path increases, so path[i] >= i: no row is
-// written before it has been read.
+// written before it has been read. Bound by a chain of four dependent reads
+// (lengths, path, page, row): 3.2 us for 32 requests, 4.3 for 256 that keep up
+// to 12 of 64 nodes (places found one after another: 8.1).
 __global__ void __launch_bounds__(128) commit_kernel(const CommitArgs a) {
     constexpr int kRound = 8;
     const int lane = threadIdx.x & 31;

@@ -13,11 +13,11 @@
 // slice of its heads when there are few tokens), so a lane computes the sines
 // of its pairs once and uses them for every head.
 //
-// Measured: 8191 tokens of 64 f16 heads in 49.7 us, 80% of the copy rate (the
+// Measured: 8191 tokens of 64 f16 heads in 45.1 us, 88% of the copy rate (the
 // last wave of warps is short of work); 7000 tokens of 80 f16 heads, 16 of them
-// into an E4M3 pool, in 65 us, 62% (lookups, divisions and codes); one token
-// in 2.7 us, which is a launch and two dependent reads. A prefetch of a
-// token's rows into L2 before its lookup made both large calls 4 us longer.
+// into an E4M3 pool, in 53.7 us, 74% (lookups and codes); one token in 2.7 us,
+// which is a launch and two dependent reads. A prefetch of a token's rows into
+// L2 before its lookup made both large calls 4 us longer.
 #include <cmath>
 #include <type_traits>
 
@@ -100,6 +100,9 @@ __device__ __forceinline__ void store_codes(uint8_t* p, const float (&f)[V], flo
     }
 }
 
+// Pools that a call writes: none, of q's type, or of E4M3 codes.
+constexpr int kNoPool = 0, kPlainPool = 1, kCodePool = 2;
+
 // The request b whose range [new_indptr[b], new_indptr[b + 1]) holds token t,
 // by a 32-way search of the whole warp (one round for up to 32 requests). On a
 // malformed table it still ends, with some b in [0, batch).
@@ -116,14 +119,19 @@ __device__ __forceinline__ int request_of(const int32_t* new_indptr, int batch, 
 }
 
 // One warp per (token, slice of the token's hq + 2 hk heads: q, k, then v).
-// Unit u of a rotated head is V pairs: elements u V .. and rot/2 + u V ..
-// (half layout) or 2 u V .. 2 u V + 2 V - 1 (pairs layout). A lane keeps one
-// unit at a time and takes heads in rounds of kRound, whose loads are all
-// issued before the first store (out may be x) and kept as they come, so that
-// 24 warps per SM have up to 4 KB each in flight.
-template <typename T, bool kFp8, int V, bool kPairs>
-__global__ void __launch_bounds__(128, 6) rope_kernel(const RopeArgs a) {
-    constexpr int kRound = 4;
+// Unit u of a rotated head is its elements u V .. and rot/2 + u V .., V of
+// each: V pairs (half layout), or V / 2 pairs in each half (pairs layout; V =
+// 1: elements 2 u and 2 u + 1), so that neighbouring lanes read neighbouring
+// 16 bytes in both layouts. A lane keeps one unit at a time and takes heads in
+// rounds of kRound, whose loads are all issued before the first store (out may
+// be x) and kept as they come. What decides is bytes in flight per SM against
+// registers: without a pool 20 warps of up to 4 KB each (8191 tokens of 64 f16
+// heads 45.1 us; 24 warps 47.1), into pools of the same type 24 of 4 KB (7000
+// tokens of 48 bf16 heads 34.9 us; 2 KB 37.0), into E4M3 pools, whose codes
+// take registers, 24 of 2 KB (7000 tokens of 80 f16 heads 53.7 us; 4 KB 61.4).
+template <typename T, int kPool, int V, bool kPairs>
+__global__ void __launch_bounds__(128, kPool == kNoPool ? 5 : 6) rope_kernel(const RopeArgs a) {
+    constexpr int kRound = kPool == kCodePool ? 2 : 4, kCopies = kPool == kCodePool ? 4 : 8;
     const int lane = threadIdx.x & 31;
     const long long w = (long long)blockIdx.x * 4 + (threadIdx.x >> 5);
     if (w >= (long long)a.tokens * a.slices) return;
@@ -131,14 +139,14 @@ __global__ void __launch_bounds__(128, 6) rope_kernel(const RopeArgs a) {
     const int D = a.head_dim, rot = a.rot_dim;
     const int items = a.hq + 2 * a.hk;
     const int i0 = int((long long)items * slice / a.slices), i1 = int((long long)items * (slice + 1) / a.slices);
-    const bool wants_kv = a.hk > 0 && i1 > a.hq;
+    const bool wants_kv = kPool != kNoPool && i1 > a.hq;
 
     // ---- where this token's k and v rows go (row offset in elements of kv head 0), and its position
     int pos = 0;
     bool write_kv = false;
     size_t dst = 0;
     const size_t head_step = size_t(a.page_size) * D;
-    if (a.hk > 0 && (wants_kv || a.positions == nullptr)) {
+    if (kPool != kNoPool && (wants_kv || a.positions == nullptr)) {
         const int b = request_of(a.new_indptr, a.batch, t, lane);
         const int s = __ldg(a.new_indptr + b), e = __ldg(a.new_indptr + b + 1);
         const int lo = __ldg(a.indptr + b), hi = __ldg(a.indptr + b + 1);
@@ -174,15 +182,15 @@ __global__ void __launch_bounds__(128, 6) rope_kernel(const RopeArgs a) {
     const T* qr = static_cast<const T*>(a.q) + (long long)t * a.q_stride;
     T* qo = static_cast<T*>(a.q_out) + (long long)t * a.q_out_stride;
     const T* kr = static_cast<const T*>(a.k) + (long long)t * a.k_stride;
-    auto source = [&](int h) { return h < a.hq ? qr + (long long)h * D : kr + (long long)(h - a.hq) * D; };
+    auto source = [&](int h) { return kPool == kNoPool || h < a.hq ? qr + (long long)h * D : kr + (long long)(h - a.hq) * D; };
     // V elements of rotated head h (q or k) at element e
     auto store = [&](int h, int e, const float(&f)[V]) {
-        if (h < a.hq) {
+        if (kPool == kNoPool || h < a.hq) {
             store_elems<T, V>(qo + (long long)h * D + e, f);
         } else if (write_kv) {
             const int kh = h - a.hq;
             const size_t at = dst + size_t(kh) * head_step + e;
-            if constexpr (kFp8)
+            if constexpr (kPool == kCodePool)
                 store_codes<V>(static_cast<uint8_t*>(a.k_data) + at, f, __ldg(a.k_scale + kh));
             else
                 store_elems<T, V>(static_cast<T*>(a.k_data) + at, f);
@@ -198,13 +206,14 @@ __global__ void __launch_bounds__(128, 6) rope_kernel(const RopeArgs a) {
             float c[V], s[V];
 #pragma unroll
             for (int i = 0; i < V; ++i) {
-                const uint64_t turns = uint64_t(int64_t(pos)) * __ldg(a.freqs + u * V + i);
+                const int pair = !kPairs || V == 1 ? u * V + i : i % (V > 1 ? V / 2 : 1) + u * (V / 2) + (2 * i < V ? 0 : rot / 4);
+                const uint64_t turns = uint64_t(int64_t(pos)) * __ldg(a.freqs + pair);
                 // int32 -> f32 rounds the phase by at most 2^-25 of half a turn
                 sincospif(float(int32_t(uint32_t(turns >> 32))) * 4.656612873077393e-10f, &s[i], &c[i]);
                 s[i] *= a.scale;
                 c[i] *= a.scale;
             }
-            const int e0 = kPairs ? 2 * u * V : u * V, e1 = kPairs ? e0 + V : rot / 2 + u * V;
+            const int e0 = kPairs && V == 1 ? 2 * u : u * V, e1 = kPairs && V == 1 ? e0 + 1 : rot / 2 + u * V;
             for (int h = i0 + lane / across; h < h_end; h += heads * kRound) {
                 Raw<T, V> xs[kRound], ys[kRound];
 #pragma unroll
@@ -224,7 +233,7 @@ __global__ void __launch_bounds__(128, 6) rope_kernel(const RopeArgs a) {
                     float lo[V], hi[V];
 #pragma unroll
                     for (int i = 0; i < V; ++i) {
-                        // pair i: (x[i], y[i]) in the half layout; (z[2i], z[2i + 1]), z = x then y, in the pairs layout
+                        // pair i: (x[i], y[i]) in the half layout; neighbours of x, then of y, in the pairs layout
                         const float p = kPairs && V > 1 ? (2 * i < V ? x[2 * i % V] : y[2 * i % V]) : x[i];
                         const float q = kPairs && V > 1 ? (2 * i < V ? x[(2 * i + 1) % V] : y[(2 * i + 1) % V]) : y[i];
                         const float pr = p * c[i] - q * s[i], qr2 = q * c[i] + p * s[i];
@@ -247,7 +256,6 @@ __global__ void __launch_bounds__(128, 6) rope_kernel(const RopeArgs a) {
     const int q_from = (a.q_out == a.q && a.q_stride == a.q_out_stride) ? max(i0, a.hq) : i0;
     // n chunks of V elements, `at` giving a chunk's head and element; loads of a round before its stores
     auto copy = [&](int n, auto at, auto from, auto to) {
-        constexpr int kCopies = 8;
         for (int x = lane; x < n; x += 32 * kCopies) {
             Raw<T, V> w[kCopies];
 #pragma unroll
@@ -285,25 +293,32 @@ __global__ void __launch_bounds__(128, 6) rope_kernel(const RopeArgs a) {
         [&](int h) { return vr + (long long)h * D; },
         [&](int h, int e, const float(&f)[V]) {
             const size_t at = dst + size_t(h) * head_step + e;
-            if constexpr (kFp8)
+            if constexpr (kPool == kCodePool)
                 store_codes<V>(static_cast<uint8_t*>(a.v_data) + at, f, __ldg(a.v_scale + h));
             else
                 store_elems<T, V>(static_cast<T*>(a.v_data) + at, f);
         });
 }
 
-template <typename T, bool kFp8, int V>
+template <typename T, int kPool, int V>
 const void* pick_layout(int layout) {
-    return layout == PD_ROPE_PAIRS ? reinterpret_cast<const void*>(rope_kernel<T, kFp8, V, true>)
-                                   : reinterpret_cast<const void*>(rope_kernel<T, kFp8, V, false>);
+    return layout == PD_ROPE_PAIRS ? reinterpret_cast<const void*>(rope_kernel<T, kPool, V, true>)
+                                   : reinterpret_cast<const void*>(rope_kernel<T, kPool, V, false>);
 }
 
 // The kernel that moves 16 bytes per access where every row allows it: the
 // rotated part a whole number of units, rows 16-byte aligned. Otherwise one
 // element per access (odd rotary sizes, unaligned views), several times slower.
-template <typename T, bool kFp8>
+template <typename T, int kPool>
 const void* pick_kernel(int layout, bool wide) {
-    return wide ? pick_layout<T, kFp8, Elt<T>::kVec>(layout) : pick_layout<T, kFp8, 1>(layout);
+    return wide ? pick_layout<T, kPool, Elt<T>::kVec>(layout) : pick_layout<T, kPool, 1>(layout);
+}
+
+template <typename T>
+const void* pick_pool(int pool, int layout, bool wide) {
+    if constexpr (sizeof(T) == 2)
+        if (pool == kCodePool) return pick_kernel<T, kCodePool>(layout, wide);
+    return pool == kNoPool ? pick_kernel<T, kNoPool>(layout, wide) : pick_kernel<T, kPlainPool>(layout, wide);
 }
 
 pd_status launch(RopeArgs& a, pd_dtype dt, bool fp8, int layout, cudaStream_t stream) {
@@ -317,7 +332,7 @@ pd_status launch(RopeArgs& a, pd_dtype dt, bool fp8, int layout, cudaStream_t st
     pd_status st = host::sm_count(&sms);
     if (st != PD_OK) return st;
     // Few tokens: cut each token's heads into slices so that the card has about 8 warps per SM. More slices make
-    // a shorter last wave and more sines and lookups: with 64 warps per SM, 8191 tokens of 64 f16 heads take 47.9
+    // a shorter last wave and more sines and lookups: with 64 warps per SM, 8191 tokens of 64 f16 heads took 47.9
     // instead of 49.7 us, but 9000 of 8 bf16 heads 22.5 instead of 16.4, and 7000 of 80 heads into an E4M3 pool
     // 68.2 instead of 64.9.
     const int items = a.hq + 2 * a.hk;
@@ -327,10 +342,10 @@ pd_status launch(RopeArgs& a, pd_dtype dt, bool fp8, int layout, cudaStream_t st
     if (a.head_dim > a.rot_dim) a.by_rest = FastDiv::of((a.head_dim - a.rot_dim) / per);
     a.by_chunks = FastDiv::of(a.head_dim / per);
     const long long warps = (long long)a.tokens * a.slices;
-    const void* fn = dt == PD_F32   ? pick_kernel<float, false>(layout, wide)
-                     : dt == PD_F16 ? (fp8 ? pick_kernel<__half, true>(layout, wide) : pick_kernel<__half, false>(layout, wide))
-                                    : (fp8 ? pick_kernel<__nv_bfloat16, true>(layout, wide)
-                                           : pick_kernel<__nv_bfloat16, false>(layout, wide));
+    const int pool = a.hk == 0 ? kNoPool : fp8 ? kCodePool : kPlainPool;
+    const void* fn = dt == PD_F32   ? pick_pool<float>(pool, layout, wide)
+                     : dt == PD_F16 ? pick_pool<__half>(pool, layout, wide)
+                                    : pick_pool<__nv_bfloat16>(pool, layout, wide);
     void* args[] = {&a};
     const cudaError_t e = cudaLaunchKernel(fn, dim3(unsigned((warps + 3) / 4)), dim3(128), args, 0, stream);
     return e == cudaSuccess ? host::ok() : host::cuda_fail(e, "rope launch");

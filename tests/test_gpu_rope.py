@@ -285,3 +285,27 @@ def test_commit_flags_bad_paths_and_leaves_those_requests():
     k = c.k.cuda()
     pd.pd_paged_tree_commit(k, v, *t, path.cuda(), torch.tensor([0, 0, 0, 2, 0], dtype=torch.int32).cuda(), ws)
     assert pd.pd_read_device_flags(ws) == pd.PD_FLAG_BAD_PAGE_ID
+
+
+@pytest.mark.parametrize("dtype", ["f16", "bf16"])
+def test_append_codes_of_every_16_bit_value(dtype):
+    """All 65,536 patterns, ties between codes among them, over scales from the smallest to the largest."""
+    import paged_kv_gqa_13_gb300 as pd
+
+    d, page, n = 128, 16, 512
+    scales = torch.tensor([1.0, 0.1, 0.0131, 7.3, 0.0625, 1e-39, 3e38, 1e-20])
+    hk = scales.numel()
+    c = Paged([n], [n], hk, d, page, dtype, fp8=True)
+    x = torch.arange(1 << 16).to(torch.int16).view(TYPES[dtype]).view(n, 1, d).expand(n, hk, d).contiguous()
+    k, v, ws = c.k.cuda(), c.v.cuda(), _ws()
+    pd.pd_paged_rope_append_fp8(None, x.cuda(), x.cuda(), None, None, None, scales.cuda(), scales.cuda(), k, v, *c.table(), ws)
+    assert pd.pd_read_device_flags(ws) == 0
+    with np.errstate(over="ignore", invalid="ignore"):
+        quotient = torch.from_numpy(x.float().numpy() / scales.numpy()[:, None])
+    want = quotient.clamp(-448, 448).to(torch.float8_e4m3fn).view(torch.uint8)
+    nan = quotient.isnan()
+    p, r = c.rows(0, np.arange(n))
+    for pool in (k, v):
+        got = pool.cpu()[p, :, r].view(torch.uint8)
+        assert torch.equal(got[~nan], want[~nan])
+        assert bool(((got[nan] & 0x7F) == 0x7F).all())

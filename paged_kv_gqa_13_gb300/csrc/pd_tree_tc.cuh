@@ -797,6 +797,7 @@ __global__ void __launch_bounds__(CfgTree<D, kWide, kFp8>::kThreads, 1)
                                 for (int e = 0; e < 32; ++e)
                                     if (((allow >> e) & 1u) == 0u) x[c + e] = __float_as_uint(kNegInf);
                             }
+                            __syncwarp();  // tensor-memory accesses are the whole warp's
                         }
                         float tops[4];
 #pragma unroll
@@ -865,11 +866,12 @@ __global__ void __launch_bounds__(CfgTree<D, kWide, kFp8>::kThreads, 1)
                 for (int c = 0; c < D; c += 32) {
                     uint32_t o[32];
                     float f[32];
+                    __syncwarp();
                     tmem_ld32(to + c, o);
                     tmem_wait_ld();
+                    if (at < 0) continue;
 #pragma unroll
                     for (int e = 0; e < 32; ++e) f[e] = __uint_as_float(o[e]) * inv;
-                    if (at < 0) continue;
                     if (fix) {
                         // non-finite elements of the node rows in these blocks, for the rows that attend them
                         for (int i = 0; i < r.n; ++i) {

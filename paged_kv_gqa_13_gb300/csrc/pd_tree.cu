@@ -9,11 +9,11 @@
 namespace pd {
 namespace {
 
-template <typename T, typename KV, int D>
+template <typename T, typename KV, int D, int kCols>
 TreeKernels cc_kernels() {
-    using C = CfgTreeCc<D>;
+    using C = CfgTreeCc<D, kCols>;
     TreeKernels k{};
-    k.main = reinterpret_cast<const void*>(tree_cc_kernel<T, KV, D>);
+    k.main = reinterpret_cast<const void*>(tree_cc_kernel<T, KV, D, kCols>);
     k.merge = reinterpret_cast<const void*>(tree_merge_kernel<T, D>);
     k.threads = C::kThreads;
     k.smem = C::kBytes;
@@ -25,29 +25,36 @@ TreeKernels cc_kernels() {
     return k;
 }
 
-template <typename T, typename KV>
+template <typename T, typename KV, int kCols>
 bool cc_by_dim(int D, TreeKernels* k) {
     switch (D) {
-        case 64: *k = cc_kernels<T, KV, 64>(); return true;
-        case 128: *k = cc_kernels<T, KV, 128>(); return true;
-        case 256: *k = cc_kernels<T, KV, 256>(); return true;
+        case 64: *k = cc_kernels<T, KV, 64, (kCols < 16 ? kCols : 16)>(); return true;
+        case 128: *k = cc_kernels<T, KV, 128, kCols>(); return true;
+        case 256: *k = cc_kernels<T, KV, 256, kCols>(); return true;
     }
     return false;
 }
 
+// The rows of a request on average: up to 8, up to 16, up to half a row tile of the tensor cores, more.
+enum Rows { kRows8, kRows16, kRows64, kRowsMany };
+
 // 16-bit q of a group that fits a row tile runs on the tensor cores; f32 q,
 // which no tensor-core type holds, and larger groups on CUDA cores.
-// `wide`: two row tiles per segment (where a kernel for it exists).
-bool pick(pd_dtype dt, bool fp8, int D, int group, bool wide, TreeKernels* k) {
+bool pick(pd_dtype dt, bool fp8, int D, int group, Rows rows, TreeKernels* k) {
     if (dt != PD_F32 && group <= 128) {
+        const bool wide = rows == kRowsMany;  // two row tiles per segment (where a kernel for it exists)
         if (fp8) return dt == PD_F16 ? tree_tc_f16_fp8(D, wide, k) : tree_tc_bf16_fp8(D, wide, k);
         return dt == PD_F16 ? tree_tc_f16(D, wide, k) : tree_tc_bf16(D, wide, k);
     }
     switch (dt) {
-        case PD_F32: return !fp8 && cc_by_dim<float, float>(D, k);
-        case PD_F16: return fp8 ? cc_by_dim<__half, uint8_t>(D, k) : cc_by_dim<__half, __half>(D, k);
+        case PD_F32:
+            if (fp8) return false;
+            return rows == kRows8    ? cc_by_dim<float, float, 32>(D, k)
+                   : rows == kRows16 ? cc_by_dim<float, float, 16>(D, k)
+                                     : cc_by_dim<float, float, 8>(D, k);
+        case PD_F16: return fp8 ? cc_by_dim<__half, uint8_t, 8>(D, k) : cc_by_dim<__half, __half, 8>(D, k);
         case PD_BF16:
-            return fp8 ? cc_by_dim<__nv_bfloat16, uint8_t>(D, k) : cc_by_dim<__nv_bfloat16, __nv_bfloat16>(D, k);
+            return fp8 ? cc_by_dim<__nv_bfloat16, uint8_t, 8>(D, k) : cc_by_dim<__nv_bfloat16, __nv_bfloat16, 8>(D, k);
     }
     return false;
 }
@@ -133,11 +140,16 @@ pd_status tree_impl(const void* q, const void* k_data, const void* v_data, const
         return host::fail(PD_ERR_UNSUPPORTED, "lse, the table, tree_mask and the scales must be 4-byte aligned");
     const int group = Hq / Hk;
     TreeKernels kn{};
-    // More than half a row tile per request on average: segments of up to two row tiles, which read K and V once
-    // for both (64 trees of 1 to 32 nodes, 8 heads a group: 191 us as two halves of a CTA, 162 so). Fewer: two
-    // independent halves of each CTA (32 chains of 4, 4 heads a group: 93 us as two row tiles, 68 so).
-    const bool wide = (long long)total_new * group > 64ll * batch;
-    if (!pick(dt, fp8, D, group, wide, &kn)) return host::fail(PD_ERR_UNSUPPORTED, "no kernel for this type and head_dim");
+    // On the tensor cores, more than half a row tile per request on average: segments of up to two row tiles, which
+    // read K and V once for both (64 trees of 1 to 32 nodes, 8 heads a group: 191 us as two halves of a CTA, 162 so).
+    // Fewer: two independent halves of each CTA (32 chains of 4, 4 heads a group: 93 us as two row tiles, 68 so). On
+    // CUDA cores, row tiles of 32, of 16 or of 8 rows (16 requests, 16 rows of head_dim 64: 104 us in 32, 72 in 16).
+    const long long all_rows = (long long)total_new * group;
+    const Rows rows = all_rows > 64ll * batch   ? kRowsMany
+                      : all_rows > 16ll * batch ? kRows64
+                      : all_rows > 8ll * batch  ? kRows16
+                                                : kRows8;
+    if (!pick(dt, fp8, D, group, rows, &kn)) return host::fail(PD_ERR_UNSUPPORTED, "no kernel for this type and head_dim");
     int sms = 0;
     if ((st = host::sm_count(&sms)) != PD_OK) return st;
     const int most = sms * kn.per_sm;
@@ -211,7 +223,7 @@ pd_status tree_impl(const void* q, const void* k_data, const void* v_data, const
     const bool merge = workers > 1 && blocks > (kn.tensor ? 3 : 1);
     a.whole = !merge;
     a.seg_cost = kn.seg_cost;
-    a.tails = merge && !(wide && kn.tensor && !fp8);
+    a.tails = merge && !(rows == kRowsMany && kn.tensor && !fp8);
     cudaStream_t cs = static_cast<cudaStream_t>(stream);
     if ((st = host::allow_smem(kn.main, kn.smem)) != PD_OK) return st;
     CUtensorMap maps[3]{};
@@ -247,9 +259,9 @@ size_t pd_paged_tree_decode_workspace_bytes(int num_qo_heads, int num_kv_heads, 
     int sms = 0;
     if (host::sm_count(&sms) != PD_OK) return 0;
     size_t most = 0;  // of the kernels that take this type, with either pool
-    for (int form = 0; form < 4; ++form) {
+    for (int form = 0; form < 8; ++form) {
         TreeKernels k{};
-        if (!pick(dtype, (form & 1) != 0, head_dim, num_qo_heads / num_kv_heads, (form & 2) != 0, &k)) continue;
+        if (!pick(dtype, form % 2 != 0, head_dim, num_qo_heads / num_kv_heads, Rows(form / 2), &k)) continue;
         const size_t n = space(k, sms * k.per_sm, head_dim).bytes;
         if (n > most) most = n;
     }

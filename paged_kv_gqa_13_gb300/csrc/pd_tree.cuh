@@ -483,9 +483,11 @@ __device__ __forceinline__ void copy16_async(void* dst, const void* src, bool th
 __device__ __forceinline__ void copy_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
 __device__ __forceinline__ void copy_wait() { asm volatile("cp.async.wait_all;" ::: "memory"); }
 
-template <int D>
+template <int D, int kCols>  // kCols: threads that share a row (at most D / 4)
 struct CfgTreeCc {
-    static constexpr int kRows = 32, kKeys = 32, kThreads = 128;
+    static constexpr int kKeys = 32, kThreads = 128;
+    static constexpr int kRows = 2 * kThreads / kCols;
+    static constexpr int kPer = kKeys / kCols;  // keys of a thread's scores
     static constexpr int kBlockTokens = 32;  // short, so that a small call spreads over SMs
     static constexpr int kWindow = 128;      // tokens whose rows are looked up at a time
     static constexpr int kLd = D + 4;  // row step of q and K in shared memory: 16-byte reads of 8 rows hit all banks
@@ -494,7 +496,7 @@ struct CfgTreeCc {
     static constexpr int kKv = kKeys * kLd + kKeys * D;
     static constexpr int kFloats = kRows * kLd + kBufs * kKv + kRows * kLdP;
     static constexpr int kBytes = kFloats * 4;
-    static constexpr int kBlocksPerSm = D == 64 ? 4 : 2;
+    static constexpr int kBlocksPerSm = D == 64 ? (kCols > 8 ? 5 : 4) : D == 128 && kCols == 32 ? 3 : 2;
 };
 
 // f32 arithmetic on CUDA cores: f32 q (no tensor-core type holds it) and
@@ -503,12 +505,18 @@ struct CfgTreeCc {
 // columns 4 tc + 32 i. The 8 lanes of a row sit in one warp, so the softmax
 // needs no block barrier. Bound by FFMA issue: 4 D flops per row and key
 // against shared-memory reads of 6 (scores) and 1 (outputs) vectors per 32 and
-// 8 multiply-adds. A small call is latency: one request of 100 tokens, 6 nodes
-// takes 9.7 us on the device, most of it the walk's and the first copies' round
-// trips (the call 11.5 us; with blocks of 128 tokens, cut and merged, 19.9).
-template <typename T, typename KV, int D>
-__global__ void __launch_bounds__(128, CfgTreeCc<D>::kBlocksPerSm) tree_cc_kernel(const TreeArgs a) {
-    using C = CfgTreeCc<D>;
+// 8 multiply-adds. Where requests have up to 8 or 16 rows, 32 or 16 threads
+// share a row, so that every thread has rows to work for (8 requests of up to
+// 2484 tokens: 2 rows of head_dim 256 over 16 kv heads 226 -> 115 us, 16 rows of
+// head_dim 128 over 8 kv heads 82 -> 59 us; 32 requests, 4 rows of head_dim 128:
+// 360 -> 154 us, 57% of the copy rate).
+// A small call is latency: one request of 100 tokens, 6 nodes takes 9.7 us on
+// the device, most of it the walk's and the first copies' round trips (the call
+// 11.5 us; with blocks of 128 tokens, cut and merged, 19.9).
+template <typename T, typename KV, int D, int kCols>
+__global__ void __launch_bounds__(128, CfgTreeCc<D, kCols>::kBlocksPerSm) tree_cc_kernel(const TreeArgs a) {
+    using C = CfgTreeCc<D, kCols>;
+    constexpr int kPer = C::kPer, kVecs = D / (4 * kCols);
     const float kNegInf = -__int_as_float(0x7f800000);
     extern __shared__ __align__(16) float tree_smem[];
     __shared__ TreePlanScratch plan;
@@ -516,7 +524,7 @@ __global__ void __launch_bounds__(128, CfgTreeCc<D>::kBlocksPerSm) tree_cc_kerne
     float* sq = tree_smem;
     float* kv = sq + C::kRows * C::kLd;
     float* sp = kv + C::kBufs * C::kKv;
-    const int tid = threadIdx.x, tr = tid >> 3, tc = tid & 7;
+    const int tid = threadIdx.x, tr = tid / kCols, tc = tid % kCols;
     tree_plan<1>(a, &plan);
     const TreeLine line = tree_line<1>(a, &plan);
     TreeWalk walk = tree_start<1>(line, &plan, 0);
@@ -548,7 +556,7 @@ __global__ void __launch_bounds__(128, CfgTreeCc<D>::kBlocksPerSm) tree_cc_kerne
             if (at >= 0) pool_load4(static_cast<const T*>(a.q) + at * D + e, 1.f, f);
             *reinterpret_cast<float4*>(sq + row * C::kLd + e) = make_float4(f[0], f[1], f[2], f[3]);
         }
-        float m[2] = {kNegInf, kNegInf}, l[2] = {}, o[2][D / 8] = {};
+        float m[2] = {kNegInf, kNegInf}, l[2] = {}, o[2][4 * kVecs] = {};
         const int node[2] = {s.node0 + a.by_hpt.div(2 * tr), s.node0 + a.by_hpt.div(2 * tr + 1)};
         int window;  // first token of row_offs
         // Keys t0 .. of the pools into buffer `buf` (zeros where there is no row): asynchronous copies of f32
@@ -605,14 +613,14 @@ __global__ void __launch_bounds__(128, CfgTreeCc<D>::kBlocksPerSm) tree_cc_kerne
             const float* sk = kv + buf * C::kKv;
             const float* sv = sk + C::kKeys * C::kLd;
             const long long* row_off = row_offs + (t0 - window);
-            float x[2][4] = {};
+            float x[2][kPer] = {};
 #pragma unroll 4
             for (int e = 0; e < D; e += 4) {
                 const float4 q0 = *reinterpret_cast<const float4*>(sq + (2 * tr) * C::kLd + e);
                 const float4 q1 = *reinterpret_cast<const float4*>(sq + (2 * tr + 1) * C::kLd + e);
 #pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    const float4 k = *reinterpret_cast<const float4*>(sk + (tc + 8 * i) * C::kLd + e);
+                for (int i = 0; i < kPer; ++i) {
+                    const float4 k = *reinterpret_cast<const float4*>(sk + (tc + kCols * i) * C::kLd + e);
                     x[0][i] = fmaf(q0.w, k.w, fmaf(q0.z, k.z, fmaf(q0.y, k.y, fmaf(q0.x, k.x, x[0][i]))));
                     x[1][i] = fmaf(q1.w, k.w, fmaf(q1.z, k.z, fmaf(q1.y, k.y, fmaf(q1.x, k.x, x[1][i]))));
                 }
@@ -623,26 +631,26 @@ __global__ void __launch_bounds__(128, CfgTreeCc<D>::kBlocksPerSm) tree_cc_kerne
                 const uint32_t allow = tree_allow(a, s.r, min(node[j], s.r.n - 1), t0, C::kKeys);
                 float top = kNegInf;
 #pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    const bool in = ((allow >> (tc + 8 * i)) & 1u) != 0 && row_off[tc + 8 * i] >= 0;
+                for (int i = 0; i < kPer; ++i) {
+                    const bool in = ((allow >> (tc + kCols * i)) & 1u) != 0 && row_off[tc + kCols * i] >= 0;
                     x[j][i] = in ? x[j][i] * a.scale_log2 : kNegInf;
                     top = fmaxf(top, x[j][i]);
                 }
 #pragma unroll
-                for (int off = 1; off < 8; off <<= 1) top = fmaxf(top, __shfl_xor_sync(kFull, top, off));
+                for (int off = 1; off < kCols; off <<= 1) top = fmaxf(top, __shfl_xor_sync(kFull, top, off));
                 const float mn = fmaxf(m[j], top), mu = mn == kNegInf ? 0.f : mn;
                 const float al = ex2(m[j] - mu);
                 m[j] = mn;
                 float sum = 0.f;
 #pragma unroll
-                for (int i = 0; i < 4; ++i) {
+                for (int i = 0; i < kPer; ++i) {
                     const float p = ex2(x[j][i] - mu);
                     sum += p;
-                    sp[(2 * tr + j) * C::kLdP + tc + 8 * i] = p;
+                    sp[(2 * tr + j) * C::kLdP + tc + kCols * i] = p;
                 }
                 l[j] = l[j] * al + sum;
 #pragma unroll
-                for (int i = 0; i < D / 8; ++i) o[j][i] *= al;
+                for (int i = 0; i < 4 * kVecs; ++i) o[j][i] *= al;
             }
             __syncwarp();
             auto accumulate = [&](auto guard) {
@@ -655,8 +663,8 @@ __global__ void __launch_bounds__(128, CfgTreeCc<D>::kBlocksPerSm) tree_cc_kerne
                     for (int x = 0; x < 4; ++x) {
                         const float p0 = p0s[x], p1 = p1s[x];
 #pragma unroll
-                        for (int i = 0; i < D / 32; ++i) {
-                            const float4 v = *reinterpret_cast<const float4*>(sv + (key4 + x) * D + 4 * tc + 32 * i);
+                        for (int i = 0; i < kVecs; ++i) {
+                            const float4 v = *reinterpret_cast<const float4*>(sv + (key4 + x) * D + 4 * (tc + kCols * i));
                             const float f[4] = {v.x, v.y, v.z, v.w};
 #pragma unroll
                             for (int c = 0; c < 4; ++c) {
@@ -679,17 +687,17 @@ __global__ void __launch_bounds__(128, CfgTreeCc<D>::kBlocksPerSm) tree_cc_kerne
             const int row = 2 * tr + j;
             float L = l[j];
 #pragma unroll
-            for (int off = 1; off < 8; off <<= 1) L += __shfl_xor_sync(kFull, L, off);
+            for (int off = 1; off < kCols; off <<= 1) L += __shfl_xor_sync(kFull, L, off);
             const long long at = tree_row(a, s.row0, s.nodes, s.hh, row);
             if (at < 0) continue;
             const float inv = m[j] == kNegInf ? 0.f : 1.f / L;
             const float lse2 = m[j] == kNegInf ? kNegInf : m[j] + log2f(L);
 #pragma unroll
-            for (int i = 0; i < D / 32; ++i) {
+            for (int i = 0; i < kVecs; ++i) {
                 float f[8] = {};
 #pragma unroll
                 for (int c = 0; c < 4; ++c) f[c] = o[j][4 * i + c] * inv;
-                const int e = 4 * tc + 32 * i;
+                const int e = 4 * (tc + kCols * i);
                 if (s.slot >= 0) {
                     *reinterpret_cast<float4*>(a.part_o + (size_t(s.slot) * a.seg_rows + row) * D + e) =
                         make_float4(f[0], f[1], f[2], f[3]);

@@ -328,3 +328,29 @@ def test_a_copy_that_never_lands_is_reported_and_later_calls_are_right(fp8, n):
     o, lse, flags = _run(c, q, masks, 3, 0.1, "bf16", ws=ws)
     assert flags == 0
     check_tree(o, lse, tree_reference(c, q, masks, 0.1), "bf16")
+
+
+@pytest.mark.parametrize("d", [64, 128, 256])
+@pytest.mark.parametrize("kind", ["chain", "tree", "nothing"])
+@pytest.mark.parametrize("hq,hk", [(2, 2), (8, 2), (16, 1)])
+@pytest.mark.parametrize("kv,new", [([6000, 0, 33, 1], [2, 0, 1, 1]), ([500, 40, 77, 2100, 9], [1, 2, 0, 13, 1])])
+def test_few_rows_in_f32(d, kind, hq, hk, kv, new):
+    """Row tiles of 8, 16 and 32 rows; requests that have more rows than a tile, and none."""
+    _case(kv, new, hq, hk, d, 16, "f32", kind)
+
+
+@pytest.mark.parametrize("d", [64, 128, 256])
+@pytest.mark.parametrize("n", [2, 4, 9])
+def test_few_rows_in_f32_next_to_what_they_do_not_attend(d, n):
+    c = Paged([n + 70], [n], 2, d, 16, "f32")
+    q = torch.randn(n, 4, d)
+    masks = [np.eye(n, dtype=bool)]
+    clean, clean_lse, _ = _run(c, q, masks, 1, 0.1, "f32")
+    p, r = c.rows(0, [70 + 1])
+    c.k[p, :, r] = math.nan
+    c.v[p, :, r] = math.inf
+    o, lse, flags = _run(c, q, masks, 1, 0.1, "f32")
+    rows = [i for i in range(n) if i != 1]
+    assert flags == 0
+    assert torch.equal(o[rows], clean[rows]) and torch.equal(lse[rows], clean_lse[rows])
+    assert bool(torch.isnan(o[1]).any())

@@ -16,14 +16,16 @@
 // holds one O).
 //
 // K and V come in blocks of kKeys keys through a ring of slots, K and V of
-// block n as loads 2 n and 2 n + 1 of the line. Every role that waits for
-// loads steps over all of them in order, so that no barrier gets two phases
-// ahead of a role (a wait tells phases apart by parity only).
+// block n as loads 2 n and 2 n + 1 of the line. A wait tells the phases of a
+// barrier apart by parity only, so no barrier may get two phases ahead of a
+// role that waits on it: whoever waits on a barrier takes part in its next
+// phase. The mma warps and inspectors wait for every load and give every slot
+// back; a slot is refilled by one producer alone (TreeProducers), which is the
+// only one that waits for it to be empty.
 //
 // Roles beside the softmax warps, per line: an mma warp per pipeline; producers
-// (TMA; load i by producer i % kProducers: a box of 16 rows x 128 bytes costs
-// its issuing warp about 75 cycles, and one warp alone kept the ring from
-// filling); inspectors, which make V safe where weights can be zero: a zero
+// (TMA, several: a box of 16 rows x 128 bytes costs its issuing warp about 75
+// cycles, and one warp alone kept the ring from filling); inspectors, which make V safe where weights can be zero: a zero
 // weight does not undo a NaN or an infinity, so in blocks that hold tokens some
 // row does not attend, rows past the end are zeroed and non-finite elements of
 // node rows are replaced by zero, to be added to the rows that attend them at
@@ -221,6 +223,17 @@ struct CfgTree {
     static_assert(kSCol + kLines * kPipes * 2 * kJobKeys <= 512, "tensor memory");
     static_assert(kBytes <= 232448, "shared memory");
     static_assert(kLineBytes % 1024 == 0 && kSlotBytes % 1024 == 0, "operand tiles stay 1024-byte aligned");
+};
+
+// Load i of a line goes to place i % kPlaces of its ring, and each place belongs
+// to one of the line's producers. That producer has issued every load of the
+// place and waits for the one before to be used up, so that the place's empty
+// barrier cannot pass the phase that it waits for; a producer that waited for
+// places of others could be overtaken by two phases and then see the wrong one.
+template <int kPlaces, int kProducers>
+struct TreeProducers {
+    static_assert(kProducers <= kPlaces, "every producer has a place");
+    __host__ __device__ static constexpr bool mine(int place, int me) { return place % kProducers == me; }
 };
 
 // Segments come to a line's roles through a ring in shared memory, filled by
@@ -476,26 +489,26 @@ __global__ void __launch_bounds__(CfgTree<D, kWide, kFp8>::kThreads, 1)
         constexpr int kPlaces = kFp8 ? C::kStages : C::kSlots, kPlaceFull = kFp8 ? C::kStFull : C::kFull,
                       kPlaceEmpty = kFp8 ? C::kStEmpty : C::kEmpty, kPlaceOff = kFp8 ? C::kStageOff : C::kRingOff,
                       kPlaceBytes = kFp8 ? C::kStageBytes : C::kSlotBytes, kQLanded = kFp8 ? C::kQRaw : C::kQFull;
+        using Own = TreeProducers<kPlaces, C::kProducers>;
         Ring<kPlaces> ring;
-        int loads = 0, qloads = 0, segments = 0, kblocks = 0, turn = 0;  // turn: the producer whose load is next
+        int loads = 0, qloads = 0, segments = 0, kblocks = 0;  // loads: of all producers
         bool ok = true;
         // one box per lane: slot_rows rows x 64 columns (codes: x head_dim columns)
         constexpr int kBoxes = kFp8 ? 1 : C::kHalves, kRowBytes = kFp8 ? D : 128;
         const int sl = lane / kBoxes, hf = lane % kBoxes, spb = 1 << a.spb_shift;
         auto load_block = [&](const TcSeg& s, int blk, const CUtensorMap* tm, bool is_k) -> bool {
-            const bool mine = turn == me;
-            const int p = (blk << a.spb_shift) + sl;
-            int page = a.num_total_pages, row = 0;  // page out of range: the copy fills zeros
-            bool bad = false;
-            if (mine && sl < spb && p < s.slots) {
-                const int at = a.by_cpp.div(p);
-                row = (p - at * a.cpp) << a.slot_shift;
-                page = __ldg(a.indices + s.lo + at);
-                bad = page < 0 || page >= a.num_total_pages;
-                if (bad) page = a.num_total_pages;
-            }
-            if (loads >= kPlaces && !wait(kPlaceEmpty + ring.slot, ring.phase ^ 1u)) return false;
-            if (mine) {
+            if (Own::mine(ring.slot, me)) {
+                const int p = (blk << a.spb_shift) + sl;
+                int page = a.num_total_pages, row = 0;  // page out of range: the copy fills zeros
+                bool bad = false;
+                if (sl < spb && p < s.slots) {
+                    const int at = a.by_cpp.div(p);
+                    row = (p - at * a.cpp) << a.slot_shift;
+                    page = __ldg(a.indices + s.lo + at);
+                    bad = page < 0 || page >= a.num_total_pages;
+                    if (bad) page = a.num_total_pages;
+                }
+                if (loads >= kPlaces && !wait(kPlaceEmpty + ring.slot, ring.phase ^ 1u)) return false;
                 if (is_k) {
                     const unsigned found = __ballot_sync(kFull, bad);
                     if (lane == 0) {
@@ -515,7 +528,6 @@ __global__ void __launch_bounds__(CfgTree<D, kWide, kFp8>::kThreads, 1)
             }
             ++loads;
             ring.next();
-            if (++turn == C::kProducers) turn = 0;
             return true;
         };
         for (; ok; ++segments) {
@@ -543,7 +555,7 @@ __global__ void __launch_bounds__(CfgTree<D, kWide, kFp8>::kThreads, 1)
         }
         // copies issued last may still be landing when another role has stopped early
         for (int i = max(0, loads - kPlaces); i < loads; ++i)
-            mbar_wait_bounded(bar(kPlaceFull + i % kPlaces), uint32_t(i / kPlaces) & 1u);
+            if (Own::mine(i % kPlaces, me)) mbar_wait_bounded(bar(kPlaceFull + i % kPlaces), uint32_t(i / kPlaces) & 1u);
         for (int i = max(0, qloads - C::kPipes); i < qloads; ++i)
             mbar_wait_bounded(bar(kQLanded + i % C::kPipes), uint32_t(i / C::kPipes) & 1u);
     } else if (!soft) {

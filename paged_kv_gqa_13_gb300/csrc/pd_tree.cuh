@@ -22,8 +22,11 @@
 // leaves a partial (o, lse) in each of its ranges, and the merge kernel combines
 // them in order. Only the device knows the lengths: every CTA sums the requests'
 // units itself (each thread a run of requests, one block-wide scan) and finds
-// its shares; the range whose start is the first cut through a segment's blocks
-// writes the merge's descriptor.
+// its shares. A segment's merge descriptor belongs to the range whose start is
+// the first cut through the segment's blocks, and the worker whose share that
+// is (or whose share's tail) writes it before it waits for anything: every
+// descriptor that the merge reads is this call's, whoever runs the tails and
+// whether or not a wait has run out.
 #pragma once
 
 #include "pd_merge.cuh"
@@ -169,6 +172,8 @@ struct TreeLine {
         l.tail = !a.tails || l.share < 48 ? 0 : l.share / 8;
         return l;
     }
+    // The range of a worker's share, or of its tail.
+    __device__ __forceinline__ int range(int worker, int of_tail) const { return tail == 0 ? worker : 2 * worker + of_tail; }
     __device__ __forceinline__ long long start(int r) const {
         return tail == 0 ? r * share : (r / 2 + 1) * share - (r % 2 != 0 ? tail : share);
     }
@@ -311,7 +316,7 @@ struct TreePlanScratch {
     struct {
         int b, hh, tau, pos;
         TreeReq r;
-    } at[2];  // where each worker of the CTA starts
+    } at[4];  // where the share of each worker of the CTA starts (even), and its tail (odd)
 };
 
 // Find the shares of this CTA's kWorkers workers. All threads of the block
@@ -336,7 +341,7 @@ __device__ __forceinline__ void tree_plan(const TreeArgs& a, TreePlanScratch* sc
         if (lane >= off) inc += x;
     }
     if (lane == 31) sc->sums[wid] = inc;
-    if (tid < kWorkers) sc->at[tid].b = -1;
+    if (tid < 2 * kWorkers) sc->at[tid].b = -1;
     __syncthreads();
     long long before = inc - mine, total = 0;
     for (int w = 0; w < min(nw, (a.batch + 31) / 32); ++w) {  // the others hold no request
@@ -350,8 +355,9 @@ __device__ __forceinline__ void tree_plan(const TreeArgs& a, TreePlanScratch* sc
         if (blockIdx.x == 0) *reinterpret_cast<TreeLine*>(a.splits) = line;
     }
 #pragma unroll
-    for (int k = 0; k < kWorkers; ++k) {
-        const long long unit = ((long long)blockIdx.x * kWorkers + k) * line.share;
+    for (int k = 0; k < 2 * kWorkers; ++k) {
+        if (k % 2 != 0 && line.tail == 0) continue;
+        const long long unit = line.start(line.range(int(blockIdx.x) * kWorkers + k / 2, k % 2));
         if (unit >= total || unit < before || unit >= before + mine) continue;
         long long left = unit - before;
         for (int b = b0; b < b1; ++b) {
@@ -370,22 +376,23 @@ __device__ __forceinline__ void tree_plan(const TreeArgs& a, TreePlanScratch* sc
     __syncthreads();
 }
 
-// The line, and the walk over the share (without its tail) of worker k of this CTA.
+// The line, and the walk over the share (without its tail), or over the share's
+// tail (tail 1, of a line that has them), of worker k of this CTA.
 template <int kWorkers>
 __device__ __forceinline__ TreeLine tree_line(const TreeArgs& a, const TreePlanScratch* sc) {
     return TreeLine::of(a, sc->total, int(gridDim.x) * kWorkers);
 }
 template <int kWorkers>
-__device__ __forceinline__ TreeWalk tree_start(const TreeLine& line, const TreePlanScratch* sc, int k) {
+__device__ __forceinline__ TreeWalk tree_start(const TreeLine& line, const TreePlanScratch* sc, int k, int tail = 0) {
     TreeWalk w;
-    const int worker = int(blockIdx.x) * kWorkers + k;
-    w.range = line.tail == 0 ? worker : 2 * worker;
+    const auto& at = sc->at[2 * k + tail];
+    w.range = line.range(int(blockIdx.x) * kWorkers + k, tail);
     w.unit = w.begin = line.start(w.range);
-    w.b = sc->at[k].b;
-    w.hh = sc->at[k].hh;
-    w.tau = sc->at[k].tau;
-    w.pos = sc->at[k].pos;
-    w.r = sc->at[k].r;
+    w.b = at.b;
+    w.hh = at.hh;
+    w.tau = at.tau;
+    w.pos = at.pos;
+    w.r = at.r;
     w.end = w.b < 0 ? w.unit : line.end(w.range);
     return w;
 }
@@ -528,7 +535,10 @@ __global__ void __launch_bounds__(128, CfgTreeCc<D, kCols>::kBlocksPerSm) tree_c
     tree_plan<1>(a, &plan);
     const TreeLine line = tree_line<1>(a, &plan);
     TreeWalk walk = tree_start<1>(line, &plan, 0);
-    if (tid == 0) walk.write_split(a, line);
+    if (tid == 0) {
+        walk.write_split(a, line);
+        if (line.tail != 0) tree_start<1>(line, &plan, 0, 1).write_split(a, line);
+    }
     launch_dependents();
     TreeWalk::Seg s;
     for (;;) {
@@ -543,7 +553,6 @@ __global__ void __launch_bounds__(128, CfgTreeCc<D, kCols>::kBlocksPerSm) tree_c
             __syncthreads();
             if (claimed < 0) break;
             walk.locate(a, line, claimed);
-            if (tid == 0) walk.write_split(a, line);
             continue;
         }
         __syncthreads();

@@ -1,0 +1,140 @@
+"""Tree decode over lines long enough for tails: ranges that go to whichever worker asks first."""
+import math
+
+import numpy as np
+import pytest
+import torch
+
+from tests.spec_helpers import TYPES, Paged, check_tree, pack, tree_bits
+
+pytestmark = pytest.mark.gpu
+
+CODES = {"f32": 0, "f16": 1, "bf16": 2}
+#: Words of the workspace: ranges asked for so far (int32), and the line's total, share and tail (int64).
+CLAIMS, LINE = 128 // 4, 256 // 8
+
+
+def reference(c, q, masks, sm_scale):
+    """(o, lse, sum of weight * |v|) in 64 bits on the card."""
+    total, hq, d = q.shape
+    hk = c.k.shape[1]
+    o = torch.zeros(total, hq, d, dtype=torch.float64)
+    mag, lse = torch.zeros_like(o), torch.full((total, hq), -math.inf, dtype=torch.float64)
+    for b, n in enumerate(c.new):
+        if n == 0:
+            continue
+        rows = slice(int(c.new_indptr[b]), int(c.new_indptr[b + 1]))
+        k, v = (x.cuda() for x in c.dense(b))
+        seen = np.concatenate([np.ones((n, c.kv[b] - n), bool), masks[b]], 1)
+        x = torch.einsum("nhgd,thd->nhgt", q[rows].double().cuda().view(n, hk, hq // hk, d), k) * sm_scale
+        x.masked_fill_(~torch.from_numpy(seen).cuda()[:, None, None], -math.inf)
+        z = torch.logsumexp(x, -1)
+        w = torch.exp(x - z[..., None]).nan_to_num(0.0)
+        o[rows] = torch.einsum("nhgt,thd->nhgd", w, v).reshape(n, hq, d).cpu()
+        mag[rows] = torch.einsum("nhgt,thd->nhgd", w, v.abs()).reshape(n, hq, d).cpu()
+        lse[rows] = z.reshape(n, hq).cpu()
+    return o, lse, mag
+
+
+class Call:
+    """One decode whose inputs and workspace stay on the card."""
+
+    def __init__(self, kv, new, hq, hk, d, page, dtype, fp8, seed=0, kind="tree"):
+        import paged_kv_gqa_13_gb300 as pd
+
+        self.c = Paged(kv, new, hk, d, page, dtype, seed, fp8)
+        rng = np.random.default_rng(seed + 7)
+        self.q = torch.randn(sum(new), hq, d, generator=torch.Generator().manual_seed(seed + 3)).to(TYPES[dtype])
+        self.masks = [tree_bits(rng, n, kind) for n in new]
+        self.dtype, self.scale = dtype, 1 / math.sqrt(d)
+        words = max(1, -(-max(new) // 32))
+        self.mask = None if kind == "chain" else pack(self.masks, words).cuda()
+        self.dev = [x.cuda() for x in (self.q, self.c.k, self.c.v)]
+        self.scales = (self.c.k_scale.cuda(), self.c.v_scale.cuda()) if fp8 else ()
+        self.table = self.c.table()
+        self.ws = pd.alloc_workspace(pd.pd_paged_tree_decode_workspace_bytes(hq, hk, d, CODES[dtype]))
+        self.o = torch.empty_like(self.dev[0])
+        self.lse = torch.empty(self.q.shape[:2], device="cuda")
+        self.fn = pd.pd_paged_tree_decode_fp8 if fp8 else pd.pd_paged_tree_decode
+
+    def run(self):
+        self.o.fill_(math.nan)
+        self.lse.fill_(math.nan)
+        self.launch()
+        torch.cuda.synchronize()
+        return self.o.clone(), self.lse.clone()
+
+    def launch(self):
+        self.fn(*self.dev, *self.scales, *self.table, self.mask, self.o, self.lse, self.scale, self.ws)
+
+    def flags(self):
+        import paged_kv_gqa_13_gb300 as pd
+
+        return pd.pd_read_device_flags(self.ws)
+
+    def line(self):
+        """(total, share, tail) in units."""
+        return tuple(int(x) for x in self.ws[256:280].view(torch.int64))
+
+    def check(self, what=""):
+        o, lse = self.run()
+        assert self.flags() == 0
+        check_tree(o, lse, reference(self.c, self.q, self.masks, self.scale), self.dtype, what)
+        return o, lse
+
+
+# dtype, E4M3 pools, q heads, kv heads, head_dim, requests, nodes up to: the narrow and the wide form, one line, CUDA cores
+FORMS = [("bf16", False, 32, 16, 64, 64, 3), ("f16", False, 32, 16, 128, 48, 3), ("bf16", False, 16, 16, 256, 40, 3),
+         ("f16", True, 32, 16, 64, 64, 3), ("bf16", True, 128, 16, 64, 64, 16), ("bf16", True, 64, 8, 128, 80, 16),
+         ("f16", True, 16, 16, 256, 40, 3), ("f32", False, 32, 16, 64, 64, 3), ("f32", False, 32, 16, 128, 48, 3)]
+
+
+def _lengths(requests, nodes, seed):
+    rng = np.random.default_rng(seed)
+    new = [int(x) for x in rng.integers(max(1, nodes - 6), nodes + 1, requests)]
+    return [int(x) for x in rng.integers(1000, 2400, requests)], new
+
+
+@pytest.mark.parametrize("dtype,fp8,hq,hk,d,requests,nodes", FORMS)
+def test_tails_are_right_and_repeat_bit_for_bit(dtype, fp8, hq, hk, d, requests, nodes):
+    call = Call(*_lengths(requests, nodes, d), hq, hk, d, 16, dtype, fp8, seed=1)
+    first = call.check((dtype, fp8, d))
+    total, share, tail = call.line()
+    assert share >= 48 and tail == share // 8 and total > share
+    assert int(call.ws[128:132].view(torch.int32)) == 0  # set back by the merge
+    for _ in range(4):
+        again = call.run()
+        assert torch.equal(first[0], again[0]) and torch.equal(first[1], again[1])
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        call.launch()
+    for _ in range(3):
+        call.o.fill_(math.nan)
+        graph.replay()
+    torch.cuda.synchronize()
+    assert torch.equal(first[0], call.o) and torch.equal(first[1], call.lse)
+    assert call.flags() == 0
+
+
+@pytest.mark.parametrize("dtype,fp8,hq,hk,d,requests,nodes", [FORMS[0], FORMS[2], FORMS[4], FORMS[7]])
+def test_tails_that_nobody_runs_leave_this_calls_descriptors(dtype, fp8, hq, hk, d, requests, nodes):
+    """As after a call whose every worker gave up: no tail is run, and the merge still reads descriptors of this call
+    alone, however the workspace looked before. The rows that need a tail are undefined; the next call is right."""
+    import paged_kv_gqa_13_gb300 as pd
+
+    call = Call(*_lengths(requests, nodes, d), hq, hk, d, 16, dtype, fp8, seed=2)
+    call.ws.fill_(0x7F)
+    pd.pd_workspace_init(call.ws)
+    # rows of the outputs' surroundings must stay as they are
+    guard = torch.full((call.o.numel() + 4096,), 7.0, dtype=call.o.dtype, device="cuda")
+    call.o = guard[2048:2048 + call.o.numel()].view(call.o.shape)
+    call.ws[128:132].view(torch.int32).fill_(1 << 20)  # every tail has been asked for
+    call.run()
+    assert call.line()[2] > 0
+    ranges = 2 * (-(-call.line()[0] // call.line()[1]))
+    splits = call.ws[256:256 + 32 * ranges].view(torch.int32).view(ranges, 8)[1:].cpu()
+    cut = splits[splits[:, 0] != 0]
+    assert len(cut) > 0 and bool((cut[:, 0] >= 2).all()) and bool((cut[:, 0] <= ranges).all())
+    assert bool((cut[:, 1] >= 0).all()) and bool((cut[:, 1] + cut[:, 2] <= sum(call.c.new)).all())
+    assert bool((guard[:2048] == 7).all()) and bool((guard[2048 + call.o.numel():] == 7).all())
+    call.check()

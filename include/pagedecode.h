@@ -507,7 +507,8 @@ pd_status pd_rope(const void* x, const int32_t* positions, const uint64_t* freqs
  *
  * q: device [total_new] tokens of num_qo_heads heads, q_stride elements apart;
  *   q_out: device [total_new, num_qo_heads, head_dim], may be q if q is laid
- *   out so. num_qo_heads = 0 leaves q out (q, q_out may be NULL).
+ *   out so (refused otherwise), and must not otherwise overlap it.
+ *   num_qo_heads = 0 leaves q out (q, q_out may be NULL).
  * k_new, v_new: device [total_new] tokens of num_kv_heads heads, k_stride and
  *   v_stride elements apart. q, k_new and v_new may be views of one tensor.
  * positions: device int32 [total_new], or NULL for each token's index in its

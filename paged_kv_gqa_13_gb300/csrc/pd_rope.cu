@@ -497,6 +497,9 @@ pd_status append_impl(const void* q, const void* k_new, const void* v_new, const
         return host::fail(PD_ERR_INVALID, "null pointer argument");
     if (k_stride < (long long)Hk * D || v_stride < (long long)Hk * D || (Hq > 0 && q_stride < (long long)Hq * D))
         return host::fail(PD_ERR_INVALID, "a token's stride must hold its heads");
+    // (one token lies where it lies whatever its stride)
+    if (Hq > 0 && total_new > 1 && q == q_out && q_stride != (long long)Hq * D)
+        return host::fail(PD_ERR_INVALID, "q_out may be q only where q_stride is num_qo_heads * head_dim");
     const size_t e = host::elem_size(dt);
     if (!host::aligned(k_data, 16) || !host::aligned(v_data, 16))
         return host::fail(PD_ERR_UNSUPPORTED, "k_data and v_data must be 16-byte aligned");

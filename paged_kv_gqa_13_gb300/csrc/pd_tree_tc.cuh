@@ -208,13 +208,14 @@ struct CfgTree {
                          kPvDone = kPFull + 2 * kPipes, kAllDone = kPvDone + 2 * kPipes, kSegFull = kAllDone + kPipes,
                          kSegFree = kSegFull + kSegRing, kStFull = kSegFree + kSegRing, kStEmpty = kStFull + kStages,
                          kBars = kStEmpty + kStages;
-    // a line's shared memory: q, ring | barriers, bad-V tags[4], bad slots, segments (of all lines, after the data)
+    // a line's shared memory: q, ring | barriers, bad-V tags, bad slots, segments (of all lines, after the data)
     static constexpr int kRingOff = kPipes * kQBytes;
     static constexpr int kStageOff = kRingOff + kSlots * kSlotBytes;
     static constexpr int kLineBytes = kStageOff + kStages * kStageBytes;
     static constexpr int kTagOff = round_up(kBars * 8, 16);
-    static constexpr int kSegOff = kTagOff + 16 + 4 * kBadRing;
-    static constexpr int kCtlBytes = kSegOff + kSegRing * 72;
+    static constexpr int kBadOff = kTagOff + 4 * kSegRing;
+    static constexpr int kSegOff = kBadOff + 4 * kBadRing;
+    static constexpr int kCtlBytes = round_up(kSegOff + kSegRing * 68, 8);
     static constexpr int kCtlOff = kLines * kLineBytes;
     static constexpr int kMiscOff = kCtlOff + kLines * kCtlBytes;  // tensor-memory address, abort flag
     static constexpr int kBytes = kMiscOff + 16 + 1024;            // 1024: alignment of the base
@@ -248,6 +249,8 @@ struct TcSeg {
         return TreeReq{n, start, len, lo, 0};
     }
 };
+
+static_assert(sizeof(TcSeg) == 68, "CfgTree::kCtlBytes");
 
 // A place in a ring of N slots and the phase of its barriers.
 template <int N>
@@ -294,9 +297,11 @@ __global__ void __launch_bounds__(CfgTree<D, kWide, kFp8>::kThreads, 1)
     uint8_t* ctl = base + C::kCtlOff + (idle ? 0 : line) * C::kCtlBytes;
     const uint32_t sbase = smem_u32(smem), bars = smem_u32(ctl);
     auto bar = [&](int i) { return bars + 8u * uint32_t(i); };
+    // of the segment in each place of their ring: its number + 1 once non-finite V elements were found. The place is
+    // filled again only after the softmax warps have read it.
     volatile int* bad_v = reinterpret_cast<volatile int*>(ctl + C::kTagOff);
     // slots of each K block whose page id is bad, by the K block's number in this line
-    volatile uint32_t* bad_slots = reinterpret_cast<volatile uint32_t*>(ctl + C::kTagOff + 16);
+    volatile uint32_t* bad_slots = reinterpret_cast<volatile uint32_t*>(ctl + C::kBadOff);
     TcSeg* segs = reinterpret_cast<TcSeg*>(ctl + C::kSegOff);
     uint32_t* tslot = reinterpret_cast<uint32_t*>(base + C::kMiscOff);
     volatile int* abort_flag = reinterpret_cast<volatile int*>(base + C::kMiscOff + 4);
@@ -330,7 +335,7 @@ __global__ void __launch_bounds__(CfgTree<D, kWide, kFp8>::kThreads, 1)
             }
             fence_mbar_init();
             *abort_flag = 0;
-            for (int i = 0; i < 4; ++i) bad_v[i] = 0;
+            for (int i = 0; i < C::kSegRing; ++i) bad_v[i] = 0;
         }
         __syncwarp();
         if (line == 0) tmem_alloc(smem_u32(tslot), 512);
@@ -666,7 +671,7 @@ __global__ void __launch_bounds__(CfgTree<D, kWide, kFp8>::kThreads, 1)
                                                e4m3x2_to_f16x2(w[x].y >> 16));
                             }
                         }
-                        if (found) bad_v[i & 3] = i + 1;
+                        if (found) bad_v[i % C::kSegRing] = i + 1;
                         fence_proxy_async_smem();
                         __syncwarp();
                         if (lane == 0) {
@@ -704,7 +709,7 @@ __global__ void __launch_bounds__(CfgTree<D, kWide, kFp8>::kThreads, 1)
                                 }
                             }
                         }
-                        if (found) bad_v[i & 3] = i + 1;
+                        if (found) bad_v[i % C::kSegRing] = i + 1;
                         fence_proxy_async_smem();
                         __syncwarp();
                         if (lane == 0) mbar_arrive(bar(C::kVok + ring.slot));
@@ -874,7 +879,7 @@ __global__ void __launch_bounds__(CfgTree<D, kWide, kFp8>::kThreads, 1)
             if (live) {
                 const float inv = (m == kNegInf ? 0.f : 1.f / l) * s.v_scale;
                 const float lse2 = m == kNegInf ? kNegInf : m - kShift + log2f(l);
-                const bool fix = bad_v[seg & 3] == seg + 1;
+                const bool fix = bad_v[seg % C::kSegRing] == seg + 1;
                 const size_t prow = size_t(s.slot) * a.seg_rows + row + p * C::kRows;
 #pragma unroll 1
                 for (int c = 0; c < D; c += 32) {

@@ -1,5 +1,7 @@
 """Edges of the speculative-decoding calls: rows in place, empty tables, NaN, bits of copied rows."""
 
+import math
+
 import numpy as np
 import pytest
 import torch
@@ -32,3 +34,44 @@ def test_append_rotates_q_in_place(dtype, tokens, wide):
     ref = rope_reference(x[:, :hq], pos, _inv(d), 0)
     assert bool(((q.double().cpu() - ref).abs() <= rope_tolerance(x[:, :hq], ref, dtype)).all())
     assert torch.equal(dev[:, hq:].cpu(), x[:, hq:])
+
+
+def _tree(c, q, masks, words, sm_scale, dtype):
+    """(o, lse, flags)"""
+    import paged_kv_gqa_13_gb300 as pd
+    from tests.spec_helpers import pack
+
+    hq, d = q.shape[1:]
+    ws = pd.alloc_workspace(pd.pd_paged_tree_decode_workspace_bytes(hq, c.k.shape[1], d, {"f32": 0, "f16": 1, "bf16": 2}[dtype]))
+    o = torch.full(q.shape, 7.0, dtype=TYPES[dtype], device="cuda")
+    lse = torch.full(q.shape[:2], 7.0, device="cuda")
+    scales = (c.k_scale.cuda(), c.v_scale.cuda()) if c.fp8 else ()
+    fn = pd.pd_paged_tree_decode_fp8 if c.fp8 else pd.pd_paged_tree_decode
+    fn(q.cuda(), c.k.cuda(), c.v.cuda(), *scales, *c.table(), None if masks is None else pack(masks, words).cuda(), o, lse,
+       sm_scale, ws)
+    torch.cuda.synchronize()
+    return o.cpu(), lse.cpu(), pd.pd_read_device_flags(ws)
+
+
+@pytest.mark.parametrize("dtype,fp8,d", [("bf16", False, 64), ("f16", False, 128), ("bf16", True, 64), ("f16", False, 256)])
+@pytest.mark.parametrize("hq,nodes", [(4, 3), (16, 20)])
+def test_non_finite_values_of_many_short_requests(dtype, fp8, d, hq, nodes):
+    """A non-finite V row in every request of one block: segment after segment of every worker has one to add."""
+    hk, batch = 2, 1500
+    new = [nodes] * batch
+    c = Paged([n + 11 for n in new], new, hk, d, 8, dtype, fp8=fp8)
+    q = torch.randn(sum(new), hq, d).to(TYPES[dtype])
+    clean, clean_lse, _ = _tree(c, q, None, 0, 0.1, dtype)
+    bad = 1  # the node with the row
+    for b in range(batch):
+        p, r = c.rows(b, [11 + bad])
+        if fp8:
+            c.v[p, :, r, 5] = 0x7F
+        else:
+            c.v[p, :, r, 5] = math.inf
+    o, lse, flags = _tree(c, q, None, 0, 0.1, dtype)
+    assert flags == 0 and torch.equal(lse, clean_lse)
+    o, clean = o.view(batch, nodes, hq, d), clean.view(batch, nodes, hq, d)
+    rest = [i for i in range(d) if i != 5]
+    assert torch.equal(o[:, :, :, rest], clean[:, :, :, rest]) and torch.equal(o[:, :bad], clean[:, :bad])
+    assert int(torch.isfinite(o[:, bad:, :, 5]).sum()) == 0

@@ -554,7 +554,7 @@ pd_status pd_paged_rope_append_fp8(const void* q, const void* k_new, const void*
  *
  * and a node that attends nothing gets o = 0, lse = -infinity. Tokens that a
  * node does not attend have no part in its result, whatever they hold (NaN and
- * infinities included).
+ * infinities included). A NaN among a node's scores makes its o and lse NaN.
  *
  * q, o: device [total_new, num_qo_heads, head_dim] T, 16-byte aligned.
  * tree_mask: device uint32 [total_new, mask_words], or NULL.

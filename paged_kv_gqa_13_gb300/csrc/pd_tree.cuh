@@ -455,8 +455,17 @@ __global__ void __launch_bounds__(256) tree_merge_kernel(const TreeArgs a) {
         if (at < 0) continue;  // past the group's last head
         auto slot = [&](int p) { return size_t(p == 0 ? s.slot0 : 2 * (s.r0 + p)) * a.seg_rows + row; };
         float acc[kPer] = {};
-        const float L = merge_rows<kPer, 8>(
+        float L = merge_rows<kPer, 8>(
             s.parts, [&](int p) { return a.part_lse[slot(p)]; }, [&](int p) { return a.part_o + slot(p) * D; }, acc);
+        if (L == kNegInf) {  // empty parts, or parts of NaN, which a maximum passes over
+            bool nan = false;
+            for (int p = threadIdx.x & 31; p < s.parts; p += 32) nan |= isnan(a.part_lse[slot(p)]);
+            if (__any_sync(kFull, nan)) {
+                L = __int_as_float(0x7fc00000);
+#pragma unroll
+                for (int e = 0; e < kPer; ++e) acc[e] = L;
+            }
+        }
         store_row<T, kPer>(static_cast<T*>(a.o) + at * D, acc);
         if ((threadIdx.x & 31) == 0) a.lse[at] = L == kNegInf ? kNegInf : L * kLn2;
     }
@@ -699,8 +708,9 @@ __global__ void __launch_bounds__(128, CfgTreeCc<D, kCols>::kBlocksPerSm) tree_c
             for (int off = 1; off < kCols; off <<= 1) L += __shfl_xor_sync(kFull, L, off);
             const long long at = tree_row(a, s.row0, s.nodes, s.hh, row);
             if (at < 0) continue;
-            const float inv = m[j] == kNegInf ? 0.f : 1.f / L;
-            const float lse2 = m[j] == kNegInf ? kNegInf : m[j] + log2f(L);
+            // empty by the sum: the maximum passes over scores of NaN, the sum does not
+            const float inv = L == 0.f ? 0.f : 1.f / L;
+            const float lse2 = L == 0.f ? kNegInf : m[j] + log2f(L);
 #pragma unroll
             for (int i = 0; i < kVecs; ++i) {
                 float f[8] = {};

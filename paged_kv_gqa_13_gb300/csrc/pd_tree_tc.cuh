@@ -877,8 +877,9 @@ __global__ void __launch_bounds__(CfgTree<D, kWide, kFp8>::kThreads, 1)
             if (!wait(C::kPvDone + 2 * p + ((jobs - 1) & 1), uint32_t((jobs - 1) >> 1) & 1u)) break;
             tc_fence_after();
             if (live) {
-                const float inv = (m == kNegInf ? 0.f : 1.f / l) * s.v_scale;
-                const float lse2 = m == kNegInf ? kNegInf : m - kShift + log2f(l);
+                // empty by the sum: the maximum passes over scores of NaN, the sum does not
+                const float inv = (l == 0.f ? 0.f : 1.f / l) * s.v_scale;
+                const float lse2 = l == 0.f ? kNegInf : m - kShift + log2f(l);
                 const bool fix = bad_v[seg % C::kSegRing] == seg + 1;
                 const size_t prow = size_t(s.slot) * a.seg_rows + row + p * C::kRows;
 #pragma unroll 1

@@ -75,3 +75,45 @@ def test_non_finite_values_of_many_short_requests(dtype, fp8, d, hq, nodes):
     rest = [i for i in range(d) if i != 5]
     assert torch.equal(o[:, :, :, rest], clean[:, :, :, rest]) and torch.equal(o[:, :bad], clean[:, :bad])
     assert int(torch.isfinite(o[:, bad:, :, 5]).sum()) == 0
+
+
+NAN_FORMS = [("f32", False, 64), ("f32", False, 128), ("f32", False, 256), ("f16", False, 128), ("bf16", False, 64),
+             ("bf16", False, 256), ("f16", True, 128), ("bf16", True, 64), ("bf16", True, 256)]
+
+
+@pytest.mark.parametrize("dtype,fp8,d", NAN_FORMS)
+@pytest.mark.parametrize("kv,n", [(3, 3), (40, 3), (9000, 3), (30, 20), (9000, 40)])
+def test_nan_in_q_makes_its_rows_nan(dtype, fp8, d, kv, n):
+    """Whether the segment is cut or not: o and lse of the row are NaN, never those of a row that attends nothing."""
+    hq, hk = 8, 2
+    c = Paged([kv, 70], [n, 2], hk, d, 16, dtype, fp8=fp8)
+    q = torch.randn(n + 2, hq, d).to(TYPES[dtype])
+    masks = [np.tril(np.ones((m, m), bool)) for m in (n, 2)]
+    masks[0][0] = False
+    masks[0][0, 0] = True
+    clean, clean_lse, _ = _tree(c, q, masks, 2, 0.1, dtype)
+    broken = q.clone()
+    broken[1, 3, 7] = math.nan
+    broken[n - 1, 6] = math.nan
+    o, lse, flags = _tree(c, broken, masks, 2, 0.1, dtype)
+    hit = torch.zeros(n + 2, hq, dtype=torch.bool)
+    hit[1, 3] = hit[n - 1, 6] = True
+    assert flags == 0
+    assert bool(torch.isnan(lse[hit]).all()) and bool(torch.isnan(o[hit]).all())
+    assert torch.equal(o[~hit], clean[~hit]) and torch.equal(lse[~hit], clean_lse[~hit])
+
+
+@pytest.mark.parametrize("dtype,fp8,d", NAN_FORMS)
+@pytest.mark.parametrize("kv", [12, 9000])
+def test_nan_in_a_cached_key_makes_every_row_nan(dtype, fp8, d, kv):
+    hq, hk, n = 4, 2, 3
+    c = Paged([kv, 70], [n, 2], hk, d, 16, dtype, fp8=fp8)
+    q = torch.randn(n + 2, hq, d).to(TYPES[dtype])
+    clean, clean_lse, _ = _tree(c, q, None, 0, 0.1, dtype)
+    p, r = c.rows(0, [kv - n - 1])
+    c.k[p, 0, r, 3] = 0x7F if fp8 else math.nan
+    o, lse, flags = _tree(c, q, None, 0, 0.1, dtype)
+    assert flags == 0
+    assert bool(torch.isnan(lse[:n, :2]).all()) and bool(torch.isnan(o[:n, :2]).all())
+    assert torch.equal(o[:n, 2:], clean[:n, 2:]) and torch.equal(lse[:n, 2:], clean_lse[:n, 2:])
+    assert torch.equal(o[n:], clean[n:]) and torch.equal(lse[n:], clean_lse[n:])

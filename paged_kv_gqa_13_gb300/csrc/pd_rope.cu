@@ -371,8 +371,8 @@ struct CommitArgs {
 // V (the next n). Lane i finds the places of the path's node i, 32 at a time;
 // then a lane owns whole columns of chunks and walks them in order, kRound rows
 // at a time, loads before stores. A path increases, so path[i] >= i: no row is
-// written before it has been read. Bound by a chain of four dependent reads
-// (lengths, path, page, row): 3.2 us for 32 requests, 4.3 for 256 that keep up
+// written before it has been read; no row moves where one of the pages is bad.
+// Bound by a chain of four dependent reads (lengths, path, page, row): 3.2 us for 32 requests, 4.3 for 256 that keep up
 // to 12 of 64 nodes (places found one after another: 8.1).
 __global__ void __launch_bounds__(128) commit_kernel(const CommitArgs a) {
     constexpr int kRound = 8;
@@ -423,16 +423,25 @@ __global__ void __launch_bounds__(128) commit_kernel(const CommitArgs a) {
         *off = ((size_t(page) * a.hk + kh) * a.page_size + size_t(at - (long long)nth * a.page_size)) * a.row_bytes;
         return page >= 0 && page < a.num_total_pages;
     };
-    bool bad_page = false;
-    for (int i0 = 0; i0 < len; i0 += 32) {
+    size_t from = 0, to = 0;
+    bool go = false;
+    // the places of node i0 + lane of the path; false: a bad page
+    auto find = [&](int i0) {
         if (i0 > 0) mine = i0 + lane < len ? __ldg(path + i0 + lane) : 0;
-        size_t from = 0, to = 0;
-        bool go = i0 + lane < len && mine != i0 + lane;
-        if (go) {
-            const bool fine = locate(first + mine, &from) & locate(first + i0 + lane, &to);
-            bad_page |= !fine;
-            go = fine;
-        }
+        go = i0 + lane < len && mine != i0 + lane;
+        return !go || (locate(first + mine, &from) & locate(first + i0 + lane, &to));
+    };
+    // every page is looked at before the first row moves
+    bool fine = true;
+    for (int i0 = (len - 1) / 32 * 32; i0 > 0; i0 -= 32) fine &= find(i0);
+    if (len > 32) mine = __ldg(path + lane);
+    fine &= find(0);
+    if (!__all_sync(kFull, fine)) {
+        if (lane == 0 && kh == 0) atomicOr(a.flags, kFlagBadPage);
+        return;
+    }
+    for (int i0 = 0; i0 < len; i0 += 32) {
+        if (i0 > 0) find(i0);
         const unsigned moves = __ballot_sync(kFull, go);
         for (unsigned rest = moves; rest != 0u;) {
             size_t src[kRound], dst[kRound];
@@ -460,7 +469,6 @@ __global__ void __launch_bounds__(128) commit_kernel(const CommitArgs a) {
             }
         }
     }
-    if (__any_sync(kFull, bad_page) && lane == 0 && kh == 0) atomicOr(a.flags, kFlagBadPage);
 }
 
 // Checks shared by pd_rope and the appends.

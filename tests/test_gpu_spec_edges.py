@@ -117,3 +117,27 @@ def test_nan_in_a_cached_key_makes_every_row_nan(dtype, fp8, d, kv):
     assert bool(torch.isnan(lse[:n, :2]).all()) and bool(torch.isnan(o[:n, :2]).all())
     assert torch.equal(o[:n, 2:], clean[:n, 2:]) and torch.equal(lse[:n, 2:], clean_lse[:n, 2:])
     assert torch.equal(o[n:], clean[n:]) and torch.equal(lse[n:], clean_lse[n:])
+
+
+@pytest.mark.parametrize("elem", [1, 2, 4])
+@pytest.mark.parametrize("n,length", [(6, 3), (64, 50), (100, 80)])
+@pytest.mark.parametrize("where", ["from", "to", "late"])
+def test_commit_leaves_a_request_with_a_bad_page_as_it_is(elem, n, length, where):
+    import paged_kv_gqa_13_gb300 as pd
+
+    kv, new = [n + 20, n + 9], [n, n]
+    c = Paged(kv, new, 3, 64, 2, {1: "f16", 2: "f16", 4: "f32"}[elem], fp8=elem == 1)
+    rng = np.random.default_rng(n)
+    path = np.stack([np.sort(rng.choice(np.arange(1, n), length, replace=False)) for _ in range(2)]).astype(np.int32)
+    t = c.table()
+    # the page of the last node's row, of its place, or of a place in the middle
+    token = 20 + {"from": int(path[0, -1]), "to": length - 1, "late": length // 2}[where]
+    t[0][int(c.indptr[0]) + token // 2] = -1
+    k, v, ws = c.k.cuda(), c.v.cuda(), pd.alloc_workspace(256)
+    pd.pd_paged_tree_commit(k, v, *t, torch.from_numpy(path).cuda(), torch.full((2,), length, dtype=torch.int32, device="cuda"), ws)
+    assert pd.pd_read_device_flags(ws) == pd.PD_FLAG_BAD_PAGE_ID
+    for got, old in ((k.cpu(), c.k), (v.cpu(), c.v)):
+        want = old.clone()
+        src, dst = c.rows(1, 9 + path[1].astype(np.int64)), c.rows(1, 9 + np.arange(length))
+        want[dst[0], :, dst[1]] = old[src[0], :, src[1]]
+        assert torch.equal(got.view(torch.uint8), want.view(torch.uint8))

@@ -196,6 +196,17 @@ __global__ void __launch_bounds__(128, kPool == kNoPool ? 5 : 6) rope_kernel(con
                 store_elems<T, V>(static_cast<T*>(a.k_data) + at, f);
         }
     };
+    // The same of elements that are not rotated: w as they came, every bit of them, f as f32. E4M3 calls take f for q
+    // too: a NaN of q stays one, its payload does not (raw stores of q there cost registers, and 7000 tokens of 80
+    // heads 56.5 us instead of 53.7).
+    auto store_raw = [&](int h, int e, const Raw<T, V>& w, const float(&f)[V]) {
+        if constexpr (kPool == kCodePool)
+            store(h, e, f);
+        else if (kPool == kNoPool || h < a.hq)
+            *reinterpret_cast<Raw<T, V>*>(qo + (long long)h * D + e) = w;
+        else if (write_kv)
+            *reinterpret_cast<Raw<T, V>*>(static_cast<T*>(a.k_data) + dst + size_t(h - a.hq) * head_step + e) = w;
+    };
     const int h_end = min(i1, a.hq + a.hk);
 
     // ---- rotated elements of the q and k heads
@@ -270,7 +281,7 @@ __global__ void __launch_bounds__(128, kPool == kNoPool ? 5 : 6) rope_kernel(con
                     const int2 c = at(x + 32 * r);
                     float f[V];
                     widen<T, V>(w[r], f);
-                    to(c.x, c.y, f);
+                    to(c.x, c.y, w[r], f);
                 }
         }
     };
@@ -280,7 +291,7 @@ __global__ void __launch_bounds__(128, kPool == kNoPool ? 5 : 6) rope_kernel(con
             const int h = a.by_rest.div(x);
             return make_int2(q_from + h, rot + (x - h * rest) * V);
         },
-        source, store);
+        source, store_raw);
     if (!write_kv) return;
     const int v0 = max(i0 - a.hq - a.hk, 0), v1 = i1 - a.hq - a.hk;
     const T* vr = static_cast<const T*>(a.v) + (long long)t * a.v_stride;
@@ -291,12 +302,12 @@ __global__ void __launch_bounds__(128, kPool == kNoPool ? 5 : 6) rope_kernel(con
             return make_int2(v0 + h, (x - h * (D / V)) * V);
         },
         [&](int h) { return vr + (long long)h * D; },
-        [&](int h, int e, const float(&f)[V]) {
+        [&](int h, int e, const Raw<T, V>& w, const float(&f)[V]) {
             const size_t at = dst + size_t(h) * head_step + e;
             if constexpr (kPool == kCodePool)
                 store_codes<V>(static_cast<uint8_t*>(a.v_data) + at, f, __ldg(a.v_scale + h));
             else
-                store_elems<T, V>(static_cast<T*>(a.v_data) + at, f);
+                *reinterpret_cast<Raw<T, V>*>(static_cast<T*>(a.v_data) + at) = w;
         });
 }
 

@@ -141,3 +141,40 @@ def test_commit_leaves_a_request_with_a_bad_page_as_it_is(elem, n, length, where
         src, dst = c.rows(1, 9 + path[1].astype(np.int64)), c.rows(1, 9 + np.arange(length))
         want[dst[0], :, dst[1]] = old[src[0], :, src[1]]
         assert torch.equal(got.view(torch.uint8), want.view(torch.uint8))
+
+
+@pytest.mark.parametrize("dtype", ["f32", "f16", "bf16"])
+@pytest.mark.parametrize("off", [0, 1])
+@pytest.mark.parametrize("layout", [0, 1])
+def test_copied_elements_keep_every_bit(dtype, off, layout):
+    """v rows, and q and k elements past rot_dim: NaNs of every payload and sign among them."""
+    import paged_kv_gqa_13_gb300 as pd
+
+    n, hq, hk, d, rot = 512, 1, 1, 256, 128
+    size = 4 if dtype == "f32" else 2
+    word = torch.int32 if size == 4 else torch.int16
+    bits = torch.arange(n * 128, dtype=torch.int64)  # every 16-bit pattern
+    if size == 4:
+        bits = bits * 65536 + (bits * 40503) % 65536
+        bits = torch.where(bits >= 1 << 31, bits - (1 << 32), bits)
+    else:
+        bits = torch.where(bits >= 1 << 15, bits - (1 << 16), bits)
+    x = torch.zeros(n, hq + 2 * hk, d, dtype=word)
+    x[:, :, rot:] = bits.to(word).view(n, 1, 128)
+    x[:, hq + hk:, :rot] = bits.to(word).view(n, 1, 128).flip(0)
+    flat = torch.zeros(x.numel() + 8, dtype=word, device="cuda")
+    flat[off:off + x.numel()] = x.flatten().cuda()  # (off 1: rows off their 16 bytes, one element per access)
+    dev = flat[off:off + x.numel()].view(x.shape).view(TYPES[dtype])
+    c = Paged([n], [n], hk, d, 16, dtype)
+    q_out = torch.empty(n, hq, d, dtype=TYPES[dtype], device="cuda")
+    freqs, _ = pd.pd_rope_frequencies(rot)
+    k, v, ws = c.k.cuda(), c.v.cuda(), pd.alloc_workspace(256)
+    pd.pd_paged_rope_append(dev[:, :hq], dev[:, hq:hq + hk], dev[:, hq + hk:], None, freqs, q_out, k, v, *c.table(), ws,
+                            layout=layout)
+    p, r = c.rows(0, np.arange(n))
+    assert torch.equal(v.cpu().view(word)[p, :, r], x[:, hq + hk:])
+    assert torch.equal(k.cpu().view(word)[p, :, r, rot:], x[:, hq:hq + hk, rot:])
+    assert torch.equal(q_out.cpu().view(word)[..., rot:], x[:, :hq, rot:])
+    out = torch.empty(n, hq + 2 * hk, d, dtype=TYPES[dtype], device="cuda")
+    pd.pd_rope(dev, torch.zeros(n, dtype=torch.int32, device="cuda"), freqs, out, layout=layout)
+    assert torch.equal(out.cpu().view(word)[..., rot:], x[..., rot:])

@@ -440,8 +440,9 @@ pd_status pd_paged_decode_noalloc_flags(int32_t* flags, void* stream);
  * of the ragged tensors (new_indptr: device int32 [batch + 1], increasing from
  * 0 to total_new), n_b of them, and are the LAST n_b tokens of its cache: the
  * page table already describes them (the caller's update for n_b tokens).
- * n_b may be 0. A malformed new_indptr, or n_b > kv_len, is flagged with
- * PD_FLAG_BAD_NEW_ROWS and that request's rows are not written to the pool.
+ * n_b may be 0, and total_new too (the rows' pointers may then be NULL). A
+ * malformed new_indptr, or n_b > kv_len, is flagged with PD_FLAG_BAD_NEW_ROWS
+ * and that request's rows are not written to the pool.
  */
 
 /*

@@ -511,8 +511,8 @@ pd_status append_impl(const void* q, const void* k_new, const void* v_new, const
         return host::fail(PD_ERR_INVALID, "batch, num_kv_heads, page_size and num_total_pages must be positive");
     if (num_indices < 0 || Hq < 0 || Hq > (1 << 20) || Hk > (1 << 20))
         return host::fail(PD_ERR_INVALID, "num_indices and num_qo_heads must not be negative, heads at most 2^20");
-    if (!k_new || !v_new || !k_data || !v_data || !indptr || !last_page_len || !new_indptr ||
-        (num_indices > 0 && !indices) || (Hq > 0 && (!q || !q_out)) || (fp8 && (!k_scale || !v_scale)))
+    if (!k_data || !v_data || !indptr || !last_page_len || !new_indptr || (num_indices > 0 && !indices) ||
+        (total_new > 0 && (!k_new || !v_new || (Hq > 0 && (!q || !q_out)))) || (fp8 && (!k_scale || !v_scale)))
         return host::fail(PD_ERR_INVALID, "null pointer argument");
     if (k_stride < (long long)Hk * D || v_stride < (long long)Hk * D || (Hq > 0 && q_stride < (long long)Hq * D))
         return host::fail(PD_ERR_INVALID, "a token's stride must hold its heads");
@@ -617,10 +617,10 @@ pd_status pd_rope(const void* x, const int32_t* positions, const uint64_t* freqs
         return host::fail(PD_ERR_INVALID, "num_heads must be in [1, 2^20] and head_dim in [1, 4096]");
     const pd_status st = check_rotation(num_tokens, head_dim, rot_dim, layout, rope_scale, freqs, dtype);
     if (st != PD_OK) return st;
-    if (!x || !out || !positions) return host::fail(PD_ERR_INVALID, "null pointer argument");
+    if (num_tokens > 0 && (!x || !out || !positions)) return host::fail(PD_ERR_INVALID, "null pointer argument");
     if (x_stride < (long long)num_heads * head_dim || out_stride < (long long)num_heads * head_dim)
         return host::fail(PD_ERR_INVALID, "a token's stride must hold its heads");
-    if (x == out && x_stride != out_stride) return host::fail(PD_ERR_INVALID, "in place, both strides must be the same");
+    if (num_tokens > 1 && x == out && x_stride != out_stride) return host::fail(PD_ERR_INVALID, "in place, both strides must be the same");
     const size_t e = host::elem_size(dtype);
     if (!host::aligned(x, e) || !host::aligned(out, e) || !host::aligned(positions, 4))
         return host::fail(PD_ERR_UNSUPPORTED, "x and out must be aligned to their element, positions to 4 bytes");

@@ -126,7 +126,7 @@ pd_status tree_impl(const void* q, const void* k_data, const void* v_data, const
         return host::fail(PD_ERR_INVALID, "batch, page_size and num_total_pages must be positive");
     if (total_new < 0 || num_indices < 0) return host::fail(PD_ERR_INVALID, "total_new and num_indices must not be negative");
     if (total_new > (1 << 30) || Hq > (1 << 20)) return host::fail(PD_ERR_INVALID, "at most 2^30 new rows and 2^20 heads");
-    if (tree_mask ? mask_words <= 0 : mask_words != 0)
+    if (tree_mask ? mask_words <= 0 : mask_words < 0 || (mask_words != 0 && total_new > 0))
         return host::fail(PD_ERR_INVALID, "mask_words must be positive with a tree_mask and 0 without (got %d)", mask_words);
     if (!std::isfinite(sm_scale)) return host::fail(PD_ERR_INVALID, "sm_scale must be finite");
     if (!k_data || !v_data || !indptr || !last_page_len || !new_indptr || (num_indices > 0 && !indices) ||

@@ -178,3 +178,28 @@ def test_copied_elements_keep_every_bit(dtype, off, layout):
     out = torch.empty(n, hq + 2 * hk, d, dtype=TYPES[dtype], device="cuda")
     pd.pd_rope(dev, torch.zeros(n, dtype=torch.int32, device="cuda"), freqs, out, layout=layout)
     assert torch.equal(out.cpu().view(word)[..., rot:], x[..., rot:])
+
+
+@pytest.mark.parametrize("dtype,fp8", [("f32", False), ("bf16", False), ("f16", True)])
+def test_a_step_without_a_new_token(dtype, fp8):
+    """Tables with requests and no new row: every call returns and writes nothing."""
+    import paged_kv_gqa_13_gb300 as pd
+
+    c = Paged([20, 0, 3], [0, 0, 0], 2, 128, 16, dtype, fp8=fp8)
+    rows = torch.zeros(0, 6, 128, dtype=TYPES[dtype], device="cuda")
+    q_out, lse = torch.empty(0, 2, 128, dtype=TYPES[dtype], device="cuda"), torch.empty(0, 2, device="cuda")
+    ws = pd.alloc_workspace(pd.pd_paged_tree_decode_workspace_bytes(2, 2, 128, {"f32": 0, "f16": 1, "bf16": 2}[dtype]))
+    k, v, t = c.k.cuda(), c.v.cuda(), c.table()
+    scales = (c.k_scale.cuda(), c.v_scale.cuda()) if fp8 else ()
+    freqs, _ = pd.pd_rope_frequencies(128)
+    pos = torch.empty(0, dtype=torch.int32, device="cuda")
+    pd.pd_rope(rows[:, :2], pos, freqs, q_out)
+    for p in (pos, None):
+        (pd.pd_paged_rope_append_fp8 if fp8 else pd.pd_paged_rope_append)(
+            rows[:, :2], rows[:, 2:4], rows[:, 4:], p, freqs, q_out, *scales, k, v, *t, ws)
+    for mask in (torch.empty(0, 2, dtype=torch.int32, device="cuda"), None):
+        (pd.pd_paged_tree_decode_fp8 if fp8 else pd.pd_paged_tree_decode)(q_out, k, v, *scales, *t, mask, q_out.clone(), lse, 0.1, ws)
+    path = torch.zeros(3, 4, dtype=torch.int32, device="cuda")
+    pd.pd_paged_tree_commit(k, v, *t, path, torch.zeros(3, dtype=torch.int32, device="cuda"), ws)
+    assert pd.pd_read_device_flags(ws) == 0
+    assert torch.equal(k.cpu().view(torch.uint8), c.k.view(torch.uint8)) and torch.equal(v.cpu().view(torch.uint8), c.v.view(torch.uint8))

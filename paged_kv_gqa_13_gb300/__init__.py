@@ -538,8 +538,8 @@ def _tree_decode(fn, scales, q, k_data, v_data, indices, indptr, last_page_len, 
         _bad("q and o [total_new, Hq, D] of one type, lse float32 [total_new, Hq], the pools' D")
     words = 0
     if tree_mask is not None:
-        if tree_mask.dim() != 2 or tree_mask.shape[0] != total_new:
-            _bad("tree_mask is [total_new, words] of 32 bits each")
+        if tree_mask.dim() != 2 or tree_mask.shape[0] != total_new or (total_new and tree_mask.shape[1] == 0):
+            _bad("tree_mask is [total_new, words] of 32 bits each, one word at least")
         words = tree_mask.shape[1]
     table, batch, entries = _table(indices, indptr, last_page_len, new_indptr)
     _check(fn(_ptr(q), _ptr(k_data), _ptr(v_data), *scales, *table, _int32(tree_mask), _ptr(o), _ptr(lse), batch, total_new,

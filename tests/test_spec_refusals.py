@@ -58,3 +58,24 @@ def test_tree_decode_without_a_node_needs_no_mask_rows():
     assert status in (pd.PD_OK, pd.PD_ERR_CUDA), pd.pd_last_error_string()  # PD_ERR_CUDA: no device here
     assert _call("pd_paged_tree_decode", TREE, mask=None, words=-1, **rows) == pd.PD_ERR_INVALID
     assert _call("pd_paged_tree_decode", TREE, mask=None, words=2) == pd.PD_ERR_INVALID
+
+
+def test_wrapper_refuses_a_mask_without_words():
+    """Its pointer would be null, which is the chain."""
+    import pytest
+    import torch
+
+    import paged_kv_gqa_13_gb300 as pd
+
+    i32 = lambda *v: torch.tensor(v, dtype=torch.int32)  # noqa: E731
+    pool, q, lse = torch.zeros(3, 2, 16, 128), torch.zeros(4, 2, 128), torch.zeros(4, 2)
+    ws = torch.zeros(4096, dtype=torch.uint8)
+    with pytest.raises(pd.PagedecodeError) as e:
+        pd.pd_paged_tree_decode(q, pool, pool, i32(0), i32(0, 1), i32(4), i32(0, 4), torch.zeros(4, 0, dtype=torch.int32),
+                                torch.zeros_like(q), lse, 0.1, ws, stream=0)
+    assert e.value.status == pd.PD_ERR_INVALID and "words" in str(e.value)
+    codes = torch.zeros(3, 2, 16, 128, dtype=torch.uint8)
+    s = torch.ones(2)
+    with pytest.raises(pd.PagedecodeError, match="words"):
+        pd.pd_paged_tree_decode_fp8(q.half(), codes, codes, s, s, i32(0), i32(0, 1), i32(4), i32(0, 4),
+                                    torch.zeros(4, 0, dtype=torch.int32), q.half(), lse, 0.1, ws, stream=0)

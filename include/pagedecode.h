@@ -442,7 +442,11 @@ pd_status pd_paged_decode_noalloc_flags(int32_t* flags, void* stream);
  * page table already describes them (the caller's update for n_b tokens).
  * n_b may be 0, and total_new too (the rows' pointers may then be NULL). A
  * malformed new_indptr, or n_b > kv_len, is flagged with PD_FLAG_BAD_NEW_ROWS
- * and that request's rows are not written to the pool.
+ * and that request's rows are not written to the pool. last_page_len may be 0
+ * (an allocated page that is still empty; the new tokens end in the page
+ * before it). Outside [0, page_size] it is flagged with
+ * PD_FLAG_BAD_LAST_PAGE_LEN: the append and the commit, which write, skip the
+ * request; the tree decode clamps it, as the decode does.
  */
 
 /*

@@ -157,7 +157,7 @@ __global__ void __launch_bounds__(128, kPool == kNoPool ? 5 : 6) rope_kernel(con
             bad = kFlagBadNewRows;
         else if (lo < 0 || hi <= lo || hi > a.num_indices)
             bad = kFlagBadIndptr;
-        else if (last < 1 || last > a.page_size)
+        else if (last < 0 || last > a.page_size)
             bad = kFlagBadLastPageLen;
         else {
             const long long kv = ((long long)hi - lo - 1) * a.page_size + last;
@@ -404,7 +404,7 @@ __global__ void __launch_bounds__(128) commit_kernel(const CommitArgs a) {
         bad = kFlagBadNewRows;
     else if (lo < 0 || hi <= lo || hi > a.num_indices)
         bad = kFlagBadIndptr;
-    else if (last < 1 || last > a.page_size)
+    else if (last < 0 || last > a.page_size)
         bad = kFlagBadLastPageLen;
     else if (kv < e - s)
         bad = kFlagBadNewRows;

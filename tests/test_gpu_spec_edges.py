@@ -203,3 +203,60 @@ def test_a_step_without_a_new_token(dtype, fp8):
     pd.pd_paged_tree_commit(k, v, *t, path, torch.zeros(3, dtype=torch.int32, device="cuda"), ws)
     assert pd.pd_read_device_flags(ws) == 0
     assert torch.equal(k.cpu().view(torch.uint8), c.k.view(torch.uint8)) and torch.equal(v.cpu().view(torch.uint8), c.v.view(torch.uint8))
+
+
+@pytest.mark.parametrize("dtype,fp8", [("f32", False), ("bf16", False), ("f16", True)])
+def test_an_allocated_page_that_is_still_empty(dtype, fp8):
+    """last_page_len = 0: the new tokens end in the page before, for the append, the tree decode and the commit alike."""
+    import paged_kv_gqa_13_gb300 as pd
+    from tests.spec_helpers import check_tree, pack, tree_bits, tree_reference
+
+    kv, new, hq, hk, d, page = [48, 16, 32, 21], [5, 16, 1, 4], 4, 2, 64, 16
+    c = Paged(kv, new, hk, d, page, dtype, fp8=fp8)
+    # a page more for the first three requests, with nothing in it
+    spare = [x for x in range(c.total) if x not in set(c.indices.tolist())]
+    parts = np.split(c.indices, c.indptr[1:-1])
+    parts = [np.append(p, spare[b]).astype(np.int32) if b < 3 else p for b, p in enumerate(parts)]
+    indices, indptr = np.concatenate(parts), np.concatenate([[0], np.cumsum([len(p) for p in parts])]).astype(np.int32)
+    last = np.array([0, 0, 0, c.last[3]], np.int32)
+    t = tuple(torch.from_numpy(x).cuda() for x in (indices, indptr, last, c.new_indptr))
+    # the nodes' rows go in by the append
+    want_k, want_v = c.k.clone(), c.v.clone()
+    n = sum(new)
+    x = torch.randn(n, 2 * hk, d).to(TYPES[dtype])
+    for b in range(4):
+        p, r = c.rows(b, np.arange(kv[b] - new[b], kv[b]))
+        rows = slice(int(c.new_indptr[b]), int(c.new_indptr[b + 1]))
+        for pool, scale, part in ((want_k, "k_scale", x[rows, :hk]), (want_v, "v_scale", x[rows, hk:])):
+            if fp8:
+                part = (part.float() / getattr(c, scale)[:, None]).clamp(-448, 448).to(torch.float8_e4m3fn).view(torch.uint8)
+            pool[p, :, r] = part
+    k, v = c.k.cuda(), c.v.cuda()
+    ws = pd.alloc_workspace(pd.pd_paged_tree_decode_workspace_bytes(hq, hk, d, {"f32": 0, "f16": 1, "bf16": 2}[dtype]))
+    scales = (c.k_scale.cuda(), c.v_scale.cuda()) if fp8 else ()
+    dev = x.cuda()
+    (pd.pd_paged_rope_append_fp8 if fp8 else pd.pd_paged_rope_append)(
+        None, dev[:, :hk], dev[:, hk:], None, None, None, *scales, k, v, *t, ws)
+    assert pd.pd_read_device_flags(ws) == 0
+    assert torch.equal(k.cpu().view(torch.uint8), want_k.view(torch.uint8))
+    assert torch.equal(v.cpu().view(torch.uint8), want_v.view(torch.uint8))
+    c.k, c.v = want_k, want_v
+    q = torch.randn(n, hq, d).to(TYPES[dtype])
+    masks = [tree_bits(np.random.default_rng(b), m) for b, m in enumerate(new)]
+    o, lse = torch.empty(n, hq, d, dtype=TYPES[dtype], device="cuda"), torch.empty(n, hq, device="cuda")
+    (pd.pd_paged_tree_decode_fp8 if fp8 else pd.pd_paged_tree_decode)(
+        q.cuda(), k, v, *scales, *t, pack(masks, 1).cuda(), o, lse, 0.1, ws)
+    assert pd.pd_read_device_flags(ws) == 0
+    check_tree(o, lse, tree_reference(c, q, masks, 0.1), dtype)
+    path = torch.tensor([[1, 4], [3, 15], [0, 0], [2, 3]], dtype=torch.int32)
+    length = torch.tensor([2, 2, 1, 2], dtype=torch.int32)
+    pd.pd_paged_tree_commit(k, v, *t, path.cuda(), length.cuda(), ws)
+    assert pd.pd_read_device_flags(ws) == 0
+    for b in range(4):
+        first = kv[b] - new[b]
+        src, dst = c.rows(b, first + path[b, :length[b]].numpy()), c.rows(b, first + np.arange(int(length[b])))
+        kept = [pool[src[0], :, src[1]].clone() for pool in (c.k, c.v)]
+        for pool, rows in zip((want_k, want_v), kept):
+            pool[dst[0], :, dst[1]] = rows
+    assert torch.equal(k.cpu().view(torch.uint8), want_k.view(torch.uint8))
+    assert torch.equal(v.cpu().view(torch.uint8), want_v.view(torch.uint8))

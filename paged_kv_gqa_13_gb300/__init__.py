@@ -506,7 +506,8 @@ def pd_paged_rope_append(q, k_new, v_new, positions, freqs, q_out, k_data, v_dat
     """Rotate q into q_out and k_new into its pages, copy v_new into its pages.
 
     q, k_new, v_new [total_new, heads, D], tokens may be strided (views of one projection); q, q_out may be None;
-    positions int32 [total_new] or None (the index in the cache); freqs None appends without rotation.
+    positions int32 [total_new] or None (the index in the cache: right for a chain or a prompt; a tree's nodes are
+    at the cached length + their depth); freqs None appends without rotation.
     """
     if k_data.dtype != k_new.dtype:
         _bad("the pools have the type of k_new")

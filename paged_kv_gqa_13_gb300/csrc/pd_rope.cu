@@ -319,7 +319,9 @@ const void* pick_layout(int layout) {
 
 // The kernel that moves 16 bytes per access where every row allows it: the
 // rotated part a whole number of units, rows 16-byte aligned. Otherwise one
-// element per access (odd rotary sizes, unaligned views), several times slower.
+// element per access (odd rotary sizes, unaligned views): 8191 tokens of 64 bf16
+// heads 80 to 85 us from rows off their 16 bytes and 128 us with rot_dim 100,
+// against 50 (with 5 us of events each).
 template <typename T, int kPool>
 const void* pick_kernel(int layout, bool wide) {
     return wide ? pick_layout<T, kPool, Elt<T>::kVec>(layout) : pick_layout<T, kPool, 1>(layout);

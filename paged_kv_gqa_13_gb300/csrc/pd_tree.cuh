@@ -473,7 +473,7 @@ __global__ void __launch_bounds__(256) tree_merge_kernel(const TreeArgs a) {
 
 // ---------------------------------------------------------------- CUDA cores
 
-// Eight or four elements of a pool row to f32.
+// Four elements of a pool row to f32 (of q too, s = 1); s scales E4M3 codes.
 template <typename KV>
 __device__ __forceinline__ void pool_load4(const KV* p, float s, float* f) {
     if constexpr (sizeof(KV) == 4) {

@@ -37,6 +37,14 @@
 // instructions), so both products run in f16 for bf16 q too: the softmax warps
 // write q rows as f16 times a power of two each.
 //
+// Rounding. S, maxima, sums and O are f32. The weights are rounded to the
+// operand type, at most half a step each, because both operands of a product
+// have one type and V is 16-bit in memory: f32 weights would take V widened to
+// tf32, twice its bytes in shared memory at half the rate, or two products of
+// a weight's two parts. Sums take the weights before rounding, so that the
+// errors stay independent of each other. Against 64 bits: bf16 0.0023 of the
+// outputs' norm (f32 sums rounded once: 0.0017), f16 0.0003 (0.0002).
+//
 // The running maximum of a row moves only when it rises by more than 2^8 (the
 // weights then stay below 2^8, and O, in tensor memory, is rescaled rarely).
 //
@@ -71,8 +79,8 @@ __device__ __forceinline__ uint64_t l2_evict_normal_policy() {
     return p;
 }
 
-// Instruction descriptor of kind::f16: 16-bit A and B of one type, f32 accumulator.
-// neg_a: A is negated; b_mn: B is MN-major.
+// Instruction descriptor of kind::f16: 16-bit A and B of one type, f32
+// accumulator; b_mn: B is MN-major. kIdescNegA, set in it, negates A.
 __host__ __device__ constexpr uint32_t tc_idesc_f16(bool bf16, int M, int N, bool b_mn) {
     return (1u << 4) | (bf16 ? (1u << 7) | (1u << 10) : 0u) | (b_mn ? 1u << 16 : 0u) | (uint32_t(N >> 3) << 17) |
            (uint32_t(M >> 4) << 24);

@@ -41,9 +41,9 @@
 // operand type, at most half a step each, because both operands of a product
 // have one type and V is 16-bit in memory: f32 weights would take V widened to
 // tf32, twice its bytes in shared memory at half the rate, or two products of
-// a weight's two parts. Sums take the weights before rounding, so that the
-// errors stay independent of each other. Against 64 bits: bf16 0.0023 of the
-// outputs' norm (f32 sums rounded once: 0.0017), f16 0.0003 (0.0002).
+// a weight's two parts. Sums take the weights before rounding, so that lse is
+// that of f32 weights. Against 64 bits: bf16 0.0023 of the outputs' norm (f32
+// sums rounded once: 0.0017), f16 0.0003 (0.0002).
 //
 // The running maximum of a row moves only when it rises by more than 2^8 (the
 // weights then stay below 2^8, and O, in tensor memory, is rescaled rarely).

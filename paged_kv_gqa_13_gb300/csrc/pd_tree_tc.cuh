@@ -207,6 +207,11 @@ struct CfgTree {
     static constexpr int kThreads = round_up(32 * (kSoftWarps + kLines * kOthers), 128);
     static constexpr int kWalkers = kOthers + 4 * kPipes;  // warps that read a line's segments
     static constexpr int kSegRing = 8;
+    // Tags of segments with non-finite V: more than inspectors can be ahead of the softmax warps at a segment's end.
+    // V of the next segment is then still in its slot, so that V of at most (kSlots - 1) / 2 more has landed. (Eight
+    // tags everywhere: 64 trees over an E4M3 pool 145.0 -> 147.6 us, by other registers.)
+    static constexpr int kTags = kSlots > 5 ? kSegRing : 4;
+    static_assert(1 + (kSlots - 1) / 2 < kTags, "tags");
     static constexpr int kClaimAhead = kWide ? 3 : 5;
     static constexpr int kSegCost = kWide ? (kFp8 ? 3 : 0) : 3;       // see TreeArgs::seg_cost: an output takes about 5,000 cycles
     static constexpr int kBadRing = 16;  // more than the K blocks that the producers are ahead of the softmax warps
@@ -221,7 +226,7 @@ struct CfgTree {
     static constexpr int kStageOff = kRingOff + kSlots * kSlotBytes;
     static constexpr int kLineBytes = kStageOff + kStages * kStageBytes;
     static constexpr int kTagOff = round_up(kBars * 8, 16);
-    static constexpr int kBadOff = kTagOff + 4 * kSegRing;
+    static constexpr int kBadOff = kTagOff + 4 * kTags;
     static constexpr int kSegOff = kBadOff + 4 * kBadRing;
     static constexpr int kCtlBytes = round_up(kSegOff + kSegRing * 68, 8);
     static constexpr int kCtlOff = kLines * kLineBytes;
@@ -305,8 +310,7 @@ __global__ void __launch_bounds__(CfgTree<D, kWide, kFp8>::kThreads, 1)
     uint8_t* ctl = base + C::kCtlOff + (idle ? 0 : line) * C::kCtlBytes;
     const uint32_t sbase = smem_u32(smem), bars = smem_u32(ctl);
     auto bar = [&](int i) { return bars + 8u * uint32_t(i); };
-    // of the segment in each place of their ring: its number + 1 once non-finite V elements were found. The place is
-    // filled again only after the softmax warps have read it.
+    // of segment i, at i % kTags: i + 1 once non-finite V elements were found
     volatile int* bad_v = reinterpret_cast<volatile int*>(ctl + C::kTagOff);
     // slots of each K block whose page id is bad, by the K block's number in this line
     volatile uint32_t* bad_slots = reinterpret_cast<volatile uint32_t*>(ctl + C::kBadOff);
@@ -343,7 +347,7 @@ __global__ void __launch_bounds__(CfgTree<D, kWide, kFp8>::kThreads, 1)
             }
             fence_mbar_init();
             *abort_flag = 0;
-            for (int i = 0; i < C::kSegRing; ++i) bad_v[i] = 0;
+            for (int i = 0; i < C::kTags; ++i) bad_v[i] = 0;
         }
         __syncwarp();
         if (line == 0) tmem_alloc(smem_u32(tslot), 512);
@@ -679,7 +683,7 @@ __global__ void __launch_bounds__(CfgTree<D, kWide, kFp8>::kThreads, 1)
                                                e4m3x2_to_f16x2(w[x].y >> 16));
                             }
                         }
-                        if (found) bad_v[i % C::kSegRing] = i + 1;
+                        if (found) bad_v[i % C::kTags] = i + 1;
                         fence_proxy_async_smem();
                         __syncwarp();
                         if (lane == 0) {
@@ -717,7 +721,7 @@ __global__ void __launch_bounds__(CfgTree<D, kWide, kFp8>::kThreads, 1)
                                 }
                             }
                         }
-                        if (found) bad_v[i % C::kSegRing] = i + 1;
+                        if (found) bad_v[i % C::kTags] = i + 1;
                         fence_proxy_async_smem();
                         __syncwarp();
                         if (lane == 0) mbar_arrive(bar(C::kVok + ring.slot));
@@ -888,7 +892,7 @@ __global__ void __launch_bounds__(CfgTree<D, kWide, kFp8>::kThreads, 1)
                 // empty by the sum: the maximum passes over scores of NaN, the sum does not
                 const float inv = (l == 0.f ? 0.f : 1.f / l) * s.v_scale;
                 const float lse2 = l == 0.f ? kNegInf : m - kShift + log2f(l);
-                const bool fix = bad_v[seg % C::kSegRing] == seg + 1;
+                const bool fix = bad_v[seg % C::kTags] == seg + 1;
                 const size_t prow = size_t(s.slot) * a.seg_rows + row + p * C::kRows;
 #pragma unroll 1
                 for (int c = 0; c < D; c += 32) {

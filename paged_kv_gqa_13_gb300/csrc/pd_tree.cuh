@@ -455,21 +455,16 @@ __global__ void __launch_bounds__(256) tree_merge_kernel(const TreeArgs a) {
         if (at < 0) continue;  // past the group's last head
         auto slot = [&](int p) { return size_t(p == 0 ? s.slot0 : 2 * (s.r0 + p)) * a.seg_rows + row; };
         float acc[kPer] = {};
-        float L = merge_rows<kPer, 8>(
+        const float L = merge_rows<kPer, 8>(
             s.parts, [&](int p) { return a.part_lse[slot(p)]; }, [&](int p) { return a.part_o + slot(p) * D; }, acc);
-        if (L == kNegInf) {  // empty parts, or parts of NaN, which a maximum passes over
-            bool nan = false;
-            for (int p = threadIdx.x & 31; p < s.parts; p += 32) nan |= isnan(a.part_lse[slot(p)]);
-            if (__any_sync(kFull, nan)) {
-                L = __int_as_float(0x7fc00000);
-#pragma unroll
-                for (int e = 0; e < kPer; ++e) acc[e] = L;
-            }
-        }
         store_row<T, kPer>(static_cast<T*>(a.o) + at * D, acc);
         if ((threadIdx.x & 31) == 0) a.lse[at] = L == kNegInf ? kNegInf : L * kLn2;
     }
 }
+
+// A partial's lse for the merge, whose maximum over the parts would pass over
+// NaN: infinity comes through it, and makes the weights, o and lse NaN again.
+__device__ __forceinline__ float tree_part_lse(float lse2) { return isnan(lse2) ? __int_as_float(0x7f800000) : lse2; }
 
 // ---------------------------------------------------------------- CUDA cores
 
@@ -729,7 +724,7 @@ __global__ void __launch_bounds__(128, CfgTreeCc<D, kCols>::kBlocksPerSm) tree_c
             }
             if (tc == 0) {
                 if (s.slot >= 0)
-                    a.part_lse[size_t(s.slot) * a.seg_rows + row] = lse2;
+                    a.part_lse[size_t(s.slot) * a.seg_rows + row] = tree_part_lse(lse2);
                 else
                     a.lse[at] = lse2 == kNegInf ? kNegInf : lse2 * kLn2;
             }

@@ -951,7 +951,7 @@ __global__ void __launch_bounds__(CfgTree<D, kWide, kFp8>::kThreads, 1)
                 }
                 if (at >= 0) {
                     if (s.slot >= 0)
-                        a.part_lse[prow] = lse2;
+                        a.part_lse[prow] = tree_part_lse(lse2);
                     else
                         a.lse[at] = lse2 == kNegInf ? kNegInf : lse2 * kLn2;
                 }

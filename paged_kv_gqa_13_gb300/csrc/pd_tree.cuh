@@ -22,11 +22,10 @@
 // leaves a partial (o, lse) in each of its ranges, and the merge kernel combines
 // them in order. Only the device knows the lengths: every CTA sums the requests'
 // units itself (each thread a run of requests, one block-wide scan) and finds
-// its shares. A segment's merge descriptor belongs to the range whose start is
-// the first cut through the segment's blocks, and the worker whose share that
-// is (or whose share's tail) writes it before it waits for anything: every
-// descriptor that the merge reads is this call's, whoever runs the tails and
-// whether or not a wait has run out.
+// its shares; the range whose start is the first cut through a segment's blocks
+// writes the merge's descriptor. After a wait that ran out a tail may have gone
+// to nobody and its descriptor may be of another call: the merge reads none
+// whose places it does not find in this call's partials and rows.
 #pragma once
 
 #include "pd_merge.cuh"
@@ -172,8 +171,6 @@ struct TreeLine {
         l.tail = !a.tails || l.share < 48 ? 0 : l.share / 8;
         return l;
     }
-    // The range of a worker's share, or of its tail.
-    __device__ __forceinline__ int range(int worker, int of_tail) const { return tail == 0 ? worker : 2 * worker + of_tail; }
     __device__ __forceinline__ long long start(int r) const {
         return tail == 0 ? r * share : (r / 2 + 1) * share - (r % 2 != 0 ? tail : share);
     }
@@ -316,7 +313,7 @@ struct TreePlanScratch {
     struct {
         int b, hh, tau, pos;
         TreeReq r;
-    } at[4];  // where the share of each worker of the CTA starts (even), and its tail (odd)
+    } at[2];  // where each worker of the CTA starts
 };
 
 // Find the shares of this CTA's kWorkers workers. All threads of the block
@@ -341,7 +338,7 @@ __device__ __forceinline__ void tree_plan(const TreeArgs& a, TreePlanScratch* sc
         if (lane >= off) inc += x;
     }
     if (lane == 31) sc->sums[wid] = inc;
-    if (tid < 2 * kWorkers) sc->at[tid].b = -1;
+    if (tid < kWorkers) sc->at[tid].b = -1;
     __syncthreads();
     long long before = inc - mine, total = 0;
     for (int w = 0; w < min(nw, (a.batch + 31) / 32); ++w) {  // the others hold no request
@@ -355,9 +352,8 @@ __device__ __forceinline__ void tree_plan(const TreeArgs& a, TreePlanScratch* sc
         if (blockIdx.x == 0) *reinterpret_cast<TreeLine*>(a.splits) = line;
     }
 #pragma unroll
-    for (int k = 0; k < 2 * kWorkers; ++k) {
-        if (k % 2 != 0 && line.tail == 0) continue;
-        const long long unit = line.start(line.range(int(blockIdx.x) * kWorkers + k / 2, k % 2));
+    for (int k = 0; k < kWorkers; ++k) {
+        const long long unit = ((long long)blockIdx.x * kWorkers + k) * line.share;
         if (unit >= total || unit < before || unit >= before + mine) continue;
         long long left = unit - before;
         for (int b = b0; b < b1; ++b) {
@@ -376,23 +372,22 @@ __device__ __forceinline__ void tree_plan(const TreeArgs& a, TreePlanScratch* sc
     __syncthreads();
 }
 
-// The line, and the walk over the share (without its tail), or over the share's
-// tail (tail 1, of a line that has them), of worker k of this CTA.
+// The line, and the walk over the share (without its tail) of worker k of this CTA.
 template <int kWorkers>
 __device__ __forceinline__ TreeLine tree_line(const TreeArgs& a, const TreePlanScratch* sc) {
     return TreeLine::of(a, sc->total, int(gridDim.x) * kWorkers);
 }
 template <int kWorkers>
-__device__ __forceinline__ TreeWalk tree_start(const TreeLine& line, const TreePlanScratch* sc, int k, int tail = 0) {
+__device__ __forceinline__ TreeWalk tree_start(const TreeLine& line, const TreePlanScratch* sc, int k) {
     TreeWalk w;
-    const auto& at = sc->at[2 * k + tail];
-    w.range = line.range(int(blockIdx.x) * kWorkers + k, tail);
+    const int worker = int(blockIdx.x) * kWorkers + k;
+    w.range = line.tail == 0 ? worker : 2 * worker;
     w.unit = w.begin = line.start(w.range);
-    w.b = at.b;
-    w.hh = at.hh;
-    w.tau = at.tau;
-    w.pos = at.pos;
-    w.r = at.r;
+    w.b = sc->at[k].b;
+    w.hh = sc->at[k].hh;
+    w.tau = sc->at[k].tau;
+    w.pos = sc->at[k].pos;
+    w.r = sc->at[k].r;
     w.end = w.b < 0 ? w.unit : line.end(w.range);
     return w;
 }
@@ -433,6 +428,14 @@ __device__ __forceinline__ long long tree_row(const TreeArgs& a, int row0, int n
     return (long long)(row0 + node) * a.num_qo_heads + kvh * a.group + h;
 }
 
+// Whether a descriptor of range `range` points into the partials of `ranges`
+// ranges and the rows of this call.
+__device__ __forceinline__ bool tree_split_fits(const TreeArgs& a, const TreeSplit& s, int range, int ranges) {
+    return s.r0 == range - 1 && unsigned(s.parts) <= unsigned(ranges - range + 1) && (s.slot0 | 1) == 2 * range - 1 &&
+           unsigned(s.hh) < unsigned(a.hs * a.num_kv_heads) && unsigned(s.nodes) <= unsigned(a.nps) && s.row0 >= 0 &&
+           s.row0 <= a.total_new - s.nodes;
+}
+
 constexpr int kMergeBlocks = 4;  // blocks per possible split
 
 // One warp per row of a split segment at a time: parts in the order of the
@@ -447,7 +450,9 @@ __global__ void __launch_bounds__(256) tree_merge_kernel(const TreeArgs a) {
     const int range = int(blockIdx.x / kMergeBlocks) + 1;
     const TreeLine line = *reinterpret_cast<const TreeLine*>(a.splits);
     if (line.start(range) >= line.total) return;
-    const TreeSplit s = a.splits[range];
+    TreeSplit s = a.splits[range];
+    // (as no split, not as another exit: that took 106 registers instead of 64, and 60 us of chains 2 us more)
+    if (!tree_split_fits(a, s, range, int(gridDim.x / kMergeBlocks) + 1)) s.parts = 0;
     if (s.parts == 0) return;
     for (int i = int(blockIdx.x % kMergeBlocks) * 8 + (threadIdx.x >> 5); i < s.nodes * a.hpt; i += 8 * kMergeBlocks) {
         const int per_tile = a.npt * a.hpt, tile = i / per_tile, row = (tile << a.tile_shift) + i - tile * per_tile;
@@ -539,10 +544,7 @@ __global__ void __launch_bounds__(128, CfgTreeCc<D, kCols>::kBlocksPerSm) tree_c
     tree_plan<1>(a, &plan);
     const TreeLine line = tree_line<1>(a, &plan);
     TreeWalk walk = tree_start<1>(line, &plan, 0);
-    if (tid == 0) {
-        walk.write_split(a, line);
-        if (line.tail != 0) tree_start<1>(line, &plan, 0, 1).write_split(a, line);
-    }
+    if (tid == 0) walk.write_split(a, line);
     launch_dependents();
     TreeWalk::Seg s;
     for (;;) {
@@ -557,6 +559,7 @@ __global__ void __launch_bounds__(128, CfgTreeCc<D, kCols>::kBlocksPerSm) tree_c
             __syncthreads();
             if (claimed < 0) break;
             walk.locate(a, line, claimed);
+            if (tid == 0) walk.write_split(a, line);
             continue;
         }
         __syncthreads();

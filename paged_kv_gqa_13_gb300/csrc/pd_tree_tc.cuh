@@ -361,10 +361,7 @@ __global__ void __launch_bounds__(CfgTree<D, kWide, kFp8>::kThreads, 1)
     TreeWalk walk;
     const bool walker = !soft && !idle && part == C::kPipes + C::kProducers;
     const TreeLine cuts = tree_line<C::kLines>(a, plan);
-    if (walker) {
-        walk = tree_start<C::kLines>(cuts, plan, line);
-        if (cuts.tail != 0 && lane == 0) tree_start<C::kLines>(cuts, plan, line, 1).write_split(a, cuts);
-    }
+    if (walker) walk = tree_start<C::kLines>(cuts, plan, line);
     tc_fence_before();
     __syncthreads();  // the walks have been read: copies may land
     tc_fence_after();
@@ -600,6 +597,7 @@ __global__ void __launch_bounds__(CfgTree<D, kWide, kFp8>::kThreads, 1)
                     break;
                 }
                 walk.locate(a, cuts, range);
+                if (lane == 0) walk.write_split(a, cuts);
             }
             if (lane == 0) {
                 if (more) {

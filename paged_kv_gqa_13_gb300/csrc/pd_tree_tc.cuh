@@ -50,10 +50,10 @@
 //
 // What bounds it. Few rows per request: the K and V bytes (32 chains of 4 over
 // 512 to 4096 tokens, bf16: 58 us, 65% of the DRAM cycles; 16 requests of head_dim
-// 256: 182 us, 77%). Many rows: S, P and O pass through tensor memory once per 64
+// 256: 181 us, 78%). Many rows: S, P and O pass through tensor memory once per 64
 // keys, so the softmax warps and the two products take turns at 48% tensor
-// cycles (64 nodes over 131,072 tokens, f16: 480 us against 317 for the bytes;
-// chunks of 1021 tokens: 418 us against 251 for the products). E4M3: converting
+// cycles (64 nodes over 131,072 tokens, f16: 466 to 490 us against 318 for the
+// bytes; chunks of 1021 tokens: 414 to 422 us against 245 for the products). E4M3: converting
 // and the padding of ragged row tiles (64 trees: 134 us, 39% tensor cycles).
 #pragma once
 

@@ -609,6 +609,109 @@ pd_status pd_paged_tree_commit(void* k_data, void* v_data, const int32_t* indice
                                int head_dim, int page_size, int num_total_pages, int num_indices, int elem_bytes,
                                void* workspace, size_t workspace_bytes, void* stream);
 
+/*
+ * Norms of q and k heads with the rotation in the same pass. An extension of
+ * this library, like the calls above. Each head x becomes
+ *
+ *   x / sqrt(mean(x^2) + eps) * w        (w: q_weight for q, k_weight for k)
+ *
+ * over its head_dim elements, and its leading rot_dim elements then turn as in
+ * pd_rope. Arithmetic is f32, rounded once to T.
+ *
+ * q_weight, k_weight: device T [head_dim], or NULL for ones. eps > 0.
+ *
+ * pd_norm_rope: q, q_out: device T [num_tokens] tokens of num_qo_heads heads;
+ *   k, k_out: the same of num_kv_heads heads (0 leaves k out: k, k_out may be
+ *   NULL). Strides between tokens in elements, as in pd_rope; q_out may be q,
+ *   and k_out k (the same stride); outputs must not otherwise overlap inputs
+ *   or each other. positions: device int32 [num_tokens] (may be NULL where
+ *   rot_dim is 0). head_dim even, up to 256. 16-byte accesses where every row
+ *   and stride allows it and rot_dim and head_dim are multiples of 16 (f32: 8);
+ *   single elements otherwise.
+ * pd_paged_norm_rope_append, _fp8: pd_paged_rope_append and its _fp8 form with
+ *   the norms in front. Arguments, results and errors as there, but that the q
+ *   rows of a request whose new_indptr entries are malformed are not written.
+ */
+pd_status pd_norm_rope(const void* q, const void* k, const void* q_weight, const void* k_weight, const int32_t* positions,
+                       const uint64_t* freqs, void* q_out, void* k_out, int num_tokens, int num_qo_heads,
+                       int num_kv_heads, int head_dim, int rot_dim, int64_t q_stride, int64_t k_stride,
+                       int64_t q_out_stride, int64_t k_out_stride, float eps, int layout, float rope_scale,
+                       pd_dtype dtype, void* stream);
+pd_status pd_paged_norm_rope_append(const void* q, const void* k_new, const void* v_new, const void* q_weight,
+                                    const void* k_weight, const int32_t* positions, const uint64_t* freqs, void* q_out,
+                                    void* k_data, void* v_data, const int32_t* indices, const int32_t* indptr,
+                                    const int32_t* last_page_len, const int32_t* new_indptr, int batch, int total_new,
+                                    int num_qo_heads, int num_kv_heads, int head_dim, int rot_dim, int page_size,
+                                    int num_total_pages, int num_indices, int64_t q_stride, int64_t k_stride,
+                                    int64_t v_stride, float eps, int layout, float rope_scale, pd_dtype dtype,
+                                    void* workspace, size_t workspace_bytes, void* stream);
+pd_status pd_paged_norm_rope_append_fp8(const void* q, const void* k_new, const void* v_new, const void* q_weight,
+                                        const void* k_weight, const int32_t* positions, const uint64_t* freqs,
+                                        void* q_out, const float* k_scale, const float* v_scale, void* k_data,
+                                        void* v_data, const int32_t* indices, const int32_t* indptr,
+                                        const int32_t* last_page_len, const int32_t* new_indptr, int batch,
+                                        int total_new, int num_qo_heads, int num_kv_heads, int head_dim, int rot_dim,
+                                        int page_size, int num_total_pages, int num_indices, int64_t q_stride,
+                                        int64_t k_stride, int64_t v_stride, float eps, int layout, float rope_scale,
+                                        pd_dtype dtype, void* workspace, size_t workspace_bytes, void* stream);
+
+/*
+ * Block-scaled pools. E4M3 codes in the layout of the E4M3 pools above, with
+ * one f32 scale for each block of block_tokens consecutive rows of a page and
+ * kv head instead of one per kv head:
+ *
+ *   k_data, v_data    [num_total_pages, num_kv_heads, page_size, head_dim]  codes
+ *   k_scale, v_scale  [num_total_pages, num_kv_heads, page_size / block_tokens]  f32
+ *   element value = E4M3 value of the code * the scale of its row's block
+ *
+ * block_tokens in [1, PD_MAX_BLOCK_TOKENS], a divisor of page_size: a scale for
+ * each token (1), or one per page and head (page_size). The scales follow the
+ * data: the append chooses them. They are not negative. Scales of rows past a
+ * request's end are not read.
+ *
+ * pd_paged_rope_append_fp8_blocks: pd_paged_rope_append (its arguments,
+ *   results, and errors, with the exception of the q rows that
+ *   pd_paged_norm_rope_append names) into such pools, with the norms of
+ *   pd_norm_rope in front where eps > 0; eps = 0 leaves them out (q_weight and
+ *   k_weight are then NULL). dtype PD_F16 or PD_BF16. Let a be the largest
+ *   finite magnitude, after norm and rotation in f32, of the new elements of a
+ *   block.
+ *    - A block whose first row is new gets the scale a / 448, at least 2^-126.
+ *    - A block that also holds older rows of the request keeps its scale s
+ *      (at least 2^-126) if a <= 464 s (what still rounds to the largest code).
+ *      Otherwise s doubles until that holds, and the codes of the older rows
+ *      are rounded again, by that power of two: exactly, but for subnormals.
+ *   A new element x is written as the code nearest to x * (1 / s), both
+ *   operations in f32, ties to even, saturating at +-448 (infinities too; NaN
+ *   stays NaN). Rows past the request's end keep their codes; a page may be
+ *   shared with another request where no new row falls into it.
+ *
+ * pd_paged_read_fp8_blocks: the values of tokens first[b] .. first[b] + n_b - 1
+ *   of request b, rounded once to T, into rows out_indptr[b] .. of k_out and
+ *   v_out (device T [total, num_kv_heads, head_dim], 16-byte aligned), n_b =
+ *   out_indptr[b + 1] - out_indptr[b] (device int32 [batch + 1], increasing from
+ *   0 to total; n_b may be 0). first: device int32 [batch], or NULL for 0.
+ *   dtype: any T. Tokens outside the request, or a malformed out_indptr:
+ *   PD_FLAG_BAD_NEW_ROWS, and that request's rows are not written. Rows on a
+ *   bad page are zero (PD_FLAG_BAD_PAGE_ID).
+ */
+#define PD_MAX_BLOCK_TOKENS 64
+pd_status pd_paged_rope_append_fp8_blocks(const void* q, const void* k_new, const void* v_new, const void* q_weight,
+                                          const void* k_weight, const int32_t* positions, const uint64_t* freqs,
+                                          void* q_out, float* k_scale, float* v_scale, void* k_data, void* v_data,
+                                          const int32_t* indices, const int32_t* indptr, const int32_t* last_page_len,
+                                          const int32_t* new_indptr, int batch, int total_new, int num_qo_heads,
+                                          int num_kv_heads, int head_dim, int rot_dim, int page_size,
+                                          int num_total_pages, int num_indices, int block_tokens, int64_t q_stride,
+                                          int64_t k_stride, int64_t v_stride, float eps, int layout, float rope_scale,
+                                          pd_dtype dtype, void* workspace, size_t workspace_bytes, void* stream);
+pd_status pd_paged_read_fp8_blocks(const void* k_data, const void* v_data, const float* k_scale, const float* v_scale,
+                                   const int32_t* indices, const int32_t* indptr, const int32_t* last_page_len,
+                                   const int32_t* out_indptr, const int32_t* first, void* k_out, void* v_out, int batch,
+                                   int total, int num_kv_heads, int head_dim, int page_size, int num_total_pages,
+                                   int num_indices, int block_tokens, pd_dtype dtype, void* workspace,
+                                   size_t workspace_bytes, void* stream);
+
 /* Message for the last error status returned on this host thread ("" if none). */
 const char* pd_last_error_string(void);
 

@@ -33,6 +33,7 @@ PD_FLAG_BAD_NEW_ROWS, PD_FLAG_BAD_PATH = 16, 32
 PD_WORKSPACE_HEADER_BYTES = 256
 PD_ROPE_HALF, PD_ROPE_PAIRS = 0, 1
 PD_ROPE_PLAIN, PD_ROPE_LINEAR, PD_ROPE_BASE, PD_ROPE_BANDED, PD_ROPE_YARN = 0, 1, 2, 3, 4
+PD_MAX_BLOCK_TOKENS = 64
 PD_KERNEL_NONE, PD_KERNEL_CUDA_CORES, PD_KERNEL_TENSOR_CORES, PD_KERNEL_FP8_TENSOR_CORES = 0, 1, 2, 3
 PD_KERNEL_FP8_TCGEN05 = 4
 
@@ -81,6 +82,11 @@ _SIGS = {
     "pd_paged_tree_decode": (_I, [_P] * 10 + [_I] * 9 + [_F, _I, _P, _S, _P]),
     "pd_paged_tree_decode_fp8": (_I, [_P] * 12 + [_I] * 9 + [_F, _I, _P, _S, _P]),
     "pd_paged_tree_commit": (_I, [_P] * 8 + [_I] * 9 + [_P, _S, _P]),
+    "pd_norm_rope": (_I, [_P] * 8 + [_I] * 5 + [_L] * 4 + [_F, _I, _F, _I, _P]),
+    "pd_paged_norm_rope_append": (_I, [_P] * 14 + [_I] * 9 + [_L] * 3 + [_F, _I, _F, _I, _P, _S, _P]),
+    "pd_paged_norm_rope_append_fp8": (_I, [_P] * 16 + [_I] * 9 + [_L] * 3 + [_F, _I, _F, _I, _P, _S, _P]),
+    "pd_paged_rope_append_fp8_blocks": (_I, [_P] * 16 + [_I] * 10 + [_L] * 3 + [_F, _I, _F, _I, _P, _S, _P]),
+    "pd_paged_read_fp8_blocks": (_I, [_P] * 11 + [_I] * 9 + [_P, _S, _P]),
     "pd_last_error_string": (ctypes.c_char_p, []),
     "pd_version": (_I, []),
 }
@@ -583,3 +589,128 @@ def pd_paged_tree_commit(k_data, v_data, indices, indptr, last_page_len, new_ind
         _ptr(k_data), _ptr(v_data), *table, _int32(path), _int32(path_len), batch,
         0x7fffffff if total_new is None else total_new, path.shape[1], num_kv_heads, head_dim, page_size, num_total_pages,
         entries, k_data.element_size(), _ptr(workspace), workspace.numel(), _stream_for(k_data, stream)))
+
+
+# --- norms of q and k heads with the rotation in the same pass -----------------------------------------------------
+
+def _weights(q_weight, k_weight, head_dim, dtype):
+    for w in (q_weight, k_weight):
+        if w is not None and (w.numel() != head_dim or w.dtype != dtype):
+            _bad("q_weight and k_weight hold one element for each of head_dim, of the rows' type")
+    return _ptr(q_weight), _ptr(k_weight)
+
+
+def pd_norm_rope(q, k, q_weight, k_weight, positions, freqs, q_out, k_out, eps: float = 1e-6,
+                 layout: int = PD_ROPE_HALF, rope_scale: float = 1.0, stream=None) -> None:
+    """Each head over the root of its mean square (+ eps), times its weight, then rotated as by pd_rope.
+
+    q, q_out [tokens, Hq, D], k, k_out [tokens, Hk, D] (tokens may be strided; q_out may be q, k_out k; k and k_out may
+    be None); q_weight, k_weight [D] or None; positions int32 [tokens]; freqs None leaves the rotation out.
+    """
+    tokens, hq, head_dim = q.shape
+    dtype, hk, kp, ks, kop, kos = q.dtype, 0, None, 0, None, 0
+    if q_out.shape != q.shape or q_out.dtype != dtype:
+        _bad("q_out is shaped and typed as q")
+    if k is not None:
+        hk = k.shape[1]
+        if k.shape[0] != tokens or k.shape[2] != head_dim or k_out.shape != k.shape or k.dtype != dtype or k_out.dtype != dtype:
+            _bad("k holds one row for each token, typed as q, and k_out is shaped and typed as k")
+        kp, ks, kop, kos = k.data_ptr(), _token_stride(k, hk, head_dim), k_out.data_ptr(), _token_stride(k_out, hk, head_dim)
+    if positions is not None and positions.shape[0] != tokens:
+        _bad("there is one position for each token")
+    fp, rot = _freqs(freqs)
+    _check(_lib.pd_norm_rope(q.data_ptr(), kp, *_weights(q_weight, k_weight, head_dim, dtype), _int32(positions), fp,
+                             q_out.data_ptr(), kop, tokens, hq, hk, head_dim, rot, _token_stride(q, hq, head_dim), ks,
+                             _token_stride(q_out, hq, head_dim), kos, eps, layout, rope_scale, _code_of(dtype),
+                             _stream_for(q, stream)))
+
+
+def _norm_append(fn, scales, blocks, q, k_new, v_new, q_weight, k_weight, positions, freqs, q_out, k_data, v_data, indices,
+                 indptr, last_page_len, new_indptr, workspace, eps, layout, rope_scale, stream):
+    total_new, num_kv_heads, head_dim = k_new.shape
+    num_total_pages, hk, page_size, d = _pools(k_data, v_data)
+    dtype = k_new.dtype
+    if hk != num_kv_heads or d != head_dim or v_new.shape != k_new.shape or v_new.dtype != dtype:
+        _bad("k_new, v_new and the pools differ in heads, head_dim or type")
+    qp, qs, op, num_qo_heads = None, 0, None, 0
+    if q is not None:
+        num_qo_heads = q.shape[1]
+        if q.shape[0] != total_new or q.shape[2] != head_dim or q_out.shape != q.shape or q.dtype != dtype or q_out.dtype != dtype:
+            _bad("q holds one row for each new token, typed as k_new, and q_out is shaped and typed as q")
+        qp, qs, op = q.data_ptr(), _token_stride(q, num_qo_heads, head_dim), _ptr(q_out)
+    if positions is not None and positions.shape[0] != total_new:
+        _bad("there is one position for each new token")
+    fp, rot = _freqs(freqs)
+    table, batch, entries = _table(indices, indptr, last_page_len, new_indptr)
+    _check(fn(qp, k_new.data_ptr(), v_new.data_ptr(), *_weights(q_weight, k_weight, head_dim, dtype), _int32(positions), fp, op,
+              *scales, _ptr(k_data), _ptr(v_data), *table, batch, total_new, num_qo_heads, num_kv_heads, head_dim, rot,
+              page_size, num_total_pages, entries, *blocks, qs, _token_stride(k_new, num_kv_heads, head_dim),
+              _token_stride(v_new, num_kv_heads, head_dim), eps, layout, rope_scale, _code_of(dtype), _ptr(workspace),
+              workspace.numel(), _stream_for(k_new, stream)))
+
+
+def pd_paged_norm_rope_append(q, k_new, v_new, q_weight, k_weight, positions, freqs, q_out, k_data, v_data, indices,
+                              indptr, last_page_len, new_indptr, workspace, eps: float = 1e-6,
+                              layout: int = PD_ROPE_HALF, rope_scale: float = 1.0, stream=None) -> None:
+    """pd_paged_rope_append with the norms of pd_norm_rope in front (q_weight, k_weight [D] or None)."""
+    if k_data.dtype != k_new.dtype:
+        _bad("the pools have the type of k_new")
+    _norm_append(_lib.pd_paged_norm_rope_append, (), (), q, k_new, v_new, q_weight, k_weight, positions, freqs, q_out, k_data,
+                 v_data, indices, indptr, last_page_len, new_indptr, workspace, eps, layout, rope_scale, stream)
+
+
+def pd_paged_norm_rope_append_fp8(q, k_new, v_new, q_weight, k_weight, positions, freqs, q_out, k_scale, v_scale, k_data,
+                                  v_data, indices, indptr, last_page_len, new_indptr, workspace, eps: float = 1e-6,
+                                  layout: int = PD_ROPE_HALF, rope_scale: float = 1.0, stream=None) -> None:
+    """pd_paged_norm_rope_append into E4M3 pools (k_data, v_data uint8; scales f32 [Hk])."""
+    _norm_append(_lib.pd_paged_norm_rope_append_fp8, _scales(k_scale, v_scale, k_data), (), q, k_new, v_new, q_weight,
+                 k_weight, positions, freqs, q_out, k_data, v_data, indices, indptr, last_page_len, new_indptr, workspace, eps,
+                 layout, rope_scale, stream)
+
+
+# --- block-scaled pools: k_data, v_data uint8 E4M3 [pages, Hk, page_size, D]; k_scale, v_scale f32
+# [pages, Hk, page_size / block_tokens], a scale for each block of rows of a page and kv head ---------------------------
+
+def _block_scales(k_scale, v_scale, k_data):
+    """(pointers, block_tokens)"""
+    pages, hk, page_size, _ = k_data.shape
+    if k_data.element_size() != 1:
+        _bad("E4M3 pools hold one byte for each element")
+    shape = k_scale.shape
+    if k_scale.dtype != v_scale.dtype or shape != v_scale.shape or k_scale.element_size() != 4 or not k_scale.is_floating_point():
+        _bad("k_scale and v_scale are float32 of one shape")
+    if len(shape) != 3 or shape[0] != pages or shape[1] != hk or shape[2] == 0 or page_size % shape[2]:
+        _bad("k_scale and v_scale are [pages, Hk, page_size / block_tokens]")
+    return (_ptr(k_scale), _ptr(v_scale)), page_size // shape[2]
+
+
+def pd_paged_rope_append_fp8_blocks(q, k_new, v_new, positions, freqs, q_out, k_scale, v_scale, k_data, v_data, indices,
+                                    indptr, last_page_len, new_indptr, workspace, q_weight=None, k_weight=None,
+                                    eps: float = 0.0, layout: int = PD_ROPE_HALF, rope_scale: float = 1.0,
+                                    stream=None) -> None:
+    """pd_paged_rope_append into block-scaled pools, whose scales it writes; eps > 0: with the norms of pd_norm_rope in
+    front (q_weight, k_weight [D] or None)."""
+    _pools(k_data, v_data)
+    scales, block = _block_scales(k_scale, v_scale, k_data)
+    _norm_append(_lib.pd_paged_rope_append_fp8_blocks, scales, (block,), q, k_new, v_new, q_weight, k_weight, positions, freqs,
+                 q_out, k_data, v_data, indices, indptr, last_page_len, new_indptr, workspace, eps, layout, rope_scale, stream)
+
+
+def pd_paged_read_fp8_blocks(k_data, v_data, k_scale, v_scale, indices, indptr, last_page_len, out_indptr, first, k_out,
+                             v_out, workspace, stream=None) -> None:
+    """Tokens first[b] .. of each request as rows out_indptr[b] .. out_indptr[b + 1] of k_out, v_out [total, Hk, D].
+
+    out_indptr int32 [batch + 1]; first int32 [batch] or None (token 0).
+    """
+    num_total_pages, num_kv_heads, page_size, head_dim = _pools(k_data, v_data)
+    scales, block = _block_scales(k_scale, v_scale, k_data)
+    total = k_out.shape[0]
+    if k_out.shape != v_out.shape or k_out.dtype != v_out.dtype or k_out.shape[1:] != (num_kv_heads, head_dim):
+        _bad("k_out and v_out are [total, Hk, D] of one type, the pools' Hk and D")
+    table, batch, entries = _table(indices, indptr, last_page_len, out_indptr)
+    if first is not None and first.shape[0] != batch:
+        _bad("first holds one token for each request")
+    _check(_lib.pd_paged_read_fp8_blocks(
+        _ptr(k_data), _ptr(v_data), *scales, *table, _int32(first), _ptr(k_out), _ptr(v_out), batch, total, num_kv_heads,
+        head_dim, page_size, num_total_pages, entries, block, _code_of(k_out.dtype), _ptr(workspace), workspace.numel(),
+        _stream_for(k_data, stream)))

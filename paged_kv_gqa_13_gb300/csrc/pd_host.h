@@ -19,6 +19,10 @@ pd_status cuda_fail(cudaError_t e, const char* what);
 pd_status check_workspace(void* ws, size_t have, size_t need);
 pd_status sm_count(int* sms);
 pd_status allow_smem(const void* fn, int bytes);
+// A block of block_tokens rows divides a page (pd_norm_rope.cu).
+pd_status check_block(int block_tokens, int page_size);
+// Checks of a rotation's arguments, shared by the calls that rotate (pd_rope.cu).
+pd_status check_rotation(int tokens, int head_dim, int rot_dim, int layout, float rope_scale, const uint64_t* freqs, pd_dtype dt);
 // pd_test_inject_wait_timeout's extra bytes (0: off).
 int test_extra_tx();
 // The driver's tensor-map encoder; null when the driver does not offer it.

@@ -21,8 +21,8 @@
 #include <cmath>
 #include <type_traits>
 
-#include "pd_device.cuh"
 #include "pd_host.h"
+#include "pd_rows.cuh"
 
 namespace pd {
 namespace {
@@ -60,63 +60,8 @@ struct RopeArgs {
     FastDiv by_rest, by_chunks;  // by the accesses of a head's elements past rot_dim, and of a whole head
 };
 
-// V elements of a row: one 16-byte access, or one element (V = 1).
-template <typename T, int V>
-using Raw = typename std::conditional<V == 1, T, uint4>::type;
-
-template <typename T, int V>
-__device__ __forceinline__ void widen(const Raw<T, V>& w, float (&f)[V]) {
-    if constexpr (V == 1)
-        f[0] = float(w);
-    else
-        Elt<T>::to_f32(w, f);
-}
-
-template <typename T, int V>
-__device__ __forceinline__ void store_elems(T* p, const float (&f)[V]) {
-    if constexpr (V == 1)
-        *p = T(f[0]);
-    else
-        *reinterpret_cast<uint4*>(p) = Elt<T>::from_f32(f);
-}
-
-// The E4M3 codes of f[i] / scale: the division in f32 (IEEE), then rounded to
-// the nearest code, ties to even, saturating at +-448 (NaN stays NaN).
-template <int V>
-__device__ __forceinline__ void store_codes(uint8_t* p, const float (&f)[V], float scale) {
-    if constexpr (V == 1) {
-        *p = __nv_cvt_float_to_fp8(__fdiv_rn(f[0], scale), __NV_SATFINITE, __NV_E4M3);
-    } else {
-        uint32_t w[V / 4] = {};
-#pragma unroll
-        for (int i = 0; i < V; i += 2) {
-            const float2 x = make_float2(__fdiv_rn(f[i], scale), __fdiv_rn(f[i + 1], scale));
-            w[i / 4] |= uint32_t(__nv_cvt_float2_to_fp8x2(x, __NV_SATFINITE, __NV_E4M3)) << (8 * (i % 4));
-        }
-        if constexpr (V == 8)
-            *reinterpret_cast<uint2*>(p) = make_uint2(w[0], w[1]);
-        else
-            *reinterpret_cast<uint32_t*>(p) = w[0];
-    }
-}
-
 // Pools that a call writes: none, of q's type, or of E4M3 codes.
 constexpr int kNoPool = 0, kPlainPool = 1, kCodePool = 2;
-
-// The request b whose range [new_indptr[b], new_indptr[b + 1]) holds token t,
-// by a 32-way search of the whole warp (one round for up to 32 requests). On a
-// malformed table it still ends, with some b in [0, batch).
-__device__ __forceinline__ int request_of(const int32_t* new_indptr, int batch, int t, int lane) {
-    int lo = 0, hi = batch;
-    while (hi - lo > 1) {
-        const int step = (hi - lo + 31) / 32;
-        const long long at = lo + (long long)(lane + 1) * step;
-        const bool below = at < hi && __ldg(new_indptr + at) <= t;
-        lo += __popc(__ballot_sync(kFull, below)) * step;
-        hi = min(hi, lo + step);
-    }
-    return lo;
-}
 
 // One warp per (token, slice of the token's hq + 2 hk heads: q, k, then v).
 // Unit u of a rotated head is its elements u V .. and rot/2 + u V .., V of
@@ -484,21 +429,6 @@ __global__ void __launch_bounds__(128) commit_kernel(const CommitArgs a) {
     }
 }
 
-// Checks shared by pd_rope and the appends.
-pd_status check_rotation(int tokens, int head_dim, int rot_dim, int layout, float rope_scale, const uint64_t* freqs,
-                         pd_dtype dt) {
-    if (!host::known_dtype(dt)) return host::fail(PD_ERR_UNSUPPORTED, "dtype must be PD_F32, PD_F16 or PD_BF16");
-    if (tokens < 0) return host::fail(PD_ERR_INVALID, "the number of tokens must not be negative");
-    if (rot_dim < 0 || rot_dim % 2 != 0 || rot_dim > head_dim)
-        return host::fail(PD_ERR_INVALID, "rot_dim must be even and in [0, head_dim] (got %d of %d)", rot_dim, head_dim);
-    if (layout != PD_ROPE_HALF && layout != PD_ROPE_PAIRS)
-        return host::fail(PD_ERR_INVALID, "layout must be PD_ROPE_HALF or PD_ROPE_PAIRS");
-    if (!std::isfinite(rope_scale)) return host::fail(PD_ERR_INVALID, "rope_scale must be finite");
-    if (rot_dim > 0 && !freqs) return host::fail(PD_ERR_INVALID, "null pointer argument");
-    if (!host::aligned(freqs, 8)) return host::fail(PD_ERR_UNSUPPORTED, "freqs must be 8-byte aligned");
-    return PD_OK;
-}
-
 pd_status append_impl(const void* q, const void* k_new, const void* v_new, const int32_t* positions,
                       const uint64_t* freqs, void* q_out, const float* k_scale, const float* v_scale, void* k_data,
                       void* v_data, const int32_t* indices, const int32_t* indptr, const int32_t* last_page_len,
@@ -507,7 +437,7 @@ pd_status append_impl(const void* q, const void* k_new, const void* v_new, const
                       long long v_stride, int layout, float rope_scale, pd_dtype dt, void* workspace,
                       size_t workspace_bytes, void* stream, bool fp8) {
     if (D != 64 && D != 128 && D != 256) return host::fail(PD_ERR_UNSUPPORTED, "head_dim must be 64, 128 or 256 (got %d)", D);
-    pd_status st = check_rotation(total_new, D, rot_dim, layout, rope_scale, freqs, dt);
+    pd_status st = host::check_rotation(total_new, D, rot_dim, layout, rope_scale, freqs, dt);
     if (st != PD_OK) return st;
     if (batch <= 0 || Hk <= 0 || page_size <= 0 || num_total_pages <= 0)
         return host::fail(PD_ERR_INVALID, "batch, num_kv_heads, page_size and num_total_pages must be positive");
@@ -568,6 +498,26 @@ pd_status append_impl(const void* q, const void* k_new, const void* v_new, const
 }  // namespace
 }  // namespace pd
 
+namespace pd {
+namespace host {
+
+pd_status check_rotation(int tokens, int head_dim, int rot_dim, int layout, float rope_scale, const uint64_t* freqs,
+                         pd_dtype dt) {
+    if (!known_dtype(dt)) return fail(PD_ERR_UNSUPPORTED, "dtype must be PD_F32, PD_F16 or PD_BF16");
+    if (tokens < 0) return fail(PD_ERR_INVALID, "the number of tokens must not be negative");
+    if (rot_dim < 0 || rot_dim % 2 != 0 || rot_dim > head_dim)
+        return fail(PD_ERR_INVALID, "rot_dim must be even and in [0, head_dim] (got %d of %d)", rot_dim, head_dim);
+    if (layout != PD_ROPE_HALF && layout != PD_ROPE_PAIRS)
+        return fail(PD_ERR_INVALID, "layout must be PD_ROPE_HALF or PD_ROPE_PAIRS");
+    if (!std::isfinite(rope_scale)) return fail(PD_ERR_INVALID, "rope_scale must be finite");
+    if (rot_dim > 0 && !freqs) return fail(PD_ERR_INVALID, "null pointer argument");
+    if (!aligned(freqs, 8)) return fail(PD_ERR_UNSUPPORTED, "freqs must be 8-byte aligned");
+    return PD_OK;
+}
+
+}  // namespace host
+}  // namespace pd
+
 using namespace pd;
 
 extern "C" {
@@ -617,7 +567,7 @@ pd_status pd_rope(const void* x, const int32_t* positions, const uint64_t* freqs
                   float rope_scale, pd_dtype dtype, void* stream) {
     if (num_heads <= 0 || num_heads > (1 << 20) || head_dim <= 0 || head_dim > 4096)
         return host::fail(PD_ERR_INVALID, "num_heads must be in [1, 2^20] and head_dim in [1, 4096]");
-    const pd_status st = check_rotation(num_tokens, head_dim, rot_dim, layout, rope_scale, freqs, dtype);
+    const pd_status st = host::check_rotation(num_tokens, head_dim, rot_dim, layout, rope_scale, freqs, dtype);
     if (st != PD_OK) return st;
     if (num_tokens > 0 && (!x || !out || !positions)) return host::fail(PD_ERR_INVALID, "null pointer argument");
     if (x_stride < (long long)num_heads * head_dim || out_stride < (long long)num_heads * head_dim)

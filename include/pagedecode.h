@@ -666,8 +666,8 @@ pd_status pd_paged_norm_rope_append_fp8(const void* q, const void* k_new, const 
  *
  * block_tokens in [1, PD_MAX_BLOCK_TOKENS], a divisor of page_size: a scale for
  * each token (1), or one per page and head (page_size). The scales follow the
- * data: the append chooses them. They are not negative. Scales of rows past a
- * request's end are not read.
+ * data: the append chooses them. They are finite and not negative. Scales of rows
+ * past a request's end are not read.
  *
  * pd_paged_rope_append_fp8_blocks: pd_paged_rope_append (its arguments,
  *   results, and errors, with the exception of the q rows that
@@ -694,6 +694,15 @@ pd_status pd_paged_norm_rope_append_fp8(const void* q, const void* k_new, const 
  *   dtype: any T. Tokens outside the request, or a malformed out_indptr:
  *   PD_FLAG_BAD_NEW_ROWS, and that request's rows are not written. Rows on a
  *   bad page are zero (PD_FLAG_BAD_PAGE_ID).
+ *
+ * pd_paged_decode_fp8_blocks: pd_paged_decode over such pools: one query row
+ *   per request, which attends all of its cached tokens. An empty request gets
+ *   o = 0, lse = -infinity.
+ * pd_paged_tree_decode_fp8_blocks: pd_paged_tree_decode over such pools.
+ *   Both: dtype (PD_F16 or PD_BF16) is the type of q and o; workspace: at least
+ *   pd_paged_tree_decode_fp8_blocks_workspace_bytes(...) bytes, which any other
+ *   call on the same stream may share. The other arguments, results and errors
+ *   are those of pd_paged_decode and pd_paged_tree_decode.
  */
 #define PD_MAX_BLOCK_TOKENS 64
 pd_status pd_paged_rope_append_fp8_blocks(const void* q, const void* k_new, const void* v_new, const void* q_weight,
@@ -711,6 +720,21 @@ pd_status pd_paged_read_fp8_blocks(const void* k_data, const void* v_data, const
                                    int total, int num_kv_heads, int head_dim, int page_size, int num_total_pages,
                                    int num_indices, int block_tokens, pd_dtype dtype, void* workspace,
                                    size_t workspace_bytes, void* stream);
+size_t pd_paged_tree_decode_fp8_blocks_workspace_bytes(int num_qo_heads, int num_kv_heads, int head_dim, pd_dtype dtype);
+pd_status pd_paged_decode_fp8_blocks(const void* q, const void* k_data, const void* v_data, const float* k_scale,
+                                     const float* v_scale, const int32_t* indices, const int32_t* indptr,
+                                     const int32_t* last_page_len, void* o, float* lse, int batch, int num_qo_heads,
+                                     int num_kv_heads, int head_dim, int page_size, int num_total_pages,
+                                     int num_indices, int block_tokens, float sm_scale, pd_dtype dtype, void* workspace,
+                                     size_t workspace_bytes, void* stream);
+pd_status pd_paged_tree_decode_fp8_blocks(const void* q, const void* k_data, const void* v_data, const float* k_scale,
+                                          const float* v_scale, const int32_t* indices, const int32_t* indptr,
+                                          const int32_t* last_page_len, const int32_t* new_indptr,
+                                          const uint32_t* tree_mask, void* o, float* lse, int batch, int total_new,
+                                          int mask_words, int num_qo_heads, int num_kv_heads, int head_dim,
+                                          int page_size, int num_total_pages, int num_indices, int block_tokens,
+                                          float sm_scale, pd_dtype dtype, void* workspace, size_t workspace_bytes,
+                                          void* stream);
 
 /* Message for the last error status returned on this host thread ("" if none). */
 const char* pd_last_error_string(void);

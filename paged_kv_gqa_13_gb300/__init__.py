@@ -87,6 +87,9 @@ _SIGS = {
     "pd_paged_norm_rope_append_fp8": (_I, [_P] * 16 + [_I] * 9 + [_L] * 3 + [_F, _I, _F, _I, _P, _S, _P]),
     "pd_paged_rope_append_fp8_blocks": (_I, [_P] * 16 + [_I] * 10 + [_L] * 3 + [_F, _I, _F, _I, _P, _S, _P]),
     "pd_paged_read_fp8_blocks": (_I, [_P] * 11 + [_I] * 9 + [_P, _S, _P]),
+    "pd_paged_tree_decode_fp8_blocks_workspace_bytes": (_S, [_I, _I, _I, _I]),
+    "pd_paged_decode_fp8_blocks": (_I, [_P] * 10 + [_I] * 8 + [_F, _I, _P, _S, _P]),
+    "pd_paged_tree_decode_fp8_blocks": (_I, [_P] * 12 + [_I] * 10 + [_F, _I, _P, _S, _P]),
     "pd_last_error_string": (ctypes.c_char_p, []),
     "pd_version": (_I, []),
 }
@@ -714,3 +717,53 @@ def pd_paged_read_fp8_blocks(k_data, v_data, k_scale, v_scale, indices, indptr, 
         _ptr(k_data), _ptr(v_data), *scales, *table, _int32(first), _ptr(k_out), _ptr(v_out), batch, total, num_kv_heads,
         head_dim, page_size, num_total_pages, entries, block, _code_of(k_out.dtype), _ptr(workspace), workspace.numel(),
         _stream_for(k_data, stream)))
+
+
+def pd_paged_tree_decode_fp8_blocks_workspace_bytes(num_qo_heads: int, num_kv_heads: int, head_dim: int, dtype: int) -> int:
+    """Of pd_paged_decode_fp8_blocks and pd_paged_tree_decode_fp8_blocks."""
+    n = _lib.pd_paged_tree_decode_fp8_blocks_workspace_bytes(num_qo_heads, num_kv_heads, head_dim, dtype)
+    if n == 0:
+        raise PagedecodeError(PD_ERR_INVALID, pd_last_error_string())
+    return n
+
+
+def _attention(q, o, lse, k_data, v_data):
+    """Shapes and types of an attention over pools: (num_total_pages, num_kv_heads, page_size)."""
+    num_total_pages, num_kv_heads, page_size, d = _pools(k_data, v_data)
+    if d != q.shape[2] or o.shape != q.shape or o.dtype != q.dtype or lse.shape != q.shape[:2] or lse.element_size() != 4 \
+            or not lse.is_floating_point():
+        _bad("q and o [rows, Hq, D] of one type, lse float32 [rows, Hq], the pools' D")
+    return num_total_pages, num_kv_heads, page_size
+
+
+def pd_paged_decode_fp8_blocks(q, k_data, v_data, k_scale, v_scale, indices, indptr, last_page_len, o, lse,
+                               sm_scale: float, workspace, stream=None) -> None:
+    """pd_paged_decode over block-scaled pools: q, o [batch, Hq, D] f16/bf16; lse [batch, Hq] f32."""
+    rows, num_qo_heads, head_dim = q.shape
+    num_total_pages, num_kv_heads, page_size = _attention(q, o, lse, k_data, v_data)
+    scales, block = _block_scales(k_scale, v_scale, k_data)
+    batch, entries = last_page_len.shape[0], indices.shape[0]
+    if rows != batch or indptr.shape[0] != batch + 1:
+        _bad("q holds one row for each request, indptr one entry more than last_page_len")
+    _check(_lib.pd_paged_decode_fp8_blocks(
+        _ptr(q), _ptr(k_data), _ptr(v_data), *scales, _int32(indices) if entries else None, _int32(indptr),
+        _int32(last_page_len), _ptr(o), _ptr(lse), batch, num_qo_heads, num_kv_heads, head_dim, page_size, num_total_pages,
+        entries, block, sm_scale, _code_of(q.dtype), _ptr(workspace), workspace.numel(), _stream_for(q, stream)))
+
+
+def pd_paged_tree_decode_fp8_blocks(q, k_data, v_data, k_scale, v_scale, indices, indptr, last_page_len, new_indptr,
+                                    tree_mask, o, lse, sm_scale: float, workspace, stream=None) -> None:
+    """pd_paged_tree_decode over block-scaled pools: q, o [total_new, Hq, D] f16/bf16; lse [total_new, Hq] f32."""
+    total_new, num_qo_heads, head_dim = q.shape
+    num_total_pages, num_kv_heads, page_size = _attention(q, o, lse, k_data, v_data)
+    scales, block = _block_scales(k_scale, v_scale, k_data)
+    words = 0
+    if tree_mask is not None:
+        if tree_mask.dim() != 2 or tree_mask.shape[0] != total_new or (total_new and tree_mask.shape[1] == 0):
+            _bad("tree_mask is [total_new, words] of 32 bits each, one word at least")
+        words = tree_mask.shape[1]
+    table, batch, entries = _table(indices, indptr, last_page_len, new_indptr)
+    _check(_lib.pd_paged_tree_decode_fp8_blocks(
+        _ptr(q), _ptr(k_data), _ptr(v_data), *scales, *table, _int32(tree_mask), _ptr(o), _ptr(lse), batch, total_new, words,
+        num_qo_heads, num_kv_heads, head_dim, page_size, num_total_pages, entries, block, sm_scale, _code_of(q.dtype),
+        _ptr(workspace), workspace.numel(), _stream_for(q, stream)))

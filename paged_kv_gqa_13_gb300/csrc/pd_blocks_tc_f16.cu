@@ -1,0 +1,6 @@
+// Attention over block-scaled E4M3 pools, f16 q and o.
+#include "pd_blocks_tc.cuh"
+
+namespace pd {
+bool blocks_tc_f16(int head_dim, int rows, TreeKernels* k) { return blocks_tc_by_rows<__half>(head_dim, rows, k); }
+}  // namespace pd

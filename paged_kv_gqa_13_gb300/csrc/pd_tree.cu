@@ -59,12 +59,17 @@ bool pick(pd_dtype dt, bool fp8, int D, int group, Rows rows, TreeKernels* k) {
     return false;
 }
 
-pd_status encode(CUtensorMap* map, CUtensorMapDataType ty, int rank, const void* base, const cuuint64_t* dims,
-                 const cuuint64_t* strides, const cuuint32_t* box) {
+// Block-scaled pools: the kernel by the rows of a request on average (its row tiles hold 16, 32 or 64).
+bool pick_blocks(pd_dtype dt, int D, long long rows, TreeKernels* k) {
+    const int most = rows > 64 ? 64 : int(rows);
+    return dt == PD_F16 ? blocks_tc_f16(D, most, k) : blocks_tc_bf16(D, most, k);
+}
+
+pd_status encode(CUtensorMap* map, CUtensorMapDataType ty, CUtensorMapSwizzle swizzle, int rank, const void* base,
+                 const cuuint64_t* dims, const cuuint64_t* strides, const cuuint32_t* box) {
     PFN_cuTensorMapEncodeTiled_v12000 enc = host::tensor_map_encoder();
     if (enc == nullptr) return host::fail(PD_ERR_CUDA, "cuTensorMapEncodeTiled is not available from the driver");
     const cuuint32_t ones[4] = {1, 1, 1, 1};
-    const CUtensorMapSwizzle swizzle = ty == CU_TENSOR_MAP_DATA_TYPE_UINT8 ? CU_TENSOR_MAP_SWIZZLE_NONE : CU_TENSOR_MAP_SWIZZLE_128B;
     const CUresult r = enc(map, ty, cuuint32_t(rank), const_cast<void*>(base), dims, strides, box, ones,
                            CU_TENSOR_MAP_INTERLEAVE_NONE, swizzle, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
                            CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
@@ -72,20 +77,25 @@ pd_status encode(CUtensorMap* map, CUtensorMapDataType ty, int rank, const void*
 }
 
 // Boxes: of q {64 columns, heads of a tile, nodes of a row tile}; of K and V {64
-// columns, rows of a slot}, of codes {head_dim columns, rows of a slot}.
-pd_status make_maps(const TreeArgs& a, pd_dtype dt, bool fp8, int D, CUtensorMap* q, CUtensorMap* k, CUtensorMap* v) {
+// columns, rows of a slot}, of codes {head_dim columns, rows of a slot}, of codes
+// that are operands as they lie {up to 128 columns, rows of a slot}, swizzled (q is then read without a map).
+pd_status make_maps(const TreeArgs& a, pd_dtype dt, bool fp8, bool operands, int D, CUtensorMap* q, CUtensorMap* k, CUtensorMap* v) {
     const CUtensorMapDataType qt = dt == PD_BF16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16;
     const CUtensorMapDataType kt = fp8 ? CU_TENSOR_MAP_DATA_TYPE_UINT8 : qt;
     const cuuint64_t d = cuuint64_t(D), ps = cuuint64_t(a.page_size), hk = cuuint64_t(a.num_kv_heads),
                      hq = cuuint64_t(a.num_qo_heads), e = fp8 ? 1 : 2;
     const cuuint64_t kd[4] = {d, ps, hk, cuuint64_t(a.num_total_pages)}, ks[3] = {d * e, ps * d * e, hk * ps * d * e};
-    const cuuint32_t kb[4] = {fp8 ? cuuint32_t(D) : 64u, 1u << a.slot_shift, 1, 1};
-    pd_status st = encode(k, kt, 4, a.k, kd, ks, kb);
-    if (st == PD_OK) st = encode(v, kt, 4, a.v, kd, ks, kb);
-    if (st != PD_OK) return st;
+    const cuuint32_t kb[4] = {!fp8 ? 64u : operands && D > 128 ? 128u : cuuint32_t(D), 1u << a.slot_shift, 1, 1};
+    const CUtensorMapSwizzle sw = !fp8               ? CU_TENSOR_MAP_SWIZZLE_128B
+                                  : !operands        ? CU_TENSOR_MAP_SWIZZLE_NONE
+                                  : D < 128          ? CU_TENSOR_MAP_SWIZZLE_64B
+                                                     : CU_TENSOR_MAP_SWIZZLE_128B;
+    pd_status st = encode(k, kt, sw, 4, a.k, kd, ks, kb);
+    if (st == PD_OK) st = encode(v, kt, sw, 4, a.v, kd, ks, kb);
+    if (st != PD_OK || operands) return st;
     const cuuint64_t qd[3] = {d, hq, cuuint64_t(a.total_new)}, qs[2] = {d * 2, hq * d * 2};
     const cuuint32_t qb[3] = {64, cuuint32_t(a.hpt), cuuint32_t(a.npt)};
-    return encode(q, qt, 3, a.q, qd, qs, qb);
+    return encode(q, qt, CU_TENSOR_MAP_SWIZZLE_128B, 3, a.q, qd, qs, qb);
 }
 
 size_t round256(size_t x) { return (x + 255) / 256 * 256; }
@@ -114,11 +124,14 @@ pd_status check_heads(int Hq, int Hk, int D, pd_dtype dt) {
     return PD_OK;
 }
 
+// block: rows of a block of a block-scaled pool (fp8 is set too); 0: another pool. single: one node per request, without
+// new_indptr.
 pd_status tree_impl(const void* q, const void* k_data, const void* v_data, const float* k_scale, const float* v_scale,
                     const int32_t* indices, const int32_t* indptr, const int32_t* last_page_len,
                     const int32_t* new_indptr, const uint32_t* tree_mask, void* o, float* lse, int batch, int total_new,
                     int mask_words, int Hq, int Hk, int D, int page_size, int num_total_pages, int num_indices,
-                    float sm_scale, pd_dtype dt, void* workspace, size_t workspace_bytes, void* stream, bool fp8) {
+                    float sm_scale, pd_dtype dt, void* workspace, size_t workspace_bytes, void* stream, bool fp8,
+                    int block = 0, bool single = false) {
     pd_status st = check_heads(Hq, Hk, D, dt);
     if (st != PD_OK) return st;
     if (fp8 && dt == PD_F32) return host::fail(PD_ERR_UNSUPPORTED, "E4M3 pools take PD_F16 or PD_BF16 q and o");
@@ -129,7 +142,7 @@ pd_status tree_impl(const void* q, const void* k_data, const void* v_data, const
     if (tree_mask ? mask_words <= 0 : mask_words < 0 || (mask_words != 0 && total_new > 0))
         return host::fail(PD_ERR_INVALID, "mask_words must be positive with a tree_mask and 0 without (got %d)", mask_words);
     if (!std::isfinite(sm_scale)) return host::fail(PD_ERR_INVALID, "sm_scale must be finite");
-    if (!k_data || !v_data || !indptr || !last_page_len || !new_indptr || (num_indices > 0 && !indices) ||
+    if (!k_data || !v_data || !indptr || !last_page_len || (!single && !new_indptr) || (num_indices > 0 && !indices) ||
         (total_new > 0 && (!q || !o || !lse)) || (fp8 && (!k_scale || !v_scale)))
         return host::fail(PD_ERR_INVALID, "null pointer argument");
     if (!host::aligned(q, 16) || !host::aligned(k_data, 16) || !host::aligned(v_data, 16) || !host::aligned(o, 16))
@@ -149,7 +162,8 @@ pd_status tree_impl(const void* q, const void* k_data, const void* v_data, const
                       : all_rows > 16ll * batch ? kRows64
                       : all_rows > 8ll * batch  ? kRows16
                                                 : kRows8;
-    if (!pick(dt, fp8, D, group, rows, &kn)) return host::fail(PD_ERR_UNSUPPORTED, "no kernel for this type and head_dim");
+    if (!(block > 0 ? pick_blocks(dt, D, (all_rows + batch - 1) / batch, &kn) : pick(dt, fp8, D, group, rows, &kn)))
+        return host::fail(PD_ERR_UNSUPPORTED, "no kernel for this type and head_dim");
     int sms = 0;
     if ((st = host::sm_count(&sms)) != PD_OK) return st;
     const int most = sms * kn.per_sm;
@@ -171,6 +185,10 @@ pd_status tree_impl(const void* q, const void* k_data, const void* v_data, const
     a.lse = lse;
     a.k_scale = k_scale;
     a.v_scale = v_scale;
+    if (block > 0) {
+        a.scales_per_page = page_size / block;
+        a.by_block = FastDiv::of(block);
+    }
     a.splits = reinterpret_cast<TreeSplit*>(ws + sp.splits);
     a.part_lse = reinterpret_cast<float*>(ws + sp.lse);
     a.part_o = reinterpret_cast<float*>(ws + sp.o);
@@ -227,8 +245,8 @@ pd_status tree_impl(const void* q, const void* k_data, const void* v_data, const
     cudaStream_t cs = static_cast<cudaStream_t>(stream);
     if ((st = host::allow_smem(kn.main, kn.smem)) != PD_OK) return st;
     CUtensorMap maps[3]{};
-    if (kn.tensor && (st = make_maps(a, dt, fp8, D, &maps[0], &maps[1], &maps[2])) != PD_OK) return st;
-    void* args[] = {&a, &maps[0], &maps[1], &maps[2]};
+    if (kn.tensor && (st = make_maps(a, dt, fp8, block > 0, D, &maps[0], &maps[1], &maps[2])) != PD_OK) return st;
+    void* args[] = {&a, &maps[block > 0 ? 1 : 0], &maps[block > 0 ? 2 : 1], &maps[2]};
     cudaError_t e = cudaLaunchKernel(kn.main, dim3(grid), dim3(kn.threads), args, kn.smem, cs);
     if (e != cudaSuccess) return host::cuda_fail(e, "tree decode launch");
     if (merge) {
@@ -267,6 +285,53 @@ size_t pd_paged_tree_decode_workspace_bytes(int num_qo_heads, int num_kv_heads, 
     }
     host::ok();
     return most;
+}
+
+size_t pd_paged_tree_decode_fp8_blocks_workspace_bytes(int num_qo_heads, int num_kv_heads, int head_dim, pd_dtype dtype) {
+    if (check_heads(num_qo_heads, num_kv_heads, head_dim, dtype) != PD_OK) return 0;
+    if (dtype == PD_F32) {
+        host::fail(PD_ERR_UNSUPPORTED, "E4M3 pools take PD_F16 or PD_BF16 q and o");
+        return 0;
+    }
+    int sms = 0;
+    if (host::sm_count(&sms) != PD_OK) return 0;
+    size_t most = 0;
+    for (int rows = 16; rows <= 64; rows *= 2) {
+        TreeKernels k{};
+        if (!pick_blocks(dtype, head_dim, rows, &k)) continue;
+        const size_t n = space(k, sms * k.per_sm, head_dim).bytes;
+        if (n > most) most = n;
+    }
+    host::ok();
+    return most;
+}
+
+pd_status pd_paged_decode_fp8_blocks(const void* q, const void* k_data, const void* v_data, const float* k_scale,
+                                     const float* v_scale, const int32_t* indices, const int32_t* indptr,
+                                     const int32_t* last_page_len, void* o, float* lse, int batch, int num_qo_heads,
+                                     int num_kv_heads, int head_dim, int page_size, int num_total_pages,
+                                     int num_indices, int block_tokens, float sm_scale, pd_dtype dtype, void* workspace,
+                                     size_t workspace_bytes, void* stream) {
+    if (page_size > 0)
+        if (const pd_status st = host::check_block(block_tokens, page_size); st != PD_OK) return st;
+    return tree_impl(q, k_data, v_data, k_scale, v_scale, indices, indptr, last_page_len, nullptr, nullptr, o, lse, batch,
+                     batch, 0, num_qo_heads, num_kv_heads, head_dim, page_size, num_total_pages, num_indices, sm_scale,
+                     dtype, workspace, workspace_bytes, stream, true, block_tokens, true);
+}
+
+pd_status pd_paged_tree_decode_fp8_blocks(const void* q, const void* k_data, const void* v_data, const float* k_scale,
+                                          const float* v_scale, const int32_t* indices, const int32_t* indptr,
+                                          const int32_t* last_page_len, const int32_t* new_indptr,
+                                          const uint32_t* tree_mask, void* o, float* lse, int batch, int total_new,
+                                          int mask_words, int num_qo_heads, int num_kv_heads, int head_dim,
+                                          int page_size, int num_total_pages, int num_indices, int block_tokens,
+                                          float sm_scale, pd_dtype dtype, void* workspace, size_t workspace_bytes,
+                                          void* stream) {
+    if (page_size > 0)
+        if (const pd_status st = host::check_block(block_tokens, page_size); st != PD_OK) return st;
+    return tree_impl(q, k_data, v_data, k_scale, v_scale, indices, indptr, last_page_len, new_indptr, tree_mask, o, lse,
+                     batch, total_new, mask_words, num_qo_heads, num_kv_heads, head_dim, page_size, num_total_pages,
+                     num_indices, sm_scale, dtype, workspace, workspace_bytes, stream, true, block_tokens);
 }
 
 pd_status pd_paged_tree_decode(const void* q, const void* k_data, const void* v_data, const int32_t* indices,

@@ -51,12 +51,14 @@ struct TreeArgs {
     const int32_t* indices;
     const int32_t* indptr;
     const int32_t* last_page_len;
-    const int32_t* new_indptr;
+    const int32_t* new_indptr;  // null: one node per request, and a request without tokens is no error
     const uint32_t* mask;  // null: a chain
     void* o;
     float* lse;
-    const float* k_scale;  // E4M3 pools
+    const float* k_scale;  // E4M3 pools: of each kv head; block-scaled pools: [page][kv head][scales_per_page]
     const float* v_scale;
+    int scales_per_page;
+    FastDiv by_block;  // by the rows of a block
     float* part_o;    // [2 * ranges][seg_rows][D], normalised
     float* part_lse;  // [2 * ranges][seg_rows], log2 units
     TreeSplit* splits;  // [ranges]; the first holds a TreeLine
@@ -88,7 +90,8 @@ struct TreeReq {
 
 __device__ __forceinline__ TreeReq tree_request(const TreeArgs& a, int b) {
     TreeReq r = {0, 0, 0, 0, 0};
-    const int s = __ldg(a.new_indptr + b), e = __ldg(a.new_indptr + b + 1);
+    const bool single = a.new_indptr == nullptr;
+    const int s = single ? b : __ldg(a.new_indptr + b), e = single ? b + 1 : __ldg(a.new_indptr + b + 1);
     const int lo = __ldg(a.indptr + b), hi = __ldg(a.indptr + b + 1);
     int last = __ldg(a.last_page_len + b);
     if (s < 0 || e < s || e > a.total_new) {
@@ -110,7 +113,7 @@ __device__ __forceinline__ TreeReq tree_request(const TreeArgs& a, int b) {
         len = (long long)(hi - lo - 1) * a.page_size + last;
     }
     if (len < r.n || len > 0x3fffffff) {
-        r.bad |= kFlagBadNewRows;
+        if (!single || len > 0) r.bad |= kFlagBadNewRows;
         return r;
     }
     r.len = int(len);

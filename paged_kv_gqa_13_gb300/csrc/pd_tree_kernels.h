@@ -18,5 +18,8 @@ bool tree_tc_f16(int head_dim, bool wide, TreeKernels* k);
 bool tree_tc_bf16(int head_dim, bool wide, TreeKernels* k);
 bool tree_tc_f16_fp8(int head_dim, bool wide, TreeKernels* k);
 bool tree_tc_bf16_fp8(int head_dim, bool wide, TreeKernels* k);
+// over block-scaled E4M3 pools; rows: of a request
+bool blocks_tc_f16(int head_dim, int rows, TreeKernels* k);
+bool blocks_tc_bf16(int head_dim, int rows, TreeKernels* k);
 
 }  // namespace pd

@@ -111,3 +111,61 @@ def append_reference(c, which, b, new, exact):
         else:
             out.append(torch.clamp((top.float() / np.float32(TOP)), min=LEAST))
     return torch.stack(out) if out else torch.empty(0), first, lead, older
+
+
+def attend_reference(c, q, masks, sm_scale, dtype):
+    """(o, lse, tolerance of o, tolerance of lse) in 64 bits, from attended tokens alone. masks[b] [n, n] booleans; None: a
+    chain.
+
+    Tolerance of o, per output: half a step of the type for the result; of each weight, its two E4M3 parts (4 significant
+    bits each: 2^-8) and its step through f16 (2^-11); 2^-10, half a step of a subnormal code, where the largest weight times
+    V scale is 2^6.5 or more; and its score's error, in f32 sums and the
+    exponential (1e-5) and where a small element of q falls between codes: 2^-10 of q's codes, whose largest is 128 or more.
+    """
+    total, hq, d = q.shape
+    hk = c.k.shape[1]
+    g = hq // hk
+    half = torch.finfo(TYPES[dtype]).eps / 2
+    o, tol = torch.zeros(total, hq, d, dtype=torch.float64), torch.zeros(total, hq, d, dtype=torch.float64)
+    lse, tol_l = torch.full((total, hq), -math.inf, dtype=torch.float64), torch.zeros(total, hq, dtype=torch.float64)
+    for b, n in enumerate(c.new):
+        if n == 0 or c.kv[b] == 0:
+            continue
+        k, v = c.held(b)
+        p, r = c.rows(b, np.arange(c.kv[b]))
+        vs = c.v_scale[p, :, r // c.block].double()  # [tokens, heads]
+        codes = values(c.v[p, :, r]).abs()
+        ctx = c.kv[b] - n
+        seen = torch.ones(n, c.kv[b], dtype=torch.bool)
+        seen[:, ctx:] = torch.from_numpy(np.tril(np.ones((n, n), bool)) if masks is None else masks[b][:n, :n])
+        t = slice(int(c.new_indptr[b]), int(c.new_indptr[b]) + n)
+        for h in range(hk):
+            hs = slice(h * g, (h + 1) * g)
+            x = torch.einsum("ngd,td->ngt", q[t, hs].double(), k[:, h]) * sm_scale
+            x = x.masked_fill(~seen[:, None], -math.inf)
+            z = torch.logsumexp(x, -1, keepdim=True)
+            w = torch.exp(x - torch.where(torch.isinf(z), torch.zeros_like(z), z))
+            vh = torch.where(torch.isnan(v[:, h]), torch.zeros_like(v[:, h]), v[:, h])
+            out = torch.einsum("ngt,td->ngd", w, vh)
+            weight = torch.einsum("ngt,td->ngd", w, vh.abs())
+            top = torch.nan_to_num((w * vs[:, h]).masked_fill(~seen[:, None], 0.0)).amax(-1, keepdim=True)
+            ch = torch.where(torch.isnan(codes[:, h]), torch.zeros_like(codes[:, h]), codes[:, h]).clamp(max=448)
+            floor = torch.einsum("nt,td->nd", seen.double(), ch)[:, None]
+            score = 1e-5 + abs(sm_scale) * 2.0 ** -17 * q[t, hs].double().abs().amax(-1) * k[:, h].nan_to_num().abs().sum(-1).max()
+            o[t, hs], lse[t, hs] = out, z[..., 0]
+            tol[t, hs] = half * out.abs() + (2.0 ** -8 + 2.0 ** -11 + 2 * score[..., None]) * weight + 2.0 ** -16.5 * top * floor
+            tol_l[t, hs] = score + 2.0 ** -20 * z[..., 0].abs().nan_to_num(posinf=0.0)
+    return o, lse, tol + 1e-9, tol_l + 1e-5
+
+
+def check_attention(o, lse, ref, what=""):
+    ro, rl, tol, tol_l = ref
+    o, lse = o.double().cpu(), lse.double().cpu()
+    assert torch.equal(torch.isinf(rl), torch.isinf(lse)), what
+    assert not torch.isnan(o).any() and not torch.isnan(lse).any(), what
+    off = (o - ro).abs() - tol
+    assert float(off.max() if off.numel() else 0.0) <= 0, (what, float(off.max()), float((o - ro).abs().max()))
+    fine = ~torch.isinf(rl)
+    if fine.any():
+        assert float(((lse - rl).abs() - tol_l)[fine].max()) <= 0, (what, float((lse - rl)[fine].abs().max()))
+    assert float(o[~fine].abs().max() if (~fine).any() else 0.0) == 0.0, what

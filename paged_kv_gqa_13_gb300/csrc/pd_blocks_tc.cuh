@@ -18,18 +18,17 @@
 //
 // Parts. Both operands of a product are E4M3, which has 4 significant bits. q is
 // scaled by a power of two for each row (its largest element into [128, 256)) and
-// split into parts, each the code nearest to what the parts before leave: two
-// hold a bf16 row and three an f16 row exactly, down to 2^-10 (elements more
-// than 2^9 below the row's largest lose at most 2^-17 of that largest). The weights,
-// below 2^8.5, are two parts: each p_r to 2^-8 of itself (a bf16's half step) and
-// 2^-10 absolutely, 2^-16.5 of the largest. The parts of an operand are
-// products one after another into the same accumulator: more reads of A from
-// shared memory, which has time for them, and nothing to add up afterwards. The
-// running sum l takes the f32 weights before rounding. S, x, sums and O are f32.
+// split into parts, each the code nearest to 16 times what the part before leaves:
+// two hold a bf16 row and three an f16 row exactly, but for elements more than
+// 2^13 (2^14) below the row's largest, which lose at most 2^-21 of it. p_r, at most 2^8.5, is
+// two parts: p_r to 2^-8 of itself (a bf16's half step) and 2^-14 absolutely, 2^-16.5 of
+// the largest. Parts are further columns of a product (an instruction takes as
+// long for 16 columns as for 128), added up in f32: those of S when it is read, those of O at
+// the end. l takes the f32 weights before rounding. S, x, sums and O are f32.
 //
-// The maximum of a row moves only when a score passes it by more than 2^2 in the
-// weight; whether one does is a vote of the four warps of a tile. A row then takes
-// the new maximum over all 128 tokens, and O is rescaled in tensor memory.
+// The maximum of a row moves only when it is passed by more than 6 (a factor of
+// 64); whether one is, is a vote of the four warps of a tile. A row then takes the
+// new maximum over all 128 tokens, and O is rescaled in tensor memory.
 //
 // Lines, segments, ranges, tails and the merge are those of the tree decode
 // (pd_tree.cuh, pd_tree_tc.cuh), with blocks of 128 tokens and a ring of K and V
@@ -108,7 +107,7 @@ struct CfgBlocks {
     static constexpr int kColBlocks = D / kRowBytes;
     static constexpr int kMode = kRowBytes == 128 ? 2 : 4;
     static constexpr int kSlotBytes = kKeys * D;
-    static constexpr int kQPart = R * D, kQBytes = kQParts * kQPart;
+    static constexpr int kQRows = kQParts * R, kQBytes = kQRows * D;  // part p of row r is row p R + r
     static constexpr int kQBufs = R == 64 && D == 256 ? 1 : 2;
     static constexpr int kPPart = kKeys * R, kPBytes = 2 * kPPart, kPBufs = 2;
     static constexpr int kProducers = kLines == 2 ? 2 : 4;
@@ -127,8 +126,8 @@ struct CfgBlocks {
     static constexpr int kRowcOff = round_up(kBars * 8, 16);              // [kQBufs][R] score scale of a row
     static constexpr int kRowAtOff = kRowcOff + kQBufs * R * 4;           // [kQBufs][R] its q row, -1: none
     static constexpr int kNodeOff = kRowAtOff + kQBufs * R * 8;           // [kQBufs][R] its node
-    static constexpr int kWarpOff = round_up(kNodeOff + kQBufs * R * 4, 16);  // per softmax warp: c, -m, factor [kCols] each
-    static constexpr int kRedOff = kWarpOff + kSoftWarps * 3 * kCols * 4;     // [warp][kCols] exchanged maxima, sums
+    static constexpr int kWarpOff = round_up(kNodeOff + kQBufs * R * 4, 16);  // per softmax warp: c, -m, a factor, a rise [kCols] each
+    static constexpr int kRedOff = kWarpOff + kSoftWarps * 4 * kCols * 4;     // [warp][kCols] exchanged maxima, sums
     static constexpr int kVoteOff = kRedOff + kSoftWarps * kCols * 4;         // [kWgs][2]
     static constexpr int kTagOff = kVoteOff + kWgs * 2 * 4;                   // [2] segment with non-finite V
     static constexpr int kBadOff = kTagOff + 2 * 4;
@@ -147,12 +146,13 @@ struct CfgBlocks {
     static constexpr int kCtlOff = kLines * kLineBytes;
     static constexpr int kMiscOff = kCtlOff + kLines * kCtlBytes;  // tensor-memory address, abort flag
     static constexpr int kBytes = kMiscOff + 16 + 1024;            // 1024: alignment of the base
-    // tensor memory of a line: two S buffers, then O
-    static constexpr int kOCol = 2 * R;
-    static constexpr int kLineCols = kOCol + kColBlocks * R;
+    // tensor memory of a line: two S buffers (a column for each part of a row), then for each column block O of the weights'
+    // first parts and of their second ones
+    static constexpr int kOCol = 2 * kQRows;
+    static constexpr int kLineCols = kOCol + kColBlocks * 2 * R;
     static_assert(kLines * kLineCols <= 512, "tensor memory");
     static_assert(kSlots >= 3 && kBytes <= 232448, "shared memory");
-    static_assert(kLineBytes % 1024 == 0 && kQPart % 1024 == 0 && kPBytes % 1024 == 0 && kSlotBytes % 1024 == 0, "alignment");
+    static_assert(kLineBytes % 1024 == 0 && kQBytes % 1024 == 0 && kPBytes % 1024 == 0 && kSlotBytes % 1024 == 0, "alignment");
     static constexpr int kSegCost = 2;
     static constexpr int kClaimAhead = 4;
 };
@@ -164,7 +164,7 @@ __global__ void __launch_bounds__(CfgBlocks<D, R, sizeof(T) == 2 && std::is_same
     blocks_tc_kernel(const TreeArgs a, const __grid_constant__ CUtensorMap tmk, const __grid_constant__ CUtensorMap tmv) {
     constexpr int kQParts = std::is_same<T, __half>::value ? 3 : 2;
     using C = CfgBlocks<D, R, kQParts>;
-    constexpr float kShift = 6.5f, kRise = 2.f;  // weights: 2^kShift at the maximum, at most 2^(kShift + kRise) < 448
+    constexpr float kShift = 2.5f, kRise = 6.f;  // weights: 2^kShift at the maximum, at most 2^(kShift + kRise) < 448
     constexpr float kLeastV = 1.2621774e-29f;    // 2^-96: smaller V scales count so for the maximum (the sums stay below 2^128)
     const float kNegInf = -__int_as_float(0x7f800000);
     extern __shared__ __align__(16) uint8_t blocks_smem[];
@@ -250,7 +250,7 @@ __global__ void __launch_bounds__(CfgBlocks<D, R, sizeof(T) == 2 && std::is_same
     if (!soft && part == 0) {
         // ================================================================ mma
         const bool lead = lane == 0;
-        constexpr uint32_t idesc_s = tc_idesc_codes(C::kKeys, R, false, false), idesc_o = tc_idesc_codes(128, R, true, true);
+        constexpr uint32_t idesc_s = tc_idesc_codes(C::kKeys, C::kQRows, false, false), idesc_o = tc_idesc_codes(128, 2 * R, true, true);
         constexpr uint32_t kGroup = 8 * C::kRowBytes;  // bytes of 8 rows
         const uint64_t kdesc = smem_desc(sbase + C::kRingOff, 16, kGroup, C::kMode);
         // (head_dim 64: M is 128 all the same, its second half the first once more, at no step)
@@ -294,17 +294,13 @@ __global__ void __launch_bounds__(CfgBlocks<D, R, sizeof(T) == 2 && std::is_same
         auto issue_s = [&]() {
             tc_fence_after();
             const uint64_t kb = kdesc + uint32_t(kslot * (C::kSlotBytes / 16)), qb = qdesc + uint32_t(q_buf(seg) * (C::kQBytes / 16));
-            const uint32_t d = tmem + (n_qk & 1) * R;
+            const uint32_t d = tmem + (n_qk & 1) * C::kQRows;
 #pragma unroll
-            for (int p = 0; p < kQParts; ++p)
-#pragma unroll
-                for (int k = 0; k < D / 32; ++k) {
-                    const int cb = k * 32 / C::kRowBytes, in = k * 32 % C::kRowBytes;
-                    tc_mma_codes(d, kb + (cb * C::kKeys * C::kRowBytes + in) / 16, qb + (p * C::kQPart + cb * R * C::kRowBytes + in) / 16,
-                                 idesc_s, p + k > 0, lead);
-                }
+            for (int k = 0; k < D / 32; ++k) {
+                const int cb = k * 32 / C::kRowBytes, in = k * 32 % C::kRowBytes;
+                tc_mma_codes(d, kb + (cb * C::kKeys * C::kRowBytes + in) / 16, qb + (cb * C::kQRows * C::kRowBytes + in) / 16, idesc_s, k > 0, lead);
+            }
             tc_commit_if(bar(C::kSFull + (n_qk & 1)), lead);
-            tc_commit_if(bar(C::kEmpty + kslot), lead);
             if (blk + 1 == blk1) {  // the segment's last S
                 tc_commit_if(bar(C::kQEmpty + q_buf(seg)), lead);
                 if (lead) mbar_arrive(bar(C::kSegFree + seg % C::kSegRing));
@@ -335,11 +331,9 @@ __global__ void __launch_bounds__(CfgBlocks<D, R, sizeof(T) == 2 && std::is_same
 #pragma unroll
             for (int cb = 0; cb < C::kColBlocks; ++cb)
 #pragma unroll
-                for (int p = 0; p < 2; ++p)
-#pragma unroll
-                    for (int k = 0; k < C::kKeys / 32; ++k)
-                        tc_mma_codes(tmem + C::kOCol + cb * R, vb + (cb * C::kKeys * C::kRowBytes + k * 32 * C::kRowBytes) / 16,
-                                     pb + (p * C::kPPart + k * 512) / 16, idesc_o, !fresh || p + k > 0, lead);
+                for (int k = 0; k < C::kKeys / 32; ++k)
+                    tc_mma_codes(tmem + C::kOCol + cb * 2 * R, vb + (cb * C::kKeys * C::kRowBytes + k * 32 * C::kRowBytes) / 16,
+                                 pb + k * 512 / 16, idesc_o, !fresh || k > 0, lead);
             tc_commit_if(bar(C::kPvDone + buf), lead);
             tc_commit_if(bar(C::kEmpty + vs), lead);
             ++n_pv;
@@ -360,21 +354,26 @@ __global__ void __launch_bounds__(CfgBlocks<D, R, sizeof(T) == 2 && std::is_same
         bool ok = true;
         // one box per lane: slot_rows rows x kRowBytes codes
         const int sl = lane / C::kColBlocks, cb = lane % C::kColBlocks, spb = 1 << a.spb_shift, slot_rows = 1 << a.slot_shift;
-        auto load_block = [&](const TcSeg& s, int blk, const CUtensorMap* tm, bool is_k) -> bool {
+        // The page and row of this lane's box in block blk; a page out of range makes the copy fill zeros.
+        struct Box {
+            int page, row;
+            bool bad;
+        };
+        auto look_up = [&](const TcSeg& s, int blk) {
+            const int p = (blk << a.spb_shift) + sl;
+            Box x{a.num_total_pages, 0, false};
+            if (sl < spb && p < s.slots) {
+                const int at = a.by_cpp.div(p);
+                x.row = (p - at * a.cpp) << a.slot_shift;
+                x.page = __ldg(a.indices + s.lo + at);
+            }
+            return x;
+        };
+        auto load_block = [&](const TcSeg& s, int blk, const Box& box, const CUtensorMap* tm, bool is_k) -> bool {
             if (!idle && Own::mine(ring.slot, me)) {
-                const int p = (blk << a.spb_shift) + sl;
-                int page = a.num_total_pages, row = 0;  // page out of range: the copy fills zeros
-                bool bad = false;
-                if (sl < spb && p < s.slots) {
-                    const int at = a.by_cpp.div(p);
-                    row = (p - at * a.cpp) << a.slot_shift;
-                    page = __ldg(a.indices + s.lo + at);
-                    bad = page < 0 || page >= a.num_total_pages;
-                    if (bad) page = a.num_total_pages;
-                }
                 if (loads >= C::kSlots && !wait(C::kEmpty + ring.slot, ring.phase ^ 1u)) return false;
                 if (is_k) {
-                    const unsigned found = __ballot_sync(kFull, bad);
+                    const unsigned found = __ballot_sync(kFull, box.bad);
                     if (lane == 0) {
                         unsigned bits = 0;
                         for (unsigned f = found; f != 0u; f &= f - 1u) bits |= 1u << ((__ffs(f) - 1) / C::kColBlocks);
@@ -388,23 +387,22 @@ __global__ void __launch_bounds__(CfgBlocks<D, R, sizeof(T) == 2 && std::is_same
                 __syncwarp();
                 if (sl < spb)
                     tma_load_4d(sbase + C::kRingOff + ring.slot * C::kSlotBytes + cb * (C::kKeys * C::kRowBytes) + (sl << a.slot_shift) * C::kRowBytes,
-                                tm, cb * C::kRowBytes, row, s.kvh, page, bar(C::kFull + ring.slot), s.n > a.nps ? again : once);
+                                tm, cb * C::kRowBytes, box.row, s.kvh, box.page, bar(C::kFull + ring.slot), s.n > a.nps ? again : once);
                 if (!is_k) {
-                    // Both scales of the tile's tokens, four to a lane (a slot has 8 rows or more: one page). Their place is
-                    // free: the copy before in this slot was of K or V of a tile kSlots / 2 before at least, its product is
-                    // done, and so are the weights of the tile two before that one.
+                    // Both scales of the tile's tokens, four tokens to a lane (a slot has 8 rows or more: one page, and where
+                    // a.quads one block). Their place is free: the copy before in this slot was of K or V of a tile kSlots / 2
+                    // before at least, its product is done, and so are the weights of the tile two before that one.
                     const int col = 4 * lane, x = col >> a.slot_shift, from = x * C::kColBlocks;
-                    const int pg = __shfl_sync(kFull, page, from), r0 = __shfl_sync(kFull, row, from) + (col & (slot_rows - 1));
-                    const int at = a.by_cpp.div((blk << a.spb_shift) + x);
-                    const uint32_t dst = smem_u32(scales) + uint32_t((sc.slot * 2 * C::kKeys + col) * 4);
+                    const int pg = __shfl_sync(kFull, box.page, from), r0 = __shfl_sync(kFull, box.row, from) + (col & (slot_rows - 1));
+                    const int t0 = a.by_cpp.div((blk << a.spb_shift) + x) * a.page_size;  // token of the page's first row
                     const long long first = ((long long)pg * a.num_kv_heads + s.kvh) * a.scales_per_page;
-#pragma unroll
-                    for (int i = 0; i < 4; ++i) {
-                        const int r = r0 + i;
-                        const bool there = pg < a.num_total_pages && r < a.page_size && at * a.page_size + r < s.len;
+                    const uint32_t dst = smem_u32(scales) + uint32_t(sc.slot * 2 * C::kKeys * 4);
+                    for (int i = 0; i < (a.quads ? 1 : 4); ++i) {
+                        const int r = r0 + i, at = a.quads ? lane : col + i;
+                        const bool there = pg < a.num_total_pages && r < a.page_size && t0 + r < s.len;
                         const long long e = there ? first + a.by_block.div(r) : 0;
-                        copy4_async(dst + 4 * i, a.k_scale + e, there);
-                        copy4_async(dst + 4 * (C::kKeys + i), a.v_scale + e, there);
+                        copy4_async(dst + 4 * at, a.k_scale + e, there);
+                        copy4_async(dst + 4 * (C::kKeys + at), a.v_scale + e, there);
                     }
                     copy_arrive(bar(C::kScFull + sc.slot));
                 }
@@ -419,8 +417,14 @@ __global__ void __launch_bounds__(CfgBlocks<D, R, sizeof(T) == 2 && std::is_same
             const TcSeg& s = seg_at(i);
             const int blk0 = s.blk0, blk1 = s.blk1;
             if (blk0 == blk1) break;
-            for (int blk = blk0; blk < blk1 && ok; ++blk, ++kblocks)
-                ok = load_block(s, blk, &tmk, true) && load_block(s, blk, &tmv, false);
+            Box next = look_up(s, blk0);
+            for (int blk = blk0; blk < blk1 && ok; ++blk, ++kblocks) {
+                Box box = next;
+                box.bad = box.page < 0 || box.page > a.num_total_pages || (box.page == a.num_total_pages && sl < spb && (blk << a.spb_shift) + sl < s.slots);
+                if (box.bad) box.page = a.num_total_pages;
+                if (blk + 1 < blk1) next = look_up(s, blk + 1);  // one block ahead of its use
+                ok = load_block(s, blk, box, &tmk, true) && load_block(s, blk, box, &tmv, false);
+            }
             if (!ok) break;
             seg_free(i);
         }
@@ -525,12 +529,12 @@ __global__ void __launch_bounds__(CfgBlocks<D, R, sizeof(T) == 2 && std::is_same
                             const uint32_t c2 = uint32_t(__nv_cvt_float2_to_fp8x2(make_float2(f[y], f[y + 1]), __NV_SATFINITE, __NV_E4M3));
                             codes[y / 4] |= c2 << (8 * (y % 4));
                             const float2 got = __half22float2(codes_half2(c2));
-                            f[y] -= got.x;
-                            f[y + 1] -= got.y;
+                            f[y] = (f[y] - got.x) * 16.f;
+                            f[y + 1] = (f[y + 1] - got.y) * 16.f;
                         }
                         const int x0 = lane * kPer, col = x0 / C::kRowBytes, in = x0 % C::kRowBytes;
                         const int sw = C::kMode == 2 ? r & 7 : (r >> 1) & 3;
-                        uint8_t* dst = to + p * C::kQPart + col * (R * C::kRowBytes) + r * C::kRowBytes + (((in >> 4) ^ sw) << 4) + (in & 15);
+                        uint8_t* dst = to + col * (C::kQRows * C::kRowBytes) + (p * R + r) * C::kRowBytes + (((in >> 4) ^ sw) << 4) + (in & 15);
                         if constexpr (kPer == 2)
                             *reinterpret_cast<uint16_t*>(dst) = uint16_t(codes[0]);
                         else if constexpr (kPer == 4)
@@ -554,9 +558,10 @@ __global__ void __launch_bounds__(CfgBlocks<D, R, sizeof(T) == 2 && std::is_same
         const int sw = wid % C::kSoftWarps, wg = sw / 4, quad = wid & 3, tok = 32 * quad + lane, col0 = wg * C::kCols;
         const uint32_t lanes = uint32_t(32 * quad) << 16;
         const uint32_t ts0 = tmem + lanes + col0, to = tmem + lanes + C::kOCol + col0;
-        float* wc = reinterpret_cast<float*>(ctl + C::kWarpOff) + sw * 3 * C::kCols;  // c of this warp's rows
+        float* wc = reinterpret_cast<float*>(ctl + C::kWarpOff) + sw * 4 * C::kCols;  // c of this warp's rows
         float* wm = wc + C::kCols;                                                      // kShift - m
         float* wf = wm + C::kCols;                                                      // a factor
+        float* wd = wf + C::kCols;                                                      // what wm rose by
         float* red = reinterpret_cast<float*>(ctl + C::kRedOff) + wg * 4 * C::kCols;
         volatile int* votes = reinterpret_cast<volatile int*>(ctl + C::kVoteOff) + 2 * wg;
         const int vote_bar = C::kVote + wg;
@@ -582,7 +587,12 @@ __global__ void __launch_bounds__(CfgBlocks<D, R, sizeof(T) == 2 && std::is_same
             const TreeReq r = s.req();
             const int qb = q_buf(seg), cols = min(C::kCols, s.nodes * a.hpt - col0);  // this warpgroup's rows
             if (!(ok = wait(C::kQFull + qb, q_phase(seg)))) break;
-            if (cols > 0 && lane < C::kCols) wc[lane] = lane < ((cols + 7) & ~7) ? rowc[qb * R + col0 + lane] : 0.f;
+            __syncwarp();
+            if (cols > 0 && lane < C::kCols) {
+                wc[lane] = lane < ((cols + 7) & ~7) ? rowc[qb * R + col0 + lane] : 0.f;
+                wm[lane] = 0.f;
+            }
+            __syncwarp();
             float m = kNegInf;  // lane: the running maximum of row `lane`
             float l[C::kCols];
 #pragma unroll
@@ -592,17 +602,37 @@ __global__ void __launch_bounds__(CfgBlocks<D, R, sizeof(T) == 2 && std::is_same
                 if (!(ok = wait(C::kSFull + buf, uint32_t(jobs >> 1) & 1u))) break;
                 if (cols > 0) {
                     tc_fence_after();
-                    uint32_t x[C::kCols];
-#pragma unroll
-                    for (int c = 0; c < C::kCols; c += 16)
-                        if (c < cols) tmem_ld16(ts0 + buf * R + c, *reinterpret_cast<uint32_t(*)[16]>(x + c));
+                    float x[C::kCols], part[16], last[16];
+                    auto load_parts = [&](int c) {
+                        const uint32_t at = ts0 + buf * C::kQRows + c;
+                        tmem_ld16(at, *reinterpret_cast<uint32_t(*)[16]>(x + c));
+                        tmem_ld16(at + R, *reinterpret_cast<uint32_t(*)[16]>(part));
+                        if (kQParts > 2) tmem_ld16(at + 2 * R, *reinterpret_cast<uint32_t(*)[16]>(last));
+                    };
+                    load_parts(0);
+                    if (sw == 0 && lane == 0) mbar_arrive(bar(C::kEmpty + ring.slot));  // S is there: K has been read
                     if (!(ok = wait(C::kScFull + sc.slot, sc.phase))) break;
                     const float* sk = scales + sc.slot * 2 * C::kKeys;
-                    const float ks = sk[tok], vs = sk[C::kKeys + tok];
+                    const int sat = a.quads ? tok >> 2 : tok;
+                    const float ks = sk[sat], vs = sk[C::kKeys + sat];
                     const float lv = log2f(fmaxf(vs, kLeastV));
                     const unsigned bad_pages = bad_slots[jobs % C::kBadRing];
-                    tmem_wait_ld();
-                    // ---- scores of the rows over their scale; what a row does not attend is minus infinity
+                    // the sums of the parts, the smallest first
+#pragma unroll
+                    for (int c = 0; c < C::kCols; c += 16) {
+                        if (c >= cols) break;
+                        if (c > 0) load_parts(c);
+                        tmem_wait_ld();
+#pragma unroll
+                        for (int e = 0; e < 16; e += 2) {
+                            const float2 by = make_float2(0.0625f, 0.0625f);
+                            float2 y = make_float2(part[e], part[e + 1]);
+                            if (kQParts > 2) y = __ffma2_rn(make_float2(last[e], last[e + 1]), by, y);
+                            y = __ffma2_rn(y, by, make_float2(x[c + e], x[c + e + 1]));
+                            x[c + e] = y.x;
+                            x[c + e + 1] = y.y;
+                        }
+                    }
                     const bool fresh = blk == blk0;
                     const bool guard = !packed || bad_pages != 0u || blk >= tail0;
                     unsigned allow = ~0u;  // rows of this warpgroup that attend the token
@@ -629,7 +659,10 @@ __global__ void __launch_bounds__(CfgBlocks<D, R, sizeof(T) == 2 && std::is_same
                             const bool landed = tree_wait(bar(C::kFull + (ring.slot + 1 == C::kSlots ? 0 : ring.slot + 1)), vphase, abort_flag, a.flags);
                             bool found = false;
                             for (int x0 = 0; landed && x0 < D / 16; ++x0) {
-                                uint4* at = reinterpret_cast<uint4*>(vrow + x0 * 16 / C::kRowBytes * (C::kKeys * C::kRowBytes) + x0 * 16 % C::kRowBytes);
+                                // (lanes in turn from another 16 bytes on: all banks)
+                                constexpr int kIn = C::kRowBytes / 16;
+                                const int in = (x0 + lane) % kIn;
+                                uint4* at = reinterpret_cast<uint4*>(vrow + x0 / kIn * (C::kKeys * C::kRowBytes) + in * 16);
                                 uint4 w = *at;
                                 uint4 n = make_uint4(~0u, ~0u, ~0u, ~0u);
                                 if (!dead)
@@ -644,53 +677,55 @@ __global__ void __launch_bounds__(CfgBlocks<D, R, sizeof(T) == 2 && std::is_same
                         }
                         __syncwarp();
                     }
+                    // ---- exponents against the running maximum (the scores themselves in a segment's first tile); minus
+                    // infinity where a row does not attend the token
+                    float top = kNegInf;
+                    const float2 ks2 = make_float2(ks, ks);
 #pragma unroll
-                    for (int c = 0; c < C::kCols; ++c) {
+                    for (int c = 0; c < C::kCols; c += 4) {
                         if (c % 8 == 0 && c >= cols) break;
-                        float y = __uint_as_float(x[c]) * ks;
-                        if (guard && ((allow >> c) & 1u) == 0u) y = __int_as_float(0x7fc00000);  // (not a score; see below)
-                        x[c] = __float_as_uint(y);
+                        const float4 cc = *reinterpret_cast<const float4*>(wc + c), mm = *reinterpret_cast<const float4*>(wm + c);
+                        float2 y = __fmul2_rn(make_float2(x[c], x[c + 1]), ks2), z = __fmul2_rn(make_float2(x[c + 2], x[c + 3]), ks2);
+                        y = __ffma2_rn(y, make_float2(cc.x, cc.y), make_float2(mm.x, mm.y));
+                        z = __ffma2_rn(z, make_float2(cc.z, cc.w), make_float2(mm.z, mm.w));
+                        x[c] = y.x, x[c + 1] = y.y, x[c + 2] = z.x, x[c + 3] = z.y;
+                        if (guard) {
+#pragma unroll
+                            for (int e = c; e < c + 4; ++e)
+                                if (((allow >> e) & 1u) == 0u) x[e] = kNegInf;
+                        }
+                        top = fmaxf(fmaxf(top, fmaxf(x[c], x[c + 1])), fmaxf(x[c + 2], x[c + 3]));
                     }
                     // ---- does a weight pass its limit?
                     bool over = fresh;
                     if (!over) {
-                        float top = kNegInf;
-#pragma unroll
-                        for (int c = 0; c < C::kCols; c += 4) {
-                            if (c >= ((cols + 7) & ~7)) break;
-                            const float4 cc = *reinterpret_cast<const float4*>(wc + c), mm = *reinterpret_cast<const float4*>(wm + c);
-                            top = fmaxf(top, fmaf(__uint_as_float(x[c]), cc.x, mm.x));
-                            top = fmaxf(top, fmaf(__uint_as_float(x[c + 1]), cc.y, mm.y));
-                            top = fmaxf(top, fmaf(__uint_as_float(x[c + 2]), cc.z, mm.z));
-                            top = fmaxf(top, fmaf(__uint_as_float(x[c + 3]), cc.w, mm.w));
-                        }
-                        if (__any_sync(kFull, top + lv > kShift + kRise) && lane == 0) votes[exchanges & 1] = exchanges + 1;
                         const int id = exchanges + 1;
+                        if (__any_sync(kFull, top + lv > kShift + kRise) && lane == 0) votes[(id - 1) & 1] = id;
                         if (!(ok = exchange())) break;
                         over = votes[(id - 1) & 1] == id;
                     }
                     if (over) {
-                        __syncwarp();
                         float mine = kNegInf;
 #pragma unroll
                         for (int c = 0; c < C::kCols; ++c) {
                             if (c >= cols) break;
-                            const float y = fmaf(__uint_as_float(x[c]), wc[c], lv);
-                            const float t = redux_max(isnan(y) ? kNegInf : y);
+                            const float t = redux_max(isnan(x[c]) ? kNegInf : x[c] + lv);
                             if (lane == c) mine = t;
                         }
-                        if (lane < C::kCols) red[(sw & 3) * C::kCols + lane] = mine;
+                        const float was = lane < C::kCols ? wm[lane] : 0.f;
+                        if (lane < C::kCols) red[(sw & 3) * C::kCols + lane] = mine - was;
                         if (!(ok = exchange())) break;
-                        float f = 1.f;
                         if (lane < C::kCols) {
-                            const float top = fmaxf(fmaxf(red[lane], red[C::kCols + lane]), fmaxf(red[2 * C::kCols + lane], red[3 * C::kCols + lane]));
-                            const float to_m = fmaxf(m, top);
-                            f = m == kNegInf ? 1.f : ex2(m - to_m);
+                            const float best = fmaxf(fmaxf(red[lane], red[C::kCols + lane]), fmaxf(red[2 * C::kCols + lane], red[3 * C::kCols + lane]));
+                            const float to_m = fmaxf(m, best), now = to_m == kNegInf ? kShift : kShift - to_m;
+                            wf[lane] = m == kNegInf ? 1.f : ex2(m - to_m);
+                            wd[lane] = now - was;
+                            wm[lane] = now;
                             m = to_m;
-                            wm[lane] = m == kNegInf ? kShift : kShift - m;
                         }
-                        if (lane < C::kCols) wf[lane] = f;
                         __syncwarp();
+#pragma unroll
+                        for (int c = 0; c < C::kCols; ++c) x[c] += wd[c];
                         if (!fresh) {
                             // O holds every tile before this one once the last P V is done
                             if (!(ok = wait(C::kPvDone + (jobs - 1) % C::kPBufs, uint32_t((jobs - 1) / C::kPBufs) & 1u))) break;
@@ -698,7 +733,7 @@ __global__ void __launch_bounds__(CfgBlocks<D, R, sizeof(T) == 2 && std::is_same
 #pragma unroll
                             for (int c = 0; c < C::kCols; ++c) l[c] *= wf[c];
 #pragma unroll 1
-                            for (int cb = 0; cb < C::kColBlocks; ++cb)
+                            for (int cb = 0; cb < 2 * C::kColBlocks; ++cb)  // both parts' O of each column block
 #pragma unroll
                                 for (int c = 0; c < C::kCols; c += 16) {
                                     uint32_t o[16];
@@ -711,34 +746,39 @@ __global__ void __launch_bounds__(CfgBlocks<D, R, sizeof(T) == 2 && std::is_same
                             tmem_wait_st();
                         }
                     }
-                    // ---- weights and their parts
+                    // ---- weights and their parts, the second one 16 times what the first leaves
                     if (jobs >= C::kPBufs && !(ok = wait(C::kPvDone + pbuf, uint32_t((jobs - C::kPBufs) / C::kPBufs) & 1u))) break;
                     uint8_t* pp = smem + C::kPOff + pbuf * C::kPBytes + (col0 / 16) * 2048 + tok * 16;
+                    const float2 vs2 = make_float2(vs, vs);
+                    auto weights = [&](auto guarded) {
 #pragma unroll
-                    for (int c = 0; c < C::kCols; c += 8) {
-                        if (c >= cols) break;
-                        uint32_t p1[2] = {}, p2[2] = {};
+                        for (int c = 0; c < C::kCols; c += 8) {
+                            if (c >= cols) break;
+                            uint32_t p1[4], p2[4];
 #pragma unroll
-                        for (int e = 0; e < 8; e += 2) {
-                            const float2 cc = *reinterpret_cast<const float2*>(wc + c + e), mm = *reinterpret_cast<const float2*>(wm + c + e);
-                            float2 y = __ffma2_rn(make_float2(__uint_as_float(x[c + e]), __uint_as_float(x[c + e + 1])), cc, mm);
-                            y = make_float2(ex2(y.x), ex2(y.y));
-                            float2 w = make_float2(y.x * vs, y.y * vs);
-                            if (guard) {
-                                if (((allow >> (c + e)) & 1u) == 0u) y.x = w.x = 0.f;
-                                if (((allow >> (c + e + 1)) & 1u) == 0u) y.y = w.y = 0.f;
+                            for (int e = 0; e < 4; ++e) {
+                                const float2 y = make_float2(ex2(x[c + 2 * e]), ex2(x[c + 2 * e + 1]));
+                                float2 w = __fmul2_rn(y, vs2);
+                                if constexpr (decltype(guarded)::value) {  // (a scale that is not a number)
+                                    if (((allow >> (c + 2 * e)) & 1u) == 0u) w.x = 0.f;
+                                    if (((allow >> (c + 2 * e + 1)) & 1u) == 0u) w.y = 0.f;
+                                }
+                                float2 sum = __fadd2_rn(make_float2(l[c + 2 * e], l[c + 2 * e + 1]), y);
+                                l[c + 2 * e] = sum.x;
+                                l[c + 2 * e + 1] = sum.y;
+                                const __half2 h = __floats2half2_rn(w.x, w.y);
+                                p1[e] = half2_codes(h);
+                                p2[e] = half2_codes(__hmul2(__hsub2(h, codes_half2(p1[e])), __float2half2_rn(16.f)));
                             }
-                            l[c + e] += y.x;
-                            l[c + e + 1] += y.y;
-                            const __half2 h = __floats2half2_rn(w.x, w.y);
-                            const uint32_t h1 = half2_codes(h);
-                            p1[e / 4] |= h1 << (8 * (e % 4));
-                            p2[e / 4] |= half2_codes(__hsub2(h, codes_half2(h1))) << (8 * (e % 4));
+                            uint8_t* at = pp + c / 16 * 2048 + c % 16;
+                            *reinterpret_cast<uint2*>(at) = make_uint2(__byte_perm(p1[0], p1[1], 0x5410), __byte_perm(p1[2], p1[3], 0x5410));
+                            *reinterpret_cast<uint2*>(at + C::kPPart) = make_uint2(__byte_perm(p2[0], p2[1], 0x5410), __byte_perm(p2[2], p2[3], 0x5410));
                         }
-                        uint8_t* at = pp + c / 16 * 2048 + c % 16;
-                        *reinterpret_cast<uint2*>(at) = make_uint2(p1[0], p1[1]);
-                        *reinterpret_cast<uint2*>(at + C::kPPart) = make_uint2(p2[0], p2[1]);
-                    }
+                    };
+                    if (guard)
+                        weights(std::true_type{});
+                    else
+                        weights(std::false_type{});
                     fence_proxy_async_smem();
                     tc_fence_before();
                 }
@@ -773,9 +813,10 @@ __global__ void __launch_bounds__(CfgBlocks<D, R, sizeof(T) == 2 && std::is_same
                 for (int x = 0; x < C::kColBlocks * (C::kCols / 16); ++x) {
                     const int cb = x / (C::kCols / 16), c = x % (C::kCols / 16) * 16;
                     if (c >= cols) continue;
-                    uint32_t o[16];
+                    uint32_t o[16], o2[16];
                     __syncwarp();
-                    tmem_ld16(to + cb * R + c, o);
+                    tmem_ld16(to + cb * 2 * R + c, o);
+                    tmem_ld16(to + cb * 2 * R + R + c, o2);
                     tmem_wait_ld();
                     const int dim = cb * 128 + tok;
                     if (dim >= D) continue;  // (head_dim 64: the second half of M)
@@ -783,7 +824,7 @@ __global__ void __launch_bounds__(CfgBlocks<D, R, sizeof(T) == 2 && std::is_same
                     for (int e = 0; e < 16; ++e) {
                         const long long at = c + e < cols ? rowat[qb * R + col0 + c + e] : -1;
                         if (at < 0) continue;
-                        float f = __uint_as_float(o[e]) * wf[c + e];
+                        float f = fmaf(__uint_as_float(o2[e]), 0.0625f, __uint_as_float(o[e])) * wf[c + e];
                         if (fix) {
                             // NaN of node rows in these blocks, for the rows that attend them
                             const int node = rownode[qb * R + col0 + c + e];
@@ -848,7 +889,7 @@ bool blocks_tc_lookup(int D, TreeKernels* k) {
 
 template <typename T>
 bool blocks_tc_by_rows(int D, int rows, TreeKernels* k) {
-    return rows > 32 ? blocks_tc_lookup<T, 64>(D, k) : rows > 16 ? blocks_tc_lookup<T, 32>(D, k) : blocks_tc_lookup<T, 16>(D, k);
+    return rows > 16 ? blocks_tc_lookup<T, 32>(D, k) : blocks_tc_lookup<T, 16>(D, k);
 }
 
 }  // namespace pd

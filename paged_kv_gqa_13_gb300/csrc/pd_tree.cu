@@ -188,6 +188,7 @@ pd_status tree_impl(const void* q, const void* k_data, const void* v_data, const
     if (block > 0) {
         a.scales_per_page = page_size / block;
         a.by_block = FastDiv::of(block);
+        a.quads = block % 4 == 0 || block == page_size;
     }
     a.splits = reinterpret_cast<TreeSplit*>(ws + sp.splits);
     a.part_lse = reinterpret_cast<float*>(ws + sp.lse);
@@ -246,7 +247,7 @@ pd_status tree_impl(const void* q, const void* k_data, const void* v_data, const
     if ((st = host::allow_smem(kn.main, kn.smem)) != PD_OK) return st;
     CUtensorMap maps[3]{};
     if (kn.tensor && (st = make_maps(a, dt, fp8, block > 0, D, &maps[0], &maps[1], &maps[2])) != PD_OK) return st;
-    void* args[] = {&a, &maps[block > 0 ? 1 : 0], &maps[block > 0 ? 2 : 1], &maps[2]};
+    void* args[] = {&a, &maps[block > 0 ? 1 : 0], &maps[block > 0 ? 2 : 1], &maps[2]};  // (blocks: K and V alone)
     cudaError_t e = cudaLaunchKernel(kn.main, dim3(grid), dim3(kn.threads), args, kn.smem, cs);
     if (e != cudaSuccess) return host::cuda_fail(e, "tree decode launch");
     if (merge) {

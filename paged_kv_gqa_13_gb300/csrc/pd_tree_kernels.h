@@ -11,7 +11,7 @@ struct TreeKernels {
     int workers;                // independent ranges of work per CTA
     int block_tokens;           // tokens of a key block
     int seg_cost;               // TreeArgs::seg_cost
-    bool tensor;                // main takes tensor maps of q, K and V
+    bool tensor;                // main runs on the tensor cores and takes tensor maps
 };
 
 bool tree_tc_f16(int head_dim, bool wide, TreeKernels* k);

@@ -118,8 +118,8 @@ def attend_reference(c, q, masks, sm_scale, dtype):
     chain.
 
     Tolerance of o, per output: half a step of the type for the result; of each weight, its two E4M3 parts (4 significant
-    bits each: 2^-8) and its step through f16 (2^-11); 2^-10, half a step of a subnormal code, where the largest weight times
-    V scale is 2^6.5 or more; and its score's error, in f32 sums and the
+    bits each: 2^-8) and its step through f16 (2^-11); 2^-14, half a step of a subnormal code of the second part, where the
+    largest weight times V scale is 2^2.5 or more; and its score's error, in f32 sums and the
     exponential (1e-5) and where a small element of q falls between codes: 2^-10 of q's codes, whose largest is 128 or more.
     """
     total, hq, d = q.shape

@@ -74,15 +74,6 @@ __device__ __forceinline__ float redux_max(float x) {
     return y;
 }
 
-// 4 bytes from global to shared memory, or 4 zero bytes.
-__device__ __forceinline__ void copy4_async(uint32_t dst, const void* src, bool there) {
-    asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(dst), "l"(src), "r"(there ? 4 : 0) : "memory");
-}
-// An arrival (one of the barrier's count) when this thread's cp.async so far have landed.
-__device__ __forceinline__ void copy_arrive(uint32_t bar) {
-    asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(bar) : "memory");
-}
-
 __device__ __forceinline__ uint32_t half2_codes(__half2 h) {
     __half2_raw r;
     memcpy(&r, &h, 4);
@@ -353,7 +344,7 @@ __global__ void __launch_bounds__(CfgBlocks<D, R, sizeof(T) == 2 && std::is_same
         int loads = 0, kblocks = 0;  // of all producers
         bool ok = true;
         // one box per lane: slot_rows rows x kRowBytes codes
-        const int sl = lane / C::kColBlocks, cb = lane % C::kColBlocks, spb = 1 << a.spb_shift, slot_rows = 1 << a.slot_shift;
+        const int sl = lane / C::kColBlocks, cb = lane % C::kColBlocks, spb = 1 << a.spb_shift;
         // The page and row of this lane's box in block blk; a page out of range makes the copy fill zeros.
         struct Box {
             int page, row;
@@ -389,22 +380,10 @@ __global__ void __launch_bounds__(CfgBlocks<D, R, sizeof(T) == 2 && std::is_same
                     tma_load_4d(sbase + C::kRingOff + ring.slot * C::kSlotBytes + cb * (C::kKeys * C::kRowBytes) + (sl << a.slot_shift) * C::kRowBytes,
                                 tm, cb * C::kRowBytes, box.row, s.kvh, box.page, bar(C::kFull + ring.slot), s.n > a.nps ? again : once);
                 if (!is_k) {
-                    // Both scales of the tile's tokens, four tokens to a lane (a slot has 8 rows or more: one page, and where
-                    // a.quads one block). Their place is free: the copy before in this slot was of K or V of a tile kSlots / 2
-                    // before at least, its product is done, and so are the weights of the tile two before that one.
-                    const int col = 4 * lane, x = col >> a.slot_shift, from = x * C::kColBlocks;
-                    const int pg = __shfl_sync(kFull, box.page, from), r0 = __shfl_sync(kFull, box.row, from) + (col & (slot_rows - 1));
-                    const int t0 = a.by_cpp.div((blk << a.spb_shift) + x) * a.page_size;  // token of the page's first row
-                    const long long first = ((long long)pg * a.num_kv_heads + s.kvh) * a.scales_per_page;
-                    const uint32_t dst = smem_u32(scales) + uint32_t(sc.slot * 2 * C::kKeys * 4);
-                    for (int i = 0; i < (a.quads ? 1 : 4); ++i) {
-                        const int r = r0 + i, at = a.quads ? lane : col + i;
-                        const bool there = pg < a.num_total_pages && r < a.page_size && t0 + r < s.len;
-                        const long long e = there ? first + a.by_block.div(r) : 0;
-                        copy4_async(dst + 4 * at, a.k_scale + e, there);
-                        copy4_async(dst + 4 * (C::kKeys + at), a.v_scale + e, there);
-                    }
-                    copy_arrive(bar(C::kScFull + sc.slot));
+                    // The place is free: the copy before in this slot was of K or V of a tile kSlots / 2 before at least, its
+                    // product is done, and so are the weights of the tile two before that one.
+                    copy_scales<C::kKeys, C::kColBlocks>(a, s.kvh, s.len, blk, box.page, box.row, smem_u32(scales) + uint32_t(sc.slot * 2 * C::kKeys * 4),
+                                                         bar(C::kScFull + sc.slot));
                 }
             }
             ++loads;
@@ -613,7 +592,7 @@ __global__ void __launch_bounds__(CfgBlocks<D, R, sizeof(T) == 2 && std::is_same
                     if (sw == 0 && lane == 0) mbar_arrive(bar(C::kEmpty + ring.slot));  // S is there: K has been read
                     if (!(ok = wait(C::kScFull + sc.slot, sc.phase))) break;
                     const float* sk = scales + sc.slot * 2 * C::kKeys;
-                    const int sat = a.quads ? tok >> 2 : tok;
+                    const int sat = a.run > 1 ? tok >> 2 : tok;
                     const float ks = sk[sat], vs = sk[C::kKeys + sat];
                     const float lv = log2f(fmaxf(vs, kLeastV));
                     const unsigned bad_pages = bad_slots[jobs % C::kBadRing];
@@ -873,7 +852,7 @@ TreeKernels blocks_tc_kernels() {
     k.workers = C::kLines;
     k.block_tokens = C::kKeys;
     k.seg_cost = C::kSegCost;
-    k.tensor = true;
+    k.tensor = k.codes = true;
     return k;
 }
 

@@ -59,10 +59,12 @@ bool pick(pd_dtype dt, bool fp8, int D, int group, Rows rows, TreeKernels* k) {
     return false;
 }
 
-// Block-scaled pools: the kernel by the rows of a request on average (its row tiles hold 16, 32 or 64).
-bool pick_blocks(pd_dtype dt, int D, long long rows, TreeKernels* k) {
-    const int most = rows > 64 ? 64 : int(rows);
-    return dt == PD_F16 ? blocks_tc_f16(D, most, k) : blocks_tc_bf16(D, most, k);
+// Block-scaled pools: the kernel by the rows of a request on average. Up to 32 rows meet the codes as operands, in row
+// tiles of 16 or 32; more rows pay for widening the codes to f16 once, in row tiles of 128 or two of 128.
+bool pick_blocks(pd_dtype dt, int D, int block, long long rows, TreeKernels* k) {
+    if (rows <= 32) return dt == PD_F16 ? blocks_tc_f16(D, int(rows), k) : blocks_tc_bf16(D, int(rows), k);
+    if (block % 16 == 0) return dt == PD_F16 ? blocks_wide16_f16(D, k) : blocks_wide16_bf16(D, k);
+    return dt == PD_F16 ? blocks_wide_f16(D, k) : blocks_wide_bf16(D, k);
 }
 
 pd_status encode(CUtensorMap* map, CUtensorMapDataType ty, CUtensorMapSwizzle swizzle, int rank, const void* base,
@@ -162,7 +164,7 @@ pd_status tree_impl(const void* q, const void* k_data, const void* v_data, const
                       : all_rows > 16ll * batch ? kRows64
                       : all_rows > 8ll * batch  ? kRows16
                                                 : kRows8;
-    if (!(block > 0 ? pick_blocks(dt, D, (all_rows + batch - 1) / batch, &kn) : pick(dt, fp8, D, group, rows, &kn)))
+    if (!(block > 0 ? pick_blocks(dt, D, block, (all_rows + batch - 1) / batch, &kn) : pick(dt, fp8, D, group, rows, &kn)))
         return host::fail(PD_ERR_UNSUPPORTED, "no kernel for this type and head_dim");
     int sms = 0;
     if ((st = host::sm_count(&sms)) != PD_OK) return st;
@@ -188,7 +190,7 @@ pd_status tree_impl(const void* q, const void* k_data, const void* v_data, const
     if (block > 0) {
         a.scales_per_page = page_size / block;
         a.by_block = FastDiv::of(block);
-        a.quads = block % 4 == 0 || block == page_size;
+        a.run = block % 16 == 0 ? 16 : block % 4 == 0 || block == page_size ? 4 : 1;
     }
     a.splits = reinterpret_cast<TreeSplit*>(ws + sp.splits);
     a.part_lse = reinterpret_cast<float*>(ws + sp.lse);
@@ -246,8 +248,8 @@ pd_status tree_impl(const void* q, const void* k_data, const void* v_data, const
     cudaStream_t cs = static_cast<cudaStream_t>(stream);
     if ((st = host::allow_smem(kn.main, kn.smem)) != PD_OK) return st;
     CUtensorMap maps[3]{};
-    if (kn.tensor && (st = make_maps(a, dt, fp8, block > 0, D, &maps[0], &maps[1], &maps[2])) != PD_OK) return st;
-    void* args[] = {&a, &maps[block > 0 ? 1 : 0], &maps[block > 0 ? 2 : 1], &maps[2]};  // (blocks: K and V alone)
+    if (kn.tensor && (st = make_maps(a, dt, fp8, kn.codes, D, &maps[0], &maps[1], &maps[2])) != PD_OK) return st;
+    void* args[] = {&a, &maps[kn.codes ? 1 : 0], &maps[kn.codes ? 2 : 1], &maps[2]};
     cudaError_t e = cudaLaunchKernel(kn.main, dim3(grid), dim3(kn.threads), args, kn.smem, cs);
     if (e != cudaSuccess) return host::cuda_fail(e, "tree decode launch");
     if (merge) {
@@ -298,10 +300,12 @@ size_t pd_paged_tree_decode_fp8_blocks_workspace_bytes(int num_qo_heads, int num
     if (host::sm_count(&sms) != PD_OK) return 0;
     size_t most = 0;
     for (int rows = 16; rows <= 64; rows *= 2) {
-        TreeKernels k{};
-        if (!pick_blocks(dtype, head_dim, rows, &k)) continue;
-        const size_t n = space(k, sms * k.per_sm, head_dim).bytes;
-        if (n > most) most = n;
+        for (int block = 1; block <= 16; block += 15) {
+            TreeKernels k{};
+            if (!pick_blocks(dtype, head_dim, block, rows, &k)) continue;
+            const size_t n = space(k, sms * k.per_sm, head_dim).bytes;
+            if (n > most) most = n;
+        }
     }
     host::ok();
     return most;

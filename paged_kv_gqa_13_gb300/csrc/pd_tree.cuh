@@ -59,7 +59,7 @@ struct TreeArgs {
     const float* v_scale;
     int scales_per_page;
     FastDiv by_block;  // by the rows of a block
-    int quads;         // any 4 rows from a multiple of 4 on are of one block
+    int run;           // 16, 4 or 1: so many rows from a multiple of that on are of one block
     float* part_o;    // [2 * ranges][seg_rows][D], normalised
     float* part_lse;  // [2 * ranges][seg_rows], log2 units
     TreeSplit* splits;  // [ranges]; the first holds a TreeLine

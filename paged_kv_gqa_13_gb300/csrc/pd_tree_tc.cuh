@@ -180,13 +180,47 @@ __device__ __forceinline__ void store32(void* p, const uint32_t (&r)[8]) {
                  : "memory");
 }
 
+// 4 bytes from global to shared memory, or 4 zero bytes.
+__device__ __forceinline__ void copy4_async(uint32_t dst, const void* src, bool there) {
+    asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(dst), "l"(src), "r"(there ? 4 : 0) : "memory");
+}
+// An arrival (one of the barrier's count) when this thread's cp.async so far have landed.
+__device__ __forceinline__ void copy_arrive(uint32_t bar) {
+    asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(bar) : "memory");
+}
+
+// Block scales of the kKeys tokens of block blk, by a whole warp: K's, then V's, of each quad of tokens (a.run > 1) or
+// token, zero where there is none. Lane x (or x kPer) knows the page and first row of the block's slot x; a slot has 8
+// rows or more, so that a lane's tokens are of one page.
+template <int kKeys, int kPer = 1>
+__device__ __forceinline__ void copy_scales(const TreeArgs& a, int kvh, int len, int blk, int page, int row, uint32_t dst, uint32_t bar) {
+    const int lane = threadIdx.x & 31, col = 4 * lane, x = min(col, kKeys - 1) >> a.slot_shift;
+    const int pg = __shfl_sync(kFull, page, x * kPer), r0 = __shfl_sync(kFull, row, x * kPer) + (col & ((1 << a.slot_shift) - 1));
+    const int t0 = a.by_cpp.div((blk << a.spb_shift) + x) * a.page_size;  // token of the page's first row
+    const long long first = ((long long)pg * a.num_kv_heads + kvh) * a.scales_per_page;
+    for (int i = 0; i < (a.run > 1 ? 1 : 4); ++i) {
+        const int r = r0 + i, at = a.run > 1 ? lane : col + i;
+        if (col >= kKeys) break;
+        const bool there = pg >= 0 && pg < a.num_total_pages && r < a.page_size && t0 + r < len;
+        const long long e = there ? first + a.by_block.div(r) : 0;
+        copy4_async(dst + 4 * at, a.k_scale + e, there);
+        copy4_async(dst + 4 * (kKeys + at), a.v_scale + e, there);
+    }
+    copy_arrive(bar);
+}
+
 // ---------------------------------------------------------------- configuration
 
 // Lines are independent: each walks a range of work of its own through a ring
 // of its own. kWide: one line, two pipelines over the same blocks. Otherwise
 // two lines of one pipeline (head_dim 256: one, for tensor memory holds one O).
-template <int D, bool kWide, bool kFp8>
+// kPool: 16-bit pools, E4M3 pools with a scale per kv head, E4M3 pools with a scale per block of rows and kv head: of any
+// size, or of 16 rows from a multiple of 16 on (TreeArgs::run).
+constexpr int kPool16 = 0, kPoolCodes = 1, kPoolBlocks = 2, kPoolBlocks16 = 3;
+template <int D, bool kWide, int kPool>
 struct CfgTree {
+    static constexpr bool kFp8 = kPool != kPool16, kBlocks = kPool >= kPoolBlocks;
+    static constexpr int kRun = kPool == kPoolBlocks16 ? 16 : 1;  // keys that share a pair of scales in the softmax
     static constexpr int kRows = 128;
     static constexpr int kLines = kWide || D == 256 ? 1 : 2;
     static constexpr int kPipes = kWide ? 2 : 1;       // pipelines (row tiles) per line
@@ -197,7 +231,7 @@ struct CfgTree {
     static constexpr int kSlotBytes = kKeys * D * 2;   // one K or V block
     static constexpr int kQBytes = kRows * D * 2;      // one row tile of q
     static constexpr int kSlots = kFp8 ? (D == 64 ? 4 : 3) : D == 64 ? 10 : 5;
-    static constexpr int kStages = kFp8 ? 4 : 0;       // E4M3 pools: blocks of codes on their way
+    static constexpr int kStages = !kFp8 ? 0 : kBlocks && D > 64 ? 3 : 4;  // E4M3 pools: blocks of codes on their way
     static constexpr int kStageBytes = kKeys * D;
     // warps of a line after the softmax warps of all lines: mma, producers, inspectors (E4M3 pools: converters)
     static constexpr int kProducers = kFp8 ? (kLines == 2 ? 1 : 2) : kLines == 2 ? 2 : 4;
@@ -220,7 +254,10 @@ struct CfgTree {
                          kQEmpty = kQFull + kPipes, kQRaw = kQEmpty + kPipes, kSFull = kQRaw + kPipes, kPFull = kSFull + 2 * kPipes,
                          kPvDone = kPFull + 2 * kPipes, kAllDone = kPvDone + 2 * kPipes, kSegFull = kAllDone + kPipes,
                          kSegFree = kSegFull + kSegRing, kStFull = kSegFree + kSegRing, kStEmpty = kStFull + kStages,
-                         kBars = kStEmpty + kStages;
+                         kScFull = kStEmpty + kStages, kBars = kScFull + (kBlocks ? 6 : 0);
+    // block scales: of the blocks on their way (see the producers), and a softmax warp's of one job, ready for use
+    static constexpr int kScales = kBlocks ? 6 : 0, kScaleBytes = kScales * 2 * kKeys * 4;
+    static constexpr int kReadyBytes = kBlocks ? 4 * kPipes * (kJobKeys / kRun) * 16 : 0;
     // a line's shared memory: q, ring | barriers, bad-V tags, bad slots, segments (of all lines, after the data)
     static constexpr int kRingOff = kPipes * kQBytes;
     static constexpr int kStageOff = kRingOff + kSlots * kSlotBytes;
@@ -228,7 +265,8 @@ struct CfgTree {
     static constexpr int kTagOff = round_up(kBars * 8, 16);
     static constexpr int kBadOff = kTagOff + 4 * kTags;
     static constexpr int kSegOff = kBadOff + 4 * kBadRing;
-    static constexpr int kCtlBytes = round_up(kSegOff + kSegRing * 68, 8);
+    static constexpr int kScaleOff = round_up(kSegOff + kSegRing * 68, 16), kReadyOff = kScaleOff + kScaleBytes;
+    static constexpr int kCtlBytes = kBlocks ? kReadyOff + kReadyBytes : round_up(kSegOff + kSegRing * 68, 8);
     static constexpr int kCtlOff = kLines * kLineBytes;
     static constexpr int kMiscOff = kCtlOff + kLines * kCtlBytes;  // tensor-memory address, abort flag
     static constexpr int kBytes = kMiscOff + 16 + 1024;            // 1024: alignment of the base
@@ -288,11 +326,12 @@ __device__ __forceinline__ int tree_token(const TreeArgs& a, int blk, int col) {
 
 // ---------------------------------------------------------------- the kernel
 
-template <typename T, int D, bool kWide, bool kFp8>
-__global__ void __launch_bounds__(CfgTree<D, kWide, kFp8>::kThreads, 1)
+template <typename T, int D, bool kWide, int kPool>
+__global__ void __launch_bounds__(CfgTree<D, kWide, kPool>::kThreads, 1)
     tree_tc_kernel(const TreeArgs a, const __grid_constant__ CUtensorMap tmq, const __grid_constant__ CUtensorMap tmk,
                    const __grid_constant__ CUtensorMap tmv) {
-    using C = CfgTree<D, kWide, kFp8>;
+    constexpr bool kFp8 = kPool != kPool16, kBlocks = kPool >= kPoolBlocks;
+    using C = CfgTree<D, kWide, kPool>;
     using M = typename std::conditional<kFp8, __half, T>::type;  // operand type
     constexpr bool kBf16 = std::is_same<M, __nv_bfloat16>::value;
     const float kNegInf = -__int_as_float(0x7f800000);
@@ -341,6 +380,7 @@ __global__ void __launch_bounds__(CfgTree<D, kWide, kFp8>::kThreads, 1)
                 mbar_init(bar(C::kPFull + i), 4);
                 mbar_init(bar(C::kPvDone + i), 1);
             }
+            for (int i = 0; i < C::kScales; ++i) mbar_init(bar(C::kScFull + i), 32);
             for (int i = 0; i < C::kSegRing; ++i) {
                 mbar_init(bar(C::kSegFull + i), 1);
                 mbar_init(bar(C::kSegFree + i), C::kWalkers);
@@ -508,6 +548,7 @@ __global__ void __launch_bounds__(CfgTree<D, kWide, kFp8>::kThreads, 1)
                       kPlaceBytes = kFp8 ? C::kStageBytes : C::kSlotBytes, kQLanded = kFp8 ? C::kQRaw : C::kQFull;
         using Own = TreeProducers<kPlaces, C::kProducers>;
         Ring<kPlaces> ring;
+        Ring<kBlocks ? C::kScales : 1> sc;
         int loads = 0, qloads = 0, segments = 0, kblocks = 0;  // loads: of all producers
         bool ok = true;
         // one box per lane: slot_rows rows x 64 columns (codes: x head_dim columns)
@@ -542,9 +583,16 @@ __global__ void __launch_bounds__(CfgTree<D, kWide, kFp8>::kThreads, 1)
                 if (sl < spb)
                     tma_load_4d(sbase + kPlaceOff + ring.slot * kPlaceBytes + hf * (C::kKeys * 128) + (sl << a.slot_shift) * kRowBytes,
                                 tm, hf * 64, row, s.kvh, page, bar(kPlaceFull + ring.slot), s.n > a.nps ? again : once);
+                if (kBlocks && !is_k) {
+                    // The place is free: this stage was given back after 3 or 4 more loads were converted into slots that
+                    // products of two blocks before had used, and those followed the weights of the blocks before them.
+                    copy_scales<C::kKeys>(a, s.kvh, s.len, blk, bad ? -1 : page, row, smem_u32(ctl + C::kScaleOff) + uint32_t(sc.slot) * (2 * C::kKeys * 4),
+                                          bar(C::kScFull + sc.slot));
+                }
             }
             ++loads;
             ring.next();
+            if (kBlocks && !is_k) sc.next();
             return true;
         };
         for (; ok; ++segments) {
@@ -575,6 +623,7 @@ __global__ void __launch_bounds__(CfgTree<D, kWide, kFp8>::kThreads, 1)
             if (Own::mine(i % kPlaces, me)) mbar_wait_bounded(bar(kPlaceFull + i % kPlaces), uint32_t(i / kPlaces) & 1u);
         for (int i = max(0, qloads - C::kPipes); i < qloads; ++i)
             mbar_wait_bounded(bar(kQLanded + i % C::kPipes), uint32_t(i / C::kPipes) & 1u);
+        if (kBlocks) copy_wait();
     } else if (!soft) {
         // ================================================================ inspectors / converters; the first also walks the segments
         constexpr uint32_t kExp = kBf16 ? 0x7f807f80u : 0x7c007c00u;
@@ -603,7 +652,7 @@ __global__ void __launch_bounds__(CfgTree<D, kWide, kFp8>::kThreads, 1)
                 if (more) {
                     x = TcSeg{s.blk0, s.blk1,  s.tail0, s.slots, s.slot,  s.row0, s.node0,   s.nodes,
                               s.hh,   s.head0, s.kvh,   s.r.lo,  s.r.len, s.r.n,  s.r.start, 1.f, 1.f};
-                    if (kFp8) {
+                    if (kFp8 && !kBlocks) {
                         x.k_scale = __ldg(a.k_scale + s.kvh);
                         x.v_scale = __ldg(a.v_scale + s.kvh);
                     }
@@ -743,6 +792,8 @@ __global__ void __launch_bounds__(CfgTree<D, kWide, kFp8>::kThreads, 1)
         const bool packed = a.packed != 0, o_wide = (reinterpret_cast<uintptr_t>(a.o) & 31u) == 0;
         int jobs = 0, kblocks = 0;  // kblocks: K blocks before this segment
         bool ok = true;
+        Ring<kBlocks ? C::kScales : 1> sc;
+        float4* ready = reinterpret_cast<float4*>(ctl + C::kReadyOff) + (kBlocks ? wid % (4 * C::kPipes) * (C::kJobKeys / C::kRun) : 0);
         auto turn_q = [&](const TcSeg& s, int seg) -> bool {
             // This thread's q row, where the copy put it, as f16 times a power of two that brings its
             // largest element near 2^14 (exact but for elements more than 2^28 below it) and the sign of
@@ -791,10 +842,24 @@ __global__ void __launch_bounds__(CfgTree<D, kWide, kFp8>::kThreads, 1)
             if (kFp8) {
                 if (!(ok = turn_q(s, seg))) break;
             }
-            for (int blk = blk0; blk < blk1 && ok; ++blk) {
+            for (int blk = blk0; blk < blk1 && ok; ++blk, sc.next()) {
 #pragma unroll 1
                 for (int half = 0; half < C::kJobs; ++half) {
                     const int buf = jobs & 1;
+                    if (kBlocks && live) {
+                        // This job's scales for each run of keys, before its scores are there: {k, log2 v, 1 / v}, v at least
+                        // 2^-96 (the sums stay below 2^128).
+                        if (half == 0 && !(ok = wait(C::kScFull + sc.slot, sc.phase))) break;
+                        const float* from = reinterpret_cast<const float*>(ctl + C::kScaleOff) + sc.slot * 2 * C::kKeys;
+                        __syncwarp();
+#pragma unroll
+                        for (int g = lane; g < C::kJobKeys / C::kRun; g += 32) {
+                            const int key = half * C::kJobKeys + g * C::kRun, at = C::kRun == 16 || a.run > 1 ? key / 4 : key;
+                            const float v = fmaxf(from[C::kKeys + at], 1.2621774e-29f);
+                            ready[g] = make_float4(from[at], __log2f(v), __frcp_rn(v), 0.f);
+                        }
+                        __syncwarp();
+                    }
                     if (!(ok = wait(C::kSFull + 2 * p + buf, uint32_t(jobs >> 1) & 1u))) break;
                     if (live) {
                         tc_fence_after();
@@ -828,12 +893,29 @@ __global__ void __launch_bounds__(CfgTree<D, kWide, kFp8>::kThreads, 1)
                             }
                             __syncwarp();  // tensor-memory accesses are the whole warp's
                         }
-                        float tops[4];
+                        // (block scales: a factor above 0 leaves minus infinity what it is)
+                        auto factor = [&](const float4& f) { return fmaxf(scale * f.x, 1e-38f); };
+                        float top;
+                        if constexpr (kBlocks) {
+                            // what a key can bring to the output: its score and its V scale
+                            top = kNegInf;
 #pragma unroll
-                        for (int c = 0; c < 4; ++c) tops[c] = __uint_as_float(x[c]);
+                            for (int g = 0; g < C::kJobKeys / C::kRun; ++g) {
+                                const float4 f = ready[g];
+                                float most = __uint_as_float(x[g * C::kRun]), more = most;
 #pragma unroll
-                        for (int c = 4; c < C::kJobKeys; ++c) tops[c % 4] = fmaxf(tops[c % 4], __uint_as_float(x[c]));
-                        const float top = fmaxf(fmaxf(tops[0], tops[1]), fmaxf(tops[2], tops[3])) * scale;
+                                for (int e = 1; e < C::kRun; ++e)
+                                    (e % 2 != 0 ? more : most) = fmaxf(e % 2 != 0 ? more : most, __uint_as_float(x[g * C::kRun + e]));
+                                top = fmaxf(top, fmaf(fmaxf(most, more), factor(f), f.y));
+                            }
+                        } else {
+                            float tops[4];
+#pragma unroll
+                            for (int c = 0; c < 4; ++c) tops[c] = __uint_as_float(x[c]);
+#pragma unroll
+                            for (int c = 4; c < C::kJobKeys; ++c) tops[c % 4] = fmaxf(tops[c % 4], __uint_as_float(x[c]));
+                            top = fmaxf(fmaxf(tops[0], tops[1]), fmaxf(tops[2], tops[3])) * scale;
+                        }
                         if (blk == blk0 && half == 0) {
                             m = top;
                         } else {
@@ -862,13 +944,32 @@ __global__ void __launch_bounds__(CfgTree<D, kWide, kFp8>::kThreads, 1)
                         float2 sums[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
                         const float2 sc2 = make_float2(scale, scale), mu2 = make_float2(-mu, -mu);
                         uint32_t w[C::kJobKeys / 2];
+                        if constexpr (kBlocks) {
+                            // the V scale as an addend of the exponent: the weights that meet the codes; out of the sums again
 #pragma unroll
-                        for (int e = 0; e < C::kJobKeys / 2; ++e) {
-                            float2 y = make_float2(__uint_as_float(x[2 * e]), __uint_as_float(x[2 * e + 1]));
-                            y = __ffma2_rn(y, sc2, mu2);
-                            y = make_float2(ex2(y.x), ex2(y.y));
-                            sums[e % 2] = __fadd2_rn(sums[e % 2], y);
-                            w[e] = Elt<M>::pack(y.x, y.y);
+                            for (int g = 0; g < C::kJobKeys / (C::kRun > 1 ? C::kRun : 2); ++g) {
+                                constexpr int kOf = C::kRun > 1 ? C::kRun : 2;
+                                const float4 f = ready[C::kRun > 1 ? g : 2 * g], f1 = C::kRun > 1 ? f : ready[2 * g + 1];
+                                const float2 by = make_float2(factor(f), factor(f1)), add = make_float2(f.y - mu, f1.y - mu);
+                                float2 part = make_float2(0.f, 0.f);
+#pragma unroll
+                                for (int e = g * kOf; e < (g + 1) * kOf; e += 2) {
+                                    float2 y = __ffma2_rn(make_float2(__uint_as_float(x[e]), __uint_as_float(x[e + 1])), by, add);
+                                    y = make_float2(ex2(y.x), ex2(y.y));
+                                    part = kOf > 2 ? __fadd2_rn(part, y) : y;
+                                    w[e / 2] = Elt<M>::pack(y.x, y.y);
+                                }
+                                sums[g % 2] = __ffma2_rn(part, make_float2(f.z, f1.z), sums[g % 2]);
+                            }
+                        } else {
+#pragma unroll
+                            for (int e = 0; e < C::kJobKeys / 2; ++e) {
+                                float2 y = make_float2(__uint_as_float(x[2 * e]), __uint_as_float(x[2 * e + 1]));
+                                y = __ffma2_rn(y, sc2, mu2);
+                                y = make_float2(ex2(y.x), ex2(y.y));
+                                sums[e % 2] = __fadd2_rn(sums[e % 2], y);
+                                w[e] = Elt<M>::pack(y.x, y.y);
+                            }
                         }
                         tmem_st32(ts, w);
                         sums[0] = __fadd2_rn(sums[0], sums[1]);
@@ -966,11 +1067,11 @@ __global__ void __launch_bounds__(CfgTree<D, kWide, kFp8>::kThreads, 1)
 
 // ---------------------------------------------------------------- lookup
 
-template <typename T, int D, bool kWide, bool kFp8>
+template <typename T, int D, bool kWide, int kPool>
 TreeKernels tree_tc_kernels() {
-    using C = CfgTree<D, kWide, kFp8>;
+    using C = CfgTree<D, kWide, kPool>;
     TreeKernels k{};
-    k.main = reinterpret_cast<const void*>(tree_tc_kernel<T, D, kWide, kFp8>);
+    k.main = reinterpret_cast<const void*>(tree_tc_kernel<T, D, kWide, kPool>);
     k.merge = reinterpret_cast<const void*>(tree_merge_kernel<T, D>);
     k.threads = C::kThreads;
     k.smem = C::kBytes;
@@ -984,12 +1085,23 @@ TreeKernels tree_tc_kernels() {
     return k;
 }
 
-template <typename T, bool kFp8>
+template <typename T, int kPool>
 bool tree_tc_lookup(int D, bool wide, TreeKernels* k) {
     switch (D) {
-        case 64: *k = wide ? tree_tc_kernels<T, 64, true, kFp8>() : tree_tc_kernels<T, 64, false, kFp8>(); return true;
-        case 128: *k = wide ? tree_tc_kernels<T, 128, true, kFp8>() : tree_tc_kernels<T, 128, false, kFp8>(); return true;
-        case 256: *k = tree_tc_kernels<T, 256, false, kFp8>(); return true;
+        case 64: *k = wide ? tree_tc_kernels<T, 64, true, kPool>() : tree_tc_kernels<T, 64, false, kPool>(); return true;
+        case 128: *k = wide ? tree_tc_kernels<T, 128, true, kPool>() : tree_tc_kernels<T, 128, false, kPool>(); return true;
+        case 256: *k = tree_tc_kernels<T, 256, false, kPool>(); return true;
+    }
+    return false;
+}
+
+// Block-scaled pools and many rows.
+template <typename T, int kPool>
+bool blocks_wide_lookup(int D, TreeKernels* k) {
+    switch (D) {
+        case 64: *k = tree_tc_kernels<T, 64, true, kPool>(); return true;
+        case 128: *k = tree_tc_kernels<T, 128, true, kPool>(); return true;
+        case 256: *k = tree_tc_kernels<T, 256, false, kPool>(); return true;
     }
     return false;
 }

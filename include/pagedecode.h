@@ -700,8 +700,8 @@ pd_status pd_paged_norm_rope_append_fp8(const void* q, const void* k_new, const 
  *   o = 0, lse = -infinity.
  * pd_paged_tree_decode_fp8_blocks: pd_paged_tree_decode over such pools.
  *   Both: dtype (PD_F16 or PD_BF16) is the type of q and o; workspace: at least
- *   pd_paged_tree_decode_fp8_blocks_workspace_bytes(...) bytes, which any other
- *   call on the same stream may share. The other arguments, results and errors
+ *   the bytes that the call's _workspace_bytes gives, which any other call on
+ *   the same stream may share. The other arguments, results and errors
  *   are those of pd_paged_decode and pd_paged_tree_decode.
  */
 #define PD_MAX_BLOCK_TOKENS 64
@@ -720,6 +720,8 @@ pd_status pd_paged_read_fp8_blocks(const void* k_data, const void* v_data, const
                                    int total, int num_kv_heads, int head_dim, int page_size, int num_total_pages,
                                    int num_indices, int block_tokens, pd_dtype dtype, void* workspace,
                                    size_t workspace_bytes, void* stream);
+size_t pd_paged_decode_fp8_blocks_workspace_bytes(int batch, int num_qo_heads, int num_kv_heads, int head_dim,
+                                                  pd_dtype dtype);
 size_t pd_paged_tree_decode_fp8_blocks_workspace_bytes(int num_qo_heads, int num_kv_heads, int head_dim, pd_dtype dtype);
 pd_status pd_paged_decode_fp8_blocks(const void* q, const void* k_data, const void* v_data, const float* k_scale,
                                      const float* v_scale, const int32_t* indices, const int32_t* indptr,

@@ -87,6 +87,7 @@ _SIGS = {
     "pd_paged_norm_rope_append_fp8": (_I, [_P] * 16 + [_I] * 9 + [_L] * 3 + [_F, _I, _F, _I, _P, _S, _P]),
     "pd_paged_rope_append_fp8_blocks": (_I, [_P] * 16 + [_I] * 10 + [_L] * 3 + [_F, _I, _F, _I, _P, _S, _P]),
     "pd_paged_read_fp8_blocks": (_I, [_P] * 11 + [_I] * 9 + [_P, _S, _P]),
+    "pd_paged_decode_fp8_blocks_workspace_bytes": (_S, [_I, _I, _I, _I, _I]),
     "pd_paged_tree_decode_fp8_blocks_workspace_bytes": (_S, [_I, _I, _I, _I]),
     "pd_paged_decode_fp8_blocks": (_I, [_P] * 10 + [_I] * 8 + [_F, _I, _P, _S, _P]),
     "pd_paged_tree_decode_fp8_blocks": (_I, [_P] * 12 + [_I] * 10 + [_F, _I, _P, _S, _P]),
@@ -719,8 +720,15 @@ def pd_paged_read_fp8_blocks(k_data, v_data, k_scale, v_scale, indices, indptr, 
         _stream_for(k_data, stream)))
 
 
+def pd_paged_decode_fp8_blocks_workspace_bytes(batch: int, num_qo_heads: int, num_kv_heads: int, head_dim: int,
+                                               dtype: int) -> int:
+    n = _lib.pd_paged_decode_fp8_blocks_workspace_bytes(batch, num_qo_heads, num_kv_heads, head_dim, dtype)
+    if n == 0:
+        raise PagedecodeError(PD_ERR_INVALID, pd_last_error_string())
+    return n
+
+
 def pd_paged_tree_decode_fp8_blocks_workspace_bytes(num_qo_heads: int, num_kv_heads: int, head_dim: int, dtype: int) -> int:
-    """Of pd_paged_decode_fp8_blocks and pd_paged_tree_decode_fp8_blocks."""
     n = _lib.pd_paged_tree_decode_fp8_blocks_workspace_bytes(num_qo_heads, num_kv_heads, head_dim, dtype)
     if n == 0:
         raise PagedecodeError(PD_ERR_INVALID, pd_last_error_string())

@@ -29,6 +29,8 @@ PD_VARIANTS(bf16)
 #undef PD_VARIANTS
 bool lookup_fp8_f16(int head_dim, int heads, bool kv_pairs, KernelSet* ks);
 bool lookup_fp8_bf16(int head_dim, int heads, bool kv_pairs, KernelSet* ks);
+bool lookup_blocks_f16(int head_dim, int heads, KernelSet* ks);
+bool lookup_blocks_bf16(int head_dim, int heads, KernelSet* ks);
 }  // namespace pd
 
 namespace {
@@ -89,6 +91,18 @@ bool lookup_fp8(pd_dtype dt, int D, int G, bool kv_pairs, pd::KernelSet* ks) {
         default: return false;
     }
 }
+
+// The same for a block-scaled E4M3 pool.
+bool lookup_blocks(pd_dtype dt, int D, int G, pd::KernelSet* ks) {
+    switch (dt) {
+        case PD_F16: return pd::lookup_kernels_f16(D, G, ks) && pd::lookup_blocks_f16(D, G, ks);
+        case PD_BF16: return pd::lookup_kernels_bf16(D, G, ks) && pd::lookup_blocks_bf16(D, G, ks);
+        default: return false;
+    }
+}
+
+// The K/V pools of a decode call: of the type of q and o, E4M3 codes with a scale per kv head, or per block.
+enum Pools { kOwnType, kCodes, kBlockCodes };
 
 // Per-device facts, read once.
 struct DeviceInfo {
@@ -183,17 +197,18 @@ void split_group(int g, int* tiles, int* per) {
     *per = g / t;
 }
 
-pd_status make_plan_uncached(pd_dtype dt, int batch, int Hq, int Hk, int D, bool contiguous, bool fp8, Plan* p);
+pd_status make_plan_uncached(pd_dtype dt, int batch, int Hq, int Hk, int D, bool contiguous, Pools pools, Plan* p);
 
 // Plans depend only on the shape and the device: keep the last few so that a
 // decode loop pays the occupancy query and the attribute set-up once.
-// fp8: the K/V pool holds E4M3 codes (dt is then the type of q and o).
-pd_status make_plan(pd_dtype dt, int batch, int Hq, int Hk, int D, bool contiguous, Plan* p, bool fp8 = false) {
+// dt is the type of q and o.
+pd_status make_plan(pd_dtype dt, int batch, int Hq, int Hk, int D, bool contiguous, Plan* p, Pools pools = kOwnType) {
     struct Entry {
         int dev;
         pd_dtype dt;
         int batch, Hq, Hk, D;
-        bool contiguous, fp8, tcgen05;
+        bool contiguous, tcgen05;
+        Pools pools;
         Plan plan;
     };
     static Entry cache[16];
@@ -206,22 +221,22 @@ pd_status make_plan(pd_dtype dt, int batch, int Hq, int Hk, int D, bool contiguo
         for (int i = 0; i < used; ++i) {
             const Entry& e = cache[i];
             if (e.dev == dev && e.dt == dt && e.batch == batch && e.Hq == Hq && e.Hk == Hk && e.D == D &&
-                e.contiguous == contiguous && e.fp8 == fp8 && e.tcgen05 == tcgen05) {
+                e.contiguous == contiguous && e.pools == pools && e.tcgen05 == tcgen05) {
                 *p = e.plan;
                 return PD_OK;
             }
         }
     }
-    const pd_status st = make_plan_uncached(dt, batch, Hq, Hk, D, contiguous, fp8, p);
+    const pd_status st = make_plan_uncached(dt, batch, Hq, Hk, D, contiguous, pools, p);
     if (st != PD_OK) return st;
     std::lock_guard<std::mutex> lk(g_mu);
-    cache[next] = Entry{dev, dt, batch, Hq, Hk, D, contiguous, fp8, tcgen05, *p};
+    cache[next] = Entry{dev, dt, batch, Hq, Hk, D, contiguous, tcgen05, pools, *p};
     next = (next + 1) % 16;
     if (used < 16) ++used;
     return PD_OK;
 }
 
-pd_status make_plan_uncached(pd_dtype dt, int batch, int Hq, int Hk, int D, bool contiguous, bool fp8, Plan* p) {
+pd_status make_plan_uncached(pd_dtype dt, int batch, int Hq, int Hk, int D, bool contiguous, Pools pools, Plan* p) {
     if (dt != PD_F32 && dt != PD_F16 && dt != PD_BF16) return fail(PD_ERR_UNSUPPORTED, "dtype must be PD_F32, PD_F16 or PD_BF16");
     if (batch <= 0 || Hq <= 0 || Hk <= 0) return fail(PD_ERR_INVALID, "batch, num_qo_heads and num_kv_heads must be positive");
     if (Hq % Hk != 0) return fail(PD_ERR_INVALID, "num_qo_heads (%d) must be a multiple of num_kv_heads (%d)", Hq, Hk);
@@ -230,8 +245,10 @@ pd_status make_plan_uncached(pd_dtype dt, int batch, int Hq, int Hk, int D, bool
     split_group(p->group, &p->head_tiles, &p->heads_per_tile);
     p->G = 1;
     while (p->G < p->heads_per_tile) p->G *= 2;
-    if (fp8 && dt == PD_F32) return fail(PD_ERR_UNSUPPORTED, "E4M3 pools take f16 or bf16 q and o");
-    if (!(fp8 ? lookup_fp8(dt, D, p->G, kv_pairs_ok(dt, Hq, Hk), &p->ks) : lookup(dt, D, p->G, &p->ks)))
+    if (pools != kOwnType && dt == PD_F32) return fail(PD_ERR_UNSUPPORTED, "E4M3 pools take f16 or bf16 q and o");
+    if (!(pools == kBlockCodes ? lookup_blocks(dt, D, p->G, &p->ks)
+          : pools == kCodes    ? lookup_fp8(dt, D, p->G, kv_pairs_ok(dt, Hq, Hk), &p->ks)
+                               : lookup(dt, D, p->G, &p->ks)))
         return fail(PD_ERR_UNSUPPORTED, "no kernel for head_dim %d, %d heads per tile", D, p->G);
     p->G = p->ks.part_heads;  // the partial-result layout of the chosen kernel
     p->walk_kv = Hk;
@@ -675,15 +692,16 @@ size_t pd_contiguous_decode_workspace_bytes(int batch, int num_qo_heads, int num
 }
 
 // The paged decode, with the fused append when k_new / v_new are not null,
-// over an E4M3 pool when k_scale / v_scale are not null.
+// over an E4M3 pool when k_scale / v_scale are not null (a scale per kv head, or
+// for each `block` rows of a page and kv head where block > 0).
 static pd_status paged_decode_impl(const void* q, const void* k_new, const void* v_new, const void* k_data,
                                    const void* v_data, const int32_t* indices, const int32_t* indptr,
                                    const int32_t* last_page_len, void* o, float* lse, int batch, int num_qo_heads,
                                    int num_kv_heads, int head_dim, int page_size, int num_total_pages,
                                    int num_indices, float sm_scale, pd_dtype dtype, void* workspace,
                                    size_t workspace_bytes, void* stream, const float* k_scale = nullptr,
-                                   const float* v_scale = nullptr, bool clear_header = false) {
-    const bool fp8 = k_scale != nullptr;
+                                   const float* v_scale = nullptr, bool clear_header = false, int block = 0) {
+    const Pools pools = block > 0 ? kBlockCodes : k_scale != nullptr ? kCodes : kOwnType;
     if (dtype != PD_F32 && dtype != PD_F16 && dtype != PD_BF16) return fail(PD_ERR_UNSUPPORTED, "dtype must be PD_F32, PD_F16 or PD_BF16");
     if (batch <= 0 || num_qo_heads <= 0 || num_kv_heads <= 0 || page_size <= 0 || num_total_pages <= 0)
         return fail(PD_ERR_INVALID, "batch, num_qo_heads, num_kv_heads, page_size and num_total_pages must be positive");
@@ -700,7 +718,7 @@ static pd_status paged_decode_impl(const void* q, const void* k_new, const void*
     if (!aligned(lse, 4) || !aligned(indptr, 4) || !aligned(last_page_len, 4) || (indices && !aligned(indices, 4)))
         return fail(PD_ERR_UNSUPPORTED, "lse, indices, indptr and last_page_len must be 4-byte aligned");
     Plan pl;
-    pd_status st = make_plan(dtype, batch, num_qo_heads, num_kv_heads, head_dim, false, &pl, fp8);
+    pd_status st = make_plan(dtype, batch, num_qo_heads, num_kv_heads, head_dim, false, &pl, pools);
     if (st != PD_OK) return st;
     if ((st = check_workspace(workspace, workspace_bytes, pl.ws_bytes)) != PD_OK) return st;
     uint8_t* ws = static_cast<uint8_t*>(workspace);
@@ -710,6 +728,10 @@ static pd_status paged_decode_impl(const void* q, const void* k_new, const void*
     a.v = v_data;
     a.k_scale = k_scale;
     a.v_scale = v_scale;
+    if (block > 0) {
+        a.scales_per_page = page_size / block;
+        a.by_block = pd::FastDiv::of(block);
+    }
     a.indices = indices;
     a.indptr = indptr;
     a.last_page_len = last_page_len;
@@ -757,7 +779,7 @@ pd_status pd_paged_decode(const void* q, const void* k_data, const void* v_data,
 size_t pd_paged_decode_fp8_workspace_bytes(int batch, int num_qo_heads, int num_kv_heads, int head_dim,
                                            pd_dtype dtype) {
     Plan p;
-    if (make_plan(dtype, batch, num_qo_heads, num_kv_heads, head_dim, false, &p, true) != PD_OK) return 0;
+    if (make_plan(dtype, batch, num_qo_heads, num_kv_heads, head_dim, false, &p, kCodes) != PD_OK) return 0;
     ok();
     return p.ws_bytes;
 }
@@ -773,6 +795,49 @@ pd_status pd_paged_decode_fp8(const void* q, const void* k_data, const void* v_d
     return paged_decode_impl(q, nullptr, nullptr, k_data, v_data, indices, indptr, last_page_len, o, lse, batch,
                              num_qo_heads, num_kv_heads, head_dim, page_size, num_total_pages, num_indices, sm_scale,
                              dtype, workspace, workspace_bytes, stream, k_scale, v_scale);
+}
+
+// Groups of 3 to 8 q heads at head_dim 128 and 256 run on decode_fp8_mma_kernel, other shapes on the kernels of the tree
+// decode with one node per request: the former holds more copies in flight per SM and starts sooner (32 requests of 512 to
+// 4096 tokens, 4 heads a group: 56 us on the other, see pd_blocks_tc.cuh), the latter reads K and V once for any group
+// and takes any head_dim.
+static bool blocks_on_decode(int num_qo_heads, int num_kv_heads, int head_dim) {
+    const int group = num_kv_heads > 0 ? num_qo_heads / num_kv_heads : 0;
+    return head_dim >= 128 && group >= 3 && group <= 8;
+}
+
+size_t pd_paged_decode_fp8_blocks_workspace_bytes(int batch, int num_qo_heads, int num_kv_heads, int head_dim,
+                                                  pd_dtype dtype) {
+    if (batch <= 0) {
+        fail(PD_ERR_INVALID, "batch must be positive");
+        return 0;
+    }
+    if (!blocks_on_decode(num_qo_heads, num_kv_heads, head_dim))
+        return pd_paged_tree_decode_fp8_blocks_workspace_bytes(num_qo_heads, num_kv_heads, head_dim, dtype);
+    Plan p;
+    if (make_plan(dtype, batch, num_qo_heads, num_kv_heads, head_dim, false, &p, kBlockCodes) != PD_OK) return 0;
+    ok();
+    return p.ws_bytes;
+}
+
+pd_status pd_paged_decode_fp8_blocks(const void* q, const void* k_data, const void* v_data, const float* k_scale,
+                                     const float* v_scale, const int32_t* indices, const int32_t* indptr,
+                                     const int32_t* last_page_len, void* o, float* lse, int batch, int num_qo_heads,
+                                     int num_kv_heads, int head_dim, int page_size, int num_total_pages,
+                                     int num_indices, int block_tokens, float sm_scale, pd_dtype dtype, void* workspace,
+                                     size_t workspace_bytes, void* stream) {
+    if (dtype != PD_F16 && dtype != PD_BF16) return fail(PD_ERR_UNSUPPORTED, "E4M3 pools take PD_F16 or PD_BF16 q and o");
+    if (page_size > 0)
+        if (const pd_status st = pd::host::check_block(block_tokens, page_size); st != PD_OK) return st;
+    if (!k_scale || !v_scale) return fail(PD_ERR_INVALID, "null pointer argument");
+    if (!aligned(k_scale, 4) || !aligned(v_scale, 4)) return fail(PD_ERR_UNSUPPORTED, "k_scale and v_scale must be 4-byte aligned");
+    if (num_kv_heads > 0 && num_qo_heads % num_kv_heads == 0 && blocks_on_decode(num_qo_heads, num_kv_heads, head_dim))
+        return paged_decode_impl(q, nullptr, nullptr, k_data, v_data, indices, indptr, last_page_len, o, lse, batch,
+                                 num_qo_heads, num_kv_heads, head_dim, page_size, num_total_pages, num_indices, sm_scale,
+                                 dtype, workspace, workspace_bytes, stream, k_scale, v_scale, false, block_tokens);
+    return pd::host::blocks_one_node(q, k_data, v_data, k_scale, v_scale, indices, indptr, last_page_len, o, lse, batch,
+                                     num_qo_heads, num_kv_heads, head_dim, page_size, num_total_pages, num_indices,
+                                     block_tokens, sm_scale, dtype, workspace, workspace_bytes, stream);
 }
 
 pd_status pd_paged_append_decode(const void* q, const void* k_new, const void* v_new, void* k_data, void* v_data,

@@ -41,6 +41,13 @@
 //    memory to its two stages of codes.
 // Work partition, walk, softmax and the partial-result layout (8 heads per
 // slot) are those of decode_mma_kernel.
+//
+// kBlocks: block-scaled pools. A lane copies the two scales of its token of a
+// stage (cp.async, counted on the stage's barrier). k_scale multiplies a
+// token's scores; its weights meet the codes times v_scale, and the running
+// maximum is that of x + log2 v_scale, of what a token can bring to the output,
+// so that these weights stay in f16's range whatever the scales are. The sum l
+// takes the weights without v_scale.
 #pragma once
 
 #include <type_traits>
@@ -48,6 +55,15 @@
 #include "pd_decode_mma.cuh"
 
 namespace pd {
+
+// 4 bytes from global to shared memory, or 4 zero bytes.
+__device__ __forceinline__ void copy4_async(uint32_t dst, const void* src, bool there) {
+    asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(dst), "l"(src), "r"(there ? 4 : 0) : "memory");
+}
+// An arrival (one of the barrier's count) when this thread's cp.async so far have landed.
+__device__ __forceinline__ void copy_arrive(uint32_t bar) {
+    asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(bar) : "memory");
+}
 
 // Two 16 x 16 byte matrices from shared memory, transposed: lanes 0-15 give
 // the addresses of matrix 0's rows, lanes 16-31 those of matrix 1. Lane
@@ -79,14 +95,15 @@ struct CfgF8 {
     // q is not staged: it is read at a segment start, from L2 (see produce)
     static constexpr int kStageBytes = round_up(2 * kSub * kTileRaw, 128);
     static constexpr int kMetaOff = kStages * kStageBytes;
-    static constexpr int kBarOff = kMetaOff + kStages * 16;
+    static constexpr int kScaleOff = kMetaOff + kStages * 16;  // block-scaled pools: [stage][K, V][token]
+    static constexpr int kBarOff = kScaleOff + kStages * 256;
     // stages stay 1024-byte aligned for the swizzle
     static constexpr int kWarpBytes = round_up(kBarOff + kStages * 8, 1024);
     static constexpr int kKSteps = D / 16;
     static constexpr int kJ = D / 64;  // 64-dim groups: one 16-byte load per row each
 };
 
-template <typename T, int D>
+template <typename T, int D, bool kBlocks = false>
 __global__ void __launch_bounds__(CfgF8<D>::kMaxWarps * 32, 1)
     decode_fp8_mma_kernel(const DecodeArgs a, const __grid_constant__ CUtensorMap tmk,
                           const __grid_constant__ CUtensorMap tmv) {
@@ -124,7 +141,7 @@ __global__ void __launch_bounds__(CfgF8<D>::kMaxWarps * 32, 1)
 
     walk.stage_table(s_indptr, s_lpl, [&] {
         if (lane == 0) {
-            for (int s = 0; s < kS; ++s) mbar_init(bar0 + 8 * s, 1);
+            for (int s = 0; s < kS; ++s) mbar_init(bar0 + 8 * s, kBlocks ? 33 : 1);
             fence_mbar_init();
         }
         // The first stage's positions: on the Llama-shaped batch, pulling in
@@ -146,8 +163,21 @@ __global__ void __launch_bounds__(CfgF8<D>::kMaxWarps * 32, 1)
         Chunk c0, c1;
         const bool have = walk.template next<kMmaRows>(&c0);
         const bool two = (C::kSub == 2 && have && !(c0.flags & kSegEnd)) ? walk.template next<kMmaRows>(&c1) : false;
-        if (lane != 0) return;
         const uint32_t bar = bar0 + 8 * slot;
+        if constexpr (kBlocks) {
+            const int r = lane & 15, rows = !have ? 0 : lane < 16 ? c0.rows : two ? c1.rows : 0;
+            if (have) {
+                const Chunk& c = lane < 16 || !two ? c0 : c1;
+                const bool there = r < rows;
+                const long long at =
+                    there ? ((long long)c.slab * a.num_kv_heads + c.kh) * a.scales_per_page + a.by_block.div(c.row0 + r) : 0;
+                const uint32_t dst = wsm_u32 + C::kScaleOff + slot * 256 + lane * 4;
+                copy4_async(dst, a.k_scale + at, there);
+                copy4_async(dst + 128, a.v_scale + at, there);
+            }
+            copy_arrive(bar);
+        }
+        if (lane != 0) return;
         const uint32_t st = wsm_u32 + slot * C::kStageBytes;
         if (!have) {
             meta[slot] = make_int4(0, kEndOfWork, 0, 0);
@@ -215,7 +245,7 @@ __global__ void __launch_bounds__(CfgF8<D>::kMaxWarps * 32, 1)
         }
         const int qrow = m.z;
         const int h0 = 2 * c, h1 = 2 * c + 1;
-        const float vsc = __ldg(a.v_scale + (qrow % a.num_qo_heads) / a.group);  // V scale, applied once
+        const float vsc = kBlocks ? 1.f : __ldg(a.v_scale + (qrow % a.num_qo_heads) / a.group);  // V scale, applied once
         const float inv0 = l0 > 0.f ? vsc / l0 : 0.f, inv1 = l1 > 0.f ? vsc / l1 : 0.f;
         const float lse0 = l0 > 0.f ? m0 - kShift + log2f(l0) : kNegInf;
         const float lse1 = l1 > 0.f ? m1 - kShift + log2f(l1) : kNegInf;
@@ -271,7 +301,7 @@ __global__ void __launch_bounds__(CfgF8<D>::kMaxWarps * 32, 1)
             // scaled by a power of two 2^-e (the head's largest |q| into
             // [2^14, 2^15)): a bf16 or f16 q is then exact in f16, and 2^e and
             // the scales multiply the f32 sums.
-            const float qs = a.q_scale * __ldg(a.k_scale + (m.z % a.num_qo_heads) / a.group);
+            const float qs = kBlocks ? a.q_scale : a.q_scale * __ldg(a.k_scale + (m.z % a.num_qo_heads) / a.group);
             const uint8_t* qb = static_cast<const uint8_t*>(a.q) + (size_t(m.z) + g) * q_row_bytes;
             uint2 w[kKS];
             float mx = 0.f;
@@ -335,15 +365,29 @@ __global__ void __launch_bounds__(CfgF8<D>::kMaxWarps * 32, 1)
         // softmax over the 32 tokens; x[s][i]: tile s, token g (i = 0, 1) or
         // g + 8 (i = 2, 3), head 2c (i even) or 2c + 1 (i odd)
         float x[2][4];
+        float ks[2][2], vs[2][2], lv[2][2];  // block-scaled pools: of tokens rg0 and rg0 + 2 of each tile
+        if constexpr (kBlocks) {
+            const float* sc_at = reinterpret_cast<const float*>(wsm + C::kScaleOff + slot * 256) + rg0;
+#pragma unroll
+            for (int s = 0; s < 2; ++s)
+#pragma unroll
+                for (int i = 0; i < 2; ++i) {
+                    ks[s][i] = sc_at[16 * s + 2 * i];
+                    vs[s][i] = sc_at[32 + 16 * s + 2 * i];
+                    lv[s][i] = __log2f(fmaxf(vs[s][i], 1.2621774e-29f));  // at least 2^-96: the sums stay below 2^128
+                }
+        }
+        auto k_of = [&](int s, int i) { return kBlocks ? ks[s][i] : 1.f; };
 #pragma unroll
         for (int s = 0; s < 2; ++s) {
-            x[s][0] = rg0 < rows[s] ? sc[s][0] * qsc0 : kNegInf;
-            x[s][1] = rg0 < rows[s] ? sc[s][1] * qsc1 : kNegInf;
-            x[s][2] = rg0 + 2 < rows[s] ? sc[s][2] * qsc0 : kNegInf;
-            x[s][3] = rg0 + 2 < rows[s] ? sc[s][3] * qsc1 : kNegInf;
+            x[s][0] = rg0 < rows[s] ? sc[s][0] * (qsc0 * k_of(s, 0)) : kNegInf;
+            x[s][1] = rg0 < rows[s] ? sc[s][1] * (qsc1 * k_of(s, 0)) : kNegInf;
+            x[s][2] = rg0 + 2 < rows[s] ? sc[s][2] * (qsc0 * k_of(s, 1)) : kNegInf;
+            x[s][3] = rg0 + 2 < rows[s] ? sc[s][3] * (qsc1 * k_of(s, 1)) : kNegInf;
         }
-        const float c0l = fmaxf(fmaxf(x[0][0], x[0][2]), fmaxf(x[1][0], x[1][2]));
-        const float c1l = fmaxf(fmaxf(x[0][1], x[0][3]), fmaxf(x[1][1], x[1][3]));
+        auto v_log = [&](int s, int i) { return kBlocks ? lv[s][i] : 0.f; };
+        const float c0l = fmaxf(fmaxf(x[0][0] + v_log(0, 0), x[0][2] + v_log(0, 1)), fmaxf(x[1][0] + v_log(1, 0), x[1][2] + v_log(1, 1)));
+        const float c1l = fmaxf(fmaxf(x[0][1] + v_log(0, 0), x[0][3] + v_log(0, 1)), fmaxf(x[1][1] + v_log(1, 0), x[1][3] + v_log(1, 1)));
         if (__any_sync(kFull, c0l > m0 + kTauM || c1l > m1 + kTauM)) {
             float c0 = c0l, c1 = c1l;
 #pragma unroll
@@ -377,8 +421,9 @@ __global__ void __launch_bounds__(CfgF8<D>::kMaxWarps * 32, 1)
             const float p3 = x[s][3] == kNegInf ? 0.f : ex2(x[s][3] - m1 + kShift);
             l0 += p0 + p2;
             l1 += p1 + p3;
-            bh[s][0] = movm_trans(pack_pair<M>(p0, p1));
-            bh[s][1] = movm_trans(pack_pair<M>(p2, p3));
+            const float va = kBlocks ? vs[s][0] : 1.f, vb = kBlocks ? vs[s][1] : 1.f;
+            bh[s][0] = movm_trans(pack_pair<M>(p0 * va, p1 * va));
+            bh[s][1] = movm_trans(pack_pair<M>(p2 * vb, p3 * vb));
         }
         // O^T[head_dim][8 heads] += V_s^T[head_dim][16 tokens] P_s[16 tokens][8 heads]. m tile mt
         // holds dims 16 mt .. 16 mt + 15; ldmatrix hands lane (g, c) the codes of tokens

@@ -502,9 +502,12 @@ struct DecodeArgs {
     // kernel then writes into k and v.
     const void* k_new;
     const void* v_new;
-    // FP8 pools (null otherwise): element value = E4M3 code value * scale[kv head].
+    // FP8 pools (null otherwise): element value = E4M3 code value * scale[kv head], or (block-scaled pools:
+    // scales_per_page > 0) * scale[page][kv head][row / rows of a block].
     const float* k_scale;
     const float* v_scale;
+    int scales_per_page;
+    FastDiv by_block;  // by the rows of a block
     int test_extra_tx;  // test-only wait-timeout injection (pd_test_inject_wait_timeout); normally 0
     // 0: warp w of block c holds unit c * warps_per_block + w. 1: unit
     // w * blocks + c, with one pass per warp of a block and passes padded to a

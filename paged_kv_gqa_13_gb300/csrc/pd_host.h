@@ -23,6 +23,12 @@ pd_status allow_smem(const void* fn, int bytes);
 pd_status check_block(int block_tokens, int page_size);
 // Checks of a rotation's arguments, shared by the calls that rotate (pd_rope.cu).
 pd_status check_rotation(int tokens, int head_dim, int rot_dim, int layout, float rope_scale, const uint64_t* freqs, pd_dtype dt);
+// pd_paged_decode_fp8_blocks on the kernels of the tree decode (pd_tree.cu).
+pd_status blocks_one_node(const void* q, const void* k_data, const void* v_data, const float* k_scale, const float* v_scale,
+                          const int32_t* indices, const int32_t* indptr, const int32_t* last_page_len, void* o, float* lse,
+                          int batch, int num_qo_heads, int num_kv_heads, int head_dim, int page_size, int num_total_pages,
+                          int num_indices, int block_tokens, float sm_scale, pd_dtype dt, void* workspace,
+                          size_t workspace_bytes, void* stream);
 // pd_test_inject_wait_timeout's extra bytes (0: off).
 int test_extra_tx();
 // The driver's tensor-map encoder; null when the driver does not offer it.

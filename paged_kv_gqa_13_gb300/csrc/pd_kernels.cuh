@@ -159,4 +159,13 @@ bool lookup_fp8_t(int D, int G, bool kv_pairs, KernelSet* ks) {
     return false;
 }
 
+// The tensor-core decode kernel over block-scaled E4M3 pools (tiles of 4 or 8 q heads, head_dim 128 or 256).
+template <typename T>
+bool lookup_blocks_t(int D, int G, KernelSet* ks) {
+    if (G < 4 || D < 128 || !lookup_fp8_t<T>(D, G, false, ks)) return false;
+    ks->decode = ks->variant[0] = D == 128 ? reinterpret_cast<const void*>(decode_fp8_mma_kernel<T, 128, true>)
+                                           : reinterpret_cast<const void*>(decode_fp8_mma_kernel<T, 256, true>);
+    return true;
+}
+
 }  // namespace pd

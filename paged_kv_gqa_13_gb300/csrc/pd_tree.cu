@@ -269,6 +269,20 @@ pd_status tree_impl(const void* q, const void* k_data, const void* v_data, const
 }
 
 }  // namespace
+
+namespace host {
+
+pd_status blocks_one_node(const void* q, const void* k_data, const void* v_data, const float* k_scale, const float* v_scale,
+                          const int32_t* indices, const int32_t* indptr, const int32_t* last_page_len, void* o, float* lse,
+                          int batch, int num_qo_heads, int num_kv_heads, int head_dim, int page_size, int num_total_pages,
+                          int num_indices, int block_tokens, float sm_scale, pd_dtype dt, void* workspace,
+                          size_t workspace_bytes, void* stream) {
+    return tree_impl(q, k_data, v_data, k_scale, v_scale, indices, indptr, last_page_len, nullptr, nullptr, o, lse, batch,
+                     batch, 0, num_qo_heads, num_kv_heads, head_dim, page_size, num_total_pages, num_indices, sm_scale, dt,
+                     workspace, workspace_bytes, stream, true, block_tokens, true);
+}
+
+}  // namespace host
 }  // namespace pd
 
 using namespace pd;
@@ -309,19 +323,6 @@ size_t pd_paged_tree_decode_fp8_blocks_workspace_bytes(int num_qo_heads, int num
     }
     host::ok();
     return most;
-}
-
-pd_status pd_paged_decode_fp8_blocks(const void* q, const void* k_data, const void* v_data, const float* k_scale,
-                                     const float* v_scale, const int32_t* indices, const int32_t* indptr,
-                                     const int32_t* last_page_len, void* o, float* lse, int batch, int num_qo_heads,
-                                     int num_kv_heads, int head_dim, int page_size, int num_total_pages,
-                                     int num_indices, int block_tokens, float sm_scale, pd_dtype dtype, void* workspace,
-                                     size_t workspace_bytes, void* stream) {
-    if (page_size > 0)
-        if (const pd_status st = host::check_block(block_tokens, page_size); st != PD_OK) return st;
-    return tree_impl(q, k_data, v_data, k_scale, v_scale, indices, indptr, last_page_len, nullptr, nullptr, o, lse, batch,
-                     batch, 0, num_qo_heads, num_kv_heads, head_dim, page_size, num_total_pages, num_indices, sm_scale,
-                     dtype, workspace, workspace_bytes, stream, true, block_tokens, true);
 }
 
 pd_status pd_paged_tree_decode_fp8_blocks(const void* q, const void* k_data, const void* v_data, const float* k_scale,

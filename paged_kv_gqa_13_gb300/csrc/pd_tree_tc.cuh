@@ -57,6 +57,7 @@
 // and the padding of ragged row tiles (64 trees: 134 us, 39% tensor cycles).
 #pragma once
 
+#include "pd_decode_fp8.cuh"
 #include "pd_decode_tc.cuh"
 #include "pd_tree.cuh"
 #include "pd_tree_kernels.h"
@@ -178,15 +179,6 @@ __device__ __forceinline__ void store32(void* p, const uint32_t (&r)[8]) {
     asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(p), "r"(r[0]), "r"(r[1]), "r"(r[2]),
                  "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7])
                  : "memory");
-}
-
-// 4 bytes from global to shared memory, or 4 zero bytes.
-__device__ __forceinline__ void copy4_async(uint32_t dst, const void* src, bool there) {
-    asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(dst), "l"(src), "r"(there ? 4 : 0) : "memory");
-}
-// An arrival (one of the barrier's count) when this thread's cp.async so far have landed.
-__device__ __forceinline__ void copy_arrive(uint32_t bar) {
-    asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(bar) : "memory");
 }
 
 // Block scales of the kKeys tokens of block blk, by a whole warp: K's, then V's, of each quad of tokens (a.run > 1) or

@@ -15,7 +15,8 @@ def _workspace(hq, hk, d, dtype):
     import paged_kv_gqa_13_gb300 as pd
 
     code = pd.PD_F16 if dtype == "f16" else pd.PD_BF16
-    return pd.alloc_workspace(pd.pd_paged_tree_decode_fp8_blocks_workspace_bytes(hq, hk, d, code))
+    return pd.alloc_workspace(max(pd.pd_paged_tree_decode_fp8_blocks_workspace_bytes(hq, hk, d, code),
+                                  pd.pd_paged_decode_fp8_blocks_workspace_bytes(16, hq, hk, d, code)))
 
 
 def _run(c, q, masks=None, sm_scale=None, words=None, single=False, ws=None, table=None, mutate=None):
@@ -105,12 +106,18 @@ def test_long_contexts_cut_and_merged(dtype, hq, hk, d, page, block, kv, new):
     assert int(ws[128:132].view(torch.int32)) == 0
 
 
-def test_one_node_is_the_decode():
-    c = BlockPaged([40, 333, 1, 2000], 2, 128, 16, 16)
-    q = _q(4, 8, 128, "bf16")
+@pytest.mark.parametrize("hq,d", [(8, 128), (2, 128), (8, 64)])
+def test_one_node_is_the_decode(hq, d):
+    """Either kernel of the decode, against the tree decode with one node per request."""
+    c = BlockPaged([40, 333, 1, 2000], 2, d, 16, 16)
+    q = _q(4, hq, d, "bf16")
     _, o, lse = _run(c, q, single=True)
     _, o2, lse2 = _run(c, q)
-    assert torch.equal(o, o2) and torch.equal(lse, lse2)
+    ref = attend_reference(c, q, None, 1 / math.sqrt(d), "bf16")
+    check_attention(o, lse, ref)
+    check_attention(o2, lse2, ref)
+    if hq == 2 or d == 64:  # one kernel for both
+        assert torch.equal(o, o2) and torch.equal(lse, lse2)
 
 
 @pytest.mark.parametrize("dtype", ["f16", "bf16"])

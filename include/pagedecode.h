@@ -629,8 +629,7 @@ pd_status pd_paged_tree_commit(void* k_data, void* v_data, const int32_t* indice
  *   and stride allows it and rot_dim and head_dim are multiples of 16 (f32: 8);
  *   single elements otherwise.
  * pd_paged_norm_rope_append, _fp8: pd_paged_rope_append and its _fp8 form with
- *   the norms in front. Arguments, results and errors as there, but that the q
- *   rows of a request whose new_indptr entries are malformed are not written.
+ *   the norms in front. Arguments, results and errors as there.
  */
 pd_status pd_norm_rope(const void* q, const void* k, const void* q_weight, const void* k_weight, const int32_t* positions,
                        const uint64_t* freqs, void* q_out, void* k_out, int num_tokens, int num_qo_heads,
@@ -670,9 +669,8 @@ pd_status pd_paged_norm_rope_append_fp8(const void* q, const void* k_new, const 
  * past a request's end are not read.
  *
  * pd_paged_rope_append_fp8_blocks: pd_paged_rope_append (its arguments,
- *   results, and errors, with the exception of the q rows that
- *   pd_paged_norm_rope_append names) into such pools, with the norms of
- *   pd_norm_rope in front where eps > 0; eps = 0 leaves them out (q_weight and
+ *   results, and errors) into such pools, with the norms of pd_norm_rope in
+ *   front where eps > 0; eps = 0 leaves them out (q_weight and
  *   k_weight are then NULL). dtype PD_F16 or PD_BF16. Let a be the largest
  *   finite magnitude, after norm and rotation in f32, of the new elements of a
  *   block.

@@ -16,14 +16,14 @@
 // as rows that came together. (A scale of a / 448 anew each time would round
 // older rows by a new factor each time.)
 //
-// One CTA takes a tile: T tokens of a request, T a whole number of blocks,
-// aligned in the cache, so that all rows of a block are in one CTA. It computes
-// the sines of the tile once for all heads (they would cost as much as
-// everything else if every head had its own), then each warp takes whole heads:
-// a group of L lanes holds a row, V elements at two places a lane (a rotated
-// element and its partner), 32 / L rows at once. With block scales a warp goes
-// over a head's rows twice, for the largest magnitudes and for the codes; rows
-// of a tile that fits the registers are loaded once.
+// Rows that pass through (q; k and v too where the pool's scales are given) go token by token, as in pd_rope.cu: a warp
+// takes a token or a slice of its heads, a group of L lanes a head, V elements at two places a lane (a rotated element and
+// its partner), whose sines a lane keeps for all heads.
+//
+// k and v rows into blocks go head by head: a CTA takes a tile of T tokens of a request, T a whole number of blocks,
+// aligned in the cache, so that all rows of a block are in one CTA. It computes the sines of the tile once for all heads,
+// then each warp takes whole heads and goes over their rows twice, for the largest magnitudes and for the codes; rows of a
+// tile that fits the registers are loaded once. Both kinds of work are CTAs of one launch.
 #include <cmath>
 
 #include "pd_host.h"
@@ -39,7 +39,7 @@ enum Pool { kNone, kPlain, kHeadScales, kBlockScales };
 
 constexpr float kTop = 448.f, kEdge = 464.f;  // the largest code; the least magnitude that no longer rounds to it
 constexpr float kLeastScale = 1.17549435e-38f;  // 2^-126: the scale of a block of zeros
-constexpr int kWarps = 8, kThreads = 32 * kWarps;
+constexpr int kWarps = 4, kThreads = 32 * kWarps;
 constexpr int kMaxTile = 64;   // tokens of a tile
 constexpr int kMaxBlocks = 16;  // blocks of a tile
 
@@ -58,7 +58,8 @@ struct NormArgs {
     const uint64_t* freqs;
     float scale;
     int head_dim, rot_dim;
-    int tokens, slices, tile, tiles;
+    int tokens, slices;            // slices of a token's heads
+    int tile, kv_slices, kv_ctas;  // block scales: tokens of a tile, slices of its k and v heads, CTAs that take them
     // the pool and its table
     void* k_data;
     void* v_data;
@@ -95,7 +96,6 @@ struct TileShared {
     long long old_dst;          // of the first old row
     unsigned most[kWarps][kMaxBlocks];  // largest magnitudes of a head's blocks, as the bits of an f32
     float inv[kWarps][kMaxBlocks];      // 1 / scale
-    __align__(16) float weight[2][256];  // of q and of k
 };
 
 // Codes of f[i] * inv.
@@ -115,24 +115,258 @@ __device__ __forceinline__ void store_codes_by(uint8_t* p, const float (&f)[V], 
     }
 }
 
+// Where lanes are in a row of D elements: L lanes to a row (a power of two), units of V elements at e0 and V at e1.
 // kUnits: units of a row per lane (V = 1 has more units than a warp has lanes).
+template <int V, bool kPairs, int kUnits>
+struct Places {
+    int L, rows, lu, lr;  // lanes of a row, rows at once; this lane's place in its row, and its row
+    int e0[kUnits], e1[kUnits];
+    bool on[kUnits];
+    __device__ __forceinline__ Places(int D, int rot, int lane) {
+        const int units = D / (2 * V), rotated = rot / (2 * V);
+        L = 1;
+        while (L < min(units, 32)) L *= 2;
+        rows = 32 / L, lu = lane & (L - 1), lr = lane / L;
+#pragma unroll
+        for (int j = 0; j < kUnits; ++j) {
+            const int u = lu + 32 * j;
+            on[j] = u < units;
+            if (u < rotated) {
+                e0[j] = kPairs && V == 1 ? 2 * u : u * V;
+                e1[j] = kPairs && V == 1 ? 2 * u + 1 : rot / 2 + u * V;
+            } else {
+                e0[j] = rot + (u - rotated) * 2 * V;
+                e1[j] = e0[j] + V;
+            }
+        }
+    }
+};
+
+// The pair that element i of unit u belongs to: (x[i], y[i]) in the half layout; neighbours of x, then of y, in the pairs
+// layout.
+template <int V, bool kPairs>
+__device__ __forceinline__ int pair_of(int u, int i, int rot) {
+    return !kPairs || V == 1 ? u * V + i : i % (V > 1 ? V / 2 : 1) + u * (V / 2) + (2 * i < V ? 0 : rot / 4);
+}
+
+__device__ __forceinline__ float2 turn_of(int pos, uint64_t freq, float scale) {
+    const uint64_t turn = uint64_t(int64_t(pos)) * freq;
+    float sn, cs;
+    // int32 -> f32 rounds the phase by at most 2^-25 of half a turn
+    sincospif(float(int32_t(uint32_t(turn >> 32))) * 4.656612873077393e-10f, &sn, &cs);
+    return make_float2(cs * scale, sn * scale);
+}
+
+// The pairs of x and y turned; turn(i): cos and sin of pair i of the unit.
+template <int V, bool kPairs, class F>
+__device__ __forceinline__ void rotate(float (&x)[V], float (&y)[V], F turn) {
+    float lo[V], hi[V];
+#pragma unroll
+    for (int i = 0; i < V; ++i) {
+        const float2 t = turn(i);
+        if constexpr (kPairs && V > 1) {
+            float(&f)[V] = 2 * i < V ? x : y;
+            float(&o)[V] = 2 * i < V ? lo : hi;
+            o[2 * i % V] = f[2 * i % V] * t.x - f[(2 * i + 1) % V] * t.y;
+            o[(2 * i + 1) % V] = f[(2 * i + 1) % V] * t.x + f[2 * i % V] * t.y;
+        } else {
+            lo[i] = x[i] * t.x - y[i] * t.y;
+            hi[i] = y[i] * t.x + x[i] * t.y;
+        }
+    }
+#pragma unroll
+    for (int i = 0; i < V; ++i) {
+        x[i] = lo[i];
+        y[i] = hi[i];
+    }
+}
+
+// x and y over the root of their row's mean square, times the weights. By all lanes of a row.
+template <int V, int kUnits>
+__device__ __forceinline__ void normalise(float (&x)[kUnits][V], float (&y)[kUnits][V], const float (&w0)[kUnits][V],
+                                          const float (&w1)[kUnits][V], int L, float inv_dim, float eps) {
+    float ss = 0.f;
+#pragma unroll
+    for (int j = 0; j < kUnits; ++j)
+#pragma unroll
+        for (int i = 0; i < V; ++i) ss = fmaf(x[j][i], x[j][i], fmaf(y[j][i], y[j][i], ss));
+    for (int off = 1; off < L; off <<= 1) ss += __shfl_xor_sync(kFull, ss, off);
+    const float by = rsqrtf(fmaf(ss, inv_dim, eps));
+#pragma unroll
+    for (int j = 0; j < kUnits; ++j)
+#pragma unroll
+        for (int i = 0; i < V; ++i) {
+            x[j][i] *= by * w0[j][i];
+            y[j][i] *= by * w1[j][i];
+        }
+}
+
+// Heads that pass through: one warp per (token, slice of its heads).
 template <typename T, int V, bool kPairs, int kPool>
-__global__ void __launch_bounds__(kThreads, 2) norm_rope_kernel(const NormArgs a) {
+__device__ __forceinline__ void token_heads(const NormArgs& a, long long w) {
     constexpr int kUnits = V == 1 ? 4 : 1, kRound = V == 1 ? 2 : 4;
-    extern __shared__ __align__(16) float turns[];  // cos, sin of the tile's rows and pairs
-    __shared__ TileShared sh;
+    const int lane = threadIdx.x & 31;
+    const int t = int(w / a.slices), slice = int(w % a.slices);
+    const int D = a.head_dim, rot = a.rot_dim, rotated = rot / (2 * V);
+    const int items = a.hq + (kPool == kNone ? a.hk : kPool == kBlockScales ? 0 : 2 * a.hk);
+    const int i0 = int((long long)items * slice / a.slices), i1 = int((long long)items * (slice + 1) / a.slices);
+    const bool wants_kv = (kPool == kPlain || kPool == kHeadScales) && i1 > a.hq;
+
+    // ---- where this token's k and v rows go (offset in elements of kv head 0), and its position
+    int pos = 0;
+    bool write_kv = false;
+    size_t dst = 0;
+    const size_t head_step = size_t(a.page_size) * D;
+    if (kPool != kNone && (wants_kv || a.positions == nullptr)) {
+        const int b = request_of(a.new_indptr, a.batch, t, lane);
+        const int s = __ldg(a.new_indptr + b), e = __ldg(a.new_indptr + b + 1);
+        const int lo = __ldg(a.indptr + b), hi = __ldg(a.indptr + b + 1);
+        const int last = __ldg(a.last_page_len + b);
+        int bad = 0;
+        long long at = 0;
+        if (s < 0 || t < s || t >= e || e > a.tokens)
+            bad = kFlagBadNewRows;
+        else if (lo < 0 || hi <= lo || hi > a.num_indices)
+            bad = kFlagBadIndptr;
+        else if (last < 0 || last > a.page_size)
+            bad = kFlagBadLastPageLen;
+        else {
+            const long long kv = ((long long)hi - lo - 1) * a.page_size + last;
+            at = kv - (e - t);  // the request's new rows are its last e - s
+            if (kv < e - s) bad = kFlagBadNewRows;
+        }
+        if (bad == 0) {
+            pos = int(at);
+            if (wants_kv) {
+                const int page = __ldg(a.indices + lo + int(at / a.page_size));
+                if (page < 0 || page >= a.num_total_pages)
+                    bad = kFlagBadPage;
+                else
+                    dst = size_t(page) * a.hk * head_step + size_t(at % a.page_size) * D;
+            }
+        }
+        write_kv = bad == 0;
+        if (bad != 0 && lane == 0) atomicOr(a.flags, bad);
+    }
+    if (a.positions != nullptr) pos = __ldg(a.positions + t);
+
+    const Places<V, kPairs, kUnits> at(D, rot, lane);
+    float2 turns[kUnits][V];
+#pragma unroll
+    for (int j = 0; j < kUnits; ++j) {
+        const int u = at.lu + 32 * j;
+#pragma unroll
+        for (int i = 0; i < V; ++i)
+            turns[j][i] = u < rotated ? turn_of(pos, __ldg(a.freqs + pair_of<V, kPairs>(u, i, rot)), a.scale) : make_float2(1.f, 0.f);
+    }
+    const float inv_dim = 1.f / float(D);
+    // Heads [h0, h1) of one kind: q, k or v.
+    auto run = [&](int h0, int h1, const T* src, const void* weight, auto kind) {
+        constexpr int kKind = decltype(kind)::value;  // 0: q, 1: k, 2: v
+        float w0[kUnits][V], w1[kUnits][V];
+        if constexpr (kKind < 2) {
+            const T* from = static_cast<const T*>(weight);
+#pragma unroll
+            for (int j = 0; j < kUnits; ++j)
+#pragma unroll
+                for (int i = 0; i < V; ++i) {
+                    w0[j][i] = from != nullptr && at.on[j] ? float(from[at.e0[j] + i]) : 1.f;
+                    w1[j][i] = from != nullptr && at.on[j] ? float(from[at.e1[j] + i]) : 1.f;
+                }
+        }
+        for (int h = h0 + at.lr; h - at.lr < h1; h += at.rows * kRound) {
+            Raw<T, V> xs[kRound][kUnits], ys[kRound][kUnits];
+#pragma unroll
+            for (int r = 0; r < kRound; ++r)
+#pragma unroll
+                for (int j = 0; j < kUnits; ++j)
+                    if (h + r * at.rows < h1 && at.on[j]) {
+                        const T* row = src + (long long)(h + r * at.rows) * D;
+                        xs[r][j] = *reinterpret_cast<const Raw<T, V>*>(row + at.e0[j]);
+                        ys[r][j] = *reinterpret_cast<const Raw<T, V>*>(row + at.e1[j]);
+                    }
+#pragma unroll
+            for (int r = 0; r < kRound; ++r) {
+                const int head = h + r * at.rows;
+                if (head - at.lr >= h1) break;  // (the whole warp)
+                const bool there = head < h1;
+                if constexpr (kPool == kPlain && kKind == 2) {  // every bit as it came
+                    T* p = static_cast<T*>(a.v_data) + dst + head * head_step;
+#pragma unroll
+                    for (int j = 0; j < kUnits; ++j)
+                        if (there && at.on[j]) {
+                            *reinterpret_cast<Raw<T, V>*>(p + at.e0[j]) = xs[r][j];
+                            *reinterpret_cast<Raw<T, V>*>(p + at.e1[j]) = ys[r][j];
+                        }
+                } else {
+                    float x[kUnits][V], y[kUnits][V];
+#pragma unroll
+                    for (int j = 0; j < kUnits; ++j) {
+                        if (there && at.on[j]) {
+                            widen<T, V>(xs[r][j], x[j]);
+                            widen<T, V>(ys[r][j], y[j]);
+                        } else {
+#pragma unroll
+                            for (int i = 0; i < V; ++i) x[j][i] = y[j][i] = 0.f;
+                        }
+                    }
+                    if constexpr (kKind < 2) {
+                        if (kPool != kBlockScales || a.eps > 0.f) normalise<V, kUnits>(x, y, w0, w1, at.L, inv_dim, a.eps);
+#pragma unroll
+                        for (int j = 0; j < kUnits; ++j)
+                            if (at.lu + 32 * j < rotated) rotate<V, kPairs>(x[j], y[j], [&](int i) { return turns[j][i]; });
+                    }
+                    if (!there) continue;
+                    if constexpr (kPool == kHeadScales && kKind > 0) {
+                        uint8_t* p = static_cast<uint8_t*>(kKind == 2 ? a.v_data : a.k_data) + dst + head * head_step;
+                        const float scale = __ldg((kKind == 2 ? a.v_scale : a.k_scale) + head);
+#pragma unroll
+                        for (int j = 0; j < kUnits; ++j)
+                            if (at.on[j]) {
+                                store_codes<V>(p + at.e0[j], x[j], scale);
+                                store_codes<V>(p + at.e1[j], y[j], scale);
+                            }
+                    } else {
+                        T* p = kKind == 0       ? static_cast<T*>(a.q_out) + t * a.q_out_stride + (long long)head * D
+                               : kPool == kNone ? static_cast<T*>(a.k_out) + t * a.k_out_stride + (long long)head * D
+                                                : static_cast<T*>(a.k_data) + dst + head * head_step;
+#pragma unroll
+                        for (int j = 0; j < kUnits; ++j)
+                            if (at.on[j]) {
+                                store_elems<T, V>(p + at.e0[j], x[j]);
+                                store_elems<T, V>(p + at.e1[j], y[j]);
+                            }
+                    }
+                }
+            }
+        }
+    };
+    if (i0 < min(i1, a.hq))
+        run(i0, min(i1, a.hq), static_cast<const T*>(a.q) + t * a.q_stride, a.q_weight, std::integral_constant<int, 0>{});
+    if constexpr (kPool != kBlockScales) {
+        if (kPool != kNone && !write_kv) return;
+        const int k0 = max(i0 - a.hq, 0), k1 = min(i1 - a.hq, a.hk);
+        if (k0 < k1) run(k0, k1, static_cast<const T*>(a.k) + t * a.k_stride, a.k_weight, std::integral_constant<int, 1>{});
+    }
+    if constexpr (kPool == kPlain || kPool == kHeadScales) {
+        const int v0 = max(i0 - a.hq - a.hk, 0), v1 = i1 - a.hq - a.hk;
+        if (v0 < v1) run(v0, v1, static_cast<const T*>(a.v) + t * a.v_stride, nullptr, std::integral_constant<int, 2>{});
+    }
+}
+
+// k and v heads of a tile into blocks.
+template <typename T, int V, bool kPairs>
+__device__ __forceinline__ void tile_blocks(const NormArgs& a, float* turns, TileShared& sh) {
+    constexpr int kUnits = V == 1 ? 4 : 1, kRound = V == 1 ? 2 : 4;
     const int tid = threadIdx.x, lane = tid & 31, wid = tid >> 5;
-    const int c = int(blockIdx.x) / a.slices, slice = int(blockIdx.x) - c * a.slices;
+    const int c = int(blockIdx.x) / a.kv_slices, slice = int(blockIdx.x) - c * a.kv_slices;
     const int D = a.head_dim, rot = a.rot_dim, T_ = a.tile;
     const int rotated = rot / (2 * V);  // units that are rotated; the rest follow
 
     // ---- the tile's rows
     if (wid == 0) {
         int count = 0, first = 0, write = 0, old = 0, bad = 0, cache0 = 0, lo = 0;
-        if constexpr (kPool == kNone) {
-            first = c * T_;
-            count = min(T_, a.tokens - first);
-        } else {
+        {
             const int b = request_of_tile(a.new_indptr, a.batch, T_, c, lane);
             const int s = __ldg(a.new_indptr + b), e = __ldg(a.new_indptr + b + 1);
             const int hi = __ldg(a.indptr + b + 1), last = __ldg(a.last_page_len + b);
@@ -160,7 +394,7 @@ __global__ void __launch_bounds__(kThreads, 2) norm_rope_kernel(const NormArgs a
                     first = s + int(t0 - ctx);
                     write = bad == 0;
                     cache0 = int(t0);
-                    if (kPool == kBlockScales && nth == 0) old = int(ctx % a.block);
+                    if (nth == 0) old = int(ctx % a.block);
                 }
             }
         }
@@ -188,301 +422,203 @@ __global__ void __launch_bounds__(kThreads, 2) norm_rope_kernel(const NormArgs a
     }
     __syncthreads();
     const int count = sh.count, first = sh.first;
-    if (count == 0) return;
-    if (a.eps > 0.f) {
-        const T* w[2] = {static_cast<const T*>(a.q_weight), static_cast<const T*>(a.k_weight)};
-        for (int x = tid; x < 2 * D; x += kThreads) {
-            const int of = x >= D, e = x - of * D;
-            sh.weight[of][e] = w[of] != nullptr ? float(w[of][e]) : 1.f;
+    if (count == 0 || !sh.write) return;
+    const Places<V, kPairs, kUnits> at(D, rot, lane);
+    const int steps = (count + at.rows - 1) / at.rows;
+    const bool norm = a.eps > 0.f;
+    const float inv_dim = 1.f / float(D);
+    const size_t head_rows = size_t(a.page_size);  // pool rows between kv heads
+    const int k0 = int((long long)2 * a.hk * slice / a.kv_slices), k1 = int((long long)2 * a.hk * (slice + 1) / a.kv_slices);
+    bool is_v = false;
+    int h = 0;
+    const T* src = nullptr;
+    long long stride = 0;
+    float w0[kUnits][V], w1[kUnits][V];  // the weights at this lane's places
+    Raw<T, V> xs[kRound][kUnits], ys[kRound][kUnits];
+    auto begin = [&](int item) {
+        is_v = item >= a.hk;
+        h = is_v ? item - a.hk : item;
+        src = static_cast<const T*>(is_v ? a.v : a.k);
+        stride = is_v ? a.v_stride : a.k_stride;
+        src += first * stride + (long long)h * D;
+    };
+    auto load = [&](int step0) {
+#pragma unroll
+        for (int r = 0; r < kRound; ++r) {
+            const int row = (step0 + r) * at.rows + at.lr;
+#pragma unroll
+            for (int j = 0; j < kUnits; ++j)
+                if (row < count && at.on[j]) {
+                    xs[r][j] = *reinterpret_cast<const Raw<T, V>*>(src + row * stride + at.e0[j]);
+                    ys[r][j] = *reinterpret_cast<const Raw<T, V>*>(src + row * stride + at.e1[j]);
+                }
         }
+    };
+    // The first head's rows are on their way while the sines are computed.
+    if (k0 + wid < k1) {
+        begin(k0 + wid);
+        load(0);
     }
+#pragma unroll
+    for (int j = 0; j < kUnits; ++j)
+#pragma unroll
+        for (int i = 0; i < V; ++i) {
+            const T* weight = static_cast<const T*>(a.k_weight);
+            w0[j][i] = weight != nullptr && at.on[j] ? float(weight[at.e0[j] + i]) : 1.f;
+            w1[j][i] = weight != nullptr && at.on[j] ? float(weight[at.e1[j] + i]) : 1.f;
+        }
     // ---- cos and sin of every row and pair, in the order in which lanes read them: V / 2 pieces of two pairs per unit
     for (int x = tid; x < count * rotated * V; x += kThreads) {
         const int i = x % V, ru = x / V, r = ru / rotated, u = ru - r * rotated;
-        const int pair = !kPairs || V == 1 ? u * V + i : i % (V > 1 ? V / 2 : 1) + u * (V / 2) + (2 * i < V ? 0 : rot / 4);
-        const uint64_t turn = uint64_t(int64_t(sh.pos[r])) * __ldg(a.freqs + pair);
-        float sn, cs;
-        // int32 -> f32 rounds the phase by at most 2^-25 of half a turn
-        sincospif(float(int32_t(uint32_t(turn >> 32))) * 4.656612873077393e-10f, &sn, &cs);
-        const int at = V == 1 ? ru : ((r * (V / 2 > 0 ? V / 2 : 1) + i / 2) * rotated + u) * 2 + (i & 1);
-        reinterpret_cast<float2*>(turns)[at] = make_float2(cs * a.scale, sn * a.scale);
+        const int place = V == 1 ? ru : ((r * (V / 2 > 0 ? V / 2 : 1) + i / 2) * rotated + u) * 2 + (i & 1);
+        reinterpret_cast<float2*>(turns)[place] = turn_of(sh.pos[r], __ldg(a.freqs + pair_of<V, kPairs>(u, i, rot)), a.scale);
     }
     __syncthreads();
-
-    // ---- heads
-    const int units = D / (2 * V);
-    int L = 1;
-    while (L < min(units, 32)) L *= 2;
-    const int rows_at_once = 32 / L, lu = lane & (L - 1), lr = lane / L;
-    const int steps = (count + rows_at_once - 1) / rows_at_once;
-    const bool norm = a.eps > 0.f;
-    const float inv_dim = 1.f / float(D);
-    int e0[kUnits], e1[kUnits];
-    bool on[kUnits];
+    // The f32 values of a row that was loaded as round r (all lanes call it).
+    auto values = [&](int r, int row, float(&x)[kUnits][V], float(&y)[kUnits][V]) {
+        const bool there = row < count;
 #pragma unroll
-    for (int j = 0; j < kUnits; ++j) {
-        const int u = lu + 32 * j;
-        on[j] = u < units;
-        if (u < rotated) {
-            e0[j] = kPairs && V == 1 ? 2 * u : u * V;
-            e1[j] = kPairs && V == 1 ? 2 * u + 1 : rot / 2 + u * V;
-        } else {
-            e0[j] = rot + (u - rotated) * 2 * V;
-            e1[j] = e0[j] + V;
+        for (int j = 0; j < kUnits; ++j) {
+            if (there && at.on[j]) {
+                widen<T, V>(xs[r][j], x[j]);
+                widen<T, V>(ys[r][j], y[j]);
+            } else {
+#pragma unroll
+                for (int i = 0; i < V; ++i) x[j][i] = y[j][i] = 0.f;
+            }
         }
-    }
-    const int items = a.hq + (kPool == kNone ? a.hk : 2 * a.hk);
-    const int i0 = int((long long)items * slice / a.slices), i1 = int((long long)items * (slice + 1) / a.slices);
-    const size_t head_rows = size_t(a.page_size);  // pool rows between kv heads
-    for (int item = i0 + wid; item < i1; item += kWarps) {
-        const bool is_q = item < a.hq, is_v = item >= a.hq + a.hk;
-        if (kPool != kNone && !is_q && !sh.write) break;  // q heads come first
-        const int h = is_q ? item : is_v ? item - a.hq - a.hk : item - a.hq;
-        const T* src = static_cast<const T*>(is_q ? a.q : is_v ? a.v : a.k);
-        const long long stride = is_q ? a.q_stride : is_v ? a.v_stride : a.k_stride;
-        src += first * stride + (long long)h * D;
-        // the head's weights at this lane's places
-        float w0[kUnits][V], w1[kUnits][V];
-        if (norm && !is_v) {
-            const float* weight = sh.weight[is_q ? 0 : 1];
+        if (is_v) return;
+        if (norm) normalise<V, kUnits>(x, y, w0, w1, at.L, inv_dim, a.eps);
+        if (!there) return;
 #pragma unroll
-            for (int j = 0; j < kUnits; ++j)
-                if (on[j]) {
-#pragma unroll
-                    for (int i = 0; i < V; ++i) {
-                        w0[j][i] = weight[e0[j] + i];
-                        w1[j][i] = weight[e1[j] + i];
+        for (int j = 0; j < kUnits; ++j) {
+            const int u = at.lu + 32 * j;
+            if (u >= rotated) continue;
+            rotate<V, kPairs>(x[j], y[j], [&](int i) {
+                if constexpr (V == 1) return reinterpret_cast<const float2*>(turns)[row * rotated + u];
+                const float4 t = reinterpret_cast<const float4*>(turns)[(row * (V > 1 ? V / 2 : 1) + i / 2) * rotated + u];
+                return i % 2 == 0 ? make_float2(t.x, t.y) : make_float2(t.z, t.w);
+            });
+        }
+    };
+    const int old = sh.old_rows;  // new row r is row old + r of the tile's blocks
+    const int nblk = (old + count + a.block - 1) / a.block;
+    // The scales of a head's blocks from their largest magnitudes, a lane for each block; then its older rows, if the first
+    // one's scale grew.
+    auto settle = [&](unsigned* most_of, float* inv_of) {
+        uint8_t* pool = static_cast<uint8_t*>(is_v ? a.v_data : a.k_data);
+        int grow = 0;  // of the first block, whose older rows it touches
+        if (lane < nblk) {
+            const int r0 = max(0, lane * a.block - old);  // the block's first new row
+            const long long dst = sh.dst[r0];
+            float inv = 0.f;
+            if (dst >= 0) {
+                const long long page = dst / (a.hk * (long long)a.page_size);
+                const int row = int(dst - page * a.hk * a.page_size), per = a.page_size / a.block;
+                float* at = (is_v ? a.v_scale : a.k_scale) + (page * a.hk + h) * per + row / a.block;
+                const float most = __uint_as_float(most_of[lane]);
+                float s;
+                if (lane == 0 && old > 0) {
+                    const float was = fmaxf(*at, kLeastScale);
+                    s = was;
+                    const float limit = kEdge * was;
+                    if (most > limit) {  // (by exponents: the quotient may be past the largest f32)
+                        int em, el;
+                        const float fm = frexpf(most, &em), fl = frexpf(limit, &el);
+                        grow = em - el + (fm > fl ? 1 : 0);
+                        s = scalbnf(was, grow);
                     }
+                    if (s != *at) *at = s;
+                } else {
+                    s = fmaxf(most / kTop, kLeastScale);
+                    *at = s;
                 }
+                inv = 1.f / s;
+            }
+            inv_of[lane] = inv;
         }
-        Raw<T, V> xs[kRound][kUnits], ys[kRound][kUnits];
-        auto load = [&](int step0) {
+        grow = __shfl_sync(kFull, grow, 0);
+        if (grow > 0) {  // the older rows, 8 codes a lane
+            const float by = scalbnf(1.f, -grow);
+            uint8_t* rows = pool + (size_t(sh.dst[0]) - old + h * head_rows) * D;
+            for (int x = lane * 8; x < old * D; x += 256) {
+                float f[8];
+                e4m3x8_to_f32(*reinterpret_cast<const uint2*>(rows + x), f);
+                store_codes_by<8>(rows + x, f, by);
+            }
+        }
+    };
+    auto magnitude = [&](const float(&x)[kUnits][V], const float(&y)[kUnits][V]) {
+        float top = 0.f;
+#pragma unroll
+        for (int j = 0; j < kUnits; ++j)
+#pragma unroll
+            for (int i = 0; i < V; ++i) {
+                const float p = fabsf(x[j][i]), q = fabsf(y[j][i]);
+                top = fmaxf(top, p <= 3.402823466e38f ? p : 0.f);  // infinities and NaN have no say
+                top = fmaxf(top, q <= 3.402823466e38f ? q : 0.f);
+            }
+        for (int off = 1; off < at.L; off <<= 1) top = fmaxf(top, __shfl_xor_sync(kFull, top, off));
+        return top;
+    };
+    auto write = [&](int row, const float(&x)[kUnits][V], const float(&y)[kUnits][V], const float* inv_of) {
+        if (row >= count || sh.dst[row] < 0) return;
+        const float inv = inv_of[(old + row) / a.block];
+        uint8_t* p = static_cast<uint8_t*>(is_v ? a.v_data : a.k_data) + (size_t(sh.dst[row]) + h * head_rows) * D;
+#pragma unroll
+        for (int j = 0; j < kUnits; ++j)
+            if (at.on[j]) {
+                store_codes_by<V>(p + at.e0[j], x[j], inv);
+                store_codes_by<V>(p + at.e1[j], y[j], inv);
+            }
+    };
+    for (int item = k0 + wid; item < k1; item += kWarps) {
+        const bool loaded = item == k0 + wid && steps <= kRound;
+        begin(item);
+        if (lane < kMaxBlocks) sh.most[wid][lane] = 0u;
+        __syncwarp();
+        for (int s0 = 0; s0 < steps; s0 += kRound) {
+            if (!loaded) load(s0);
 #pragma unroll
             for (int r = 0; r < kRound; ++r) {
-                const int row = (step0 + r) * rows_at_once + lr;
-#pragma unroll
-                for (int j = 0; j < kUnits; ++j)
-                    if (row < count && on[j]) {
-                        xs[r][j] = *reinterpret_cast<const Raw<T, V>*>(src + row * stride + e0[j]);
-                        ys[r][j] = *reinterpret_cast<const Raw<T, V>*>(src + row * stride + e1[j]);
-                    }
+                const int row = (s0 + r) * at.rows + at.lr;
+                if (s0 + r >= steps) break;
+                float x[kUnits][V], y[kUnits][V];
+                values(r, row, x, y);
+                const float top = magnitude(x, y);
+                if (at.lu == 0 && row < count) atomicMax(&sh.most[wid][(old + row) / a.block], __float_as_uint(top));
             }
-        };
-        // The f32 values of a row that was loaded as round r (all lanes call it).
-        auto values = [&](int r, int row, float(&x)[kUnits][V], float(&y)[kUnits][V]) {
-            const bool there = row < count;
+        }
+        __syncwarp();
+        settle(sh.most[wid], sh.inv[wid]);
+        __syncwarp();
+        for (int s0 = 0; s0 < steps; s0 += kRound) {
+            if (steps > kRound) load(s0);
 #pragma unroll
-            for (int j = 0; j < kUnits; ++j) {
-                if (there && on[j]) {
-                    widen<T, V>(xs[r][j], x[j]);
-                    widen<T, V>(ys[r][j], y[j]);
-                } else {
-#pragma unroll
-                    for (int i = 0; i < V; ++i) x[j][i] = y[j][i] = 0.f;
-                }
+            for (int r = 0; r < kRound; ++r) {
+                const int row = (s0 + r) * at.rows + at.lr;
+                if (s0 + r >= steps) break;
+                float x[kUnits][V], y[kUnits][V];
+                values(r, row, x, y);
+                write(row, x, y, sh.inv[wid]);
             }
-            if (is_v) return;
-            if (norm) {
-                float ss = 0.f;
-#pragma unroll
-                for (int j = 0; j < kUnits; ++j)
-#pragma unroll
-                    for (int i = 0; i < V; ++i) ss = fmaf(x[j][i], x[j][i], fmaf(y[j][i], y[j][i], ss));
-                for (int off = 1; off < L; off <<= 1) ss += __shfl_xor_sync(kFull, ss, off);
-                const float by = rsqrtf(fmaf(ss, inv_dim, a.eps));
-#pragma unroll
-                for (int j = 0; j < kUnits; ++j)
-#pragma unroll
-                    for (int i = 0; i < V; ++i) {
-                        x[j][i] *= by * w0[j][i];
-                        y[j][i] *= by * w1[j][i];
-                    }
-            }
-            if (!there) return;
-#pragma unroll
-            for (int j = 0; j < kUnits; ++j) {
-                const int u = lu + 32 * j;
-                if (u >= rotated) continue;
-                if constexpr (V == 1) {
-                    const float2 t = reinterpret_cast<const float2*>(turns)[row * rotated + u];
-                    const float p = x[j][0], q = y[j][0];
-                    x[j][0] = p * t.x - q * t.y;
-                    y[j][0] = q * t.x + p * t.y;
-                } else {
-                    float lo[V], hi[V];
-#pragma unroll
-                    for (int i = 0; i < V; i += 2) {
-                        const float4 t = reinterpret_cast<const float4*>(turns)[(row * (V / 2) + i / 2) * rotated + u];
-#pragma unroll
-                        for (int n = i; n < i + 2; ++n) {
-                            const float cs = n == i ? t.x : t.z, sn = n == i ? t.y : t.w;
-                            // pair n: (x[n], y[n]) in the half layout; neighbours of x, then of y, in the pairs layout
-                            if constexpr (kPairs) {
-                                float(&f)[V] = 2 * n < V ? x[j] : y[j];
-                                float(&o)[V] = 2 * n < V ? lo : hi;
-                                o[2 * n % V] = f[2 * n % V] * cs - f[(2 * n + 1) % V] * sn;
-                                o[(2 * n + 1) % V] = f[(2 * n + 1) % V] * cs + f[2 * n % V] * sn;
-                            } else {
-                                lo[n] = x[j][n] * cs - y[j][n] * sn;
-                                hi[n] = y[j][n] * cs + x[j][n] * sn;
-                            }
-                        }
-                    }
-#pragma unroll
-                    for (int i = 0; i < V; ++i) {
-                        x[j][i] = lo[i];
-                        y[j][i] = hi[i];
-                    }
-                }
-            }
-        };
-        if (kPool != kBlockScales || is_q) {
-            const bool to_pool = kPool != kNone && !is_q;
-            T* out = static_cast<T*>(is_q ? a.q_out : a.k_out);
-            const long long out_stride = is_q ? a.q_out_stride : a.k_out_stride;
-            float head_scale = 1.f;
-            if (kPool == kHeadScales && to_pool) head_scale = __ldg((is_v ? a.v_scale : a.k_scale) + h);
-            for (int s0 = 0; s0 < steps; s0 += kRound) {
-                load(s0);
-#pragma unroll
-                for (int r = 0; r < kRound; ++r) {
-                    const int row = (s0 + r) * rows_at_once + lr;
-                    if (s0 + r >= steps) break;
-                    if (kPool == kPlain && is_v) {  // every bit as it came
-                        if (row < count && sh.dst[row] >= 0) {
-                            T* p = static_cast<T*>(a.v_data) + (size_t(sh.dst[row]) + h * head_rows) * D;
-#pragma unroll
-                            for (int j = 0; j < kUnits; ++j)
-                                if (on[j]) {
-                                    *reinterpret_cast<Raw<T, V>*>(p + e0[j]) = xs[r][j];
-                                    *reinterpret_cast<Raw<T, V>*>(p + e1[j]) = ys[r][j];
-                                }
-                        }
-                        continue;
-                    }
-                    float x[kUnits][V], y[kUnits][V];
-                    values(r, row, x, y);
-                    if (row >= count) continue;
-                    if (!to_pool) {
-                        T* p = out + (first + row) * out_stride + (long long)h * D;
-#pragma unroll
-                        for (int j = 0; j < kUnits; ++j)
-                            if (on[j]) {
-                                store_elems<T, V>(p + e0[j], x[j]);
-                                store_elems<T, V>(p + e1[j], y[j]);
-                            }
-                    } else if (sh.dst[row] >= 0) {
-                        const size_t at = (size_t(sh.dst[row]) + h * head_rows) * D;
-#pragma unroll
-                        for (int j = 0; j < kUnits; ++j)
-                            if (on[j]) {
-                                if constexpr (kPool == kHeadScales) {
-                                    uint8_t* p = static_cast<uint8_t*>(is_v ? a.v_data : a.k_data) + at;
-                                    store_codes<V>(p + e0[j], x[j], head_scale);
-                                    store_codes<V>(p + e1[j], y[j], head_scale);
-                                } else {
-                                    T* p = static_cast<T*>(a.k_data) + at;
-                                    store_elems<T, V>(p + e0[j], x[j]);
-                                    store_elems<T, V>(p + e1[j], y[j]);
-                                }
-                            }
-                    }
-                }
-            }
-        } else if constexpr (kPool == kBlockScales) {
-            const int old = sh.old_rows;  // new row r is row old + r of the tile's blocks
-            const int nblk = (old + count + a.block - 1) / a.block;
-            if (lane < nblk) sh.most[wid][lane] = 0u;
-            __syncwarp();
-            // ---- largest magnitudes
-            for (int s0 = 0; s0 < steps; s0 += kRound) {
-                load(s0);
-#pragma unroll
-                for (int r = 0; r < kRound; ++r) {
-                    const int row = (s0 + r) * rows_at_once + lr;
-                    if (s0 + r >= steps) break;
-                    float x[kUnits][V], y[kUnits][V];
-                    values(r, row, x, y);
-                    float top = 0.f;
-#pragma unroll
-                    for (int j = 0; j < kUnits; ++j)
-#pragma unroll
-                        for (int i = 0; i < V; ++i) {
-                            const float p = fabsf(x[j][i]), q = fabsf(y[j][i]);
-                            top = fmaxf(top, p <= 3.402823466e38f ? p : 0.f);  // infinities and NaN have no say
-                            top = fmaxf(top, q <= 3.402823466e38f ? q : 0.f);
-                        }
-                    for (int off = 1; off < L; off <<= 1) top = fmaxf(top, __shfl_xor_sync(kFull, top, off));
-                    if (lu == 0 && row < count) atomicMax(&sh.most[wid][(old + row) / a.block], __float_as_uint(top));
-                }
-            }
-            __syncwarp();
-            // ---- scales; a lane for each block
-            uint8_t* pool = static_cast<uint8_t*>(is_v ? a.v_data : a.k_data);
-            int grow = 0;  // of the first block, whose older rows it touches
-            if (lane < nblk) {
-                const int r0 = max(0, lane * a.block - old);  // the block's first new row
-                const long long dst = sh.dst[r0];
-                float inv = 0.f;
-                if (dst >= 0) {
-                    const long long page = dst / (a.hk * (long long)a.page_size);
-                    const int row = int(dst - page * a.hk * a.page_size), per = a.page_size / a.block;
-                    float* at = (is_v ? a.v_scale : a.k_scale) + (page * a.hk + h) * per + row / a.block;
-                    const float most = __uint_as_float(sh.most[wid][lane]);
-                    float s;
-                    if (lane == 0 && old > 0) {
-                        const float was = fmaxf(*at, kLeastScale);
-                        s = was;
-                        const float limit = kEdge * was;
-                        if (most > limit) {  // (by exponents: the quotient may be past the largest f32)
-                            int em, el;
-                            const float fm = frexpf(most, &em), fl = frexpf(limit, &el);
-                            grow = em - el + (fm > fl ? 1 : 0);
-                            s = scalbnf(was, grow);
-                        }
-                        if (s != *at) *at = s;
-                    } else {
-                        s = fmaxf(most / kTop, kLeastScale);
-                        *at = s;
-                    }
-                    inv = 1.f / s;
-                }
-                sh.inv[wid][lane] = inv;
-            }
-            grow = __shfl_sync(kFull, grow, 0);
-            __syncwarp();
-            if (grow > 0) {  // the older rows, 8 codes a lane
-                const float by = scalbnf(1.f, -grow);
-                uint8_t* rows = pool + (size_t(sh.dst[0]) - old + h * head_rows) * D;
-                for (int x = lane * 8; x < old * D; x += 256) {
-                    float f[8];
-                    e4m3x8_to_f32(*reinterpret_cast<const uint2*>(rows + x), f);
-                    store_codes_by<8>(rows + x, f, by);
-                }
-            }
-            // ---- codes
-            for (int s0 = 0; s0 < steps; s0 += kRound) {
-                if (steps > kRound) load(s0);
-#pragma unroll
-                for (int r = 0; r < kRound; ++r) {
-                    const int row = (s0 + r) * rows_at_once + lr;
-                    if (s0 + r >= steps) break;
-                    float x[kUnits][V], y[kUnits][V];
-                    values(r, row, x, y);
-                    if (row >= count || sh.dst[row] < 0) continue;
-                    const float inv = sh.inv[wid][(old + row) / a.block];
-                    uint8_t* p = pool + (size_t(sh.dst[row]) + h * head_rows) * D;
-#pragma unroll
-                    for (int j = 0; j < kUnits; ++j)
-                        if (on[j]) {
-                            store_codes_by<V>(p + e0[j], x[j], inv);
-                            store_codes_by<V>(p + e1[j], y[j], inv);
-                        }
-                }
-            }
-            __syncwarp();  // the next head uses the same places
+        }
+        __syncwarp();  // the next head uses the same places
+    }
+}
+
+template <typename T, int V, bool kPairs, int kPool>
+__global__ void __launch_bounds__(kThreads, kPool == kBlockScales ? 4 : 5) norm_rope_kernel(const NormArgs a) {
+    if constexpr (kPool == kBlockScales) {
+        extern __shared__ __align__(16) float turns[];  // cos, sin of the tile's rows and pairs
+        __shared__ TileShared sh;
+        if (int(blockIdx.x) < a.kv_ctas) {
+            tile_blocks<T, V, kPairs>(a, turns, sh);
+            return;
         }
     }
+    const long long w = (long long)(int(blockIdx.x) - a.kv_ctas) * kWarps + (threadIdx.x >> 5);
+    if (w < (long long)a.tokens * a.slices) token_heads<T, V, kPairs, kPool>(a, w);
 }
 
 template <typename T, int V, bool kPairs>
@@ -514,19 +650,33 @@ pd_status launch(NormArgs& a, pd_dtype dt, Pool pool, int layout, cudaStream_t s
     int sms = 0;
     pd_status st = host::sm_count(&sms);
     if (st != PD_OK) return st;
-    a.tile = pool == kBlockScales ? a.block * (a.block < 16 ? 16 / a.block : 1) : 16;
-    const long long tiles = pool == kNone ? ((long long)a.tokens + a.tile - 1) / a.tile : (long long)a.tokens / a.tile + 2ll * a.batch;
-    const int items = a.hq + (pool == kNone ? a.hk : 2 * a.hk);
-    const long long want = ((long long)sms * 8 + tiles - 1) / tiles, most = (items + kWarps - 1) / kWarps;
-    a.slices = int(want < 1 ? 1 : want > most ? most : want);
-    if (tiles * a.slices > 0x7fffffff) return host::fail(PD_ERR_INVALID, "batch and the number of tokens are too large");
-    const int smem = (a.tile * a.rot_dim / 2) * 8;
+    // Few tokens: a token's heads in slices, so that the card has about 8 warps per SM (see pd_rope.cu).
+    const int items = a.hq + (pool == kNone ? a.hk : pool == kBlockScales ? 0 : 2 * a.hk);
+    const long long want = ((long long)sms * 8 + a.tokens - 1) / a.tokens, most = (items + 3) / 4;
+    a.slices = int(want < 1 || most < 1 ? 1 : want > most ? most : want);
+    const long long warps = items > 0 ? (long long)a.tokens * a.slices : 0;
+    // Tiles: their k and v heads in slices of whole rounds of a CTA's warps, for about 4 CTAs per SM.
+    long long kv = 0;
+    int smem = 0;
+    if (pool == kBlockScales) {
+        a.tile = a.block * (a.block < 16 ? 16 / a.block : 1);
+        const long long tiles = (long long)a.tokens / a.tile + 2ll * a.batch, rounds = (2ll * a.hk + kWarps - 1) / kWarps;
+        const long long cut = ((long long)sms * 4 + tiles - 1) / tiles;
+        long long each = cut >= rounds ? 1 : (rounds + cut - 1) / cut;  // rounds of a slice
+        while (rounds % each != 0) ++each;
+        a.kv_slices = int(rounds / each);
+        kv = tiles * a.kv_slices;
+        smem = a.tile * a.rot_dim / 2 * 8;
+    }
+    const long long ctas = kv + (warps + kWarps - 1) / kWarps;
+    if (ctas > 0x7fffffff) return host::fail(PD_ERR_INVALID, "batch and the number of tokens are too large");
+    a.kv_ctas = int(kv);
     const void* fn = dt == PD_F32   ? pick<float>(pool, layout, wide)
                      : dt == PD_F16 ? pick<__half>(pool, layout, wide)
                                     : pick<__nv_bfloat16>(pool, layout, wide);
     if (smem > 40 * 1024 && (st = host::allow_smem(fn, smem)) != PD_OK) return st;
     void* args[] = {&a};
-    const cudaError_t e = cudaLaunchKernel(fn, dim3(unsigned(tiles * a.slices)), dim3(kThreads), args, size_t(smem), stream);
+    const cudaError_t e = cudaLaunchKernel(fn, dim3(unsigned(ctas)), dim3(kThreads), args, size_t(smem), stream);
     return e == cudaSuccess ? host::ok() : host::cuda_fail(e, "norm and rotation launch");
 }
 

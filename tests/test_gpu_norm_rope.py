@@ -202,8 +202,8 @@ def test_bad_tables_are_flagged_and_nothing_is_written():
     flags, k, v, qo = run(last=[17, c.last[1], c.last[2]])
     assert flags == pd.PD_FLAG_BAD_LAST_PAGE_LEN
     unchanged(k, v, [0])
-    flags, k, v, qo = run(new_indptr=[0, 4, 24, 26])  # fewer rows than tensors hold: request 2 has 2
-    assert flags == 0
+    flags, k, v, qo = run(new_indptr=[0, 4, 24, 26])  # the last row is no request's: flagged, as by pd_paged_rope_append
+    assert flags == pd.PD_FLAG_BAD_NEW_ROWS
     flags, k, v, qo = run(new_indptr=[0, 24, 4, 27])
     assert flags & pd.PD_FLAG_BAD_NEW_ROWS
     flags, k, v, qo = run(new_indptr=[0, 4, 24, 1000])

@@ -31,14 +31,27 @@ struct ReadArgs {
     int* flags;
 };
 
-template <typename T>
+// 16 elements, in stores of whole 32-byte sectors where the rows lie so: a warp's 16-byte stores, two to a sector and 32
+// bytes apart, take 68 us where these take 58 (16 requests, 97,000 tokens of 8 heads of 128 to bf16).
+template <bool kSectors, typename T>
 __device__ __forceinline__ void store16(T* p, const float (&f)[16]) {
     constexpr int kVec = Elt<T>::kVec;
 #pragma unroll
-    for (int i = 0; i < 16; i += kVec) *reinterpret_cast<uint4*>(p + i) = Elt<T>::from_f32(f + i);
+    for (int i = 0; i < 16; i += 2 * kVec) {
+        const uint4 x = Elt<T>::from_f32(f + i), y = Elt<T>::from_f32(f + i + kVec);
+        if constexpr (kSectors) {
+            asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(p + i), "r"(x.x), "r"(x.y), "r"(x.z),
+                         "r"(x.w), "r"(y.x), "r"(y.y), "r"(y.z), "r"(y.w)
+                         : "memory");
+        } else {
+            *reinterpret_cast<uint4*>(p + i) = x;
+            *reinterpret_cast<uint4*>(p + i + kVec) = y;
+        }
+    }
 }
 
-template <typename T, int D>
+// kSectors: k_out and v_out are 32-byte aligned
+template <typename T, int D, bool kSectors>
 __global__ void __launch_bounds__(kThreads) blocks_read_kernel(const ReadArgs a) {
     constexpr int kPieces = D / 16, kAhead = 4;  // 16-byte pieces of a row; loads in flight
     __shared__ int s_count, s_first;
@@ -124,16 +137,23 @@ __global__ void __launch_bounds__(kThreads) blocks_read_kernel(const ReadArgs a)
             e4m3x8_to_f32(make_uint2(w[j].z, w[j].w), f + 8);
 #pragma unroll
             for (int x = 0; x < 16; ++x) f[x] *= s[j];
-            store16<T>(to[j], f);
+            store16<kSectors>(to[j], f);
         }
     }
 }
 
-template <typename T>
+template <typename T, bool kSectors>
 const void* by_dim(int D) {
-    return D == 64    ? reinterpret_cast<const void*>(blocks_read_kernel<T, 64>)
-           : D == 128 ? reinterpret_cast<const void*>(blocks_read_kernel<T, 128>)
-                      : reinterpret_cast<const void*>(blocks_read_kernel<T, 256>);
+    return D == 64    ? reinterpret_cast<const void*>(blocks_read_kernel<T, 64, kSectors>)
+           : D == 128 ? reinterpret_cast<const void*>(blocks_read_kernel<T, 128, kSectors>)
+                      : reinterpret_cast<const void*>(blocks_read_kernel<T, 256, kSectors>);
+}
+
+template <bool kSectors>
+const void* by_type(pd_dtype dtype, int D) {
+    return dtype == PD_F32   ? by_dim<float, kSectors>(D)
+           : dtype == PD_F16 ? by_dim<__half, kSectors>(D)
+                             : by_dim<__nv_bfloat16, kSectors>(D);
 }
 
 }  // namespace
@@ -177,7 +197,8 @@ pd_status pd_paged_read_fp8_blocks(const void* k_data, const void* v_data, const
                last_page_len, out_indptr, first, k_out, v_out, batch, total, num_kv_heads, page_size, num_total_pages,
                num_indices, block_tokens, int(want > num_kv_heads ? num_kv_heads : want), static_cast<int*>(workspace)};
     if (tiles * a.slices > 0x7fffffff) return host::fail(PD_ERR_INVALID, "batch and the number of tokens are too large");
-    const void* fn = dtype == PD_F32 ? by_dim<float>(head_dim) : dtype == PD_F16 ? by_dim<__half>(head_dim) : by_dim<__nv_bfloat16>(head_dim);
+    const bool sectors = host::aligned(k_out, 32) && host::aligned(v_out, 32);
+    const void* fn = sectors ? by_type<true>(dtype, head_dim) : by_type<false>(dtype, head_dim);
     void* args[] = {&a};
     const cudaError_t e = cudaLaunchKernel(fn, dim3(unsigned(tiles * a.slices)), dim3(kThreads), args, 0, static_cast<cudaStream_t>(stream));
     return e == cudaSuccess ? host::ok() : host::cuda_fail(e, "block-scaled read launch");

@@ -340,3 +340,23 @@ def test_append_then_read_in_one_graph():
         # half a step of the code and of bf16; half a step of a subnormal code at scales below 1 / 8
         tol = (2.0 ** -4 + 2.0 ** -8) * new.float().abs() + 2.0 ** -13
         assert bool(((y.float() - new.float()).abs() <= tol).all())
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+def test_read_into_rows_that_lie_16_bytes_off_a_sector(dtype):
+    import paged_kv_gqa_13_gb300 as pd
+
+    c = BlockPaged([37, 64], 2, 64, 16, 16, seed=5)
+    ptr = torch.tensor([0, 37, 101], dtype=torch.int32, device="cuda")
+    out, off = [], []
+    for shift in (0, 16):
+        for _ in range(2):
+            n = shift // TYPES[dtype].itemsize
+            (off if shift else out).append(torch.zeros(101 * 2 * 64 + n, dtype=TYPES[dtype], device="cuda")[n:].view(101, 2, 64))
+    assert all(x.data_ptr() % 32 == 16 for x in off)
+    ws = pd.alloc_workspace(256)
+    k, v, ks, vs = c.pools()
+    for to in (out, off):
+        pd.pd_paged_read_fp8_blocks(k, v, ks, vs, *c.table(), ptr, None, *to, ws)
+    assert pd.pd_read_device_flags(ws) == 0
+    assert torch.equal(out[0], off[0]) and torch.equal(out[1], off[1])

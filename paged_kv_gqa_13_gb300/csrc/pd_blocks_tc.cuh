@@ -5,8 +5,8 @@
 // A code is never widened. The pool is the A operand of both products: per tile
 // of 128 tokens S^T[128 tokens][R rows] = K Q^T (A = K as it lies, K-major), and
 // O^T[head_dim][R] += V^T P^T (A = V as it lies, MN-major). Rows (nodes x q heads
-// of one kv head) are the N of the products, 16, 32 or 64 of them, so that few
-// rows cost few products, and a token is a lane of tensor memory: its two scales
+// of one kv head) are the N of the products, 16 or 32 of them, so that no
+// column is spent on rows that are not there, and a token is a lane of tensor memory: its two scales
 // are one register each of the thread that owns it,
 //
 //   x_r = S_r * k_scale * c_r          e_r = 2^(x_r - m_r)          p_r = e_r * v_scale
@@ -32,10 +32,9 @@
 //
 // Lines, segments, ranges, tails and the merge are those of the tree decode
 // (pd_tree.cuh, pd_tree_tc.cuh), with blocks of 128 tokens and a ring of K and V
-// slots for each line. Roles of a line: softmax warps (four for each 32 rows; a
-// thread owns a token), an mma warp, producers (TMA copies of the codes, cp.async
-// of the scales), and a warp that walks the segments and writes the parts of a
-// segment's q ahead of time.
+// slots for each line. Roles of a line: four softmax warps (a thread owns a token),
+// an mma warp, producers (TMA copies of the codes, cp.async of the scales), and a
+// warp that walks the segments and writes the parts of a segment's q ahead of time.
 //
 // Whoever waits on a barrier takes part in its next phase, or waits for a load
 // whose slot cannot be filled again before it has given its weights.
@@ -91,19 +90,18 @@ __device__ __forceinline__ __half2 codes_half2(uint32_t w) {
 template <int D, int R, int kQParts>
 struct CfgBlocks {
     static constexpr int kKeys = 128;                     // tokens of a tile, the M of S^T
-    static constexpr int kWgs = R > 32 ? R / 32 : 1;      // softmax warpgroups of a line
-    static constexpr int kCols = R > 32 ? 32 : R;         // rows of a warpgroup
-    static constexpr int kLines = R <= 32 && D <= 128 ? 2 : 1;
+    static_assert(R == 16 || R == 32, "rows of a segment");
+    static constexpr int kLines = D <= 128 ? 2 : 1;
     static constexpr int kRowBytes = D < 128 ? D : 128;   // of a column block of codes
     static constexpr int kColBlocks = D / kRowBytes;
     static constexpr int kMode = kRowBytes == 128 ? 2 : 4;
     static constexpr int kSlotBytes = kKeys * D;
     static constexpr int kQRows = kQParts * R, kQBytes = kQRows * D;  // part p of row r is row p R + r
-    static constexpr int kQBufs = R == 64 && D == 256 ? 1 : 2;
+    static constexpr int kQBufs = 2;
     static constexpr int kPPart = kKeys * R, kPBytes = 2 * kPPart, kPBufs = 2;
     static constexpr int kProducers = kLines == 2 ? 2 : 4;
     static constexpr int kOthers = 2 + kProducers;        // mma, producers, walker
-    static constexpr int kSoftWarps = 4 * kWgs;           // of a line
+    static constexpr int kSoftWarps = 4;                  // of a line
     static constexpr int kThreads = 32 * kLines * (kSoftWarps + kOthers);
     static constexpr int kWalkers = 1 + kProducers + kSoftWarps;  // warps that read a line's segments
     static constexpr int kSegRing = 8, kBadRing = 16, kMaxSlots = 10;
@@ -111,16 +109,16 @@ struct CfgBlocks {
     // a line's barriers (8 bytes each)
     static constexpr int kFull = 0, kEmpty = kFull + kMaxSlots, kScFull = kEmpty + kMaxSlots, kQFull = kScFull + kScales,
                          kQEmpty = kQFull + 2, kSFull = kQEmpty + 2, kPFull = kSFull + 2, kPvDone = kPFull + 2,
-                         kVote = kPvDone + 2, kSegFull = kVote + kWgs, kSegFree = kSegFull + kSegRing,
+                         kVote = kPvDone + 2, kSegFull = kVote + 1, kSegFree = kSegFull + kSegRing,
                          kAllDone = kSegFree + kSegRing, kBars = kAllDone + 1;
     // a line's small shared memory
     static constexpr int kRowcOff = round_up(kBars * 8, 16);              // [kQBufs][R] score scale of a row
     static constexpr int kRowAtOff = kRowcOff + kQBufs * R * 4;           // [kQBufs][R] its q row, -1: none
     static constexpr int kNodeOff = kRowAtOff + kQBufs * R * 8;           // [kQBufs][R] its node
-    static constexpr int kWarpOff = round_up(kNodeOff + kQBufs * R * 4, 16);  // per softmax warp: c, -m, a factor, a rise [kCols] each
-    static constexpr int kRedOff = kWarpOff + kSoftWarps * 4 * kCols * 4;     // [warp][kCols] exchanged maxima, sums
-    static constexpr int kVoteOff = kRedOff + kSoftWarps * kCols * 4;         // [kWgs][2]
-    static constexpr int kTagOff = kVoteOff + kWgs * 2 * 4;                   // [2] segment with non-finite V
+    static constexpr int kWarpOff = round_up(kNodeOff + kQBufs * R * 4, 16);  // per softmax warp: c, -m, a factor, a rise [R] each
+    static constexpr int kRedOff = kWarpOff + kSoftWarps * 4 * R * 4;     // [maxima, sums][warp][R]
+    static constexpr int kVoteOff = kRedOff + 2 * kSoftWarps * R * 4;     // [2]
+    static constexpr int kTagOff = kVoteOff + 2 * 4;                          // [2] segment with non-finite V
     static constexpr int kBadOff = kTagOff + 2 * 4;
     static constexpr int kProgressOff = kBadOff + kBadRing * 4;
     static constexpr int kSegOff = round_up(kProgressOff + 4, 8);
@@ -196,7 +194,7 @@ __global__ void __launch_bounds__(CfgBlocks<D, R, sizeof(T) == 2 && std::is_same
                 mbar_init(bar(C::kPvDone + i), 1);
                 tag[i] = 0;
             }
-            for (int i = 0; i < C::kWgs; ++i) mbar_init(bar(C::kVote + i), 4);
+            mbar_init(bar(C::kVote), C::kSoftWarps);
             for (int i = 0; i < C::kSegRing; ++i) {
                 mbar_init(bar(C::kSegFull + i), 1);
                 mbar_init(bar(C::kSegFree + i), C::kWalkers);
@@ -204,7 +202,7 @@ __global__ void __launch_bounds__(CfgBlocks<D, R, sizeof(T) == 2 && std::is_same
             mbar_init(bar(C::kAllDone), 1);
             fence_mbar_init();
             int* votes = reinterpret_cast<int*>(ctl + C::kVoteOff);
-            for (int i = 0; i < 2 * C::kWgs; ++i) votes[i] = 0;
+            votes[0] = votes[1] = 0;
             *progress = 0;
             *abort_flag = 0;
         }
@@ -534,22 +532,24 @@ __global__ void __launch_bounds__(CfgBlocks<D, R, sizeof(T) == 2 && std::is_same
         }
     } else {
         // ================================================================ softmax: a thread owns a token of every tile
-        const int sw = wid % C::kSoftWarps, wg = sw / 4, quad = wid & 3, tok = 32 * quad + lane, col0 = wg * C::kCols;
+        const int quad = wid & 3, tok = 32 * quad + lane;
         const uint32_t lanes = uint32_t(32 * quad) << 16;
-        const uint32_t ts0 = tmem + lanes + col0, to = tmem + lanes + C::kOCol + col0;
-        float* wc = reinterpret_cast<float*>(ctl + C::kWarpOff) + sw * 4 * C::kCols;  // c of this warp's rows
-        float* wm = wc + C::kCols;                                                      // kShift - m
-        float* wf = wm + C::kCols;                                                      // a factor
-        float* wd = wf + C::kCols;                                                      // what wm rose by
-        float* red = reinterpret_cast<float*>(ctl + C::kRedOff) + wg * 4 * C::kCols;
-        volatile int* votes = reinterpret_cast<volatile int*>(ctl + C::kVoteOff) + 2 * wg;
-        const int vote_bar = C::kVote + wg;
+        const uint32_t ts0 = tmem + lanes, to = tmem + lanes + C::kOCol;
+        float* wc = reinterpret_cast<float*>(ctl + C::kWarpOff) + quad * 4 * R;  // c of this warp's rows
+        float* wm = wc + R;                                                      // kShift - m
+        float* wf = wm + R;                                                      // a factor
+        float* wd = wf + R;                                                      // what wm rose by
+        // Exchanged maxima and, apart from them, sums: a segment's first maxima are written while a slow warp may still be
+        // reading the sums of the segment before.
+        float* red = reinterpret_cast<float*>(ctl + C::kRedOff);
+        float* sums = red + 4 * R;
+        volatile int* votes = reinterpret_cast<volatile int*>(ctl + C::kVoteOff);
         int exchanges = 0;
-        // All four warps of the warpgroup have come here, with what their lanes wrote.
+        // All four warps of the line have come here, with what their lanes wrote.
         auto exchange = [&]() -> bool {
             __syncwarp();
-            if (lane == 0) mbar_arrive(bar(vote_bar));
-            const bool got = wait(vote_bar, uint32_t(exchanges) & 1u);
+            if (lane == 0) mbar_arrive(bar(C::kVote));
+            const bool got = wait(C::kVote, uint32_t(exchanges) & 1u);
             ++exchanges;
             return got;
         };
@@ -564,267 +564,263 @@ __global__ void __launch_bounds__(CfgBlocks<D, R, sizeof(T) == 2 && std::is_same
             const int blk0 = s.blk0, blk1 = s.blk1, tail0 = s.tail0;
             if (blk0 == blk1) break;
             const TreeReq r = s.req();
-            const int qb = q_buf(seg), cols = min(C::kCols, s.nodes * a.hpt - col0);  // this warpgroup's rows
+            const int qb = q_buf(seg), cols = min(R, s.nodes * a.hpt);  // rows
             if (!(ok = wait(C::kQFull + qb, q_phase(seg)))) break;
             __syncwarp();
-            if (cols > 0 && lane < C::kCols) {
-                wc[lane] = lane < ((cols + 7) & ~7) ? rowc[qb * R + col0 + lane] : 0.f;
+            if (lane < R) {
+                wc[lane] = lane < ((cols + 7) & ~7) ? rowc[qb * R + lane] : 0.f;
                 wm[lane] = 0.f;
             }
             __syncwarp();
             float m = kNegInf;  // lane: the running maximum of row `lane`
-            float l[C::kCols];
+            float l[R];
 #pragma unroll
-            for (int c = 0; c < C::kCols; ++c) l[c] = 0.f;
+            for (int c = 0; c < R; ++c) l[c] = 0.f;
             for (int blk = blk0; blk < blk1; ++blk, ++jobs, sc.next(), ring.next(), ring.next()) {
                 const int buf = jobs & 1, pbuf = jobs % C::kPBufs;
                 if (!(ok = wait(C::kSFull + buf, uint32_t(jobs >> 1) & 1u))) break;
-                if (cols > 0) {
-                    tc_fence_after();
-                    float x[C::kCols], part[16], last[16];
-                    auto load_parts = [&](int c) {
-                        const uint32_t at = ts0 + buf * C::kQRows + c;
-                        tmem_ld16(at, *reinterpret_cast<uint32_t(*)[16]>(x + c));
-                        tmem_ld16(at + R, *reinterpret_cast<uint32_t(*)[16]>(part));
-                        if (kQParts > 2) tmem_ld16(at + 2 * R, *reinterpret_cast<uint32_t(*)[16]>(last));
-                    };
-                    load_parts(0);
-                    if (sw == 0 && lane == 0) mbar_arrive(bar(C::kEmpty + ring.slot));  // S is there: K has been read
-                    if (!(ok = wait(C::kScFull + sc.slot, sc.phase))) break;
-                    const float* sk = scales + sc.slot * 2 * C::kKeys;
-                    const int sat = a.run > 1 ? tok >> 2 : tok;
-                    const float ks = sk[sat], vs = sk[C::kKeys + sat];
-                    const float lv = log2f(fmaxf(vs, kLeastV));
-                    const unsigned bad_pages = bad_slots[jobs % C::kBadRing];
-                    // the sums of the parts, the smallest first
+                tc_fence_after();
+                float x[R], part[16], last[16];
+                auto load_parts = [&](int c) {
+                    const uint32_t at = ts0 + buf * C::kQRows + c;
+                    tmem_ld16(at, *reinterpret_cast<uint32_t(*)[16]>(x + c));
+                    tmem_ld16(at + R, *reinterpret_cast<uint32_t(*)[16]>(part));
+                    if (kQParts > 2) tmem_ld16(at + 2 * R, *reinterpret_cast<uint32_t(*)[16]>(last));
+                };
+                load_parts(0);
+                if (quad == 0 && lane == 0) mbar_arrive(bar(C::kEmpty + ring.slot));  // S is there: K has been read
+                if (!(ok = wait(C::kScFull + sc.slot, sc.phase))) break;
+                const float* sk = scales + sc.slot * 2 * C::kKeys;
+                const int sat = a.run > 1 ? tok >> 2 : tok;
+                const float ks = sk[sat], vs = sk[C::kKeys + sat];
+                const float lv = log2f(fmaxf(vs, kLeastV));
+                const unsigned bad_pages = bad_slots[jobs % C::kBadRing];
+                // the sums of the parts, the smallest first
 #pragma unroll
-                    for (int c = 0; c < C::kCols; c += 16) {
-                        if (c >= cols) break;
-                        if (c > 0) load_parts(c);
-                        tmem_wait_ld();
+                for (int c = 0; c < R; c += 16) {
+                    if (c >= cols) break;
+                    if (c > 0) load_parts(c);
+                    tmem_wait_ld();
 #pragma unroll
-                        for (int e = 0; e < 16; e += 2) {
-                            const float2 by = make_float2(0.0625f, 0.0625f);
-                            float2 y = make_float2(part[e], part[e + 1]);
-                            if (kQParts > 2) y = __ffma2_rn(make_float2(last[e], last[e + 1]), by, y);
-                            y = __ffma2_rn(y, by, make_float2(x[c + e], x[c + e + 1]));
-                            x[c + e] = y.x;
-                            x[c + e + 1] = y.y;
-                        }
+                    for (int e = 0; e < 16; e += 2) {
+                        const float2 by = make_float2(0.0625f, 0.0625f);
+                        float2 y = make_float2(part[e], part[e + 1]);
+                        if (kQParts > 2) y = __ffma2_rn(make_float2(last[e], last[e + 1]), by, y);
+                        y = __ffma2_rn(y, by, make_float2(x[c + e], x[c + e + 1]));
+                        x[c + e] = y.x;
+                        x[c + e + 1] = y.y;
                     }
-                    const bool fresh = blk == blk0;
-                    const bool guard = !packed || bad_pages != 0u || blk >= tail0;
-                    unsigned allow = ~0u;  // rows of this warpgroup that attend the token
-                    if (guard) {
-                        const int t = (bad_pages >> (tok >> a.slot_shift)) & 1u ? -1 : tree_token(a, blk, tok), ctx = r.ctx(), i = t - ctx;
-                        allow = t < 0 || t >= r.len ? 0u : ~0u;
-                        if (allow != 0u && i >= 0) {
-#pragma unroll 4
-                            for (int c = 0; c < cols; ++c) {
-                                const int node = min(rownode[qb * R + col0 + c], r.n - 1);
-                                bool sees;
-                                if (a.mask == nullptr)
-                                    sees = i <= node;
-                                else
-                                    sees = i / 32 < a.mask_words && ((__ldg(a.mask + size_t(r.start + node) * a.mask_words + i / 32) >> (i % 32)) & 1u) != 0u;
-                                if (!sees) allow &= ~(1u << c);
-                            }
-                        }
-                        if (wg == 0 && (t < 0 || t >= ctx)) {
-                            // V of a token that some row does not attend: a weight of zero does not undo NaN
-                            uint8_t* vrow = smem + C::kRingOff + (ring.slot + 1 == C::kSlots ? 0 : ring.slot + 1) * C::kSlotBytes + tok * C::kRowBytes;
-                            const uint32_t vphase = ring.phase ^ (ring.slot + 1 == C::kSlots ? 1u : 0u);
-                            const bool dead = t < 0 || t >= r.len;
-                            const bool landed = tree_wait(bar(C::kFull + (ring.slot + 1 == C::kSlots ? 0 : ring.slot + 1)), vphase, abort_flag, a.flags);
-                            bool found = false;
-                            for (int x0 = 0; landed && x0 < D / 16; ++x0) {
-                                // (lanes in turn from another 16 bytes on: all banks)
-                                constexpr int kIn = C::kRowBytes / 16;
-                                const int in = (x0 + lane) % kIn;
-                                uint4* at = reinterpret_cast<uint4*>(vrow + x0 / kIn * (C::kKeys * C::kRowBytes) + in * 16);
-                                uint4 w = *at;
-                                uint4 n = make_uint4(~0u, ~0u, ~0u, ~0u);
-                                if (!dead)
-                                    n = make_uint4(__vcmpeq4(w.x & 0x7f7f7f7fu, 0x7f7f7f7fu), __vcmpeq4(w.y & 0x7f7f7f7fu, 0x7f7f7f7fu),
-                                                   __vcmpeq4(w.z & 0x7f7f7f7fu, 0x7f7f7f7fu), __vcmpeq4(w.w & 0x7f7f7f7fu, 0x7f7f7f7fu));
-                                if ((n.x | n.y | n.z | n.w) != 0u) {
-                                    found |= !dead;
-                                    *at = make_uint4(w.x & ~n.x, w.y & ~n.y, w.z & ~n.z, w.w & ~n.w);
-                                }
-                            }
-                            if (found) tag[seg & 1] = seg + 1;
-                        }
-                        __syncwarp();
-                    }
-                    // ---- exponents against the running maximum (the scores themselves in a segment's first tile); minus
-                    // infinity where a row does not attend the token
-                    float top = kNegInf;
-                    const float2 ks2 = make_float2(ks, ks);
-#pragma unroll
-                    for (int c = 0; c < C::kCols; c += 4) {
-                        if (c % 8 == 0 && c >= cols) break;
-                        const float4 cc = *reinterpret_cast<const float4*>(wc + c), mm = *reinterpret_cast<const float4*>(wm + c);
-                        float2 y = __fmul2_rn(make_float2(x[c], x[c + 1]), ks2), z = __fmul2_rn(make_float2(x[c + 2], x[c + 3]), ks2);
-                        y = __ffma2_rn(y, make_float2(cc.x, cc.y), make_float2(mm.x, mm.y));
-                        z = __ffma2_rn(z, make_float2(cc.z, cc.w), make_float2(mm.z, mm.w));
-                        x[c] = y.x, x[c + 1] = y.y, x[c + 2] = z.x, x[c + 3] = z.y;
-                        if (guard) {
-#pragma unroll
-                            for (int e = c; e < c + 4; ++e)
-                                if (((allow >> e) & 1u) == 0u) x[e] = kNegInf;
-                        }
-                        top = fmaxf(fmaxf(top, fmaxf(x[c], x[c + 1])), fmaxf(x[c + 2], x[c + 3]));
-                    }
-                    // ---- does a weight pass its limit?
-                    bool over = fresh;
-                    if (!over) {
-                        const int id = exchanges + 1;
-                        if (__any_sync(kFull, top + lv > kShift + kRise) && lane == 0) votes[(id - 1) & 1] = id;
-                        if (!(ok = exchange())) break;
-                        over = votes[(id - 1) & 1] == id;
-                    }
-                    if (over) {
-                        float mine = kNegInf;
-#pragma unroll
-                        for (int c = 0; c < C::kCols; ++c) {
-                            if (c >= cols) break;
-                            const float t = redux_max(isnan(x[c]) ? kNegInf : x[c] + lv);
-                            if (lane == c) mine = t;
-                        }
-                        const float was = lane < C::kCols ? wm[lane] : 0.f;
-                        if (lane < C::kCols) red[(sw & 3) * C::kCols + lane] = mine - was;
-                        if (!(ok = exchange())) break;
-                        if (lane < C::kCols) {
-                            const float best = fmaxf(fmaxf(red[lane], red[C::kCols + lane]), fmaxf(red[2 * C::kCols + lane], red[3 * C::kCols + lane]));
-                            const float to_m = fmaxf(m, best), now = to_m == kNegInf ? kShift : kShift - to_m;
-                            wf[lane] = m == kNegInf ? 1.f : ex2(m - to_m);
-                            wd[lane] = now - was;
-                            wm[lane] = now;
-                            m = to_m;
-                        }
-                        __syncwarp();
-#pragma unroll
-                        for (int c = 0; c < C::kCols; ++c) x[c] += wd[c];
-                        if (!fresh) {
-                            // O holds every tile before this one once the last P V is done
-                            if (!(ok = wait(C::kPvDone + (jobs - 1) % C::kPBufs, uint32_t((jobs - 1) / C::kPBufs) & 1u))) break;
-                            tc_fence_after();
-#pragma unroll
-                            for (int c = 0; c < C::kCols; ++c) l[c] *= wf[c];
-#pragma unroll 1
-                            for (int cb = 0; cb < 2 * C::kColBlocks; ++cb)  // both parts' O of each column block
-#pragma unroll
-                                for (int c = 0; c < C::kCols; c += 16) {
-                                    uint32_t o[16];
-                                    tmem_ld16(to + cb * R + c, o);
-                                    tmem_wait_ld();
-#pragma unroll
-                                    for (int e = 0; e < 16; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * wf[c + e]);
-                                    tmem_st16(to + cb * R + c, o);
-                                }
-                            tmem_wait_st();
-                        }
-                    }
-                    // ---- weights and their parts, the second one 16 times what the first leaves
-                    if (jobs >= C::kPBufs && !(ok = wait(C::kPvDone + pbuf, uint32_t((jobs - C::kPBufs) / C::kPBufs) & 1u))) break;
-                    uint8_t* pp = smem + C::kPOff + pbuf * C::kPBytes + (col0 / 16) * 2048 + tok * 16;
-                    const float2 vs2 = make_float2(vs, vs);
-                    auto weights = [&](auto guarded) {
-#pragma unroll
-                        for (int c = 0; c < C::kCols; c += 8) {
-                            if (c >= cols) break;
-                            uint32_t p1[4], p2[4];
-#pragma unroll
-                            for (int e = 0; e < 4; ++e) {
-                                const float2 y = make_float2(ex2(x[c + 2 * e]), ex2(x[c + 2 * e + 1]));
-                                float2 w = __fmul2_rn(y, vs2);
-                                if constexpr (decltype(guarded)::value) {  // (a scale that is not a number)
-                                    if (((allow >> (c + 2 * e)) & 1u) == 0u) w.x = 0.f;
-                                    if (((allow >> (c + 2 * e + 1)) & 1u) == 0u) w.y = 0.f;
-                                }
-                                float2 sum = __fadd2_rn(make_float2(l[c + 2 * e], l[c + 2 * e + 1]), y);
-                                l[c + 2 * e] = sum.x;
-                                l[c + 2 * e + 1] = sum.y;
-                                const __half2 h = __floats2half2_rn(w.x, w.y);
-                                p1[e] = half2_codes(h);
-                                p2[e] = half2_codes(__hmul2(__hsub2(h, codes_half2(p1[e])), __float2half2_rn(16.f)));
-                            }
-                            uint8_t* at = pp + c / 16 * 2048 + c % 16;
-                            *reinterpret_cast<uint2*>(at) = make_uint2(__byte_perm(p1[0], p1[1], 0x5410), __byte_perm(p1[2], p1[3], 0x5410));
-                            *reinterpret_cast<uint2*>(at + C::kPPart) = make_uint2(__byte_perm(p2[0], p2[1], 0x5410), __byte_perm(p2[2], p2[3], 0x5410));
-                        }
-                    };
-                    if (guard)
-                        weights(std::true_type{});
-                    else
-                        weights(std::false_type{});
-                    fence_proxy_async_smem();
-                    tc_fence_before();
                 }
+                const bool fresh = blk == blk0;
+                const bool guard = !packed || bad_pages != 0u || blk >= tail0;
+                unsigned allow = ~0u;  // rows that attend the token
+                if (guard) {
+                    const int t = (bad_pages >> (tok >> a.slot_shift)) & 1u ? -1 : tree_token(a, blk, tok), ctx = r.ctx(), i = t - ctx;
+                    allow = t < 0 || t >= r.len ? 0u : ~0u;
+                    if (allow != 0u && i >= 0) {
+#pragma unroll 4
+                        for (int c = 0; c < cols; ++c) {
+                            const int node = min(rownode[qb * R + c], r.n - 1);
+                            bool sees;
+                            if (a.mask == nullptr)
+                                sees = i <= node;
+                            else
+                                sees = i / 32 < a.mask_words && ((__ldg(a.mask + size_t(r.start + node) * a.mask_words + i / 32) >> (i % 32)) & 1u) != 0u;
+                            if (!sees) allow &= ~(1u << c);
+                        }
+                    }
+                    if ((t < 0 || t >= ctx)) {
+                        // V of a token that some row does not attend: a weight of zero does not undo NaN
+                        uint8_t* vrow = smem + C::kRingOff + (ring.slot + 1 == C::kSlots ? 0 : ring.slot + 1) * C::kSlotBytes + tok * C::kRowBytes;
+                        const uint32_t vphase = ring.phase ^ (ring.slot + 1 == C::kSlots ? 1u : 0u);
+                        const bool dead = t < 0 || t >= r.len;
+                        const bool landed = tree_wait(bar(C::kFull + (ring.slot + 1 == C::kSlots ? 0 : ring.slot + 1)), vphase, abort_flag, a.flags);
+                        bool found = false;
+                        for (int x0 = 0; landed && x0 < D / 16; ++x0) {
+                            // (lanes in turn from another 16 bytes on: all banks)
+                            constexpr int kIn = C::kRowBytes / 16;
+                            const int in = (x0 + lane) % kIn;
+                            uint4* at = reinterpret_cast<uint4*>(vrow + x0 / kIn * (C::kKeys * C::kRowBytes) + in * 16);
+                            uint4 w = *at;
+                            uint4 n = make_uint4(~0u, ~0u, ~0u, ~0u);
+                            if (!dead)
+                                n = make_uint4(__vcmpeq4(w.x & 0x7f7f7f7fu, 0x7f7f7f7fu), __vcmpeq4(w.y & 0x7f7f7f7fu, 0x7f7f7f7fu),
+                                               __vcmpeq4(w.z & 0x7f7f7f7fu, 0x7f7f7f7fu), __vcmpeq4(w.w & 0x7f7f7f7fu, 0x7f7f7f7fu));
+                            if ((n.x | n.y | n.z | n.w) != 0u) {
+                                found |= !dead;
+                                *at = make_uint4(w.x & ~n.x, w.y & ~n.y, w.z & ~n.z, w.w & ~n.w);
+                            }
+                        }
+                        if (found) tag[seg & 1] = seg + 1;
+                    }
+                    __syncwarp();
+                }
+                // ---- exponents against the running maximum (the scores themselves in a segment's first tile); minus
+                // infinity where a row does not attend the token
+                float top = kNegInf;
+                const float2 ks2 = make_float2(ks, ks);
+#pragma unroll
+                for (int c = 0; c < R; c += 4) {
+                    if (c % 8 == 0 && c >= cols) break;
+                    const float4 cc = *reinterpret_cast<const float4*>(wc + c), mm = *reinterpret_cast<const float4*>(wm + c);
+                    float2 y = __fmul2_rn(make_float2(x[c], x[c + 1]), ks2), z = __fmul2_rn(make_float2(x[c + 2], x[c + 3]), ks2);
+                    y = __ffma2_rn(y, make_float2(cc.x, cc.y), make_float2(mm.x, mm.y));
+                    z = __ffma2_rn(z, make_float2(cc.z, cc.w), make_float2(mm.z, mm.w));
+                    x[c] = y.x, x[c + 1] = y.y, x[c + 2] = z.x, x[c + 3] = z.y;
+                    if (guard) {
+#pragma unroll
+                        for (int e = c; e < c + 4; ++e)
+                            if (((allow >> e) & 1u) == 0u) x[e] = kNegInf;
+                    }
+                    top = fmaxf(fmaxf(top, fmaxf(x[c], x[c + 1])), fmaxf(x[c + 2], x[c + 3]));
+                }
+                // ---- does a weight pass its limit?
+                bool over = fresh;
+                if (!over) {
+                    const int id = exchanges + 1;
+                    if (__any_sync(kFull, top + lv > kShift + kRise) && lane == 0) votes[(id - 1) & 1] = id;
+                    if (!(ok = exchange())) break;
+                    over = votes[(id - 1) & 1] == id;
+                }
+                if (over) {
+                    float mine = kNegInf;
+#pragma unroll
+                    for (int c = 0; c < R; ++c) {
+                        if (c >= cols) break;
+                        const float t = redux_max(isnan(x[c]) ? kNegInf : x[c] + lv);
+                        if (lane == c) mine = t;
+                    }
+                    const float was = lane < R ? wm[lane] : 0.f;
+                    if (lane < R) red[quad * R + lane] = mine - was;
+                    if (!(ok = exchange())) break;
+                    if (lane < R) {
+                        const float best = fmaxf(fmaxf(red[lane], red[R + lane]), fmaxf(red[2 * R + lane], red[3 * R + lane]));
+                        const float to_m = fmaxf(m, best), now = to_m == kNegInf ? kShift : kShift - to_m;
+                        wf[lane] = m == kNegInf ? 1.f : ex2(m - to_m);
+                        wd[lane] = now - was;
+                        wm[lane] = now;
+                        m = to_m;
+                    }
+                    __syncwarp();
+#pragma unroll
+                    for (int c = 0; c < R; ++c) x[c] += wd[c];
+                    if (!fresh) {
+                        // O holds every tile before this one once the last P V is done
+                        if (!(ok = wait(C::kPvDone + (jobs - 1) % C::kPBufs, uint32_t((jobs - 1) / C::kPBufs) & 1u))) break;
+                        tc_fence_after();
+#pragma unroll
+                        for (int c = 0; c < R; ++c) l[c] *= wf[c];
+#pragma unroll 1
+                        for (int cb = 0; cb < 2 * C::kColBlocks; ++cb)  // both parts' O of each column block
+#pragma unroll
+                            for (int c = 0; c < R; c += 16) {
+                                uint32_t o[16];
+                                tmem_ld16(to + cb * R + c, o);
+                                tmem_wait_ld();
+#pragma unroll
+                                for (int e = 0; e < 16; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * wf[c + e]);
+                                tmem_st16(to + cb * R + c, o);
+                            }
+                        tmem_wait_st();
+                    }
+                }
+                // ---- weights and their parts, the second one 16 times what the first leaves
+                if (jobs >= C::kPBufs && !(ok = wait(C::kPvDone + pbuf, uint32_t((jobs - C::kPBufs) / C::kPBufs) & 1u))) break;
+                uint8_t* pp = smem + C::kPOff + pbuf * C::kPBytes + tok * 16;
+                const float2 vs2 = make_float2(vs, vs);
+                auto weights = [&](auto guarded) {
+#pragma unroll
+                    for (int c = 0; c < R; c += 8) {
+                        if (c >= cols) break;
+                        uint32_t p1[4], p2[4];
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) {
+                            const float2 y = make_float2(ex2(x[c + 2 * e]), ex2(x[c + 2 * e + 1]));
+                            float2 w = __fmul2_rn(y, vs2);
+                            if constexpr (decltype(guarded)::value) {  // (a scale that is not a number)
+                                if (((allow >> (c + 2 * e)) & 1u) == 0u) w.x = 0.f;
+                                if (((allow >> (c + 2 * e + 1)) & 1u) == 0u) w.y = 0.f;
+                            }
+                            float2 sum = __fadd2_rn(make_float2(l[c + 2 * e], l[c + 2 * e + 1]), y);
+                            l[c + 2 * e] = sum.x;
+                            l[c + 2 * e + 1] = sum.y;
+                            const __half2 h = __floats2half2_rn(w.x, w.y);
+                            p1[e] = half2_codes(h);
+                            p2[e] = half2_codes(__hmul2(__hsub2(h, codes_half2(p1[e])), __float2half2_rn(16.f)));
+                        }
+                        uint8_t* at = pp + c / 16 * 2048 + c % 16;
+                        *reinterpret_cast<uint2*>(at) = make_uint2(__byte_perm(p1[0], p1[1], 0x5410), __byte_perm(p1[2], p1[3], 0x5410));
+                        *reinterpret_cast<uint2*>(at + C::kPPart) = make_uint2(__byte_perm(p2[0], p2[1], 0x5410), __byte_perm(p2[2], p2[3], 0x5410));
+                    }
+                };
+                if (guard)
+                    weights(std::true_type{});
+                else
+                    weights(std::false_type{});
+                fence_proxy_async_smem();
+                tc_fence_before();
                 __syncwarp();
                 if (lane == 0) mbar_arrive(bar(C::kPFull + pbuf));
             }
             if (!ok) break;
             // ---- the segment's end
             if (!(ok = wait(C::kPvDone + (jobs - 1) % C::kPBufs, uint32_t((jobs - 1) / C::kPBufs) & 1u))) break;
-            if (cols > 0) {
-                tc_fence_after();
-                // sums of the rows over the four warps, in their order
-                ReduceScatter<C::kCols, 16>::run(l, lane);
-                red[(sw & 3) * C::kCols + ReduceScatter<C::kCols, 16>::index(0, lane)] = l[0];
-                if (!(ok = exchange())) break;
-                if (lane < C::kCols) {
-                    const float sum = (red[lane] + red[C::kCols + lane]) + (red[2 * C::kCols + lane] + red[3 * C::kCols + lane]);
-                    wf[lane] = sum == 0.f ? 0.f : 1.f / sum;
-                    // empty by the sum: the maximum passes over scores of NaN, the sum does not
-                    const float lse2 = sum == 0.f ? kNegInf : (m == kNegInf ? 0.f : m) - kShift + log2f(sum);
-                    const long long at = lane < cols ? rowat[qb * R + col0 + lane] : -1;
-                    if ((sw & 3) == 0 && at >= 0) {
-                        if (s.slot >= 0)
-                            a.part_lse[size_t(s.slot) * a.seg_rows + col0 + lane] = tree_part_lse(lse2);
-                        else
-                            a.lse[at] = lse2 == kNegInf ? kNegInf : lse2 * kLn2;
-                    }
+            tc_fence_after();
+            // sums of the rows over the four warps, in their order
+            ReduceScatter<R, 16>::run(l, lane);
+            sums[quad * R + ReduceScatter<R, 16>::index(0, lane)] = l[0];
+            if (!(ok = exchange())) break;
+            if (lane < R) {
+                const float sum = (sums[lane] + sums[R + lane]) + (sums[2 * R + lane] + sums[3 * R + lane]);
+                wf[lane] = sum == 0.f ? 0.f : 1.f / sum;
+                // empty by the sum: the maximum passes over scores of NaN, the sum does not
+                const float lse2 = sum == 0.f ? kNegInf : (m == kNegInf ? 0.f : m) - kShift + log2f(sum);
+                const long long at = lane < cols ? rowat[qb * R + lane] : -1;
+                if (quad == 0 && at >= 0) {
+                    if (s.slot >= 0)
+                        a.part_lse[size_t(s.slot) * a.seg_rows + lane] = tree_part_lse(lse2);
+                    else
+                        a.lse[at] = lse2 == kNegInf ? kNegInf : lse2 * kLn2;
                 }
-                __syncwarp();
-                const bool fix = tag[seg & 1] == seg + 1;
-#pragma unroll 1
-                for (int x = 0; x < C::kColBlocks * (C::kCols / 16); ++x) {
-                    const int cb = x / (C::kCols / 16), c = x % (C::kCols / 16) * 16;
-                    if (c >= cols) continue;
-                    uint32_t o[16], o2[16];
-                    __syncwarp();
-                    tmem_ld16(to + cb * 2 * R + c, o);
-                    tmem_ld16(to + cb * 2 * R + R + c, o2);
-                    tmem_wait_ld();
-                    const int dim = cb * 128 + tok;
-                    if (dim >= D) continue;  // (head_dim 64: the second half of M)
-#pragma unroll
-                    for (int e = 0; e < 16; ++e) {
-                        const long long at = c + e < cols ? rowat[qb * R + col0 + c + e] : -1;
-                        if (at < 0) continue;
-                        float f = fmaf(__uint_as_float(o2[e]), 0.0625f, __uint_as_float(o[e])) * wf[c + e];
-                        if (fix) {
-                            // NaN of node rows in these blocks, for the rows that attend them
-                            const int node = rownode[qb * R + col0 + c + e];
-                            for (int i = 0; i < r.n; ++i) {
-                                const int t = r.ctx() + i, b = tree_slot_of(a, t) >> a.spb_shift;
-                                if (b < blk0 || b >= blk1) continue;
-                                if ((tree_allow(a, r, node, t, 1) & 1u) == 0u) continue;
-                                const int page = __ldg(a.indices + r.lo + t / a.page_size);
-                                if (page < 0 || page >= a.num_total_pages) continue;
-                                const size_t vrow = ((size_t(page) * a.num_kv_heads + s.kvh) * a.page_size + t % a.page_size) * D;
-                                if ((static_cast<const uint8_t*>(a.v)[vrow + dim] & 0x7f) == 0x7f) f = __int_as_float(0x7fc00000);
-                            }
-                        }
-                        if (s.slot >= 0)
-                            a.part_o[(size_t(s.slot) * a.seg_rows + col0 + c + e) * D + dim] = f;
-                        else
-                            static_cast<T*>(a.o)[at * D + dim] = T(f);
-                    }
-                }
-                tc_fence_before();
             }
+            __syncwarp();
+            const bool fix = tag[seg & 1] == seg + 1;
+#pragma unroll 1
+            for (int x = 0; x < C::kColBlocks * (R / 16); ++x) {
+                const int cb = x / (R / 16), c = x % (R / 16) * 16;
+                if (c >= cols) continue;
+                uint32_t o[16], o2[16];
+                __syncwarp();
+                tmem_ld16(to + cb * 2 * R + c, o);
+                tmem_ld16(to + cb * 2 * R + R + c, o2);
+                tmem_wait_ld();
+                const int dim = cb * 128 + tok;
+                if (dim >= D) continue;  // (head_dim 64: the second half of M)
+#pragma unroll
+                for (int e = 0; e < 16; ++e) {
+                    const long long at = c + e < cols ? rowat[qb * R + c + e] : -1;
+                    if (at < 0) continue;
+                    float f = fmaf(__uint_as_float(o2[e]), 0.0625f, __uint_as_float(o[e])) * wf[c + e];
+                    if (fix) {
+                        // NaN of node rows in these blocks, for the rows that attend them
+                        const int node = rownode[qb * R + c + e];
+                        for (int i = 0; i < r.n; ++i) {
+                            const int t = r.ctx() + i, b = tree_slot_of(a, t) >> a.spb_shift;
+                            if (b < blk0 || b >= blk1) continue;
+                            if ((tree_allow(a, r, node, t, 1) & 1u) == 0u) continue;
+                            const int page = __ldg(a.indices + r.lo + t / a.page_size);
+                            if (page < 0 || page >= a.num_total_pages) continue;
+                            const size_t vrow = ((size_t(page) * a.num_kv_heads + s.kvh) * a.page_size + t % a.page_size) * D;
+                            if ((static_cast<const uint8_t*>(a.v)[vrow + dim] & 0x7f) == 0x7f) f = __int_as_float(0x7fc00000);
+                        }
+                    }
+                    if (s.slot >= 0)
+                        a.part_o[(size_t(s.slot) * a.seg_rows + c + e) * D + dim] = f;
+                    else
+                        static_cast<T*>(a.o)[at * D + dim] = T(f);
+                }
+            }
+            tc_fence_before();
             __syncwarp();
             if (lane == 0) mbar_arrive(bar(C::kQEmpty + qb));
             seg_free(seg);

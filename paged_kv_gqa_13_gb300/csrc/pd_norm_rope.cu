@@ -18,7 +18,10 @@
 //
 // Rows that pass through (q; k and v too where the pool's scales are given) go token by token, as in pd_rope.cu: a warp
 // takes a token or a slice of its heads, a group of L lanes a head, V elements at two places a lane (a rotated element and
-// its partner), whose sines a lane keeps for all heads.
+// its partner), whose sines a lane keeps for all heads. The groups share the work of the sines, and the first q heads are
+// loaded before them (8191 tokens x 64 heads of 128: 60 us before both, 57 after). More slices of a token than the card
+// needs repeat that start (two: 66 us, four: 76). Into pools, two heads of a group at once and 6 CTAs on an SM (7000 tokens,
+// bf16: 39.6 us; four heads: 41.6 with 4 CTAs, 44 with 5); rotation alone, four heads and 5 CTAs (57 us; 60 to 62 so).
 //
 // k and v rows into blocks go head by head: a CTA takes a tile of T tokens of a request, T a whole number of blocks,
 // aligned in the cache, so that all rows of a block are in one CTA. It computes the sines of the tile once for all heads,
@@ -204,13 +207,32 @@ __device__ __forceinline__ void normalise(float (&x)[kUnits][V], float (&y)[kUni
 // Heads that pass through: one warp per (token, slice of its heads).
 template <typename T, int V, bool kPairs, int kPool>
 __device__ __forceinline__ void token_heads(const NormArgs& a, long long w) {
-    constexpr int kUnits = V == 1 ? 4 : 1, kRound = V == 1 ? 2 : 4;
+    constexpr int kUnits = V == 1 ? 4 : 1, kRound = V == 1 || kPool == kPlain || kPool == kHeadScales ? 2 : 4;
     const int lane = threadIdx.x & 31;
     const int t = int(w / a.slices), slice = int(w % a.slices);
     const int D = a.head_dim, rot = a.rot_dim, rotated = rot / (2 * V);
     const int items = a.hq + (kPool == kNone ? a.hk : kPool == kBlockScales ? 0 : 2 * a.hk);
     const int i0 = int((long long)items * slice / a.slices), i1 = int((long long)items * (slice + 1) / a.slices);
     const bool wants_kv = (kPool == kPlain || kPool == kHeadScales) && i1 > a.hq;
+
+    const Places<V, kPairs, kUnits> at(D, rot, lane);
+    Raw<T, V> xs[kRound][kUnits], ys[kRound][kUnits];
+    // A round of heads [h, h1): kRound of each group of lanes.
+    auto fetch = [&](const T* src, int h, int h1) {
+#pragma unroll
+        for (int r = 0; r < kRound; ++r)
+#pragma unroll
+            for (int j = 0; j < kUnits; ++j)
+                if (h + r * at.rows < h1 && at.on[j]) {
+                    const T* row = src + (long long)(h + r * at.rows) * D;
+                    xs[r][j] = *reinterpret_cast<const Raw<T, V>*>(row + at.e0[j]);
+                    ys[r][j] = *reinterpret_cast<const Raw<T, V>*>(row + at.e1[j]);
+                }
+    };
+    // The first q heads are on their way while the table is read and the sines are computed.
+    const int q1 = min(i1, a.hq);
+    const T* q_row = static_cast<const T*>(a.q) + t * a.q_stride;
+    if (i0 < q1) fetch(q_row, i0 + at.lr, q1);
 
     // ---- where this token's k and v rows go (offset in elements of kv head 0), and its position
     int pos = 0;
@@ -250,15 +272,31 @@ __device__ __forceinline__ void token_heads(const NormArgs& a, long long w) {
     }
     if (a.positions != nullptr) pos = __ldg(a.positions + t);
 
-    const Places<V, kPairs, kUnits> at(D, rot, lane);
     float2 turns[kUnits][V];
+    auto turn = [&](int u, int i) {
+        return u < rotated ? turn_of(pos, __ldg(a.freqs + pair_of<V, kPairs>(u, i, rot)), a.scale) : make_float2(1.f, 0.f);
+    };
+    // The groups of lanes hold the same pairs of different heads: each of kGroups computes its share of the sines.
+    auto share = [&](auto groups) {
+        constexpr int kGroups = decltype(groups)::value;
+        float2 mine[V / kGroups > 0 ? V / kGroups : 1];
 #pragma unroll
-    for (int j = 0; j < kUnits; ++j) {
-        const int u = at.lu + 32 * j;
+        for (int i = 0; i < V / kGroups; ++i) mine[i] = turn(at.lu, i * kGroups + (at.lr & (kGroups - 1)));
 #pragma unroll
-        for (int i = 0; i < V; ++i)
-            turns[j][i] = u < rotated ? turn_of(pos, __ldg(a.freqs + pair_of<V, kPairs>(u, i, rot)), a.scale) : make_float2(1.f, 0.f);
-    }
+        for (int i = 0; i < V; ++i) {
+            const int from = i % kGroups * at.L + at.lu;
+            turns[0][i] = make_float2(__shfl_sync(kFull, mine[i / kGroups].x, from), __shfl_sync(kFull, mine[i / kGroups].y, from));
+        }
+    };
+    if (V > 1 && at.rows >= 4)
+        share(std::integral_constant<int, (V > 1 ? 4 : 1)>{});
+    else if (V > 1 && at.rows == 2)
+        share(std::integral_constant<int, (V > 1 ? 2 : 1)>{});
+    else
+#pragma unroll
+        for (int j = 0; j < kUnits; ++j)
+#pragma unroll
+            for (int i = 0; i < V; ++i) turns[j][i] = turn(at.lu + 32 * j, i);
     const float inv_dim = 1.f / float(D);
     // Heads [h0, h1) of one kind: q, k or v.
     auto run = [&](int h0, int h1, const T* src, const void* weight, auto kind) {
@@ -275,16 +313,7 @@ __device__ __forceinline__ void token_heads(const NormArgs& a, long long w) {
                 }
         }
         for (int h = h0 + at.lr; h - at.lr < h1; h += at.rows * kRound) {
-            Raw<T, V> xs[kRound][kUnits], ys[kRound][kUnits];
-#pragma unroll
-            for (int r = 0; r < kRound; ++r)
-#pragma unroll
-                for (int j = 0; j < kUnits; ++j)
-                    if (h + r * at.rows < h1 && at.on[j]) {
-                        const T* row = src + (long long)(h + r * at.rows) * D;
-                        xs[r][j] = *reinterpret_cast<const Raw<T, V>*>(row + at.e0[j]);
-                        ys[r][j] = *reinterpret_cast<const Raw<T, V>*>(row + at.e1[j]);
-                    }
+            if (kKind != 0 || h - at.lr != h0) fetch(src, h, h1);
 #pragma unroll
             for (int r = 0; r < kRound; ++r) {
                 const int head = h + r * at.rows;
@@ -341,8 +370,7 @@ __device__ __forceinline__ void token_heads(const NormArgs& a, long long w) {
             }
         }
     };
-    if (i0 < min(i1, a.hq))
-        run(i0, min(i1, a.hq), static_cast<const T*>(a.q) + t * a.q_stride, a.q_weight, std::integral_constant<int, 0>{});
+    if (i0 < q1) run(i0, q1, q_row, a.q_weight, std::integral_constant<int, 0>{});
     if constexpr (kPool != kBlockScales) {
         if (kPool != kNone && !write_kv) return;
         const int k0 = max(i0 - a.hq, 0), k1 = min(i1 - a.hq, a.hk);
@@ -608,7 +636,8 @@ __device__ __forceinline__ void tile_blocks(const NormArgs& a, float* turns, Til
 }
 
 template <typename T, int V, bool kPairs, int kPool>
-__global__ void __launch_bounds__(kThreads, kPool == kBlockScales ? 4 : 5) norm_rope_kernel(const NormArgs a) {
+__global__ void __launch_bounds__(kThreads, kPool == kBlockScales ? 4 : kPool == kNone ? 5 : 6)
+    norm_rope_kernel(const NormArgs a) {
     if constexpr (kPool == kBlockScales) {
         extern __shared__ __align__(16) float turns[];  // cos, sin of the tile's rows and pairs
         __shared__ TileShared sh;

@@ -249,7 +249,8 @@ struct CfgTree {
                          kScFull = kStEmpty + kStages, kBars = kScFull + (kBlocks ? 6 : 0);
     // block scales: of the blocks on their way (see the producers), and a softmax warp's of one job, ready for use
     static constexpr int kScales = kBlocks ? 6 : 0, kScaleBytes = kScales * 2 * kKeys * 4;
-    static constexpr int kReadyBytes = kBlocks ? 4 * kPipes * (kJobKeys / kRun) * 16 : 0;
+    static constexpr int kReadyKeys = kRun == 16 ? kKeys : kJobKeys, kReadyRuns = kReadyKeys / kRun;  // of a warp at a time
+    static constexpr int kReadyBytes = kBlocks ? 4 * kPipes * kReadyRuns * 16 : 0;
     // a line's shared memory: q, ring | barriers, bad-V tags, bad slots, segments (of all lines, after the data)
     static constexpr int kRingOff = kPipes * kQBytes;
     static constexpr int kStageOff = kRingOff + kSlots * kSlotBytes;
@@ -785,7 +786,7 @@ __global__ void __launch_bounds__(CfgTree<D, kWide, kPool>::kThreads, 1)
         int jobs = 0, kblocks = 0;  // kblocks: K blocks before this segment
         bool ok = true;
         Ring<kBlocks ? C::kScales : 1> sc;
-        float4* ready = reinterpret_cast<float4*>(ctl + C::kReadyOff) + (kBlocks ? wid % (4 * C::kPipes) * (C::kJobKeys / C::kRun) : 0);
+        float4* ready = reinterpret_cast<float4*>(ctl + C::kReadyOff) + (kBlocks ? wid % (4 * C::kPipes) * C::kReadyRuns : 0);
         auto turn_q = [&](const TcSeg& s, int seg) -> bool {
             // This thread's q row, where the copy put it, as f16 times a power of two that brings its
             // largest element near 2^14 (exact but for elements more than 2^28 below it) and the sign of
@@ -838,14 +839,14 @@ __global__ void __launch_bounds__(CfgTree<D, kWide, kPool>::kThreads, 1)
 #pragma unroll 1
                 for (int half = 0; half < C::kJobs; ++half) {
                     const int buf = jobs & 1;
-                    if (kBlocks && live) {
-                        // This job's scales for each run of keys, before its scores are there: {k, log2 v, 1 / v}, v at least
-                        // 2^-96 (the sums stay below 2^128).
+                    if (kBlocks && live && half * C::kJobKeys % C::kReadyKeys == 0) {
+                        // The scales of each run of keys, of this job or of the block, before the scores are there: {k, log2 v,
+                        // 1 / v}, v at least 2^-96 (the sums stay below 2^128).
                         if (half == 0 && !(ok = wait(C::kScFull + sc.slot, sc.phase))) break;
                         const float* from = reinterpret_cast<const float*>(ctl + C::kScaleOff) + sc.slot * 2 * C::kKeys;
                         __syncwarp();
 #pragma unroll
-                        for (int g = lane; g < C::kJobKeys / C::kRun; g += 32) {
+                        for (int g = lane; g < C::kReadyRuns; g += 32) {
                             const int key = half * C::kJobKeys + g * C::kRun, at = C::kRun == 16 || a.run > 1 ? key / 4 : key;
                             const float v = fmaxf(from[C::kKeys + at], 1.2621774e-29f);
                             ready[g] = make_float4(from[at], __log2f(v), __frcp_rn(v), 0.f);
@@ -887,13 +888,14 @@ __global__ void __launch_bounds__(CfgTree<D, kWide, kPool>::kThreads, 1)
                         }
                         // (block scales: a factor above 0 leaves minus infinity what it is)
                         auto factor = [&](const float4& f) { return fmaxf(scale * f.x, 1e-38f); };
+                        const float4* runs = ready + half * C::kJobKeys % C::kReadyKeys / C::kRun;  // this job's
                         float top;
                         if constexpr (kBlocks) {
                             // what a key can bring to the output: its score and its V scale
                             top = kNegInf;
 #pragma unroll
                             for (int g = 0; g < C::kJobKeys / C::kRun; ++g) {
-                                const float4 f = ready[g];
+                                const float4 f = runs[g];
                                 float most = __uint_as_float(x[g * C::kRun]), more = most;
 #pragma unroll
                                 for (int e = 1; e < C::kRun; ++e)
@@ -941,7 +943,7 @@ __global__ void __launch_bounds__(CfgTree<D, kWide, kPool>::kThreads, 1)
 #pragma unroll
                             for (int g = 0; g < C::kJobKeys / (C::kRun > 1 ? C::kRun : 2); ++g) {
                                 constexpr int kOf = C::kRun > 1 ? C::kRun : 2;
-                                const float4 f = ready[C::kRun > 1 ? g : 2 * g], f1 = C::kRun > 1 ? f : ready[2 * g + 1];
+                                const float4 f = runs[C::kRun > 1 ? g : 2 * g], f1 = C::kRun > 1 ? f : runs[2 * g + 1];
                                 const float2 by = make_float2(factor(f), factor(f1)), add = make_float2(f.y - mu, f1.y - mu);
                                 float2 part = make_float2(0.f, 0.f);
 #pragma unroll

@@ -20,9 +20,11 @@
 // scaled by a power of two for each row (its largest element into [128, 256)) and
 // split into parts, each the code nearest to 16 times what the part before leaves:
 // two hold a bf16 row and three an f16 row exactly, but for elements more than
-// 2^13 (2^14) below the row's largest, which lose at most 2^-21 of it. p_r, at most 2^8.5, is
-// two parts: p_r to 2^-8 of itself (a bf16's half step) and 2^-14 absolutely, 2^-16.5 of
-// the largest. Parts are further columns of a product (an instruction takes as
+// 2^13 (2^14) below the row's largest, which lose at most 2^-21 of it. p_r, at most
+// 2^8.5, is rounded to f16 and then split likewise: for a bf16 output two parts, p_r to 2^-8
+// of itself (a bf16's half step) and 2^-14 absolutely, 2^-16.5 of the largest; for an f16
+// output three, to 2^-12 beside the f16's own 2^-11 (two made the error of an f16 output
+// 1.5 times that of its rounding alone). Parts are further columns of a product (an instruction takes as
 // long for 16 columns as for 128), added up in f32: those of S when it is read, those of O at
 // the end. l takes the f32 weights before rounding. S, x, sums and O are f32.
 //
@@ -35,6 +37,13 @@
 // slots for each line. Roles of a line: four softmax warps (a thread owns a token),
 // an mma warp, producers (TMA copies of the codes, cp.async of the scales), and a
 // warp that walks the segments and writes the parts of a segment's q ahead of time.
+//
+// What bounds it. Each product instruction takes 80 to 90 cycles to issue whatever
+// N is up to 128, 4 for S and 4 for O of a tile at head_dim 128, and the softmax is
+// short; the copies keep two lines of an SM at the rate that TMA boxes of a page
+// come in. 4 requests of 65,536 tokens, 4 kv heads of 128, 16 rows, bf16: 89 us
+// between events (widened codes: 126); 32 of 512 to 4096 tokens, 16 kv heads, one row:
+// 89 (201). From 17 rows on see pick_blocks.
 //
 // Whoever waits on a barrier takes part in its next phase, or waits for a load
 // whose slot cannot be filled again before it has given its weights.
@@ -87,18 +96,19 @@ __device__ __forceinline__ __half2 codes_half2(uint32_t w) {
 
 // ---------------------------------------------------------------- configuration
 
-template <int D, int R, int kQParts>
+// kParts: of an element of q (f16: 3, bf16: 2), and of a weight.
+template <int D, int R, int kParts>
 struct CfgBlocks {
     static constexpr int kKeys = 128;                     // tokens of a tile, the M of S^T
     static_assert(R == 16 || R == 32, "rows of a segment");
-    static constexpr int kLines = D <= 128 ? 2 : 1;
+    static constexpr int kLines = D <= 128 && kParts * R <= 64 ? 2 : 1;  // what tensor memory holds
     static constexpr int kRowBytes = D < 128 ? D : 128;   // of a column block of codes
     static constexpr int kColBlocks = D / kRowBytes;
     static constexpr int kMode = kRowBytes == 128 ? 2 : 4;
     static constexpr int kSlotBytes = kKeys * D;
-    static constexpr int kQRows = kQParts * R, kQBytes = kQRows * D;  // part p of row r is row p R + r
+    static constexpr int kQRows = kParts * R, kQBytes = kQRows * D;  // part p of row r is row p R + r
     static constexpr int kQBufs = 2;
-    static constexpr int kPPart = kKeys * R, kPBytes = 2 * kPPart, kPBufs = 2;
+    static constexpr int kPPart = kKeys * R, kPBytes = kParts * kPPart, kPBufs = 2;
     static constexpr int kProducers = kLines == 2 ? 2 : 4;
     static constexpr int kOthers = 2 + kProducers;        // mma, producers, walker
     static constexpr int kSoftWarps = 4;                  // of a line
@@ -135,10 +145,10 @@ struct CfgBlocks {
     static constexpr int kCtlOff = kLines * kLineBytes;
     static constexpr int kMiscOff = kCtlOff + kLines * kCtlBytes;  // tensor-memory address, abort flag
     static constexpr int kBytes = kMiscOff + 16 + 1024;            // 1024: alignment of the base
-    // tensor memory of a line: two S buffers (a column for each part of a row), then for each column block O of the weights'
-    // first parts and of their second ones
+    // tensor memory of a line: two S buffers (a column for each part of a row), then for each column block O of each part
+    // of the weights
     static constexpr int kOCol = 2 * kQRows;
-    static constexpr int kLineCols = kOCol + kColBlocks * 2 * R;
+    static constexpr int kLineCols = kOCol + kColBlocks * kParts * R;
     static_assert(kLines * kLineCols <= 512, "tensor memory");
     static_assert(kSlots >= 3 && kBytes <= 232448, "shared memory");
     static_assert(kLineBytes % 1024 == 0 && kQBytes % 1024 == 0 && kPBytes % 1024 == 0 && kSlotBytes % 1024 == 0, "alignment");
@@ -149,10 +159,10 @@ struct CfgBlocks {
 // ---------------------------------------------------------------- the kernel
 
 template <typename T, int D, int R>
-__global__ void __launch_bounds__(CfgBlocks<D, R, sizeof(T) == 2 && std::is_same<T, __half>::value ? 3 : 2>::kThreads, 1)
+__global__ void __launch_bounds__(CfgBlocks<D, R, std::is_same<T, __half>::value ? 3 : 2>::kThreads, 1)
     blocks_tc_kernel(const TreeArgs a, const __grid_constant__ CUtensorMap tmk, const __grid_constant__ CUtensorMap tmv) {
-    constexpr int kQParts = std::is_same<T, __half>::value ? 3 : 2;
-    using C = CfgBlocks<D, R, kQParts>;
+    constexpr int kParts = std::is_same<T, __half>::value ? 3 : 2;
+    using C = CfgBlocks<D, R, kParts>;
     constexpr float kShift = 2.5f, kRise = 6.f;  // weights: 2^kShift at the maximum, at most 2^(kShift + kRise) < 448
     constexpr float kLeastV = 1.2621774e-29f;    // 2^-96: smaller V scales count so for the maximum (the sums stay below 2^128)
     const float kNegInf = -__int_as_float(0x7f800000);
@@ -239,7 +249,7 @@ __global__ void __launch_bounds__(CfgBlocks<D, R, sizeof(T) == 2 && std::is_same
     if (!soft && part == 0) {
         // ================================================================ mma
         const bool lead = lane == 0;
-        constexpr uint32_t idesc_s = tc_idesc_codes(C::kKeys, C::kQRows, false, false), idesc_o = tc_idesc_codes(128, 2 * R, true, true);
+        constexpr uint32_t idesc_s = tc_idesc_codes(C::kKeys, C::kQRows, false, false), idesc_o = tc_idesc_codes(128, kParts * R, true, true);
         constexpr uint32_t kGroup = 8 * C::kRowBytes;  // bytes of 8 rows
         const uint64_t kdesc = smem_desc(sbase + C::kRingOff, 16, kGroup, C::kMode);
         // (head_dim 64: M is 128 all the same, its second half the first once more, at no step)
@@ -321,7 +331,7 @@ __global__ void __launch_bounds__(CfgBlocks<D, R, sizeof(T) == 2 && std::is_same
             for (int cb = 0; cb < C::kColBlocks; ++cb)
 #pragma unroll
                 for (int k = 0; k < C::kKeys / 32; ++k)
-                    tc_mma_codes(tmem + C::kOCol + cb * 2 * R, vb + (cb * C::kKeys * C::kRowBytes + k * 32 * C::kRowBytes) / 16,
+                    tc_mma_codes(tmem + C::kOCol + cb * kParts * R, vb + (cb * C::kKeys * C::kRowBytes + k * 32 * C::kRowBytes) / 16,
                                  pb + k * 512 / 16, idesc_o, !fresh || k > 0, lead);
             tc_commit_if(bar(C::kPvDone + buf), lead);
             tc_commit_if(bar(C::kEmpty + vs), lead);
@@ -499,7 +509,7 @@ __global__ void __launch_bounds__(CfgBlocks<D, R, sizeof(T) == 2 && std::is_same
 #pragma unroll
                     for (int y = 0; y < kPer; ++y) f[y] *= by;
 #pragma unroll
-                    for (int p = 0; p < kQParts; ++p) {
+                    for (int p = 0; p < kParts; ++p) {
                         uint32_t codes[(kPer + 3) / 4] = {};
 #pragma unroll
                         for (int y = 0; y < kPer; y += 2) {
@@ -585,7 +595,7 @@ __global__ void __launch_bounds__(CfgBlocks<D, R, sizeof(T) == 2 && std::is_same
                     const uint32_t at = ts0 + buf * C::kQRows + c;
                     tmem_ld16(at, *reinterpret_cast<uint32_t(*)[16]>(x + c));
                     tmem_ld16(at + R, *reinterpret_cast<uint32_t(*)[16]>(part));
-                    if (kQParts > 2) tmem_ld16(at + 2 * R, *reinterpret_cast<uint32_t(*)[16]>(last));
+                    if (kParts > 2) tmem_ld16(at + 2 * R, *reinterpret_cast<uint32_t(*)[16]>(last));
                 };
                 load_parts(0);
                 if (quad == 0 && lane == 0) mbar_arrive(bar(C::kEmpty + ring.slot));  // S is there: K has been read
@@ -605,7 +615,7 @@ __global__ void __launch_bounds__(CfgBlocks<D, R, sizeof(T) == 2 && std::is_same
                     for (int e = 0; e < 16; e += 2) {
                         const float2 by = make_float2(0.0625f, 0.0625f);
                         float2 y = make_float2(part[e], part[e + 1]);
-                        if (kQParts > 2) y = __ffma2_rn(make_float2(last[e], last[e + 1]), by, y);
+                        if (kParts > 2) y = __ffma2_rn(make_float2(last[e], last[e + 1]), by, y);
                         y = __ffma2_rn(y, by, make_float2(x[c + e], x[c + e + 1]));
                         x[c + e] = y.x;
                         x[c + e + 1] = y.y;
@@ -711,7 +721,7 @@ __global__ void __launch_bounds__(CfgBlocks<D, R, sizeof(T) == 2 && std::is_same
 #pragma unroll
                         for (int c = 0; c < R; ++c) l[c] *= wf[c];
 #pragma unroll 1
-                        for (int cb = 0; cb < 2 * C::kColBlocks; ++cb)  // both parts' O of each column block
+                        for (int cb = 0; cb < kParts * C::kColBlocks; ++cb)  // each part's O of each column block
 #pragma unroll
                             for (int c = 0; c < R; c += 16) {
                                 uint32_t o[16];
@@ -724,7 +734,7 @@ __global__ void __launch_bounds__(CfgBlocks<D, R, sizeof(T) == 2 && std::is_same
                         tmem_wait_st();
                     }
                 }
-                // ---- weights and their parts, the second one 16 times what the first leaves
+                // ---- weights and their parts, each 16 times what the one before leaves
                 if (jobs >= C::kPBufs && !(ok = wait(C::kPvDone + pbuf, uint32_t((jobs - C::kPBufs) / C::kPBufs) & 1u))) break;
                 uint8_t* pp = smem + C::kPOff + pbuf * C::kPBytes + tok * 16;
                 const float2 vs2 = make_float2(vs, vs);
@@ -732,7 +742,7 @@ __global__ void __launch_bounds__(CfgBlocks<D, R, sizeof(T) == 2 && std::is_same
 #pragma unroll
                     for (int c = 0; c < R; c += 8) {
                         if (c >= cols) break;
-                        uint32_t p1[4], p2[4];
+                        uint32_t p1[4], p2[4], p3[4];
 #pragma unroll
                         for (int e = 0; e < 4; ++e) {
                             const float2 y = make_float2(ex2(x[c + 2 * e]), ex2(x[c + 2 * e + 1]));
@@ -746,11 +756,15 @@ __global__ void __launch_bounds__(CfgBlocks<D, R, sizeof(T) == 2 && std::is_same
                             l[c + 2 * e + 1] = sum.y;
                             const __half2 h = __floats2half2_rn(w.x, w.y);
                             p1[e] = half2_codes(h);
-                            p2[e] = half2_codes(__hmul2(__hsub2(h, codes_half2(p1[e])), __float2half2_rn(16.f)));
+                            const __half2 left = __hmul2(__hsub2(h, codes_half2(p1[e])), __float2half2_rn(16.f));
+                            p2[e] = half2_codes(left);
+                            if (kParts > 2) p3[e] = half2_codes(__hmul2(__hsub2(left, codes_half2(p2[e])), __float2half2_rn(16.f)));
                         }
                         uint8_t* at = pp + c / 16 * 2048 + c % 16;
                         *reinterpret_cast<uint2*>(at) = make_uint2(__byte_perm(p1[0], p1[1], 0x5410), __byte_perm(p1[2], p1[3], 0x5410));
                         *reinterpret_cast<uint2*>(at + C::kPPart) = make_uint2(__byte_perm(p2[0], p2[1], 0x5410), __byte_perm(p2[2], p2[3], 0x5410));
+                        if (kParts > 2)
+                            *reinterpret_cast<uint2*>(at + 2 * C::kPPart) = make_uint2(__byte_perm(p3[0], p3[1], 0x5410), __byte_perm(p3[2], p3[3], 0x5410));
                     }
                 };
                 if (guard)
@@ -789,10 +803,11 @@ __global__ void __launch_bounds__(CfgBlocks<D, R, sizeof(T) == 2 && std::is_same
             for (int x = 0; x < C::kColBlocks * (R / 16); ++x) {
                 const int cb = x / (R / 16), c = x % (R / 16) * 16;
                 if (c >= cols) continue;
-                uint32_t o[16], o2[16];
+                uint32_t o[16], o2[16], o3[16];
                 __syncwarp();
-                tmem_ld16(to + cb * 2 * R + c, o);
-                tmem_ld16(to + cb * 2 * R + R + c, o2);
+                tmem_ld16(to + cb * kParts * R + c, o);
+                tmem_ld16(to + cb * kParts * R + R + c, o2);
+                if (kParts > 2) tmem_ld16(to + cb * kParts * R + 2 * R + c, o3);
                 tmem_wait_ld();
                 const int dim = cb * 128 + tok;
                 if (dim >= D) continue;  // (head_dim 64: the second half of M)
@@ -800,7 +815,9 @@ __global__ void __launch_bounds__(CfgBlocks<D, R, sizeof(T) == 2 && std::is_same
                 for (int e = 0; e < 16; ++e) {
                     const long long at = c + e < cols ? rowat[qb * R + c + e] : -1;
                     if (at < 0) continue;
-                    float f = fmaf(__uint_as_float(o2[e]), 0.0625f, __uint_as_float(o[e])) * wf[c + e];
+                    float f = __uint_as_float(o2[e]);
+                    if (kParts > 2) f = fmaf(__uint_as_float(o3[e]), 0.0625f, f);
+                    f = fmaf(f, 0.0625f, __uint_as_float(o[e])) * wf[c + e];
                     if (fix) {
                         // NaN of node rows in these blocks, for the rows that attend them
                         const int node = rownode[qb * R + c + e];
@@ -860,11 +877,6 @@ bool blocks_tc_lookup(int D, TreeKernels* k) {
         case 256: *k = blocks_tc_kernels<T, 256, R>(); return true;
     }
     return false;
-}
-
-template <typename T>
-bool blocks_tc_by_rows(int D, int rows, TreeKernels* k) {
-    return rows > 16 ? blocks_tc_lookup<T, 32>(D, k) : blocks_tc_lookup<T, 16>(D, k);
 }
 
 }  // namespace pd

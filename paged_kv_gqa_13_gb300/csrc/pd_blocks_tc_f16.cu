@@ -2,5 +2,5 @@
 #include "pd_blocks_tc.cuh"
 
 namespace pd {
-bool blocks_tc_f16(int head_dim, int rows, TreeKernels* k) { return blocks_tc_by_rows<__half>(head_dim, rows, k); }
+bool blocks_tc_f16(int head_dim, TreeKernels* k) { return blocks_tc_lookup<__half, 16>(head_dim, k); }
 }  // namespace pd

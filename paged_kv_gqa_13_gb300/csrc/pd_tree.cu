@@ -59,11 +59,17 @@ bool pick(pd_dtype dt, bool fp8, int D, int group, Rows rows, TreeKernels* k) {
     return false;
 }
 
-// Block-scaled pools: the kernel by the rows of a request on average. Up to 32 rows meet the codes as operands, in row
-// tiles of 16 or 32; more rows pay for widening the codes to f16 once, in row tiles of 128 or two of 128.
-bool pick_blocks(pd_dtype dt, int D, int block, long long rows, TreeKernels* k) {
-    if (rows <= 32) return dt == PD_F16 ? blocks_tc_f16(D, int(rows), k) : blocks_tc_bf16(D, int(rows), k);
-    if (block % 16 == 0) return dt == PD_F16 ? blocks_wide16_f16(D, k) : blocks_wide16_bf16(D, k);
+// Block-scaled pools: the kernel by the rows of a request on average and the pairs of a request and a kv head. Few rows
+// meet the codes as operands, in row tiles of 16 or 32 (f16, with more parts of everything: 16); more pay for widening the
+// codes to f16 once, in row tiles of 128 or two of 128. 512 to 4096 tokens, head_dim 128, blocks of 16 tokens, bf16, as
+// operands and widened: 16 rows, 128 pairs 56 and 63 us; 32 rows, 64 pairs 62 and 41, 256 pairs 109 and 109, 512 pairs 192
+// and 211. With a scale for each token: 32 rows, 64 pairs 61 and 50, 128 pairs 77 and 80, 512 pairs 188 and 250 (f16: 267
+// and 249).
+bool pick_blocks(pd_dtype dt, int D, int block, long long rows, long long pairs, TreeKernels* k) {
+    const bool runs = block % 16 == 0;  // 16 keys share their scales
+    if (rows <= 16 || (rows <= 32 && dt == PD_BF16 && pairs >= (runs ? 256 : 128)))
+        return dt == PD_F16 ? blocks_tc_f16(D, k) : blocks_tc_bf16(D, int(rows), k);
+    if (runs) return dt == PD_F16 ? blocks_wide16_f16(D, k) : blocks_wide16_bf16(D, k);
     return dt == PD_F16 ? blocks_wide_f16(D, k) : blocks_wide_bf16(D, k);
 }
 
@@ -164,7 +170,7 @@ pd_status tree_impl(const void* q, const void* k_data, const void* v_data, const
                       : all_rows > 16ll * batch ? kRows64
                       : all_rows > 8ll * batch  ? kRows16
                                                 : kRows8;
-    if (!(block > 0 ? pick_blocks(dt, D, block, (all_rows + batch - 1) / batch, &kn) : pick(dt, fp8, D, group, rows, &kn)))
+    if (!(block > 0 ? pick_blocks(dt, D, block, (all_rows + batch - 1) / batch, (long long)batch * Hk, &kn) : pick(dt, fp8, D, group, rows, &kn)))
         return host::fail(PD_ERR_UNSUPPORTED, "no kernel for this type and head_dim");
     int sms = 0;
     if ((st = host::sm_count(&sms)) != PD_OK) return st;
@@ -316,7 +322,7 @@ size_t pd_paged_tree_decode_fp8_blocks_workspace_bytes(int num_qo_heads, int num
     for (int rows = 16; rows <= 64; rows *= 2) {
         for (int block = 1; block <= 16; block += 15) {
             TreeKernels k{};
-            if (!pick_blocks(dtype, head_dim, block, rows, &k)) continue;
+            if (!pick_blocks(dtype, head_dim, block, rows, 1 << 20, &k)) continue;
             const size_t n = space(k, sms * k.per_sm, head_dim).bytes;
             if (n > most) most = n;
         }

@@ -21,7 +21,7 @@ bool tree_tc_f16_fp8(int head_dim, bool wide, TreeKernels* k);
 bool tree_tc_bf16_fp8(int head_dim, bool wide, TreeKernels* k);
 // over block-scaled E4M3 pools: up to 16 or 32 rows a row tile; many rows, with any blocks or (16) blocks of a multiple of
 // 16 rows
-bool blocks_tc_f16(int head_dim, int rows, TreeKernels* k);
+bool blocks_tc_f16(int head_dim, TreeKernels* k);
 bool blocks_tc_bf16(int head_dim, int rows, TreeKernels* k);
 bool blocks_wide_f16(int head_dim, TreeKernels* k);
 bool blocks_wide_bf16(int head_dim, TreeKernels* k);

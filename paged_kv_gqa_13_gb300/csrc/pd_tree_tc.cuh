@@ -37,6 +37,15 @@
 // instructions), so both products run in f16 for bf16 q too: the softmax warps
 // write q rows as f16 times a power of two each.
 //
+// Block-scaled E4M3 pools (kPoolBlocks, kPoolBlocks16): the scales of a block's
+// keys come by cp.async beside its codes. k_scale multiplies a key's scores and
+// log2 of v_scale is added to their exponents, so that the weights that meet the
+// codes, and the running maximum, are of what a key can bring to the output; the
+// sum l takes them over v_scale again. Blocks of a multiple of 16 rows: one pair
+// of scales for 16 keys (64 trees of 1 to 32 nodes, 8 heads a group, bf16: 172 us
+// between events, 149 with a scale per head; 4 chunks of 1021 tokens: 477 and 414);
+// others: a pair for each key (204 and 622 us).
+//
 // Rounding. S, maxima, sums and O are f32. The weights are rounded to the
 // operand type, at most half a step each, because both operands of a product
 // have one type and V is 16-bit in memory: f32 weights would take V widened to
@@ -840,8 +849,8 @@ __global__ void __launch_bounds__(CfgTree<D, kWide, kPool>::kThreads, 1)
                 for (int half = 0; half < C::kJobs; ++half) {
                     const int buf = jobs & 1;
                     if (kBlocks && live && half * C::kJobKeys % C::kReadyKeys == 0) {
-                        // The scales of each run of keys, of this job or of the block, before the scores are there: {k, log2 v,
-                        // 1 / v}, v at least 2^-96 (the sums stay below 2^128).
+                        // The scales of each run of keys, of this job or of the block, before the scores are there: k, log2 v
+                        // and 1 / v, v at least 2^-96 (the sums stay below 2^128); runs of one key as three arrays.
                         if (half == 0 && !(ok = wait(C::kScFull + sc.slot, sc.phase))) break;
                         const float* from = reinterpret_cast<const float*>(ctl + C::kScaleOff) + sc.slot * 2 * C::kKeys;
                         __syncwarp();
@@ -849,7 +858,14 @@ __global__ void __launch_bounds__(CfgTree<D, kWide, kPool>::kThreads, 1)
                         for (int g = lane; g < C::kReadyRuns; g += 32) {
                             const int key = half * C::kJobKeys + g * C::kRun, at = C::kRun == 16 || a.run > 1 ? key / 4 : key;
                             const float v = fmaxf(from[C::kKeys + at], 1.2621774e-29f);
-                            ready[g] = make_float4(from[at], __log2f(v), __frcp_rn(v), 0.f);
+                            if constexpr (C::kRun > 1) {
+                                ready[g] = make_float4(from[at], __log2f(v), __frcp_rn(v), 0.f);
+                            } else {
+                                float* to = reinterpret_cast<float*>(ready) + g;
+                                to[0] = from[at];
+                                to[C::kJobKeys] = __log2f(v);
+                                to[2 * C::kJobKeys] = __frcp_rn(v);
+                            }
                         }
                         __syncwarp();
                     }
@@ -862,6 +878,21 @@ __global__ void __launch_bounds__(CfgTree<D, kWide, kPool>::kThreads, 1)
                         tmem_ld32(ts + 32, x + 32);
                         const unsigned bad_pages = bad_slots[(kblocks + blk - blk0) % C::kBadRing];
                         tmem_wait_ld();
+                        const float4* runs = ready + half * C::kJobKeys % C::kReadyKeys / C::kRun;  // this job's
+                        if constexpr (kBlocks && C::kRun == 1) {
+                            // scores in the exponent's unit, with log2 of the V scale: what a key can bring to the output
+#pragma unroll
+                            for (int e = 0; e < C::kJobKeys; e += 4) {
+                                const float4 k = runs[e / 4], v = runs[(C::kJobKeys + e) / 4];
+                                const float2 sc2 = make_float2(scale, scale);
+                                const float2 y = __ffma2_rn(make_float2(__uint_as_float(x[e]), __uint_as_float(x[e + 1])),
+                                                            __fmul2_rn(make_float2(k.x, k.y), sc2), make_float2(v.x, v.y));
+                                const float2 z = __ffma2_rn(make_float2(__uint_as_float(x[e + 2]), __uint_as_float(x[e + 3])),
+                                                            __fmul2_rn(make_float2(k.z, k.w), sc2), make_float2(v.z, v.w));
+                                x[e] = __float_as_uint(y.x), x[e + 1] = __float_as_uint(y.y);
+                                x[e + 2] = __float_as_uint(z.x), x[e + 3] = __float_as_uint(z.y);
+                            }
+                        }
                         if (!packed || bad_pages != 0u || blk >= tail0) {
                             const int nd = min(node, r.n - 1);
 #pragma unroll
@@ -888,9 +919,8 @@ __global__ void __launch_bounds__(CfgTree<D, kWide, kPool>::kThreads, 1)
                         }
                         // (block scales: a factor above 0 leaves minus infinity what it is)
                         auto factor = [&](const float4& f) { return fmaxf(scale * f.x, 1e-38f); };
-                        const float4* runs = ready + half * C::kJobKeys % C::kReadyKeys / C::kRun;  // this job's
                         float top;
-                        if constexpr (kBlocks) {
+                        if constexpr (kBlocks && C::kRun > 1) {
                             // what a key can bring to the output: its score and its V scale
                             top = kNegInf;
 #pragma unroll
@@ -908,7 +938,7 @@ __global__ void __launch_bounds__(CfgTree<D, kWide, kPool>::kThreads, 1)
                             for (int c = 0; c < 4; ++c) tops[c] = __uint_as_float(x[c]);
 #pragma unroll
                             for (int c = 4; c < C::kJobKeys; ++c) tops[c % 4] = fmaxf(tops[c % 4], __uint_as_float(x[c]));
-                            top = fmaxf(fmaxf(tops[0], tops[1]), fmaxf(tops[2], tops[3])) * scale;
+                            top = fmaxf(fmaxf(tops[0], tops[1]), fmaxf(tops[2], tops[3])) * (kBlocks ? 1.f : scale);
                         }
                         if (blk == blk0 && half == 0) {
                             m = top;
@@ -938,22 +968,34 @@ __global__ void __launch_bounds__(CfgTree<D, kWide, kPool>::kThreads, 1)
                         float2 sums[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
                         const float2 sc2 = make_float2(scale, scale), mu2 = make_float2(-mu, -mu);
                         uint32_t w[C::kJobKeys / 2];
-                        if constexpr (kBlocks) {
+                        if constexpr (kBlocks && C::kRun > 1) {
                             // the V scale as an addend of the exponent: the weights that meet the codes; out of the sums again
 #pragma unroll
-                            for (int g = 0; g < C::kJobKeys / (C::kRun > 1 ? C::kRun : 2); ++g) {
-                                constexpr int kOf = C::kRun > 1 ? C::kRun : 2;
-                                const float4 f = runs[C::kRun > 1 ? g : 2 * g], f1 = C::kRun > 1 ? f : runs[2 * g + 1];
-                                const float2 by = make_float2(factor(f), factor(f1)), add = make_float2(f.y - mu, f1.y - mu);
+                            for (int g = 0; g < C::kJobKeys / C::kRun; ++g) {
+                                const float4 f = runs[g];
+                                const float2 by = make_float2(factor(f), factor(f)), add = make_float2(f.y - mu, f.y - mu);
                                 float2 part = make_float2(0.f, 0.f);
 #pragma unroll
-                                for (int e = g * kOf; e < (g + 1) * kOf; e += 2) {
+                                for (int e = g * C::kRun; e < (g + 1) * C::kRun; e += 2) {
                                     float2 y = __ffma2_rn(make_float2(__uint_as_float(x[e]), __uint_as_float(x[e + 1])), by, add);
                                     y = make_float2(ex2(y.x), ex2(y.y));
-                                    part = kOf > 2 ? __fadd2_rn(part, y) : y;
+                                    part = __fadd2_rn(part, y);
                                     w[e / 2] = Elt<M>::pack(y.x, y.y);
                                 }
-                                sums[g % 2] = __ffma2_rn(part, make_float2(f.z, f1.z), sums[g % 2]);
+                                sums[g % 2] = __ffma2_rn(part, make_float2(f.z, f.z), sums[g % 2]);
+                            }
+                        } else if constexpr (kBlocks) {
+#pragma unroll
+                            for (int e = 0; e < C::kJobKeys; e += 4) {
+                                const float4 out = runs[(2 * C::kJobKeys + e) / 4];
+                                float2 y = __fadd2_rn(make_float2(__uint_as_float(x[e]), __uint_as_float(x[e + 1])), mu2);
+                                float2 z = __fadd2_rn(make_float2(__uint_as_float(x[e + 2]), __uint_as_float(x[e + 3])), mu2);
+                                y = make_float2(ex2(y.x), ex2(y.y));
+                                z = make_float2(ex2(z.x), ex2(z.y));
+                                sums[0] = __ffma2_rn(y, make_float2(out.x, out.y), sums[0]);
+                                sums[1] = __ffma2_rn(z, make_float2(out.z, out.w), sums[1]);
+                                w[e / 2] = Elt<M>::pack(y.x, y.y);
+                                w[e / 2 + 1] = Elt<M>::pack(z.x, z.y);
                             }
                         } else {
 #pragma unroll

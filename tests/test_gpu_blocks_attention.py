@@ -357,3 +357,29 @@ def test_the_cache_that_the_append_writes():
         # parts of a weight 2^-8, the result's half step 2^-8, at values below 5
         assert float((o.double() - ref).abs().max()) <= 2 * 2.0 ** -8 * 5
         assert float((lse.double() - torch.logsumexp(xs, -1)).abs().max()) <= 1e-4
+
+
+@pytest.mark.parametrize("hq,hk,d,page,block", [(96, 4, 128, 16, 16), (48, 2, 64, 16, 4), (64, 2, 256, 8, 8), (100, 4, 64, 32, 32)])
+@pytest.mark.parametrize("dtype", ["f16", "bf16"])
+def test_many_requests_of_17_to_32_rows(dtype, hq, hk, d, page, block):
+    rng = np.random.default_rng(hq)
+    kv = [5000, 0, 1, 31] + rng.integers(1, 300, 68).tolist()
+    c = BlockPaged(kv, hk, d, page, block, seed=hq + d)
+    q = _q(len(kv), hq, d, dtype)
+    flags, o, lse = _run(c, q, single=True)
+    assert flags == 0
+    check_attention(o, lse, attend_reference(c, q, None, 1 / math.sqrt(d), dtype))
+
+
+@pytest.mark.parametrize("block", [16, 2])
+@pytest.mark.parametrize("kind", ["chain", "tree", "random"])
+def test_many_trees_of_17_to_32_rows(block, kind):
+    rng = np.random.default_rng(block)
+    new = rng.integers(6, 18, 72).tolist()
+    kv = [n + int(x) for n, x in zip(new, rng.integers(0, 400, 72))]
+    c = BlockPaged(kv, 4, 128, 16, block, new, seed=block)
+    masks = None if kind == "chain" else [tree_bits(rng, n, kind) for n in new]
+    q = _q(sum(new), 8, 128, "bf16")
+    flags, o, lse = _run(c, q, masks)
+    assert flags == 0
+    check_attention(o, lse, attend_reference(c, q, masks, 1 / math.sqrt(128), "bf16"))

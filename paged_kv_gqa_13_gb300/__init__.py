@@ -629,17 +629,18 @@ def pd_norm_rope(q, k, q_weight, k_weight, positions, freqs, q_out, k_out, eps: 
                              _stream_for(q, stream)))
 
 
-def _norm_append(fn, scales, blocks, q, k_new, v_new, q_weight, k_weight, positions, freqs, q_out, k_data, v_data, indices,
+def _norm_append(fn, scales, blocks, pools, q, k_new, v_new, q_weight, k_weight, positions, freqs, q_out, k_data, v_data, indices,
                  indptr, last_page_len, new_indptr, workspace, eps, layout, rope_scale, stream):
-    total_new, num_kv_heads, head_dim = k_new.shape
-    num_total_pages, hk, page_size, d = _pools(k_data, v_data)
-    dtype = k_new.dtype
-    if hk != num_kv_heads or d != head_dim or v_new.shape != k_new.shape or v_new.dtype != dtype:
+    rows, dtype = k_new.shape, k_new.dtype
+    total_new, num_kv_heads, head_dim = rows
+    num_total_pages, hk, page_size, d = pools
+    if hk != num_kv_heads or d != head_dim or v_new.shape != rows or v_new.dtype != dtype:
         _bad("k_new, v_new and the pools differ in heads, head_dim or type")
     qp, qs, op, num_qo_heads = None, 0, None, 0
     if q is not None:
-        num_qo_heads = q.shape[1]
-        if q.shape[0] != total_new or q.shape[2] != head_dim or q_out.shape != q.shape or q.dtype != dtype or q_out.dtype != dtype:
+        q_rows = q.shape
+        tokens, num_qo_heads, q_dim = q_rows
+        if tokens != total_new or q_dim != head_dim or q_out.shape != q_rows or q.dtype != dtype or q_out.dtype != dtype:
             _bad("q holds one row for each new token, typed as k_new, and q_out is shaped and typed as q")
         qp, qs, op = q.data_ptr(), _token_stride(q, num_qo_heads, head_dim), _ptr(q_out)
     if positions is not None and positions.shape[0] != total_new:
@@ -659,7 +660,7 @@ def pd_paged_norm_rope_append(q, k_new, v_new, q_weight, k_weight, positions, fr
     """pd_paged_rope_append with the norms of pd_norm_rope in front (q_weight, k_weight [D] or None)."""
     if k_data.dtype != k_new.dtype:
         _bad("the pools have the type of k_new")
-    _norm_append(_lib.pd_paged_norm_rope_append, (), (), q, k_new, v_new, q_weight, k_weight, positions, freqs, q_out, k_data,
+    _norm_append(_lib.pd_paged_norm_rope_append, (), (), _pools(k_data, v_data), q, k_new, v_new, q_weight, k_weight, positions, freqs, q_out, k_data,
                  v_data, indices, indptr, last_page_len, new_indptr, workspace, eps, layout, rope_scale, stream)
 
 
@@ -667,25 +668,34 @@ def pd_paged_norm_rope_append_fp8(q, k_new, v_new, q_weight, k_weight, positions
                                   v_data, indices, indptr, last_page_len, new_indptr, workspace, eps: float = 1e-6,
                                   layout: int = PD_ROPE_HALF, rope_scale: float = 1.0, stream=None) -> None:
     """pd_paged_norm_rope_append into E4M3 pools (k_data, v_data uint8; scales f32 [Hk])."""
-    _norm_append(_lib.pd_paged_norm_rope_append_fp8, _scales(k_scale, v_scale, k_data), (), q, k_new, v_new, q_weight,
-                 k_weight, positions, freqs, q_out, k_data, v_data, indices, indptr, last_page_len, new_indptr, workspace, eps,
+    _norm_append(_lib.pd_paged_norm_rope_append_fp8, _scales(k_scale, v_scale, k_data), (), _pools(k_data, v_data), q,
+                 k_new, v_new, q_weight, k_weight, positions, freqs, q_out, k_data, v_data, indices, indptr, last_page_len, new_indptr, workspace, eps,
                  layout, rope_scale, stream)
 
 
 # --- block-scaled pools: k_data, v_data uint8 E4M3 [pages, Hk, page_size, D]; k_scale, v_scale f32
 # [pages, Hk, page_size / block_tokens], a scale for each block of rows of a page and kv head ---------------------------
 
-def _block_scales(k_scale, v_scale, k_data):
-    """(pointers, block_tokens)"""
-    pages, hk, page_size, _ = k_data.shape
+def _is_f32(t) -> bool:
+    if not _TYPES:
+        _torch_facts()
+    return _TYPES.get(t.dtype) == PD_F32
+
+
+def _block_scales(k_scale, v_scale, k_data, pools):
+    """(pointers, block_tokens); pools: the shape of both pools"""
+    pages, hk, page_size, _ = pools
     if k_data.element_size() != 1:
         _bad("E4M3 pools hold one byte for each element")
     shape = k_scale.shape
-    if k_scale.dtype != v_scale.dtype or shape != v_scale.shape or k_scale.element_size() != 4 or not k_scale.is_floating_point():
+    if shape != v_scale.shape or not _is_f32(k_scale) or not _is_f32(v_scale):
         _bad("k_scale and v_scale are float32 of one shape")
-    if len(shape) != 3 or shape[0] != pages or shape[1] != hk or shape[2] == 0 or page_size % shape[2]:
+    if len(shape) != 3:
         _bad("k_scale and v_scale are [pages, Hk, page_size / block_tokens]")
-    return (_ptr(k_scale), _ptr(v_scale)), page_size // shape[2]
+    p, h, per = shape
+    if p != pages or h != hk or per == 0 or page_size % per:
+        _bad("k_scale and v_scale are [pages, Hk, page_size / block_tokens]")
+    return (_ptr(k_scale), _ptr(v_scale)), page_size // per
 
 
 def pd_paged_rope_append_fp8_blocks(q, k_new, v_new, positions, freqs, q_out, k_scale, v_scale, k_data, v_data, indices,
@@ -694,9 +704,9 @@ def pd_paged_rope_append_fp8_blocks(q, k_new, v_new, positions, freqs, q_out, k_
                                     stream=None) -> None:
     """pd_paged_rope_append into block-scaled pools, whose scales it writes; eps > 0: with the norms of pd_norm_rope in
     front (q_weight, k_weight [D] or None)."""
-    _pools(k_data, v_data)
-    scales, block = _block_scales(k_scale, v_scale, k_data)
-    _norm_append(_lib.pd_paged_rope_append_fp8_blocks, scales, (block,), q, k_new, v_new, q_weight, k_weight, positions, freqs,
+    pools = _pools(k_data, v_data)
+    scales, block = _block_scales(k_scale, v_scale, k_data, pools)
+    _norm_append(_lib.pd_paged_rope_append_fp8_blocks, scales, (block,), pools, q, k_new, v_new, q_weight, k_weight, positions, freqs,
                  q_out, k_data, v_data, indices, indptr, last_page_len, new_indptr, workspace, eps, layout, rope_scale, stream)
 
 
@@ -706,8 +716,9 @@ def pd_paged_read_fp8_blocks(k_data, v_data, k_scale, v_scale, indices, indptr, 
 
     out_indptr int32 [batch + 1]; first int32 [batch] or None (token 0).
     """
-    num_total_pages, num_kv_heads, page_size, head_dim = _pools(k_data, v_data)
-    scales, block = _block_scales(k_scale, v_scale, k_data)
+    pools = _pools(k_data, v_data)
+    num_total_pages, num_kv_heads, page_size, head_dim = pools
+    scales, block = _block_scales(k_scale, v_scale, k_data, pools)
     total = k_out.shape[0]
     if k_out.shape != v_out.shape or k_out.dtype != v_out.dtype or k_out.shape[1:] != (num_kv_heads, head_dim):
         _bad("k_out and v_out are [total, Hk, D] of one type, the pools' Hk and D")
@@ -736,20 +747,20 @@ def pd_paged_tree_decode_fp8_blocks_workspace_bytes(num_qo_heads: int, num_kv_he
 
 
 def _attention(q, o, lse, k_data, v_data):
-    """Shapes and types of an attention over pools: (num_total_pages, num_kv_heads, page_size)."""
-    num_total_pages, num_kv_heads, page_size, d = _pools(k_data, v_data)
-    if d != q.shape[2] or o.shape != q.shape or o.dtype != q.dtype or lse.shape != q.shape[:2] or lse.element_size() != 4 \
-            or not lse.is_floating_point():
+    """Shapes and types of an attention over pools: the pools' shape."""
+    pools, rows = _pools(k_data, v_data), q.shape
+    if pools[3] != rows[2] or o.shape != rows or o.dtype != q.dtype or lse.shape != rows[:2] or not _is_f32(lse):
         _bad("q and o [rows, Hq, D] of one type, lse float32 [rows, Hq], the pools' D")
-    return num_total_pages, num_kv_heads, page_size
+    return pools
 
 
 def pd_paged_decode_fp8_blocks(q, k_data, v_data, k_scale, v_scale, indices, indptr, last_page_len, o, lse,
                                sm_scale: float, workspace, stream=None) -> None:
     """pd_paged_decode over block-scaled pools: q, o [batch, Hq, D] f16/bf16; lse [batch, Hq] f32."""
     rows, num_qo_heads, head_dim = q.shape
-    num_total_pages, num_kv_heads, page_size = _attention(q, o, lse, k_data, v_data)
-    scales, block = _block_scales(k_scale, v_scale, k_data)
+    pools = _attention(q, o, lse, k_data, v_data)
+    num_total_pages, num_kv_heads, page_size, _ = pools
+    scales, block = _block_scales(k_scale, v_scale, k_data, pools)
     batch, entries = last_page_len.shape[0], indices.shape[0]
     if rows != batch or indptr.shape[0] != batch + 1:
         _bad("q holds one row for each request, indptr one entry more than last_page_len")
@@ -763,8 +774,9 @@ def pd_paged_tree_decode_fp8_blocks(q, k_data, v_data, k_scale, v_scale, indices
                                     tree_mask, o, lse, sm_scale: float, workspace, stream=None) -> None:
     """pd_paged_tree_decode over block-scaled pools: q, o [total_new, Hq, D] f16/bf16; lse [total_new, Hq] f32."""
     total_new, num_qo_heads, head_dim = q.shape
-    num_total_pages, num_kv_heads, page_size = _attention(q, o, lse, k_data, v_data)
-    scales, block = _block_scales(k_scale, v_scale, k_data)
+    pools = _attention(q, o, lse, k_data, v_data)
+    num_total_pages, num_kv_heads, page_size, _ = pools
+    scales, block = _block_scales(k_scale, v_scale, k_data, pools)
     words = 0
     if tree_mask is not None:
         if tree_mask.dim() != 2 or tree_mask.shape[0] != total_new or (total_new and tree_mask.shape[1] == 0):

@@ -16,17 +16,21 @@
 // weights that meet the codes keep their precision whatever the scales are. l_r
 // sums e_r, and the output is O_r / l_r.
 //
-// Parts. Both operands of a product are E4M3, which has 4 significant bits. q is
-// scaled by a power of two for each row (its largest element into [128, 256)) and
-// split into parts, each the code nearest to 16 times what the part before leaves:
-// two hold a bf16 row and three an f16 row exactly, but for elements more than
-// 2^13 (2^14) below the row's largest, which lose at most 2^-21 of it. p_r, at most
-// 2^8.5, is rounded to f16 and then split likewise: for a bf16 output two parts, p_r to 2^-8
-// of itself (a bf16's half step) and 2^-14 absolutely, 2^-16.5 of the largest; for an f16
-// output three, to 2^-12 beside the f16's own 2^-11 (two made the error of an f16 output
-// 1.5 times that of its rounding alone). Parts are further columns of a product (an instruction takes as
-// long for 16 columns as for 128), added up in f32: those of S when it is read, those of O at
-// the end. l takes the f32 weights before rounding. S, x, sums and O are f32.
+// Parts. Both operands of a product have 8 bits. q goes in as E4M3, which has 4
+// significant bits: it is scaled by a power of two for each row (its largest element
+// into [128, 256)) and split into parts, each the code nearest to 16 times what the
+// part before leaves: two hold a bf16 row and three an f16 row exactly, but for elements
+// more than 2^13 (2^14) below the row's largest, which lose at most 2^-21 of it. The
+// weights go in as E5M2, 3 significant bits a part but f16's range: p_r, 2^9.5 to 2^15.5
+// at the row's maximum, is rounded to f16 and split into parts, each the code nearest to 8
+// times what the part before leaves: for a bf16 output three, p_r to 2^-9 of itself
+// beside the f16's 2^-11, for an f16 output four, which hold an f16 exactly. What is lost absolutely is 2^-23
+// (2^-25) of a weight, 2^-32.5 (2^-34.5) of the largest: a tail of many small weights keeps
+// its mass. (As two and three E4M3 parts a weight 2^-16.5 of the largest became
+// zero: beside one key 12 above the mean of 16,384, in natural units of the score,
+// more than half of their mass was gone.) Parts are further columns of a product (an instruction
+// takes as long for 16 columns as for 128), added up in f32: those of S when it is read, those
+// of O at the end. l takes the f32 weights before rounding. S, x, sums and O are f32.
 //
 // The maximum of a row moves only when it is passed by more than 6 (a factor of
 // 64); whether one is, is a vote of the four warps of a tile. A row then takes the
@@ -62,8 +66,9 @@ __device__ __forceinline__ uint64_t smem_desc(uint32_t addr, uint32_t lbo, uint3
            (uint64_t((sbo >> 4) & 0x3fffu) << 32) | (uint64_t(1) << 46) | (uint64_t(mode) << 61);
 }
 
-__host__ __device__ constexpr uint32_t tc_idesc_codes(int M, int N, bool a_mn, bool b_mn) {
-    return (1u << 4) | (a_mn ? 1u << 15 : 0u) | (b_mn ? 1u << 16 : 0u) | (uint32_t(N >> 3) << 17) | (uint32_t(M >> 4) << 24);
+// A of E4M3, B of E4M3 or E5M2
+__host__ __device__ constexpr uint32_t tc_idesc_codes(int M, int N, bool a_mn, bool b_mn, bool b_e5m2) {
+    return (1u << 4) | (b_e5m2 ? 1u << 10 : 0u) | (a_mn ? 1u << 15 : 0u) | (b_mn ? 1u << 16 : 0u) | (uint32_t(N >> 3) << 17) | (uint32_t(M >> 4) << 24);
 }
 
 // D (tensor memory) = A * B (+ D when acc), issued by lane 0 (`lead`) of a warp.
@@ -82,10 +87,17 @@ __device__ __forceinline__ float redux_max(float x) {
     return y;
 }
 
-__device__ __forceinline__ uint32_t half2_codes(__half2 h) {
+// The E5M2 codes nearest to a pair, and their values: an E5M2 code is the upper byte of an f16.
+__device__ __forceinline__ uint32_t half2_e5m2(__half2 h) {
     __half2_raw r;
     memcpy(&r, &h, 4);
-    return uint32_t(__nv_cvt_halfraw2_to_fp8x2(r, __NV_SATFINITE, __NV_E4M3));
+    return uint32_t(__nv_cvt_halfraw2_to_fp8x2(r, __NV_SATFINITE, __NV_E5M2));
+}
+__device__ __forceinline__ __half2 e5m2_half2(uint32_t w) {
+    const uint32_t x = __byte_perm(w, 0u, 0x1404);
+    __half2 h;
+    memcpy(&h, &x, 4);
+    return h;
 }
 __device__ __forceinline__ __half2 codes_half2(uint32_t w) {
     const uint32_t x = e4m3x2_to_f16x2(w);
@@ -96,7 +108,7 @@ __device__ __forceinline__ __half2 codes_half2(uint32_t w) {
 
 // ---------------------------------------------------------------- configuration
 
-// kParts: of an element of q (f16: 3, bf16: 2), and of a weight.
+// kParts: of an element of q (f16: 3, bf16: 2). A weight has one more.
 template <int D, int R, int kParts>
 struct CfgBlocks {
     static constexpr int kKeys = 128;                     // tokens of a tile, the M of S^T
@@ -108,7 +120,7 @@ struct CfgBlocks {
     static constexpr int kSlotBytes = kKeys * D;
     static constexpr int kQRows = kParts * R, kQBytes = kQRows * D;  // part p of row r is row p R + r
     static constexpr int kQBufs = 2;
-    static constexpr int kPPart = kKeys * R, kPBytes = kParts * kPPart, kPBufs = 2;
+    static constexpr int kPParts = kParts + 1, kPPart = kKeys * R, kPBytes = kPParts * kPPart, kPBufs = 2;
     static constexpr int kProducers = kLines == 2 ? 2 : 4;
     static constexpr int kOthers = 2 + kProducers;        // mma, producers, walker
     static constexpr int kSoftWarps = 4;                  // of a line
@@ -148,7 +160,7 @@ struct CfgBlocks {
     // tensor memory of a line: two S buffers (a column for each part of a row), then for each column block O of each part
     // of the weights
     static constexpr int kOCol = 2 * kQRows;
-    static constexpr int kLineCols = kOCol + kColBlocks * kParts * R;
+    static constexpr int kLineCols = kOCol + kColBlocks * kPParts * R;
     static_assert(kLines * kLineCols <= 512, "tensor memory");
     static_assert(kSlots >= 3 && kBytes <= 232448, "shared memory");
     static_assert(kLineBytes % 1024 == 0 && kQBytes % 1024 == 0 && kPBytes % 1024 == 0 && kSlotBytes % 1024 == 0, "alignment");
@@ -165,8 +177,9 @@ __global__ void __launch_bounds__(CfgBlocks<D, R, std::is_same<T, __half>::value
     blocks_tc_kernel(const TreeArgs a, const __grid_constant__ CUtensorMap tmk, const __grid_constant__ CUtensorMap tmv) {
     constexpr int kParts = std::is_same<T, __half>::value ? 3 : 2;
     using C = CfgBlocks<D, R, kParts>;
-    constexpr float kShift = 2.5f, kRise = 6.f;  // weights: 2^kShift at the maximum, at most 2^(kShift + kRise) < 448
-    constexpr float kLeastV = 1.2621774e-29f;    // 2^-96: smaller V scales count so for the maximum (the sums stay below 2^128)
+    constexpr int kPParts = C::kPParts;
+    constexpr float kShift = 9.5f, kRise = 6.f;  // weights: 2^kShift at the maximum, at most 2^(kShift + kRise) < 57344
+    constexpr float kLeastV = 3.2311743e-27f;    // 2^-88: smaller V scales count so for the maximum (the sums stay below 2^128)
     const float kNegInf = -__int_as_float(0x7f800000);
     extern __shared__ __align__(16) uint8_t blocks_smem[];
     uint8_t* base = blocks_smem + ((1024u - (smem_u32(blocks_smem) & 1023u)) & 1023u);
@@ -251,7 +264,7 @@ __global__ void __launch_bounds__(CfgBlocks<D, R, std::is_same<T, __half>::value
     if (!soft && part == 0) {
         // ================================================================ mma
         const bool lead = lane == 0;
-        constexpr uint32_t idesc_s = tc_idesc_codes(C::kKeys, C::kQRows, false, false), idesc_o = tc_idesc_codes(128, kParts * R, true, true);
+        constexpr uint32_t idesc_s = tc_idesc_codes(C::kKeys, C::kQRows, false, false, false), idesc_o = tc_idesc_codes(128, kPParts * R, true, true, true);
         constexpr uint32_t kGroup = 8 * C::kRowBytes;  // bytes of 8 rows
         const uint64_t kdesc = smem_desc(sbase + C::kRingOff, 16, kGroup, C::kMode);
         // (head_dim 64: M is 128 all the same, its second half the first once more, at no step)
@@ -333,7 +346,7 @@ __global__ void __launch_bounds__(CfgBlocks<D, R, std::is_same<T, __half>::value
             for (int cb = 0; cb < C::kColBlocks; ++cb)
 #pragma unroll
                 for (int k = 0; k < C::kKeys / 32; ++k)
-                    tc_mma_codes(tmem + C::kOCol + cb * kParts * R, vb + (cb * C::kKeys * C::kRowBytes + k * 32 * C::kRowBytes) / 16,
+                    tc_mma_codes(tmem + C::kOCol + cb * kPParts * R, vb + (cb * C::kKeys * C::kRowBytes + k * 32 * C::kRowBytes) / 16,
                                  pb + k * 512 / 16, idesc_o, !fresh || k > 0, lead);
             tc_commit_if(bar(C::kPvDone + buf), lead);
             tc_commit_if(bar(C::kEmpty + vs), lead);
@@ -723,7 +736,7 @@ __global__ void __launch_bounds__(CfgBlocks<D, R, std::is_same<T, __half>::value
 #pragma unroll
                         for (int c = 0; c < R; ++c) l[c] *= wf[c];
 #pragma unroll 1
-                        for (int cb = 0; cb < kParts * C::kColBlocks; ++cb)  // each part's O of each column block
+                        for (int cb = 0; cb < kPParts * C::kColBlocks; ++cb)  // each part's O of each column block
 #pragma unroll
                             for (int c = 0; c < R; c += 16) {
                                 uint32_t o[16];
@@ -736,7 +749,7 @@ __global__ void __launch_bounds__(CfgBlocks<D, R, std::is_same<T, __half>::value
                         tmem_wait_st();
                     }
                 }
-                // ---- weights and their parts, each 16 times what the one before leaves
+                // ---- weights and their parts, each 8 times what the one before leaves
                 if (jobs >= C::kPBufs && !(ok = wait(C::kPvDone + pbuf, uint32_t((jobs - C::kPBufs) / C::kPBufs) & 1u))) break;
                 uint8_t* pp = smem + C::kPOff + pbuf * C::kPBytes + tok * 16;
                 const float2 vs2 = make_float2(vs, vs);
@@ -744,7 +757,7 @@ __global__ void __launch_bounds__(CfgBlocks<D, R, std::is_same<T, __half>::value
 #pragma unroll
                     for (int c = 0; c < R; c += 8) {
                         if (c >= cols) break;
-                        uint32_t p1[4], p2[4], p3[4];
+                        uint32_t parts[kPParts][4];
 #pragma unroll
                         for (int e = 0; e < 4; ++e) {
                             const float2 y = make_float2(ex2(x[c + 2 * e]), ex2(x[c + 2 * e + 1]));
@@ -756,17 +769,18 @@ __global__ void __launch_bounds__(CfgBlocks<D, R, std::is_same<T, __half>::value
                             float2 sum = __fadd2_rn(make_float2(l[c + 2 * e], l[c + 2 * e + 1]), y);
                             l[c + 2 * e] = sum.x;
                             l[c + 2 * e + 1] = sum.y;
-                            const __half2 h = __floats2half2_rn(w.x, w.y);
-                            p1[e] = half2_codes(h);
-                            const __half2 left = __hmul2(__hsub2(h, codes_half2(p1[e])), __float2half2_rn(16.f));
-                            p2[e] = half2_codes(left);
-                            if (kParts > 2) p3[e] = half2_codes(__hmul2(__hsub2(left, codes_half2(p2[e])), __float2half2_rn(16.f)));
+                            __half2 left = __floats2half2_rn(w.x, w.y);
+#pragma unroll
+                            for (int p = 0; p < kPParts; ++p) {
+                                parts[p][e] = half2_e5m2(left);
+                                left = __hmul2(__hsub2(left, e5m2_half2(parts[p][e])), __float2half2_rn(8.f));
+                            }
                         }
                         uint8_t* at = pp + c / 16 * 2048 + c % 16;
-                        *reinterpret_cast<uint2*>(at) = make_uint2(__byte_perm(p1[0], p1[1], 0x5410), __byte_perm(p1[2], p1[3], 0x5410));
-                        *reinterpret_cast<uint2*>(at + C::kPPart) = make_uint2(__byte_perm(p2[0], p2[1], 0x5410), __byte_perm(p2[2], p2[3], 0x5410));
-                        if (kParts > 2)
-                            *reinterpret_cast<uint2*>(at + 2 * C::kPPart) = make_uint2(__byte_perm(p3[0], p3[1], 0x5410), __byte_perm(p3[2], p3[3], 0x5410));
+#pragma unroll
+                        for (int p = 0; p < kPParts; ++p)
+                            *reinterpret_cast<uint2*>(at + p * C::kPPart) =
+                                make_uint2(__byte_perm(parts[p][0], parts[p][1], 0x5410), __byte_perm(parts[p][2], parts[p][3], 0x5410));
                     }
                 };
                 if (guard)
@@ -805,11 +819,10 @@ __global__ void __launch_bounds__(CfgBlocks<D, R, std::is_same<T, __half>::value
             for (int x = 0; x < C::kColBlocks * (R / 16); ++x) {
                 const int cb = x / (R / 16), c = x % (R / 16) * 16;
                 if (c >= cols) continue;
-                uint32_t o[16], o2[16], o3[16];
+                uint32_t o[kPParts][16];  // of each part of the weights
                 __syncwarp();
-                tmem_ld16(to + cb * kParts * R + c, o);
-                tmem_ld16(to + cb * kParts * R + R + c, o2);
-                if (kParts > 2) tmem_ld16(to + cb * kParts * R + 2 * R + c, o3);
+#pragma unroll
+                for (int p = 0; p < kPParts; ++p) tmem_ld16(to + (cb * kPParts + p) * R + c, o[p]);
                 tmem_wait_ld();
                 const int dim = cb * 128 + tok;
                 if (dim >= D) continue;  // (head_dim 64: the second half of M)
@@ -817,9 +830,10 @@ __global__ void __launch_bounds__(CfgBlocks<D, R, std::is_same<T, __half>::value
                 for (int e = 0; e < 16; ++e) {
                     const long long at = c + e < cols ? rowat[qb * R + c + e] : -1;
                     if (at < 0) continue;
-                    float f = __uint_as_float(o2[e]);
-                    if (kParts > 2) f = fmaf(__uint_as_float(o3[e]), 0.0625f, f);
-                    f = fmaf(f, 0.0625f, __uint_as_float(o[e])) * wf[c + e];
+                    float f = __uint_as_float(o[kPParts - 1][e]);
+#pragma unroll
+                    for (int p = kPParts - 2; p >= 0; --p) f = fmaf(f, 0.125f, __uint_as_float(o[p][e]));  // the smallest first
+                    f *= wf[c + e];
                     if (fix) {
                         // NaN of node rows in these blocks, for the rows that attend them
                         const int node = rownode[qb * R + c + e];

@@ -33,7 +33,8 @@
 // of O at the end. l takes the f32 weights before rounding. S, x, sums and O are f32.
 //
 // The maximum of a row moves only when it is passed by more than 6 (a factor of
-// 64); whether one is, is a vote of the four warps of a tile. A row then takes the
+// 64), or when a row that has attended nothing so far has its first score; whether one is, is a
+// vote of the four warps of a tile. A row then takes the
 // new maximum over all 128 tokens, and O is rescaled in tensor memory.
 //
 // Lines, segments, ranges, tails and the merge are those of the tree decode
@@ -598,6 +599,7 @@ __global__ void __launch_bounds__(CfgBlocks<D, R, std::is_same<T, __half>::value
             }
             __syncwarp();
             float m = kNegInf;  // lane: the running maximum of row `lane`
+            unsigned unset = 0u;  // rows that have none yet: they attended no token of the tiles so far
             float l[R];
 #pragma unroll
             for (int c = 0; c < R; ++c) l[c] = 0.f;
@@ -703,7 +705,12 @@ __global__ void __launch_bounds__(CfgBlocks<D, R, std::is_same<T, __half>::value
                 bool over = fresh;
                 if (!over) {
                     const int id = exchanges + 1;
-                    if (__any_sync(kFull, top + lv > kShift + kRise) && lane == 0) votes[(id - 1) & 1] = id;
+                    bool passed = top + lv > kShift + kRise;
+                    if (unset != 0u) {
+#pragma unroll
+                        for (int c = 0; c < R; ++c) passed |= ((unset >> c) & 1u) != 0u && x[c] > kNegInf;
+                    }
+                    if (__any_sync(kFull, passed) && lane == 0) votes[(id - 1) & 1] = id;
                     if (!(ok = exchange())) break;
                     over = votes[(id - 1) & 1] == id;
                 }
@@ -726,7 +733,7 @@ __global__ void __launch_bounds__(CfgBlocks<D, R, std::is_same<T, __half>::value
                         wm[lane] = now;
                         m = to_m;
                     }
-                    __syncwarp();
+                    unset = __ballot_sync(kFull, lane < cols && m == kNegInf);
 #pragma unroll
                     for (int c = 0; c < R; ++c) x[c] += wd[c];
                     if (!fresh) {

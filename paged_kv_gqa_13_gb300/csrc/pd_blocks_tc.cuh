@@ -180,7 +180,6 @@ __global__ void __launch_bounds__(CfgBlocks<D, R, std::is_same<T, __half>::value
     using C = CfgBlocks<D, R, kParts>;
     constexpr int kPParts = C::kPParts;
     constexpr float kShift = 9.5f, kRise = 6.f;  // weights: 2^kShift at the maximum, at most 2^(kShift + kRise) < 57344
-    constexpr float kLeastV = 3.2311743e-27f;    // 2^-88: smaller V scales count so for the maximum (the sums stay below 2^128)
     const float kNegInf = -__int_as_float(0x7f800000);
     extern __shared__ __align__(16) uint8_t blocks_smem[];
     uint8_t* base = blocks_smem + ((1024u - (smem_u32(blocks_smem) & 1023u)) & 1023u);
@@ -620,7 +619,7 @@ __global__ void __launch_bounds__(CfgBlocks<D, R, std::is_same<T, __half>::value
                 const float* sk = scales + sc.slot * 2 * C::kKeys;
                 const int sat = a.run > 1 ? tok >> 2 : tok;
                 const float ks = sk[sat], vs = sk[C::kKeys + sat];
-                const float lv = log2f(fmaxf(vs, kLeastV));
+                const float lv = log2f(fmaxf(vs, kLeastV));  // (smaller scales count so for the maximum)
                 const unsigned bad_pages = bad_slots[jobs % C::kBadRing];
                 // the sums of the parts, the smallest first
 #pragma unroll

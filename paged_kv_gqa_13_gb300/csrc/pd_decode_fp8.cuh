@@ -376,7 +376,7 @@ __global__ void __launch_bounds__(CfgF8<D>::kMaxWarps * 32, 1)
                 for (int i = 0; i < 2; ++i) {
                     ks[s][i] = sc_at[16 * s + 2 * i];
                     vs[s][i] = sc_at[32 + 16 * s + 2 * i];
-                    lv[s][i] = __log2f(fmaxf(vs[s][i], 1.2621774e-29f));  // at least 2^-96: the sums stay below 2^128
+                    lv[s][i] = __log2f(fmaxf(vs[s][i], 3.2311743e-27f));  // at least 2^-88: the sums stay below 2^128
                 }
         }
         auto k_of = [&](int s, int i) { return kBlocks ? ks[s][i] : 1.f; };

@@ -41,10 +41,12 @@
 // keys come by cp.async beside its codes. k_scale multiplies a key's scores and
 // log2 of v_scale is added to their exponents, so that the weights that meet the
 // codes, and the running maximum, are of what a key can bring to the output; the
-// sum l takes them over v_scale again. Blocks of a multiple of 16 rows: one pair
-// of scales for 16 keys (64 trees of 1 to 32 nodes, 8 heads a group, bf16: 172 us
-// between events, 149 with a scale per head; 4 chunks of 1021 tokens: 477 and 414);
-// others: a pair for each key (204 and 622 us).
+// sum l takes them over v_scale again. V scales below 2^-88 (kLeastV) count as that in
+// both, and the weights that meet their codes are then multiplied by what is missing.
+// Blocks of a multiple of 16 rows: one pair
+// of scales for 16 keys (64 trees of 1 to 32 nodes, 8 heads a group, bf16: 178 us
+// between events, 149 with a scale per head; 4 chunks of 1021 tokens: 490 and 414);
+// others: a pair for each key (212 and 631 us).
 //
 // Rounding. S, maxima, sums and O are f32. The weights are rounded to the
 // operand type, at most half a step each, because both operands of a product
@@ -190,6 +192,9 @@ __device__ __forceinline__ void store32(void* p, const uint32_t (&r)[8]) {
                  : "memory");
 }
 
+// The least V scale that counts for maxima and sums: 2^-88, so that the sums stay below 2^128.
+constexpr float kLeastV = 3.2311743e-27f;
+
 // Block scales of the kKeys tokens of block blk, by a whole warp: K's, then V's, of each quad of tokens (a.run > 1) or
 // token, zero where there is none. Lane x (or x kPer) knows the page and first row of the block's slot x; a slot has 8
 // rows or more, so that a lane's tokens are of one page.
@@ -208,6 +213,25 @@ __device__ __forceinline__ void copy_scales(const TreeArgs& a, int kvh, int len,
         copy4_async(dst + 4 * (kKeys + at), a.v_scale + e, there);
     }
     copy_arrive(bar);
+}
+
+// The weights of a job where a V scale is below kLeastV: kPairs pairs of f16 in tensor memory, times how far below each
+// key's is (`runs`: see the softmax). A pair at a time, from there and back: multiplied on their way there, or 16 pairs at a
+// time, the registers cost every job of a call more (4 chunks of 1021 tokens 520 and 504 us; 488 so, 477 without).
+template <int kPairs, int kRun>
+__device__ __forceinline__ void scale_weights(uint32_t ts, const float4* runs) {
+#pragma unroll 1
+    for (int c = 0; c < kPairs; ++c) {
+        uint32_t w;
+        asm volatile("tcgen05.ld.sync.aligned.32x32b.x1.b32 {%0}, [%1];" : "=r"(w) : "r"(ts + c) : "memory");
+        const float* below = kRun > 1 ? &runs[2 * c / kRun].w : reinterpret_cast<const float*>(runs) + 6 * kPairs + 2 * c;
+        tmem_wait_ld();
+        const float2 y = unpack_pair<__half>(w);
+        asm volatile("tcgen05.st.sync.aligned.32x32b.x1.b32 [%0], {%1};" ::"r"(ts + c),
+                     "r"(Elt<__half>::pack(y.x * below[0], y.y * below[kRun > 1 ? 0 : 1]))
+                     : "memory");
+    }
+    tmem_wait_st();
 }
 
 // ---------------------------------------------------------------- configuration
@@ -795,6 +819,7 @@ __global__ void __launch_bounds__(CfgTree<D, kWide, kPool>::kThreads, 1)
         int jobs = 0, kblocks = 0;  // kblocks: K blocks before this segment
         bool ok = true;
         Ring<kBlocks ? C::kScales : 1> sc;
+        bool small = false;  // block scales: a V scale of these keys is below kLeastV
         float4* ready = reinterpret_cast<float4*>(ctl + C::kReadyOff) + (kBlocks ? wid % (4 * C::kPipes) * C::kReadyRuns : 0);
         auto turn_q = [&](const TcSeg& s, int seg) -> bool {
             // This thread's q row, where the copy put it, as f16 times a power of two that brings its
@@ -850,24 +875,27 @@ __global__ void __launch_bounds__(CfgTree<D, kWide, kPool>::kThreads, 1)
                     const int buf = jobs & 1;
                     if (kBlocks && live && half * C::kJobKeys % C::kReadyKeys == 0) {
                         // The scales of each run of keys, of this job or of the block, before the scores are there: k, log2 v
-                        // and 1 / v, v at least 2^-96 (the sums stay below 2^128); runs of one key as three arrays.
+                        // and 1 / v, v at least kLeastV, and the factor that v is below that; runs of one key as four arrays.
                         if (half == 0 && !(ok = wait(C::kScFull + sc.slot, sc.phase))) break;
                         const float* from = reinterpret_cast<const float*>(ctl + C::kScaleOff) + sc.slot * 2 * C::kKeys;
                         __syncwarp();
+                        small = false;
 #pragma unroll
                         for (int g = lane; g < C::kReadyRuns; g += 32) {
                             const int key = half * C::kJobKeys + g * C::kRun, at = C::kRun == 16 || a.run > 1 ? key / 4 : key;
-                            const float v = fmaxf(from[C::kKeys + at], 1.2621774e-29f);
+                            const float own = from[C::kKeys + at], v = fmaxf(own, kLeastV), below = own < kLeastV ? own * (1.f / kLeastV) : 1.f;
+                            small |= own < kLeastV;
                             if constexpr (C::kRun > 1) {
-                                ready[g] = make_float4(from[at], __log2f(v), __frcp_rn(v), 0.f);
+                                ready[g] = make_float4(from[at], __log2f(v), __frcp_rn(v), below);
                             } else {
                                 float* to = reinterpret_cast<float*>(ready) + g;
                                 to[0] = from[at];
                                 to[C::kJobKeys] = __log2f(v);
                                 to[2 * C::kJobKeys] = __frcp_rn(v);
+                                to[3 * C::kJobKeys] = below;
                             }
                         }
-                        __syncwarp();
+                        small = __any_sync(kFull, small);
                     }
                     if (!(ok = wait(C::kSFull + 2 * p + buf, uint32_t(jobs >> 1) & 1u))) break;
                     if (live) {
@@ -1011,6 +1039,9 @@ __global__ void __launch_bounds__(CfgTree<D, kWide, kPool>::kThreads, 1)
                         sums[0] = __fadd2_rn(sums[0], sums[1]);
                         l += sums[0].x + sums[0].y;
                         tmem_wait_st();
+                        if constexpr (kBlocks) {
+                            if (small) scale_weights<C::kJobKeys / 2, C::kRun>(ts, runs);
+                        }
                         tc_fence_before();
                     }
                     ++jobs;

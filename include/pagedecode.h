@@ -695,7 +695,7 @@ pd_status pd_paged_norm_rope_append_fp8(const void* q, const void* k_new, const 
  *
  * pd_paged_decode_fp8_blocks: pd_paged_decode over such pools: one query row
  *   per request, which attends all of its cached tokens. An empty request gets
- *   o = 0, lse = -infinity.
+ *   o = 0, lse = -infinity. A NaN among a row's scores makes its o and lse NaN.
  * pd_paged_tree_decode_fp8_blocks: pd_paged_tree_decode over such pools.
  *   Both: dtype (PD_F16 or PD_BF16) is the type of q and o; workspace: at least
  *   the bytes that the call's _workspace_bytes gives, which any other call on

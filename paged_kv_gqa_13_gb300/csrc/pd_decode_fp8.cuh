@@ -248,9 +248,11 @@ __global__ void __launch_bounds__(CfgF8<D>::kMaxWarps * 32, 1)
         const int qrow = m.z;
         const int h0 = 2 * c, h1 = 2 * c + 1;
         const float vsc = kBlocks ? 1.f : __ldg(a.v_scale + (qrow % a.num_qo_heads) / a.group);  // V scale, applied once
-        const float inv0 = l0 > 0.f ? vsc / l0 : 0.f, inv1 = l1 > 0.f ? vsc / l1 : 0.f;
-        const float lse0 = l0 > 0.f ? m0 - kShift + log2f(l0) : kNegInf;
-        const float lse1 = l1 > 0.f ? m1 - kShift + log2f(l1) : kNegInf;
+        // (block-scaled pools: a sum of NaN, of a NaN among the scores, is not taken for an empty one)
+        const bool some0 = kBlocks ? l0 != 0.f : l0 > 0.f, some1 = kBlocks ? l1 != 0.f : l1 > 0.f;
+        const float inv0 = some0 ? vsc / l0 : 0.f, inv1 = some1 ? vsc / l1 : 0.f;
+        const float lse0 = some0 ? m0 - kShift + log2f(l0) : kNegInf;
+        const float lse1 = some1 ? m1 - kShift + log2f(l1) : kNegInf;
         if (m.y & kSegComplete) {
             T* o0 = static_cast<T*>(a.o) + (size_t(qrow) + h0) * D;
             T* o1 = o0 + D;
@@ -287,8 +289,10 @@ __global__ void __launch_bounds__(CfgF8<D>::kMaxWarps * 32, 1)
                 }
             }
             if (g == 0) {
-                if (h0 < GT) a.part_lse[size_t(slot) * 8 + h0] = lse0;
-                if (h1 < GT) a.part_lse[size_t(slot) * 8 + h1] = lse1;
+                // (a partial of NaN carries infinity: the merge's maximum would pass over NaN)
+                auto part = [](float x) { return kBlocks && isnan(x) ? __int_as_float(0x7f800000) : x; };
+                if (h0 < GT) a.part_lse[size_t(slot) * 8 + h0] = part(lse0);
+                if (h1 < GT) a.part_lse[size_t(slot) * 8 + h1] = part(lse1);
             }
         }
         reset_state();

@@ -673,7 +673,8 @@ pd_status pd_paged_norm_rope_append_fp8(const void* q, const void* k_new, const 
  *   front where eps > 0; eps = 0 leaves them out (q_weight and
  *   k_weight are then NULL). dtype PD_F16 or PD_BF16. Let a be the largest
  *   finite magnitude, after norm and rotation in f32, of the new elements of a
- *   block.
+ *   block. A new_indptr that does not run from 0 to total_new without decreasing
+ *   is flagged (PD_FLAG_BAD_NEW_ROWS).
  *    - A block whose first row is new gets the scale a / 448, at least 2^-126.
  *    - A block that also holds older rows of the request keeps its scale s
  *      (at least 2^-126) if a <= 464 s (what still rounds to the largest code).
@@ -687,9 +688,10 @@ pd_status pd_paged_norm_rope_append_fp8(const void* q, const void* k_new, const 
  * pd_paged_read_fp8_blocks: the values of tokens first[b] .. first[b] + n_b - 1
  *   of request b, rounded once to T, into rows out_indptr[b] .. of k_out and
  *   v_out (device T [total, num_kv_heads, head_dim], 16-byte aligned), n_b =
- *   out_indptr[b + 1] - out_indptr[b] (device int32 [batch + 1], increasing from
- *   0 to total; n_b may be 0). first: device int32 [batch], or NULL for 0.
- *   dtype: any T. Tokens outside the request, or a malformed out_indptr:
+ *   out_indptr[b + 1] - out_indptr[b] (device int32 [batch + 1], not decreasing,
+ *   within 0 .. total; n_b may be 0). Rows before out_indptr[0] and from
+ *   out_indptr[batch] on stay as they are. first: device int32 [batch], or NULL
+ *   for 0. dtype: any T. Tokens outside the request, or a malformed out_indptr:
  *   PD_FLAG_BAD_NEW_ROWS, and that request's rows are not written. Rows on a
  *   bad page are zero (PD_FLAG_BAD_PAGE_ID).
  *

@@ -63,6 +63,11 @@ __global__ void __launch_bounds__(kThreads) blocks_read_kernel(const ReadArgs a)
     const int tid = threadIdx.x, lane = tid & 31;
     const int c = int(blockIdx.x) / a.slices, slice = int(blockIdx.x) - c * a.slices;
     const int per = a.page_size / a.block;
+    // Each request's range is checked by a tile of its number (there are as many and more).
+    if (tid == 32 && slice == 0 && c < a.batch) {
+        const int s = __ldg(a.out_indptr + c), e = __ldg(a.out_indptr + c + 1);
+        if (s < 0 || e < s || e > a.total) atomicOr(a.flags, kFlagBadNewRows);
+    }
     if (tid < 32) {
         // request b's tiles start at out_indptr[b] / kTile + b
         int lo_b = 0, hi_b = a.batch;

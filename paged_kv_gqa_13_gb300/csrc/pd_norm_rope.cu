@@ -391,6 +391,12 @@ __device__ __forceinline__ void tile_blocks(const NormArgs& a, float* turns, Til
     const int D = a.head_dim, rot = a.rot_dim, T_ = a.tile;
     const int rotated = rot / (2 * V);  // units that are rotated; the rest follow
 
+    // Each request's range is checked by a tile of its number (there are two and more for each): a row that is no request's,
+    // or two's, is in nobody's tile or in two.
+    if (tid == 32 && slice == 0 && c < a.batch) {
+        const int s = __ldg(a.new_indptr + c), e = __ldg(a.new_indptr + c + 1);
+        if (s < 0 || e < s || e > a.tokens || (c == 0 && s != 0) || (c == a.batch - 1 && e != a.tokens)) atomicOr(a.flags, kFlagBadNewRows);
+    }
     // ---- the tile's rows
     if (wid == 0) {
         int count = 0, first = 0, write = 0, old = 0, bad = 0, cache0 = 0, lo = 0;

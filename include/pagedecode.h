@@ -601,7 +601,10 @@ pd_status pd_paged_tree_decode_fp8(const void* q, const void* k_data, const void
  * path: device int32 [batch, max_path]; path_len: device int32 [batch], 0 ..
  * max_path. elem_bytes: 1 (E4M3 pools), 2 or 4. workspace as for
  * pd_paged_rope_append. The table is the one of the tree decode. A request
- * with a bad path or table is flagged and left as it is.
+ * with a bad path or table is flagged and left as it is. Not for block-scaled
+ * pools (below), which this call cannot tell from other E4M3 pools: a code is
+ * another value under another block's scale. There the accepted nodes' rows are
+ * appended again (see pd_paged_rope_append_fp8_blocks).
  */
 pd_status pd_paged_tree_commit(void* k_data, void* v_data, const int32_t* indices, const int32_t* indptr,
                                const int32_t* last_page_len, const int32_t* new_indptr, const int32_t* path,
@@ -684,6 +687,14 @@ pd_status pd_paged_norm_rope_append_fp8(const void* q, const void* k_new, const 
  *   operations in f32, ties to even, saturating at +-448 (infinities too; NaN
  *   stays NaN). Rows past the request's end keep their codes; a page may be
  *   shared with another request where no new row falls into it.
+ *
+ *   After a step with drafted tokens the accepted ones are kept by a second
+ *   call: the table with the request's length shortened to its context and the
+ *   accepted nodes, and the accepted nodes' rows of k_new and v_new as the new
+ *   rows (num_qo_heads = 0), positions as before or NULL (a path's depths are
+ *   its indices). An accepted prefix of a chain is kept by shortening alone.
+ *   The scale of the block that the context ends in stays what the drafted rows
+ *   made it.
  *
  * pd_paged_read_fp8_blocks: the values of tokens first[b] .. first[b] + n_b - 1
  *   of request b, rounded once to T, into rows out_indptr[b] .. of k_out and

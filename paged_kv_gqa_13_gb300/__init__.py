@@ -583,7 +583,8 @@ def pd_paged_tree_commit(k_data, v_data, indices, indptr, last_page_len, new_ind
     """Move the K/V rows of each request's accepted nodes path[b, :path_len[b]] to the places of its first nodes.
 
     path int32 [batch, max_path], strictly increasing; path_len int32 [batch]. total_new bounds new_indptr (default:
-    no bound).
+    no bound). Not for block-scaled pools: it moves codes, and their scales do not move along. There the accepted rows are
+    appended again by pd_paged_rope_append_fp8_blocks, over the shortened requests.
     """
     num_total_pages, num_kv_heads, page_size, head_dim = _pools(k_data, v_data)
     table, batch, entries = _table(indices, indptr, last_page_len, new_indptr)

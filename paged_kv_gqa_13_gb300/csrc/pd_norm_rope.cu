@@ -361,7 +361,10 @@ __device__ __forceinline__ void token_heads(const NormArgs& a, long long w) {
                                                 : static_cast<T*>(a.k_data) + dst + head * head_step;
 #pragma unroll
                         for (int j = 0; j < kUnits; ++j)
-                            if (at.on[j]) {
+                            if (kPool == kBlockScales && at.on[j] && !(a.eps > 0.f) && at.lu + 32 * j >= rotated) {
+                                *reinterpret_cast<Raw<T, V>*>(p + at.e0[j]) = xs[r][j];  // every bit as it came
+                                *reinterpret_cast<Raw<T, V>*>(p + at.e1[j]) = ys[r][j];
+                            } else if (at.on[j]) {
                                 store_elems<T, V>(p + at.e0[j], x[j]);
                                 store_elems<T, V>(p + at.e1[j], y[j]);
                             }

@@ -896,7 +896,12 @@ bool blocks_tc_lookup(int D, TreeKernels* k) {
     switch (D) {
         case 64: *k = blocks_tc_kernels<T, 64, R>(); return true;
         case 128: *k = blocks_tc_kernels<T, 128, R>(); return true;
-        case 256: *k = blocks_tc_kernels<T, 256, R>(); return true;
+    }
+    if constexpr (R == 16) {
+        if (D == 256) {
+            *k = blocks_tc_kernels<T, 256, R>();
+            return true;
+        }
     }
     return false;
 }

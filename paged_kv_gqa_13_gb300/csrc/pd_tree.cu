@@ -61,13 +61,17 @@ bool pick(pd_dtype dt, bool fp8, int D, int group, Rows rows, TreeKernels* k) {
 
 // Block-scaled pools: the kernel by the rows of a request on average and the pairs of a request and a kv head. Few rows
 // meet the codes as operands, in row tiles of 16 or 32 (f16, with more parts of everything: 16); more pay for widening the
-// codes to f16 once, in row tiles of 128 or two of 128. 512 to 4096 tokens, head_dim 128, blocks of 16 tokens, bf16, as
-// operands and widened: 16 rows, 128 pairs 56 and 63 us; 32 rows, 64 pairs 62 and 41, 256 pairs 109 and 109, 512 pairs 192
-// and 211. With a scale for each token: 32 rows, 64 pairs 61 and 50, 128 pairs 77 and 80, 512 pairs 188 and 250 (f16: 267
-// and 249).
+// codes to f16 once, in row tiles of 128 or two of 128. 512 to 4096 tokens, bf16, as operands and widened, in us:
+//   16 rows, blocks of 16 tokens, head_dim 64, 128 and 256: 64 pairs 44, 50, 63 and 40, 46, 55; 128 pairs 52, 58, 84 and 58,
+//   66, 85; 384 pairs 94, 104, 178 and 143, 170, 213
+//   32 rows, blocks of 16 tokens: head_dim 128, 64 pairs 64 and 44, 256 pairs 118 and 111, 512 pairs 204 and 210 (24 rows 181
+//   and 209); head_dim 64, 512 pairs 191 and 194; head_dim 256, 512 pairs 337 and 258
+//   32 rows, a scale for each token: head_dim 128, 128 pairs 83 and 81, 256 pairs 119 and 130, 512 pairs 204 and 259; head_dim
+//   64, 256 pairs 113 and 109, 512 pairs 191 and 206; head_dim 256, 512 pairs 335 and 300
+// The mean goes for the whole call: one long prompt piece among many single tokens runs in row tiles of 16.
 bool pick_blocks(pd_dtype dt, int D, int block, long long rows, long long pairs, TreeKernels* k) {
     const bool runs = block % 16 == 0;  // 16 keys share their scales
-    if (rows <= 16 || (rows <= 32 && dt == PD_BF16 && pairs >= (runs ? 256 : 128)))
+    if (rows <= 16 || (rows <= 32 && dt == PD_BF16 && D <= 128 && pairs >= (runs || D < 128 ? 512 : 256)))
         return dt == PD_F16 ? blocks_tc_f16(D, k) : blocks_tc_bf16(D, int(rows), k);
     if (runs) return dt == PD_F16 ? blocks_wide16_f16(D, k) : blocks_wide16_bf16(D, k);
     return dt == PD_F16 ? blocks_wide_f16(D, k) : blocks_wide_bf16(D, k);

@@ -697,7 +697,7 @@ pd_status pd_paged_norm_rope_append_fp8(const void* q, const void* k_new, const 
  *   made it.
  *
  * pd_paged_read_fp8_blocks: the values of tokens first[b] .. first[b] + n_b - 1
- *   of request b, rounded once to T, into rows out_indptr[b] .. of k_out and
+ *   of request b (f32 products, rounded to T) in rows out_indptr[b] .. of k_out and
  *   v_out (device T [total, num_kv_heads, head_dim], 16-byte aligned), n_b =
  *   out_indptr[b + 1] - out_indptr[b] (device int32 [batch + 1], not decreasing,
  *   within 0 .. total; n_b may be 0). Rows before out_indptr[0] and from
@@ -710,7 +710,15 @@ pd_status pd_paged_norm_rope_append_fp8(const void* q, const void* k_new, const 
  *   per request, which attends all of its cached tokens. An empty request gets
  *   o = 0, lse = -infinity. A NaN among a row's scores makes its o and lse NaN.
  * pd_paged_tree_decode_fp8_blocks: pd_paged_tree_decode over such pools.
- *   Both: dtype (PD_F16 or PD_BF16) is the type of q and o; workspace: at least
+ *   Both: dtype (PD_F16 or PD_BF16) is the type of q and o. Scores, maxima, sums
+ *   and outputs are f32 until the last rounding; a weight times its V scale is
+ *   rounded to f16 before it meets the codes, and for bf16 outputs of few rows to
+ *   9 significant bits. An f16 output so has a fifth to a third more error than
+ *   its own rounding. V scales below 2^-88 lose precision by how far they are below it.
+ *   One kernel is chosen for the whole call, by the mean number of rows of a
+ *   request: a prompt piece beside many single tokens runs faster in a call of
+ *   its own.
+ *   workspace: at least
  *   the bytes that the call's _workspace_bytes gives, which any other call on
  *   the same stream may share. The other arguments, results and errors
  *   are those of pd_paged_decode and pd_paged_tree_decode.

@@ -799,7 +799,7 @@ pd_status pd_paged_decode_fp8(const void* q, const void* k_data, const void* v_d
 
 // Groups of 3 to 8 q heads at head_dim 128 and 256 run on decode_fp8_mma_kernel, other shapes on the kernels of the tree
 // decode with one node per request: the former holds more copies in flight per SM and starts sooner (32 requests of 512 to
-// 4096 tokens, 4 heads a group: 39 us, 63 on the other; 4 requests of 131,072: 187 and 212), the latter reads K and V once
+// 4096 tokens, 4 heads a group: 41 us, 66 on the other; 4 requests of 131,072: 191 and 208), the latter reads K and V once
 // for any group and takes any head_dim.
 static bool blocks_on_decode(int num_qo_heads, int num_kv_heads, int head_dim) {
     const int group = num_kv_heads > 0 ? num_qo_heads / num_kv_heads : 0;

@@ -43,12 +43,14 @@
 // an mma warp, producers (TMA copies of the codes, cp.async of the scales), and a
 // warp that walks the segments and writes the parts of a segment's q ahead of time.
 //
-// What bounds it. Each product instruction takes 80 to 90 cycles to issue whatever
-// N is up to 128, 4 for S and 4 for O of a tile at head_dim 128, and the softmax is
-// short; the copies keep two lines of an SM at the rate that TMA boxes of a page
-// come in. 4 requests of 65,536 tokens, 4 kv heads of 128, 16 rows, bf16: 89 us
-// between events (widened codes: 126); 32 of 512 to 4096 tokens, 16 kv heads, one row:
-// 89 (201). From 17 rows on see pick_blocks.
+// What bounds it. Not the products: one instruction takes 80 to 90 cycles to issue
+// whatever N is up to 128, 4 for S and 4 for O of a tile at head_dim 128, about 14 TB/s of
+// codes on 152 SMs, and the tensor pipe is 3 % busy. What does not grow with the work
+// (partition, q's parts, first copies, the slowest line, the merge), 45 to 50 us between
+// events: 58 us over a floor of 11 (32 requests of 512 to 4096 tokens, 4 kv heads of 128, 16
+// rows, bf16), 93 over 40 (4 of 65,536), 208 over 158 (4 of 131,072, 8 kv heads, 4 rows), 91
+// over 44 (32 short ones, 16 kv heads, one row; widened codes: 209). Which part of it is not
+// measured; one CTA over one tile takes 13. From 17 rows on see pick_blocks.
 //
 // Whoever waits on a barrier takes part in its next phase, or waits for a load
 // whose slot cannot be filled again before it has given its weights.

@@ -28,7 +28,7 @@ def _shared(c, batch):
 @pytest.mark.parametrize("hq,hk,d,block,new,batch", [
     (2, 2, 128, 16, 1, 160), (4, 2, 64, 16, 1, 160), (16, 1, 128, 1, 1, 320), (16, 1, 256, 16, 1, 160), (8, 1, 64, 4, 1, 3),
     (24, 1, 128, 16, 1, 320), (4, 1, 64, 16, 4, 320), (4, 1, 128, 16, 1, 310), (8, 1, 256, 16, 1, 160), (4, 1, 128, 16, 40, 160),
-    (4, 1, 64, 2, 40, 160),
+    (4, 1, 64, 2, 40, 160), (24, 1, 128, 1, 1, 320), (24, 1, 128, 16, 1, 600), (32, 1, 64, 4, 1, 600),
 ])
 @pytest.mark.parametrize("n,ahead,where", [(4096, 12.0, 0), (16384, 12.0, 0), (16384, 14.0, 16000), (65536, 16.0, 100)])
 def test_a_long_tail_beside_one_dominant_key(dtype, hq, hk, d, block, new, batch, n, ahead, where):
@@ -83,3 +83,14 @@ def test_requests_of_very_different_numbers_of_rows(dtype, kind):
     flags, o, lse = _run(c, q, masks)
     assert flags == 0
     check_attention(o, lse, attend_tight(c, q, masks, 1 / math.sqrt(128), dtype))
+
+
+@pytest.mark.parametrize("d,block", [(64, 16), (64, 2), (128, 16), (128, 1), (256, 16)])
+def test_many_requests_of_17_to_32_rows(d, block):
+    rng = np.random.default_rng(d)
+    kv = [3000, 0, 1, 31] + rng.integers(1, 200, 68).tolist()
+    c = BlockPaged(kv, 8, d, 16, block, seed=d)
+    q = _q(len(kv), 8 * 24, d, "bf16", spread=1.0)
+    flags, o, lse = _run(c, q, single=True)
+    assert flags == 0
+    check_attention(o, lse, attend_tight(c, q, None, 1 / math.sqrt(d), "bf16"))

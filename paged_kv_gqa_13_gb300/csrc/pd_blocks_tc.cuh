@@ -735,6 +735,7 @@ __global__ void __launch_bounds__(CfgBlocks<D, R, std::is_same<T, __half>::value
                         m = to_m;
                     }
                     unset = __ballot_sync(kFull, lane < cols && m == kNegInf);
+                    __syncwarp();
 #pragma unroll
                     for (int c = 0; c < R; ++c) x[c] += wd[c];
                     if (!fresh) {

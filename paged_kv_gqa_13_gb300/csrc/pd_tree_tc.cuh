@@ -896,6 +896,7 @@ __global__ void __launch_bounds__(CfgTree<D, kWide, kPool>::kThreads, 1)
                             }
                         }
                         small = __any_sync(kFull, small);
+                        __syncwarp();
                     }
                     if (!(ok = wait(C::kSFull + 2 * p + buf, uint32_t(jobs >> 1) & 1u))) break;
                     if (live) {
